@@ -60,7 +60,8 @@ typedef enum fattn_status {
     FATTN_ERR_UNSUPPORTED = 2, /* d not supported by the call, tensor too large, device is not sm_103 */
     FATTN_ERR_CUDA = 3,        /* a CUDA runtime/driver call failed; see fattn_last_cuda_error() */
     FATTN_ERR_TIMEOUT = 4,     /* a kernel gave up on a pipeline wait (see fattn_get_device_status) */
-    FATTN_ERR_RANGE = 5        /* a non-finite output row, e.g. from |V| >= 65520 (see attn_fwd) */
+    FATTN_ERR_RANGE = 5,       /* a non-finite output row, e.g. from |V| >= 65520 (see attn_fwd) */
+    FATTN_ERR_INDEX = 6        /* a page, position or length read from device memory is out of range */
 } fattn_status_t;
 
 /*
@@ -368,6 +369,109 @@ fattn_status_t fattn_softmax_rows(const void *x, void *y, int M, int N, int dtyp
 fattn_status_t fattn_row_sum(const void *x, float *out, int M, int N, int dtype,
                              struct CUstream_st *stream);
 
+/*
+ * fattn_qk_norm_rope -- the per-head norm and the position rotation of
+ * queries and keys, the step between a decoder layer's projections and its
+ * attention ("OpenAI Triton: from introduction to model practice", section 3,
+ * the layer's q and k before the scores), in one pass over each:
+ *
+ *   y = R(p) ( w * x / sqrt(mean(x^2) + eps) )      for every row x of q and k
+ *
+ * R(p) turns pairs of the first rot_dim elements by the angles of the row's
+ * position p: (a, b) -> (a cos - b sin, b cos + a sin); the rest passes.
+ *
+ *   q, q_out   : [B][Hq][N][d], k, k_out : [B][Hk][N][d], 16-bit, with element
+ *                strides (batch, head, token), last dimension contiguous.
+ *                Hq or Hk 0: that tensor is absent (its pointers are ignored).
+ *   wq, wk     : [d] in the tensors' type, or NULL: no norm (y = R x)
+ *   rope       : fp32 [max_pos][rot_dim]: each position's rot_dim/2 cosines,
+ *                then its rot_dim/2 sines; ignored when rot_dim is 0
+ *   positions  : int32 [B][N] on the device, or NULL for 0 .. N-1
+ *   rot_dim    : multiple of 16, 0 (no rotation) .. d
+ *   interleaved: 0: pairs (c, c + rot_dim/2); 1: neighbours (2c, 2c + 1)
+ *   eps        : finite and > 0
+ *   dtype      : 0 = bf16, 1 = fp16;  d in {64, 96, 128, 256}
+ *
+ * Arithmetic is fp32, rounded once at the end.  q_out may be q itself (same
+ * pointer and strides), k_out likewise k; otherwise an output shares no
+ * element with an input or the other output: their address spans are apart,
+ * or they lie side by side in one layout (windows of one packed projection
+ * output).  A token whose position is outside [0, max_pos) is left unwritten
+ * and records FATTN_ERR_INDEX (role 7) in the device status word.  Strides of
+ * dimensions longer than 1 are positive multiples of 8 elements, pointers
+ * 16-byte aligned (positions: 4).  Errors as for attn_fwd_strided.
+ *
+ * fattn_qk_norm_rope_bwd -- its gradients.  From the upstream gradients
+ * dq_out, dk_out and the forward's inputs (the statistics are recomputed):
+ *   g = R(p)^T dy,  r = 1 / sqrt(mean(x^2) + eps),
+ *   dx = r ( g w - x r^2 mean(g w x) ),   dw = sum over all rows of g r x.
+ * dq, dk have the inputs' type; dwq, dwk are fp32 [d], overwritten, given
+ * exactly when wq, wk are (without a norm dx = R^T dy, and x is not read).
+ * dq may be dq_out or q itself, dk dk_out or k.  workspace: device, 16-byte
+ * aligned, fattn_qk_norm_rope_bwd_workspace_size(d) bytes on the current
+ * device (0 on invalid arguments); may be NULL when neither wq nor wk is
+ * given.  Its contents are ignored on entry and undefined on exit; calls that
+ * share one must not overlap on the device.  Sums are taken in a fixed order:
+ * equal calls give equal bits.  With no rows dwq and dwk are set to zero.  A
+ * token with a position out of range is left unwritten and adds nothing.
+ */
+fattn_status_t fattn_qk_norm_rope(const void *q, const void *k, void *q_out, void *k_out,
+                                  const void *wq, const void *wk, const float *rope,
+                                  const int *positions, int B, int Hq, int Hk, int N, int d,
+                                  int rot_dim, int max_pos, const long long *q_strides,
+                                  const long long *k_strides, const long long *q_out_strides,
+                                  const long long *k_out_strides, float eps, int interleaved,
+                                  int dtype, struct CUstream_st *stream);
+size_t fattn_qk_norm_rope_bwd_workspace_size(int d);
+fattn_status_t fattn_qk_norm_rope_bwd(const void *dq_out, const void *dk_out, const void *q,
+                                      const void *k, const void *wq, const void *wk,
+                                      const float *rope, const int *positions, void *dq, void *dk,
+                                      float *dwq, float *dwk, int B, int Hq, int Hk, int N, int d,
+                                      int rot_dim, int max_pos, const long long *dq_out_strides,
+                                      const long long *dk_out_strides, const long long *q_strides,
+                                      const long long *k_strides, const long long *dq_strides,
+                                      const long long *dk_strides, float eps, int interleaved,
+                                      int dtype, void *workspace, size_t workspace_bytes,
+                                      struct CUstream_st *stream);
+
+/*
+ * The paged cache.  Keys and values of many sequences live in pools of pages:
+ * element (page, head, slot, c) of a pool at page*s[0] + head*s[1] +
+ * slot*s[2] + c for its strides s (so [pages][Hk][page_size][d] and
+ * [pages][page_size][Hk][d] both fit).  page_size is a power of two, 16 or
+ * more.  Position j of sequence b is slot j % page_size of page
+ * page_table[b*page_table_stride + j / page_size], j < max_pages * page_size.
+ * The new tokens of all sequences are packed: those of sequence b are tokens
+ * cu_q[b] .. cu_q[b+1]-1 (cu_q: int32 [B+1], non-decreasing, from 0) and are
+ * the last positions of its kv_len[b] keys (kv_len: int32 [B], the new tokens
+ * among them).  Tokens from cu_q[B] on belong to no sequence.  page_table,
+ * cu_q and kv_len are device memory, read when the kernel runs, so a captured
+ * graph follows their contents.  Table entries past a sequence's last page
+ * are never read.
+ *
+ * fattn_kv_append -- writes the new tokens' keys, turned by the rotation of
+ * their positions, and values into the cache.
+ *   k, v           : 16-bit [T][Hk][d], element strides (token, head)
+ *   k_cache, v_cache: the pools, num_pages pages, element strides (page, head,
+ *                    slot); the two may be windows of one buffer
+ *   rope, rot_dim, max_pos, interleaved, dtype, d: as fattn_qk_norm_rope
+ *                    (rot_dim 0: keys are copied)
+ * Elements not turned are copied bit for bit.  A token with no valid place
+ * (position < 0 or beyond max_pages * page_size or max_pos, a page outside
+ * [0, num_pages), cu_q out of order or past T) is skipped and records
+ * FATTN_ERR_INDEX (role 8) in the device status word.  Two tokens must not
+ * share a place.  T, B or Hk 0 enqueues nothing.  One kernel; takes no
+ * memory.
+ */
+fattn_status_t fattn_kv_append(const void *k, const void *v, void *k_cache, void *v_cache,
+                               const int *page_table, const int *cu_q, const int *kv_len,
+                               const float *rope, int T, int B, int Hk, int d, int num_pages,
+                               int page_size, int max_pages, long long page_table_stride,
+                               int rot_dim, int max_pos, const long long *k_strides,
+                               const long long *v_strides, const long long *k_cache_strides,
+                               const long long *v_cache_strides, int interleaved, int dtype,
+                               struct CUstream_st *stream);
+
 /* Human-readable name of a status code (static storage, never NULL). */
 const char *fattn_status_string(fattn_status_t status);
 
@@ -380,12 +484,13 @@ int fattn_last_cuda_error(void);
  * current device, after synchronising `stream`.
  *
  * *status receives 0 when no kernel reported a problem since the last read,
- * otherwise the first code recorded: bits 0..7 = FATTN_ERR_TIMEOUT or
- * FATTN_ERR_RANGE, bits 8..15 = the role that reported it (1 load, 2 mma,
- * 3 softmax, 4 epilogue, 5 self-test, 6 V conversion), bits 16..31 = the CTA
- * index.  Returns the status in bits 0..7 (FATTN_ERR_TIMEOUT or
- * FATTN_ERR_RANGE) if *status is nonzero, FATTN_OK if it is zero, or
- * FATTN_ERR_INVALID_ARG / FATTN_ERR_CUDA.
+ * otherwise the first code recorded: bits 0..7 = FATTN_ERR_TIMEOUT,
+ * FATTN_ERR_RANGE or FATTN_ERR_INDEX, bits 8..15 = the role that reported it
+ * (1 load, 2 mma, 3 softmax, 4 epilogue, 5 self-test, 6 V conversion,
+ * 7 norm and rotation, 8 cache append), bits 16..31 = the CTA
+ * index.  Returns the status in bits 0..7 (FATTN_ERR_TIMEOUT,
+ * FATTN_ERR_RANGE or FATTN_ERR_INDEX) if *status is nonzero, FATTN_OK if it
+ * is zero, or FATTN_ERR_INVALID_ARG / FATTN_ERR_CUDA.
  *
  * The library keeps per-device state for the life of the process (the
  * helper streams of attn_fwd_host, the scratch address of

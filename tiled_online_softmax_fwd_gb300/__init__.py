@@ -6,7 +6,8 @@ Importing the package does not load the library: the first call does, and it
 raises if the library has not been built (there is no CPU fallback).
 """
 __all__ = ["attn_fwd", "attn_fwd_fp16", "attn_bwd", "attn_fwd_host", "attn_fwd_simt", "attn_fwd_split", "split_count",
-           "split_workspace_size", "softmax_rows", "row_sum", "FattnError", "device_status",
+           "split_workspace_size", "qk_norm_rope", "qk_norm_rope_bwd", "rope_table", "kv_append",
+           "softmax_rows", "row_sum", "FattnError", "device_status",
            "library_path", "version"]
 
 

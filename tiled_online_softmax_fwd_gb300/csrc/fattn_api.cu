@@ -667,6 +667,372 @@ fattn_status_t host_pipe(int dev, HostPipe **out)
     return FATTN_OK;
 }
 
+// ---------------------------------------------------------------- row sets
+// One strided tensor of 16-bit rows of d elements: base, element strides and
+// extents of its outer dimensions (unused ones have extent 1).
+struct Rows {
+    const void *p;
+    long long st[3];
+    long long ext[3];
+    int d;
+};
+
+Rows rows_of(const void *p, const long long *st, int n_dims, long long e0, long long e1,
+             long long e2, int d)
+{
+    Rows r{p, {1, 1, 1}, {e0, e1, n_dims > 2 ? e2 : 1}, d};
+    for (int i = 0; i < n_dims; ++i)
+        r.st[i] = st[i];
+    return r;
+}
+
+bool empty(const Rows &r) { return r.ext[0] == 0 || r.ext[1] == 0 || r.ext[2] == 0; }
+
+// Elements from the base to one past the last.
+long long extent_of(const Rows &r)
+{
+    long long n = r.d;
+    for (int i = 0; i < 3; ++i)
+        n += r.st[i] * (r.ext[i] - 1);
+    return n;
+}
+
+// Alignment and stride rules: base 16-byte aligned; each stride of a
+// dimension of extent > 1 a positive multiple of 8 elements, at most 2^38;
+// the span below 2^39 bytes.
+fattn_status_t check_rows(const Rows &r)
+{
+    if (!r.p || !aligned16(r.p))
+        return FATTN_ERR_INVALID_ARG;
+    long double far = r.d;
+    for (int i = 0; i < 3; ++i) {
+        if (r.ext[i] <= 1)
+            continue;
+        if (r.st[i] < 1 || r.st[i] % 8 != 0 || r.st[i] > (1LL << 38))
+            return FATTN_ERR_INVALID_ARG;
+        far += static_cast<long double>(r.st[i]) * (r.ext[i] - 1);
+    }
+    return far * 2 >= static_cast<long double>(1LL << 39) ? FATTN_ERR_UNSUPPORTED : FATTN_OK;
+}
+
+// Whether all elements are distinct, by nesting: the strides sorted by size,
+// each at least the span of the smaller dimensions.
+bool distinct(const Rows &r)
+{
+    int at[3] = {0, 1, 2};
+    std::sort(at, at + 3, [&](int a, int b) { return r.st[a] < r.st[b]; });
+    long long covered = r.d;
+    for (int i : at) {
+        if (r.ext[i] <= 1)
+            continue;
+        if (r.st[i] < covered)
+            return false;
+        covered += r.st[i] * (r.ext[i] - 1);
+    }
+    return true;
+}
+
+// Whether two row sets share no element, as far as can be told: their spans
+// are apart, or they are side by side in the cells of one layout (for some
+// stride C, each set is a window smaller than C repeated at multiples of C,
+// and the windows of a cell are apart), as q and k in one packed projection
+// output or the keys and values of one [pages][2]... cache.
+bool apart(const Rows &a, const Rows &b)
+{
+    if (empty(a) || empty(b) ||
+        !overlap(a.p, static_cast<size_t>(extent_of(a)) * 2, b.p, static_cast<size_t>(extent_of(b)) * 2))
+        return true;
+    const long long delta_bytes = static_cast<long long>(reinterpret_cast<uintptr_t>(b.p)) -
+                                  static_cast<long long>(reinterpret_cast<uintptr_t>(a.p));
+    const long long delta = delta_bytes / 2;  // bases are 16-byte aligned
+    const Rows *both[2] = {&a, &b};
+    for (const Rows *from : both)
+        for (int i = 0; i < 3; ++i) {
+            const long long cell = from->st[i];
+            if (from->ext[i] <= 1)
+                continue;
+            long long window[2];
+            bool regular = true;
+            for (int t = 0; t < 2; ++t) {
+                window[t] = both[t]->d;
+                for (int k = 0; k < 3; ++k) {
+                    if (both[t]->ext[k] <= 1)
+                        continue;
+                    if (both[t]->st[k] < cell)
+                        window[t] += both[t]->st[k] * (both[t]->ext[k] - 1);
+                    else
+                        regular = regular && both[t]->st[k] % cell == 0;
+                }
+            }
+            const long long at = ((delta % cell) + cell) % cell;
+            if (regular && at >= window[0] && at + window[1] <= cell)
+                return true;
+        }
+    return false;
+}
+
+bool same_rows(const Rows &a, const Rows &b)
+{
+    if (a.p != b.p)
+        return false;
+    for (int i = 0; i < 3; ++i)
+        if (a.ext[i] != b.ext[i] || (a.ext[i] > 1 && a.st[i] != b.st[i]))
+            return false;
+    return true;
+}
+
+// An output against a plain buffer.
+bool apart(const Rows &a, const void *p, size_t bytes)
+{
+    return empty(a) || p == nullptr || bytes == 0 ||
+           !overlap(a.p, static_cast<size_t>(extent_of(a)) * 2, p, bytes);
+}
+
+bool head_dim_ok(int d) { return d == 64 || d == 96 || d == 128 || d == 256; }
+
+// Rotation arguments shared by the norm and append calls.
+fattn_status_t check_rope(const float *rope, int rot_dim, int max_pos, int d, int interleaved)
+{
+    if (interleaved != 0 && interleaved != 1)
+        return FATTN_ERR_INVALID_ARG;
+    if (rot_dim < 0 || rot_dim > d || rot_dim % 16 != 0)
+        return FATTN_ERR_INVALID_ARG;
+    if (rot_dim == 0)
+        return FATTN_OK;
+    if (!rope || !aligned16(rope) || max_pos < 1)
+        return FATTN_ERR_INVALID_ARG;
+    return FATTN_OK;
+}
+
+// A paged cache's geometry and the lists that describe its sequences.
+struct Paging {
+    const int *page_table, *cu_q, *kv_len;
+    int B, num_pages, page_size, max_pages;
+    long long table_stride;
+};
+
+fattn_status_t check_paging(const Paging &g)
+{
+    if (g.B < 0 || g.num_pages < 0 || g.max_pages < 0)
+        return FATTN_ERR_INVALID_ARG;
+    if (g.page_size < 16 || (g.page_size & (g.page_size - 1)) != 0)
+        return FATTN_ERR_UNSUPPORTED;
+    // Positions are 32-bit.
+    if (static_cast<long long>(g.max_pages) * g.page_size > 0x7fffffffLL - 256)
+        return FATTN_ERR_UNSUPPORTED;
+    return FATTN_OK;
+}
+
+fattn_status_t check_lists(const Paging &g)
+{
+    if (!g.cu_q || !g.kv_len || (!g.page_table && g.max_pages > 0))
+        return FATTN_ERR_INVALID_ARG;
+    if (g.B > 1 && (g.table_stride < g.max_pages || g.table_stride > (1LL << 38)))
+        return FATTN_ERR_INVALID_ARG;
+    const int *lists[3] = {g.page_table, g.cu_q, g.kv_len};
+    for (const int *l : lists)
+        if (reinterpret_cast<uintptr_t>(l) % 4 != 0)
+            return FATTN_ERR_INVALID_ARG;
+    return FATTN_OK;
+}
+
+size_t table_bytes(const Paging &g)
+{
+    return g.B == 0 || g.max_pages == 0
+               ? 0
+               : static_cast<size_t>(g.table_stride * (g.B - 1) + g.max_pages) * 4;
+}
+
+// Device pointers of a call (null entries are skipped) on the current device.
+template <size_t n>
+fattn_status_t check_buffers(const void *const (&bufs)[n], int *dev, DeviceInfo *info)
+{
+    fattn_status_t s = current_device(dev, info);
+    for (size_t i = 0; i < n && s == FATTN_OK; ++i)
+        if (bufs[i] != nullptr)
+            s = check_device_buffer(bufs[i], *dev);
+    return s;
+}
+
+fattn_status_t status_word(uint32_t **out)
+{
+    const cudaError_t e = fattn::status_word_address(out);
+    return e == cudaSuccess ? FATTN_OK : cuda_fail(e);
+}
+
+void copy_strides(long long (&dst)[3], const Rows &r)
+{
+    for (int i = 0; i < 3; ++i)
+        dst[i] = r.st[i];
+}
+
+// Both passes of the norm and rotation.  g, dw and the workspace belong to
+// the backward pass (backward true), whose outputs are y = dx.
+struct NormCall {
+    const void *x[2], *g[2], *w[2];
+    void *y[2];
+    float *dw[2];
+    const long long *x_st[2], *g_st[2], *y_st[2];
+};
+
+fattn_status_t norm_rope(const NormCall &c, bool backward, const float *rope, const int *positions,
+                         int B, int Hq, int Hk, int N, int d, int rot_dim, int max_pos, float eps,
+                         int interleaved, int dtype, void *workspace, size_t workspace_bytes,
+                         cudaStream_t stream)
+{
+    if (B < 0 || Hq < 0 || Hk < 0 || N < 0 || (dtype != 0 && dtype != 1))
+        return FATTN_ERR_INVALID_ARG;
+    if (!(eps > 0.f) || !isfinite(eps))
+        return FATTN_ERR_INVALID_ARG;
+    if (!head_dim_ok(d))
+        return FATTN_ERR_UNSUPPORTED;
+    fattn_status_t s = check_rope(rope, rot_dim, max_pos, d, interleaved);
+    if (s != FATTN_OK)
+        return s;
+    const int H[2] = {Hq, Hk};
+    const bool any_w = (Hq > 0 && c.w[0]) || (Hk > 0 && c.w[1]);
+    if (backward)
+        for (int t = 0; t < 2; ++t)
+            if (H[t] > 0 && (c.w[t] != nullptr) != (c.dw[t] != nullptr))
+                return FATTN_ERR_INVALID_ARG;
+    const long long tokens = static_cast<long long>(B) * N;
+    if (tokens == 0 || Hq + static_cast<long long>(Hk) == 0) {
+        // No rows: the sums of an empty set are zero.
+        for (int t = 0; t < 2 && backward; ++t) {
+            if (H[t] == 0 || !c.dw[t])
+                continue;
+            int dev = 0;
+            DeviceInfo info;
+            const void *bufs[1] = {c.dw[t]};
+            if (reinterpret_cast<uintptr_t>(c.dw[t]) % 4 != 0)
+                return FATTN_ERR_INVALID_ARG;
+            if ((s = check_buffers(bufs, &dev, &info)) != FATTN_OK)
+                return s;
+            const cudaError_t e = cudaMemsetAsync(c.dw[t], 0, static_cast<size_t>(d) * 4, stream);
+            if (e != cudaSuccess)
+                return cuda_fail(e);
+        }
+        return FATTN_OK;
+    }
+    // Inputs and outputs of each present tensor.
+    Rows x[2] = {}, g[2] = {}, y[2] = {};
+    for (int t = 0; t < 2; ++t) {
+        if (H[t] == 0)
+            continue;
+        if (!c.y_st[t] || (backward && !c.g_st[t]))
+            return FATTN_ERR_INVALID_ARG;
+        const bool reads_x = !backward || c.w[t] != nullptr;
+        if (reads_x && !c.x_st[t])
+            return FATTN_ERR_INVALID_ARG;
+        y[t] = rows_of(c.y[t], c.y_st[t], 3, B, H[t], N, d);
+        if ((s = check_rows(y[t])) != FATTN_OK)
+            return s;
+        if (!distinct(y[t]))
+            return FATTN_ERR_INVALID_ARG;
+        if (reads_x) {
+            x[t] = rows_of(c.x[t], c.x_st[t], 3, B, H[t], N, d);
+            if ((s = check_rows(x[t])) != FATTN_OK)
+                return s;
+        }
+        if (backward) {
+            g[t] = rows_of(c.g[t], c.g_st[t], 3, B, H[t], N, d);
+            if ((s = check_rows(g[t])) != FATTN_OK)
+                return s;
+        }
+        if (c.w[t] && !aligned16(c.w[t]))
+            return FATTN_ERR_INVALID_ARG;
+        if (backward && c.dw[t] && reinterpret_cast<uintptr_t>(c.dw[t]) % 4 != 0)
+            return FATTN_ERR_INVALID_ARG;
+    }
+    if (reinterpret_cast<uintptr_t>(positions) % 4 != 0)
+        return FATTN_ERR_INVALID_ARG;
+    const size_t need = backward && any_w ? fattn_qk_norm_rope_bwd_workspace_size(d) : 0;
+    if (backward && any_w && need == 0)
+        return FATTN_ERR_CUDA;
+    if (need > 0 && (!workspace || !aligned16(workspace) || workspace_bytes < need))
+        return FATTN_ERR_INVALID_ARG;
+    // Plain buffers of the call, and no output over any of them; an output
+    // may be its own tensor's input (in place), else it is apart from every
+    // row set.
+    const size_t pos_bytes = positions ? static_cast<size_t>(tokens) * 4 : 0;
+    const size_t rope_bytes = rot_dim ? static_cast<size_t>(max_pos) * rot_dim * 4 : 0;
+    struct Plain {
+        const void *p;
+        size_t n;
+        bool out;
+    };
+    const Plain plain[] = {{rot_dim ? rope : nullptr, rope_bytes, false},
+                           {rot_dim ? positions : nullptr, pos_bytes, false},
+                           {Hq ? c.w[0] : nullptr, static_cast<size_t>(d) * 2, false},
+                           {Hk ? c.w[1] : nullptr, static_cast<size_t>(d) * 2, false},
+                           {backward && Hq ? c.dw[0] : nullptr, static_cast<size_t>(d) * 4, true},
+                           {backward && Hk ? c.dw[1] : nullptr, static_cast<size_t>(d) * 4, true},
+                           {need ? workspace : nullptr, need, true}};
+    for (int t = 0; t < 2; ++t) {
+        if (H[t] == 0)
+            continue;
+        for (const Plain &q : plain)
+            if (!apart(y[t], q.p, q.n))
+                return FATTN_ERR_INVALID_ARG;
+        for (int o = 0; o < 2; ++o) {
+            if (H[o] == 0)
+                continue;
+            if (o > t && !apart(y[t], y[o]))
+                return FATTN_ERR_INVALID_ARG;
+            const bool reads_x = !backward || c.w[o] != nullptr;
+            if (reads_x && !(o == t && same_rows(y[t], x[o])) && !apart(y[t], x[o]))
+                return FATTN_ERR_INVALID_ARG;
+            if (backward && !(o == t && same_rows(y[t], g[o])) && !apart(y[t], g[o]))
+                return FATTN_ERR_INVALID_ARG;
+            for (const Plain &q : plain)
+                if (q.out && ((reads_x && !apart(x[o], q.p, q.n)) ||
+                              (backward && !apart(g[o], q.p, q.n))))
+                    return FATTN_ERR_INVALID_ARG;
+        }
+    }
+    for (const Plain &a : plain)
+        for (const Plain &b : plain)
+            if (&a != &b && a.out && a.p && b.p && overlap(a.p, a.n, b.p, b.n))
+                return FATTN_ERR_INVALID_ARG;
+    int dev = 0;
+    DeviceInfo info;
+    const void *bufs[] = {Hq ? x[0].p : nullptr, Hk ? x[1].p : nullptr,
+                          Hq && backward ? g[0].p : nullptr, Hk && backward ? g[1].p : nullptr,
+                          Hq ? y[0].p : nullptr, Hk ? y[1].p : nullptr, plain[0].p, plain[1].p,
+                          plain[2].p, plain[3].p, plain[4].p, plain[5].p, plain[6].p};
+    if ((s = check_buffers(bufs, &dev, &info)) != FATTN_OK)
+        return s;
+    fattn::NormRopeArgs a = {};
+    if ((s = status_word(&a.status)) != FATTN_OK)
+        return s;
+    for (int t = 0; t < 2; ++t) {
+        a.H[t] = H[t];
+        if (H[t] == 0)
+            continue;
+        a.x[t] = x[t].p;
+        a.y[t] = c.y[t];
+        a.w[t] = c.w[t];
+        a.g[t] = backward ? g[t].p : nullptr;
+        a.dw[t] = backward ? c.dw[t] : nullptr;
+        copy_strides(a.x_st[t], x[t]);
+        copy_strides(a.y_st[t], y[t]);
+        copy_strides(a.g_st[t], g[t]);
+    }
+    a.partial = need > 0 ? static_cast<float *>(workspace) : nullptr;
+    a.table = rope;
+    a.positions = positions;
+    a.tokens = tokens;
+    a.N = N;
+    a.d = d;
+    a.rot = rot_dim;
+    a.max_pos = max_pos;
+    a.interleaved = interleaved;
+    a.f16 = dtype;
+    a.eps = eps;
+    const cudaError_t e = fattn::launch_norm_rope(a, info.num_sms, stream);
+    return e == cudaSuccess ? FATTN_OK : cuda_fail(e);
+}
+
 }  // namespace
 
 extern "C" {
@@ -1045,6 +1411,153 @@ fattn_status_t attn_fwd_host(const void *q_host, const void *k_host, const void 
     return FATTN_OK;
 }
 
+fattn_status_t fattn_qk_norm_rope(const void *q, const void *k, void *q_out, void *k_out,
+                                  const void *wq, const void *wk, const float *rope,
+                                  const int *positions, int B, int Hq, int Hk, int N, int d,
+                                  int rot_dim, int max_pos, const long long *q_strides,
+                                  const long long *k_strides, const long long *q_out_strides,
+                                  const long long *k_out_strides, float eps, int interleaved,
+                                  int dtype, struct CUstream_st *stream)
+{
+    NormCall c = {};
+    c.x[0] = q;
+    c.x[1] = k;
+    c.y[0] = q_out;
+    c.y[1] = k_out;
+    c.w[0] = wq;
+    c.w[1] = wk;
+    c.x_st[0] = q_strides;
+    c.x_st[1] = k_strides;
+    c.y_st[0] = q_out_strides;
+    c.y_st[1] = k_out_strides;
+    return norm_rope(c, false, rope, positions, B, Hq, Hk, N, d, rot_dim, max_pos, eps, interleaved,
+                     dtype, nullptr, 0, stream);
+}
+
+size_t fattn_qk_norm_rope_bwd_workspace_size(int d)
+{
+    int dev = 0;
+    DeviceInfo info;
+    if (!head_dim_ok(d) || current_device(&dev, &info) != FATTN_OK)
+        return 0;
+    return static_cast<size_t>(fattn::norm_rope_bwd_blocks(info.num_sms)) * 2 * d * 4;
+}
+
+fattn_status_t fattn_qk_norm_rope_bwd(const void *dq_out, const void *dk_out, const void *q,
+                                      const void *k, const void *wq, const void *wk,
+                                      const float *rope, const int *positions, void *dq, void *dk,
+                                      float *dwq, float *dwk, int B, int Hq, int Hk, int N, int d,
+                                      int rot_dim, int max_pos, const long long *dq_out_strides,
+                                      const long long *dk_out_strides, const long long *q_strides,
+                                      const long long *k_strides, const long long *dq_strides,
+                                      const long long *dk_strides, float eps, int interleaved,
+                                      int dtype, void *workspace, size_t workspace_bytes,
+                                      struct CUstream_st *stream)
+{
+    NormCall c = {};
+    c.x[0] = q;
+    c.x[1] = k;
+    c.g[0] = dq_out;
+    c.g[1] = dk_out;
+    c.y[0] = dq;
+    c.y[1] = dk;
+    c.w[0] = wq;
+    c.w[1] = wk;
+    c.dw[0] = dwq;
+    c.dw[1] = dwk;
+    c.x_st[0] = q_strides;
+    c.x_st[1] = k_strides;
+    c.g_st[0] = dq_out_strides;
+    c.g_st[1] = dk_out_strides;
+    c.y_st[0] = dq_strides;
+    c.y_st[1] = dk_strides;
+    return norm_rope(c, true, rope, positions, B, Hq, Hk, N, d, rot_dim, max_pos, eps, interleaved,
+                     dtype, workspace, workspace_bytes, stream);
+}
+
+fattn_status_t fattn_kv_append(const void *k, const void *v, void *k_cache, void *v_cache,
+                               const int *page_table, const int *cu_q, const int *kv_len,
+                               const float *rope, int T, int B, int Hk, int d, int num_pages,
+                               int page_size, int max_pages, long long page_table_stride,
+                               int rot_dim, int max_pos, const long long *k_strides,
+                               const long long *v_strides, const long long *k_cache_strides,
+                               const long long *v_cache_strides, int interleaved, int dtype,
+                               struct CUstream_st *stream)
+{
+    if (T < 0 || Hk < 0 || (dtype != 0 && dtype != 1))
+        return FATTN_ERR_INVALID_ARG;
+    if (!head_dim_ok(d))
+        return FATTN_ERR_UNSUPPORTED;
+    const Paging g{page_table, cu_q, kv_len, B, num_pages, page_size, max_pages, page_table_stride};
+    fattn_status_t s = check_paging(g);
+    if (s != FATTN_OK || (s = check_rope(rope, rot_dim, max_pos, d, interleaved)) != FATTN_OK)
+        return s;
+    if (T == 0 || B == 0 || Hk == 0)
+        return FATTN_OK;
+    if ((s = check_lists(g)) != FATTN_OK)
+        return s;
+    if (!k_strides || !v_strides || !k_cache_strides || !v_cache_strides || num_pages == 0)
+        return FATTN_ERR_INVALID_ARG;
+    const Rows in[2] = {rows_of(k, k_strides, 2, T, Hk, 1, d), rows_of(v, v_strides, 2, T, Hk, 1, d)};
+    const Rows out[2] = {rows_of(k_cache, k_cache_strides, 3, num_pages, Hk, page_size, d),
+                         rows_of(v_cache, v_cache_strides, 3, num_pages, Hk, page_size, d)};
+    const size_t lists[4] = {table_bytes(g), (static_cast<size_t>(B) + 1) * 4,
+                             static_cast<size_t>(B) * 4,
+                             rot_dim ? static_cast<size_t>(max_pos) * rot_dim * 4 : 0};
+    const void *list[4] = {page_table, cu_q, kv_len, rope};
+    for (const Rows &r : in)
+        if ((s = check_rows(r)) != FATTN_OK)
+            return s;
+    for (const Rows &r : out) {
+        if ((s = check_rows(r)) != FATTN_OK)
+            return s;
+        if (!distinct(r) || !apart(r, in[0]) || !apart(r, in[1]))
+            return FATTN_ERR_INVALID_ARG;
+        for (int i = 0; i < 4; ++i)
+            if (lists[i] > 0 && !apart(r, list[i], lists[i]))
+                return FATTN_ERR_INVALID_ARG;
+    }
+    if (!apart(out[0], out[1]))
+        return FATTN_ERR_INVALID_ARG;
+    int dev = 0;
+    DeviceInfo info;
+    const void *bufs[] = {k, v, k_cache, v_cache, max_pages ? page_table : nullptr, cu_q, kv_len,
+                          rot_dim ? rope : nullptr};
+    if ((s = check_buffers(bufs, &dev, &info)) != FATTN_OK)
+        return s;
+    fattn::KvAppendArgs a = {};
+    if ((s = status_word(&a.status)) != FATTN_OK)
+        return s;
+    a.k = k;
+    a.v = v;
+    a.k_cache = k_cache;
+    a.v_cache = v_cache;
+    a.page_table = page_table;
+    a.cu_q = cu_q;
+    a.kv_len = kv_len;
+    a.table = rope;
+    for (int i = 0; i < 2; ++i) {
+        a.k_st[i] = in[0].st[i];
+        a.v_st[i] = in[1].st[i];
+    }
+    copy_strides(a.kc_st, out[0]);
+    copy_strides(a.vc_st, out[1]);
+    a.table_stride = page_table_stride;
+    a.T = T;
+    a.B = B;
+    a.H = Hk;
+    a.d = d;
+    a.rot = rot_dim;
+    a.max_pos = max_pos;
+    a.interleaved = interleaved;
+    a.f16 = dtype;
+    a.num_pages = num_pages;
+    a.page_shift = __builtin_ctz(static_cast<unsigned>(page_size));
+    a.max_pages = max_pages;
+    const cudaError_t e = fattn::launch_kv_append(a, info.num_sms, stream);
+    return e == cudaSuccess ? FATTN_OK : cuda_fail(e);
+}
+
 const char *fattn_status_string(fattn_status_t status)
 {
     switch (status) {
@@ -1054,6 +1567,7 @@ const char *fattn_status_string(fattn_status_t status)
     case FATTN_ERR_CUDA: return "FATTN_ERR_CUDA";
     case FATTN_ERR_TIMEOUT: return "FATTN_ERR_TIMEOUT";
     case FATTN_ERR_RANGE: return "FATTN_ERR_RANGE";
+    case FATTN_ERR_INDEX: return "FATTN_ERR_INDEX";
     }
     return "FATTN_UNKNOWN_STATUS";
 }
@@ -1071,7 +1585,10 @@ fattn_status_t fattn_get_device_status(int *status, struct CUstream_st *stream)
     *status = static_cast<int>(word);
     if (word == 0)
         return FATTN_OK;
-    return (word & 0xffu) == FATTN_ERR_RANGE ? FATTN_ERR_RANGE : FATTN_ERR_TIMEOUT;
+    const uint32_t code = word & 0xffu;
+    return code == FATTN_ERR_RANGE   ? FATTN_ERR_RANGE
+           : code == FATTN_ERR_INDEX ? FATTN_ERR_INDEX
+                                     : FATTN_ERR_TIMEOUT;
 }
 
 fattn_status_t fattn_selftest_wait_timeout(unsigned int limit_us, struct CUstream_st *stream)

@@ -67,7 +67,9 @@ enum DeviceRole : uint32_t {
     kRoleSoftmax = 3,
     kRoleEpilogue = 4,
     kRoleSelfTest = 5,
-    kRoleConvert = 6
+    kRoleConvert = 6,
+    kRoleRotate = 7,  // norm and rotation: a position outside the table
+    kRoleAppend = 8   // cache append: a page, position or length out of range
 };
 
 // tcgen05 / TMA kernel: one persistent CTA per SM.
@@ -108,5 +110,48 @@ cudaError_t launch_softmax_rows(const void *x, void *y, int M, int N, int dtype,
                                 cudaStream_t stream);
 cudaError_t launch_row_sum(const void *x, float *out, int M, int N, int dtype, int num_sms,
                            cudaStream_t stream);
+
+// Norm and rotation of q (index 0) and k (index 1), already validated; H[t]
+// 0: that tensor is absent.  Strides are (batch, head, token) in elements.
+// With g non-null the call is the backward pass: y receives dx, dw[t] the
+// weight gradients by way of `partial` (null when no tensor has weights).
+struct NormRopeArgs {
+    const void *x[2];
+    const void *g[2];
+    void *y[2];
+    const void *w[2];  // null: no norm
+    float *dw[2];
+    float *partial;  // backward: norm_rope_bwd_blocks x 2 x d
+    const float *table;      // [max_pos][rot]: cosines, then sines
+    const int *positions;    // [B * N], or null: 0 .. N-1
+    uint32_t *status;
+    long long x_st[2][3], g_st[2][3], y_st[2][3];
+    long long tokens;  // B * N
+    int N, H[2], d, rot, max_pos, interleaved, f16;
+    float eps;
+    // Filled in by the launch: heads an item, items of each tensor, all items.
+    int heads_per_chunk, chunks[2];
+    long long items;
+};
+cudaError_t launch_norm_rope(const NormRopeArgs &a, int num_sms, cudaStream_t stream);
+// Blocks (partials) of a backward launch at most.
+int norm_rope_bwd_blocks(int num_sms);
+
+// Append of T tokens' keys and values to a paged cache, already validated.
+// Strides in elements: k, v (token, head); caches (page, head, slot).
+struct KvAppendArgs {
+    const void *k, *v;
+    void *k_cache, *v_cache;
+    const int *page_table, *cu_q, *kv_len;
+    const float *table;  // null when rot is 0
+    uint32_t *status;
+    long long k_st[2], v_st[2], kc_st[3], vc_st[3], table_stride;
+    long long T;
+    int B, H, d, rot, max_pos, interleaved, f16;
+    int num_pages, page_shift, max_pages;
+    int heads_per_chunk, chunks;  // filled in by the launch
+    long long items;
+};
+cudaError_t launch_kv_append(const KvAppendArgs &a, int num_sms, cudaStream_t stream);
 
 }  // namespace fattn

@@ -20,13 +20,16 @@ _LIB_PATH = os.path.join(_HERE, "_build", "libfattn.so")
 
 FATTN_OK = 0
 STATUS_NAMES = {0: "FATTN_OK", 1: "FATTN_ERR_INVALID_ARG", 2: "FATTN_ERR_UNSUPPORTED",
-                3: "FATTN_ERR_CUDA", 4: "FATTN_ERR_TIMEOUT", 5: "FATTN_ERR_RANGE"}
+                3: "FATTN_ERR_CUDA", 4: "FATTN_ERR_TIMEOUT", 5: "FATTN_ERR_RANGE",
+                6: "FATTN_ERR_INDEX"}
 EXPORTED = ["attn_bwd", "attn_bwd_workspace_size", "attn_fwd", "attn_fwd_fp16", "attn_fwd_host",
             "attn_fwd_kv", "attn_fwd_kv_workspace_size", "attn_fwd_simt", "attn_fwd_strided",
             "attn_fwd_split",
             "attn_fwd_split_count", "attn_fwd_split_noalloc", "attn_fwd_split_workspace_size",
             "fattn_status_string",
-            "fattn_last_cuda_error", "fattn_get_device_status", "fattn_row_sum",
+            "fattn_kv_append", "fattn_last_cuda_error", "fattn_get_device_status",
+            "fattn_qk_norm_rope", "fattn_qk_norm_rope_bwd",
+            "fattn_qk_norm_rope_bwd_workspace_size", "fattn_row_sum",
             "fattn_selftest_wait_timeout", "fattn_set_v_conversion", "fattn_softmax_rows",
             "fattn_trim_scratch", "fattn_v_conversion_route", "fattn_version"]
 V_CONVERT = {"auto": 0, "on_chip": 1, "prepass": 2}
@@ -103,6 +106,16 @@ def load():
             f = getattr(lib, name)
             f.restype = ctypes.c_int
             f.argtypes = [vp, vp, ip, ip, ip, vp]
+        lib.fattn_qk_norm_rope.restype = ctypes.c_int
+        lib.fattn_qk_norm_rope.argtypes = [vp] * 8 + [ip] * 7 + [i64p] * 4 + [fp, ip, ip, vp]
+        lib.fattn_qk_norm_rope_bwd_workspace_size.restype = ctypes.c_size_t
+        lib.fattn_qk_norm_rope_bwd_workspace_size.argtypes = [ip]
+        lib.fattn_qk_norm_rope_bwd.restype = ctypes.c_int
+        lib.fattn_qk_norm_rope_bwd.argtypes = [vp] * 12 + [ip] * 7 + [i64p] * 6 + [
+            fp, ip, ip, vp, ctypes.c_size_t, vp]
+        lib.fattn_kv_append.restype = ctypes.c_int
+        lib.fattn_kv_append.argtypes = [vp] * 8 + [ip] * 7 + [ctypes.c_longlong, ip, ip] + \
+            [i64p] * 4 + [ip, ip, vp]
         lib.fattn_version.restype = ctypes.c_char_p
         lib.fattn_version.argtypes = []
         lib.fattn_set_v_conversion.restype = ctypes.c_int
@@ -405,7 +418,7 @@ def device_status(stream=None, device=None) -> int:
     word = ctypes.c_int(0)
     with torch.cuda.device(dev):
         st = lib.fattn_get_device_status(ctypes.byref(word), _stream_handle(stream, dev))
-    if st not in (FATTN_OK, 4, 5):
+    if st not in (FATTN_OK, 4, 5, 6):
         _check(st, "fattn_get_device_status")
     return word.value
 
@@ -459,6 +472,244 @@ def row_sum(x, out=None, stream=None):
                                   _stream_handle(stream, x.device))
     _check(st, "fattn_row_sum")
     return out
+
+
+# ------------------------------------------------------------------ serving
+# Norm and rotation, and the paged cache.  These calls run once a layer of a
+# decode step, where the host's share counts: the checks read each tensor's
+# attributes once and the device is switched only when it has to be.
+_HALF = {torch.bfloat16: 0, torch.float16: 1}
+_I64x2, _I64x3 = ctypes.c_longlong * 2, ctypes.c_longlong * 3
+
+
+def _half_tensor(name, t, dims, like=None):
+    """A 16-bit CUDA tensor of `dims` dimensions with a contiguous last one,
+    of `like`'s type and device."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("%s must be a torch.Tensor" % name)
+    if not t.is_cuda or t.dtype not in _HALF or t.dim() != dims:
+        raise ValueError("%s must be a %d-dimensional bf16 or fp16 CUDA tensor" % (name, dims))
+    if t.stride(-1) != 1 and t.shape[-1] > 1:
+        raise ValueError("%s must have a contiguous last dimension" % name)
+    if like is not None and (t.dtype != like.dtype or t.device != like.device):
+        raise ValueError("%s must have the other tensors' type and device" % name)
+    return t
+
+
+def _plain_tensor(name, t, dtype, shape, device, contiguous=True):
+    if not isinstance(t, torch.Tensor) or t.dtype != dtype or t.device != device:
+        raise ValueError("%s must be a %s tensor on %s" % (name, dtype, device))
+    if tuple(t.shape) != tuple(shape) or (contiguous and not t.is_contiguous()):
+        raise ValueError("%s must be a contiguous %s tensor" % (name, list(shape)))
+    return t
+
+
+def _rope_args(rope, d, device):
+    """(pointer, rot_dim, max_pos) of a rotation table, or none."""
+    if rope is None:
+        return 0, 0, 0
+    if not isinstance(rope, torch.Tensor) or rope.dtype != torch.float32 or rope.dim() != 2 \
+            or not rope.is_contiguous() or rope.device != device:
+        raise ValueError("rope must be a contiguous fp32 [positions, rot_dim] tensor on %s" % device)
+    if rope.shape[1] % 16 or not 0 < rope.shape[1] <= d:
+        raise ValueError("rope must have 16, 32, ... up to %d columns, got %d" % (d, rope.shape[1]))
+    return rope.data_ptr(), rope.shape[1], rope.shape[0]
+
+
+def _call(entry, device, stream, *args):
+    """Call an entry point whose last argument is the stream, with `device` current."""
+    f = getattr(load(), entry)
+    if torch.cuda.current_device() == device.index:
+        st = f(*args, _stream_handle(stream, device))
+    else:
+        with torch.cuda.device(device):
+            st = f(*args, _stream_handle(stream, device))
+    _check(st, entry)
+
+
+def _empty(shape, dtype, device, stream):
+    """A new tensor of the call's stream: memory that is freed while the call
+    still runs there is then reused only behind it."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if not isinstance(stream, torch.cuda.Stream):
+        handle = _stream_handle(stream, device)
+        stream = (torch.cuda.ExternalStream(handle, device=device) if handle
+                  else torch.cuda.default_stream(device))
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def rope_table(positions: int, rot_dim: int, theta: float = 10000.0, device="cuda"):
+    """The fp32 [positions, rot_dim] table that qk_norm_rope and kv_append
+    take: each position's rot_dim/2 cosines, then its sines, of the angles
+    p * theta^(-2 i / rot_dim).  The angles are formed in fp64: in fp32 those
+    of far positions lose their fraction."""
+    if rot_dim < 16 or rot_dim % 16:
+        raise ValueError("rot_dim must be a positive multiple of 16, got %d" % rot_dim)
+    inv = theta ** (-torch.arange(0, rot_dim, 2, dtype=torch.float64) / rot_dim)
+    ang = torch.arange(positions, dtype=torch.float64)[:, None] * inv
+    return torch.cat([ang.cos(), ang.sin()], 1).float().to(device)
+
+
+def _norm_shapes(q, k, wq, wk, rope, positions):
+    """The checks shared by both passes; q or k may be None."""
+    first = q if q is not None else k
+    if first is None:
+        raise ValueError("q and k are both None")
+    for name, t in (("q", q), ("k", k)):
+        if t is not None:
+            _half_tensor(name, t, 4, first)
+    B, _, N, d = first.shape
+    if k is not None and (k.shape[0], k.shape[2], k.shape[3]) != (B, N, d):
+        raise ValueError("q and k differ in batch, tokens or head dimension: %s %s"
+                         % (tuple(first.shape), tuple(k.shape)))
+    if d not in (64, 96, 128, 256):
+        raise ValueError("head dimension must be 64, 96, 128 or 256, got %d" % d)
+    for name, w, t in (("wq", wq, q), ("wk", wk, k)):
+        if w is not None:
+            if t is None:
+                raise ValueError("%s is given without its tensor" % name)
+            _plain_tensor(name, w, first.dtype, (d,), first.device)
+    rope_ptr, rot, max_pos = _rope_args(rope, d, first.device)
+    if positions is not None:
+        _plain_tensor("positions", positions, torch.int32, (B, N), first.device)
+    return first, B, N, d, rope_ptr, rot, max_pos
+
+
+def _ptr(t):
+    return 0 if t is None else t.data_ptr()
+
+
+def _strides3(t):
+    return None if t is None else _I64x3(*t.stride()[:3])
+
+
+def _heads(t):
+    return 0 if t is None else t.shape[1]
+
+
+def _like(name, out, t, stream):
+    """The output for t: `out` checked, or a new contiguous tensor."""
+    if t is None:
+        if out is not None:
+            raise ValueError("%s is given without its tensor" % name)
+        return None
+    if out is None:
+        return _empty(t.shape, t.dtype, t.device, stream)
+    _half_tensor(name, out, 4, t)
+    if out.shape != t.shape:
+        raise ValueError("%s must have its input's shape" % name)
+    return out
+
+
+def qk_norm_rope(q, k, wq=None, wk=None, rope=None, positions=None, eps: float = 1e-6,
+                 interleaved: bool = False, q_out=None, k_out=None, stream=None):
+    """Per-head norm and position rotation of q [B, Hq, N, d] and k
+    [B, Hk, N, d] (libfattn fattn_qk_norm_rope): bf16 or fp16 views with any
+    strides and a contiguous last dimension; either may be None.
+
+    ``wq``/``wk`` [d] are the norms' weights (None: no norm), ``rope`` the
+    fp32 [positions, rot_dim] table of rope_table (None: no rotation),
+    ``positions`` int32 [B, N] (None: 0..N-1).  ``q_out``/``k_out`` may be
+    given (the inputs themselves for in place).  Returns (q_out, k_out)."""
+    first, B, N, d, rope_ptr, rot, max_pos = _norm_shapes(q, k, wq, wk, rope, positions)
+    q_out, k_out = _like("q_out", q_out, q, stream), _like("k_out", k_out, k, stream)
+    _call("fattn_qk_norm_rope", first.device, stream, _ptr(q), _ptr(k), _ptr(q_out), _ptr(k_out),
+          _ptr(wq), _ptr(wk), rope_ptr, _ptr(positions), B, _heads(q), _heads(k), N, d, rot,
+          max_pos, _strides3(q), _strides3(k), _strides3(q_out), _strides3(k_out), eps,
+          1 if interleaved else 0, _HALF[first.dtype])
+    return q_out, k_out
+
+
+def qk_norm_rope_bwd(dq_out, dk_out, q, k, wq=None, wk=None, rope=None, positions=None,
+                     eps: float = 1e-6, interleaved: bool = False, dq=None, dk=None,
+                     workspace=None, stream=None):
+    """Gradients of qk_norm_rope for the upstream gradients dq_out, dk_out
+    (libfattn fattn_qk_norm_rope_bwd).  Returns (dq, dk, dwq, dwk): dq and dk
+    in the inputs' type, dwq and dwk fp32 [d] (None without weights)."""
+    first, B, N, d, rope_ptr, rot, max_pos = _norm_shapes(q, k, wq, wk, rope, positions)
+    for name, g, t in (("dq_out", dq_out, q), ("dk_out", dk_out, k)):
+        if (g is None) != (t is None):
+            raise ValueError("%s goes with its tensor" % name)
+        if g is not None:
+            _half_tensor(name, g, 4, first)
+            if g.shape != t.shape:
+                raise ValueError("%s must have its tensor's shape" % name)
+    dq, dk = _like("dq", dq, q, stream), _like("dk", dk, k, stream)
+    dev = first.device
+    dwq = None if wq is None else _empty(d, torch.float32, dev, stream)
+    dwk = None if wk is None else _empty(d, torch.float32, dev, stream)
+    if workspace is None and (wq is not None or wk is not None):
+        workspace = _empty(qk_norm_rope_bwd_workspace_size(d, dev), torch.uint8, dev, stream)
+    _call("fattn_qk_norm_rope_bwd", dev, stream, _ptr(dq_out), _ptr(dk_out), _ptr(q), _ptr(k),
+          _ptr(wq), _ptr(wk), rope_ptr, _ptr(positions), _ptr(dq), _ptr(dk), _ptr(dwq), _ptr(dwk),
+          B, _heads(q), _heads(k), N, d, rot, max_pos, _strides3(dq_out), _strides3(dk_out),
+          _strides3(q), _strides3(k), _strides3(dq), _strides3(dk), eps, 1 if interleaved else 0,
+          _HALF[first.dtype], _ptr(workspace), 0 if workspace is None else workspace.nbytes)
+    return dq, dk, dwq, dwk
+
+
+def qk_norm_rope_bwd_workspace_size(d: int, device=None) -> int:
+    """Scratch bytes qk_norm_rope_bwd needs with weights."""
+    with torch.cuda.device(device):
+        return int(load().fattn_qk_norm_rope_bwd_workspace_size(d))
+
+
+def _paged_lists(page_table, cu_q, kv_len, device):
+    """Checks the lists of a paged call; (sequences, pages a sequence, row stride)."""
+    for name, t, dims in (("page_table", page_table, 2), ("cu_q", cu_q, 1), ("kv_len", kv_len, 1)):
+        if not isinstance(t, torch.Tensor) or t.dtype != torch.int32 or t.dim() != dims \
+                or t.device != device:
+            raise ValueError("%s must be a %d-dimensional int32 tensor on %s" % (name, dims, device))
+    B, max_pages = page_table.shape
+    if cu_q.shape[0] != B + 1 or kv_len.shape[0] != B or not cu_q.is_contiguous() \
+            or not kv_len.is_contiguous() or (max_pages > 1 and page_table.stride(1) != 1):
+        raise ValueError("page_table [B, pages], cu_q [B + 1] and kv_len [B] do not match or are "
+                         "not contiguous: %s %s %s" % (tuple(page_table.shape), tuple(cu_q.shape),
+                                                       tuple(kv_len.shape)))
+    return B, max_pages, (page_table.stride(0) if B > 1 else max_pages)
+
+
+def _paged_cache(k_cache, v_cache, like, Hk=None):
+    _half_tensor("k_cache", k_cache, 4, like)
+    _half_tensor("v_cache", v_cache, 4, like)
+    if k_cache.shape != v_cache.shape or k_cache.shape[3] != like.shape[-1] \
+            or (Hk is not None and k_cache.shape[1] != Hk):
+        raise ValueError("k_cache and v_cache must both be [pages, Hk, page_size, d] for the call's "
+                         "heads and d, got %s %s" % (tuple(k_cache.shape), tuple(v_cache.shape)))
+    page = k_cache.shape[2]
+    if page < 16 or page & (page - 1):
+        raise ValueError("page size must be a power of two, 16 or more, got %d" % page)
+    return k_cache.shape[0], page
+
+
+def kv_append(k, v, k_cache, v_cache, page_table, cu_q, kv_len, rope=None,
+              interleaved: bool = False, stream=None):
+    """Append the new tokens' keys and values k, v [T, Hk, d] to the paged
+    cache (libfattn fattn_kv_append), the keys turned by ``rope`` at their
+    positions (None: as they are).
+
+    ``k_cache``/``v_cache`` are [pages, Hk, page_size, d] views with any
+    strides; ``page_table`` int32 [B, pages], ``cu_q`` int32 [B + 1],
+    ``kv_len`` int32 [B] (keys of each sequence, the new ones included).
+    Returns (k_cache, v_cache)."""
+    _half_tensor("k", k, 3)
+    _half_tensor("v", v, 3, k)
+    if k.shape != v.shape:
+        raise ValueError("k and v must have one shape, got %s %s" % (tuple(k.shape), tuple(v.shape)))
+    T, Hk, d = k.shape
+    if d not in (64, 96, 128, 256):
+        raise ValueError("head dimension must be 64, 96, 128 or 256, got %d" % d)
+    pages, page = _paged_cache(k_cache, v_cache, k, Hk)
+    B, max_pages, row = _paged_lists(page_table, cu_q, kv_len, k.device)
+    rope_ptr, rot, max_pos = _rope_args(rope, d, k.device)
+    _call("fattn_kv_append", k.device, stream, k.data_ptr(), v.data_ptr(), k_cache.data_ptr(),
+          v_cache.data_ptr(), page_table.data_ptr(), cu_q.data_ptr(), kv_len.data_ptr(), rope_ptr,
+          T, B, Hk, d, pages, page, max_pages, row, rot, max_pos, _I64x2(*k.stride()[:2]),
+          _I64x2(*v.stride()[:2]), _I64x3(*k_cache.stride()[:3]), _I64x3(*v_cache.stride()[:3]),
+          1 if interleaved else 0, _HALF[k.dtype])
+    return k_cache, v_cache
 
 
 def version() -> str:
