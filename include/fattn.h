@@ -472,6 +472,46 @@ fattn_status_t fattn_kv_append(const void *k, const void *v, void *k_cache, void
                                const long long *v_cache_strides, int interleaved, int dtype,
                                struct CUstream_st *stream);
 
+/*
+ * attn_fwd_paged -- attention of the new tokens over the paged cache (keys
+ * and values appended beforehand): decode steps, drafted tokens and chunks of
+ * a prompt, mixed in one call.  For new token i of sequence b (n new tokens,
+ * L = kv_len[b] keys) and query head h, whose key head is h / (Hq / Hk):
+ *
+ *   o   = sum_j softmax_j( scale * q . k_j ) v_j        over keys j < L, with
+ *   lse = log( sum_j exp( scale * q . k_j ) )           causal: j <= L - n + i
+ *
+ *   q, o      : 16-bit [T][Hq][d], element strides (token, head)
+ *   lse       : fp32 [T][Hq], contiguous
+ *   d         : 64, 96 or 128;  Hq a multiple of Hk, Hq / Hk <= 128
+ *   max_q     : at least the new tokens of every sequence (it sizes the
+ *               workspace; a sequence with more has only max_q served)
+ *   dtype     : 0 = bf16 (P and V rounded to fp16, as attn_fwd), 1 = fp16
+ *   workspace : device, 16-byte aligned, attn_fwd_paged_workspace_size(...)
+ *               bytes on the current device (0 on invalid arguments); contents
+ *               ignored on entry, undefined on exit; calls that share one must
+ *               not overlap on the device
+ *
+ * A row that sees no key gets o = 0 and lse = -inf.  Rows of o and lse from
+ * cu_q[B] on are left as they were.  Cache slots and table entries behind a
+ * sequence's last key may hold anything, NaN included.  A list value out of
+ * range (cu_q out of order or past T, more than max_q new tokens, kv_len
+ * outside 0 .. max_pages * page_size) is brought into range, a page outside
+ * [0, num_pages) reads as zeros, and FATTN_ERR_INDEX (role 1) is recorded in
+ * the device status word.  |v| >= 65520 in bf16 records FATTN_ERR_RANGE, as
+ * in attn_fwd.  Two kernels are enqueued; the lists are read when they run.
+ * Equal calls give equal bits.  Errors as for attn_fwd_strided.
+ */
+size_t attn_fwd_paged_workspace_size(int Hq, int Hk, int d, int max_q);
+fattn_status_t attn_fwd_paged(const void *q, const void *k_cache, const void *v_cache,
+                              const int *page_table, const int *cu_q, const int *kv_len, void *o,
+                              float *lse, int T, int B, int Hq, int Hk, int d, int num_pages,
+                              int page_size, int max_pages, long long page_table_stride, int max_q,
+                              const long long *q_strides, const long long *k_cache_strides,
+                              const long long *v_cache_strides, const long long *o_strides,
+                              float scale, int causal, int dtype, void *workspace,
+                              size_t workspace_bytes, struct CUstream_st *stream);
+
 /* Human-readable name of a status code (static storage, never NULL). */
 const char *fattn_status_string(fattn_status_t status);
 

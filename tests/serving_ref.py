@@ -92,12 +92,17 @@ def append(k, v, k_cache, v_cache, table, cu, kv_len, rope, interleaved):
 
 
 def paged_attention(q, k_cache, v_cache, table, cu, kv_len, causal, scale):
-    """o [T, Hq, d] and lse [T, Hq] in fp64; rows without a sequence are NaN."""
+    """o [T, Hq, d], lse [T, Hq], and what their errors are relative to: the
+    weighted sizes sum_j p_j |v_j| [T, Hq, d], each row's largest scale sum_c
+    |q_c k_c| [T, Hq] and largest |v| [T, Hq].  All fp64; rows without a
+    sequence are NaN."""
     T, Hq, d = q.shape
     Hk, page = k_cache.shape[1], k_cache.shape[2]
     G = Hq // Hk
     o = torch.full((T, Hq, d), math.nan, dtype=torch.float64)
+    size = torch.zeros((T, Hq, d), dtype=torch.float64)
     lse = torch.full((T, Hq), math.nan, dtype=torch.float64)
+    terms, vmax = torch.zeros((T, Hq), dtype=torch.float64), torch.zeros((T, Hq), dtype=torch.float64)
     for b in range(len(kv_len)):
         t0, t1, n = cu[b], cu[b + 1], kv_len[b]
         if t1 == t0:
@@ -108,13 +113,18 @@ def paged_attention(q, k_cache, v_cache, table, cu, kv_len, causal, scale):
             k = k_cache[rows, h, idx % page].double()
             v = v_cache[rows, h, idx % page].double()
             for g in range(G):
-                x = q[t0:t1, h * G + g].double() @ k.T * scale
+                at = (slice(t0, t1), h * G + g)
+                x = q[at].double() @ k.T * scale
                 if causal:
                     pos = torch.arange(n - (t1 - t0), n)
                     x = x.masked_fill(idx[None, :] > pos[:, None], -math.inf)
-                y = torch.logsumexp(x, -1) if n > 0 else torch.full((t1 - t0,), -math.inf).double()
-                lse[t0:t1, h * G + g] = y
+                if n == 0:
+                    o[at], lse[at] = 0.0, -math.inf
+                    continue
+                y = torch.logsumexp(x, -1)
                 p = torch.exp(x - torch.where(y == -math.inf, 0.0, y)[:, None])
                 p = torch.where(x == -math.inf, torch.zeros_like(p), p)
-                o[t0:t1, h * G + g] = p @ v
-    return o, lse
+                o[at], lse[at], size[at] = p @ v, y, p @ v.abs()
+                terms[at] = (q[at].double().abs() @ k.abs().T * scale).amax(-1)
+                vmax[at] = v.abs().max()
+    return o, lse, size, terms, vmax

@@ -176,3 +176,49 @@ def test_reference_gradient_against_differences():
         f = [float((dy * ref.norm_rope(x.detach(), w.detach() + s * h * t, ang, 1e-6, inter)).sum())
              for s in (1, -1)]
         assert abs((f[0] - f[1]) / (2 * h) - float((dw * t).sum())) < 1e-6
+
+
+# ------------------------------------------------------------------ paged attention
+def paged(lib, **kw):
+    a = dict(q=A, kc=A + 2 * MB, vc=A + 4 * MB, table=A + 6 * MB, cu=A + 7 * MB, kv_len=A + 8 * MB,
+             o=A + 9 * MB, lse=A + 10 * MB, T=5, B=2, Hq=4, Hk=2, d=64, pages=8, page=16, max_pages=4,
+             row=4, max_q=3, qs=(256, 64), kcs=(2048, 1024, 64), vcs=(2048, 1024, 64), os=(256, 64),
+             scale=0.125, causal=1, dtype=0, ws=A + 64 * MB, bytes=1 << 30)
+    a.update(kw)
+    return lib.attn_fwd_paged(a["q"], a["kc"], a["vc"], a["table"], a["cu"], a["kv_len"], a["o"],
+                              a["lse"], a["T"], a["B"], a["Hq"], a["Hk"], a["d"], a["pages"],
+                              a["page"], a["max_pages"], a["row"], a["max_q"], i64(a["qs"]),
+                              i64(a["kcs"]), i64(a["vcs"]), i64(a["os"]), a["scale"], a["causal"],
+                              a["dtype"], a["ws"], a["bytes"], None)
+
+
+def test_paged_attention_of_nothing_is_a_noop(lib):
+    for kw in (dict(T=0), dict(B=0), dict(Hq=0)):
+        assert paged(lib, q=0, kc=0, vc=0, table=0, cu=0, kv_len=0, o=0, lse=0, ws=0, **kw) == OK
+
+
+@pytest.mark.parametrize("kw,expect", [
+    (dict(T=-1), INVALID), (dict(B=-1), INVALID), (dict(Hq=-4), INVALID), (dict(Hk=0), INVALID),
+    (dict(Hq=5), INVALID), (dict(Hq=258, Hk=2), UNSUPPORTED), (dict(max_q=0), INVALID),
+    (dict(d=256), UNSUPPORTED), (dict(d=80), UNSUPPORTED), (dict(page=8), UNSUPPORTED),
+    (dict(page=48), UNSUPPORTED), (dict(pages=0), INVALID), (dict(page=1 << 20, max_pages=1 << 12), UNSUPPORTED),
+    (dict(dtype=2), INVALID), (dict(causal=2), INVALID), (dict(scale=0.0), INVALID),
+    (dict(scale=float("nan")), INVALID), (dict(table=0), INVALID), (dict(cu=0), INVALID),
+    (dict(kv_len=A + 8 * MB + 1), INVALID), (dict(row=3), INVALID), (dict(q=0), INVALID),
+    (dict(kc=0), INVALID), (dict(vc=A + 4 * MB + 4), INVALID), (dict(o=0), INVALID),
+    (dict(lse=0), INVALID), (dict(lse=A + 10 * MB + 2), INVALID), (dict(qs=None), INVALID),
+    (dict(os=None), INVALID), (dict(kcs=None), INVALID), (dict(qs=(256, 60)), INVALID),
+    (dict(os=(256, 32)), INVALID), (dict(os=(128, 64)), INVALID),  # rows of o overlap
+    (dict(o=A), INVALID), (dict(o=A + 64), INVALID),               # over q
+    (dict(o=A + 2 * MB), INVALID), (dict(o=A + 4 * MB), INVALID),  # over the caches
+    (dict(o=A + 6 * MB), INVALID), (dict(lse=A + 9 * MB), INVALID), (dict(lse=A + 2 * MB), INVALID),
+    (dict(lse=A + 7 * MB), INVALID), (dict(kcs=(1 << 39, 1024, 64)), INVALID),
+])
+def test_paged_attention_refusals(lib, kw, expect):
+    assert paged(lib, **kw) == expect
+
+
+def test_workspace_sizes_of_bad_arguments_are_zero(lib):
+    for args in ((0, 1, 64, 1), (4, 3, 64, 1), (4, 2, 80, 1), (4, 2, 64, 0), (-1, 1, 64, 1)):
+        assert lib.attn_fwd_paged_workspace_size(*args) == 0
+    assert lib.fattn_qk_norm_rope_bwd_workspace_size(80) == 0

@@ -7,6 +7,7 @@ raises if the library has not been built (there is no CPU fallback).
 """
 __all__ = ["attn_fwd", "attn_fwd_fp16", "attn_bwd", "attn_fwd_host", "attn_fwd_simt", "attn_fwd_split", "split_count",
            "split_workspace_size", "qk_norm_rope", "qk_norm_rope_bwd", "rope_table", "kv_append",
+           "attn_fwd_paged", "paged_workspace_size", "qk_norm_rope_bwd_workspace_size",
            "softmax_rows", "row_sum", "FattnError", "device_status",
            "library_path", "version"]
 

@@ -23,7 +23,7 @@ BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(BUILD, "libfattn.so")
 
 SOURCES = ["fattn_api.cu", "fattn_fwd_sm103.cu", "fattn_bwd_sm103.cu", "fattn_fwd_simt.cu",
-           "fattn_rowops.cu", "fattn_rope.cu"]
+           "fattn_rowops.cu", "fattn_rope.cu", "fattn_paged_sm103.cu"]
 GENCODE = ["-gencode", "arch=compute_103a,code=sm_103a"]
 EXPORTS = "{ global: attn_fwd*; attn_bwd*; fattn_*; local: *; };\n"
 

@@ -1033,6 +1033,60 @@ fattn_status_t norm_rope(const NormCall &c, bool backward, const float *rope, co
     return e == cudaSuccess ? FATTN_OK : cuda_fail(e);
 }
 
+// ---------------------------------------------------------------- paged attention
+// Workspace of a paged call: the CTAs' starts, then (256-byte aligned each)
+// the partial log-sum-exps and the partial O of two slots a CTA.
+struct PagedWs {
+    size_t l, o, bytes;
+    int slot_rows, tile_tokens;
+};
+
+PagedWs paged_ws(int Hq, int Hk, int d, int max_q, int num_sms)
+{
+    PagedWs w;
+    const int G = Hq / Hk;
+    w.tile_tokens = 128 / G;
+    w.slot_rows = max_q <= w.tile_tokens ? (max_q * G + 31) / 32 * 32 : 256;
+    w.l = align_up(static_cast<size_t>(num_sms) * sizeof(int4), kWsAlign);
+    w.o = align_up(w.l + 2ull * num_sms * w.slot_rows * 4, kWsAlign);
+    w.bytes = w.o + 2ull * num_sms * w.slot_rows * d * 4;
+    return w;
+}
+
+fattn_status_t check_heads(int Hq, int Hk, int d, int max_q)
+{
+    if (Hq < 0 || Hk < 0 || (Hq > 0 && (Hk == 0 || Hq % Hk != 0)) || max_q < 1)
+        return FATTN_ERR_INVALID_ARG;
+    if ((d != 64 && d != 96 && d != 128) || (Hq > 0 && Hq / Hk > 128))
+        return FATTN_ERR_UNSUPPORTED;
+    return FATTN_OK;
+}
+
+// 4-D tensor map of 16-bit rows of d elements, box (64, b1, b2, b3).  The
+// stride of a dimension of extent 1 is not used; it only has to be valid.
+fattn_status_t make_row_map(PFN_cuTensorMapEncodeTiled_v12000 encode, CUtensorMap *m, const void *p,
+                            int d, const long long (&ext)[3], const long long (&st)[3],
+                            const unsigned (&box_rows)[3], bool f16)
+{
+    cuuint64_t dims[4] = {static_cast<cuuint64_t>(d)}, strides[3];
+    cuuint32_t box[4] = {64};
+    const cuuint32_t elem_strides[4] = {1, 1, 1, 1};
+    for (int i = 0; i < 3; ++i) {
+        dims[i + 1] = static_cast<cuuint64_t>(ext[i]);
+        strides[i] = static_cast<cuuint64_t>(ext[i] > 1 ? st[i] : d) * 2;
+        box[i + 1] = box_rows[i];
+    }
+    const CUresult r = encode(m, f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+                              4, const_cast<void *>(p), dims, strides, box, elem_strides,
+                              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) {
+        t_last_cuda_error = static_cast<int>(r);
+        return FATTN_ERR_CUDA;
+    }
+    return FATTN_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -1555,6 +1609,126 @@ fattn_status_t fattn_kv_append(const void *k, const void *v, void *k_cache, void
     a.page_shift = __builtin_ctz(static_cast<unsigned>(page_size));
     a.max_pages = max_pages;
     const cudaError_t e = fattn::launch_kv_append(a, info.num_sms, stream);
+    return e == cudaSuccess ? FATTN_OK : cuda_fail(e);
+}
+
+size_t attn_fwd_paged_workspace_size(int Hq, int Hk, int d, int max_q)
+{
+    int dev = 0;
+    DeviceInfo info;
+    if (Hq == 0 || check_heads(Hq, Hk, d, max_q) != FATTN_OK || current_device(&dev, &info) != FATTN_OK)
+        return 0;
+    return paged_ws(Hq, Hk, d, max_q, info.num_sms).bytes;
+}
+
+fattn_status_t attn_fwd_paged(const void *q, const void *k_cache, const void *v_cache,
+                              const int *page_table, const int *cu_q, const int *kv_len, void *o,
+                              float *lse, int T, int B, int Hq, int Hk, int d, int num_pages,
+                              int page_size, int max_pages, long long page_table_stride, int max_q,
+                              const long long *q_strides, const long long *k_cache_strides,
+                              const long long *v_cache_strides, const long long *o_strides,
+                              float scale, int causal, int dtype, void *workspace,
+                              size_t workspace_bytes, struct CUstream_st *stream)
+{
+    if (T < 0 || (dtype != 0 && dtype != 1) || (causal != 0 && causal != 1))
+        return FATTN_ERR_INVALID_ARG;
+    if (!(scale > 0.f) || !isfinite(scale))
+        return FATTN_ERR_INVALID_ARG;
+    const Paging g{page_table, cu_q, kv_len, B, num_pages, page_size, max_pages, page_table_stride};
+    fattn_status_t s = check_heads(Hq, Hk, d, max_q);
+    if (s != FATTN_OK || (s = check_paging(g)) != FATTN_OK)
+        return s;
+    if (T == 0 || B == 0 || Hq == 0)
+        return FATTN_OK;
+    if ((s = check_lists(g)) != FATTN_OK)
+        return s;
+    if (!q_strides || !k_cache_strides || !v_cache_strides || !o_strides || num_pages == 0 || !lse ||
+        reinterpret_cast<uintptr_t>(lse) % 4 != 0)
+        return FATTN_ERR_INVALID_ARG;
+    const Rows rows[4] = {rows_of(q, q_strides, 2, T, Hq, 1, d),
+                          rows_of(k_cache, k_cache_strides, 3, num_pages, Hk, page_size, d),
+                          rows_of(v_cache, v_cache_strides, 3, num_pages, Hk, page_size, d),
+                          rows_of(o, o_strides, 2, T, Hq, 1, d)};
+    for (const Rows &r : rows)
+        if ((s = check_rows(r)) != FATTN_OK)
+            return s;
+    // The tensor map steps from one key head's query heads to the next's.
+    if (Hq > 1 && rows[0].st[1] > (1LL << 38) / (Hq / Hk))
+        return FATTN_ERR_UNSUPPORTED;
+    const Rows &out = rows[3];
+    const size_t lse_bytes = static_cast<size_t>(T) * Hq * 4;
+    const size_t lists[3] = {table_bytes(g), (static_cast<size_t>(B) + 1) * 4, static_cast<size_t>(B) * 4};
+    const void *list[3] = {page_table, cu_q, kv_len};
+    if (!distinct(out) || !apart(out, lse, lse_bytes))
+        return FATTN_ERR_INVALID_ARG;
+    for (int i = 0; i < 3; ++i)
+        if (!apart(out, rows[i]) || !apart(rows[i], lse, lse_bytes) || !apart(out, list[i], lists[i]) ||
+            (lists[i] > 0 && overlap(lse, lse_bytes, list[i], lists[i])))
+            return FATTN_ERR_INVALID_ARG;
+    int dev = 0;
+    DeviceInfo info;
+    const void *bufs[] = {q, k_cache, v_cache, o, lse, max_pages ? page_table : nullptr, cu_q, kv_len,
+                          workspace};
+    if ((s = check_buffers(bufs, &dev, &info)) != FATTN_OK)
+        return s;
+    const PagedWs ws = paged_ws(Hq, Hk, d, max_q, info.num_sms);
+    if (!workspace || !aligned16(workspace) || workspace_bytes < ws.bytes ||
+        overlap(workspace, ws.bytes, lse, lse_bytes))
+        return FATTN_ERR_INVALID_ARG;
+    for (int i = 0; i < 4; ++i)
+        if (!apart(rows[i], workspace, ws.bytes) ||
+            (i < 3 && lists[i] > 0 && overlap(workspace, ws.bytes, list[i], lists[i])))
+            return FATTN_ERR_INVALID_ARG;
+    PFN_cuTensorMapEncodeTiled_v12000 encode;
+    if ((s = get_encoder(&encode)) != FATTN_OK)
+        return s;
+    fattn::PagedArgs a = {};
+    if ((s = status_word(&a.status)) != FATTN_OK)
+        return s;
+    const int G = Hq / Hk;
+    const unsigned box_tokens = static_cast<unsigned>(max_q < ws.tile_tokens ? max_q : ws.tile_tokens);
+    const unsigned box_slots = static_cast<unsigned>(page_size < 128 ? page_size : 128);
+    fattn::FwdMaps maps;
+    if ((s = make_row_map(encode, &maps.q, q, d, {G, Hk, T},
+                          {rows[0].st[1], rows[0].st[1] * G, rows[0].st[0]},
+                          {static_cast<unsigned>(G), 1u, box_tokens}, dtype == 1)) != FATTN_OK)
+        return s;
+    CUtensorMap *cache[2] = {&maps.k, &maps.v};
+    for (int i = 0; i < 2; ++i) {
+        const Rows &r = rows[1 + i];
+        if ((s = make_row_map(encode, cache[i], r.p, d, {page_size, Hk, num_pages},
+                              {r.st[2], r.st[1], r.st[0]}, {box_slots, 1u, 1u}, dtype == 1)) != FATTN_OK)
+            return s;
+    }
+    uint8_t *base = static_cast<uint8_t *>(workspace);
+    a.o = o;
+    a.lse = lse;
+    a.starts = reinterpret_cast<int4 *>(base);
+    a.ws_l = reinterpret_cast<float *>(base + ws.l);
+    a.ws_o = reinterpret_cast<float *>(base + ws.o);
+    a.page_table = page_table;
+    a.cu_q = cu_q;
+    a.kv_len = kv_len;
+    a.o_st[0] = out.st[0];
+    a.o_st[1] = out.st[1];
+    a.table_stride = page_table_stride;
+    a.T = T;
+    a.B = B;
+    a.Hk = Hk;
+    a.G = G;
+    a.d = d;
+    a.f16 = dtype;
+    a.causal = causal;
+    a.max_q = max_q;
+    a.num_pages = num_pages;
+    a.page_shift = __builtin_ctz(static_cast<unsigned>(page_size));
+    a.max_keys = max_pages * page_size;
+    a.tile_tokens = ws.tile_tokens;
+    a.q_box_tokens = static_cast<int>(box_tokens);
+    a.slot_rows = ws.slot_rows;
+    a.g_inverse = (65536u + G - 1) / G;
+    a.sl2 = scale * 1.4426950408889634f;
+    const cudaError_t e = fattn::launch_paged(a, maps, info.num_sms, stream);
     return e == cudaSuccess ? FATTN_OK : cuda_fail(e);
 }
 

@@ -154,4 +154,26 @@ struct KvAppendArgs {
 };
 cudaError_t launch_kv_append(const KvAppendArgs &a, int num_sms, cudaStream_t stream);
 
+// Attention of T packed new tokens over a paged cache, already validated.
+// G = Hq / Hk query heads share a key head; a Q tile holds tile_tokens = 128
+// / G tokens, its copy q_box_tokens of them.  Strides in elements.
+struct PagedArgs {
+    void *o;
+    float *lse;
+    float *ws_o, *ws_l;  // partial O [2 SMs][slot_rows][d], base-2 lse [2 SMs][slot_rows]
+    int4 *starts;        // [SMs]: (sequence, key head, unit, key tile or 0) a CTA starts at
+    const int *page_table, *cu_q, *kv_len;
+    uint32_t *status;
+    long long o_st[2];  // token, head
+    long long table_stride;
+    int T, B, Hk, G, d, f16, causal, max_q;
+    int num_pages, page_shift, max_keys;
+    int tile_tokens, q_box_tokens, slot_rows;
+    uint32_t g_inverse;  // ceil(2^16 / G)
+    float sl2;           // scale * log2(e)
+};
+// maps.q: (d, G, Hk, T), box (64, G, 1, q_box_tokens); maps.k, v: (d, slot,
+// Hk, page), box (64, min(page_size, 128), 1, 1); 128-byte swizzle.
+cudaError_t launch_paged(const PagedArgs &a, const FwdMaps &maps, int num_sms, cudaStream_t stream);
+
 }  // namespace fattn

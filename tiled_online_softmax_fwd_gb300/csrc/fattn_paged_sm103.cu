@@ -1,0 +1,1244 @@
+// fattn_paged_sm103.cu -- attention of new tokens over a paged key/value
+// cache for GB300 (sm_103a): ragged batches, grouped heads, single tokens to
+// long chunks in one call.
+//
+// For sequence b with n new tokens, the last of its L cached keys, and query
+// head h reading key head h / G:
+//
+//   x_ij = scale q_i . k_j   for j < L and (causal) j <= L - n + i
+//   o_i  = sum_j softmax(x_i)_j v_j,    lse_i = log sum_j exp(x_ij)
+//
+// by the online softmax (running maximum m and sum l, O rescaled when m
+// grows; base 2, and m raised only past a threshold, which is exact algebra).
+//
+// Rows.  The G query heads of a key head attend to the same keys, so a Q tile
+// packs them: row r of a tile is token r / G, head r % G, 128 / G tokens a
+// tile.  A key tile is then read once for all of them: a decode step moves
+// each key once, whatever G is.
+//
+// Bound.  With few new tokens the cache's bytes (HBM); with many, the tensor
+// cores and exponentials.  One persistent CTA a SM serves both:
+//   warps 0-7    two softmax warpgroups (thread = row)
+//   warp 8       TMA producer: pages -> a ring of 128-key tiles
+//   warp 9       MMA issuer: S = Q K^T and O += P V on tcgen05
+//   warps 10-11  V in place: bf16 -> fp16 (P is fp16, and both operands of a
+//                product share one type), and zeros behind the last key: a
+//                slot no token has written may hold anything, and 0 * NaN
+//                would reach every row
+// A unit of work is a pair of Q tiles of one (sequence, key head).  Both tiles
+// use each key tile (the warpgroups alternate, one in exponentials while the
+// other's products run).  A unit with a single tile -- decode, drafts, the odd
+// last tile -- has the two warpgroups take alternate key tiles of the same Q
+// tile instead, into accumulators of their own that the epilogue merges, so
+// the chain S -> softmax -> P V of one key tile overlaps the next one's.
+//
+// Schedule.  Lengths live in device memory (a captured graph follows them),
+// so the grid finds its own work: the units' costs, in keys plus a constant
+// for a unit's start and end, have closed-form prefix sums; CTA c takes the
+// c-th of equal ranges of their total.  A range may begin or end inside a
+// unit: the unit is then split between CTAs by key tiles, each writes a
+// partial O and log-sum-exp to its slot in the workspace (at most two a CTA),
+// and combine_paged_kernel merges them in slot order.  Ranges depend only on
+// the lengths and the SM count, so equal calls give equal bits.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <float.h>
+#include <stdint.h>
+
+#include "fattn_internal.h"
+#include "ptx_sm103.cuh"
+
+namespace fattn {
+namespace {
+
+using namespace ptx;
+
+constexpr int kBM = 128;  // rows of a Q tile
+constexpr int kBN = 128;  // keys of a key tile
+constexpr int kThreads = 384;
+constexpr int kWarpLoad = 8, kWarpMma = 9, kWarpConv = 10;
+constexpr uint32_t kTmemCols = 512;
+constexpr uint64_t kWaitLimitNs = 2000000000ull;
+constexpr float kRescaleLog2 = 8.0f;
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr uint32_t kChunkBytes = kBM * 128;  // 128 rows x 64 16-bit columns
+// Cost of a unit besides its keys, in keys: its Q copy, first S and epilogue
+// take about as long as two key tiles.
+constexpr int kUnitKeys = 256;
+// A CTA's share of the work is at least this many keys: below, the merge
+// costs more than the shorter ranges save.
+constexpr int kMinShare = kUnitKeys + 2 * kBN;
+
+template <int D, bool kF16> struct Cfg {
+    static constexpr int kChunks = (D + 63) / 64;
+    static constexpr uint32_t kTileBytes = kChunks * kChunkBytes;
+    static constexpr int kStages = kChunks == 2 ? 4 : 8;
+    static constexpr uint32_t kStageOffset = (2 + kStages) * kTileBytes;  // epilogue staging
+    static constexpr uint32_t kBarsOffset = kStageOffset + 8 * 4096;
+    static constexpr uint32_t kColO0 = 256, kColO1 = 256 + D;
+};
+
+// Where a CTA starts: a unit, the keys-plus-overhead already behind in it,
+// and how much of the total cost this CTA takes.
+struct Start {
+    int b, h, p;
+    int snap;  // no split within this many key tiles of a unit's ends
+    long long y, left;
+};
+
+struct Bars {
+    uint64_t q_full[2], q_empty[2];
+    uint64_t kv_full[8], kv_empty[8], v_ready[8];
+    uint64_t s_full[2], p_half[2], p_full[2], o_full[2], o_empty[2];
+    uint64_t other_done;  // single-tile units: warpgroup 1's statistics are written
+    uint64_t drain;
+    uint32_t tmem_base;
+    int abort;
+    Start start;
+    long long warp_sum[kThreads / 32];
+    float2 other[kBM];  // (m, l) of warpgroup 1's half of a single-tile unit
+};
+
+// ------------------------------------------------------------------ schedule
+struct Seq {
+    int q0, n, L;  // first token, new tokens, keys
+};
+
+// A sequence's lists, brought into range (bad: some value was not).
+__device__ __forceinline__ Seq load_seq(const PagedArgs &a, int b, bool &bad)
+{
+    const int c0 = a.cu_q[b], c1 = a.cu_q[b + 1], kl = a.kv_len[b];
+    Seq s;
+    s.q0 = min(max(c0, 0), a.T);
+    s.n = min(max(c1, s.q0), a.T) - s.q0;
+    s.n = min(s.n, a.max_q);
+    s.L = min(max(kl, 0), a.max_keys);
+    bad = s.q0 != c0 || s.n != static_cast<long long>(c1) - c0 || s.L != kl;
+    return s;
+}
+
+__device__ __forceinline__ int tiles_of(const PagedArgs &a, const Seq &s)
+{
+    return (s.n + a.tile_tokens - 1) / a.tile_tokens;
+}
+
+// Keys that tokens before `end` see together.
+__device__ __forceinline__ int keys_seen(const PagedArgs &a, const Seq &s, int end)
+{
+    return a.causal ? max(s.L - s.n + min(end, s.n), 0) : s.L;
+}
+
+// Cost of the first p of a (sequence, head)'s units.  Under the causal mask
+// unit i sees off + (i + 1) R keys (none while that is negative), off = L - n,
+// R tokens a unit; the last one sees L.
+__device__ __forceinline__ long long cost_before(const PagedArgs &a, const Seq &s, int units, int p)
+{
+    long long c = static_cast<long long>(p) * kUnitKeys;
+    if (!a.causal)
+        return c + static_cast<long long>(p) * s.L;
+    const long long off = static_cast<long long>(s.L) - s.n, R = 2 * a.tile_tokens;
+    const long long i = max(min(p, units - 1), 0);
+    const long long z = off < 0 ? min(i, -off / R) : 0;
+    c += (i - z) * off + R * ((i * (i + 1) - z * (z + 1)) / 2);
+    return p == units && units > 0 ? c + s.L : c;
+}
+
+// Key tile that a cost of y inside a unit of `keys` keys falls on.
+__device__ __forceinline__ int tile_at(long long y, int keys, int snap)
+{
+    const int F = (keys + kBN - 1) / kBN;
+    if (y <= 0)
+        return 0;
+    if (y >= kUnitKeys + static_cast<long long>(keys))
+        return F;
+    const int t = y < kUnitKeys ? 0 : static_cast<int>((y - kUnitKeys) / kBN);
+    return t < snap ? 0 : F - t < snap ? F : t;
+}
+
+// The whole block finds this CTA's start: each thread sums the costs of a run
+// of sequences, a scan gives the total and every run's place, and the thread
+// whose run holds the CTA's first cost walks it.
+__device__ void find_start(const PagedArgs &a, Bars &b)
+{
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid / 32;
+    const int per = (a.B + kThreads - 1) / kThreads;
+    const int b0 = min(tid * per, a.B), b1 = min(b0 + per, a.B);
+    long long sum = 0;
+    bool any_bad = false;
+    for (int i = b0; i < b1; ++i) {
+        bool bad;
+        const Seq s = load_seq(a, i, bad);
+        any_bad = any_bad || bad;
+        const int units = (tiles_of(a, s) + 1) / 2;
+        sum += a.Hk * cost_before(a, s, units, units);
+    }
+    if (any_bad && blockIdx.x == 0)
+        atomicCAS(a.status, 0u, 6u /* FATTN_ERR_INDEX */ | (kRoleLoad << 8));
+    long long incl = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o *= 2) {
+        const long long x = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o)
+            incl += x;
+    }
+    if (lane == 31)
+        b.warp_sum[warp] = incl;
+    if (tid == 0) {
+        b.start.b = -1;
+        b.start.left = 0;
+    }
+    __syncthreads();
+    long long before = incl - sum, total = 0;
+#pragma unroll
+    for (int w = 0; w < kThreads / 32; ++w) {
+        before += w < warp ? b.warp_sum[w] : 0;
+        total += b.warp_sum[w];
+    }
+    const long long shares = min(static_cast<long long>(gridDim.x), max(total / kMinShare, 1LL));
+    const long long lo = blockIdx.x * total / shares, hi = (blockIdx.x + 1) * total / shares;
+    if (blockIdx.x < shares && lo < hi && before <= lo && lo < before + sum) {
+        long long x = lo - before;
+        for (int i = b0; i < b1; ++i) {
+            bool bad;
+            const Seq s = load_seq(a, i, bad);
+            const int units = (tiles_of(a, s) + 1) / 2;
+            const long long head = cost_before(a, s, units, units);
+            if (x >= head * a.Hk) {
+                x -= head * a.Hk;
+                continue;
+            }
+            Start st;
+            st.b = i;
+            st.h = static_cast<int>(x / head);
+            x -= st.h * head;
+            int p = 0, end = units;  // largest p with cost_before(p) <= x
+            while (end - p > 1) {
+                const int mid = (p + end) / 2;
+                if (cost_before(a, s, units, mid) <= x)
+                    p = mid;
+                else
+                    end = mid;
+            }
+            st.p = p;
+            st.y = x - cost_before(a, s, units, p);
+            st.left = hi - lo;
+            st.snap = max(2, static_cast<int>(min(total / shares / (32 * kBN), 1LL << 20)));
+            b.start = st;
+            const int keys = keys_seen(a, s, (p + 1) * 2 * a.tile_tokens);
+            const int t = tile_at(st.y, keys, st.snap);
+            const bool split = t > 0 && t < (keys + kBN - 1) / kBN;
+            a.starts[blockIdx.x] = make_int4(st.b, st.h, st.p, split ? t : 0);
+            break;
+        }
+    }
+    if (tid == 0 && (blockIdx.x >= shares || lo >= hi))
+        a.starts[blockIdx.x] = make_int4(-1, 0, 0, 0);
+}
+
+// A piece of work: key tiles [j0, j1) of a unit.
+struct Piece {
+    int b, h, p;
+    Seq s;
+    int j0, j1;
+    int slot;     // workspace slot of a partial result, or -1: the whole unit
+    bool alt;     // one Q tile: the warpgroups take alternate key tiles
+    int tile[2];  // Q tile of each warpgroup
+    int rows[2];  // its rows (0: absent)
+    int n[2];     // its key tiles in this piece
+};
+
+// The same value on every lane of a converged warp, passed through a shuffle.
+// Copy coordinates and descriptors are read from uniform registers; with a
+// loop whose trip count comes from memory around it, a coordinate computed
+// from values loaded outside the loop reached the copy without one of its
+// terms (the rows of a later unit were then some other tokens'), although
+// every lane held the right sum.  Shuffled values are read afresh.
+__device__ __forceinline__ int uniform(int x)
+{
+    return __shfl_sync(0xffffffffu, x, 0);
+}
+
+// The pieces of this CTA in order; every role walks the same ones.
+struct Walk {
+    Start at;
+    Seq s;
+    bool loaded;
+};
+__device__ __forceinline__ bool next_piece(const PagedArgs &a, Walk &w, Piece &u)
+{
+    while (w.at.left > 0 && w.at.b >= 0 && w.at.b < a.B) {
+        bool bad;
+        if (!w.loaded)
+            w.s = load_seq(a, w.at.b, bad);
+        w.loaded = true;
+        const int tiles = tiles_of(a, w.s);
+        const int units = (tiles + 1) / 2;
+        if (w.at.p >= units) {  // past the head's (or an empty sequence's) last unit
+            w.at.p = 0;
+            if (units == 0 || ++w.at.h >= a.Hk) {
+                w.at.h = 0;
+                ++w.at.b;
+                w.loaded = false;
+            }
+            continue;
+        }
+        const int R = 2 * a.tile_tokens;
+        const int keys = keys_seen(a, w.s, (w.at.p + 1) * R);
+        const int F = (keys + kBN - 1) / kBN;
+        const long long cost = kUnitKeys + static_cast<long long>(keys);
+        const long long y0 = w.at.y, y1 = min(y0 + w.at.left, cost);
+        u.b = w.at.b;
+        u.h = w.at.h;
+        u.p = w.at.p;
+        u.s = w.s;
+        u.j0 = tile_at(y0, keys, w.at.snap);
+        u.j1 = tile_at(y1, keys, w.at.snap);
+        w.at.left -= y1 - y0;
+        w.at.y = 0;
+        ++w.at.p;
+        // Nothing of this unit falls to this CTA (a unit without keys belongs
+        // to the CTA that holds its start).
+        if (F == 0 ? y0 > 0 : u.j0 == u.j1)
+            continue;
+        u.slot = u.j0 > 0 ? 2 * blockIdx.x : u.j1 < F ? 2 * blockIdx.x + 1 : -1;
+        u.alt = 2 * u.p + 1 >= tiles;
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+            u.tile[t] = u.alt ? 2 * u.p : 2 * u.p + t;
+            const int first = u.tile[t] * a.tile_tokens;
+            u.rows[t] = min(a.tile_tokens, u.s.n - first) * a.G;
+            if (u.alt) {
+                u.n[t] = (u.j1 - u.j0 + 1 - t) / 2;
+            } else {
+                const int ft = (keys_seen(a, u.s, first + a.tile_tokens) + kBN - 1) / kBN;
+                u.n[t] = max(min(u.j1, ft) - u.j0, 0);
+            }
+            u.tile[t] = uniform(u.tile[t]);
+            u.rows[t] = uniform(u.rows[t]);
+            u.n[t] = uniform(u.n[t]);
+        }
+        u.b = uniform(u.b);
+        u.h = uniform(u.h);
+        u.p = uniform(u.p);
+        u.s.q0 = uniform(u.s.q0);
+        u.s.n = uniform(u.s.n);
+        u.s.L = uniform(u.s.L);
+        u.j0 = uniform(u.j0);
+        u.j1 = uniform(u.j1);
+        return true;
+    }
+    return false;
+}
+__device__ __forceinline__ Walk first_walk(const Bars &b)
+{
+    Walk w;
+    w.at = b.start;
+    w.loaded = false;
+    return w;
+}
+
+__device__ __forceinline__ void record_failure(const PagedArgs &a, Bars &b, uint32_t role)
+{
+    const uint32_t code = 4u /* FATTN_ERR_TIMEOUT */ | (role << 8) | ((blockIdx.x & 0xffffu) << 16);
+    atomicCAS(a.status, 0u, code);
+    *reinterpret_cast<volatile int *>(&b.abort) = 1;
+}
+
+// Waits by a whole warp; the outcome is uniform.
+__device__ __forceinline__ bool warp_wait(uint64_t &bar, uint32_t parity, const volatile int *abort)
+{
+    const bool ok = mbar_wait(smem_addr(&bar), parity, kWaitLimitNs, abort);
+    return __all_sync(0xffffffffu, ok);
+}
+
+template <bool kF16> __device__ __forceinline__ uint32_t pack2(float lo, float hi)
+{
+    if constexpr (kF16) {
+        const __half2 v = __floats2half2_rn(lo, hi);
+        return *reinterpret_cast<const uint32_t *>(&v);
+    } else {
+        const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+        return *reinterpret_cast<const uint32_t *>(&v);
+    }
+}
+
+// ------------------------------------------------------------------ producer
+// K_j and V_j alternate through the ring, V on the odd stages.  A tile is 8
+// pages of 16 slots down to part of one, a copy a page and 64-column box, all
+// issued by one elected lane; the warp holds 32 table entries and the next 32.
+template <int D, bool kF16>
+__device__ void run_load(const PagedArgs &a, Bars &b, uint32_t smem_base, const CUtensorMap *mq,
+                         const CUtensorMap *mk, const CUtensorMap *mv)
+{
+    using C = Cfg<D, kF16>;
+    const volatile int *abort = &b.abort;
+    const int lane = threadIdx.x & 31;
+    const bool leader = elect_one();
+    const int shift = a.page_shift;
+    const int per_tile = shift < 7 ? kBN >> shift : 1;  // pages a key tile touches
+    const int box_rows = shift < 7 ? 1 << shift : kBN;
+    const uint32_t q_bytes = C::kChunks * a.q_box_tokens * a.G * 128u;
+    uint32_t q_phase[2] = {0, 0}, pos = 0;
+    int last_q[2] = {-1, -1};
+    bool ok = true;
+    Walk w = first_walk(b);
+    Piece u;
+    while (ok && next_piece(a, w, u)) {
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+            if (!ok || u.n[t] == 0 || (u.alt && t == 1))
+                continue;
+            ok = warp_wait(b.q_empty[t], q_phase[t] ^ 1, abort);
+            if (!ok)
+                continue;
+            if (leader) {
+                const uint32_t full = smem_addr(&b.q_full[t]);
+                mbar_arrive_expect_tx(full, q_bytes);
+#pragma unroll
+                for (int c = 0; c < C::kChunks; ++c)
+                    tma_load_4d(smem_base + t * C::kTileBytes + c * kChunkBytes, mq, full, 64 * c, 0,
+                                u.h, u.s.q0 + u.tile[t] * a.tile_tokens);
+            }
+            last_q[t] = q_phase[t];
+            q_phase[t] ^= 1;
+        }
+        pos = uniform(pos);
+        const int pages = (u.s.L + (1 << shift) - 1) >> shift;  // of the sequence
+        const int *row = a.page_table + static_cast<long long>(u.b) * a.table_stride;
+        auto entries = [&](int first) { return first + lane < pages ? row[first + lane] : 0; };
+        int held = static_cast<int>((static_cast<long long>(u.j0) * kBN) >> shift);
+        int cur = entries(held), ahead = entries(held + 32);
+        for (int j = u.j0; ok && j < u.j1; ++j) {
+            const int p0 = (j * kBN) >> shift;
+            if (p0 >= held + 32) {  // 32 is a multiple of per_tile
+                held += 32;
+                cur = ahead;
+                ahead = entries(held + 32);
+            }
+            const int count = min(per_tile, pages - p0);
+            // This lane's entry, brought into range: a page outside the pool
+            // becomes the one behind it, which the copy fills with zeros.
+            const bool stray = cur < 0 || cur >= a.num_pages;
+            const int entry = stray ? a.num_pages : cur;
+            if (stray && lane >= p0 - held && lane < p0 - held + count)
+                atomicCAS(a.status, 0u,
+                          6u /* FATTN_ERR_INDEX */ | (kRoleLoad << 8) | ((blockIdx.x & 0xffffu) << 16));
+            const int slot = shift < 7 ? 0 : (j * kBN) & ((1 << shift) - 1);
+#pragma unroll
+            for (int which = 0; which < 2; ++which, ++pos) {
+                const uint32_t stage = pos % C::kStages;
+                ok = ok && warp_wait(b.kv_empty[stage], ((pos / C::kStages) & 1) ^ 1, abort);
+                if (!ok)
+                    break;
+                const uint32_t full = smem_addr(&b.kv_full[stage]);
+                uint32_t dst = smem_base + (2 + stage) * C::kTileBytes;
+                if (leader)
+                    mbar_arrive_expect_tx(full, count * box_rows * 128u * C::kChunks);
+                for (int i = 0; i < count; ++i, dst += box_rows * 128) {
+                    const int page = __shfl_sync(0xffffffffu, entry, p0 - held + i);
+                    if (leader) {
+#pragma unroll
+                        for (int c = 0; c < C::kChunks; ++c)
+                            tma_load_4d(dst + c * kChunkBytes, which == 0 ? mk : mv, full, 64 * c, slot,
+                                        u.h, page);
+                    }
+                }
+            }
+        }
+    }
+    if (!ok) {
+        if (leader)
+            record_failure(a, b, kRoleLoad);
+        // Copies already issued land before the CTA exits.
+        const uint32_t first = pos > (uint32_t)C::kStages ? pos - C::kStages : 0;
+        for (uint32_t q = first; q < pos; ++q)
+            mbar_wait(smem_addr(&b.kv_full[q % C::kStages]), (q / C::kStages) & 1, kWaitLimitNs / 8,
+                      nullptr);
+        for (int t = 0; t < 2; ++t)
+            if (last_q[t] >= 0)
+                mbar_wait(smem_addr(&b.q_full[t]), last_q[t], kWaitLimitNs / 8, nullptr);
+    }
+}
+
+// ------------------------------------------------------------------ V in place
+// Exact for |v| < 65520 down to fp16's subnormals (off by at most 2^-25); a
+// larger v becomes infinite, which the epilogue reports.
+__device__ __forceinline__ uint32_t bf16x2_to_f16x2(uint32_t w)
+{
+    const __half2 h = __floats2half2_rn(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+__device__ __forceinline__ uint4 bf16x8_to_f16x8(uint4 w)
+{
+    return make_uint4(bf16x2_to_f16x2(w.x), bf16x2_to_f16x2(w.y), bf16x2_to_f16x2(w.z),
+                      bf16x2_to_f16x2(w.w));
+}
+
+// One V tile by 64 threads: rows from `valid` on become zero, the others are
+// converted (bf16).  Eight 16-byte steps in flight a thread; a thread writes
+// only what it read.
+template <int D, bool kF16, bool kRagged>
+__device__ __forceinline__ void fix_v_tile(uint4 *tile, int tid, int valid)
+{
+    constexpr int kVecs = Cfg<D, kF16>::kTileBytes / 16, kBatch = 8;
+#pragma unroll 1
+    for (int base = tid; base < kVecs; base += 64 * kBatch) {
+        uint4 x[kBatch];
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i)
+            x[i] = tile[base + i * 64];
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+            const int at = base + i * 64;
+            const bool keep = !kRagged || ((at / 8) % kBN) < valid;
+            const uint4 y = kF16 ? x[i] : bf16x8_to_f16x8(x[i]);
+            tile[at] = keep ? y : make_uint4(0, 0, 0, 0);
+        }
+    }
+}
+
+template <int D, bool kF16>
+__device__ void run_convert(const PagedArgs &a, Bars &b, uint8_t *tiles, int cw)
+{
+    using C = Cfg<D, kF16>;
+    const volatile int *abort = &b.abort;
+    const int lane = threadIdx.x & 31, tid = cw * 32 + lane;
+    uint32_t pos = 0;
+    bool ok = true;
+    Walk w = first_walk(b);
+    Piece u;
+    while (ok && next_piece(a, w, u)) {
+        for (int j = u.j0; ok && j < u.j1; ++j, pos += 2) {
+            const uint32_t at = pos + 1, stage = at % C::kStages;
+            const int valid = u.s.L - j * kBN;
+            // Every copy is waited for: a waiter that ran two rounds of the
+            // ring ahead would take an older phase for its own.
+            ok = warp_wait(b.kv_full[stage], (at / C::kStages) & 1, abort);
+            if (!ok)
+                break;
+            if (kF16 && valid >= kBN)
+                continue;  // whole fp16 tiles are used as they land
+            uint4 *tile = reinterpret_cast<uint4 *>(tiles + (2 + stage) * C::kTileBytes);
+            if (valid < kBN)
+                fix_v_tile<D, kF16, true>(tile, tid, valid);
+            else
+                fix_v_tile<D, kF16, false>(tile, tid, valid);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(smem_addr(&b.v_ready[stage]));
+        }
+    }
+    if (!ok && lane == 0)
+        record_failure(a, b, kRoleConvert);
+}
+
+// ------------------------------------------------------------------ MMA issue
+// S = Q K^T: both operands K-major, 128-byte swizzled, 8-row groups 1024
+// bytes apart; a K = 16 step is 32 bytes along d, or the next 16 KB box.
+template <int D, bool kF16>
+__device__ __forceinline__ void issue_s(uint32_t tmem_d, uint32_t q_smem, uint32_t k_smem)
+{
+    constexpr uint32_t idesc = idesc_f32acc(kBM, kBN, false, kF16);
+    constexpr uint32_t hi = smem_desc_hi(1024);
+    const uint32_t a_lo = smem_desc_lo(q_smem, 16), b_lo = smem_desc_lo(k_smem, 16);
+#pragma unroll
+    for (int kk = 0; kk < D / 16; ++kk) {
+        const uint32_t off = ((kk >> 2) * kChunkBytes + (kk & 3) * 32) >> 4;
+        mma_ss_w(tmem_d, a_lo + off, hi, b_lo + off, hi, idesc, kk > 0 ? 1u : 0u);
+    }
+}
+
+// O (+)= P V, K-steps [kK0, kK1) of 16 keys: P from TMEM, V MN-major (64-column
+// boxes 16 KB apart), both fp16.
+template <int D, int kK0, int kK1>
+__device__ __forceinline__ void issue_pv(uint32_t tmem_d, uint32_t tmem_p, uint32_t v_smem,
+                                         bool accumulate)
+{
+    constexpr uint32_t idesc = idesc_f32acc(kBM, D, true, true);
+    constexpr uint32_t hi = smem_desc_hi(1024);
+    const uint32_t b_lo = smem_desc_lo(v_smem, D > 64 ? kChunkBytes : 1024);
+#pragma unroll
+    for (int kk = kK0; kk < kK1; ++kk)
+        mma_ts_w(tmem_d, tmem_p + kk * 8, b_lo + ((kk * 16 * 128) >> 4), hi, idesc,
+                 kk > 0 || accumulate ? 1u : 0u);
+}
+
+template <int D, bool kF16>
+__device__ void run_mma(const PagedArgs &a, Bars &b, uint32_t smem_base, uint32_t tmem)
+{
+    using C = Cfg<D, kF16>;
+    const volatile int *abort = &b.abort;
+    const bool leader = elect_one();
+    uint32_t q_phase[2] = {0, 0}, p_phase[2] = {0, 0}, oe_phase[2] = {0, 0}, vr_bits = 0;
+    uint32_t pos = 0;
+    bool ok = true;
+    auto stage_of = [&](uint32_t at) { return at % C::kStages; };
+    auto kv_smem = [&](uint32_t at) { return smem_base + (2 + stage_of(at)) * C::kTileBytes; };
+    auto k_wait = [&](uint32_t at) {
+        return warp_wait(b.kv_full[stage_of(at)], (at / C::kStages) & 1, abort);
+    };
+    auto v_wait = [&](uint32_t at, bool whole) {
+        if (kF16 && whole)
+            return k_wait(at);
+        const uint32_t st = stage_of(at);
+        const bool r = warp_wait(b.v_ready[st], (vr_bits >> st) & 1u, abort);
+        vr_bits ^= 1u << st;
+        return r;
+    };
+    auto commit = [&](uint64_t &bar) {
+        if (leader)
+            mma_commit(smem_addr(&bar));
+    };
+    // P V of one key tile into warpgroup t's accumulator, the keys in two
+    // halves: the first as soon as its P is written.
+    auto pv = [&](int t, uint32_t at_v, bool first) {
+        const uint32_t col_s = tmem + (t == 0 ? 0u : 128u);
+        const uint32_t col_o = tmem + (t == 0 ? C::kColO0 : C::kColO1);
+        bool r = warp_wait(b.p_half[t], p_phase[t], abort);
+        if (r && first) {  // overwrites O: the last unit's has to be read
+            r = warp_wait(b.o_empty[t], oe_phase[t] ^ 1, abort);
+            oe_phase[t] ^= 1;
+        }
+        if (!r)
+            return false;
+        tc_fence_after();
+        if (leader)
+            issue_pv<D, 0, kBN / 32>(col_o, col_s, kv_smem(at_v), !first);
+        r = warp_wait(b.p_full[t], p_phase[t], abort);
+        p_phase[t] ^= 1;
+        if (!r)
+            return false;
+        tc_fence_after();
+        if (leader)
+            issue_pv<D, kBN / 32, kBN / 16>(col_o, col_s, kv_smem(at_v), true);
+        return true;
+    };
+    auto s_product = [&](int t, int q_tile, uint32_t at_k) {
+        if (leader)
+            issue_s<D, kF16>(tmem + (t == 0 ? 0u : 128u), smem_base + q_tile * C::kTileBytes,
+                             kv_smem(at_k));
+        commit(b.s_full[t]);
+    };
+
+    Walk w = first_walk(b);
+    Piece u;
+    while (ok && next_piece(a, w, u)) {
+        const int n = u.j1 - u.j0;
+        if (n == 0)
+            continue;
+        const uint32_t base = uniform(pos);  // K_(j0+i) at base + 2i, V_(j0+i) at base + 2i + 1
+        pos = base + 2 * n;
+        auto whole = [&](int i) { return (u.j0 + i + 1) * kBN <= u.s.L; };
+        if (u.alt) {
+            ok = warp_wait(b.q_full[0], q_phase[0], abort);
+            q_phase[0] ^= 1;
+            for (int i = 0; ok && i < min(n, 2); ++i) {
+                ok = k_wait(base + 2 * i);
+                if (!ok)
+                    break;
+                tc_fence_after();
+                s_product(i, 0, base + 2 * i);
+                commit(b.kv_empty[stage_of(base + 2 * i)]);
+                if (i == n - 1)
+                    commit(b.q_empty[0]);
+            }
+            for (int i = 0; ok && i < n; ++i) {
+                const int t = i & 1;
+                const uint32_t at_v = base + 2 * i + 1, at_k = base + 2 * (i + 2);
+                ok = v_wait(at_v, whole(i)) && pv(t, at_v, i < 2);
+                if (!ok)
+                    break;
+                commit(b.kv_empty[stage_of(at_v)]);
+                if (i + 2 >= n) {
+                    commit(b.o_full[t]);
+                    continue;
+                }
+                ok = k_wait(at_k);
+                if (!ok)
+                    break;
+                tc_fence_after();
+                s_product(t, 0, at_k);
+                commit(b.kv_empty[stage_of(at_k)]);
+                if (i + 2 == n - 1)
+                    commit(b.q_empty[0]);
+            }
+            continue;
+        }
+        for (int t = 0; t < 2 && ok; ++t)
+            if (u.n[t] > 0) {
+                ok = warp_wait(b.q_full[t], q_phase[t], abort);
+                q_phase[t] ^= 1;
+            }
+        ok = ok && k_wait(base);
+        if (!ok)
+            break;
+        tc_fence_after();
+        for (int t = 0; t < 2; ++t) {
+            if (u.n[t] == 0)
+                continue;
+            s_product(t, t, base);
+            if (u.n[t] == 1)
+                commit(b.q_empty[t]);
+        }
+        commit(b.kv_empty[stage_of(base)]);
+        for (int i = 0; i < n && ok; ++i) {
+            const uint32_t at_v = base + 2 * i + 1, at_k = base + 2 * (i + 1);
+            const bool more = i + 1 < n;
+            ok = v_wait(at_v, whole(i)) && (!more || k_wait(at_k));
+            for (int t = 0; t < 2 && ok; ++t) {
+                if (i >= u.n[t])
+                    continue;
+                ok = pv(t, at_v, i == 0);
+                if (!ok)
+                    break;
+                if (i + 1 < u.n[t]) {
+                    s_product(t, t, at_k);
+                    if (i + 2 == u.n[t])
+                        commit(b.q_empty[t]);
+                } else {
+                    commit(b.o_full[t]);
+                }
+            }
+            if (!ok)
+                break;
+            commit(b.kv_empty[stage_of(at_v)]);
+            if (more)
+                commit(b.kv_empty[stage_of(at_k)]);
+        }
+    }
+    if (!ok && leader)
+        record_failure(a, b, kRoleMma);
+    commit(b.drain);
+    mbar_wait(smem_addr(&b.drain), 0, kWaitLimitNs, nullptr);
+}
+
+// ------------------------------------------------------------------ softmax
+// One key tile of one row: S from TMEM, mask (keys past `limit`, an index in
+// the tile), row maximum, P (fp16) over the first 64 columns of S, l.
+// pre(alpha) runs before any P is written, mid() once P of 64 keys is.
+template <class Pre, class Mid>
+__device__ __forceinline__ float softmax_tile(float sl2, uint32_t t_s, bool masked, int limit,
+                                              bool first, float m, float &m_new, float &l, Pre pre,
+                                              Mid mid)
+{
+    uint32_t raw[kBN / 32][32];
+    float cmax[kBN / 32];
+#pragma unroll
+    for (int c = 0; c < kBN / 32; ++c)
+        tmem_ld32_max(t_s + c * 32, raw[c], cmax[c]);
+    tmem_wait_ld();
+    float s[kBN];
+#pragma unroll
+    for (int i = 0; i < kBN; ++i)
+        s[i] = __uint_as_float(raw[i / 32][i % 32]);
+    float smax = fmaxf(fmaxf(cmax[0], cmax[1]), fmaxf(cmax[2], cmax[3]));
+    if (masked) {  // uniform in the warp
+#pragma unroll
+        for (int i = 0; i < kBN; ++i)
+            s[i] = i > limit ? -INFINITY : s[i];
+        float mx[4] = {fmaxf(s[0], s[1]), fmaxf(s[2], s[3]), fmaxf(s[4], s[5]), fmaxf(s[6], s[7])};
+#pragma unroll
+        for (int i = 8; i < kBN; i += 8) {
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+                mx[c] = fmax3(mx[c], s[i + 2 * c], s[i + 2 * c + 1]);
+        }
+        smax = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+    }
+    // m starts at -FLT_MAX: a row that sees no key keeps it, with l = 0.
+    const float cand = smax * sl2;
+    m_new = (first || cand > m + kRescaleLog2) ? fmaxf(m, cand) : m;
+    const float alpha = ex2(m - m_new);
+    pre(alpha);
+    const uint64_t sl2x2 = f2_pack(sl2, sl2), negm = f2_pack(-m_new, -m_new);
+    uint64_t sum[2] = {f2_pack(0.f, 0.f), f2_pack(0.f, 0.f)};
+#pragma unroll
+    for (int c = 0; c < kBN / 32; ++c) {
+        uint32_t pk[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            float x0, x1;
+            f2_unpack(f2_fma(f2_pack(s[c * 32 + 2 * i], s[c * 32 + 2 * i + 1]), sl2x2, negm), x0, x1);
+            const float p0 = ex2(x0), p1 = ex2(x1);
+            pk[i] = pack2<true>(p0, p1);
+            sum[i & 1] = f2_add(sum[i & 1], f2_pack(p0, p1));
+        }
+        tmem_st16(t_s + c * 16, pk);
+        if (c == kBN / 64 - 1)
+            mid();
+    }
+    float e0, e1, e2, e3;
+    f2_unpack(sum[0], e0, e1);
+    f2_unpack(sum[1], e2, e3);
+    l = l * alpha + ((e0 + e1) + (e2 + e3));
+    return alpha;
+}
+
+template <int D> __device__ __forceinline__ void rescale_o(uint32_t t_o, float alpha)
+{
+    const uint64_t alpha2 = f2_pack(alpha, alpha);
+    uint32_t o[D / 32][32];
+#pragma unroll
+    for (int c = 0; c < D / 32; ++c)
+        tmem_ld32(t_o + c * 32, o[c]);
+    tmem_wait_ld();
+#pragma unroll
+    for (int c = 0; c < D / 32; ++c) {
+#pragma unroll
+        for (int i = 0; i < 32; i += 2) {
+            float x, y;
+            f2_unpack(f2_mul(f2_pack(__uint_as_float(o[c][i]), __uint_as_float(o[c][i + 1])), alpha2),
+                      x, y);
+            o[c][i] = __float_as_uint(x);
+            o[c][i + 1] = __float_as_uint(y);
+        }
+        tmem_st32(t_o + c * 32, o[c]);
+    }
+}
+
+// Row stores go through 4 KB of staging a warp: thread r puts a 128-byte
+// piece of its row into staging row r, granule g at g ^ (r % 8), and eight
+// lanes a row copy whole lines out.
+__device__ __forceinline__ void stage_put(uint8_t *stage, int lane, int g, uint4 v)
+{
+    reinterpret_cast<uint4 *>(stage + lane * 128)[g ^ (lane & 7)] = v;
+}
+// at(row): destination of staging row `row`, or nullptr; half: 64-byte pieces.
+template <class At>
+__device__ __forceinline__ void stage_flush(const uint8_t *stage, int lane, bool half, At at)
+{
+    __syncwarp();
+    const int g = half ? lane % 4 : lane % 8, step = half ? 8 : 4;
+    for (int row = half ? lane / 4 : lane / 8; row < 32; row += step) {
+        const uint4 x = reinterpret_cast<const uint4 *>(stage + row * 128)[g ^ (row & 7)];
+        char *dst = at(row);
+        if (dst != nullptr)
+            *reinterpret_cast<uint4 *>(dst + g * 16) = x;
+    }
+    __syncwarp();
+}
+
+// Row r of a tile: token r / G, head r % G, by a multiplication (exact for r
+// < 128 and G <= 128).
+__device__ __forceinline__ int row_token(const PagedArgs &a, int r)
+{
+    return static_cast<int>((static_cast<uint32_t>(r) * a.g_inverse) >> 16);
+}
+
+// Writes warp rows [r0, r0 + 32) of tile t of the piece: O = w0 O_t0 + w1
+// O_t1 (single-tile units merge two accumulators; w1 is ignored otherwise) and
+// the base-2 log-sum-exp lse2.  To o and lse, or to the piece's slot.
+template <int D, bool kF16>
+__device__ __forceinline__ void write_rows(const PagedArgs &a, const Piece &u, int t, int r0,
+                                           uint32_t t_o0, uint32_t t_o1, bool two, float w0, float w1,
+                                           float lse2, bool some, uint8_t *stage)
+{
+    const int lane = threadIdx.x & 31, rows = u.rows[t];
+    const bool live = r0 + lane < rows;
+    const int first = u.s.q0 + u.tile[t] * a.tile_tokens;
+    const long long out0 = static_cast<long long>(first) * a.o_st[0] +
+                           static_cast<long long>(u.h) * a.G * a.o_st[1];
+    const long long slot_row = static_cast<long long>(u.slot) * a.slot_rows + (u.alt ? 0 : t * kBM) + r0;
+    auto out_row = [&](int row) -> char * {
+        const int r = r0 + row;
+        if (r >= rows)
+            return nullptr;
+        const int tok = row_token(a, r), g = r - tok * a.G;
+        return reinterpret_cast<char *>(static_cast<uint16_t *>(a.o) + out0 + tok * a.o_st[0] +
+                                        g * a.o_st[1]);
+    };
+    auto slot_at = [&](int row) -> char * {
+        return r0 + row < rows ? reinterpret_cast<char *>(a.ws_o + (slot_row + row) * D) : nullptr;
+    };
+    // A sum over the row of O is finite unless some element is not: |O| < 2^8
+    // keys * 65504.
+    float nonfinite = 0.f;
+#pragma unroll 1
+    for (int c = 0; c < D / 32; ++c) {
+        float y[32];
+        if (some) {
+            uint32_t o[32];
+            tmem_ld32(t_o0 + c * 32, o);
+            tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+                y[i] = __uint_as_float(o[i]) * w0;
+            if (two) {
+                tmem_ld32(t_o1 + c * 32, o);
+                tmem_wait_ld();
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                    y[i] = fmaf(__uint_as_float(o[i]), w1, y[i]);
+            }
+            if (!kF16) {
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                    nonfinite += y[i];
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+                y[i] = 0.f;
+        }
+        if (u.slot < 0) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                stage_put(stage, lane, (c % 2) * 4 + i,
+                          make_uint4(pack2<kF16>(y[8 * i], y[8 * i + 1]),
+                                     pack2<kF16>(y[8 * i + 2], y[8 * i + 3]),
+                                     pack2<kF16>(y[8 * i + 4], y[8 * i + 5]),
+                                     pack2<kF16>(y[8 * i + 6], y[8 * i + 7])));
+            if (c % 2 == 1 || c + 1 == D / 32)
+                stage_flush(stage, lane, c % 2 == 0, [&](int row) {
+                    char *dst = out_row(row);
+                    return dst == nullptr ? dst : dst + (c / 2) * 128;
+                });
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                stage_put(stage, lane, i,
+                          make_uint4(__float_as_uint(y[4 * i]), __float_as_uint(y[4 * i + 1]),
+                                     __float_as_uint(y[4 * i + 2]), __float_as_uint(y[4 * i + 3])));
+            stage_flush(stage, lane, false, [&](int row) {
+                char *dst = slot_at(row);
+                return dst == nullptr ? dst : dst + c * 128;
+            });
+        }
+    }
+    if (!live)
+        return;
+    if (u.slot < 0) {
+        const int tok = row_token(a, r0 + lane), g = r0 + lane - tok * a.G;
+        a.lse[static_cast<long long>(first + tok) * a.Hk * a.G + u.h * a.G + g] = lse2 * kLn2;
+    } else {
+        a.ws_l[slot_row + lane] = lse2;
+    }
+    if (!kF16 && !(fabsf(nonfinite) <= FLT_MAX))
+        atomicCAS(a.status, 0u,
+                  5u /* FATTN_ERR_RANGE */ | (kRoleEpilogue << 8) | ((blockIdx.x & 0xffffu) << 16));
+}
+
+template <int D, bool kF16>
+__device__ void run_softmax(const PagedArgs &a, Bars &b, uint8_t *smem, uint32_t tmem, int t)
+{
+    using C = Cfg<D, kF16>;
+    const volatile int *abort = &b.abort;
+    const int warp = (threadIdx.x / 32) & 3, lane = threadIdx.x & 31;
+    const int r = warp * 32 + lane;
+    const uint32_t lane_off = static_cast<uint32_t>(warp * 32) << 16;
+    const uint32_t t_s = tmem + lane_off + (t == 0 ? 0u : 128u);
+    const uint32_t t_o0 = tmem + lane_off + C::kColO0, t_o1 = tmem + lane_off + C::kColO1;
+    const uint32_t t_o = t == 0 ? t_o0 : t_o1;
+    uint8_t *stage = smem + C::kStageOffset + (t * 4 + warp) * 4096;
+    uint32_t s_phase = 0, of_phase = 0, other_phase = 0;
+    const int tok = row_token(a, r);
+    bool ok = true;
+    Walk w = first_walk(b);
+    Piece u;
+    while (ok && next_piece(a, w, u)) {
+        if (u.rows[t] <= 0)
+            continue;
+        const int nt = u.n[t];
+        // Rows of this warp that exist (a warp without any only keeps step).
+        const bool busy = warp * 32 < u.rows[t];
+        float m = -FLT_MAX, l = 0.f;
+        const int step = u.alt ? 2 : 1;
+        const int first_tok = u.s.L - u.s.n + u.tile[t] * a.tile_tokens;  // its position
+        int j = u.j0 + (u.alt ? t : 0);
+        for (int i = 0; i < nt; ++i, j += step) {
+            ok = warp_wait(b.s_full[t], s_phase, abort);
+            s_phase ^= 1;
+            if (!ok)
+                break;
+            tc_fence_after();
+            __syncwarp();
+            bool rescale = false;
+            if (busy) {
+                // Keys this row sees in the tile: 0 .. limit.
+                const int diag = a.causal ? first_tok - j * kBN : kBN;
+                const int tail = u.s.L - 1 - j * kBN;
+                const bool masked = diag < kBN - 1 || tail < kBN - 1;
+                const int limit = min(a.causal ? diag + tok : kBN, tail);
+                const bool first = i == 0;
+                float m_new;
+                auto pre = [&](float) { rescale = !first && __any_sync(0xffffffffu, m_new != m); };
+                auto mid = [&]() {
+                    if (!rescale) {
+                        tmem_wait_st();
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0)
+                            mbar_arrive(smem_addr(&b.p_half[t]));
+                    }
+                };
+                const float alpha =
+                    softmax_tile(a.sl2, t_s, masked, limit, first, m, m_new, l, pre, mid);
+                if (rescale)
+                    rescale_o<D>(t_o, alpha);
+                m = m_new;
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+            }
+            if (lane == 0) {
+                if (!busy || rescale)
+                    mbar_arrive(smem_addr(&b.p_half[t]));
+                mbar_arrive(smem_addr(&b.p_full[t]));
+            }
+        }
+        if (!ok)
+            break;
+        if (nt > 0) {
+            ok = warp_wait(b.o_full[t], of_phase, abort);
+            of_phase ^= 1;
+            if (!ok)
+                break;
+        }
+        const bool two = u.alt && u.n[1] > 0;
+        if (u.alt && t == 1) {
+            if (nt > 0) {
+                b.other[r] = make_float2(m, l);
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(smem_addr(&b.other_done));
+            }
+            continue;
+        }
+        float w0, w1 = 0.f, lse2;
+        if (two) {
+            ok = warp_wait(b.other_done, other_phase, abort);
+            other_phase ^= 1;
+            if (!ok)
+                break;
+            const float2 ml = b.other[r];
+            const float mm = fmaxf(m, ml.x);
+            const float a0 = ex2(m - mm), a1 = ex2(ml.x - mm);
+            l = l * a0 + ml.y * a1;
+            const float inv = l > 0.f ? 1.f / l : 0.f;
+            w0 = a0 * inv;
+            w1 = a1 * inv;
+            m = mm;
+        } else {
+            w0 = l > 0.f ? 1.f / l : 0.f;
+        }
+        lse2 = l > 0.f ? m + log2f(l) : -INFINITY;
+        tc_fence_after();
+        __syncwarp();
+        if (busy) {
+            if (nt == 0 && u.slot >= 0) {  // no key tile of this piece: an empty partial
+                const long long row = static_cast<long long>(u.slot) * a.slot_rows + t * kBM + r;
+                if (r < u.rows[t])
+                    a.ws_l[row] = -INFINITY;
+            } else {
+                write_rows<D, kF16>(a, u, t, warp * 32, u.alt ? t_o0 : t_o, t_o1, two, w0, w1, lse2,
+                                    nt > 0, stage);
+            }
+        }
+        if (nt > 0) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(smem_addr(&b.o_empty[t]));
+                if (two)
+                    mbar_arrive(smem_addr(&b.o_empty[1]));
+            }
+        }
+    }
+    if (!ok)
+        record_failure(a, b, kRoleSoftmax);
+}
+
+template <int D, bool kF16>
+__global__ void __launch_bounds__(kThreads, 1)
+    paged_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
+                 const __grid_constant__ CUtensorMap mv, const PagedArgs a)
+{
+    using C = Cfg<D, kF16>;
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    const uint32_t raw = smem_addr(smem_raw);
+    const uint32_t smem_base = (raw + 1023u) & ~1023u;
+    uint8_t *smem = smem_raw + (smem_base - raw);
+    Bars &b = *reinterpret_cast<Bars *>(smem + C::kBarsOffset);
+    const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        for (int t = 0; t < 2; ++t) {
+            mbar_init(smem_addr(&b.q_full[t]), 1);
+            mbar_init(smem_addr(&b.q_empty[t]), 1);
+            mbar_init(smem_addr(&b.s_full[t]), 1);
+            mbar_init(smem_addr(&b.p_half[t]), 4);
+            mbar_init(smem_addr(&b.p_full[t]), 4);
+            mbar_init(smem_addr(&b.o_full[t]), 1);
+            mbar_init(smem_addr(&b.o_empty[t]), 4);
+        }
+        for (int s = 0; s < C::kStages; ++s) {
+            mbar_init(smem_addr(&b.kv_full[s]), 1);
+            mbar_init(smem_addr(&b.kv_empty[s]), 1);
+            mbar_init(smem_addr(&b.v_ready[s]), 2);
+        }
+        mbar_init(smem_addr(&b.other_done), 4);
+        mbar_init(smem_addr(&b.drain), 1);
+        b.abort = 0;
+        fence_barrier_init();
+    }
+    if (warp == kWarpMma) {
+        tmem_alloc(smem_addr(&b.tmem_base), kTmemCols);
+        tmem_relinquish();
+    }
+    if (warp == kWarpLoad && lane == 0) {
+        prefetch_tensormap(&mq);
+        prefetch_tensormap(&mk);
+        prefetch_tensormap(&mv);
+    }
+    find_start(a, b);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = b.tmem_base;
+    if (warp < 8)
+        run_softmax<D, kF16>(a, b, smem, tmem, warp / 4);
+    else if (warp == kWarpLoad)
+        run_load<D, kF16>(a, b, smem_base, &mq, &mk, &mv);
+    else if (warp == kWarpMma)
+        run_mma<D, kF16>(a, b, smem_base, tmem);
+    else
+        run_convert<D, kF16>(a, b, smem, warp - kWarpConv);
+    grid_launch_dependents();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == kWarpMma) {
+        __syncwarp();
+        tmem_dealloc(tmem, kTmemCols);
+    }
+}
+
+// ------------------------------------------------------------------ combine
+// Block x handles the unit that CTA x + 1 starts inside, if that is the first
+// boundary in it: the partial of CTA x (its last slot) and those of CTAs x +
+// 1, x + 2, ... that start inside the same unit.  With base-2 partial
+// log-sum-exps e_s: lse = ln2 log2 sum 2^e_s, O = sum 2^(e_s - lse2) O_s.
+// One warp a row, D / 32 columns a lane, eight slots in flight.
+constexpr int kCombineRows = 32;  // rows a block
+
+template <int D, bool kF16>
+__global__ void __launch_bounds__(128) combine_paged_kernel(const PagedArgs a, int grid)
+{
+    constexpr int kCols = D / 32, kBatch = 8;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
+    grid_dependency_wait();
+    const int c = blockIdx.x + 1;
+    const int4 mine = a.starts[c];
+    if (mine.x < 0 || mine.w == 0)
+        return;
+    auto same = [&](int4 o) { return o.x == mine.x && o.y == mine.y && o.z == mine.z && o.w > 0; };
+    if (same(a.starts[c - 1]))
+        return;
+    int count = 0;  // CTAs from c on that start inside this unit
+    for (;;) {
+        const int k = c + count + lane;
+        const unsigned hit = __ballot_sync(0xffffffffu, k < grid && same(a.starts[min(k, grid - 1)]));
+        const int run = hit == 0xffffffffu ? 32 : __ffs(~hit) - 1;
+        count += run;
+        if (run < 32)
+            break;
+    }
+    bool bad;
+    const Seq s = load_seq(a, mine.x, bad);
+    const int tiles = tiles_of(a, s);
+    const long long slot0 = 2LL * (c - 1) + 1;
+    for (int row = blockIdx.y * kCombineRows + warp; row < min(a.slot_rows, (static_cast<int>(blockIdx.y) + 1) * kCombineRows);
+         row += 4) {
+        const int tile = 2 * mine.z + row / kBM, r = row % kBM;
+        const int tok = row_token(a, r), g = r - tok * a.G;
+        if (tile >= tiles || tok >= a.tile_tokens || tile * a.tile_tokens + tok >= s.n)
+            continue;
+        float mx = -INFINITY, se = 0.f, acc[kCols];
+#pragma unroll
+        for (int i = 0; i < kCols; ++i)
+            acc[i] = 0.f;
+        for (int k0 = 0; k0 <= count; k0 += kBatch) {
+            float e[kBatch], o[kBatch][kCols];
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k) {
+                e[k] = -INFINITY;
+                if (k0 + k <= count) {
+                    const long long slot = k0 + k == 0 ? slot0 : 2LL * (c + k0 + k - 1);
+                    const long long at = slot * a.slot_rows + row;
+                    e[k] = a.ws_l[at];
+#pragma unroll
+                    for (int i = 0; i < kCols; ++i)
+                        o[k][i] = a.ws_o[at * D + i * 32 + lane];
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k) {
+                if (e[k] == -INFINITY)  // holds no key of this row (its O is not written)
+                    continue;
+                const float ne = fmaxf(mx, e[k]);
+                const float f = ex2(mx - ne), x = ex2(e[k] - ne);
+                se = se * f + x;
+#pragma unroll
+                for (int i = 0; i < kCols; ++i)
+                    acc[i] = fmaf(x, o[k][i], acc[i] * f);
+                mx = ne;
+            }
+        }
+        const float inv = se > 0.f ? 1.f / se : 0.f;
+        const long long token = static_cast<long long>(s.q0) + tile * a.tile_tokens + tok;
+        const int head = mine.y * a.G + g;
+        uint16_t *dst = static_cast<uint16_t *>(a.o) + token * a.o_st[0] + head * a.o_st[1];
+#pragma unroll
+        for (int i = 0; i < kCols; ++i)
+            dst[i * 32 + lane] = static_cast<uint16_t>(pack2<kF16>(acc[i] * inv, 0.f) & 0xffffu);
+        if (lane == 0)
+            a.lse[token * a.Hk * a.G + head] = se > 0.f ? (mx + log2f(se)) * kLn2 : -INFINITY;
+    }
+}
+
+template <int D, bool kF16>
+cudaError_t launch(const PagedArgs &a, const FwdMaps &maps, int num_sms, cudaStream_t stream)
+{
+    using C = Cfg<D, kF16>;
+    const size_t smem = C::kBarsOffset + sizeof(Bars) + 1024;
+    cudaError_t e = cudaFuncSetAttribute(paged_kernel<D, kF16>,
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         static_cast<int>(smem));
+    if (e != cudaSuccess)
+        return e;
+    paged_kernel<D, kF16><<<num_sms, kThreads, smem, stream>>>(maps.q, maps.k, maps.v, a);
+    e = cudaGetLastError();
+    if (e != cudaSuccess || num_sms < 2)
+        return e;
+    cudaLaunchAttribute pdl[1];
+    pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    pdl[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(num_sms - 1, (a.slot_rows + kCombineRows - 1) / kCombineRows);
+    cfg.blockDim = dim3(128);
+    cfg.stream = stream;
+    cfg.attrs = pdl;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, combine_paged_kernel<D, kF16>, a, num_sms);
+}
+
+template <int D>
+cudaError_t launch_typed(const PagedArgs &a, const FwdMaps &maps, int num_sms, cudaStream_t stream)
+{
+    return a.f16 ? launch<D, true>(a, maps, num_sms, stream) : launch<D, false>(a, maps, num_sms, stream);
+}
+
+}  // namespace
+
+cudaError_t launch_paged(const PagedArgs &a, const FwdMaps &maps, int num_sms, cudaStream_t stream)
+{
+    switch (a.d) {
+    case 64: return launch_typed<64>(a, maps, num_sms, stream);
+    case 96: return launch_typed<96>(a, maps, num_sms, stream);
+    case 128: return launch_typed<128>(a, maps, num_sms, stream);
+    }
+    return cudaErrorInvalidValue;
+}
+
+}  // namespace fattn

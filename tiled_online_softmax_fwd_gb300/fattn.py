@@ -23,7 +23,8 @@ STATUS_NAMES = {0: "FATTN_OK", 1: "FATTN_ERR_INVALID_ARG", 2: "FATTN_ERR_UNSUPPO
                 3: "FATTN_ERR_CUDA", 4: "FATTN_ERR_TIMEOUT", 5: "FATTN_ERR_RANGE",
                 6: "FATTN_ERR_INDEX"}
 EXPORTED = ["attn_bwd", "attn_bwd_workspace_size", "attn_fwd", "attn_fwd_fp16", "attn_fwd_host",
-            "attn_fwd_kv", "attn_fwd_kv_workspace_size", "attn_fwd_simt", "attn_fwd_strided",
+            "attn_fwd_kv", "attn_fwd_kv_workspace_size", "attn_fwd_paged",
+            "attn_fwd_paged_workspace_size", "attn_fwd_simt", "attn_fwd_strided",
             "attn_fwd_split",
             "attn_fwd_split_count", "attn_fwd_split_noalloc", "attn_fwd_split_workspace_size",
             "fattn_status_string",
@@ -116,6 +117,11 @@ def load():
         lib.fattn_kv_append.restype = ctypes.c_int
         lib.fattn_kv_append.argtypes = [vp] * 8 + [ip] * 7 + [ctypes.c_longlong, ip, ip] + \
             [i64p] * 4 + [ip, ip, vp]
+        lib.attn_fwd_paged_workspace_size.restype = ctypes.c_size_t
+        lib.attn_fwd_paged_workspace_size.argtypes = [ip] * 4
+        lib.attn_fwd_paged.restype = ctypes.c_int
+        lib.attn_fwd_paged.argtypes = [vp] * 8 + [ip] * 8 + [ctypes.c_longlong, ip] + [i64p] * 4 + [
+            fp, ip, ip, vp, ctypes.c_size_t, vp]
         lib.fattn_version.restype = ctypes.c_char_p
         lib.fattn_version.argtypes = []
         lib.fattn_set_v_conversion.restype = ctypes.c_int
@@ -710,6 +716,54 @@ def kv_append(k, v, k_cache, v_cache, page_table, cu_q, kv_len, rope=None,
           _I64x2(*v.stride()[:2]), _I64x3(*k_cache.stride()[:3]), _I64x3(*v_cache.stride()[:3]),
           1 if interleaved else 0, _HALF[k.dtype])
     return k_cache, v_cache
+
+
+def paged_workspace_size(Hq: int, Hk: int, d: int, max_q: int, device=None) -> int:
+    """Scratch bytes attn_fwd_paged needs for these heads and at most max_q
+    new tokens a sequence."""
+    with torch.cuda.device(device):
+        return int(load().attn_fwd_paged_workspace_size(Hq, Hk, d, max_q))
+
+
+def attn_fwd_paged(q, k_cache, v_cache, page_table, cu_q, kv_len, max_q: int,
+                   causal: bool = True, scale: float | None = None, workspace=None, out=None,
+                   lse=None, stream=None):
+    """Attention of the packed new tokens q [T, Hq, d] over the paged cache
+    (libfattn attn_fwd_paged): bf16 or fp16, d 64, 96 or 128, Hq a multiple of
+    the caches' Hk.  The cache and its lists are as in kv_append, the new
+    tokens' keys already appended; ``max_q`` is at least the new tokens of
+    every sequence.  Returns (out [T, Hq, d], lse fp32 [T, Hq]); rows from
+    cu_q[B] on are not written."""
+    _half_tensor("q", q, 3)
+    T, Hq, d = q.shape
+    if d not in (64, 96, 128):
+        raise ValueError("head dimension must be 64, 96 or 128, got %d" % d)
+    pages, page = _paged_cache(k_cache, v_cache, q)
+    Hk = k_cache.shape[1]
+    if Hk == 0 or Hq % Hk or Hq > 128 * Hk:
+        raise ValueError("Hq must be 1 to 128 times Hk, got %d and %d" % (Hq, Hk))
+    dev = q.device
+    B, max_pages, row = _paged_lists(page_table, cu_q, kv_len, dev)
+    if max_q < 1:
+        raise ValueError("max_q must be at least 1, got %d" % max_q)
+    if out is None:
+        out = _empty((T, Hq, d), q.dtype, dev, stream)
+    elif _half_tensor("out", out, 3, q).shape != q.shape:
+        raise ValueError("out must have q's shape")
+    if lse is None:
+        lse = _empty((T, Hq), torch.float32, dev, stream)
+    else:
+        _plain_tensor("lse", lse, torch.float32, (T, Hq), dev)
+    if workspace is None:
+        workspace = _empty(max(paged_workspace_size(Hq, Hk, d, max_q, dev), 16), torch.uint8, dev,
+                           stream)
+    _call("attn_fwd_paged", dev, stream, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+          page_table.data_ptr(), cu_q.data_ptr(), kv_len.data_ptr(), out.data_ptr(), lse.data_ptr(),
+          T, B, Hq, Hk, d, pages, page, max_pages, row, max_q, _I64x2(*q.stride()[:2]),
+          _I64x3(*k_cache.stride()[:3]), _I64x3(*v_cache.stride()[:3]), _I64x2(*out.stride()[:2]),
+          default_scale(d) if scale is None else scale, 1 if causal else 0, _HALF[q.dtype],
+          workspace.data_ptr(), workspace.nbytes)
+    return out, lse
 
 
 def version() -> str:
