@@ -9,6 +9,7 @@ checks again and is the authority.
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 import os
 import threading
@@ -140,6 +141,7 @@ def _check(status: int, what: str):
         raise FattnError(status, what, cuda_err)
 
 
+@functools.lru_cache(maxsize=None)
 def default_scale(d: int) -> float:
     """1/sqrt(d) rounded to the fp32 value the kernel receives."""
     return float(torch.tensor(1.0 / math.sqrt(d), dtype=torch.float32))
@@ -481,69 +483,99 @@ def row_sum(x, out=None, stream=None):
 
 
 # ------------------------------------------------------------------ serving
-# Norm and rotation, and the paged cache.  These calls run once a layer of a
-# decode step, where the host's share counts: the checks read each tensor's
-# attributes once and the device is switched only when it has to be.
+# Norm and rotation, and the paged cache.  A decode step makes these calls once
+# a layer on a few microseconds of GPU work, so the host's share counts: each
+# tensor is checked by one expression of plain attributes, stride arrays and
+# sizes that depend on shapes alone are kept by value, and the device is
+# switched only when it has to be.
 _HALF = {torch.bfloat16: 0, torch.float16: 1}
-_I64x2, _I64x3 = ctypes.c_longlong * 2, ctypes.c_longlong * 3
+_Tensor, _raw_stream = torch.Tensor, torch._C._cuda_getCurrentRawStream
 
 
-def _half_tensor(name, t, dims, like=None):
-    """A 16-bit CUDA tensor of `dims` dimensions with a contiguous last one,
-    of `like`'s type and device."""
-    if not isinstance(t, torch.Tensor):
+def _check_half(name, t, dims, dtype, dev):
+    """A tensor of `dims` dimensions, type `dtype` on CUDA device `dev`, with a
+    contiguous last dimension."""
+    if isinstance(t, _Tensor) and t.dim() == dims and t.dtype == dtype and t.get_device() == dev \
+            and (t.stride(-1) == 1 or t.shape[-1] == 1):
+        return
+    if not isinstance(t, _Tensor):
         raise TypeError("%s must be a torch.Tensor" % name)
-    if not t.is_cuda or t.dtype not in _HALF or t.dim() != dims:
-        raise ValueError("%s must be a %d-dimensional bf16 or fp16 CUDA tensor" % (name, dims))
-    if t.stride(-1) != 1 and t.shape[-1] > 1:
-        raise ValueError("%s must have a contiguous last dimension" % name)
-    if like is not None and (t.dtype != like.dtype or t.device != like.device):
-        raise ValueError("%s must have the other tensors' type and device" % name)
-    return t
+    raise ValueError("%s must be a %d-dimensional %s tensor on CUDA device %d with a contiguous "
+                     "last dimension, got %s %s on %s" % (name, dims, dtype, dev, tuple(t.shape),
+                                                          t.dtype, t.device))
 
 
-def _plain_tensor(name, t, dtype, shape, device, contiguous=True):
-    if not isinstance(t, torch.Tensor) or t.dtype != dtype or t.device != device:
-        raise ValueError("%s must be a %s tensor on %s" % (name, dtype, device))
-    if tuple(t.shape) != tuple(shape) or (contiguous and not t.is_contiguous()):
-        raise ValueError("%s must be a contiguous %s tensor" % (name, list(shape)))
-    return t
+def _first_half(name, t, dims):
+    """Type and device index of the tensor that sets them for a call."""
+    if not isinstance(t, _Tensor):
+        raise TypeError("%s must be a torch.Tensor" % name)
+    dtype, dev = t.dtype, t.get_device()
+    if dev < 0 or dtype not in _HALF:
+        raise ValueError("%s must be a bf16 or fp16 CUDA tensor, got %s on %s" % (name, dtype, t.device))
+    _check_half(name, t, dims, dtype, dev)
+    return dtype, dev
 
 
-def _rope_args(rope, d, device):
+def _check_plain(name, t, dtype, shape, dev):
+    if isinstance(t, _Tensor) and t.dtype == dtype and t.shape == shape and t.get_device() == dev \
+            and t.is_contiguous():
+        return
+    raise ValueError("%s must be a contiguous %s %s tensor on CUDA device %d"
+                     % (name, dtype, list(shape), dev))
+
+
+@functools.lru_cache(maxsize=4096)
+def _strides(st):
+    """A stride tuple as the C array that the calls take (read only)."""
+    return (ctypes.c_longlong * len(st))(*st)
+
+
+def _outer(t):
+    return None if t is None else _strides(t.stride()[:-1])
+
+
+def _ptr(t):
+    return 0 if t is None else t.data_ptr()
+
+
+def _rope_args(rope, d, dev):
     """(pointer, rot_dim, max_pos) of a rotation table, or none."""
     if rope is None:
         return 0, 0, 0
-    if not isinstance(rope, torch.Tensor) or rope.dtype != torch.float32 or rope.dim() != 2 \
-            or not rope.is_contiguous() or rope.device != device:
-        raise ValueError("rope must be a contiguous fp32 [positions, rot_dim] tensor on %s" % device)
-    if rope.shape[1] % 16 or not 0 < rope.shape[1] <= d:
-        raise ValueError("rope must have 16, 32, ... up to %d columns, got %d" % (d, rope.shape[1]))
-    return rope.data_ptr(), rope.shape[1], rope.shape[0]
+    if not isinstance(rope, _Tensor) or rope.dtype != torch.float32 or rope.dim() != 2 \
+            or not rope.is_contiguous() or rope.get_device() != dev:
+        raise ValueError("rope must be a contiguous fp32 [positions, rot_dim] tensor on CUDA "
+                         "device %d" % dev)
+    max_pos, rot = rope.shape
+    if rot % 16 or not 0 < rot <= d:
+        raise ValueError("rope must have 16, 32, ... up to %d columns, got %d" % (d, rot))
+    return rope.data_ptr(), rot, max_pos
 
 
-def _call(entry, device, stream, *args):
-    """Call an entry point whose last argument is the stream, with `device` current."""
-    f = getattr(load(), entry)
-    if torch.cuda.current_device() == device.index:
-        st = f(*args, _stream_handle(stream, device))
+def _call(entry, dev, stream, *args):
+    """Call an entry point whose last argument is the stream, with device `dev` current."""
+    f = getattr(_lib or load(), entry)
+    handle = _raw_stream(dev) if stream is None else _stream_handle(stream, dev)
+    if torch.cuda.current_device() == dev:
+        st = f(*args, handle)
     else:
-        with torch.cuda.device(device):
-            st = f(*args, _stream_handle(stream, device))
-    _check(st, entry)
+        with torch.cuda.device(dev):
+            st = f(*args, handle)
+    if st != FATTN_OK:
+        _check(st, entry)
 
 
-def _empty(shape, dtype, device, stream):
+def _empty(shape, dtype, dev, stream):
     """A new tensor of the call's stream: memory that is freed while the call
     still runs there is then reused only behind it."""
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
+        return torch.empty(shape, dtype=dtype, device=dev)
     if not isinstance(stream, torch.cuda.Stream):
-        handle = _stream_handle(stream, device)
-        stream = (torch.cuda.ExternalStream(handle, device=device) if handle
-                  else torch.cuda.default_stream(device))
+        handle = _stream_handle(stream, dev)
+        stream = (torch.cuda.ExternalStream(handle, device=dev) if handle
+                  else torch.cuda.default_stream(dev))
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=device)
+        return torch.empty(shape, dtype=dtype, device=dev)
 
 
 def rope_table(positions: int, rot_dim: int, theta: float = 10000.0, device="cuda"):
@@ -558,52 +590,42 @@ def rope_table(positions: int, rot_dim: int, theta: float = 10000.0, device="cud
     return torch.cat([ang.cos(), ang.sin()], 1).float().to(device)
 
 
-def _norm_shapes(q, k, wq, wk, rope, positions):
-    """The checks shared by both passes; q or k may be None."""
-    first = q if q is not None else k
-    if first is None:
+def _norm_args(q, k, wq, wk, rope, positions):
+    """The checks shared by both passes; q or k may be None.  Returns type,
+    device, (B, Hq, Hk, N, d) and the rotation's arguments."""
+    if q is None and k is None:
         raise ValueError("q and k are both None")
-    for name, t in (("q", q), ("k", k)):
-        if t is not None:
-            _half_tensor(name, t, 4, first)
-    B, _, N, d = first.shape
-    if k is not None and (k.shape[0], k.shape[2], k.shape[3]) != (B, N, d):
-        raise ValueError("q and k differ in batch, tokens or head dimension: %s %s"
-                         % (tuple(first.shape), tuple(k.shape)))
+    dtype, dev = _first_half("q", q, 4) if q is not None else _first_half("k", k, 4)
+    B, Hq, N, d = q.shape if q is not None else (k.shape[0], 0, k.shape[2], k.shape[3])
+    Hk = 0
+    if k is not None:
+        _check_half("k", k, 4, dtype, dev)
+        Bk, Hk, Nk, dk = k.shape
+        if Bk != B or Nk != N or dk != d:
+            raise ValueError("q and k differ in batch, tokens or head dimension: %s %s"
+                             % (tuple(q.shape), tuple(k.shape)))
     if d not in (64, 96, 128, 256):
         raise ValueError("head dimension must be 64, 96, 128 or 256, got %d" % d)
-    for name, w, t in (("wq", wq, q), ("wk", wk, k)):
-        if w is not None:
-            if t is None:
-                raise ValueError("%s is given without its tensor" % name)
-            _plain_tensor(name, w, first.dtype, (d,), first.device)
-    rope_ptr, rot, max_pos = _rope_args(rope, d, first.device)
+    if wq is not None:
+        _check_plain("wq", wq, dtype, (d,), dev)
+    if wk is not None:
+        _check_plain("wk", wk, dtype, (d,), dev)
+    if (wq is not None and q is None) or (wk is not None and k is None):
+        raise ValueError("weights are given without their tensor")
     if positions is not None:
-        _plain_tensor("positions", positions, torch.int32, (B, N), first.device)
-    return first, B, N, d, rope_ptr, rot, max_pos
+        _check_plain("positions", positions, torch.int32, (B, N), dev)
+    return dtype, dev, (B, Hq, Hk, N, d), _rope_args(rope, d, dev)
 
 
-def _ptr(t):
-    return 0 if t is None else t.data_ptr()
-
-
-def _strides3(t):
-    return None if t is None else _I64x3(*t.stride()[:3])
-
-
-def _heads(t):
-    return 0 if t is None else t.shape[1]
-
-
-def _like(name, out, t, stream):
+def _like(name, out, t, dtype, dev, stream):
     """The output for t: `out` checked, or a new contiguous tensor."""
     if t is None:
         if out is not None:
             raise ValueError("%s is given without its tensor" % name)
         return None
     if out is None:
-        return _empty(t.shape, t.dtype, t.device, stream)
-    _half_tensor(name, out, 4, t)
+        return _empty(t.shape, dtype, dev, stream)
+    _check_half(name, out, 4, dtype, dev)
     if out.shape != t.shape:
         raise ValueError("%s must have its input's shape" % name)
     return out
@@ -619,12 +641,12 @@ def qk_norm_rope(q, k, wq=None, wk=None, rope=None, positions=None, eps: float =
     fp32 [positions, rot_dim] table of rope_table (None: no rotation),
     ``positions`` int32 [B, N] (None: 0..N-1).  ``q_out``/``k_out`` may be
     given (the inputs themselves for in place).  Returns (q_out, k_out)."""
-    first, B, N, d, rope_ptr, rot, max_pos = _norm_shapes(q, k, wq, wk, rope, positions)
-    q_out, k_out = _like("q_out", q_out, q, stream), _like("k_out", k_out, k, stream)
-    _call("fattn_qk_norm_rope", first.device, stream, _ptr(q), _ptr(k), _ptr(q_out), _ptr(k_out),
-          _ptr(wq), _ptr(wk), rope_ptr, _ptr(positions), B, _heads(q), _heads(k), N, d, rot,
-          max_pos, _strides3(q), _strides3(k), _strides3(q_out), _strides3(k_out), eps,
-          1 if interleaved else 0, _HALF[first.dtype])
+    dtype, dev, (B, Hq, Hk, N, d), (table, rot, max_pos) = _norm_args(q, k, wq, wk, rope, positions)
+    q_out = _like("q_out", q_out, q, dtype, dev, stream)
+    k_out = _like("k_out", k_out, k, dtype, dev, stream)
+    _call("fattn_qk_norm_rope", dev, stream, _ptr(q), _ptr(k), _ptr(q_out), _ptr(k_out), _ptr(wq),
+          _ptr(wk), table, _ptr(positions), B, Hq, Hk, N, d, rot, max_pos, _outer(q), _outer(k),
+          _outer(q_out), _outer(k_out), eps, 1 if interleaved else 0, _HALF[dtype])
     return q_out, k_out
 
 
@@ -634,60 +656,81 @@ def qk_norm_rope_bwd(dq_out, dk_out, q, k, wq=None, wk=None, rope=None, position
     """Gradients of qk_norm_rope for the upstream gradients dq_out, dk_out
     (libfattn fattn_qk_norm_rope_bwd).  Returns (dq, dk, dwq, dwk): dq and dk
     in the inputs' type, dwq and dwk fp32 [d] (None without weights)."""
-    first, B, N, d, rope_ptr, rot, max_pos = _norm_shapes(q, k, wq, wk, rope, positions)
+    dtype, dev, (B, Hq, Hk, N, d), (table, rot, max_pos) = _norm_args(q, k, wq, wk, rope, positions)
     for name, g, t in (("dq_out", dq_out, q), ("dk_out", dk_out, k)):
-        if (g is None) != (t is None):
-            raise ValueError("%s goes with its tensor" % name)
-        if g is not None:
-            _half_tensor(name, g, 4, first)
-            if g.shape != t.shape:
-                raise ValueError("%s must have its tensor's shape" % name)
-    dq, dk = _like("dq", dq, q, stream), _like("dk", dk, k, stream)
-    dev = first.device
+        if t is None:
+            if g is not None:
+                raise ValueError("%s is given without its tensor" % name)
+            continue
+        _check_half(name, g, 4, dtype, dev)
+        if g.shape != t.shape:
+            raise ValueError("%s must have its tensor's shape" % name)
+    dq = _like("dq", dq, q, dtype, dev, stream)
+    dk = _like("dk", dk, k, dtype, dev, stream)
     dwq = None if wq is None else _empty(d, torch.float32, dev, stream)
     dwk = None if wk is None else _empty(d, torch.float32, dev, stream)
     if workspace is None and (wq is not None or wk is not None):
         workspace = _empty(qk_norm_rope_bwd_workspace_size(d, dev), torch.uint8, dev, stream)
     _call("fattn_qk_norm_rope_bwd", dev, stream, _ptr(dq_out), _ptr(dk_out), _ptr(q), _ptr(k),
-          _ptr(wq), _ptr(wk), rope_ptr, _ptr(positions), _ptr(dq), _ptr(dk), _ptr(dwq), _ptr(dwk),
-          B, _heads(q), _heads(k), N, d, rot, max_pos, _strides3(dq_out), _strides3(dk_out),
-          _strides3(q), _strides3(k), _strides3(dq), _strides3(dk), eps, 1 if interleaved else 0,
-          _HALF[first.dtype], _ptr(workspace), 0 if workspace is None else workspace.nbytes)
+          _ptr(wq), _ptr(wk), table, _ptr(positions), _ptr(dq), _ptr(dk), _ptr(dwq), _ptr(dwk), B,
+          Hq, Hk, N, d, rot, max_pos, _outer(dq_out), _outer(dk_out), _outer(q), _outer(k),
+          _outer(dq), _outer(dk), eps, 1 if interleaved else 0, _HALF[dtype], _ptr(workspace),
+          0 if workspace is None else workspace.nbytes)
     return dq, dk, dwq, dwk
+
+
+@functools.lru_cache(maxsize=1024)
+def _workspace_bytes(entry, dev, *args):
+    """A size query of the library: it depends on the device and shapes alone."""
+    with torch.cuda.device(dev):
+        return int(getattr(load(), entry)(*args))
+
+
+def _device_index(device) -> int:
+    if device is None:
+        return torch.cuda.current_device()
+    if isinstance(device, int):
+        return device
+    index = torch.device(device).index
+    return torch.cuda.current_device() if index is None else index
 
 
 def qk_norm_rope_bwd_workspace_size(d: int, device=None) -> int:
     """Scratch bytes qk_norm_rope_bwd needs with weights."""
-    with torch.cuda.device(device):
-        return int(load().fattn_qk_norm_rope_bwd_workspace_size(d))
+    return _workspace_bytes("fattn_qk_norm_rope_bwd_workspace_size", _device_index(device), d)
 
 
-def _paged_lists(page_table, cu_q, kv_len, device):
-    """Checks the lists of a paged call; (sequences, pages a sequence, row stride)."""
-    for name, t, dims in (("page_table", page_table, 2), ("cu_q", cu_q, 1), ("kv_len", kv_len, 1)):
-        if not isinstance(t, torch.Tensor) or t.dtype != torch.int32 or t.dim() != dims \
-                or t.device != device:
-            raise ValueError("%s must be a %d-dimensional int32 tensor on %s" % (name, dims, device))
+def paged_workspace_size(Hq: int, Hk: int, d: int, max_q: int, device=None) -> int:
+    """Scratch bytes attn_fwd_paged needs for these heads and at most max_q
+    new tokens a sequence."""
+    return _workspace_bytes("attn_fwd_paged_workspace_size", _device_index(device), Hq, Hk, d, max_q)
+
+
+def _paged_args(page_table, cu_q, kv_len, k_cache, v_cache, dtype, dev, d):
+    """The checks of a paged call's lists and cache: (sequences, pages a
+    sequence, table row stride, pages, key heads, page size)."""
+    i32 = torch.int32
+    if not (isinstance(page_table, _Tensor) and page_table.dtype == i32 and page_table.dim() == 2
+            and page_table.get_device() == dev and isinstance(cu_q, _Tensor) and cu_q.dtype == i32
+            and cu_q.dim() == 1 and cu_q.get_device() == dev and isinstance(kv_len, _Tensor)
+            and kv_len.dtype == i32 and kv_len.dim() == 1 and kv_len.get_device() == dev):
+        raise ValueError("page_table [B, pages], cu_q [B + 1] and kv_len [B] must be int32 tensors "
+                         "on CUDA device %d" % dev)
     B, max_pages = page_table.shape
     if cu_q.shape[0] != B + 1 or kv_len.shape[0] != B or not cu_q.is_contiguous() \
             or not kv_len.is_contiguous() or (max_pages > 1 and page_table.stride(1) != 1):
         raise ValueError("page_table [B, pages], cu_q [B + 1] and kv_len [B] do not match or are "
                          "not contiguous: %s %s %s" % (tuple(page_table.shape), tuple(cu_q.shape),
                                                        tuple(kv_len.shape)))
-    return B, max_pages, (page_table.stride(0) if B > 1 else max_pages)
-
-
-def _paged_cache(k_cache, v_cache, like, Hk=None):
-    _half_tensor("k_cache", k_cache, 4, like)
-    _half_tensor("v_cache", v_cache, 4, like)
-    if k_cache.shape != v_cache.shape or k_cache.shape[3] != like.shape[-1] \
-            or (Hk is not None and k_cache.shape[1] != Hk):
-        raise ValueError("k_cache and v_cache must both be [pages, Hk, page_size, d] for the call's "
-                         "heads and d, got %s %s" % (tuple(k_cache.shape), tuple(v_cache.shape)))
-    page = k_cache.shape[2]
+    _check_half("k_cache", k_cache, 4, dtype, dev)
+    _check_half("v_cache", v_cache, 4, dtype, dev)
+    pages, Hk, page, dc = k_cache.shape
+    if v_cache.shape != k_cache.shape or dc != d:
+        raise ValueError("k_cache and v_cache must both be [pages, Hk, page_size, %d], got %s %s"
+                         % (d, tuple(k_cache.shape), tuple(v_cache.shape)))
     if page < 16 or page & (page - 1):
         raise ValueError("page size must be a power of two, 16 or more, got %d" % page)
-    return k_cache.shape[0], page
+    return B, max_pages, page_table.stride(0) if B > 1 else max_pages, pages, Hk, page
 
 
 def kv_append(k, v, k_cache, v_cache, page_table, cu_q, kv_len, rope=None,
@@ -700,29 +743,23 @@ def kv_append(k, v, k_cache, v_cache, page_table, cu_q, kv_len, rope=None,
     strides; ``page_table`` int32 [B, pages], ``cu_q`` int32 [B + 1],
     ``kv_len`` int32 [B] (keys of each sequence, the new ones included).
     Returns (k_cache, v_cache)."""
-    _half_tensor("k", k, 3)
-    _half_tensor("v", v, 3, k)
-    if k.shape != v.shape:
-        raise ValueError("k and v must have one shape, got %s %s" % (tuple(k.shape), tuple(v.shape)))
+    dtype, dev = _first_half("k", k, 3)
+    _check_half("v", v, 3, dtype, dev)
     T, Hk, d = k.shape
+    if v.shape != k.shape:
+        raise ValueError("k and v must have one shape, got %s %s" % (tuple(k.shape), tuple(v.shape)))
     if d not in (64, 96, 128, 256):
         raise ValueError("head dimension must be 64, 96, 128 or 256, got %d" % d)
-    pages, page = _paged_cache(k_cache, v_cache, k, Hk)
-    B, max_pages, row = _paged_lists(page_table, cu_q, kv_len, k.device)
-    rope_ptr, rot, max_pos = _rope_args(rope, d, k.device)
-    _call("fattn_kv_append", k.device, stream, k.data_ptr(), v.data_ptr(), k_cache.data_ptr(),
-          v_cache.data_ptr(), page_table.data_ptr(), cu_q.data_ptr(), kv_len.data_ptr(), rope_ptr,
-          T, B, Hk, d, pages, page, max_pages, row, rot, max_pos, _I64x2(*k.stride()[:2]),
-          _I64x2(*v.stride()[:2]), _I64x3(*k_cache.stride()[:3]), _I64x3(*v_cache.stride()[:3]),
-          1 if interleaved else 0, _HALF[k.dtype])
+    B, max_pages, row, pages, heads, page = _paged_args(page_table, cu_q, kv_len, k_cache, v_cache,
+                                                        dtype, dev, d)
+    if heads != Hk:
+        raise ValueError("the caches have %d heads, k and v %d" % (heads, Hk))
+    table, rot, max_pos = _rope_args(rope, d, dev)
+    _call("fattn_kv_append", dev, stream, k.data_ptr(), v.data_ptr(), k_cache.data_ptr(),
+          v_cache.data_ptr(), page_table.data_ptr(), cu_q.data_ptr(), kv_len.data_ptr(), table, T,
+          B, Hk, d, pages, page, max_pages, row, rot, max_pos, _outer(k), _outer(v), _outer(k_cache),
+          _outer(v_cache), 1 if interleaved else 0, _HALF[dtype])
     return k_cache, v_cache
-
-
-def paged_workspace_size(Hq: int, Hk: int, d: int, max_q: int, device=None) -> int:
-    """Scratch bytes attn_fwd_paged needs for these heads and at most max_q
-    new tokens a sequence."""
-    with torch.cuda.device(device):
-        return int(load().attn_fwd_paged_workspace_size(Hq, Hk, d, max_q))
 
 
 def attn_fwd_paged(q, k_cache, v_cache, page_table, cu_q, kv_len, max_q: int,
@@ -734,35 +771,34 @@ def attn_fwd_paged(q, k_cache, v_cache, page_table, cu_q, kv_len, max_q: int,
     tokens' keys already appended; ``max_q`` is at least the new tokens of
     every sequence.  Returns (out [T, Hq, d], lse fp32 [T, Hq]); rows from
     cu_q[B] on are not written."""
-    _half_tensor("q", q, 3)
+    dtype, dev = _first_half("q", q, 3)
     T, Hq, d = q.shape
     if d not in (64, 96, 128):
         raise ValueError("head dimension must be 64, 96 or 128, got %d" % d)
-    pages, page = _paged_cache(k_cache, v_cache, q)
-    Hk = k_cache.shape[1]
+    B, max_pages, row, pages, Hk, page = _paged_args(page_table, cu_q, kv_len, k_cache, v_cache,
+                                                     dtype, dev, d)
     if Hk == 0 or Hq % Hk or Hq > 128 * Hk:
         raise ValueError("Hq must be 1 to 128 times Hk, got %d and %d" % (Hq, Hk))
-    dev = q.device
-    B, max_pages, row = _paged_lists(page_table, cu_q, kv_len, dev)
     if max_q < 1:
         raise ValueError("max_q must be at least 1, got %d" % max_q)
     if out is None:
-        out = _empty((T, Hq, d), q.dtype, dev, stream)
-    elif _half_tensor("out", out, 3, q).shape != q.shape:
-        raise ValueError("out must have q's shape")
+        out = _empty((T, Hq, d), dtype, dev, stream)
+    else:
+        _check_half("out", out, 3, dtype, dev)
+        if out.shape != q.shape:
+            raise ValueError("out must have q's shape")
     if lse is None:
         lse = _empty((T, Hq), torch.float32, dev, stream)
     else:
-        _plain_tensor("lse", lse, torch.float32, (T, Hq), dev)
+        _check_plain("lse", lse, torch.float32, (T, Hq), dev)
     if workspace is None:
-        workspace = _empty(max(paged_workspace_size(Hq, Hk, d, max_q, dev), 16), torch.uint8, dev,
-                           stream)
+        need = _workspace_bytes("attn_fwd_paged_workspace_size", dev, Hq, Hk, d, max_q)
+        workspace = _empty(need, torch.uint8, dev, stream)
     _call("attn_fwd_paged", dev, stream, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
           page_table.data_ptr(), cu_q.data_ptr(), kv_len.data_ptr(), out.data_ptr(), lse.data_ptr(),
-          T, B, Hq, Hk, d, pages, page, max_pages, row, max_q, _I64x2(*q.stride()[:2]),
-          _I64x3(*k_cache.stride()[:3]), _I64x3(*v_cache.stride()[:3]), _I64x2(*out.stride()[:2]),
-          default_scale(d) if scale is None else scale, 1 if causal else 0, _HALF[q.dtype],
-          workspace.data_ptr(), workspace.nbytes)
+          T, B, Hq, Hk, d, pages, page, max_pages, row, max_q, _outer(q), _outer(k_cache),
+          _outer(v_cache), _outer(out), default_scale(d) if scale is None else scale,
+          1 if causal else 0, _HALF[dtype], workspace.data_ptr(), workspace.nbytes)
     return out, lse
 
 
