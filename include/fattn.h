@@ -399,7 +399,8 @@ fattn_status_t fattn_row_sum(const void *x, float *out, int M, int N, int dtype,
  * output).  A token whose position is outside [0, max_pos) is left unwritten
  * and records FATTN_ERR_INDEX (role 7) in the device status word.  Strides of
  * dimensions longer than 1 are positive multiples of 8 elements, pointers
- * 16-byte aligned (positions: 4).  Errors as for attn_fwd_strided.
+ * 16-byte aligned (positions: 4), B*N below 2^31 - 64.  Errors as for
+ * attn_fwd_strided.
  *
  * fattn_qk_norm_rope_bwd -- its gradients.  From the upstream gradients
  * dq_out, dk_out and the forward's inputs (the statistics are recomputed):

@@ -896,6 +896,8 @@ fattn_status_t norm_rope(const NormCall &c, bool backward, const float *rope, co
             if (H[t] > 0 && (c.w[t] != nullptr) != (c.dw[t] != nullptr))
                 return FATTN_ERR_INVALID_ARG;
     const long long tokens = static_cast<long long>(B) * N;
+    if (tokens > 0x7fffffffLL - 64)
+        return FATTN_ERR_UNSUPPORTED;
     if (tokens == 0 || Hq + static_cast<long long>(Hk) == 0) {
         // No rows: the sums of an empty set are zero.
         for (int t = 0; t < 2 && backward; ++t) {
@@ -1494,7 +1496,7 @@ size_t fattn_qk_norm_rope_bwd_workspace_size(int d)
     DeviceInfo info;
     if (!head_dim_ok(d) || current_device(&dev, &info) != FATTN_OK)
         return 0;
-    return static_cast<size_t>(fattn::norm_rope_bwd_blocks(info.num_sms)) * 2 * d * 4;
+    return static_cast<size_t>(fattn::norm_rope_bwd_blocks(info.num_sms)) * d * 4;
 }
 
 fattn_status_t fattn_qk_norm_rope_bwd(const void *dq_out, const void *dk_out, const void *q,

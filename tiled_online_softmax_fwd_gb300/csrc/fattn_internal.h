@@ -121,7 +121,7 @@ struct NormRopeArgs {
     void *y[2];
     const void *w[2];  // null: no norm
     float *dw[2];
-    float *partial;  // backward: norm_rope_bwd_blocks x 2 x d
+    float *partial;  // backward: norm_rope_bwd_blocks x d
     const float *table;      // [max_pos][rot]: cosines, then sines
     const int *positions;    // [B * N], or null: 0 .. N-1
     uint32_t *status;
@@ -129,9 +129,10 @@ struct NormRopeArgs {
     long long tokens;  // B * N
     int N, H[2], d, rot, max_pos, interleaved, f16;
     float eps;
-    // Filled in by the launch: heads an item, items of each tensor, all items.
-    int heads_per_chunk, chunks[2];
-    long long items;
+    // Filled in by the launch: heads an item, chunks of heads and items of each tensor.
+    // Backward: blocks that work on each tensor.
+    int heads_per_chunk, chunks[2], blocks[2];
+    long long items[2];
 };
 cudaError_t launch_norm_rope(const NormRopeArgs &a, int num_sms, cudaStream_t stream);
 // Blocks (partials) of a backward launch at most.

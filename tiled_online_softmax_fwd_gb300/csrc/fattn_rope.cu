@@ -11,15 +11,17 @@
 //             dx = r (g w - x r^2 mean(g w x))
 //   append    k_cache[page, head, slot] = R(p) k,   v_cache[...] = v
 //
-// All are bound by HBM: a forward row is read and written once, 12 flops an
-// element pair.  Layout: a row's 16-byte vectors sit on consecutive lanes (8
-// lanes for d = 64, 16 for 96 and 128, 32 for 256), so a warp holds 1 to 4
-// rows, one token each, and walks over the heads of its tokens: the angles
-// (64 bytes a lane, four times the row's own 16) are read once a token, not
-// once a row.  A row's rotation partner is d-dependent lanes away and comes
-// by shuffles of the packed 16-bit words, before any arithmetic.  A row lives
-// in one lane group from load to store, so the outputs may be the inputs.
-// Arithmetic is fp32 with one rounding, at the store.
+// All are bound by HBM: a forward row is read and written once, some 12 flops
+// an element pair.  Layout: a lane holds two 16-byte vectors of a row, a
+// rotation pair's first elements and its second ones (8 lanes a row at d =
+// 128), so the turn needs no exchange between lanes and one set of angles
+// serves both; a warp holds 2 to 8 rows, one token each, and walks over the
+// heads of its tokens, so the angles (64 bytes a lane) are read once a token,
+// not once a row.  With one vector a lane, partners fetched by shuffles, the
+// backward pass ran at 152 registers and issued twice the instructions: 143 us
+// for B4 H16 N4096 d128 (405 MB).  Arithmetic is fp32, two elements an
+// instruction, with one rounding, at the store.  A row lives in one lane group
+// from load to store, so the outputs may be the inputs.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <stdint.h>
@@ -32,52 +34,70 @@ namespace {
 
 constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
-// Rows in flight per lane group: four 16-byte loads a lane, issued together.
-constexpr int kBatch = 4;
+// Residency that the registers are capped for: forward and append 5 blocks a
+// SM (96 registers), backward 4 (128).
+constexpr int kBlocksPerSm = 5, kBwdBlocksPerSm = 4;
 
 template <int D> struct Geo {
-    static constexpr int kVecs = D / 8;  // 16-byte vectors of a row
-    static constexpr int kLanes = D == 64 ? 8 : D == 256 ? 32 : 16;
+    static constexpr int kLanes = D / 16;        // lanes that hold a row, two vectors each
     static constexpr int kTokens = 32 / kLanes;  // tokens (rows) a warp holds
+    // d = 96: five rows of six lanes; the last two lanes hold none.
+    static __device__ __forceinline__ bool in_row(int lane)
+    {
+        return kLanes * kTokens == 32 || lane < kLanes * kTokens;
+    }
 };
 
-template <bool kF16> __device__ __forceinline__ float2 widen(uint32_t w)
-{
-    if constexpr (kF16) {
-        return __half22float2(*reinterpret_cast<const __half2 *>(&w));
-    } else {
-        return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
-    }
-}
-
-template <bool kF16> __device__ __forceinline__ uint32_t narrow(float lo, float hi)
-{
-    if constexpr (kF16) {
-        const __half2 h = __floats2half2_rn(lo, hi);
-        return *reinterpret_cast<const uint32_t *>(&h);
-    } else {
-        const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
-        return *reinterpret_cast<const uint32_t *>(&h);
-    }
-}
-
-template <bool kF16> __device__ __forceinline__ void widen8(uint4 u, float (&x)[8])
+// Eight 16-bit elements as four fp32 pairs, and back.
+using F8 = uint64_t[4];
+template <bool kF16> __device__ __forceinline__ void widen(uint4 u, F8 &x)
 {
     const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const float2 f = widen<kF16>(w[i]);
-        x[2 * i] = f.x;
-        x[2 * i + 1] = f.y;
+        if constexpr (kF16) {
+            const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&w[i]));
+            x[i] = ptx::f2_pack(f.x, f.y);
+        } else {
+            x[i] = ptx::f2_pack(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
+        }
     }
 }
-
-template <bool kF16> __device__ __forceinline__ uint4 narrow8(const float (&x)[8])
+template <bool kF16> __device__ __forceinline__ uint4 narrow(const F8 &x)
 {
-    return make_uint4(narrow<kF16>(x[0], x[1]), narrow<kF16>(x[2], x[3]),
-                      narrow<kF16>(x[4], x[5]), narrow<kF16>(x[6], x[7]));
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        float lo, hi;
+        ptx::f2_unpack(x[i], lo, hi);
+        if constexpr (kF16) {
+            const __half2 h = __floats2half2_rn(lo, hi);
+            w[i] = *reinterpret_cast<const uint32_t *>(&h);
+        } else {
+            const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+            w[i] = *reinterpret_cast<const uint32_t *>(&h);
+        }
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+__device__ __forceinline__ uint64_t both(float x) { return ptx::f2_pack(x, x); }
+__device__ __forceinline__ float add_pair(uint64_t x)
+{
+    float a, b;
+    ptx::f2_unpack(x, a, b);
+    return a + b;
+}
+__device__ __forceinline__ uint64_t swapped(uint64_t x)
+{
+    float a, b;
+    ptx::f2_unpack(x, a, b);
+    return ptx::f2_pack(b, a);
 }
 
+__device__ __forceinline__ const uint16_t *elem_ptr(const void *base, long long elem)
+{
+    return static_cast<const uint16_t *>(base) + elem;
+}
 __device__ __forceinline__ uint4 load16(const void *base, long long elem)
 {
     return *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(base) + elem);
@@ -93,347 +113,455 @@ __device__ __forceinline__ void record_index(uint32_t *status, uint32_t role)
     atomicCAS(status, 0u, code);
 }
 
-// Where a lane's vector v takes its rotation partner from.  rot is a multiple
-// of 16, so both halves of a half-split row are whole vectors.
-struct Partner {
-    int vec;     // vector that holds the partners (v itself: none, or in the vector)
-    float sign;  // of the partner's sine term: -1 first of a pair, +1 second, 0 not rotated
+// The two vectors of lane `l` of a group.  rot is a multiple of 16: the first
+// rot / 16 lanes hold vectors l and l + rot / 16 (half-split pairs face each
+// other), the others the unturned rest in the same manner.
+struct Place {
+    int a, b;     // element offsets in the row
+    bool turned;
 };
-__device__ __forceinline__ Partner partner_of(int v, int rot, int interleaved)
+template <int D> __device__ __forceinline__ Place place_of(int l, int rot)
 {
-    const int half = rot / 16;
-    if (v >= 2 * half)
-        return Partner{v, 0.f};
-    if (interleaved)
-        return Partner{v, 1.f};  // the sign alternates inside the vector
-    return v < half ? Partner{v + half, -1.f} : Partner{v - half, 1.f};
+    const int half = rot / 16, rest = D / 16 - half;
+    if (l < half)
+        return Place{l * 8, (l + half) * 8, true};
+    return Place{(l + half) * 8, (l + half + rest) * 8, false};
 }
 
-// Cosines and signed sines for the 8 elements of vector v at position pos:
-// forward y = x cos + x_partner sin_signed.
-__device__ __forceinline__ void load_angles(const float *table, long long pos, int v, int rot,
-                                            int interleaved, Partner pr, float (&c)[8],
-                                            float (&s)[8])
+// Factors of a lane's turn, y_a = x_a ca + o_a sa and y_b = x_b cb + o_b sb:
+// half-split, o_a = x_b and o_b = x_a; neighbouring pairs, o = x with each
+// pair swapped.  dir = -1 turns back.
+struct Turn {
+    F8 ca, sa, cb, sb;
+};
+template <bool kInter>
+__device__ __forceinline__ void load_turn(const float *table, long long pos, int rot, Place at,
+                                          float dir, Turn &t)
 {
-    if (pr.sign == 0.f) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            c[i] = 1.f;
-            s[i] = 0.f;
-        }
-        return;
-    }
     const float *row = table + pos * rot;
-    if (interleaved) {
-        const float4 cc = *reinterpret_cast<const float4 *>(row + v * 4);
-        const float4 ss = *reinterpret_cast<const float4 *>(row + rot / 2 + v * 4);
-        const float cv[4] = {cc.x, cc.y, cc.z, cc.w}, sv[4] = {ss.x, ss.y, ss.z, ss.w};
+    if constexpr (kInter) {
+        auto one = [&](int elem, F8 &c, F8 &s) {
+            const float4 cc = *reinterpret_cast<const float4 *>(row + elem / 2);
+            const float4 ss = *reinterpret_cast<const float4 *>(row + rot / 2 + elem / 2);
+            const float cv[4] = {cc.x, cc.y, cc.z, cc.w}, sv[4] = {ss.x, ss.y, ss.z, ss.w};
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            c[2 * i] = c[2 * i + 1] = cv[i];
-            s[2 * i] = -sv[i];
-            s[2 * i + 1] = sv[i];
-        }
+            for (int i = 0; i < 4; ++i) {
+                c[i] = both(cv[i]);
+                s[i] = ptx::f2_pack(-dir * sv[i], dir * sv[i]);
+            }
+        };
+        one(at.a, t.ca, t.sa);
+        one(at.b, t.cb, t.sb);
     } else {
-        const float *p = row + min(v, pr.vec) * 8;
+        const float *p = row + at.a;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             const float4 cc = *reinterpret_cast<const float4 *>(p + 4 * i);
             const float4 ss = *reinterpret_cast<const float4 *>(p + rot / 2 + 4 * i);
-            const float cv[4] = {cc.x, cc.y, cc.z, cc.w}, sv[4] = {ss.x, ss.y, ss.z, ss.w};
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                c[4 * i + k] = cv[k];
-                s[4 * i + k] = pr.sign * sv[k];
-            }
+            t.ca[2 * i] = t.cb[2 * i] = ptx::f2_pack(cc.x, cc.y);
+            t.ca[2 * i + 1] = t.cb[2 * i + 1] = ptx::f2_pack(cc.z, cc.w);
+            t.sa[2 * i] = ptx::f2_pack(-dir * ss.x, -dir * ss.y);
+            t.sa[2 * i + 1] = ptx::f2_pack(-dir * ss.z, -dir * ss.w);
+            t.sb[2 * i] = ptx::f2_pack(dir * ss.x, dir * ss.y);
+            t.sb[2 * i + 1] = ptx::f2_pack(dir * ss.z, dir * ss.w);
         }
     }
 }
-
-// The partner elements of a lane's vector: another lane's words, or for
-// neighbouring pairs the vector's own with each pair swapped.
-__device__ __forceinline__ uint4 partner_words(uint4 u, int src_lane, int interleaved)
-{
-    if (interleaved)
-        return make_uint4(__funnelshift_l(u.x, u.x, 16), __funnelshift_l(u.y, u.y, 16),
-                          __funnelshift_l(u.z, u.z, 16), __funnelshift_l(u.w, u.w, 16));
-    return make_uint4(__shfl_sync(0xffffffffu, u.x, src_lane), __shfl_sync(0xffffffffu, u.y, src_lane),
-                      __shfl_sync(0xffffffffu, u.z, src_lane), __shfl_sync(0xffffffffu, u.w, src_lane));
-}
-
-template <int kLanes> __device__ __forceinline__ float group_sum(float x)
+template <bool kInter> __device__ __forceinline__ void turn(const Turn &t, F8 &a, F8 &b)
 {
 #pragma unroll
-    for (int o = kLanes / 2; o > 0; o /= 2)
-        x += __shfl_xor_sync(0xffffffffu, x, o);
-    return x;
+    for (int i = 0; i < 4; ++i) {
+        const uint64_t oa = kInter ? swapped(a[i]) : b[i], ob = kInter ? swapped(b[i]) : a[i];
+        const uint64_t ya = ptx::f2_fma(oa, t.sa[i], ptx::f2_mul(a[i], t.ca[i]));
+        b[i] = ptx::f2_fma(ob, t.sb[i], ptx::f2_mul(b[i], t.cb[i]));
+        a[i] = ya;
+    }
 }
 
-// One tensor of a norm call: its rows and their layout (batch, head, token
-// strides in elements).
-__device__ __forceinline__ long long row_at(const long long (&st)[3], int b, int h, int n)
+// Sum over the lanes of a row, on each of them.
+template <int kLanes> __device__ __forceinline__ float group_sum(float x)
 {
-    return b * st[0] + h * st[1] + n * st[2];
+    if constexpr (kLanes == 6) {
+        const int lane = threadIdx.x & 31, l = lane % 6, base = lane - l;
+        x += __shfl_sync(0xffffffffu, x, base + (l + 3) % 6);
+        return x + __shfl_sync(0xffffffffu, x, base + (l + 1) % 6) +
+               __shfl_sync(0xffffffffu, x, base + (l + 2) % 6);
+    } else {
+#pragma unroll
+        for (int o = kLanes / 2; o > 0; o /= 2)
+            x += __shfl_xor_sync(0xffffffffu, x, o);
+        return x;
+    }
+}
+// Sum over the warp's rows, on the lanes of the first.
+template <int D> __device__ __forceinline__ float row_total(float x)
+{
+    constexpr int kLanes = Geo<D>::kLanes;
+    float sum = x;
+#pragma unroll
+    for (int g = 1; g < Geo<D>::kTokens; ++g)
+        sum += __shfl_down_sync(0xffffffffu, x, g * kLanes);
+    return sum;
 }
 
 // A warp's work: kTokens consecutive tokens (of the flattened batch) and a
 // run of heads of q (which = 0) or k (which = 1).
 struct Item {
-    int which, h0, h1;
-    long long tok0;
+    int h0, h1, b, n;
+    long long pos;
+    bool live;  // the lane's token exists, and has a position in the table
 };
-__device__ __forceinline__ Item item_at(const NormRopeArgs &a, long long it, int tokens)
+template <int D>
+__device__ __forceinline__ Item item_at(const NormRopeArgs &a, int which, int block, int chunk, int lane)
 {
     Item x;
-    const int chunks = a.chunks[0] + a.chunks[1];
-    const long long blk = it / chunks;
-    int c = static_cast<int>(it - blk * chunks);
-    x.which = c >= a.chunks[0] ? 1 : 0;
-    if (x.which)
-        c -= a.chunks[0];
-    x.h0 = c * a.heads_per_chunk;
-    x.h1 = min(x.h0 + a.heads_per_chunk, a.H[x.which]);
-    x.tok0 = blk * tokens;
+    x.h0 = chunk * a.heads_per_chunk;
+    x.h1 = min(x.h0 + a.heads_per_chunk, a.H[which]);
+    const unsigned tok = static_cast<unsigned>(block) * Geo<D>::kTokens + lane / Geo<D>::kLanes;
+    x.live = tok < static_cast<unsigned>(a.tokens) && Geo<D>::in_row(lane);
+    const unsigned b = x.live ? tok / static_cast<unsigned>(a.N) : 0u;
+    x.b = static_cast<int>(b);
+    x.n = x.live ? static_cast<int>(tok - b * static_cast<unsigned>(a.N)) : 0;
+    x.pos = 0;
+    if (x.live && a.rot > 0) {
+        x.pos = a.positions != nullptr ? a.positions[tok] : x.n;
+        if (x.pos < 0 || x.pos >= a.max_pos) {
+            x.live = false;
+            if (lane % Geo<D>::kLanes == 0 && x.h0 == 0)
+                record_index(a.status, kRoleRotate);
+        }
+    }
     return x;
 }
-
-// Position of a token; false where it has none in the table.
-__device__ __forceinline__ bool position_of(const NormRopeArgs &a, long long tok, int n, long long &pos)
+__device__ __forceinline__ long long row_at(const long long (&st)[3], const Item &x)
 {
-    pos = 0;
-    if (a.rot == 0)
-        return true;
-    pos = a.positions != nullptr ? a.positions[tok] : n;
-    return pos >= 0 && pos < a.max_pos;
+    return x.b * st[0] + x.n * st[2];
 }
 
 // ------------------------------------------------------------------ forward
-template <int D, bool kF16>
-__global__ void __launch_bounds__(kThreads) norm_rope_kernel(const NormRopeArgs a)
+template <int D, bool kF16, bool kInter>
+__global__ void __launch_bounds__(kThreads, kBlocksPerSm) norm_rope_kernel(const NormRopeArgs a)
 {
     using G = Geo<D>;
-    const int lane = threadIdx.x & 31, v = lane % G::kLanes, base = lane - v;
-    const long long it = static_cast<long long>(blockIdx.x) * kWarps + threadIdx.x / 32;
-    if (it >= a.items)
+    constexpr int kBatch = 4;  // rows in flight a lane group
+    const int lane = threadIdx.x & 31;
+    long long it = static_cast<long long>(blockIdx.x) * kWarps + threadIdx.x / 32;
+    if (it >= a.items[0] + a.items[1])
         return;
-    const Item item = item_at(a, it, G::kTokens);
-    const int w = item.which;
-    const long long tok = item.tok0 + lane / G::kLanes;
-    const bool in_row = v < G::kVecs;  // d = 96: lanes 12-15 of a group idle
-    bool live = tok < a.tokens;
-    const int b = live ? static_cast<int>(tok / a.N) : 0;
-    const int n = live ? static_cast<int>(tok - static_cast<long long>(b) * a.N) : 0;
-    long long pos;
-    if (live && !position_of(a, tok, n, pos)) {
-        live = false;
-        if (v == 0 && item.h0 == 0)
-            record_index(a.status, kRoleRotate);
-    }
-    live = live && in_row;
-    const void *src = a.x[w];
-    void *dst = a.y[w];
-    const long long in0 = row_at(a.x_st[w], b, 0, n) + v * 8;
-    const long long out0 = row_at(a.y_st[w], b, 0, n) + v * 8;
-    // y = r (x ca + x_partner sb), the weights folded into the angles.
-    float ca[8], sb[8];
-    const Partner pr = partner_of(v, a.rot, a.interleaved);
+    const int w = it < a.items[0] ? 0 : 1;
+    it -= w == 0 ? 0 : a.items[0];
+    const int block = static_cast<int>(it / a.chunks[w]);
+    const Item x = item_at<D>(a, w, block, static_cast<int>(it - static_cast<long long>(block) * a.chunks[w]),
+                              lane);
+    const Place at = place_of<D>(lane % G::kLanes, a.rot);
+    const uint16_t *x_at = elem_ptr(a.x[w], row_at(a.x_st[w], x) + x.h0 * a.x_st[w][1]);
+    uint16_t *y_at = static_cast<uint16_t *>(a.y[w]) + row_at(a.y_st[w], x) + x.h0 * a.y_st[w][1];
+    const long long x_step = a.x_st[w][1], y_step = a.y_st[w][1];
     const bool norm = a.w[w] != nullptr;
-    if (live) {
-        load_angles(a.table, pos, v, a.rot, a.interleaved, pr, ca, sb);
-        if (norm) {
-            float own[8], other[8];
-            const uint4 wo = load16(a.w[w], v * 8);
-            widen8<kF16>(wo, own);
-            widen8<kF16>(a.interleaved ? partner_words(wo, 0, 1) : load16(a.w[w], pr.vec * 8), other);
+    // The weights are folded into the turn: y_a = r (x_a ca w_a + o_a sa w_o).
+    Turn t;
+    if (x.live) {
+        if (at.turned) {
+            load_turn<kInter>(a.table, x.pos, a.rot, at, 1.f, t);
+        } else {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                ca[i] *= own[i];
-                sb[i] *= other[i];
+            for (int i = 0; i < 4; ++i)
+                t.ca[i] = t.cb[i] = both(1.f);
+        }
+        if (norm) {
+            F8 wa, wb;
+            widen<kF16>(load16(a.w[w], at.a), wa);
+            widen<kF16>(load16(a.w[w], at.b), wb);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                t.ca[i] = ptx::f2_mul(t.ca[i], wa[i]);
+                t.cb[i] = ptx::f2_mul(t.cb[i], wb[i]);
+                t.sa[i] = ptx::f2_mul(t.sa[i], kInter ? swapped(wa[i]) : wb[i]);
+                t.sb[i] = ptx::f2_mul(t.sb[i], kInter ? swapped(wb[i]) : wa[i]);
             }
         }
     }
-    const int src_lane = base + pr.vec;
-    for (int h = item.h0; h < item.h1; h += kBatch) {
-        uint4 u[kBatch];
+    for (int h = x.h0; h < x.h1; h += kBatch) {
+        uint4 u[kBatch][2];
 #pragma unroll
         for (int k = 0; k < kBatch; ++k) {
-            u[k] = make_uint4(0, 0, 0, 0);
-            if (live && h + k < item.h1)
-                u[k] = load16(src, in0 + (h + k) * a.x_st[w][1]);
+            u[k][0] = u[k][1] = make_uint4(0, 0, 0, 0);
+            if (x.live && h + k < x.h1) {
+                u[k][0] = load16(x_at, at.a);
+                u[k][1] = load16(x_at, at.b);
+                x_at += x_step;
+            }
         }
 #pragma unroll
         for (int k = 0; k < kBatch; ++k) {
-            float x[8], xp[8], y[8];
-            widen8<kF16>(u[k], x);
-            float r = 1.f;
+            F8 xa, xb;
+            widen<kF16>(u[k][0], xa);
+            widen<kF16>(u[k][1], xb);
+            uint64_t r = both(1.f);
             if (norm) {
-                float ss = 0.f;
+                uint64_t ss = ptx::f2_mul(xa[0], xa[0]);
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
-                    ss = fmaf(x[i], x[i], ss);
-                r = rsqrtf(group_sum<G::kLanes>(ss) * (1.f / D) + a.eps);
+                    if (i > 0)
+                        ss = ptx::f2_fma(i < 4 ? xa[i] : xb[i - 4], i < 4 ? xa[i] : xb[i - 4], ss);
+                r = both(rsqrtf(group_sum<G::kLanes>(add_pair(ss)) * (1.f / D) + a.eps));
             }
-            if (a.rot > 0) {
-                widen8<kF16>(partner_words(u[k], src_lane, a.interleaved), xp);
+            if (at.turned) {
+                turn<kInter>(t, xa, xb);
+            } else if (norm) {
 #pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    y[i] = r * fmaf(x[i], ca[i], pr.sign != 0.f ? xp[i] * sb[i] : 0.f);
-            } else {
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    y[i] = r * (x[i] * ca[i]);
+                for (int i = 0; i < 4; ++i) {
+                    xa[i] = ptx::f2_mul(xa[i], t.ca[i]);
+                    xb[i] = ptx::f2_mul(xb[i], t.cb[i]);
+                }
             }
-            if (live && h + k < item.h1)
-                store16(dst, out0 + (h + k) * a.y_st[w][1], narrow8<kF16>(y));
+            if (norm) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    xa[i] = ptx::f2_mul(xa[i], r);
+                    xb[i] = ptx::f2_mul(xb[i], r);
+                }
+            }
+            if (x.live && h + k < x.h1) {
+                store16(y_at, at.a, narrow<kF16>(xa));
+                store16(y_at, at.b, narrow<kF16>(xb));
+                y_at += y_step;
+            }
         }
     }
 }
 
 // ------------------------------------------------------------------ backward
-// A persistent grid: every warp keeps the weight gradients of its rows in
-// registers (fp32) over all its items, the block adds its warps' sums in a
-// fixed order and writes one partial a block; dw_reduce_kernel adds those in
-// fp64, also in a fixed order, so equal calls give equal bits.
-template <int D, bool kF16>
-__global__ void __launch_bounds__(kThreads) norm_rope_bwd_kernel(const NormRopeArgs a)
+// A persistent grid, its first blocks for q and the others for k in the ratio
+// of their rows: every warp keeps the weight gradients of its rows in registers
+// (fp32) over all its items, the block adds its warps' sums in a fixed order
+// and writes one partial; dw_reduce_kernel adds those, also in a fixed order,
+// so equal calls give equal bits.
+//
+// A row's two reductions stand between its loads and its stores, and with the
+// rows in flight held in registers (two a lane group) a warp spent most of its
+// time waiting: 80 us for B4 H16 N4096 d128.  So each lane copies its own
+// vectors ahead into its own shared-memory slots (cp.async, no barrier: nobody
+// else reads them), across the ends of items, and its addresses step from head
+// to head: 65 us, 6.2 TB/s.  A ring of 3 rows; with 4 and 5 it was 66 and 69.
+constexpr int kRing = 3;
+
+__device__ __forceinline__ void copy_ahead(uint32_t dst, const void *src, bool live)
+{
+    // Zero bytes read fill the slot with zeros.
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0)
+                 : "memory");
+}
+
+template <int D, bool kF16, bool kInter>
+__global__ void __launch_bounds__(kThreads, kBwdBlocksPerSm) norm_rope_bwd_kernel(const NormRopeArgs a)
 {
     using G = Geo<D>;
+    __shared__ uint4 ring[kRing][kWarps][4][32];  // g_a, g_b, x_a, x_b of each lane
     ptx::grid_launch_dependents();
-    const int lane = threadIdx.x & 31, v = lane % G::kLanes, base = lane - v;
-    const bool in_row = v < G::kVecs;
-    const Partner pr = partner_of(v, a.rot, a.interleaved);
-    const int src_lane = base + pr.vec;
-    float dw[2][8];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
+    const Place at = place_of<D>(lane % G::kLanes, a.rot);
+    const int w = static_cast<int>(blockIdx.x) < a.blocks[0] ? 0 : 1;
+    const int block = w == 0 ? blockIdx.x : blockIdx.x - a.blocks[0];
+    const int chunks = a.chunks[w];
+    const int token_blocks = static_cast<int>(a.items[w] / chunks);
+    const int stride = a.blocks[w] * kWarps;
+    const int step_blk = stride / chunks, step_chunk = stride - step_blk * chunks;
+    const bool norm = a.w[w] != nullptr, in_row = G::in_row(lane);
+    F8 wa, wb, acc_a, acc_b;
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-        dw[0][i] = dw[1][i] = 0.f;
-    const long long stride = static_cast<long long>(gridDim.x) * kWarps;
-    for (long long it = static_cast<long long>(blockIdx.x) * kWarps + threadIdx.x / 32; it < a.items;
-         it += stride) {
-        const Item item = item_at(a, it, G::kTokens);
-        const int w = item.which;
-        const long long tok = item.tok0 + lane / G::kLanes;
-        bool live = tok < a.tokens;
-        const int b = live ? static_cast<int>(tok / a.N) : 0;
-        const int n = live ? static_cast<int>(tok - static_cast<long long>(b) * a.N) : 0;
-        long long pos;
-        if (live && !position_of(a, tok, n, pos)) {
-            live = false;
-            if (v == 0 && item.h0 == 0)
-                record_index(a.status, kRoleRotate);
+    for (int i = 0; i < 4; ++i)
+        wa[i] = wb[i] = acc_a[i] = acc_b[i] = both(0.f);
+    if (norm && in_row) {
+        widen<kF16>(load16(a.w[w], at.a), wa);
+        widen<kF16>(load16(a.w[w], at.b), wb);
+    }
+    // Two walks over the warp's (item, head) rows: `ahead` copies, `now` computes.
+    struct Walk {
+        int blk, chunk, left;  // rows left of the item
+        Item x;
+    };
+    auto enter = [&](Walk &k) {
+        if (k.blk < token_blocks) {
+            k.x = item_at<D>(a, w, k.blk, k.chunk, lane);
+            k.left = k.x.h1 - k.x.h0;
         }
-        live = live && in_row;
-        const bool norm = a.w[w] != nullptr;
-        const long long x0 = row_at(a.x_st[w], b, 0, n) + v * 8;
-        const long long g0 = row_at(a.g_st[w], b, 0, n) + v * 8;
-        const long long y0 = row_at(a.y_st[w], b, 0, n) + v * 8;
-        float c[8], s[8], wt[8], acc[8];
+    };
+    auto next_item = [&](Walk &k) {
+        k.blk += step_blk;
+        k.chunk += step_chunk;
+        if (k.chunk >= chunks) {
+            k.chunk -= chunks;
+            ++k.blk;
+        }
+        enter(k);
+    };
+    Walk ahead, now;
+    ahead.blk = (block * kWarps + warp) / chunks;
+    ahead.chunk = block * kWarps + warp - ahead.blk * chunks;
+    enter(ahead);
+    now = ahead;
+    // Where the copies read: stepped from head to head.  A lane without a row
+    // stays at the tensor's base, of which it reads nothing.
+    const uint16_t *g_at, *x_at;
+    long long g_step, x_step;
+    auto point = [&]() {
+        if (ahead.blk >= token_blocks)
+            return;
+        const bool live = ahead.x.live;
+        g_at = elem_ptr(a.g[w], live ? row_at(a.g_st[w], ahead.x) + ahead.x.h0 * a.g_st[w][1] + at.a : 0);
+        g_step = live ? a.g_st[w][1] : 0;
+        if (norm) {
+            x_at = elem_ptr(a.x[w], live ? row_at(a.x_st[w], ahead.x) + ahead.x.h0 * a.x_st[w][1] + at.a : 0);
+            x_step = live ? a.x_st[w][1] : 0;
+        }
+    };
+    point();
+    const int b_off = in_row ? at.b - at.a : 0;
+    const uint32_t ring0 = ptx::smem_addr(&ring[0][warp][0][lane]);
+    constexpr uint32_t kSlot = sizeof(ring[0]);
+    uint32_t put = ring0;
+    int get = 0;
+    auto copy_row = [&]() {
+        if (ahead.blk < token_blocks) {
+            const bool live = ahead.x.live;
+            copy_ahead(put, g_at, live);
+            copy_ahead(put + 512, g_at + b_off, live);
+            g_at += g_step;
+            if (norm) {
+                copy_ahead(put + 1024, x_at, live);
+                copy_ahead(put + 1536, x_at + b_off, live);
+                x_at += x_step;
+            }
+            put = put == ring0 + (kRing - 1) * kSlot ? ring0 : put + kSlot;
+            if (--ahead.left == 0) {
+                next_item(ahead);
+                point();
+            }
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+#pragma unroll 1
+    for (int i = 0; i < kRing - 1; ++i)
+        copy_row();
+    while (now.blk < token_blocks) {
+        const bool live = now.x.live;
+        uint16_t *y_at = static_cast<uint16_t *>(a.y[w]) + row_at(a.y_st[w], now.x) +
+                         now.x.h0 * a.y_st[w][1] + at.a;
+        Turn t;
+        if (live && at.turned)
+            load_turn<kInter>(a.table, now.x.pos, a.rot, at, -1.f, t);
+#pragma unroll 1
+        for (; now.left > 0; --now.left) {
+            asm volatile("cp.async.wait_group %0;" ::"n"(kRing - 2) : "memory");
+            const uint4(&slot)[4][32] = ring[get][warp];
+            F8 ga, gb;
+            widen<kF16>(slot[0][lane], ga);
+            widen<kF16>(slot[1][lane], gb);
+            if (at.turned && live)
+                turn<kInter>(t, ga, gb);
+            if (norm) {
+                F8 xa, xb;
+                widen<kF16>(slot[2][lane], xa);
+                widen<kF16>(slot[3][lane], xb);
+                uint64_t ss = both(0.f), gx = both(0.f);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            c[i] = wt[i] = 1.f;
-            s[i] = acc[i] = 0.f;
-        }
-        if (live) {
-            load_angles(a.table, pos, v, a.rot, a.interleaved, pr, c, s);
-            if (norm)
-                widen8<kF16>(load16(a.w[w], v * 8), wt);
-        }
-        for (int h = item.h0; h < item.h1; h += kBatch) {
-            uint4 ux[kBatch], ug[kBatch];
+                for (int i = 0; i < 4; ++i) {
+                    ss = ptx::f2_fma(xa[i], xa[i], ss);
+                    gx = ptx::f2_fma(ptx::f2_mul(ga[i], wa[i]), xa[i], gx);
+                    ss = ptx::f2_fma(xb[i], xb[i], ss);
+                    gx = ptx::f2_fma(ptx::f2_mul(gb[i], wb[i]), xb[i], gx);
+                }
+                const float r = rsqrtf(group_sum<G::kLanes>(add_pair(ss)) * (1.f / D) + a.eps);
+                const float m = group_sum<G::kLanes>(add_pair(gx)) * (1.f / D) * r * r;
+                const uint64_t rr = both(r), mr = both(-m * r);
 #pragma unroll
-            for (int k = 0; k < kBatch; ++k) {
-                ux[k] = ug[k] = make_uint4(0, 0, 0, 0);
-                if (live && h + k < item.h1) {
-                    ug[k] = load16(a.g[w], g0 + (h + k) * a.g_st[w][1]);
-                    if (norm)
-                        ux[k] = load16(a.x[w], x0 + (h + k) * a.x_st[w][1]);
+                for (int i = 0; i < 4; ++i) {
+                    const uint64_t ra = ptx::f2_mul(ga[i], rr), rb = ptx::f2_mul(gb[i], rr);
+                    acc_a[i] = ptx::f2_fma(ra, xa[i], acc_a[i]);
+                    acc_b[i] = ptx::f2_fma(rb, xb[i], acc_b[i]);
+                    ga[i] = ptx::f2_fma(ra, wa[i], ptx::f2_mul(xa[i], mr));
+                    gb[i] = ptx::f2_fma(rb, wb[i], ptx::f2_mul(xb[i], mr));
                 }
             }
-#pragma unroll
-            for (int k = 0; k < kBatch; ++k) {
-                float g[8];
-                widen8<kF16>(ug[k], g);
-                if (a.rot > 0) {  // the transposed rotation: the sines change sign
-                    float gp[8];
-                    widen8<kF16>(partner_words(ug[k], src_lane, a.interleaved), gp);
-#pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        g[i] = fmaf(g[i], c[i], pr.sign != 0.f ? -gp[i] * s[i] : 0.f);
-                }
-                if (norm) {
-                    float x[8], ss = 0.f, gx = 0.f;
-                    widen8<kF16>(ux[k], x);
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        ss = fmaf(x[i], x[i], ss);
-                        gx = fmaf(g[i] * wt[i], x[i], gx);
-                    }
-                    const float r = rsqrtf(group_sum<G::kLanes>(ss) * (1.f / D) + a.eps);
-                    const float m = group_sum<G::kLanes>(gx) * (1.f / D) * r * r;
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        acc[i] = fmaf(g[i], x[i] * r, acc[i]);
-                        g[i] = r * fmaf(-x[i], m, g[i] * wt[i]);
-                    }
-                }
-                if (live && h + k < item.h1)
-                    store16(a.y[w], y0 + (h + k) * a.y_st[w][1], narrow8<kF16>(g));
+            if (live) {
+                store16(y_at, 0, narrow<kF16>(ga));
+                store16(y_at, b_off, narrow<kF16>(gb));
+                y_at += a.y_st[w][1];
             }
+            get = get + 1 == kRing ? 0 : get + 1;
+            copy_row();
         }
+        next_item(now);
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    if (!norm)  // no weights: nothing to sum
+        return;
+    // Groups of the warp, then the block's warps (the ring's memory is free).
+    float(&part)[kWarps][D] = *reinterpret_cast<float(*)[kWarps][D]>(ring);
+    __syncthreads();
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            dw[0][i] += w == 0 ? acc[i] : 0.f;
-            dw[1][i] += w == 1 ? acc[i] : 0.f;
+    for (int i = 0; i < 8; ++i) {
+        float lo, hi;
+        ptx::f2_unpack(i < 4 ? acc_a[i] : acc_b[i - 4], lo, hi);
+        lo = row_total<D>(lo);
+        hi = row_total<D>(hi);
+        if (lane < G::kLanes) {
+            float *dst = &part[warp][(i < 4 ? at.a : at.b) + 2 * (i % 4)];
+            dst[0] = lo;
+            dst[1] = hi;
         }
     }
-    if (a.partial == nullptr)  // no weights: nothing to sum
-        return;
-    // Groups of a warp first, then the block's warps through shared memory.
-    __shared__ float part[kWarps][2][D];
-#pragma unroll
-    for (int t = 0; t < 2; ++t)
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            float x = dw[t][i];
-#pragma unroll
-            for (int o = G::kLanes; o < 32; o *= 2)
-                x += __shfl_xor_sync(0xffffffffu, x, o);
-            if (lane < G::kVecs)
-                part[threadIdx.x / 32][t][lane * 8 + i] = x;
-        }
     __syncthreads();
-    for (int i = threadIdx.x; i < 2 * D; i += kThreads) {
+    for (int i = threadIdx.x; i < D; i += kThreads) {
         float x = 0.f;
 #pragma unroll
         for (int k = 0; k < kWarps; ++k)
-            x += part[k][i / D][i % D];
-        a.partial[static_cast<size_t>(blockIdx.x) * 2 * D + i] = x;
+            x += part[k][i];
+        a.partial[static_cast<size_t>(blockIdx.x) * D + i] = x;
     }
 }
 
-// dw[t][c] = sum over the blocks' partials.  32 columns a CTA, 32 rows of
-// threads over the blocks.
-constexpr int kReduceRows = 32;
-__global__ void __launch_bounds__(32 * kReduceRows)
-    dw_reduce_kernel(const float *partial, int blocks, int D, float *dwq, float *dwk)
+// dw[t][c] = sum over the partials of tensor t's blocks, kept to twice fp32's
+// length by carrying each addition's rounding error along (Knuth's two-sum);
+// fp64 additions, at this chip's rate, took 8 to 14 us here.  Eight columns a
+// CTA, 32 rows of threads over the blocks.
+constexpr int kReduceRows = 32, kReduceCols = 8;
+struct Sum2 {
+    float s = 0.f, e = 0.f;
+    __device__ __forceinline__ void add(float x)
+    {
+        const float t = s + x, z = t - s;
+        e += (s - (t - z)) + (x - z);
+        s = t;
+    }
+};
+__global__ void __launch_bounds__(kReduceCols *kReduceRows)
+    dw_reduce_kernel(const float *partial, int q_blocks, int k_blocks, int D, float *dwq, float *dwk)
 {
-    __shared__ double part[kReduceRows][33];
+    __shared__ float2 part[kReduceRows][kReduceCols];
+    const int t = blockIdx.x * kReduceCols >= D ? 1 : 0;
+    const int col = blockIdx.x * kReduceCols - t * D + threadIdx.x;
+    float *dst = t == 0 ? dwq : dwk;
+    if (dst == nullptr)
+        return;
     ptx::grid_dependency_wait();
-    const int col = blockIdx.x * 32 + threadIdx.x;  // of 2 D, a multiple of 32
-    double x = 0.0;
-    for (int b = threadIdx.y; b < blocks; b += kReduceRows)
-        x += partial[static_cast<size_t>(b) * 2 * D + col];
-    part[threadIdx.y][threadIdx.x] = x;
+    const int b0 = t == 0 ? 0 : q_blocks, b1 = t == 0 ? q_blocks : q_blocks + k_blocks;
+    Sum2 x;
+#pragma unroll 8
+    for (int b = b0 + threadIdx.y; b < b1; b += kReduceRows)
+        x.add(partial[static_cast<size_t>(b) * D + col]);
+    part[threadIdx.y][threadIdx.x] = make_float2(x.s, x.e);
     __syncthreads();
     if (threadIdx.y != 0)
         return;
-    x = 0.0;
+    x = Sum2();
 #pragma unroll
-    for (int r = 0; r < kReduceRows; ++r)
-        x += part[r][threadIdx.x];
-    float *dst = col < D ? dwq : dwk;
-    if (dst != nullptr)
-        dst[col < D ? col : col - D] = static_cast<float>(x);
+    for (int r = 0; r < kReduceRows; ++r) {
+        x.add(part[r][threadIdx.x].x);
+        x.e += part[r][threadIdx.x].y;
+    }
+    dst[col] = x.s + x.e;
 }
 
 // ------------------------------------------------------------------ append
@@ -461,11 +589,12 @@ __device__ __forceinline__ int find_sequence(const int *cu, int B, long long t, 
 
 // Token t = cu_q[b] + i of sequence b goes to position kv_len[b] - (new
 // tokens of b) + i of its pages, a key turned by that position's angles.
-template <int D, bool kF16>
-__global__ void __launch_bounds__(kThreads) kv_append_kernel(const KvAppendArgs a)
+template <int D, bool kF16, bool kInter>
+__global__ void __launch_bounds__(kThreads, kBlocksPerSm) kv_append_kernel(const KvAppendArgs a)
 {
     using G = Geo<D>;
-    const int lane = threadIdx.x & 31, v = lane % G::kLanes, base = lane - v;
+    constexpr int kBatch = 4;
+    const int lane = threadIdx.x & 31, l = lane % G::kLanes, base = lane - l;
     const long long it = static_cast<long long>(blockIdx.x) * kWarps + threadIdx.x / 32;
     if (it >= a.items)
         return;
@@ -477,25 +606,29 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const KvAppendArgs 
         c -= a.chunks;
     const int h0 = c * a.heads_per_chunk, h1 = min(h0 + a.heads_per_chunk, a.H);
     const long long tok = blk * G::kTokens + lane / G::kLanes;
-    const bool exists = tok < a.T && v < G::kVecs;
+    const bool exists = tok < a.T && G::in_row(lane);
+    const Place at = place_of<D>(l, is_v ? 0 : a.rot);
     const void *src = is_v ? a.v : a.k;
     const long long tok_stride = is_v ? a.v_st[0] : a.k_st[0];
     const long long head_stride = is_v ? a.v_st[1] : a.k_st[1];
-    const long long in0 = (exists ? tok : 0) * tok_stride + v * 8;
+    const long long in0 = (exists ? tok : 0) * tok_stride;
     // The rows do not depend on where they go: the first batch is in flight
     // while the token's sequence, page and angles are looked up.
-    uint4 u[kBatch];
+    uint4 u[kBatch][2];
     auto load = [&](int h) {
 #pragma unroll
         for (int k = 0; k < kBatch; ++k) {
-            u[k] = make_uint4(0, 0, 0, 0);
-            if (exists && h + k < h1)
-                u[k] = load16(src, in0 + (h + k) * head_stride);
+            u[k][0] = u[k][1] = make_uint4(0, 0, 0, 0);
+            if (exists && h + k < h1) {
+                const long long row = in0 + (h + k) * head_stride;
+                u[k][0] = load16(src, row + at.a);
+                u[k][1] = load16(src, row + at.b);
+            }
         }
     };
     load(h0);
-    bool live = tok < a.T, bad = false;
-    const int b = find_sequence<G::kLanes>(a.cu_q, a.B, tok, v, base);
+    bool live = exists, bad = false;
+    const int b = find_sequence<G::kLanes>(a.cu_q, a.B, tok, l, base);
     long long pos = 0, out0 = 0;
     if (live && b >= 0 && b < a.B) {
         const int q0 = a.cu_q[b], q1 = a.cu_q[b + 1];
@@ -507,40 +640,38 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const KvAppendArgs 
             const int page = a.page_table[static_cast<long long>(b) * a.table_stride + col];
             bad = page < 0 || page >= a.num_pages;
             const long long slot = pos & ((1LL << a.page_shift) - 1);
-            out0 = (is_v ? a.vc_st[0] * page + a.vc_st[2] * slot
-                         : a.kc_st[0] * page + a.kc_st[2] * slot) + v * 8;
+            out0 = is_v ? a.vc_st[0] * page + a.vc_st[2] * slot
+                        : a.kc_st[0] * page + a.kc_st[2] * slot;
         }
-        if (bad && v == 0 && h0 == 0 && !is_v)
+        if (bad && l == 0 && h0 == 0 && !is_v)
             record_index(a.status, kRoleAppend);
-        live = !bad && v < G::kVecs;
+        live = !bad;
     } else {
         live = false;  // behind the last sequence (or before the first)
     }
     void *dst = is_v ? a.v_cache : a.k_cache;
     const long long out_head = is_v ? a.vc_st[1] : a.kc_st[1];
-    const bool turn = !is_v && a.rot > 0;
-    const Partner pr = partner_of(v, turn ? a.rot : 0, a.interleaved);
-    float ca[8], sa[8];
-    if (turn && live)
-        load_angles(a.table, pos, v, a.rot, a.interleaved, pr, ca, sa);
+    Turn t;
+    if (live && at.turned)
+        load_turn<kInter>(a.table, pos, a.rot, at, 1.f, t);
     for (int h = h0;;) {
+        if (live) {
 #pragma unroll
-        for (int k = 0; k < kBatch; ++k) {
-            uint4 y = u[k];
-            if (turn) {
-                const uint4 up = partner_words(u[k], base + pr.vec, a.interleaved);
-                if (pr.sign != 0.f) {  // unrotated elements keep their bits
-                    float x[8], xp[8];
-                    widen8<kF16>(u[k], x);
-                    widen8<kF16>(up, xp);
-#pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        x[i] = fmaf(x[i], ca[i], xp[i] * sa[i]);
-                    y = narrow8<kF16>(x);
+            for (int k = 0; k < kBatch; ++k) {
+                if (at.turned) {  // unturned elements keep their bits
+                    F8 xa, xb;
+                    widen<kF16>(u[k][0], xa);
+                    widen<kF16>(u[k][1], xb);
+                    turn<kInter>(t, xa, xb);
+                    u[k][0] = narrow<kF16>(xa);
+                    u[k][1] = narrow<kF16>(xb);
+                }
+                if (h + k < h1) {
+                    const long long row = out0 + (h + k) * out_head;
+                    store16(dst, row + at.a, u[k][0]);
+                    store16(dst, row + at.b, u[k][1]);
                 }
             }
-            if (live && h + k < h1)
-                store16(dst, out0 + (h + k) * out_head, y);
         }
         h += kBatch;
         if (h >= h1)
@@ -550,90 +681,98 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const KvAppendArgs 
 }
 
 // Heads an item: enough items to give every SM kItemsPerSm warps, at least
-// one batch of rows each.  More heads an item read the angles less often.
-constexpr int kItemsPerSm = 32;
+// kMinHeads heads each.  More heads an item read the angles less often.
+constexpr int kItemsPerSm = 64, kMinHeads = 4;
 int heads_per_item(long long token_blocks, int heads, int num_sms)
 {
     const long long want = static_cast<long long>(num_sms) * kItemsPerSm;
-    int n = kBatch;
+    int n = kMinHeads;
     while (n < heads && token_blocks * ((heads + 2 * n - 1) / (2 * n)) >= want)
         n *= 2;
     return n;
 }
 
-cudaError_t grid_of(long long items, unsigned *grid)
-{
-    const long long blocks = (items + kWarps - 1) / kWarps;
-    if (blocks > 0x7fffffffLL)
-        return cudaErrorInvalidConfiguration;
-    *grid = static_cast<unsigned>(blocks);
-    return cudaSuccess;
-}
-
-template <int D, bool kF16>
+template <int D, bool kF16, bool kInter>
 cudaError_t norm_rope(NormRopeArgs a, int num_sms, cudaStream_t stream)
 {
     const long long blocks = (a.tokens + Geo<D>::kTokens - 1) / Geo<D>::kTokens;
     a.heads_per_chunk = heads_per_item(blocks, a.H[0] + a.H[1], num_sms);
-    for (int t = 0; t < 2; ++t)
+    for (int t = 0; t < 2; ++t) {
         a.chunks[t] = (a.H[t] + a.heads_per_chunk - 1) / a.heads_per_chunk;
-    a.items = blocks * (a.chunks[0] + a.chunks[1]);
+        a.items[t] = blocks * a.chunks[t];
+    }
     if (a.g[0] == nullptr && a.g[1] == nullptr) {
-        unsigned grid;
-        cudaError_t e = grid_of(a.items, &grid);
-        if (e != cudaSuccess)
-            return e;
-        norm_rope_kernel<D, kF16><<<grid, kThreads, 0, stream>>>(a);
+        const long long grid = (a.items[0] + a.items[1] + kWarps - 1) / kWarps;
+        if (grid > 0x7fffffffLL)
+            return cudaErrorInvalidConfiguration;
+        norm_rope_kernel<D, kF16, kInter><<<static_cast<unsigned>(grid), kThreads, 0, stream>>>(a);
         return cudaGetLastError();
     }
-    const long long want = (a.items + kWarps - 1) / kWarps;
-    const int grid = static_cast<int>(want < norm_rope_bwd_blocks(num_sms)
-                                          ? want : norm_rope_bwd_blocks(num_sms));
-    norm_rope_bwd_kernel<D, kF16><<<grid, kThreads, 0, stream>>>(a);
-    cudaError_t e = cudaGetLastError();
+    // One block a kWarps items while they all fit on the SMs, else the SMs'
+    // blocks in the ratio of the rows, each tensor at least one.
+    const long long need[2] = {(a.items[0] + kWarps - 1) / kWarps, (a.items[1] + kWarps - 1) / kWarps};
+    const int all = norm_rope_bwd_blocks(num_sms);
+    if (need[0] + need[1] <= all) {
+        a.blocks[0] = static_cast<int>(need[0]);
+        a.blocks[1] = static_cast<int>(need[1]);
+    } else {
+        const long long q = (static_cast<long long>(all) * a.H[0] + (a.H[0] + a.H[1]) / 2) /
+                            (static_cast<long long>(a.H[0]) + a.H[1]);
+        a.blocks[0] = static_cast<int>(a.H[0] == 0 ? 0 : a.H[1] == 0 ? all : q < 1 ? 1 : q > all - 1 ? all - 1 : q);
+        a.blocks[1] = all - a.blocks[0];
+    }
+    const int grid = a.blocks[0] + a.blocks[1];
+    norm_rope_bwd_kernel<D, kF16, kInter><<<grid, kThreads, 0, stream>>>(a);
+    const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess || a.partial == nullptr)
         return e;
     cudaLaunchAttribute pdl[1];
     pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     pdl[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(2 * D / 32);
-    cfg.blockDim = dim3(32, kReduceRows);
+    cfg.gridDim = dim3(2 * D / kReduceCols);
+    cfg.blockDim = dim3(kReduceCols, kReduceRows);
     cfg.stream = stream;
     cfg.attrs = pdl;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, dw_reduce_kernel, static_cast<const float *>(a.partial), grid, D,
-                              a.dw[0], a.dw[1]);
+    return cudaLaunchKernelEx(&cfg, dw_reduce_kernel, static_cast<const float *>(a.partial),
+                              a.blocks[0], a.blocks[1], D, a.dw[0], a.dw[1]);
 }
 
-template <int D, bool kF16>
+template <int D, bool kF16, bool kInter>
 cudaError_t kv_append(KvAppendArgs a, int num_sms, cudaStream_t stream)
 {
     const long long blocks = (a.T + Geo<D>::kTokens - 1) / Geo<D>::kTokens;
     a.heads_per_chunk = heads_per_item(2 * blocks, a.H, num_sms);
     a.chunks = (a.H + a.heads_per_chunk - 1) / a.heads_per_chunk;
     a.items = blocks * 2 * a.chunks;
-    unsigned grid;
-    cudaError_t e = grid_of(a.items, &grid);
-    if (e != cudaSuccess)
-        return e;
-    kv_append_kernel<D, kF16><<<grid, kThreads, 0, stream>>>(a);
+    const long long grid = (a.items + kWarps - 1) / kWarps;
+    if (grid > 0x7fffffffLL)
+        return cudaErrorInvalidConfiguration;
+    kv_append_kernel<D, kF16, kInter><<<static_cast<unsigned>(grid), kThreads, 0, stream>>>(a);
     return cudaGetLastError();
 }
 
 template <int D> cudaError_t norm_rope_typed(const NormRopeArgs &a, int num_sms, cudaStream_t stream)
 {
-    return a.f16 ? norm_rope<D, true>(a, num_sms, stream) : norm_rope<D, false>(a, num_sms, stream);
+    if (a.f16)
+        return a.interleaved ? norm_rope<D, true, true>(a, num_sms, stream)
+                             : norm_rope<D, true, false>(a, num_sms, stream);
+    return a.interleaved ? norm_rope<D, false, true>(a, num_sms, stream)
+                         : norm_rope<D, false, false>(a, num_sms, stream);
 }
 template <int D> cudaError_t kv_append_typed(const KvAppendArgs &a, int num_sms, cudaStream_t stream)
 {
-    return a.f16 ? kv_append<D, true>(a, num_sms, stream) : kv_append<D, false>(a, num_sms, stream);
+    if (a.f16)
+        return a.interleaved ? kv_append<D, true, true>(a, num_sms, stream)
+                             : kv_append<D, true, false>(a, num_sms, stream);
+    return a.interleaved ? kv_append<D, false, true>(a, num_sms, stream)
+                         : kv_append<D, false, false>(a, num_sms, stream);
 }
 
 }  // namespace
 
-// Eight blocks of four warps a SM fill it at the backward kernel's registers.
-int norm_rope_bwd_blocks(int num_sms) { return 8 * num_sms; }
+int norm_rope_bwd_blocks(int num_sms) { return kBwdBlocksPerSm * num_sms; }
 
 cudaError_t launch_norm_rope(const NormRopeArgs &a, int num_sms, cudaStream_t stream)
 {
