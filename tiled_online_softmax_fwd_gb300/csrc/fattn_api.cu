@@ -1688,12 +1688,19 @@ fattn_status_t attn_fwd_paged(const void *q, const void *k_cache, const void *v_
     if ((s = status_word(&a.status)) != FATTN_OK)
         return s;
     const int G = Hq / Hk;
-    const unsigned box_tokens = static_cast<unsigned>(max_q < ws.tile_tokens ? max_q : ws.tile_tokens);
+    const int box_tokens = std::min(max_q, ws.tile_tokens), quad_tokens = std::min(max_q, 32 / G);
     const unsigned box_slots = static_cast<unsigned>(page_size < 128 ? page_size : 128);
-    fattn::FwdMaps maps;
-    if ((s = make_row_map(encode, &maps.q, q, d, {G, Hk, T},
-                          {rows[0].st[1], rows[0].st[1] * G, rows[0].st[0]},
-                          {static_cast<unsigned>(G), 1u, box_tokens}, dtype == 1)) != FATTN_OK)
+    fattn::PagedMaps maps;
+    const long long q_ext[3] = {G, Hk, T}, q_st[3] = {rows[0].st[1], rows[0].st[1] * G, rows[0].st[0]};
+    if ((s = make_row_map(encode, &maps.q, q, d, q_ext, q_st,
+                          {static_cast<unsigned>(G), 1u, static_cast<unsigned>(box_tokens)},
+                          dtype == 1)) != FATTN_OK)
+        return s;
+    maps.q_quad = maps.q;
+    if (quad_tokens > 0 && quad_tokens != box_tokens &&
+        (s = make_row_map(encode, &maps.q_quad, q, d, q_ext, q_st,
+                          {static_cast<unsigned>(G), 1u, static_cast<unsigned>(quad_tokens)},
+                          dtype == 1)) != FATTN_OK)
         return s;
     CUtensorMap *cache[2] = {&maps.k, &maps.v};
     for (int i = 0; i < 2; ++i) {
@@ -1726,7 +1733,8 @@ fattn_status_t attn_fwd_paged(const void *q, const void *k_cache, const void *v_
     a.page_shift = __builtin_ctz(static_cast<unsigned>(page_size));
     a.max_keys = max_pages * page_size;
     a.tile_tokens = ws.tile_tokens;
-    a.q_box_tokens = static_cast<int>(box_tokens);
+    a.q_box_tokens = box_tokens;
+    a.q_quad_tokens = quad_tokens;
     a.slot_rows = ws.slot_rows;
     a.g_inverse = (65536u + G - 1) / G;
     a.sl2 = scale * 1.4426950408889634f;

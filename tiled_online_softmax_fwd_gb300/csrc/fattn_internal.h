@@ -170,11 +170,16 @@ struct PagedArgs {
     int T, B, Hk, G, d, f16, causal, max_q;
     int num_pages, page_shift, max_keys;
     int tile_tokens, q_box_tokens, slot_rows;
+    int q_quad_tokens;   // tokens of a copy of at most 32 rows (0: G > 32)
     uint32_t g_inverse;  // ceil(2^16 / G)
     float sl2;           // scale * log2(e)
 };
-// maps.q: (d, G, Hk, T), box (64, G, 1, q_box_tokens); maps.k, v: (d, slot,
-// Hk, page), box (64, min(page_size, 128), 1, 1); 128-byte swizzle.
-cudaError_t launch_paged(const PagedArgs &a, const FwdMaps &maps, int num_sms, cudaStream_t stream);
+// q: (d, G, Hk, T), box (64, G, 1, q_box_tokens); q_quad: the same tensor, box
+// (64, G, 1, q_quad_tokens) (q's where that is 0); k, v: (d, slot, Hk, page),
+// box (64, min(page_size, 128), 1, 1); 128-byte swizzle.
+struct PagedMaps {
+    CUtensorMap q, q_quad, k, v;
+};
+cudaError_t launch_paged(const PagedArgs &a, const PagedMaps &maps, int num_sms, cudaStream_t stream);
 
 }  // namespace fattn

@@ -19,7 +19,9 @@
 // Bound.  With few new tokens the cache's bytes (HBM); with many, the tensor
 // cores and exponentials.  One persistent CTA a SM serves both:
 //   warps 0-7    two softmax warpgroups (thread = row)
-//   warp 8       TMA producer: pages -> a ring of 128-key tiles
+//   warp 8       walks the CTA's work, publishes each piece of it to the other
+//                warps, and copies: Q tiles, and pages into a ring of 128-key
+//                tiles (TMA)
 //   warp 9       MMA issuer: S = Q K^T and O += P V on tcgen05
 //   warps 10-11  V in place: bf16 -> fp16 (P is fp16, and both operands of a
 //                product share one type), and zeros behind the last key: a
@@ -31,6 +33,13 @@
 // last tile -- has the two warpgroups take alternate key tiles of the same Q
 // tile instead, into accumulators of their own that the epilogue merges, so
 // the chain S -> softmax -> P V of one key tile overlaps the next one's.
+//
+// A single tile of at most 32 rows (decode steps) would leave one warp of each
+// warpgroup with 128 exponentials a key tile, one after the other, and three
+// idle: a warp reaches only its own 32 TMEM lanes.  So such rows are copied
+// into all four lane quarters, and warp w takes keys 32 w .. 32 w + 31 of each
+// key tile for its copy, with P zero at the others: four rows' statistics and
+// accumulators instead of one, merged once a unit.
 //
 // Schedule.  Lengths live in device memory (a captured graph follows them),
 // so the grid finds its own work: the units' costs, in keys plus a constant
@@ -45,6 +54,8 @@
 #include <float.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "fattn_internal.h"
 #include "ptx_sm103.cuh"
 
@@ -57,6 +68,8 @@ constexpr int kBM = 128;  // rows of a Q tile
 constexpr int kBN = 128;  // keys of a key tile
 constexpr int kThreads = 384;
 constexpr int kWarpLoad = 8, kWarpMma = 9, kWarpConv = 10;
+constexpr int kPieces = 4;     // pieces published ahead
+constexpr int kQuadRows = 32;  // rows of a tile that fit a lane quarter
 constexpr uint32_t kTmemCols = 512;
 constexpr uint64_t kWaitLimitNs = 2000000000ull;
 constexpr float kRescaleLog2 = 8.0f;
@@ -87,35 +100,64 @@ struct Start {
     long long y, left;
 };
 
+struct Seq {
+    int q0, n, L;  // first token, new tokens, keys
+};
+
+// A piece of work: key tiles [j0, j1) of a unit.
+struct Piece {
+    int h;        // key head; -1: no more work
+    Seq s;
+    int j0, j1;
+    int slot;     // workspace slot of a partial result, or -1: the whole unit
+    int alt;      // one Q tile: the warpgroups take alternate key tiles
+    int quad;     // ... of at most 32 rows, copied to all four lane quarters
+    int q_buf;    // a single tile's Q buffer: the two in turn
+    int tile[2];  // Q tile of each warpgroup
+    int rows[2];  // its rows
+    int n[2];     // its key tiles in this piece
+};
+
 struct Bars {
     uint64_t q_full[2], q_empty[2];
     uint64_t kv_full[8], kv_empty[8], v_ready[8];
     uint64_t s_full[2], p_half[2], p_full[2], o_full[2], o_empty[2];
     uint64_t other_done;  // single-tile units: warpgroup 1's statistics are written
+    uint64_t quarters;    // quad units: the four warps' merge steps
+    uint64_t piece_full[kPieces], piece_empty[kPieces];
     uint64_t drain;
     uint32_t tmem_base;
     int abort;
     Start start;
+    Piece pieces[kPieces];
     long long warp_sum[kThreads / 32];
     float2 other[kBM];  // (m, l) of warpgroup 1's half of a single-tile unit
 };
 
 // ------------------------------------------------------------------ schedule
-struct Seq {
-    int q0, n, L;  // first token, new tokens, keys
-};
 
-// A sequence's lists, brought into range (bad: some value was not).
+// A sequence's entries of the lists as they stand, and brought into range
+// (bad: some value was not).
+struct Raw {
+    int c0, c1, L;
+};
+__device__ __forceinline__ Raw load_raw(const PagedArgs &a, int b)
+{
+    return Raw{a.cu_q[b], a.cu_q[b + 1], a.kv_len[b]};
+}
+__device__ __forceinline__ Seq in_range(const PagedArgs &a, Raw r, bool &bad)
+{
+    Seq s;
+    s.q0 = min(max(r.c0, 0), a.T);
+    s.n = min(max(r.c1, s.q0), a.T) - s.q0;
+    s.n = min(s.n, a.max_q);
+    s.L = min(max(r.L, 0), a.max_keys);
+    bad = s.q0 != r.c0 || s.n != static_cast<long long>(r.c1) - r.c0 || s.L != r.L;
+    return s;
+}
 __device__ __forceinline__ Seq load_seq(const PagedArgs &a, int b, bool &bad)
 {
-    const int c0 = a.cu_q[b], c1 = a.cu_q[b + 1], kl = a.kv_len[b];
-    Seq s;
-    s.q0 = min(max(c0, 0), a.T);
-    s.n = min(max(c1, s.q0), a.T) - s.q0;
-    s.n = min(s.n, a.max_q);
-    s.L = min(max(kl, 0), a.max_keys);
-    bad = s.q0 != c0 || s.n != static_cast<long long>(c1) - c0 || s.L != kl;
-    return s;
+    return in_range(a, load_raw(a, b), bad);
 }
 
 __device__ __forceinline__ int tiles_of(const PagedArgs &a, const Seq &s)
@@ -236,18 +278,6 @@ __device__ void find_start(const PagedArgs &a, Bars &b)
         a.starts[blockIdx.x] = make_int4(-1, 0, 0, 0);
 }
 
-// A piece of work: key tiles [j0, j1) of a unit.
-struct Piece {
-    int b, h, p;
-    Seq s;
-    int j0, j1;
-    int slot;     // workspace slot of a partial result, or -1: the whole unit
-    bool alt;     // one Q tile: the warpgroups take alternate key tiles
-    int tile[2];  // Q tile of each warpgroup
-    int rows[2];  // its rows (0: absent)
-    int n[2];     // its key tiles in this piece
-};
-
 // The same value on every lane of a converged warp, passed through a shuffle.
 // Copy coordinates and descriptors are read from uniform registers; with a
 // loop whose trip count comes from memory around it, a coordinate computed
@@ -259,27 +289,44 @@ __device__ __forceinline__ int uniform(int x)
     return __shfl_sync(0xffffffffu, x, 0);
 }
 
-// The pieces of this CTA in order; every role walks the same ones.
+// The pieces of this CTA in order.  The next sequence's list entries are
+// fetched while the current one is worked on.
 struct Walk {
     Start at;
     Seq s;
-    bool loaded;
+    int tiles, units;
+    Raw next;
+    int q_buf;
+    int at_b;  // sequence of the piece given last
 };
+__device__ __forceinline__ void enter(const PagedArgs &a, Walk &w, Raw r)
+{
+    bool bad;
+    w.s = in_range(a, r, bad);
+    w.tiles = tiles_of(a, w.s);
+    w.units = (w.tiles + 1) / 2;
+    if (w.at.b + 1 < a.B)
+        w.next = Raw{r.c1, a.cu_q[w.at.b + 2], a.kv_len[w.at.b + 1]};
+}
+__device__ __forceinline__ Walk first_walk(const PagedArgs &a, const Bars &b)
+{
+    Walk w;
+    w.at = b.start;
+    w.q_buf = 0;
+    if (w.at.left > 0)
+        enter(a, w, load_raw(a, w.at.b));
+    return w;
+}
 __device__ __forceinline__ bool next_piece(const PagedArgs &a, Walk &w, Piece &u)
 {
-    while (w.at.left > 0 && w.at.b >= 0 && w.at.b < a.B) {
-        bool bad;
-        if (!w.loaded)
-            w.s = load_seq(a, w.at.b, bad);
-        w.loaded = true;
-        const int tiles = tiles_of(a, w.s);
-        const int units = (tiles + 1) / 2;
-        if (w.at.p >= units) {  // past the head's (or an empty sequence's) last unit
+    while (w.at.left > 0) {
+        if (w.at.p >= w.units) {  // past the head's (or an empty sequence's) last unit
             w.at.p = 0;
-            if (units == 0 || ++w.at.h >= a.Hk) {
+            if (w.units == 0 || ++w.at.h >= a.Hk) {
                 w.at.h = 0;
-                ++w.at.b;
-                w.loaded = false;
+                if (++w.at.b >= a.B)
+                    return false;
+                enter(a, w, w.next);
             }
             continue;
         }
@@ -288,9 +335,9 @@ __device__ __forceinline__ bool next_piece(const PagedArgs &a, Walk &w, Piece &u
         const int F = (keys + kBN - 1) / kBN;
         const long long cost = kUnitKeys + static_cast<long long>(keys);
         const long long y0 = w.at.y, y1 = min(y0 + w.at.left, cost);
-        u.b = w.at.b;
+        const int pair = w.at.p;
+        w.at_b = w.at.b;
         u.h = w.at.h;
-        u.p = w.at.p;
         u.s = w.s;
         u.j0 = tile_at(y0, keys, w.at.snap);
         u.j1 = tile_at(y1, keys, w.at.snap);
@@ -302,10 +349,13 @@ __device__ __forceinline__ bool next_piece(const PagedArgs &a, Walk &w, Piece &u
         if (F == 0 ? y0 > 0 : u.j0 == u.j1)
             continue;
         u.slot = u.j0 > 0 ? 2 * blockIdx.x : u.j1 < F ? 2 * blockIdx.x + 1 : -1;
-        u.alt = 2 * u.p + 1 >= tiles;
+        u.alt = 2 * pair + 1 >= w.tiles;
+        u.q_buf = w.q_buf;
+        if (u.alt && F > 0)
+            w.q_buf ^= 1;
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
-            u.tile[t] = u.alt ? 2 * u.p : 2 * u.p + t;
+            u.tile[t] = u.alt ? 2 * pair : 2 * pair + t;
             const int first = u.tile[t] * a.tile_tokens;
             u.rows[t] = min(a.tile_tokens, u.s.n - first) * a.G;
             if (u.alt) {
@@ -314,28 +364,11 @@ __device__ __forceinline__ bool next_piece(const PagedArgs &a, Walk &w, Piece &u
                 const int ft = (keys_seen(a, u.s, first + a.tile_tokens) + kBN - 1) / kBN;
                 u.n[t] = max(min(u.j1, ft) - u.j0, 0);
             }
-            u.tile[t] = uniform(u.tile[t]);
-            u.rows[t] = uniform(u.rows[t]);
-            u.n[t] = uniform(u.n[t]);
         }
-        u.b = uniform(u.b);
-        u.h = uniform(u.h);
-        u.p = uniform(u.p);
-        u.s.q0 = uniform(u.s.q0);
-        u.s.n = uniform(u.s.n);
-        u.s.L = uniform(u.s.L);
-        u.j0 = uniform(u.j0);
-        u.j1 = uniform(u.j1);
+        u.quad = u.alt && F > 0 && u.rows[0] <= kQuadRows && a.q_quad_tokens > 0;
         return true;
     }
     return false;
-}
-__device__ __forceinline__ Walk first_walk(const Bars &b)
-{
-    Walk w;
-    w.at = b.start;
-    w.loaded = false;
-    return w;
 }
 
 __device__ __forceinline__ void record_failure(const PagedArgs &a, Bars &b, uint32_t role)
@@ -350,6 +383,32 @@ __device__ __forceinline__ bool warp_wait(uint64_t &bar, uint32_t parity, const 
 {
     const bool ok = mbar_wait(smem_addr(&bar), parity, kWaitLimitNs, abort);
     return __all_sync(0xffffffffu, ok);
+}
+
+// The producer's end of the pieces: waits for a free place, writes, signals.
+__device__ __forceinline__ bool publish(Bars &b, uint32_t k, const Piece &u)
+{
+    if (!warp_wait(b.piece_empty[k % kPieces], ((k / kPieces) & 1) ^ 1, &b.abort))
+        return false;
+    if ((threadIdx.x & 31) == 0)
+        b.pieces[k % kPieces] = u;
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0)
+        mbar_arrive(smem_addr(&b.piece_full[k % kPieces]));
+    return true;
+}
+// The k-th piece, read in place; false when there is none (ok) or the wait
+// failed (!ok).  Held until given back.
+__device__ __forceinline__ bool receive(Bars &b, uint32_t k, bool &ok)
+{
+    ok = ok && warp_wait(b.piece_full[k % kPieces], (k / kPieces) & 1, &b.abort);
+    return ok && b.pieces[k % kPieces].h >= 0;
+}
+__device__ __forceinline__ void give_back(Bars &b, uint32_t k)
+{
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0)
+        mbar_arrive(smem_addr(&b.piece_empty[k % kPieces]));
 }
 
 template <bool kF16> __device__ __forceinline__ uint32_t pack2(float lo, float hi)
@@ -369,7 +428,7 @@ template <bool kF16> __device__ __forceinline__ uint32_t pack2(float lo, float h
 // issued by one elected lane; the warp holds 32 table entries and the next 32.
 template <int D, bool kF16>
 __device__ void run_load(const PagedArgs &a, Bars &b, uint32_t smem_base, const CUtensorMap *mq,
-                         const CUtensorMap *mk, const CUtensorMap *mv)
+                         const CUtensorMap *mq_quad, const CUtensorMap *mk, const CUtensorMap *mv)
 {
     using C = Cfg<D, kF16>;
     const volatile int *abort = &b.abort;
@@ -378,37 +437,53 @@ __device__ void run_load(const PagedArgs &a, Bars &b, uint32_t smem_base, const 
     const int shift = a.page_shift;
     const int per_tile = shift < 7 ? kBN >> shift : 1;  // pages a key tile touches
     const int box_rows = shift < 7 ? 1 << shift : kBN;
-    const uint32_t q_bytes = C::kChunks * a.q_box_tokens * a.G * 128u;
+    const uint32_t q_row_bytes = C::kChunks * a.G * 128u;  // of a token
     uint32_t q_phase[2] = {0, 0}, pos = 0;
     int last_q[2] = {-1, -1};
     bool ok = true;
-    Walk w = first_walk(b);
+    uint32_t pieces = 0;
+    Walk w = first_walk(a, b);
     Piece u;
     while (ok && next_piece(a, w, u)) {
+        ok = publish(b, pieces++, u);
+        if (!ok)
+            break;
+        // Copy coordinates, afresh (see uniform).
+        const int head = uniform(u.h), q0 = uniform(u.s.q0);
+        pos = uniform(pos);
+        // The first table entries are on their way while the Q buffer is waited for.
+        const int pages = (u.s.L + (1 << shift) - 1) >> shift;  // of the sequence
+        const int *row = a.page_table + static_cast<long long>(w.at_b) * a.table_stride;
+        auto entries = [&](int first) { return first + lane < pages ? row[first + lane] : 0; };
+        int held = static_cast<int>((static_cast<long long>(u.j0) * kBN) >> shift);
+        int cur = entries(held), ahead = entries(held + 32);
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
-            if (!ok || u.n[t] == 0 || (u.alt && t == 1))
+            if (!ok || (u.alt ? u.n[0] == 0 || u.q_buf != t : u.n[t] == 0))
                 continue;
             ok = warp_wait(b.q_empty[t], q_phase[t] ^ 1, abort);
             if (!ok)
                 continue;
+            const int token = uniform(q0 + u.tile[t] * a.tile_tokens);
             if (leader) {
                 const uint32_t full = smem_addr(&b.q_full[t]);
-                mbar_arrive_expect_tx(full, q_bytes);
+                const uint32_t dst = smem_base + t * C::kTileBytes;
+                mbar_arrive_expect_tx(full, q_row_bytes * (u.quad ? 4 * a.q_quad_tokens : a.q_box_tokens));
 #pragma unroll
-                for (int c = 0; c < C::kChunks; ++c)
-                    tma_load_4d(smem_base + t * C::kTileBytes + c * kChunkBytes, mq, full, 64 * c, 0,
-                                u.h, u.s.q0 + u.tile[t] * a.tile_tokens);
+                for (int c = 0; c < C::kChunks; ++c) {
+                    if (!u.quad) {
+                        tma_load_4d(dst + c * kChunkBytes, mq, full, 64 * c, 0, head, token);
+                        continue;
+                    }
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        tma_load_4d(dst + c * kChunkBytes + k * kQuadRows * 128, mq_quad, full, 64 * c, 0,
+                                    head, token);
+                }
             }
             last_q[t] = q_phase[t];
             q_phase[t] ^= 1;
         }
-        pos = uniform(pos);
-        const int pages = (u.s.L + (1 << shift) - 1) >> shift;  // of the sequence
-        const int *row = a.page_table + static_cast<long long>(u.b) * a.table_stride;
-        auto entries = [&](int first) { return first + lane < pages ? row[first + lane] : 0; };
-        int held = static_cast<int>((static_cast<long long>(u.j0) * kBN) >> shift);
-        int cur = entries(held), ahead = entries(held + 32);
         for (int j = u.j0; ok && j < u.j1; ++j) {
             const int p0 = (j * kBN) >> shift;
             if (p0 >= held + 32) {  // 32 is a multiple of per_tile
@@ -441,11 +516,15 @@ __device__ void run_load(const PagedArgs &a, Bars &b, uint32_t smem_base, const 
 #pragma unroll
                         for (int c = 0; c < C::kChunks; ++c)
                             tma_load_4d(dst + c * kChunkBytes, which == 0 ? mk : mv, full, 64 * c, slot,
-                                        u.h, page);
+                                        head, page);
                     }
                 }
             }
         }
+    }
+    if (ok) {
+        u.h = -1;
+        ok = publish(b, pieces, u);
     }
     if (!ok) {
         if (leader)
@@ -506,12 +585,13 @@ __device__ void run_convert(const PagedArgs &a, Bars &b, uint8_t *tiles, int cw)
     const int lane = threadIdx.x & 31, tid = cw * 32 + lane;
     uint32_t pos = 0;
     bool ok = true;
-    Walk w = first_walk(b);
-    Piece u;
-    while (ok && next_piece(a, w, u)) {
-        for (int j = u.j0; ok && j < u.j1; ++j, pos += 2) {
+    for (uint32_t k = 0; receive(b, k, ok); ++k) {
+        const Piece &u = b.pieces[k % kPieces];
+        const int j0 = u.j0, j1 = u.j1, L = u.s.L;
+        give_back(b, k);
+        for (int j = j0; ok && j < j1; ++j, pos += 2) {
             const uint32_t at = pos + 1, stage = at % C::kStages;
-            const int valid = u.s.L - j * kBN;
+            const int valid = L - j * kBN;
             // Every copy is waited for: a waiter that ran two rounds of the
             // ring ahead would take an older phase for its own.
             ok = warp_wait(b.kv_full[stage], (at / C::kStages) & 1, abort);
@@ -622,27 +702,32 @@ __device__ void run_mma(const PagedArgs &a, Bars &b, uint32_t smem_base, uint32_
         commit(b.s_full[t]);
     };
 
-    Walk w = first_walk(b);
-    Piece u;
-    while (ok && next_piece(a, w, u)) {
-        const int n = u.j1 - u.j0;
+    for (uint32_t k = 0; receive(b, k, ok); ++k) {
+        Piece &in = b.pieces[k % kPieces];
+        struct {
+            int j0, L, alt, q_buf, n[2];
+        } u = {uniform(in.j0), uniform(in.s.L), uniform(in.alt), uniform(in.q_buf),
+               {uniform(in.n[0]), uniform(in.n[1])}};
+        const int n = uniform(in.j1) - u.j0;
+        give_back(b, k);
         if (n == 0)
             continue;
         const uint32_t base = uniform(pos);  // K_(j0+i) at base + 2i, V_(j0+i) at base + 2i + 1
         pos = base + 2 * n;
-        auto whole = [&](int i) { return (u.j0 + i + 1) * kBN <= u.s.L; };
+        auto whole = [&](int i) { return (u.j0 + i + 1) * kBN <= u.L; };
         if (u.alt) {
-            ok = warp_wait(b.q_full[0], q_phase[0], abort);
-            q_phase[0] ^= 1;
+            const int qb = u.q_buf;
+            ok = warp_wait(b.q_full[qb], q_phase[qb], abort);
+            q_phase[qb] ^= 1;
             for (int i = 0; ok && i < min(n, 2); ++i) {
                 ok = k_wait(base + 2 * i);
                 if (!ok)
                     break;
                 tc_fence_after();
-                s_product(i, 0, base + 2 * i);
+                s_product(i, qb, base + 2 * i);
                 commit(b.kv_empty[stage_of(base + 2 * i)]);
                 if (i == n - 1)
-                    commit(b.q_empty[0]);
+                    commit(b.q_empty[qb]);
             }
             for (int i = 0; ok && i < n; ++i) {
                 const int t = i & 1;
@@ -659,10 +744,10 @@ __device__ void run_mma(const PagedArgs &a, Bars &b, uint32_t smem_base, uint32_
                 if (!ok)
                     break;
                 tc_fence_after();
-                s_product(t, 0, at_k);
+                s_product(t, qb, at_k);
                 commit(b.kv_empty[stage_of(at_k)]);
                 if (i + 2 == n - 1)
-                    commit(b.q_empty[0]);
+                    commit(b.q_empty[qb]);
             }
             continue;
         }
@@ -776,6 +861,60 @@ __device__ __forceinline__ float softmax_tile(float sl2, uint32_t t_s, bool mask
     return alpha;
 }
 
+// The same for a quad unit: keys 32 w .. 32 w + 31 of the tile for this warp's
+// copy of the rows (t_s: its lanes of S; limit: an index in the tile).
+template <class Pre>
+__device__ __forceinline__ float softmax_quarter(float sl2, uint32_t t_s, int w, bool masked, int limit,
+                                                 bool first, float m, float &m_new, float &l, Pre pre)
+{
+    uint32_t raw[32];
+    float smax;
+    tmem_ld32_max(t_s + 32 * w, raw, smax);
+    tmem_wait_ld();
+    float s[32];
+#pragma unroll
+    for (int i = 0; i < 32; ++i)
+        s[i] = __uint_as_float(raw[i]);
+    if (masked) {
+        limit -= 32 * w;
+        smax = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < 32; i += 2) {
+            s[i] = i > limit ? -INFINITY : s[i];
+            s[i + 1] = i + 1 > limit ? -INFINITY : s[i + 1];
+            smax = fmax3(smax, s[i], s[i + 1]);
+        }
+    }
+    const float cand = smax * sl2;
+    m_new = (first || cand > m + kRescaleLog2) ? fmaxf(m, cand) : m;
+    const float alpha = ex2(m - m_new);
+    pre(alpha);
+    const uint64_t sl2x2 = f2_pack(sl2, sl2), negm = f2_pack(-m_new, -m_new);
+    uint64_t sum[2] = {f2_pack(0.f, 0.f), f2_pack(0.f, 0.f)};
+    uint32_t pk[16], zero[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        float x0, x1;
+        f2_unpack(f2_fma(f2_pack(s[2 * i], s[2 * i + 1]), sl2x2, negm), x0, x1);
+        const float p0 = ex2(x0), p1 = ex2(x1);
+        pk[i] = pack2<true>(p0, p1);
+        sum[i & 1] = f2_add(sum[i & 1], f2_pack(p0, p1));
+        zero[i] = 0;
+    }
+#pragma unroll
+    for (int c = 0; c < kBN / 32; ++c) {
+        if (c == w)
+            tmem_st16(t_s + c * 16, pk);
+        else
+            tmem_st16(t_s + c * 16, zero);
+    }
+    float e0, e1, e2, e3;
+    f2_unpack(sum[0], e0, e1);
+    f2_unpack(sum[1], e2, e3);
+    l = l * alpha + ((e0 + e1) + (e2 + e3));
+    return alpha;
+}
+
 template <int D> __device__ __forceinline__ void rescale_o(uint32_t t_o, float alpha)
 {
     const uint64_t alpha2 = f2_pack(alpha, alpha);
@@ -805,15 +944,16 @@ __device__ __forceinline__ void stage_put(uint8_t *stage, int lane, int g, uint4
 {
     reinterpret_cast<uint4 *>(stage + lane * 128)[g ^ (lane & 7)] = v;
 }
-// at(row): destination of staging row `row`, or nullptr; half: 64-byte pieces.
-template <class At>
-__device__ __forceinline__ void stage_flush(const uint8_t *stage, int lane, bool half, At at)
+// `mine`: where this lane's row goes (null: nowhere); half: 64-byte pieces.
+__device__ __forceinline__ void stage_flush(const uint8_t *stage, int lane, bool half, char *mine)
 {
     __syncwarp();
     const int g = half ? lane % 4 : lane % 8, step = half ? 8 : 4;
-    for (int row = half ? lane / 4 : lane / 8; row < 32; row += step) {
+    for (int r0 = 0; r0 < 32; r0 += step) {
+        const int row = r0 + (half ? lane / 4 : lane / 8);
         const uint4 x = reinterpret_cast<const uint4 *>(stage + row * 128)[g ^ (row & 7)];
-        char *dst = at(row);
+        char *dst = reinterpret_cast<char *>(
+            __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(mine), row));
         if (dst != nullptr)
             *reinterpret_cast<uint4 *>(dst + g * 16) = x;
     }
@@ -829,29 +969,28 @@ __device__ __forceinline__ int row_token(const PagedArgs &a, int r)
 
 // Writes warp rows [r0, r0 + 32) of tile t of the piece: O = w0 O_t0 + w1
 // O_t1 (single-tile units merge two accumulators; w1 is ignored otherwise) and
-// the base-2 log-sum-exp lse2.  To o and lse, or to the piece's slot.
+// the base-2 log-sum-exp lse2.  To o and lse, or to the piece's slot.  A warp
+// with at most kFewRows rows (decode) stores them from its registers: going
+// through the staging area costs it 32 rows' steps whatever is in them.
+constexpr int kFewRows = 8;
 template <int D, bool kF16>
 __device__ __forceinline__ void write_rows(const PagedArgs &a, const Piece &u, int t, int r0,
                                            uint32_t t_o0, uint32_t t_o1, bool two, float w0, float w1,
                                            float lse2, bool some, uint8_t *stage)
 {
-    const int lane = threadIdx.x & 31, rows = u.rows[t];
-    const bool live = r0 + lane < rows;
-    const int first = u.s.q0 + u.tile[t] * a.tile_tokens;
-    const long long out0 = static_cast<long long>(first) * a.o_st[0] +
-                           static_cast<long long>(u.h) * a.G * a.o_st[1];
-    const long long slot_row = static_cast<long long>(u.slot) * a.slot_rows + (u.alt ? 0 : t * kBM) + r0;
-    auto out_row = [&](int row) -> char * {
-        const int r = r0 + row;
-        if (r >= rows)
-            return nullptr;
-        const int tok = row_token(a, r), g = r - tok * a.G;
-        return reinterpret_cast<char *>(static_cast<uint16_t *>(a.o) + out0 + tok * a.o_st[0] +
-                                        g * a.o_st[1]);
-    };
-    auto slot_at = [&](int row) -> char * {
-        return r0 + row < rows ? reinterpret_cast<char *>(a.ws_o + (slot_row + row) * D) : nullptr;
-    };
+    const int lane = threadIdx.x & 31, rows = u.rows[t] - r0;
+    const bool live = lane < rows, whole = u.slot < 0;
+    const int tok = row_token(a, r0 + lane), g = r0 + lane - tok * a.G;
+    const long long token = static_cast<long long>(u.s.q0) +
+                            u.tile[t] * a.tile_tokens + tok;
+    const int head = u.h * a.G + g;
+    const long long slot_row = static_cast<long long>(u.slot) * a.slot_rows + (u.alt ? 0 : t * kBM) + r0 +
+                               lane;
+    char *dst = nullptr;
+    if (live)
+        dst = whole ? reinterpret_cast<char *>(static_cast<uint16_t *>(a.o) + token * a.o_st[0] +
+                                               head * a.o_st[1])
+                    : reinterpret_cast<char *>(a.ws_o + slot_row * D);
     // A sum over the row of O is finite unless some element is not: |O| < 2^8
     // keys * 65504.
     float nonfinite = 0.f;
@@ -882,42 +1021,173 @@ __device__ __forceinline__ void write_rows(const PagedArgs &a, const Piece &u, i
             for (int i = 0; i < 32; ++i)
                 y[i] = 0.f;
         }
-        if (u.slot < 0) {
+        if (whole) {
+            uint4 v[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                stage_put(stage, lane, (c % 2) * 4 + i,
-                          make_uint4(pack2<kF16>(y[8 * i], y[8 * i + 1]),
-                                     pack2<kF16>(y[8 * i + 2], y[8 * i + 3]),
-                                     pack2<kF16>(y[8 * i + 4], y[8 * i + 5]),
-                                     pack2<kF16>(y[8 * i + 6], y[8 * i + 7])));
+                v[i] = make_uint4(pack2<kF16>(y[8 * i], y[8 * i + 1]),
+                                  pack2<kF16>(y[8 * i + 2], y[8 * i + 3]),
+                                  pack2<kF16>(y[8 * i + 4], y[8 * i + 5]),
+                                  pack2<kF16>(y[8 * i + 6], y[8 * i + 7]));
+            if (rows <= kFewRows) {
+                if (live) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        reinterpret_cast<uint4 *>(dst)[c * 4 + i] = v[i];
+                }
+                continue;
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                stage_put(stage, lane, (c % 2) * 4 + i, v[i]);
             if (c % 2 == 1 || c + 1 == D / 32)
-                stage_flush(stage, lane, c % 2 == 0, [&](int row) {
-                    char *dst = out_row(row);
-                    return dst == nullptr ? dst : dst + (c / 2) * 128;
-                });
+                stage_flush(stage, lane, c % 2 == 0, dst == nullptr ? dst : dst + (c / 2) * 128);
         } else {
+            uint4 v[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i)
-                stage_put(stage, lane, i,
-                          make_uint4(__float_as_uint(y[4 * i]), __float_as_uint(y[4 * i + 1]),
-                                     __float_as_uint(y[4 * i + 2]), __float_as_uint(y[4 * i + 3])));
-            stage_flush(stage, lane, false, [&](int row) {
-                char *dst = slot_at(row);
-                return dst == nullptr ? dst : dst + c * 128;
-            });
+                v[i] = make_uint4(__float_as_uint(y[4 * i]), __float_as_uint(y[4 * i + 1]),
+                                  __float_as_uint(y[4 * i + 2]), __float_as_uint(y[4 * i + 3]));
+            if (rows <= kFewRows) {
+                if (live) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        reinterpret_cast<uint4 *>(dst)[c * 8 + i] = v[i];
+                }
+                continue;
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                stage_put(stage, lane, i, v[i]);
+            stage_flush(stage, lane, false, dst == nullptr ? dst : dst + c * 128);
         }
     }
     if (!live)
         return;
-    if (u.slot < 0) {
-        const int tok = row_token(a, r0 + lane), g = r0 + lane - tok * a.G;
-        a.lse[static_cast<long long>(first + tok) * a.Hk * a.G + u.h * a.G + g] = lse2 * kLn2;
-    } else {
-        a.ws_l[slot_row + lane] = lse2;
-    }
+    if (whole)
+        a.lse[token * a.Hk * a.G + head] = lse2 * kLn2;
+    else
+        a.ws_l[slot_row] = lse2;
     if (!kF16 && !(fabsf(nonfinite) <= FLT_MAX))
         atomicCAS(a.status, 0u,
                   5u /* FATTN_ERR_RANGE */ | (kRoleEpilogue << 8) | ((blockIdx.x & 0xffffu) << 16));
+}
+
+// A step that the four warps of warpgroup 0 take together.
+__device__ __forceinline__ bool quarters_meet(Bars &b, uint32_t &phase)
+{
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0)
+        mbar_arrive(smem_addr(&b.quarters));
+    const bool ok = warp_wait(b.quarters, phase, &b.abort);
+    phase ^= 1;
+    return ok;
+}
+
+// Epilogue of a quad unit: each warp has (m, l) and O (w0 O_0 + w1 O_1) of its
+// keys for all rows, lane = row; the four are brought to one m, added through
+// the staging areas (4 KB a warp: whole rows of up to eight, else 32 columns at
+// a time) and written, eight columns a thread.
+template <int D, bool kF16>
+__device__ __forceinline__ bool write_quad(const PagedArgs &a, Bars &b, const Piece &u, uint8_t *stages,
+                                           uint32_t t_o0, uint32_t t_o1, bool two, float w0, float w1,
+                                           float m, float l, uint32_t &phase)
+{
+    const int lane = threadIdx.x & 31, warp = threadIdx.x / 32, rows = u.rows[0];
+    const bool whole = u.slot < 0;
+    b.other[warp * 32 + lane] = make_float2(m, l);
+    if (!quarters_meet(b, phase))
+        return false;
+    float2 ml[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+        ml[k] = b.other[k * 32 + lane];
+    const float mm = fmaxf(fmaxf(ml[0].x, ml[1].x), fmaxf(ml[2].x, ml[3].x));
+    float sum = 0.f;
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+        sum += ml[k].y * ex2(ml[k].x - mm);
+    const float f = sum > 0.f ? ex2(m - mm) / sum : 0.f;
+    w0 *= f;
+    w1 *= f;
+    const long long first = static_cast<long long>(u.s.q0) + u.tile[0] * a.tile_tokens;
+    if (warp == 0 && lane < rows) {
+        const float lse2 = sum > 0.f ? mm + log2f(sum) : -INFINITY;
+        const int tok = row_token(a, lane);
+        if (whole)
+            a.lse[(first + tok) * a.Hk * a.G + u.h * a.G + lane - tok * a.G] = lse2 * kLn2;
+        else
+            a.ws_l[static_cast<long long>(u.slot) * a.slot_rows + lane] = lse2;
+    }
+    // Blocks of columns: put, meet, add and write, meet.
+    const int width = rows <= 8 ? D : 32, each = width / 8;
+    const int q = warp * 32 + lane, my_row = q / each, my_col = (q - my_row * each) * 8;
+    uint8_t *mine = stages + warp * 4096 + lane * width * 4;
+    const uint8_t *theirs = stages + my_row * width * 4;
+#pragma unroll 1
+    for (int c0 = 0; c0 < D; c0 += width) {
+#pragma unroll 1
+        for (int c = 0; c < width; c += 16) {
+            uint32_t o0[16], o1[16];
+            tmem_ld16(t_o0 + c0 + c, o0);
+            if (two)
+                tmem_ld16(t_o1 + c0 + c, o1);
+            tmem_wait_ld();
+            if (lane >= rows)
+                continue;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                float y[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    y[k] = __uint_as_float(o0[4 * i + k]) * w0;
+                    if (two)
+                        y[k] = fmaf(__uint_as_float(o1[4 * i + k]), w1, y[k]);
+                }
+                *reinterpret_cast<float4 *>(mine + (((c / 4 + i) ^ (lane & 7)) << 4)) =
+                    make_float4(y[0], y[1], y[2], y[3]);
+            }
+        }
+        if (!quarters_meet(b, phase))
+            return false;
+        if (my_row < rows) {
+            float y[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                y[i] = 0.f;
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const float4 x = *reinterpret_cast<const float4 *>(
+                        theirs + k * 4096 + (((my_col / 4 + h) ^ (my_row & 7)) << 4));
+                    y[4 * h] += x.x;
+                    y[4 * h + 1] += x.y;
+                    y[4 * h + 2] += x.z;
+                    y[4 * h + 3] += x.w;
+                }
+            // Finite unless one of them is not.
+            if (!kF16 && !(fabsf(((y[0] + y[1]) + (y[2] + y[3])) + ((y[4] + y[5]) + (y[6] + y[7]))) <= FLT_MAX))
+                atomicCAS(a.status, 0u,
+                          5u /* FATTN_ERR_RANGE */ | (kRoleEpilogue << 8) | ((blockIdx.x & 0xffffu) << 16));
+            if (whole) {
+                const int tok = row_token(a, my_row);
+                uint16_t *dst = static_cast<uint16_t *>(a.o) + (first + tok) * a.o_st[0] +
+                                (static_cast<long long>(u.h) * a.G + my_row - tok * a.G) * a.o_st[1] + c0 +
+                                my_col;
+                *reinterpret_cast<uint4 *>(dst) =
+                    make_uint4(pack2<kF16>(y[0], y[1]), pack2<kF16>(y[2], y[3]), pack2<kF16>(y[4], y[5]),
+                               pack2<kF16>(y[6], y[7]));
+            } else {
+                float *dst = a.ws_o + (static_cast<long long>(u.slot) * a.slot_rows + my_row) * D + c0 + my_col;
+                reinterpret_cast<float4 *>(dst)[0] = make_float4(y[0], y[1], y[2], y[3]);
+                reinterpret_cast<float4 *>(dst)[1] = make_float4(y[4], y[5], y[6], y[7]);
+            }
+        }
+        if (!quarters_meet(b, phase))
+            return false;
+    }
+    return true;
 }
 
 template <int D, bool kF16>
@@ -931,61 +1201,85 @@ __device__ void run_softmax(const PagedArgs &a, Bars &b, uint8_t *smem, uint32_t
     const uint32_t t_s = tmem + lane_off + (t == 0 ? 0u : 128u);
     const uint32_t t_o0 = tmem + lane_off + C::kColO0, t_o1 = tmem + lane_off + C::kColO1;
     const uint32_t t_o = t == 0 ? t_o0 : t_o1;
-    uint8_t *stage = smem + C::kStageOffset + (t * 4 + warp) * 4096;
-    uint32_t s_phase = 0, of_phase = 0, other_phase = 0;
-    const int tok = row_token(a, r);
+    uint8_t *stages = smem + C::kStageOffset + t * 4 * 4096;
+    uint32_t s_phase = 0, of_phase = 0, other_phase = 0, quarter_phase = 0;
     bool ok = true;
-    Walk w = first_walk(b);
-    Piece u;
-    while (ok && next_piece(a, w, u)) {
-        if (u.rows[t] <= 0)
-            continue;
+    for (uint32_t k = 0; receive(b, k, ok); ++k) {
+        // Read in place where it is needed: the inner loops have no registers
+        // to hold it.
+        const Piece &u = b.pieces[k % kPieces];
         const int nt = u.n[t];
+        const bool alt = u.alt, quad = u.quad;
         // Rows of this warp that exist (a warp without any only keeps step).
-        const bool busy = warp * 32 < u.rows[t];
+        const bool busy = quad || warp * 32 < u.rows[t];
         float m = -FLT_MAX, l = 0.f;
-        const int step = u.alt ? 2 : 1;
-        const int first_tok = u.s.L - u.s.n + u.tile[t] * a.tile_tokens;  // its position
-        int j = u.j0 + (u.alt ? t : 0);
-        for (int i = 0; i < nt; ++i, j += step) {
-            ok = warp_wait(b.s_full[t], s_phase, abort);
-            s_phase ^= 1;
-            if (!ok)
-                break;
-            tc_fence_after();
-            __syncwarp();
-            bool rescale = false;
-            if (busy) {
-                // Keys this row sees in the tile: 0 .. limit.
-                const int diag = a.causal ? first_tok - j * kBN : kBN;
-                const int tail = u.s.L - 1 - j * kBN;
-                const bool masked = diag < kBN - 1 || tail < kBN - 1;
-                const int limit = min(a.causal ? diag + tok : kBN, tail);
-                const bool first = i == 0;
-                float m_new;
-                auto pre = [&](float) { rescale = !first && __any_sync(0xffffffffu, m_new != m); };
-                auto mid = [&]() {
-                    if (!rescale) {
-                        tmem_wait_st();
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0)
-                            mbar_arrive(smem_addr(&b.p_half[t]));
-                    }
-                };
-                const float alpha =
-                    softmax_tile(a.sl2, t_s, masked, limit, first, m, m_new, l, pre, mid);
-                if (rescale)
-                    rescale_o<D>(t_o, alpha);
-                m = m_new;
+        {
+            // Keys that this row sees in key tile j: its indexes 0 .. min(diag +
+            // tok, tail), diag and tail counted from the tile's first key.
+            const int step = alt ? 2 * kBN : kBN;
+            const int tok = a.causal ? row_token(a, quad ? lane : r) : 0;
+            int tail = u.s.L - 1 - (u.j0 + (alt ? t : 0)) * kBN;
+            int diag = a.causal ? tail + 1 - u.s.n + u.tile[t] * a.tile_tokens : tail;
+            bool rescale = false, first = true;
+            float m_new;
+            auto pre = [&](float) { rescale = !first && __any_sync(0xffffffffu, m_new != m); };
+            auto arrive = [&](uint64_t &bar) {
                 tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
-            }
-            if (lane == 0) {
-                if (!busy || rescale)
-                    mbar_arrive(smem_addr(&b.p_half[t]));
-                mbar_arrive(smem_addr(&b.p_full[t]));
+                if (lane == 0)
+                    mbar_arrive(smem_addr(&bar));
+            };
+            auto s_wait = [&]() {
+                ok = warp_wait(b.s_full[t], s_phase, abort);
+                s_phase ^= 1;
+                tc_fence_after();
+                __syncwarp();
+                return ok;
+            };
+            if (quad) {
+#pragma unroll 1
+                for (int i = 0; i < nt && s_wait(); ++i) {
+                    const bool masked = min(diag, tail) < kBN - 1;
+                    const float alpha = softmax_quarter(a.sl2, t_s, warp, masked, min(diag + tok, tail),
+                                                        first, m, m_new, l, pre);
+                    if (rescale)
+                        rescale_o<D>(t_o, alpha);
+                    m = m_new;
+                    first = false;
+                    diag -= step;
+                    tail -= step;
+                    arrive(b.p_half[t]);
+                    if (lane == 0)
+                        mbar_arrive(smem_addr(&b.p_full[t]));
+                }
+            } else if (busy) {
+                auto mid = [&]() {
+                    if (!rescale)
+                        arrive(b.p_half[t]);
+                };
+#pragma unroll 1
+                for (int i = 0; i < nt && s_wait(); ++i) {
+                    const bool masked = min(diag, tail) < kBN - 1;
+                    const float alpha = softmax_tile(a.sl2, t_s, masked, min(diag + tok, tail), first, m,
+                                                     m_new, l, pre, mid);
+                    if (rescale) {
+                        rescale_o<D>(t_o, alpha);
+                        arrive(b.p_half[t]);
+                    }
+                    m = m_new;
+                    first = false;
+                    diag -= step;
+                    tail -= step;
+                    arrive(b.p_full[t]);
+                }
+            } else {
+#pragma unroll 1
+                for (int i = 0; i < nt && s_wait(); ++i)
+                    if (lane == 0) {
+                        mbar_arrive(smem_addr(&b.p_half[t]));
+                        mbar_arrive(smem_addr(&b.p_full[t]));
+                    }
             }
         }
         if (!ok)
@@ -996,8 +1290,9 @@ __device__ void run_softmax(const PagedArgs &a, Bars &b, uint8_t *smem, uint32_t
             if (!ok)
                 break;
         }
-        const bool two = u.alt && u.n[1] > 0;
-        if (u.alt && t == 1) {
+        const bool two = alt && u.n[1] > 0;
+        if (alt && t == 1) {
+            give_back(b, k);
             if (nt > 0) {
                 b.other[r] = make_float2(m, l);
                 __syncwarp();
@@ -1006,7 +1301,8 @@ __device__ void run_softmax(const PagedArgs &a, Bars &b, uint8_t *smem, uint32_t
             }
             continue;
         }
-        float w0, w1 = 0.f, lse2;
+        // O = w0 O_0 + w1 O_1 of this warp's rows, times 1 / l.
+        float w0 = 1.f, w1 = 0.f;
         if (two) {
             ok = warp_wait(b.other_done, other_phase, abort);
             other_phase ^= 1;
@@ -1014,28 +1310,29 @@ __device__ void run_softmax(const PagedArgs &a, Bars &b, uint8_t *smem, uint32_t
                 break;
             const float2 ml = b.other[r];
             const float mm = fmaxf(m, ml.x);
-            const float a0 = ex2(m - mm), a1 = ex2(ml.x - mm);
-            l = l * a0 + ml.y * a1;
-            const float inv = l > 0.f ? 1.f / l : 0.f;
-            w0 = a0 * inv;
-            w1 = a1 * inv;
+            w0 = ex2(m - mm);
+            w1 = ex2(ml.x - mm);
+            l = l * w0 + ml.y * w1;
             m = mm;
-        } else {
-            w0 = l > 0.f ? 1.f / l : 0.f;
         }
-        lse2 = l > 0.f ? m + log2f(l) : -INFINITY;
         tc_fence_after();
         __syncwarp();
-        if (busy) {
+        if (quad) {
+            ok = write_quad<D, kF16>(a, b, u, stages, t_o0, t_o1, two, w0, w1, m, l, quarter_phase);
+            if (!ok)
+                break;
+        } else if (busy) {
             if (nt == 0 && u.slot >= 0) {  // no key tile of this piece: an empty partial
-                const long long row = static_cast<long long>(u.slot) * a.slot_rows + t * kBM + r;
                 if (r < u.rows[t])
-                    a.ws_l[row] = -INFINITY;
+                    a.ws_l[static_cast<long long>(u.slot) * a.slot_rows + t * kBM + r] = -INFINITY;
             } else {
-                write_rows<D, kF16>(a, u, t, warp * 32, u.alt ? t_o0 : t_o, t_o1, two, w0, w1, lse2,
-                                    nt > 0, stage);
+                const float inv = l > 0.f ? 1.f / l : 0.f;
+                const float lse2 = l > 0.f ? m + log2f(l) : -INFINITY;
+                write_rows<D, kF16>(a, u, t, warp * 32, t_o, t_o1, two, w0 * inv, w1 * inv,
+                                    lse2, nt > 0, stages + warp * 4096);
             }
         }
+        give_back(b, k);
         if (nt > 0) {
             tc_fence_before();
             __syncwarp();
@@ -1052,8 +1349,9 @@ __device__ void run_softmax(const PagedArgs &a, Bars &b, uint8_t *smem, uint32_t
 
 template <int D, bool kF16>
 __global__ void __launch_bounds__(kThreads, 1)
-    paged_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
-                 const __grid_constant__ CUtensorMap mv, const PagedArgs a)
+    paged_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mq_quad,
+                 const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv,
+                 const PagedArgs a)
 {
     using C = Cfg<D, kF16>;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -1077,7 +1375,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(smem_addr(&b.kv_empty[s]), 1);
             mbar_init(smem_addr(&b.v_ready[s]), 2);
         }
+        for (int k = 0; k < kPieces; ++k) {
+            mbar_init(smem_addr(&b.piece_full[k]), 1);
+            mbar_init(smem_addr(&b.piece_empty[k]), kThreads / 32 - 1);
+        }
         mbar_init(smem_addr(&b.other_done), 4);
+        mbar_init(smem_addr(&b.quarters), 4);
         mbar_init(smem_addr(&b.drain), 1);
         b.abort = 0;
         fence_barrier_init();
@@ -1088,6 +1391,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (warp == kWarpLoad && lane == 0) {
         prefetch_tensormap(&mq);
+        prefetch_tensormap(&mq_quad);
         prefetch_tensormap(&mk);
         prefetch_tensormap(&mv);
     }
@@ -1099,7 +1403,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp < 8)
         run_softmax<D, kF16>(a, b, smem, tmem, warp / 4);
     else if (warp == kWarpLoad)
-        run_load<D, kF16>(a, b, smem_base, &mq, &mk, &mv);
+        run_load<D, kF16>(a, b, smem_base, &mq, &mq_quad, &mk, &mv);
     else if (warp == kWarpMma)
         run_mma<D, kF16>(a, b, smem_base, tmem);
     else
@@ -1198,7 +1502,7 @@ __global__ void __launch_bounds__(128) combine_paged_kernel(const PagedArgs a, i
 }
 
 template <int D, bool kF16>
-cudaError_t launch(const PagedArgs &a, const FwdMaps &maps, int num_sms, cudaStream_t stream)
+cudaError_t launch(const PagedArgs &a, const PagedMaps &maps, int num_sms, cudaStream_t stream)
 {
     using C = Cfg<D, kF16>;
     const size_t smem = C::kBarsOffset + sizeof(Bars) + 1024;
@@ -1207,7 +1511,7 @@ cudaError_t launch(const PagedArgs &a, const FwdMaps &maps, int num_sms, cudaStr
                                          static_cast<int>(smem));
     if (e != cudaSuccess)
         return e;
-    paged_kernel<D, kF16><<<num_sms, kThreads, smem, stream>>>(maps.q, maps.k, maps.v, a);
+    paged_kernel<D, kF16><<<num_sms, kThreads, smem, stream>>>(maps.q, maps.q_quad, maps.k, maps.v, a);
     e = cudaGetLastError();
     if (e != cudaSuccess || num_sms < 2)
         return e;
@@ -1224,14 +1528,14 @@ cudaError_t launch(const PagedArgs &a, const FwdMaps &maps, int num_sms, cudaStr
 }
 
 template <int D>
-cudaError_t launch_typed(const PagedArgs &a, const FwdMaps &maps, int num_sms, cudaStream_t stream)
+cudaError_t launch_typed(const PagedArgs &a, const PagedMaps &maps, int num_sms, cudaStream_t stream)
 {
     return a.f16 ? launch<D, true>(a, maps, num_sms, stream) : launch<D, false>(a, maps, num_sms, stream);
 }
 
 }  // namespace
 
-cudaError_t launch_paged(const PagedArgs &a, const FwdMaps &maps, int num_sms, cudaStream_t stream)
+cudaError_t launch_paged(const PagedArgs &a, const PagedMaps &maps, int num_sms, cudaStream_t stream)
 {
     switch (a.d) {
     case 64: return launch_typed<64>(a, maps, num_sms, stream);
