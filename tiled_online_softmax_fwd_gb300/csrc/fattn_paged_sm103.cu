@@ -42,7 +42,7 @@
 // accumulators instead of one, merged once a unit.
 //
 // Schedule.  Lengths live in device memory (a captured graph follows them),
-// so the grid finds its own work: the units' costs, in keys plus a constant
+// so the grid finds its own work: the units' costs, so much a key plus so much
 // for a unit's start and end, have closed-form prefix sums; CTA c takes the
 // c-th of equal ranges of their total.  A range may begin or end inside a
 // unit: the unit is then split between CTAs by key tiles, each writes a
@@ -73,23 +73,48 @@ constexpr int kQuadRows = 32;  // rows of a tile that fit a lane quarter
 constexpr uint32_t kTmemCols = 512;
 constexpr uint64_t kWaitLimitNs = 2000000000ull;
 constexpr float kRescaleLog2 = 8.0f;
-constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr uint32_t kChunkBytes = kBM * 128;  // 128 rows x 64 16-bit columns
-// Cost of a unit besides its keys, in keys: its Q copy, first S and epilogue
-// take about as long as two key tiles.
-constexpr int kUnitKeys = 256;
-// A CTA's share of the work is at least this many keys: below, the merge
-// costs more than the shorter ranges save.
-constexpr int kMinShare = kUnitKeys + 2 * kBN;
+// Epilogue staging of a softmax warp: 32 rows of 128 bytes, and room for the
+// (m, l) of its rows, from the end.
+constexpr uint32_t kStageBytes = 4096 + 128;
+// Costs of a unit, in eighths of a key in a quad unit: its start and end, and
+// each key it sees.  From a fit of the CTAs' cycles over eighteen ragged
+// batches (16 to 40 sequences, up to 500 new tokens and 6000 keys): at d = 64 a
+// quad unit took 4800 cycles and 1300 a key tile, another single tile 5800 and
+// 1600, a pair of tiles 8300 and 2100; at d = 128 (bf16) 5800 and 2700, 9800 and
+// 2700, 9800 and 3600.  With one cost for all, the slowest CTA of such a batch
+// took 1.8 times the mean.
+enum UnitKind { kQuad, kSingle, kPair };
+struct Costs {
+    int unit[3], key[3];
+    // By a variable kind: selected, not indexed (the arrays stay constants).
+    __device__ __forceinline__ int unit_of(int k) const
+    {
+        return k == kQuad ? unit[kQuad] : k == kSingle ? unit[kSingle] : unit[kPair];
+    }
+    __device__ __forceinline__ int key_of(int k) const
+    {
+        return k == kQuad ? key[kQuad] : k == kSingle ? key[kSingle] : key[kPair];
+    }
+};
+template <int D> __device__ __forceinline__ constexpr Costs costs_of()
+{
+    return D == 64   ? Costs{{3750, 4530, 6550}, {8, 10, 13}}
+           : D == 96 ? Costs{{2720, 3270, 4330}, {8, 9, 11}}
+                     : Costs{{2190, 3730, 3740}, {8, 8, 11}};
+}
+// A CTA's share of the work is at least a quad unit of this many keys: below,
+// the merge costs more than the shorter ranges save.
+constexpr int kMinShareKeys = 2 * kBN;
 
 template <int D, bool kF16> struct Cfg {
     static constexpr int kChunks = (D + 63) / 64;
     static constexpr uint32_t kTileBytes = kChunks * kChunkBytes;
     static constexpr int kStages = kChunks == 2 ? 4 : 8;
     static constexpr uint32_t kStageOffset = (2 + kStages) * kTileBytes;  // epilogue staging
-    static constexpr uint32_t kBarsOffset = kStageOffset + 8 * 4096;
-    static constexpr uint32_t kColO0 = 256, kColO1 = 256 + D;
+    static constexpr uint32_t kBarsOffset = kStageOffset + 8 * kStageBytes;
+    static constexpr uint32_t kColO0 = 256;  // O of warpgroup t at kColO0 + t D
 };
 
 // Where a CTA starts: a unit, the keys-plus-overhead already behind in it,
@@ -111,6 +136,7 @@ struct Piece {
     int j0, j1;
     int slot;     // workspace slot of a partial result, or -1: the whole unit
     int alt;      // one Q tile: the warpgroups take alternate key tiles
+    int lead;     // ... beginning with this one, which writes the result
     int quad;     // ... of at most 32 rows, copied to all four lane quarters
     int q_buf;    // a single tile's Q buffer: the two in turn
     int tile[2];  // Q tile of each warpgroup
@@ -122,8 +148,8 @@ struct Bars {
     uint64_t q_full[2], q_empty[2];
     uint64_t kv_full[8], kv_empty[8], v_ready[8];
     uint64_t s_full[2], p_half[2], p_full[2], o_full[2], o_empty[2];
-    uint64_t other_done;  // single-tile units: warpgroup 1's statistics are written
-    uint64_t quarters;    // quad units: the four warps' merge steps
+    uint64_t other_done;   // single-tile units: the statistics of the one that does not lead
+    uint64_t quarters[2];  // quad units: merge steps of a warpgroup's four warps
     uint64_t piece_full[kPieces], piece_empty[kPieces];
     uint64_t drain;
     uint32_t tmem_base;
@@ -131,7 +157,6 @@ struct Bars {
     Start start;
     Piece pieces[kPieces];
     long long warp_sum[kThreads / 32];
-    float2 other[kBM];  // (m, l) of warpgroup 1's half of a single-tile unit
 };
 
 // ------------------------------------------------------------------ schedule
@@ -171,37 +196,54 @@ __device__ __forceinline__ int keys_seen(const PagedArgs &a, const Seq &s, int e
     return a.causal ? max(s.L - s.n + min(end, s.n), 0) : s.L;
 }
 
+// The kind of a (sequence, head)'s unit p.
+__device__ __forceinline__ int kind_of(const PagedArgs &a, const Seq &s, int tiles, int p)
+{
+    if (2 * p + 1 < tiles)
+        return kPair;
+    return (s.n - 2 * p * a.tile_tokens) * a.G <= kQuadRows && a.q_quad_tokens > 0 ? kQuad : kSingle;
+}
+
 // Cost of the first p of a (sequence, head)'s units.  Under the causal mask
 // unit i sees off + (i + 1) R keys (none while that is negative), off = L - n,
-// R tokens a unit; the last one sees L.
-__device__ __forceinline__ long long cost_before(const PagedArgs &a, const Seq &s, int units, int p)
+// R tokens a unit; the last one sees L, and alone may be other than a pair.
+__device__ __forceinline__ long long cost_before(const PagedArgs &a, const Costs &cost, const Seq &s,
+                                                 int tiles, int p)
 {
-    long long c = static_cast<long long>(p) * kUnitKeys;
-    if (!a.causal)
-        return c + static_cast<long long>(p) * s.L;
-    const long long off = static_cast<long long>(s.L) - s.n, R = 2 * a.tile_tokens;
-    const long long i = max(min(p, units - 1), 0);
-    const long long z = off < 0 ? min(i, -off / R) : 0;
-    c += (i - z) * off + R * ((i * (i + 1) - z * (z + 1)) / 2);
-    return p == units && units > 0 ? c + s.L : c;
+    const int units = (tiles + 1) / 2;
+    if (units == 0)
+        return 0;
+    const long long i = min(p, units - 1);
+    long long keys = i * s.L;
+    if (a.causal) {
+        const long long off = static_cast<long long>(s.L) - s.n, R = 2 * a.tile_tokens;
+        const long long z = off < 0 ? min(i, -off / R) : 0;
+        keys = (i - z) * off + R * ((i * (i + 1) - z * (z + 1)) / 2);
+    }
+    long long c = i * cost.unit[kPair] + keys * cost.key[kPair];
+    if (p == units) {
+        const int kind = kind_of(a, s, tiles, units - 1);
+        c += cost.unit_of(kind) + static_cast<long long>(s.L) * cost.key_of(kind);
+    }
+    return c;
 }
 
 // Key tile that a cost of y inside a unit of `keys` keys falls on.
-__device__ __forceinline__ int tile_at(long long y, int keys, int snap)
+__device__ __forceinline__ int tile_at(long long y, int keys, int unit_cost, int key_cost, int snap)
 {
     const int F = (keys + kBN - 1) / kBN;
     if (y <= 0)
         return 0;
-    if (y >= kUnitKeys + static_cast<long long>(keys))
+    if (y >= unit_cost + static_cast<long long>(keys) * key_cost)
         return F;
-    const int t = y < kUnitKeys ? 0 : static_cast<int>((y - kUnitKeys) / kBN);
+    const int t = y < unit_cost ? 0 : static_cast<int>((y - unit_cost) / (kBN * key_cost));
     return t < snap ? 0 : F - t < snap ? F : t;
 }
 
 // The whole block finds this CTA's start: each thread sums the costs of a run
 // of sequences, a scan gives the total and every run's place, and the thread
 // whose run holds the CTA's first cost walks it.
-__device__ void find_start(const PagedArgs &a, Bars &b)
+__device__ void find_start(const PagedArgs &a, const Costs &cost, Bars &b)
 {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid / 32;
     const int per = (a.B + kThreads - 1) / kThreads;
@@ -212,8 +254,8 @@ __device__ void find_start(const PagedArgs &a, Bars &b)
         bool bad;
         const Seq s = load_seq(a, i, bad);
         any_bad = any_bad || bad;
-        const int units = (tiles_of(a, s) + 1) / 2;
-        sum += a.Hk * cost_before(a, s, units, units);
+        const int tiles = tiles_of(a, s);
+        sum += a.Hk * cost_before(a, cost, s, tiles, (tiles + 1) / 2);
     }
     if (any_bad && blockIdx.x == 0)
         atomicCAS(a.status, 0u, 6u /* FATTN_ERR_INDEX */ | (kRoleLoad << 8));
@@ -237,15 +279,16 @@ __device__ void find_start(const PagedArgs &a, Bars &b)
         before += w < warp ? b.warp_sum[w] : 0;
         total += b.warp_sum[w];
     }
-    const long long shares = min(static_cast<long long>(gridDim.x), max(total / kMinShare, 1LL));
+    const int least = cost.unit[kQuad] + kMinShareKeys * cost.key[kQuad];
+    const long long shares = min(static_cast<long long>(gridDim.x), max(total / least, 1LL));
     const long long lo = blockIdx.x * total / shares, hi = (blockIdx.x + 1) * total / shares;
     if (blockIdx.x < shares && lo < hi && before <= lo && lo < before + sum) {
         long long x = lo - before;
         for (int i = b0; i < b1; ++i) {
             bool bad;
             const Seq s = load_seq(a, i, bad);
-            const int units = (tiles_of(a, s) + 1) / 2;
-            const long long head = cost_before(a, s, units, units);
+            const int tiles = tiles_of(a, s), units = (tiles + 1) / 2;
+            const long long head = cost_before(a, cost, s, tiles, units);
             if (x >= head * a.Hk) {
                 x -= head * a.Hk;
                 continue;
@@ -257,18 +300,19 @@ __device__ void find_start(const PagedArgs &a, Bars &b)
             int p = 0, end = units;  // largest p with cost_before(p) <= x
             while (end - p > 1) {
                 const int mid = (p + end) / 2;
-                if (cost_before(a, s, units, mid) <= x)
+                if (cost_before(a, cost, s, tiles, mid) <= x)
                     p = mid;
                 else
                     end = mid;
             }
             st.p = p;
-            st.y = x - cost_before(a, s, units, p);
+            st.y = x - cost_before(a, cost, s, tiles, p);
             st.left = hi - lo;
-            st.snap = max(2, static_cast<int>(min(total / shares / (32 * kBN), 1LL << 20)));
+            st.snap = max(2, static_cast<int>(min(total / shares / (32 * kBN * cost.key[kQuad]), 1LL << 20)));
             b.start = st;
             const int keys = keys_seen(a, s, (p + 1) * 2 * a.tile_tokens);
-            const int t = tile_at(st.y, keys, st.snap);
+            const int kind = kind_of(a, s, tiles, p);
+            const int t = tile_at(st.y, keys, cost.unit_of(kind), cost.key_of(kind), st.snap);
             const bool split = t > 0 && t < (keys + kBN - 1) / kBN;
             a.starts[blockIdx.x] = make_int4(st.b, st.h, st.p, split ? t : 0);
             break;
@@ -296,8 +340,10 @@ struct Walk {
     Seq s;
     int tiles, units;
     Raw next;
-    int q_buf;
-    int at_b;  // sequence of the piece given last
+    int q_buf, lead;
+    int at_b;    // sequence of the piece given last
+    int again;       // heads that follow it with the same piece of their own
+    long long cost;  // of that unit
 };
 __device__ __forceinline__ void enter(const PagedArgs &a, Walk &w, Raw r)
 {
@@ -312,13 +358,33 @@ __device__ __forceinline__ Walk first_walk(const PagedArgs &a, const Bars &b)
 {
     Walk w;
     w.at = b.start;
-    w.q_buf = 0;
+    w.q_buf = w.lead = w.again = 0;
     if (w.at.left > 0)
         enter(a, w, load_raw(a, w.at.b));
     return w;
 }
-__device__ __forceinline__ bool next_piece(const PagedArgs &a, Walk &w, Piece &u)
+// What changes from one single-tile piece to the next.
+__device__ __forceinline__ void take_turn(Walk &w, Piece &u)
 {
+    const int n = u.j1 - u.j0;
+    u.q_buf = w.q_buf;
+    u.lead = w.lead;
+    u.n[0] = (n + (w.lead == 0 ? 1 : 0)) / 2;
+    u.n[1] = n - u.n[0];
+    w.q_buf ^= 1;
+    w.lead ^= n & 1;
+}
+__device__ __forceinline__ bool next_piece(const PagedArgs &a, const Costs &costs, Walk &w, Piece &u)
+{
+    if (w.again > 0) {  // the next head of the same sequence: all else is the same
+        --w.again;
+        ++w.at.h;
+        w.at.left -= w.cost;
+        u.h = w.at.h;
+        if (u.alt)
+            take_turn(w, u);
+        return true;
+    }
     while (w.at.left > 0) {
         if (w.at.p >= w.units) {  // past the head's (or an empty sequence's) last unit
             w.at.p = 0;
@@ -333,14 +399,15 @@ __device__ __forceinline__ bool next_piece(const PagedArgs &a, Walk &w, Piece &u
         const int R = 2 * a.tile_tokens;
         const int keys = keys_seen(a, w.s, (w.at.p + 1) * R);
         const int F = (keys + kBN - 1) / kBN;
-        const long long cost = kUnitKeys + static_cast<long long>(keys);
+        const int kind = kind_of(a, w.s, w.tiles, w.at.p);
+        const long long cost = costs.unit_of(kind) + static_cast<long long>(keys) * costs.key_of(kind);
         const long long y0 = w.at.y, y1 = min(y0 + w.at.left, cost);
         const int pair = w.at.p;
         w.at_b = w.at.b;
         u.h = w.at.h;
         u.s = w.s;
-        u.j0 = tile_at(y0, keys, w.at.snap);
-        u.j1 = tile_at(y1, keys, w.at.snap);
+        u.j0 = tile_at(y0, keys, costs.unit_of(kind), costs.key_of(kind), w.at.snap);
+        u.j1 = tile_at(y1, keys, costs.unit_of(kind), costs.key_of(kind), w.at.snap);
         w.at.left -= y1 - y0;
         w.at.y = 0;
         ++w.at.p;
@@ -348,24 +415,29 @@ __device__ __forceinline__ bool next_piece(const PagedArgs &a, Walk &w, Piece &u
         // to the CTA that holds its start).
         if (F == 0 ? y0 > 0 : u.j0 == u.j1)
             continue;
-        u.slot = u.j0 > 0 ? 2 * blockIdx.x : u.j1 < F ? 2 * blockIdx.x + 1 : -1;
-        u.alt = 2 * pair + 1 >= w.tiles;
-        u.q_buf = w.q_buf;
-        if (u.alt && F > 0)
-            w.q_buf ^= 1;
+        const int cta = static_cast<int>(blockIdx.x);
+        u.slot = u.j0 > 0 ? 2 * cta : u.j1 < F ? 2 * cta + 1 : -1;
+        u.alt = kind != kPair;
+        u.lead = u.q_buf = u.n[0] = u.n[1] = 0;
+        u.tile[0] = 2 * pair;
+        u.tile[1] = u.alt ? 2 * pair : 2 * pair + 1;
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
-            u.tile[t] = u.alt ? 2 * pair : 2 * pair + t;
             const int first = u.tile[t] * a.tile_tokens;
             u.rows[t] = min(a.tile_tokens, u.s.n - first) * a.G;
-            if (u.alt) {
-                u.n[t] = (u.j1 - u.j0 + 1 - t) / 2;
-            } else {
+            if (!u.alt) {
                 const int ft = (keys_seen(a, u.s, first + a.tile_tokens) + kBN - 1) / kBN;
                 u.n[t] = max(min(u.j1, ft) - u.j0, 0);
             }
         }
-        u.quad = u.alt && F > 0 && u.rows[0] <= kQuadRows && a.q_quad_tokens > 0;
+        if (u.alt && F > 0)
+            take_turn(w, u);
+        // One unit a head, given whole: the heads after it that fit into this
+        // CTA's share whole get the same piece.
+        w.cost = cost;
+        if (w.units == 1 && u.slot < 0 && F > 0)
+            w.again = static_cast<int>(min(w.at.left / cost, static_cast<long long>(a.Hk - 1 - u.h)));
+        u.quad = kind == kQuad && F > 0;
         return true;
     }
     return false;
@@ -442,9 +514,11 @@ __device__ void run_load(const PagedArgs &a, Bars &b, uint32_t smem_base, const 
     int last_q[2] = {-1, -1};
     bool ok = true;
     uint32_t pieces = 0;
+    // The first table entries of the last piece: the next head's are the same.
+    int held_b = -1, held_page = -1, held_cur = 0, held_ahead = 0;
     Walk w = first_walk(a, b);
     Piece u;
-    while (ok && next_piece(a, w, u)) {
+    while (ok && next_piece(a, costs_of<D>(), w, u)) {
         ok = publish(b, pieces++, u);
         if (!ok)
             break;
@@ -455,11 +529,17 @@ __device__ void run_load(const PagedArgs &a, Bars &b, uint32_t smem_base, const 
         const int pages = (u.s.L + (1 << shift) - 1) >> shift;  // of the sequence
         const int *row = a.page_table + static_cast<long long>(w.at_b) * a.table_stride;
         auto entries = [&](int first) { return first + lane < pages ? row[first + lane] : 0; };
-        int held = static_cast<int>((static_cast<long long>(u.j0) * kBN) >> shift);
-        int cur = entries(held), ahead = entries(held + 32);
+        const int first_page = static_cast<int>((static_cast<long long>(u.j0) * kBN) >> shift);
+        if (w.at_b != held_b || first_page != held_page) {
+            held_b = w.at_b;
+            held_page = first_page;
+            held_cur = entries(first_page);
+            held_ahead = entries(first_page + 32);
+        }
+        int held = first_page, cur = held_cur, ahead = held_ahead;
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
-            if (!ok || (u.alt ? u.n[0] == 0 || u.q_buf != t : u.n[t] == 0))
+            if (!ok || (u.alt ? u.j0 == u.j1 || u.q_buf != t : u.n[t] == 0))
                 continue;
             ok = warp_wait(b.q_empty[t], q_phase[t] ^ 1, abort);
             if (!ok)
@@ -500,6 +580,10 @@ __device__ void run_load(const PagedArgs &a, Bars &b, uint32_t smem_base, const 
                 atomicCAS(a.status, 0u,
                           6u /* FATTN_ERR_INDEX */ | (kRoleLoad << 8) | ((blockIdx.x & 0xffffu) << 16));
             const int slot = shift < 7 ? 0 : (j * kBN) & ((1 << shift) - 1);
+            int page[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                page[i] = __shfl_sync(0xffffffffu, entry, min(p0 - held + i, 31));
 #pragma unroll
             for (int which = 0; which < 2; ++which, ++pos) {
                 const uint32_t stage = pos % C::kStages;
@@ -507,16 +591,17 @@ __device__ void run_load(const PagedArgs &a, Bars &b, uint32_t smem_base, const 
                 if (!ok)
                     break;
                 const uint32_t full = smem_addr(&b.kv_full[stage]);
-                uint32_t dst = smem_base + (2 + stage) * C::kTileBytes;
-                if (leader)
+                const uint32_t dst = smem_base + (2 + stage) * C::kTileBytes;
+                if (leader) {
                     mbar_arrive_expect_tx(full, count * box_rows * 128u * C::kChunks);
-                for (int i = 0; i < count; ++i, dst += box_rows * 128) {
-                    const int page = __shfl_sync(0xffffffffu, entry, p0 - held + i);
-                    if (leader) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        if (i >= count)
+                            break;
 #pragma unroll
                         for (int c = 0; c < C::kChunks; ++c)
-                            tma_load_4d(dst + c * kChunkBytes, which == 0 ? mk : mv, full, 64 * c, slot,
-                                        head, page);
+                            tma_load_4d(dst + c * kChunkBytes + i * box_rows * 128, which == 0 ? mk : mv, full,
+                                        64 * c, slot, head, page[i]);
                     }
                 }
             }
@@ -651,9 +736,12 @@ __device__ void run_mma(const PagedArgs &a, Bars &b, uint32_t smem_base, uint32_
     using C = Cfg<D, kF16>;
     const volatile int *abort = &b.abort;
     const bool leader = elect_one();
-    uint32_t q_phase[2] = {0, 0}, p_phase[2] = {0, 0}, oe_phase[2] = {0, 0}, vr_bits = 0;
+    // Phases, a bit each (an array indexed by a variable would live in memory):
+    // Q buffers, P halves and O by warpgroup, V by stage.
+    uint32_t q_bits = 0, p_bits = 0, ph_bits = 0, oe_bits = 0, vr_bits = 0;
     uint32_t pos = 0;
     bool ok = true;
+    auto bit = [](uint32_t bits, int i) { return (bits >> i) & 1u; };
     auto stage_of = [&](uint32_t at) { return at % C::kStages; };
     auto kv_smem = [&](uint32_t at) { return smem_base + (2 + stage_of(at)) * C::kTileBytes; };
     auto k_wait = [&](uint32_t at) {
@@ -663,124 +751,181 @@ __device__ void run_mma(const PagedArgs &a, Bars &b, uint32_t smem_base, uint32_
         if (kF16 && whole)
             return k_wait(at);
         const uint32_t st = stage_of(at);
-        const bool r = warp_wait(b.v_ready[st], (vr_bits >> st) & 1u, abort);
+        const bool r = warp_wait(b.v_ready[st], bit(vr_bits, st), abort);
         vr_bits ^= 1u << st;
+        return r;
+    };
+    auto q_wait = [&](int buf) {
+        const bool r = warp_wait(b.q_full[buf], bit(q_bits, buf), abort);
+        q_bits ^= 1u << buf;
         return r;
     };
     auto commit = [&](uint64_t &bar) {
         if (leader)
             mma_commit(smem_addr(&bar));
     };
-    // P V of one key tile into warpgroup t's accumulator, the keys in two
-    // halves: the first as soon as its P is written.
-    auto pv = [&](int t, uint32_t at_v, bool first) {
-        const uint32_t col_s = tmem + (t == 0 ? 0u : 128u);
-        const uint32_t col_o = tmem + (t == 0 ? C::kColO0 : C::kColO1);
-        bool r = warp_wait(b.p_half[t], p_phase[t], abort);
-        if (r && first) {  // overwrites O: the last unit's has to be read
-            r = warp_wait(b.o_empty[t], oe_phase[t] ^ 1, abort);
-            oe_phase[t] ^= 1;
+    // P V of one key tile into warpgroup t's accumulator; where a warp writes
+    // a whole row of P, the keys in two halves: the first as soon as it is written.
+    auto pv = [&](int t, uint32_t at_v, bool first, bool halves) {
+        const uint32_t col_s = tmem + t * 128, col_o = tmem + C::kColO0 + t * D;
+        const uint32_t v = kv_smem(at_v);
+        if (first) {  // overwrites O: the last unit's has to be read
+            if (!warp_wait(b.o_empty[t], bit(oe_bits, t) ^ 1, abort))
+                return false;
+            oe_bits ^= 1u << t;
         }
-        if (!r)
+        if (halves) {
+            if (!warp_wait(b.p_half[t], bit(ph_bits, t), abort))
+                return false;
+            ph_bits ^= 1u << t;
+            tc_fence_after();
+            if (leader)
+                issue_pv<D, 0, kBN / 32>(col_o, col_s, v, !first);
+        }
+        if (!warp_wait(b.p_full[t], bit(p_bits, t), abort))
             return false;
+        p_bits ^= 1u << t;
         tc_fence_after();
-        if (leader)
-            issue_pv<D, 0, kBN / 32>(col_o, col_s, kv_smem(at_v), !first);
-        r = warp_wait(b.p_full[t], p_phase[t], abort);
-        p_phase[t] ^= 1;
-        if (!r)
-            return false;
-        tc_fence_after();
-        if (leader)
-            issue_pv<D, kBN / 32, kBN / 16>(col_o, col_s, kv_smem(at_v), true);
+        if (leader) {
+            if (!halves)
+                issue_pv<D, 0, kBN / 32>(col_o, col_s, v, !first);
+            issue_pv<D, kBN / 32, kBN / 16>(col_o, col_s, v, true);
+        }
         return true;
     };
     auto s_product = [&](int t, int q_tile, uint32_t at_k) {
         if (leader)
-            issue_s<D, kF16>(tmem + (t == 0 ? 0u : 128u), smem_base + q_tile * C::kTileBytes,
-                             kv_smem(at_k));
+            issue_s<D, kF16>(tmem + t * 128, smem_base + q_tile * C::kTileBytes, kv_smem(at_k));
         commit(b.s_full[t]);
     };
 
-    for (uint32_t k = 0; receive(b, k, ok); ++k) {
-        Piece &in = b.pieces[k % kPieces];
-        struct {
-            int j0, L, alt, q_buf, n[2];
-        } u = {uniform(in.j0), uniform(in.s.L), uniform(in.alt), uniform(in.q_buf),
-               {uniform(in.n[0]), uniform(in.n[1])}};
-        const int n = uniform(in.j1) - u.j0;
-        give_back(b, k);
-        if (n == 0)
+    struct Unit {
+        int n, alt, quad, q_buf;
+        int whole;  // leading key tiles that lie in the sequence whole
+        int nt[2];
+    };
+    auto read = [&](uint32_t k) {
+        const Piece &u = b.pieces[k % kPieces];
+        Unit x;
+        x.n = uniform(u.j1 - u.j0);
+        x.whole = uniform(u.s.L / kBN - u.j0);
+        x.alt = uniform(u.alt);
+        x.quad = uniform(u.quad);
+        x.q_buf = uniform(u.q_buf);
+        x.nt[0] = uniform(u.n[0]);
+        x.nt[1] = uniform(u.n[1]);
+        return x;
+    };
+    uint32_t turn = 0;  // key tiles of single-tile units so far: tile g is warpgroup g % 2's
+    uint32_t k = 0;
+    while (receive(b, k, ok)) {
+        Unit u = read(k);
+        if (u.n == 0) {
+            give_back(b, k++);
             continue;
-        const uint32_t base = uniform(pos);  // K_(j0+i) at base + 2i, V_(j0+i) at base + 2i + 1
-        pos = base + 2 * n;
-        auto whole = [&](int i) { return (u.j0 + i + 1) * kBN <= u.L; };
+        }
         if (u.alt) {
-            const int qb = u.q_buf;
-            ok = warp_wait(b.q_full[qb], q_phase[qb], abort);
-            q_phase[qb] ^= 1;
-            for (int i = 0; ok && i < min(n, 2); ++i) {
-                ok = k_wait(base + 2 * i);
-                if (!ok)
-                    break;
-                tc_fence_after();
-                s_product(i, qb, base + 2 * i);
-                commit(b.kv_empty[stage_of(base + 2 * i)]);
-                if (i == n - 1)
-                    commit(b.q_empty[qb]);
-            }
-            for (int i = 0; ok && i < n; ++i) {
-                const int t = i & 1;
-                const uint32_t at_v = base + 2 * i + 1, at_k = base + 2 * (i + 2);
-                ok = v_wait(at_v, whole(i)) && pv(t, at_v, i < 2);
-                if (!ok)
-                    break;
-                commit(b.kv_empty[stage_of(at_v)]);
-                if (i + 2 >= n) {
-                    commit(b.o_full[t]);
-                    continue;
+            // A run of single-tile units as one stream of key tiles: S goes up to
+            // two tiles ahead of P V, across the units' ends.  The run's piece
+            // at ks is where S is, the one at k where P V is.
+            uint32_t ks = k, pos_s = pos, turn_s = turn;
+            Unit us = u;
+            int is = 0;
+            bool open = true;  // S has not come to the run's end
+            auto next_s = [&]() {
+                // Tile g + 2 overwrites tile g's S and P.
+                if (!open || turn_s - turn >= 2)
+                    return;
+                while (is == us.n) {
+                    // The next piece, while the pieces held leave the producer a
+                    // place to publish it in.
+                    if (ks + 1 - k >= kPieces - 1)
+                        return;
+                    open = receive(b, ks + 1, ok);
+                    if (!open)
+                        return;
+                    us = read(++ks);
+                    is = 0;
+                    open = us.alt;
+                    if (!open)
+                        return;
                 }
-                ok = k_wait(at_k);
+                if (is == 0) {
+                    ok = q_wait(us.q_buf);
+                    pos_s = uniform(pos_s);
+                }
+                ok = ok && k_wait(pos_s);
+                if (!ok)
+                    return;
+                tc_fence_after();
+                s_product(turn_s & 1, us.q_buf, pos_s);
+                commit(b.kv_empty[stage_of(pos_s)]);
+                if (++is == us.n)
+                    commit(b.q_empty[us.q_buf]);
+                pos_s += 2;
+                ++turn_s;
+            };
+            next_s();
+            for (;;) {  // the run's units
+                pos = uniform(pos);
+                for (int i = 0; ok && i < u.n; ++i) {
+                    next_s();
+                    const int t = turn & 1;
+                    const uint32_t at_v = pos + 1;
+                    ok = ok && v_wait(at_v, i < u.whole) && pv(t, at_v, i < 2, !u.quad);
+                    if (!ok)
+                        break;
+                    commit(b.kv_empty[stage_of(at_v)]);
+                    if (i + 2 >= u.n)
+                        commit(b.o_full[t]);
+                    pos = at_v + 1;
+                    ++turn;
+                    next_s();
+                }
                 if (!ok)
                     break;
-                tc_fence_after();
-                s_product(t, qb, at_k);
-                commit(b.kv_empty[stage_of(at_k)]);
-                if (i + 2 == n - 1)
-                    commit(b.q_empty[qb]);
+                give_back(b, k++);
+                if (ks < k)
+                    next_s();
+                if (!ok || ks < k || (ks == k && !us.alt))
+                    break;  // no more work, or a unit of two tiles
+                u = ks == k ? us : read(k);
             }
             continue;
         }
+        give_back(b, k++);
+        const int n = u.n;
+        const uint32_t base = uniform(pos);  // K_(j0+i) at base + 2i, V_(j0+i) at base + 2i + 1
+        pos = base + 2 * n;
         for (int t = 0; t < 2 && ok; ++t)
-            if (u.n[t] > 0) {
-                ok = warp_wait(b.q_full[t], q_phase[t], abort);
-                q_phase[t] ^= 1;
+            if (u.nt[t] > 0) {
+                ok = q_wait(t);
             }
         ok = ok && k_wait(base);
         if (!ok)
             break;
         tc_fence_after();
         for (int t = 0; t < 2; ++t) {
-            if (u.n[t] == 0)
+            if (u.nt[t] == 0)
                 continue;
             s_product(t, t, base);
-            if (u.n[t] == 1)
+            if (u.nt[t] == 1)
                 commit(b.q_empty[t]);
         }
         commit(b.kv_empty[stage_of(base)]);
         for (int i = 0; i < n && ok; ++i) {
             const uint32_t at_v = base + 2 * i + 1, at_k = base + 2 * (i + 1);
             const bool more = i + 1 < n;
-            ok = v_wait(at_v, whole(i)) && (!more || k_wait(at_k));
+            ok = v_wait(at_v, i < u.whole) && (!more || k_wait(at_k));
             for (int t = 0; t < 2 && ok; ++t) {
-                if (i >= u.n[t])
+                if (i >= u.nt[t])
                     continue;
-                ok = pv(t, at_v, i == 0);
+                ok = pv(t, at_v, i == 0, true);
                 if (!ok)
                     break;
-                if (i + 1 < u.n[t]) {
+                if (i + 1 < u.nt[t]) {
                     s_product(t, t, at_k);
-                    if (i + 2 == u.n[t])
+                    if (i + 2 == u.nt[t])
                         commit(b.q_empty[t]);
                 } else {
                     commit(b.o_full[t]);
@@ -970,8 +1115,10 @@ __device__ __forceinline__ int row_token(const PagedArgs &a, int r)
 // Writes warp rows [r0, r0 + 32) of tile t of the piece: O = w0 O_t0 + w1
 // O_t1 (single-tile units merge two accumulators; w1 is ignored otherwise) and
 // the base-2 log-sum-exp lse2.  To o and lse, or to the piece's slot.  A warp
-// with at most kFewRows rows (decode) stores them from its registers: going
-// through the staging area costs it 32 rows' steps whatever is in them.
+// with at most kFewRows rows stores them from its registers: going through the
+// staging area costs it 32 rows' steps whatever is in them.  So does one
+// without keys (!some): nothing orders it behind the other warpgroup's reading
+// of this one's (m, l).
 constexpr int kFewRows = 8;
 template <int D, bool kF16>
 __device__ __forceinline__ void write_rows(const PagedArgs &a, const Piece &u, int t, int r0,
@@ -1029,7 +1176,7 @@ __device__ __forceinline__ void write_rows(const PagedArgs &a, const Piece &u, i
                                   pack2<kF16>(y[8 * i + 2], y[8 * i + 3]),
                                   pack2<kF16>(y[8 * i + 4], y[8 * i + 5]),
                                   pack2<kF16>(y[8 * i + 6], y[8 * i + 7]));
-            if (rows <= kFewRows) {
+            if (rows <= kFewRows || !some) {
                 if (live) {
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
@@ -1073,35 +1220,43 @@ __device__ __forceinline__ void write_rows(const PagedArgs &a, const Piece &u, i
                   5u /* FATTN_ERR_RANGE */ | (kRoleEpilogue << 8) | ((blockIdx.x & 0xffffu) << 16));
 }
 
-// A step that the four warps of warpgroup 0 take together.
-__device__ __forceinline__ bool quarters_meet(Bars &b, uint32_t &phase)
+// A step that the four warps of warpgroup t take together.
+__device__ __forceinline__ bool quarters_meet(Bars &b, int t, uint32_t &phase)
 {
     __syncwarp();
     if ((threadIdx.x & 31) == 0)
-        mbar_arrive(smem_addr(&b.quarters));
-    const bool ok = warp_wait(b.quarters, phase, &b.abort);
+        mbar_arrive(smem_addr(&b.quarters[t]));
+    const bool ok = warp_wait(b.quarters[t], phase, &b.abort);
     phase ^= 1;
     return ok;
 }
 
+// (m, l) of row `lane` of a softmax warp, at the end of its staging area:
+// written for the warpgroup that leads a unit, or for the other quarters.
+__device__ __forceinline__ float2 *stats_of(uint8_t *stage, int lane)
+{
+    return reinterpret_cast<float2 *>(stage + kStageBytes) - (lane + 1);
+}
+
 // Epilogue of a quad unit: each warp has (m, l) and O (w0 O_0 + w1 O_1) of its
 // keys for all rows, lane = row; the four are brought to one m, added through
-// the staging areas (4 KB a warp: whole rows of up to eight, else 32 columns at
-// a time) and written, eight columns a thread.
+// the staging areas (as many columns at a time as fit for the rows there are)
+// and written, eight columns a thread.
 template <int D, bool kF16>
-__device__ __forceinline__ bool write_quad(const PagedArgs &a, Bars &b, const Piece &u, uint8_t *stages,
-                                           uint32_t t_o0, uint32_t t_o1, bool two, float w0, float w1,
+__device__ __forceinline__ bool write_quad(const PagedArgs &a, Bars &b, const Piece &u, int t,
+                                           uint8_t *stages, uint32_t t_o0, uint32_t t_o1, bool two, float w0, float w1,
                                            float m, float l, uint32_t &phase)
 {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x / 32, rows = u.rows[0];
+    const int lane = threadIdx.x & 31, warp = (threadIdx.x / 32) & 3, rows = u.rows[0];
     const bool whole = u.slot < 0;
-    b.other[warp * 32 + lane] = make_float2(m, l);
-    if (!quarters_meet(b, phase))
+    if (lane < rows)
+        *stats_of(stages + warp * kStageBytes, lane) = make_float2(m, l);
+    if (!quarters_meet(b, t, phase))
         return false;
     float2 ml[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k)
-        ml[k] = b.other[k * 32 + lane];
+        ml[k] = lane < rows ? *stats_of(stages + k * kStageBytes, lane) : make_float2(-FLT_MAX, 0.f);
     const float mm = fmaxf(fmaxf(ml[0].x, ml[1].x), fmaxf(ml[2].x, ml[3].x));
     float sum = 0.f;
 #pragma unroll
@@ -1120,9 +1275,13 @@ __device__ __forceinline__ bool write_quad(const PagedArgs &a, Bars &b, const Pi
             a.ws_l[static_cast<long long>(u.slot) * a.slot_rows + lane] = lse2;
     }
     // Blocks of columns: put, meet, add and write, meet.
-    const int width = rows <= 8 ? D : 32, each = width / 8;
+    int width = D;
+    while (static_cast<uint32_t>(rows * (width * 4 + 8)) > kStageBytes)
+        width = width > 32 ? width == 96 ? 32 : width / 2 : 16;
+    const int each = width / 8;
     const int q = warp * 32 + lane, my_row = q / each, my_col = (q - my_row * each) * 8;
-    uint8_t *mine = stages + warp * 4096 + lane * width * 4;
+    const int swz = width == 16 ? 3 : 7;  // granules of a row trade places by row
+    uint8_t *mine = stages + warp * kStageBytes + lane * width * 4;
     const uint8_t *theirs = stages + my_row * width * 4;
 #pragma unroll 1
     for (int c0 = 0; c0 < D; c0 += width) {
@@ -1144,11 +1303,11 @@ __device__ __forceinline__ bool write_quad(const PagedArgs &a, Bars &b, const Pi
                     if (two)
                         y[k] = fmaf(__uint_as_float(o1[4 * i + k]), w1, y[k]);
                 }
-                *reinterpret_cast<float4 *>(mine + (((c / 4 + i) ^ (lane & 7)) << 4)) =
+                *reinterpret_cast<float4 *>(mine + (((c / 4 + i) ^ (lane & swz)) << 4)) =
                     make_float4(y[0], y[1], y[2], y[3]);
             }
         }
-        if (!quarters_meet(b, phase))
+        if (!quarters_meet(b, t, phase))
             return false;
         if (my_row < rows) {
             float y[8];
@@ -1160,7 +1319,7 @@ __device__ __forceinline__ bool write_quad(const PagedArgs &a, Bars &b, const Pi
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     const float4 x = *reinterpret_cast<const float4 *>(
-                        theirs + k * 4096 + (((my_col / 4 + h) ^ (my_row & 7)) << 4));
+                        theirs + k * kStageBytes + (((my_col / 4 + h) ^ (my_row & swz)) << 4));
                     y[4 * h] += x.x;
                     y[4 * h + 1] += x.y;
                     y[4 * h + 2] += x.z;
@@ -1184,25 +1343,33 @@ __device__ __forceinline__ bool write_quad(const PagedArgs &a, Bars &b, const Pi
                 reinterpret_cast<float4 *>(dst)[1] = make_float4(y[4], y[5], y[6], y[7]);
             }
         }
-        if (!quarters_meet(b, phase))
+        if (!quarters_meet(b, t, phase))
             return false;
     }
     return true;
 }
 
 template <int D, bool kF16>
-__device__ void run_softmax(const PagedArgs &a, Bars &b, uint8_t *smem, uint32_t tmem, int t)
+__device__ void run_softmax(const PagedArgs &a, Bars &b, uint32_t tmem, int t)
 {
     using C = Cfg<D, kF16>;
-    const volatile int *abort = &b.abort;
     const int warp = (threadIdx.x / 32) & 3, lane = threadIdx.x & 31;
     const int r = warp * 32 + lane;
-    const uint32_t lane_off = static_cast<uint32_t>(warp * 32) << 16;
-    const uint32_t t_s = tmem + lane_off + (t == 0 ? 0u : 128u);
-    const uint32_t t_o0 = tmem + lane_off + C::kColO0, t_o1 = tmem + lane_off + C::kColO1;
-    const uint32_t t_o = t == 0 ? t_o0 : t_o1;
-    uint8_t *stages = smem + C::kStageOffset + t * 4 * 4096;
-    uint32_t s_phase = 0, of_phase = 0, other_phase = 0, quarter_phase = 0;
+    // The inner loops need all but a few registers: what follows from `b` and
+    // `tmem` (this warp's lanes of it) is formed where it is used, and the
+    // phases share a word.
+    tmem += static_cast<uint32_t>(warp * 32) << 16;
+    auto t_o = [&](int of) { return tmem + C::kColO0 + of * D; };
+    auto stages = [&](int of) {
+        return reinterpret_cast<uint8_t *>(&b) - C::kBarsOffset + C::kStageOffset + of * 4 * kStageBytes;
+    };
+    enum { kPhaseS, kPhaseO, kPhaseOther, kPhaseQuarters };
+    uint32_t phases = 0;
+    auto wait = [&](uint64_t &bar, int phase) {
+        const bool r = warp_wait(bar, (phases >> phase) & 1u, &b.abort);
+        phases ^= 1u << phase;
+        return r;
+    };
     bool ok = true;
     for (uint32_t k = 0; receive(b, k, ok); ++k) {
         // Read in place where it is needed: the inner loops have no registers
@@ -1218,7 +1385,7 @@ __device__ void run_softmax(const PagedArgs &a, Bars &b, uint8_t *smem, uint32_t
             // tok, tail), diag and tail counted from the tile's first key.
             const int step = alt ? 2 * kBN : kBN;
             const int tok = a.causal ? row_token(a, quad ? lane : r) : 0;
-            int tail = u.s.L - 1 - (u.j0 + (alt ? t : 0)) * kBN;
+            int tail = u.s.L - 1 - (u.j0 + (alt && t != u.lead ? 1 : 0)) * kBN;
             int diag = a.causal ? tail + 1 - u.s.n + u.tile[t] * a.tile_tokens : tail;
             bool rescale = false, first = true;
             float m_new;
@@ -1231,8 +1398,7 @@ __device__ void run_softmax(const PagedArgs &a, Bars &b, uint8_t *smem, uint32_t
                     mbar_arrive(smem_addr(&bar));
             };
             auto s_wait = [&]() {
-                ok = warp_wait(b.s_full[t], s_phase, abort);
-                s_phase ^= 1;
+                ok = wait(b.s_full[t], kPhaseS);
                 tc_fence_after();
                 __syncwarp();
                 return ok;
@@ -1241,17 +1407,15 @@ __device__ void run_softmax(const PagedArgs &a, Bars &b, uint8_t *smem, uint32_t
 #pragma unroll 1
                 for (int i = 0; i < nt && s_wait(); ++i) {
                     const bool masked = min(diag, tail) < kBN - 1;
-                    const float alpha = softmax_quarter(a.sl2, t_s, warp, masked, min(diag + tok, tail),
+                    const float alpha = softmax_quarter(a.sl2, tmem + t * 128, warp, masked, min(diag + tok, tail),
                                                         first, m, m_new, l, pre);
                     if (rescale)
-                        rescale_o<D>(t_o, alpha);
+                        rescale_o<D>(t_o(t), alpha);
                     m = m_new;
                     first = false;
                     diag -= step;
                     tail -= step;
-                    arrive(b.p_half[t]);
-                    if (lane == 0)
-                        mbar_arrive(smem_addr(&b.p_full[t]));
+                    arrive(b.p_full[t]);
                 }
             } else if (busy) {
                 auto mid = [&]() {
@@ -1261,10 +1425,10 @@ __device__ void run_softmax(const PagedArgs &a, Bars &b, uint8_t *smem, uint32_t
 #pragma unroll 1
                 for (int i = 0; i < nt && s_wait(); ++i) {
                     const bool masked = min(diag, tail) < kBN - 1;
-                    const float alpha = softmax_tile(a.sl2, t_s, masked, min(diag + tok, tail), first, m,
+                    const float alpha = softmax_tile(a.sl2, tmem + t * 128, masked, min(diag + tok, tail), first, m,
                                                      m_new, l, pre, mid);
                     if (rescale) {
-                        rescale_o<D>(t_o, alpha);
+                        rescale_o<D>(t_o(t), alpha);
                         arrive(b.p_half[t]);
                     }
                     m = m_new;
@@ -1285,30 +1449,29 @@ __device__ void run_softmax(const PagedArgs &a, Bars &b, uint8_t *smem, uint32_t
         if (!ok)
             break;
         if (nt > 0) {
-            ok = warp_wait(b.o_full[t], of_phase, abort);
-            of_phase ^= 1;
+            ok = wait(b.o_full[t], kPhaseO);
             if (!ok)
                 break;
         }
-        const bool two = alt && u.n[1] > 0;
-        if (alt && t == 1) {
-            give_back(b, k);
+        const bool two = alt && u.n[t ^ 1] > 0 && nt > 0;
+        if (alt && t != u.lead) {
             if (nt > 0) {
-                b.other[r] = make_float2(m, l);
+                *stats_of(stages(t) + warp * kStageBytes, lane) = make_float2(m, l);
                 __syncwarp();
                 if (lane == 0)
                     mbar_arrive(smem_addr(&b.other_done));
+                phases ^= 1u << kPhaseOther;
             }
+            give_back(b, k);
             continue;
         }
-        // O = w0 O_0 + w1 O_1 of this warp's rows, times 1 / l.
+        // O = w0 of the own accumulator + w1 of the other's, times 1 / l.
         float w0 = 1.f, w1 = 0.f;
         if (two) {
-            ok = warp_wait(b.other_done, other_phase, abort);
-            other_phase ^= 1;
+            ok = wait(b.other_done, kPhaseOther);
             if (!ok)
                 break;
-            const float2 ml = b.other[r];
+            const float2 ml = *stats_of(stages(t ^ 1) + warp * kStageBytes, lane);
             const float mm = fmaxf(m, ml.x);
             w0 = ex2(m - mm);
             w1 = ex2(ml.x - mm);
@@ -1318,7 +1481,10 @@ __device__ void run_softmax(const PagedArgs &a, Bars &b, uint8_t *smem, uint32_t
         tc_fence_after();
         __syncwarp();
         if (quad) {
-            ok = write_quad<D, kF16>(a, b, u, stages, t_o0, t_o1, two, w0, w1, m, l, quarter_phase);
+            uint32_t phase = (phases >> kPhaseQuarters) & 1u;
+            phases ^= phase << kPhaseQuarters;
+            ok = write_quad<D, kF16>(a, b, u, t, stages(t), t_o(t), t_o(t ^ 1), two, w0, w1, m, l, phase);
+            phases ^= phase << kPhaseQuarters;
             if (!ok)
                 break;
         } else if (busy) {
@@ -1328,8 +1494,8 @@ __device__ void run_softmax(const PagedArgs &a, Bars &b, uint8_t *smem, uint32_t
             } else {
                 const float inv = l > 0.f ? 1.f / l : 0.f;
                 const float lse2 = l > 0.f ? m + log2f(l) : -INFINITY;
-                write_rows<D, kF16>(a, u, t, warp * 32, t_o, t_o1, two, w0 * inv, w1 * inv,
-                                    lse2, nt > 0, stages + warp * 4096);
+                write_rows<D, kF16>(a, u, t, warp * 32, t_o(t), t_o(t ^ 1), two, w0 * inv, w1 * inv,
+                                    lse2, nt > 0, stages(t) + warp * kStageBytes);
             }
         }
         give_back(b, k);
@@ -1339,7 +1505,7 @@ __device__ void run_softmax(const PagedArgs &a, Bars &b, uint8_t *smem, uint32_t
             if (lane == 0) {
                 mbar_arrive(smem_addr(&b.o_empty[t]));
                 if (two)
-                    mbar_arrive(smem_addr(&b.o_empty[1]));
+                    mbar_arrive(smem_addr(&b.o_empty[t ^ 1]));
             }
         }
     }
@@ -1380,7 +1546,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(smem_addr(&b.piece_empty[k]), kThreads / 32 - 1);
         }
         mbar_init(smem_addr(&b.other_done), 4);
-        mbar_init(smem_addr(&b.quarters), 4);
+        mbar_init(smem_addr(&b.quarters[0]), 4);
+        mbar_init(smem_addr(&b.quarters[1]), 4);
         mbar_init(smem_addr(&b.drain), 1);
         b.abort = 0;
         fence_barrier_init();
@@ -1395,13 +1562,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         prefetch_tensormap(&mk);
         prefetch_tensormap(&mv);
     }
-    find_start(a, b);
+    find_start(a, costs_of<D>(), b);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = b.tmem_base;
     if (warp < 8)
-        run_softmax<D, kF16>(a, b, smem, tmem, warp / 4);
+        run_softmax<D, kF16>(a, b, tmem, warp / 4);
     else if (warp == kWarpLoad)
         run_load<D, kF16>(a, b, smem_base, &mq, &mq_quad, &mk, &mv);
     else if (warp == kWarpMma)
