@@ -117,13 +117,6 @@ template <int D, bool kF16> struct Cfg {
     static constexpr uint32_t kColO0 = 256;  // O of warpgroup t at kColO0 + t D
 };
 
-// Where a CTA starts: a unit, the keys-plus-overhead already behind in it,
-// and how much of the total cost this CTA takes.
-struct Start {
-    int b, h, p;
-    int snap;  // no split within this many key tiles of a unit's ends
-    long long y, left;
-};
 
 struct Seq {
     int q0, n, L;  // first token, new tokens, keys
@@ -144,6 +137,20 @@ struct Piece {
     int n[2];     // its key tiles in this piece
 };
 
+// A sequence's entries of the lists as they stand.
+struct Raw {
+    int c0, c1, L;
+};
+
+// Where a CTA starts: a unit (and its sequence's entries), the cost already
+// behind in it, and how much of the total cost this CTA takes.
+struct Start {
+    int b, h, p;
+    int snap;  // no split within this many key tiles of a unit's ends
+    Raw raw;
+    long long y, left;
+};
+
 struct Bars {
     uint64_t q_full[2], q_empty[2];
     uint64_t kv_full[8], kv_empty[8], v_ready[8];
@@ -161,11 +168,8 @@ struct Bars {
 
 // ------------------------------------------------------------------ schedule
 
-// A sequence's entries of the lists as they stand, and brought into range
-// (bad: some value was not).
-struct Raw {
-    int c0, c1, L;
-};
+// A sequence's entries of the lists, and brought into range (bad: some value
+// was not).
 __device__ __forceinline__ Raw load_raw(const PagedArgs &a, int b)
 {
     return Raw{a.cu_q[b], a.cu_q[b + 1], a.kv_len[b]};
@@ -196,6 +200,15 @@ __device__ __forceinline__ int keys_seen(const PagedArgs &a, const Seq &s, int e
     return a.causal ? max(s.L - s.n + min(end, s.n), 0) : s.L;
 }
 
+// a / b of non-negative values, in 32 bits where they fit (64-bit division is a
+// routine of some hundred instructions).
+__device__ __forceinline__ long long quotient(long long a, long long b)
+{
+    if (((a | b) >> 32) == 0)
+        return static_cast<unsigned>(a) / static_cast<unsigned>(b);
+    return a / b;
+}
+
 // The kind of a (sequence, head)'s unit p.
 __device__ __forceinline__ int kind_of(const PagedArgs &a, const Seq &s, int tiles, int p)
 {
@@ -216,8 +229,9 @@ __device__ __forceinline__ long long cost_before(const PagedArgs &a, const Costs
     const long long i = min(p, units - 1);
     long long keys = i * s.L;
     if (a.causal) {
-        const long long off = static_cast<long long>(s.L) - s.n, R = 2 * a.tile_tokens;
-        const long long z = off < 0 ? min(i, -off / R) : 0;
+        const int over = s.n - s.L, per = 2 * a.tile_tokens;  // off = -over, R
+        const long long off = -over, R = per;
+        const long long z = over > 0 ? min(i, static_cast<long long>(over / per)) : 0;
         keys = (i - z) * off + R * ((i * (i + 1) - z * (z + 1)) / 2);
     }
     long long c = i * cost.unit[kPair] + keys * cost.key[kPair];
@@ -236,7 +250,7 @@ __device__ __forceinline__ int tile_at(long long y, int keys, int unit_cost, int
         return 0;
     if (y >= unit_cost + static_cast<long long>(keys) * key_cost)
         return F;
-    const int t = y < unit_cost ? 0 : static_cast<int>((y - unit_cost) / (kBN * key_cost));
+    const int t = y < unit_cost ? 0 : static_cast<int>(quotient(y - unit_cost, kBN * key_cost));
     return t < snap ? 0 : F - t < snap ? F : t;
 }
 
@@ -250,9 +264,11 @@ __device__ void find_start(const PagedArgs &a, const Costs &cost, Bars &b)
     const int b0 = min(tid * per, a.B), b1 = min(b0 + per, a.B);
     long long sum = 0;
     bool any_bad = false;
+    Raw raw = {0, 0, 0};  // of the run's last sequence
     for (int i = b0; i < b1; ++i) {
         bool bad;
-        const Seq s = load_seq(a, i, bad);
+        raw = load_raw(a, i);
+        const Seq s = in_range(a, raw, bad);
         any_bad = any_bad || bad;
         const int tiles = tiles_of(a, s);
         sum += a.Hk * cost_before(a, cost, s, tiles, (tiles + 1) / 2);
@@ -280,13 +296,20 @@ __device__ void find_start(const PagedArgs &a, const Costs &cost, Bars &b)
         total += b.warp_sum[w];
     }
     const int least = cost.unit[kQuad] + kMinShareKeys * cost.key[kQuad];
-    const long long shares = min(static_cast<long long>(gridDim.x), max(total / least, 1LL));
-    const long long lo = blockIdx.x * total / shares, hi = (blockIdx.x + 1) * total / shares;
-    if (blockIdx.x < shares && lo < hi && before <= lo && lo < before + sum) {
+    // CTA c takes [c total / shares, (c + 1) total / shares), formed without
+    // long products.
+    const int shares = static_cast<int>(
+        min(static_cast<long long>(gridDim.x), max(quotient(total, least), 1LL)));
+    const long long each = quotient(total, shares);
+    const int rest = static_cast<int>(total - each * shares), c = blockIdx.x;
+    const long long lo = c * each + c * rest / shares, hi = (c + 1) * each + (c + 1) * rest / shares;
+    if (c < shares && lo < hi && before <= lo && lo < before + sum) {
         long long x = lo - before;
         for (int i = b0; i < b1; ++i) {
             bool bad;
-            const Seq s = load_seq(a, i, bad);
+            if (i + 1 < b1 || b1 - b0 > 1)
+                raw = load_raw(a, i);
+            const Seq s = in_range(a, raw, bad);
             const int tiles = tiles_of(a, s), units = (tiles + 1) / 2;
             const long long head = cost_before(a, cost, s, tiles, units);
             if (x >= head * a.Hk) {
@@ -295,7 +318,8 @@ __device__ void find_start(const PagedArgs &a, const Costs &cost, Bars &b)
             }
             Start st;
             st.b = i;
-            st.h = static_cast<int>(x / head);
+            st.raw = raw;
+            st.h = static_cast<int>(quotient(x, head));
             x -= st.h * head;
             int p = 0, end = units;  // largest p with cost_before(p) <= x
             while (end - p > 1) {
@@ -308,7 +332,7 @@ __device__ void find_start(const PagedArgs &a, const Costs &cost, Bars &b)
             st.p = p;
             st.y = x - cost_before(a, cost, s, tiles, p);
             st.left = hi - lo;
-            st.snap = max(2, static_cast<int>(min(total / shares / (32 * kBN * cost.key[kQuad]), 1LL << 20)));
+            st.snap = max(2, static_cast<int>(min(each / (64 * kBN * cost.key[kQuad]), 1LL << 20)));
             b.start = st;
             const int keys = keys_seen(a, s, (p + 1) * 2 * a.tile_tokens);
             const int kind = kind_of(a, s, tiles, p);
@@ -318,7 +342,7 @@ __device__ void find_start(const PagedArgs &a, const Costs &cost, Bars &b)
             break;
         }
     }
-    if (tid == 0 && (blockIdx.x >= shares || lo >= hi))
+    if (tid == 0 && (c >= shares || lo >= hi))
         a.starts[blockIdx.x] = make_int4(-1, 0, 0, 0);
 }
 
@@ -360,7 +384,7 @@ __device__ __forceinline__ Walk first_walk(const PagedArgs &a, const Bars &b)
     w.at = b.start;
     w.q_buf = w.lead = w.again = 0;
     if (w.at.left > 0)
-        enter(a, w, load_raw(a, w.at.b));
+        enter(a, w, w.at.raw);
     return w;
 }
 // What changes from one single-tile piece to the next.
@@ -436,7 +460,7 @@ __device__ __forceinline__ bool next_piece(const PagedArgs &a, const Costs &cost
         // CTA's share whole get the same piece.
         w.cost = cost;
         if (w.units == 1 && u.slot < 0 && F > 0)
-            w.again = static_cast<int>(min(w.at.left / cost, static_cast<long long>(a.Hk - 1 - u.h)));
+            w.again = static_cast<int>(min(quotient(w.at.left, cost), static_cast<long long>(a.Hk - 1 - u.h)));
         u.quad = kind == kQuad && F > 0;
         return true;
     }
@@ -1562,6 +1586,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         prefetch_tensormap(&mk);
         prefetch_tensormap(&mv);
     }
+    // Launched ahead of the work before it in the stream: nothing above touches
+    // global memory.
+    grid_dependency_wait();
     find_start(a, costs_of<D>(), b);
     tc_fence_before();
     __syncthreads();
@@ -1575,6 +1602,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         run_mma<D, kF16>(a, b, smem_base, tmem);
     else
         run_convert<D, kF16>(a, b, smem, warp - kWarpConv);
+    // Here, not at the start: merge CTAs waiting on the SMs that finish first cost
+    // the others 1 to 3 %.
     grid_launch_dependents();
     tc_fence_before();
     __syncthreads();
@@ -1598,6 +1627,7 @@ __global__ void __launch_bounds__(128) combine_paged_kernel(const PagedArgs a, i
 {
     constexpr int kCols = D / 32, kBatch = 8;
     const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
+    grid_launch_dependents();
     grid_dependency_wait();
     const int c = blockIdx.x + 1;
     const int4 mine = a.starts[c];
@@ -1678,19 +1708,22 @@ cudaError_t launch(const PagedArgs &a, const PagedMaps &maps, int num_sms, cudaS
                                          static_cast<int>(smem));
     if (e != cudaSuccess)
         return e;
-    paged_kernel<D, kF16><<<num_sms, kThreads, smem, stream>>>(maps.q, maps.q_quad, maps.k, maps.v, a);
-    e = cudaGetLastError();
-    if (e != cudaSuccess || num_sms < 2)
-        return e;
     cudaLaunchAttribute pdl[1];
     pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     pdl[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(num_sms - 1, (a.slot_rows + kCombineRows - 1) / kCombineRows);
-    cfg.blockDim = dim3(128);
+    cfg.gridDim = dim3(num_sms);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cfg.attrs = pdl;
     cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, paged_kernel<D, kF16>, maps.q, maps.q_quad, maps.k, maps.v, a);
+    if (e != cudaSuccess || num_sms < 2)
+        return e;
+    cfg.gridDim = dim3(num_sms - 1, (a.slot_rows + kCombineRows - 1) / kCombineRows);
+    cfg.blockDim = dim3(128);
+    cfg.dynamicSmemBytes = 0;
     return cudaLaunchKernelEx(&cfg, combine_paged_kernel<D, kF16>, a, num_sms);
 }
 

@@ -484,64 +484,49 @@ def row_sum(x, out=None, stream=None):
 
 # ------------------------------------------------------------------ serving
 # Norm and rotation, and the paged cache.  A decode step makes these calls once
-# a layer on a few microseconds of GPU work, so the host's share counts: each
-# tensor is checked by one expression of plain attributes, stride arrays and
-# sizes that depend on shapes alone are kept by value, and the device is
-# switched only when it has to be.
+# a layer on a few microseconds of GPU work, so the host's share counts.  All
+# that a call checks and derives from its tensors' shapes, strides, types and
+# devices is kept by those values (a plan); their memory is never looked at.
 _HALF = {torch.bfloat16: 0, torch.float16: 1}
 _Tensor, _raw_stream = torch.Tensor, torch._C._cuda_getCurrentRawStream
+_plans = {}
+_MAX_PLANS = 4096
 
 
 def _check_half(name, t, dims, dtype, dev):
     """A tensor of `dims` dimensions, type `dtype` on CUDA device `dev`, with a
     contiguous last dimension."""
-    if isinstance(t, _Tensor) and t.dim() == dims and t.dtype == dtype and t.get_device() == dev \
-            and (t.stride(-1) == 1 or t.shape[-1] == 1):
-        return
     if not isinstance(t, _Tensor):
         raise TypeError("%s must be a torch.Tensor" % name)
-    raise ValueError("%s must be a %d-dimensional %s tensor on CUDA device %d with a contiguous "
-                     "last dimension, got %s %s on %s" % (name, dims, dtype, dev, tuple(t.shape),
-                                                          t.dtype, t.device))
+    if t.dim() != dims or t.dtype != dtype or t.get_device() != dev \
+            or (t.stride(-1) != 1 and t.shape[-1] > 1):
+        raise ValueError("%s must be a %d-dimensional %s tensor on CUDA device %d with a contiguous "
+                         "last dimension, got %s %s on %s" % (name, dims, dtype, dev, tuple(t.shape),
+                                                              t.dtype, t.device))
 
 
 def _first_half(name, t, dims):
     """Type and device index of the tensor that sets them for a call."""
     if not isinstance(t, _Tensor):
         raise TypeError("%s must be a torch.Tensor" % name)
-    dtype, dev = t.dtype, t.get_device()
-    if dev < 0 or dtype not in _HALF:
-        raise ValueError("%s must be a bf16 or fp16 CUDA tensor, got %s on %s" % (name, dtype, t.device))
-    _check_half(name, t, dims, dtype, dev)
-    return dtype, dev
+    if not t.is_cuda or t.dtype not in _HALF:
+        raise ValueError("%s must be a bf16 or fp16 CUDA tensor, got %s on %s"
+                         % (name, t.dtype, t.device))
+    _check_half(name, t, dims, t.dtype, t.get_device())
+    return t.dtype, t.get_device()
 
 
 def _check_plain(name, t, dtype, shape, dev):
-    if isinstance(t, _Tensor) and t.dtype == dtype and t.shape == shape and t.get_device() == dev \
-            and t.is_contiguous():
-        return
-    raise ValueError("%s must be a contiguous %s %s tensor on CUDA device %d"
-                     % (name, dtype, list(shape), dev))
+    if not isinstance(t, _Tensor) or t.dtype != dtype or tuple(t.shape) != tuple(shape) \
+            or t.get_device() != dev or not t.is_contiguous():
+        raise ValueError("%s must be a contiguous %s %s tensor on CUDA device %d"
+                         % (name, dtype, list(shape), dev))
 
 
-@functools.lru_cache(maxsize=4096)
-def _strides(st):
-    """A stride tuple as the C array that the calls take (read only)."""
-    return (ctypes.c_longlong * len(st))(*st)
-
-
-def _outer(t):
-    return None if t is None else _strides(t.stride()[:-1])
-
-
-def _ptr(t):
-    return 0 if t is None else t.data_ptr()
-
-
-def _rope_args(rope, d, dev):
-    """(pointer, rot_dim, max_pos) of a rotation table, or none."""
+def _check_rope(rope, d, dev):
+    """(rot_dim, max_pos) of a rotation table."""
     if rope is None:
-        return 0, 0, 0
+        return 0, 0
     if not isinstance(rope, _Tensor) or rope.dtype != torch.float32 or rope.dim() != 2 \
             or not rope.is_contiguous() or rope.get_device() != dev:
         raise ValueError("rope must be a contiguous fp32 [positions, rot_dim] tensor on CUDA "
@@ -549,7 +534,28 @@ def _rope_args(rope, d, dev):
     max_pos, rot = rope.shape
     if rot % 16 or not 0 < rot <= d:
         raise ValueError("rope must have 16, 32, ... up to %d columns, got %d" % (d, rot))
-    return rope.data_ptr(), rot, max_pos
+    return rot, max_pos
+
+
+def _of(t):
+    """What a plan depends on in an optional tensor."""
+    return None if t is None else (t.shape, t.stride(), t.dtype, t.get_device())
+
+
+def _keep(key, plan):
+    if len(_plans) >= _MAX_PLANS:
+        _plans.clear()
+    _plans[key] = plan
+    return plan
+
+
+def _outer(t):
+    """Strides of the outer dimensions, as the C calls take them."""
+    return None if t is None else (ctypes.c_longlong * (t.dim() - 1))(*t.stride()[:-1])
+
+
+def _ptr(t):
+    return 0 if t is None else t.data_ptr()
 
 
 def _call(entry, dev, stream, *args):
@@ -590,9 +596,17 @@ def rope_table(positions: int, rot_dim: int, theta: float = 10000.0, device="cud
     return torch.cat([ang.cos(), ang.sin()], 1).float().to(device)
 
 
-def _norm_args(q, k, wq, wk, rope, positions):
-    """The checks shared by both passes; q or k may be None.  Returns type,
-    device, (B, Hq, Hk, N, d) and the rotation's arguments."""
+def _norm_key(q, k, wq, wk, rope, positions, interleaved):
+    try:
+        return ("norm", _of(q), _of(k), _of(wq), _of(wk), _of(rope), _of(positions),
+                bool(interleaved))
+    except AttributeError:  # not tensors: the checks say which
+        return None
+
+
+def _norm_plan(key, q, k, wq, wk, rope, positions, interleaved):
+    """The checks shared by both passes; q or k may be None.  (device, type,
+    arguments B .. max_pos, strides of q and k, arguments interleaved, dtype)."""
     if q is None and k is None:
         raise ValueError("q and k are both None")
     dtype, dev = _first_half("q", q, 4) if q is not None else _first_half("k", k, 4)
@@ -600,21 +614,22 @@ def _norm_args(q, k, wq, wk, rope, positions):
     Hk = 0
     if k is not None:
         _check_half("k", k, 4, dtype, dev)
-        Bk, Hk, Nk, dk = k.shape
-        if Bk != B or Nk != N or dk != d:
+        Hk = k.shape[1]
+        if tuple(k.shape) != (B, Hk, N, d):
             raise ValueError("q and k differ in batch, tokens or head dimension: %s %s"
                              % (tuple(q.shape), tuple(k.shape)))
     if d not in (64, 96, 128, 256):
         raise ValueError("head dimension must be 64, 96, 128 or 256, got %d" % d)
-    if wq is not None:
-        _check_plain("wq", wq, dtype, (d,), dev)
-    if wk is not None:
-        _check_plain("wk", wk, dtype, (d,), dev)
-    if (wq is not None and q is None) or (wk is not None and k is None):
-        raise ValueError("weights are given without their tensor")
+    for name, w, t in (("wq", wq, q), ("wk", wk, k)):
+        if w is not None:
+            if t is None:
+                raise ValueError("%s is given without its tensor" % name)
+            _check_plain(name, w, dtype, (d,), dev)
     if positions is not None:
         _check_plain("positions", positions, torch.int32, (B, N), dev)
-    return dtype, dev, (B, Hq, Hk, N, d), _rope_args(rope, d, dev)
+    rot, max_pos = _check_rope(rope, d, dev)
+    return _keep(key, (dev, dtype, (B, Hq, Hk, N, d, rot, max_pos), _outer(q), _outer(k),
+                       (1 if interleaved else 0, _HALF[dtype])))
 
 
 def _like(name, out, t, dtype, dev, stream):
@@ -631,6 +646,13 @@ def _like(name, out, t, dtype, dev, stream):
     return out
 
 
+def _out_strides(out, t, t_strides):
+    """Strides of an output that is t itself, laid out like it, or other."""
+    if out is None or (out is t) or out.stride() == t.stride():
+        return t_strides
+    return _outer(out)
+
+
 def qk_norm_rope(q, k, wq=None, wk=None, rope=None, positions=None, eps: float = 1e-6,
                  interleaved: bool = False, q_out=None, k_out=None, stream=None):
     """Per-head norm and position rotation of q [B, Hq, N, d] and k
@@ -641,12 +663,14 @@ def qk_norm_rope(q, k, wq=None, wk=None, rope=None, positions=None, eps: float =
     fp32 [positions, rot_dim] table of rope_table (None: no rotation),
     ``positions`` int32 [B, N] (None: 0..N-1).  ``q_out``/``k_out`` may be
     given (the inputs themselves for in place).  Returns (q_out, k_out)."""
-    dtype, dev, (B, Hq, Hk, N, d), (table, rot, max_pos) = _norm_args(q, k, wq, wk, rope, positions)
+    key = _norm_key(q, k, wq, wk, rope, positions, interleaved)
+    dev, dtype, sizes, q_st, k_st, flags = _plans.get(key) or _norm_plan(
+        key, q, k, wq, wk, rope, positions, interleaved)
     q_out = _like("q_out", q_out, q, dtype, dev, stream)
     k_out = _like("k_out", k_out, k, dtype, dev, stream)
     _call("fattn_qk_norm_rope", dev, stream, _ptr(q), _ptr(k), _ptr(q_out), _ptr(k_out), _ptr(wq),
-          _ptr(wk), table, _ptr(positions), B, Hq, Hk, N, d, rot, max_pos, _outer(q), _outer(k),
-          _outer(q_out), _outer(k_out), eps, 1 if interleaved else 0, _HALF[dtype])
+          _ptr(wk), _ptr(rope), _ptr(positions), *sizes, q_st, k_st, _out_strides(q_out, q, q_st),
+          _out_strides(k_out, k, k_st), eps, *flags)
     return q_out, k_out
 
 
@@ -656,7 +680,10 @@ def qk_norm_rope_bwd(dq_out, dk_out, q, k, wq=None, wk=None, rope=None, position
     """Gradients of qk_norm_rope for the upstream gradients dq_out, dk_out
     (libfattn fattn_qk_norm_rope_bwd).  Returns (dq, dk, dwq, dwk): dq and dk
     in the inputs' type, dwq and dwk fp32 [d] (None without weights)."""
-    dtype, dev, (B, Hq, Hk, N, d), (table, rot, max_pos) = _norm_args(q, k, wq, wk, rope, positions)
+    key = _norm_key(q, k, wq, wk, rope, positions, interleaved)
+    dev, dtype, sizes, q_st, k_st, flags = _plans.get(key) or _norm_plan(
+        key, q, k, wq, wk, rope, positions, interleaved)
+    d = sizes[4]
     for name, g, t in (("dq_out", dq_out, q), ("dk_out", dk_out, k)):
         if t is None:
             if g is not None:
@@ -672,9 +699,9 @@ def qk_norm_rope_bwd(dq_out, dk_out, q, k, wq=None, wk=None, rope=None, position
     if workspace is None and (wq is not None or wk is not None):
         workspace = _empty(qk_norm_rope_bwd_workspace_size(d, dev), torch.uint8, dev, stream)
     _call("fattn_qk_norm_rope_bwd", dev, stream, _ptr(dq_out), _ptr(dk_out), _ptr(q), _ptr(k),
-          _ptr(wq), _ptr(wk), table, _ptr(positions), _ptr(dq), _ptr(dk), _ptr(dwq), _ptr(dwk), B,
-          Hq, Hk, N, d, rot, max_pos, _outer(dq_out), _outer(dk_out), _outer(q), _outer(k),
-          _outer(dq), _outer(dk), eps, 1 if interleaved else 0, _HALF[dtype], _ptr(workspace),
+          _ptr(wq), _ptr(wk), _ptr(rope), _ptr(positions), _ptr(dq), _ptr(dk), _ptr(dwq), _ptr(dwk),
+          *sizes, _out_strides(dq_out, q, q_st), _out_strides(dk_out, k, k_st), q_st, k_st,
+          _out_strides(dq, q, q_st), _out_strides(dk, k, k_st), eps, *flags, _ptr(workspace),
           0 if workspace is None else workspace.nbytes)
     return dq, dk, dwq, dwk
 
@@ -706,16 +733,14 @@ def paged_workspace_size(Hq: int, Hk: int, d: int, max_q: int, device=None) -> i
     return _workspace_bytes("attn_fwd_paged_workspace_size", _device_index(device), Hq, Hk, d, max_q)
 
 
-def _paged_args(page_table, cu_q, kv_len, k_cache, v_cache, dtype, dev, d):
+def _paged_checks(page_table, cu_q, kv_len, k_cache, v_cache, dtype, dev, d):
     """The checks of a paged call's lists and cache: (sequences, pages a
     sequence, table row stride, pages, key heads, page size)."""
-    i32 = torch.int32
-    if not (isinstance(page_table, _Tensor) and page_table.dtype == i32 and page_table.dim() == 2
-            and page_table.get_device() == dev and isinstance(cu_q, _Tensor) and cu_q.dtype == i32
-            and cu_q.dim() == 1 and cu_q.get_device() == dev and isinstance(kv_len, _Tensor)
-            and kv_len.dtype == i32 and kv_len.dim() == 1 and kv_len.get_device() == dev):
-        raise ValueError("page_table [B, pages], cu_q [B + 1] and kv_len [B] must be int32 tensors "
-                         "on CUDA device %d" % dev)
+    for name, t, dims in (("page_table", page_table, 2), ("cu_q", cu_q, 1), ("kv_len", kv_len, 1)):
+        if not isinstance(t, _Tensor) or t.dtype != torch.int32 or t.dim() != dims \
+                or t.get_device() != dev:
+            raise ValueError("%s must be a %d-dimensional int32 tensor on CUDA device %d"
+                             % (name, dims, dev))
     B, max_pages = page_table.shape
     if cu_q.shape[0] != B + 1 or kv_len.shape[0] != B or not cu_q.is_contiguous() \
             or not kv_len.is_contiguous() or (max_pages > 1 and page_table.stride(1) != 1):
@@ -733,6 +758,24 @@ def _paged_args(page_table, cu_q, kv_len, k_cache, v_cache, dtype, dev, d):
     return B, max_pages, page_table.stride(0) if B > 1 else max_pages, pages, Hk, page
 
 
+def _append_plan(key, k, v, k_cache, v_cache, page_table, cu_q, kv_len, rope, interleaved):
+    dtype, dev = _first_half("k", k, 3)
+    _check_half("v", v, 3, dtype, dev)
+    T, Hk, d = k.shape
+    if v.shape != k.shape:
+        raise ValueError("k and v must have one shape, got %s %s" % (tuple(k.shape), tuple(v.shape)))
+    if d not in (64, 96, 128, 256):
+        raise ValueError("head dimension must be 64, 96, 128 or 256, got %d" % d)
+    B, max_pages, row, pages, heads, page = _paged_checks(page_table, cu_q, kv_len, k_cache, v_cache,
+                                                          dtype, dev, d)
+    if heads != Hk:
+        raise ValueError("the caches have %d heads, k and v %d" % (heads, Hk))
+    rot, max_pos = _check_rope(rope, d, dev)
+    return _keep(key, (dev, (T, B, Hk, d, pages, page, max_pages, row, rot, max_pos, _outer(k),
+                             _outer(v), _outer(k_cache), _outer(v_cache), 1 if interleaved else 0,
+                             _HALF[dtype])))
+
+
 def kv_append(k, v, k_cache, v_cache, page_table, cu_q, kv_len, rope=None,
               interleaved: bool = False, stream=None):
     """Append the new tokens' keys and values k, v [T, Hk, d] to the paged
@@ -743,23 +786,37 @@ def kv_append(k, v, k_cache, v_cache, page_table, cu_q, kv_len, rope=None,
     strides; ``page_table`` int32 [B, pages], ``cu_q`` int32 [B + 1],
     ``kv_len`` int32 [B] (keys of each sequence, the new ones included).
     Returns (k_cache, v_cache)."""
-    dtype, dev = _first_half("k", k, 3)
-    _check_half("v", v, 3, dtype, dev)
-    T, Hk, d = k.shape
-    if v.shape != k.shape:
-        raise ValueError("k and v must have one shape, got %s %s" % (tuple(k.shape), tuple(v.shape)))
-    if d not in (64, 96, 128, 256):
-        raise ValueError("head dimension must be 64, 96, 128 or 256, got %d" % d)
-    B, max_pages, row, pages, heads, page = _paged_args(page_table, cu_q, kv_len, k_cache, v_cache,
-                                                        dtype, dev, d)
-    if heads != Hk:
-        raise ValueError("the caches have %d heads, k and v %d" % (heads, Hk))
-    table, rot, max_pos = _rope_args(rope, d, dev)
+    try:
+        key = ("append", _of(k), _of(v), _of(k_cache), _of(v_cache), _of(page_table), _of(cu_q),
+               _of(kv_len), _of(rope), bool(interleaved))
+    except AttributeError:  # not tensors: the checks say which
+        key = None
+    dev, args = _plans.get(key) or _append_plan(key, k, v, k_cache, v_cache, page_table, cu_q, kv_len,
+                                                rope, interleaved)
     _call("fattn_kv_append", dev, stream, k.data_ptr(), v.data_ptr(), k_cache.data_ptr(),
-          v_cache.data_ptr(), page_table.data_ptr(), cu_q.data_ptr(), kv_len.data_ptr(), table, T,
-          B, Hk, d, pages, page, max_pages, row, rot, max_pos, _outer(k), _outer(v), _outer(k_cache),
-          _outer(v_cache), 1 if interleaved else 0, _HALF[dtype])
+          v_cache.data_ptr(), page_table.data_ptr(), cu_q.data_ptr(), kv_len.data_ptr(), _ptr(rope),
+          *args)
     return k_cache, v_cache
+
+
+def _paged_plan(key, q, k_cache, v_cache, page_table, cu_q, kv_len, max_q, causal, scale):
+    dtype, dev = _first_half("q", q, 3)
+    T, Hq, d = q.shape
+    if d not in (64, 96, 128):
+        raise ValueError("head dimension must be 64, 96 or 128, got %d" % d)
+    B, max_pages, row, pages, Hk, page = _paged_checks(page_table, cu_q, kv_len, k_cache, v_cache,
+                                                       dtype, dev, d)
+    if Hk == 0 or Hq % Hk or Hq > 128 * Hk:
+        raise ValueError("Hq must be 1 to 128 times Hk, got %d and %d" % (Hq, Hk))
+    if max_q < 1:
+        raise ValueError("max_q must be at least 1, got %d" % max_q)
+    need = _workspace_bytes("attn_fwd_paged_workspace_size", dev, Hq, Hk, d, max_q)
+    dense = (ctypes.c_longlong * 2)(Hq * d, d)
+    return _keep(key, (dev, dtype, (T, Hq, d), (T, Hq), max(need, 16), dense,
+                       (T, B, Hq, Hk, d, pages, page, max_pages, row, max_q, _outer(q),
+                        _outer(k_cache), _outer(v_cache)),
+                       (default_scale(d) if scale is None else scale, 1 if causal else 0,
+                        _HALF[dtype])))
 
 
 def attn_fwd_paged(q, k_cache, v_cache, page_table, cu_q, kv_len, max_q: int,
@@ -771,34 +828,30 @@ def attn_fwd_paged(q, k_cache, v_cache, page_table, cu_q, kv_len, max_q: int,
     tokens' keys already appended; ``max_q`` is at least the new tokens of
     every sequence.  Returns (out [T, Hq, d], lse fp32 [T, Hq]); rows from
     cu_q[B] on are not written."""
-    dtype, dev = _first_half("q", q, 3)
-    T, Hq, d = q.shape
-    if d not in (64, 96, 128):
-        raise ValueError("head dimension must be 64, 96 or 128, got %d" % d)
-    B, max_pages, row, pages, Hk, page = _paged_args(page_table, cu_q, kv_len, k_cache, v_cache,
-                                                     dtype, dev, d)
-    if Hk == 0 or Hq % Hk or Hq > 128 * Hk:
-        raise ValueError("Hq must be 1 to 128 times Hk, got %d and %d" % (Hq, Hk))
-    if max_q < 1:
-        raise ValueError("max_q must be at least 1, got %d" % max_q)
+    try:
+        key = ("paged", _of(q), _of(k_cache), _of(v_cache), _of(page_table), _of(cu_q), _of(kv_len),
+               max_q, bool(causal), scale)
+    except AttributeError:  # not tensors: the checks say which
+        key = None
+    dev, dtype, shape, lse_shape, need, dense, args, flags = _plans.get(key) or _paged_plan(
+        key, q, k_cache, v_cache, page_table, cu_q, kv_len, max_q, causal, scale)
+    o_st = dense
     if out is None:
-        out = _empty((T, Hq, d), dtype, dev, stream)
+        out = _empty(shape, dtype, dev, stream)
     else:
         _check_half("out", out, 3, dtype, dev)
         if out.shape != q.shape:
             raise ValueError("out must have q's shape")
+        o_st = _outer(out)
     if lse is None:
-        lse = _empty((T, Hq), torch.float32, dev, stream)
+        lse = _empty(lse_shape, torch.float32, dev, stream)
     else:
-        _check_plain("lse", lse, torch.float32, (T, Hq), dev)
+        _check_plain("lse", lse, torch.float32, lse_shape, dev)
     if workspace is None:
-        need = _workspace_bytes("attn_fwd_paged_workspace_size", dev, Hq, Hk, d, max_q)
         workspace = _empty(need, torch.uint8, dev, stream)
     _call("attn_fwd_paged", dev, stream, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
           page_table.data_ptr(), cu_q.data_ptr(), kv_len.data_ptr(), out.data_ptr(), lse.data_ptr(),
-          T, B, Hq, Hk, d, pages, page, max_pages, row, max_q, _outer(q), _outer(k_cache),
-          _outer(v_cache), _outer(out), default_scale(d) if scale is None else scale,
-          1 if causal else 0, _HALF[dtype], workspace.data_ptr(), workspace.nbytes)
+          *args, o_st, *flags, workspace.data_ptr(), workspace.nbytes)
     return out, lse
 
 
