@@ -1049,7 +1049,7 @@ PagedWs paged_ws(int Hq, int Hk, int d, int max_q, int num_sms)
     const int G = Hq / Hk;
     w.tile_tokens = 128 / G;
     w.slot_rows = max_q <= w.tile_tokens ? (max_q * G + 31) / 32 * 32 : 256;
-    w.l = align_up(static_cast<size_t>(num_sms) * sizeof(int4), kWsAlign);
+    w.l = align_up(2 * static_cast<size_t>(num_sms) * sizeof(int4), kWsAlign);
     w.o = align_up(w.l + 2ull * num_sms * w.slot_rows * 4, kWsAlign);
     w.bytes = w.o + 2ull * num_sms * w.slot_rows * d * 4;
     return w;

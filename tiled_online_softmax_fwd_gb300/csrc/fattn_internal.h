@@ -162,7 +162,9 @@ struct PagedArgs {
     void *o;
     float *lse;
     float *ws_o, *ws_l;  // partial O [2 SMs][slot_rows][d], base-2 lse [2 SMs][slot_rows]
-    int4 *starts;        // [SMs]: (sequence, key head, unit, key tile or 0) a CTA starts at
+    // [SMs][2]: where a CTA starts, (sequence, key head, unit, key tile or 0),
+    // and that unit's (first token, tokens).
+    int4 *starts;
     const int *page_table, *cu_q, *kv_len;
     uint32_t *status;
     long long o_st[2];  // token, head

@@ -338,12 +338,14 @@ __device__ void find_start(const PagedArgs &a, const Costs &cost, Bars &b)
             const int kind = kind_of(a, s, tiles, p);
             const int t = tile_at(st.y, keys, cost.unit_of(kind), cost.key_of(kind), st.snap);
             const bool split = t > 0 && t < (keys + kBN - 1) / kBN;
-            a.starts[blockIdx.x] = make_int4(st.b, st.h, st.p, split ? t : 0);
+            const int first = st.p * 2 * a.tile_tokens;
+            a.starts[2 * c] = make_int4(st.b, st.h, st.p, split ? t : 0);
+            a.starts[2 * c + 1] = make_int4(s.q0 + first, min(s.n - first, 2 * a.tile_tokens), 0, 0);
             break;
         }
     }
     if (tid == 0 && (c >= shares || lo >= hi))
-        a.starts[blockIdx.x] = make_int4(-1, 0, 0, 0);
+        a.starts[2 * c] = make_int4(-1, 0, 0, 0);
 }
 
 // The same value on every lane of a converged warp, passed through a shuffle.
@@ -1619,82 +1621,137 @@ __global__ void __launch_bounds__(kThreads, 1)
 // boundary in it: the partial of CTA x (its last slot) and those of CTAs x +
 // 1, x + 2, ... that start inside the same unit.  With base-2 partial
 // log-sum-exps e_s: lse = ln2 log2 sum 2^e_s, O = sum 2^(e_s - lse2) O_s.
-// One warp a row, D / 32 columns a lane, eight slots in flight.
-constexpr int kCombineRows = 32;  // rows a block
+// A warp takes kRows rows at a time and kSlots of their partials, all loads of
+// such a group in flight together, D / 32 consecutive columns a lane: one row
+// and eight partials where units are single tiles (few rows, long chains), two
+// rows and two where they may be pairs (256 rows, mostly one boundary): the
+// ragged d = 64 batch took 73 us with that, 80 with four rows, 83 with one.
+template <int N> struct Cols;
+template <> struct Cols<2> {
+    static __device__ __forceinline__ void load(const float *p, float (&x)[2])
+    {
+        const float2 v = *reinterpret_cast<const float2 *>(p);
+        x[0] = v.x;
+        x[1] = v.y;
+    }
+};
+template <> struct Cols<3> {
+    static __device__ __forceinline__ void load(const float *p, float (&x)[3])
+    {
+        x[0] = p[0];
+        x[1] = p[1];
+        x[2] = p[2];
+    }
+};
+template <> struct Cols<4> {
+    static __device__ __forceinline__ void load(const float *p, float (&x)[4])
+    {
+        const float4 v = *reinterpret_cast<const float4 *>(p);
+        x[0] = v.x;
+        x[1] = v.y;
+        x[2] = v.z;
+        x[3] = v.w;
+    }
+};
 
-template <int D, bool kF16>
+template <int D, bool kF16, int kRows, int kSlots>
 __global__ void __launch_bounds__(128) combine_paged_kernel(const PagedArgs a, int grid)
 {
-    constexpr int kCols = D / 32, kBatch = 8;
+    constexpr int kCols = D / 32;
     const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
     grid_launch_dependents();
     grid_dependency_wait();
+    // One round of loads: the starts from CTA c - 1 on, a lane each, and what
+    // this unit's rows are.
     const int c = blockIdx.x + 1;
-    const int4 mine = a.starts[c];
-    if (mine.x < 0 || mine.w == 0)
+    int4 start = a.starts[2 * min(c - 1 + lane, grid - 1)];
+    const int4 unit = a.starts[2 * c + 1];  // first token, tokens
+    const int mine_b = __shfl_sync(0xffffffffu, start.x, 1), mine_h = __shfl_sync(0xffffffffu, start.y, 1),
+              mine_p = __shfl_sync(0xffffffffu, start.z, 1), mine_t = __shfl_sync(0xffffffffu, start.w, 1);
+    if (mine_b < 0 || mine_t == 0)
         return;
-    auto same = [&](int4 o) { return o.x == mine.x && o.y == mine.y && o.z == mine.z && o.w > 0; };
-    if (same(a.starts[c - 1]))
-        return;
-    int count = 0;  // CTAs from c on that start inside this unit
-    for (;;) {
-        const int k = c + count + lane;
-        const unsigned hit = __ballot_sync(0xffffffffu, k < grid && same(a.starts[min(k, grid - 1)]));
+    // CTAs from c on that start inside this unit; c - 1 must not.
+    int count = 0;
+    for (int at = c - 1;;) {
+        const bool same = start.x == mine_b && start.y == mine_h && start.z == mine_p && start.w > 0;
+        const unsigned hit = __ballot_sync(0xffffffffu, at + lane < grid && same) | (at == c - 1 ? 1u : 0u);
+        if (at == c - 1 && __shfl_sync(0xffffffffu, same ? 1 : 0, 0))
+            return;
         const int run = hit == 0xffffffffu ? 32 : __ffs(~hit) - 1;
-        count += run;
+        count += run - (at == c - 1 ? 1 : 0);
         if (run < 32)
             break;
+        at += 32;
+        start = a.starts[2 * min(at + lane, grid - 1)];
     }
-    bool bad;
-    const Seq s = load_seq(a, mine.x, bad);
-    const int tiles = tiles_of(a, s);
     const long long slot0 = 2LL * (c - 1) + 1;
-    for (int row = blockIdx.y * kCombineRows + warp; row < min(a.slot_rows, (static_cast<int>(blockIdx.y) + 1) * kCombineRows);
-         row += 4) {
-        const int tile = 2 * mine.z + row / kBM, r = row % kBM;
-        const int tok = row_token(a, r), g = r - tok * a.G;
-        if (tile >= tiles || tok >= a.tile_tokens || tile * a.tile_tokens + tok >= s.n)
-            continue;
-        float mx = -INFINITY, se = 0.f, acc[kCols];
+    const int row0 = (blockIdx.y * 4 + warp) * kRows;
+    bool live[kRows];
+    bool any = false;
+    float mx[kRows], se[kRows], acc[kRows][kCols];
 #pragma unroll
-        for (int i = 0; i < kCols; ++i)
-            acc[i] = 0.f;
-        for (int k0 = 0; k0 <= count; k0 += kBatch) {
-            float e[kBatch], o[kBatch][kCols];
+    for (int i = 0; i < kRows; ++i) {
+        const int row = row0 + i, tok = row_token(a, row % kBM);
+        live[i] = row < a.slot_rows && tok < a.tile_tokens && row / kBM * a.tile_tokens + tok < unit.y;
+        any = any || live[i];
+        mx[i] = -INFINITY;
+        se[i] = 0.f;
 #pragma unroll
-            for (int k = 0; k < kBatch; ++k) {
-                e[k] = -INFINITY;
-                if (k0 + k <= count) {
-                    const long long slot = k0 + k == 0 ? slot0 : 2LL * (c + k0 + k - 1);
-                    const long long at = slot * a.slot_rows + row;
-                    e[k] = a.ws_l[at];
+        for (int j = 0; j < kCols; ++j)
+            acc[i][j] = 0.f;
+    }
+    if (!any)
+        return;
+    for (int k0 = 0; k0 <= count; k0 += kSlots) {
+        float e[kSlots][kRows], o[kSlots][kRows][kCols];
 #pragma unroll
-                    for (int i = 0; i < kCols; ++i)
-                        o[k][i] = a.ws_o[at * D + i * 32 + lane];
+        for (int k = 0; k < kSlots; ++k) {
+            const long long slot = k0 + k == 0 ? slot0 : 2LL * (c + k0 + k - 1);
+#pragma unroll
+            for (int i = 0; i < kRows; ++i) {
+                e[k][i] = -INFINITY;
+                if (k0 + k <= count && live[i]) {
+                    const long long at = slot * a.slot_rows + row0 + i;
+                    e[k][i] = a.ws_l[at];
+                    Cols<kCols>::load(a.ws_o + at * D + lane * kCols, o[k][i]);
                 }
             }
-#pragma unroll
-            for (int k = 0; k < kBatch; ++k) {
-                if (e[k] == -INFINITY)  // holds no key of this row (its O is not written)
-                    continue;
-                const float ne = fmaxf(mx, e[k]);
-                const float f = ex2(mx - ne), x = ex2(e[k] - ne);
-                se = se * f + x;
-#pragma unroll
-                for (int i = 0; i < kCols; ++i)
-                    acc[i] = fmaf(x, o[k][i], acc[i] * f);
-                mx = ne;
-            }
         }
-        const float inv = se > 0.f ? 1.f / se : 0.f;
-        const long long token = static_cast<long long>(s.q0) + tile * a.tile_tokens + tok;
-        const int head = mine.y * a.G + g;
-        uint16_t *dst = static_cast<uint16_t *>(a.o) + token * a.o_st[0] + head * a.o_st[1];
 #pragma unroll
-        for (int i = 0; i < kCols; ++i)
-            dst[i * 32 + lane] = static_cast<uint16_t>(pack2<kF16>(acc[i] * inv, 0.f) & 0xffffu);
+        for (int k = 0; k < kSlots; ++k)
+#pragma unroll
+            for (int i = 0; i < kRows; ++i) {
+                if (e[k][i] == -INFINITY)  // holds no key of this row (its O is not written)
+                    continue;
+                const float ne = fmaxf(mx[i], e[k][i]);
+                const float f = ex2(mx[i] - ne), x = ex2(e[k][i] - ne);
+                se[i] = se[i] * f + x;
+#pragma unroll
+                for (int j = 0; j < kCols; ++j)
+                    acc[i][j] = fmaf(x, o[k][i][j], acc[i][j] * f);
+                mx[i] = ne;
+            }
+    }
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+        if (!live[i])
+            continue;
+        const int row = row0 + i, r = row % kBM, tok = row_token(a, r);
+        const long long token = static_cast<long long>(unit.x) + row / kBM * a.tile_tokens + tok;
+        const int head = mine_h * a.G + r - tok * a.G;
+        const float inv = se[i] > 0.f ? 1.f / se[i] : 0.f;
+        uint16_t *dst = static_cast<uint16_t *>(a.o) + token * a.o_st[0] + head * a.o_st[1] + lane * kCols;
+        if constexpr (kCols % 2 == 0) {
+#pragma unroll
+            for (int j = 0; j < kCols; j += 2)
+                *reinterpret_cast<uint32_t *>(dst + j) = pack2<kF16>(acc[i][j] * inv, acc[i][j + 1] * inv);
+        } else {
+#pragma unroll
+            for (int j = 0; j < kCols; ++j)
+                dst[j] = static_cast<uint16_t>(pack2<kF16>(acc[i][j] * inv, 0.f) & 0xffffu);
+        }
         if (lane == 0)
-            a.lse[token * a.Hk * a.G + head] = se > 0.f ? (mx + log2f(se)) * kLn2 : -INFINITY;
+            a.lse[token * a.Hk * a.G + head] = se[i] > 0.f ? (mx[i] + log2f(se[i])) * kLn2 : -INFINITY;
     }
 }
 
@@ -1721,10 +1778,13 @@ cudaError_t launch(const PagedArgs &a, const PagedMaps &maps, int num_sms, cudaS
     e = cudaLaunchKernelEx(&cfg, paged_kernel<D, kF16>, maps.q, maps.q_quad, maps.k, maps.v, a);
     if (e != cudaSuccess || num_sms < 2)
         return e;
-    cfg.gridDim = dim3(num_sms - 1, (a.slot_rows + kCombineRows - 1) / kCombineRows);
+    const bool pairs = a.slot_rows > kBM;
+    const int rows = pairs ? 2 : 1;  // a warp
+    cfg.gridDim = dim3(num_sms - 1, (a.slot_rows + 4 * rows - 1) / (4 * rows));
     cfg.blockDim = dim3(128);
     cfg.dynamicSmemBytes = 0;
-    return cudaLaunchKernelEx(&cfg, combine_paged_kernel<D, kF16>, a, num_sms);
+    return pairs ? cudaLaunchKernelEx(&cfg, combine_paged_kernel<D, kF16, 2, 2>, a, num_sms)
+                 : cudaLaunchKernelEx(&cfg, combine_paged_kernel<D, kF16, 1, 8>, a, num_sms);
 }
 
 template <int D>
