@@ -486,7 +486,8 @@ fattn_status_t fattn_kv_append(const void *k, const void *v, void *k_cache, void
  *   lse       : fp32 [T][Hq], contiguous
  *   d         : 64, 96 or 128;  Hq a multiple of Hk, Hq / Hk <= 128
  *   max_q     : at least the new tokens of every sequence (it sizes the
- *               workspace; a sequence with more has only max_q served)
+ *               workspace; of a sequence with more, at most max_q rows are
+ *               written, and they are not meaningful)
  *   dtype     : 0 = bf16 (P and V rounded to fp16, as attn_fwd), 1 = fp16
  *   workspace : device, 16-byte aligned, attn_fwd_paged_workspace_size(...)
  *               bytes on the current device (0 on invalid arguments); contents

@@ -131,6 +131,50 @@ def test_unused_slots_may_hold_anything(fill, dtype):
         check(o, lse, reference(p, q), dtype, max(lens), "fill %s unused %d" % (fill, unused))
 
 
+@pytest.mark.parametrize("d", [64, 96, 128])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+def test_rows_around_a_lane_quarter(d, dtype):
+    """Tiles of at most 32 rows are shared by the four warps of a warpgroup:
+    row counts on both sides of that and of the epilogue's block widths, whole
+    and split over CTAs."""
+    for G, n in ((1, 32), (1, 33), (1, 31), (32, 1), (33, 1), (16, 2), (11, 3), (10, 3), (8, 4),
+                 (8, 1), (9, 1), (5, 2), (11, 1), (5, 3), (4, 4), (17, 1)):
+        lens = [n, 130, 700 + n]
+        for q_lens, kv_lens in (([n] * 3, lens), ([n], [9000])):
+            p = make_paged(q_lens, kv_lens, 1, d, 32, dtype, seed=G + n, fill=float("nan"))
+            q = queries(p.T, G, d, dtype, 3)
+            for max_q in (n, 150):
+                o, lse = run(p, q, max_q=max_q)
+                assert fattn.device_status() == 0
+                check(o, lse, reference(p, q), dtype, max(kv_lens), "G %d n %d max_q %d" % (G, n, max_q))
+
+
+@pytest.mark.parametrize("seed", range(24))
+def test_random_batches(seed):
+    """Mixed units in any order: empty sequences, rows without keys, single
+    tokens, drafts, chunks, long and short caches."""
+    import random
+    rng = random.Random(seed)
+    d, Hk = rng.choice([64, 64, 96, 128]), rng.choice([1, 2, 3])
+    G = rng.choice([1, 1, 2, 3, 4, 7, 8, 12, 40])
+    dtype = rng.choice([torch.bfloat16, torch.float16])
+    q_lens, kv_lens = [], []
+    for _ in range(rng.randint(1, 14)):
+        n = rng.choice([0, 1, 1, 1, rng.randint(2, 9), rng.randint(10, 140), rng.randint(1, 400)])
+        L = rng.choice([n, n + rng.randint(0, 300), n + rng.randint(0, 4000), rng.randint(0, 2 * n + 1), 0])
+        q_lens.append(n)
+        kv_lens.append(L)
+    page, causal = rng.choice([16, 32, 64, 128, 256]), rng.random() < 0.8
+    p = make_paged(q_lens, kv_lens, Hk, d, page, dtype, seed=seed, fill=float("nan"))
+    if p.T == 0:
+        pytest.skip("no tokens")
+    q = queries(p.T, Hk * G, d, dtype, seed, 1.5)
+    o, lse = run(p, q, causal, max_q=p.max_q + rng.randint(0, 50))
+    assert fattn.device_status() == 0
+    check(o, lse, reference(p, q, causal), dtype, max(kv_lens + [1]),
+          "q %s k %s G %d Hk %d d %d page %d" % (q_lens, kv_lens, G, Hk, d, page))
+
+
 def test_rows_that_see_no_key():
     """More new tokens than keys: the first ones see nothing (o = 0, lse =
     -inf), in units that start, end and lie wholly there; and no keys at all."""
@@ -324,6 +368,67 @@ def test_streams_and_replayed_graphs():
     for _, o, lse in outs:
         check(o, lse, want, torch.bfloat16, 300)
     assert torch.equal(outs[0][1], outs[1][1])
+    assert fattn.device_status() == 0
+
+
+def test_two_calls_at_once():
+    """Two streams, a workspace each, both filling the GPU; many times."""
+    cases = []
+    for seed, (q_lens, kv_lens, d) in enumerate((([1] * 12, [3000 + 17 * i for i in range(12)], 128),
+                                                 ([200, 1, 60], [900, 4000, 60], 64))):
+        p = make_paged(q_lens, kv_lens, 4, d, 32, seed=30 + seed)
+        q = queries(p.T, 8, d, torch.bfloat16, 14 + seed).cuda()
+        args = (q, p.k_cache.cuda(), p.v_cache.cuda(), *p.lists(), p.max_q)
+        cases.append((args, fattn.attn_fwd_paged(*args), torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(10):
+        for args, _, s in cases:
+            got.append(fattn.attn_fwd_paged(*args, stream=s))
+    torch.cuda.synchronize()
+    for i, (o, lse) in enumerate(got):
+        want = cases[i % 2][1]
+        assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
+    assert fattn.device_status() == 0
+
+
+def test_a_captured_step_behind_copies_and_a_joined_stream():
+    """Copies, the append and the attention in one graph, the queries produced
+    on another stream that joins before the attention: the attention is
+    launched ahead of its predecessors and has to wait for them."""
+    p = make_paged([1] * 4, [300, 40, 129, 700], 2, 128, 16, seed=33)
+    g = torch.Generator().manual_seed(1)
+    steps = [[torch.randn(4, h, 128, generator=g).to(torch.bfloat16) for h in (8, 2, 2)] for _ in range(6)]
+    q, k, v = [torch.zeros_like(t).cuda() for t in steps[0]]
+    src = [torch.zeros_like(t).cuda() for t in steps[0]]
+    kc, vc = p.k_cache.cuda(), p.v_cache.cuda()
+    lists = p.lists()
+    o, lse = torch.empty_like(q), torch.empty(4, 8, device="cuda")
+    ws = torch.empty(fattn.paged_workspace_size(8, 2, 128, 1), dtype=torch.uint8, device="cuda")
+    side = torch.cuda.Stream()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        main = torch.cuda.current_stream()
+        k.copy_(src[1])
+        v.copy_(src[2])
+        side.wait_stream(main)
+        with torch.cuda.stream(side):
+            q.copy_(src[0])
+            q.mul_(0.5)
+        fattn.kv_append(k, v, kc, vc, *lists)
+        main.wait_stream(side)
+        fattn.attn_fwd_paged(q, kc, vc, *lists, 1, workspace=ws, out=o, lse=lse)
+        q.zero_()
+    for step in steps:
+        for a, b in zip(src, step):
+            a.copy_(b)
+        graph.replay()
+        torch.cuda.synchronize()
+        for b in range(4):
+            at = p.kv_len[b] - 1
+            page = int(p.table[b, at // 16])
+            p.k_cache[page, :, at % 16], p.v_cache[page, :, at % 16] = step[1][b], step[2][b]
+        check(o, lse, reference(p, step[0] * 0.5), torch.bfloat16, 700)
     assert fattn.device_status() == 0
 
 

@@ -543,9 +543,9 @@ __global__ void __launch_bounds__(kReduceCols *kReduceRows)
     const int t = blockIdx.x * kReduceCols >= D ? 1 : 0;
     const int col = blockIdx.x * kReduceCols - t * D + threadIdx.x;
     float *dst = t == 0 ? dwq : dwk;
+    ptx::grid_dependency_wait();  // before any way out: what follows this grid relies on it
     if (dst == nullptr)
         return;
-    ptx::grid_dependency_wait();
     const int b0 = t == 0 ? 0 : q_blocks, b1 = t == 0 ? q_blocks : q_blocks + k_blocks;
     Sum2 x;
 #pragma unroll 8

@@ -543,6 +543,8 @@ def _of(t):
 
 
 def _keep(key, plan):
+    if key is None:
+        return plan
     if len(_plans) >= _MAX_PLANS:
         _plans.clear()
     _plans[key] = plan
