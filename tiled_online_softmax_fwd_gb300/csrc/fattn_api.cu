@@ -1634,6 +1634,8 @@ fattn_status_t attn_fwd_paged(const void *q, const void *k_cache, const void *v_
 {
     if (T < 0 || (dtype != 0 && dtype != 1) || (causal != 0 && causal != 1))
         return FATTN_ERR_INVALID_ARG;
+    if (T > 0x7fffffff - 256)  // token indexes are 32-bit, tiles included
+        return FATTN_ERR_UNSUPPORTED;
     if (!(scale > 0.f) || !isfinite(scale))
         return FATTN_ERR_INVALID_ARG;
     const Paging g{page_table, cu_q, kv_len, B, num_pages, page_size, max_pages, page_table_stride};
