@@ -746,7 +746,7 @@ cudaError_t norm_rope(NormRopeArgs a, int num_sms, cudaStream_t stream)
 template <int D, bool kF16, bool kInter>
 cudaError_t kv_append(KvAppendArgs a, int num_sms, cudaStream_t stream)
 {
-    const long long blocks = (a.T + Geo<D>::kTokens - 1) / Geo<D>::kTokens;
+    const long long blocks = (static_cast<long long>(a.T) + Geo<D>::kTokens - 1) / Geo<D>::kTokens;
     a.heads_per_chunk = heads_per_item(2 * blocks, a.H, num_sms);
     a.chunks = (a.H + a.heads_per_chunk - 1) / a.heads_per_chunk;
     a.items = blocks * 2 * a.chunks;
