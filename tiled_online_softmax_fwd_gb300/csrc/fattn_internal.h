@@ -129,10 +129,12 @@ struct NormRopeArgs {
     long long tokens;  // B * N
     int N, H[2], d, rot, max_pos, interleaved, f16;
     float eps;
-    // Filled in by the launch: heads an item, chunks of heads and items of each tensor.
-    // Backward: blocks that work on each tensor.
+    // Filled in by the launch.  Forward: heads an item, chunks of heads and
+    // items of each tensor.  Backward: blocks that work on each tensor, its
+    // (block of tokens, head) rows, the rows of a warp, and warps with one more.
     int heads_per_chunk, chunks[2], blocks[2];
-    long long items[2];
+    long long items[2], rows_each[2];
+    int rows_over[2];
 };
 cudaError_t launch_norm_rope(const NormRopeArgs &a, int num_sms, cudaStream_t stream);
 // Blocks (partials) of a backward launch at most.

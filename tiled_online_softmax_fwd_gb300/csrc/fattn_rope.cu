@@ -26,6 +26,8 @@
 #include <cuda_fp16.h>
 #include <stdint.h>
 
+#include <algorithm>
+
 #include "fattn_internal.h"
 #include "ptx_sm103.cuh"
 
@@ -204,19 +206,17 @@ template <int D> __device__ __forceinline__ float row_total(float x)
     return sum;
 }
 
-// A warp's work: kTokens consecutive tokens (of the flattened batch) and a
-// run of heads of q (which = 0) or k (which = 1).
+// A lane's token in block `block` of kTokens consecutive tokens (of the
+// flattened batch).
 struct Item {
-    int h0, h1, b, n;
+    int b, n;
     long long pos;
-    bool live;  // the lane's token exists, and has a position in the table
+    bool live;  // the token exists, and has a position in the table
 };
 template <int D>
-__device__ __forceinline__ Item item_at(const NormRopeArgs &a, int which, int block, int chunk, int lane)
+__device__ __forceinline__ Item item_at(const NormRopeArgs &a, int block, int lane)
 {
     Item x;
-    x.h0 = chunk * a.heads_per_chunk;
-    x.h1 = min(x.h0 + a.heads_per_chunk, a.H[which]);
     const unsigned tok = static_cast<unsigned>(block) * Geo<D>::kTokens + lane / Geo<D>::kLanes;
     x.live = tok < static_cast<unsigned>(a.tokens) && Geo<D>::in_row(lane);
     const unsigned b = x.live ? tok / static_cast<unsigned>(a.N) : 0u;
@@ -227,7 +227,7 @@ __device__ __forceinline__ Item item_at(const NormRopeArgs &a, int which, int bl
         x.pos = a.positions != nullptr ? a.positions[tok] : x.n;
         if (x.pos < 0 || x.pos >= a.max_pos) {
             x.live = false;
-            if (lane % Geo<D>::kLanes == 0 && x.h0 == 0)
+            if (lane % Geo<D>::kLanes == 0)
                 record_index(a.status, kRoleRotate);
         }
     }
@@ -253,11 +253,12 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) norm_rope_kernel(const
     const int w = it < a.items[0] ? 0 : 1;
     it -= w == 0 ? 0 : a.items[0];
     const int block = static_cast<int>(it / a.chunks[w]);
-    const Item x = item_at<D>(a, w, block, static_cast<int>(it - static_cast<long long>(block) * a.chunks[w]),
-                              lane);
+    const int chunk = static_cast<int>(it - static_cast<long long>(block) * a.chunks[w]);
+    const int h0 = chunk * a.heads_per_chunk, h1 = min(h0 + a.heads_per_chunk, a.H[w]);
+    const Item x = item_at<D>(a, block, lane);
     const Place at = place_of<D>(lane % G::kLanes, a.rot);
-    const uint16_t *x_at = elem_ptr(a.x[w], row_at(a.x_st[w], x) + x.h0 * a.x_st[w][1]);
-    uint16_t *y_at = static_cast<uint16_t *>(a.y[w]) + row_at(a.y_st[w], x) + x.h0 * a.y_st[w][1];
+    const uint16_t *x_at = elem_ptr(a.x[w], row_at(a.x_st[w], x) + h0 * a.x_st[w][1]);
+    uint16_t *y_at = static_cast<uint16_t *>(a.y[w]) + row_at(a.y_st[w], x) + h0 * a.y_st[w][1];
     const long long x_step = a.x_st[w][1], y_step = a.y_st[w][1];
     const bool norm = a.w[w] != nullptr;
     // The weights are folded into the turn: y_a = r (x_a ca w_a + o_a sa w_o).
@@ -283,12 +284,12 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) norm_rope_kernel(const
             }
         }
     }
-    for (int h = x.h0; h < x.h1; h += kBatch) {
+    for (int h = h0; h < h1; h += kBatch) {
         uint4 u[kBatch][2];
 #pragma unroll
         for (int k = 0; k < kBatch; ++k) {
             u[k][0] = u[k][1] = make_uint4(0, 0, 0, 0);
-            if (x.live && h + k < x.h1) {
+            if (x.live && h + k < h1) {
                 u[k][0] = load16(x_at, at.a);
                 u[k][1] = load16(x_at, at.b);
                 x_at += x_step;
@@ -324,7 +325,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) norm_rope_kernel(const
                     xb[i] = ptx::f2_mul(xb[i], r);
                 }
             }
-            if (x.live && h + k < x.h1) {
+            if (x.live && h + k < h1) {
                 store16(y_at, at.a, narrow<kF16>(xa));
                 store16(y_at, at.b, narrow<kF16>(xb));
                 y_at += y_step;
@@ -335,18 +336,24 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) norm_rope_kernel(const
 
 // ------------------------------------------------------------------ backward
 // A persistent grid, its first blocks for q and the others for k in the ratio
-// of their rows: every warp keeps the weight gradients of its rows in registers
-// (fp32) over all its items, the block adds its warps' sums in a fixed order
-// and writes one partial; dw_reduce_kernel adds those, also in a fixed order,
-// so equal calls give equal bits.
+// of their rows, and each warp with one of equal runs of the tensor's (block of
+// tokens, head) rows, in that order.  With items of 8 heads dealt in turn the
+// slowest warp had 10 % more than the mean: B3 H32/4 N4096 d96 took 54 us, now
+// 51 (5.0 TB/s).  Every warp keeps the weight gradients of its rows in
+// registers (fp32), the block adds its warps' sums in a fixed order and writes
+// one partial; dw_reduce_kernel adds those, also in a fixed order, so equal
+// calls give equal bits.
 //
 // A row's two reductions stand between its loads and its stores, and with the
 // rows in flight held in registers (two a lane group) a warp spent most of its
 // time waiting: 80 us for B4 H16 N4096 d128.  So each lane copies its own
 // vectors ahead into its own shared-memory slots (cp.async, no barrier: nobody
-// else reads them), across the ends of items, and its addresses step from head
-// to head: 65 us, 6.2 TB/s.  A ring of 3 rows; with 4 and 5 it was 66 and 69.
+// else reads them), across the ends of blocks, and its addresses step from head
+// to head: 65.5 us, 6.2 TB/s.  A ring of 3 rows; with 4 and 5 it was 66 and 69.
 constexpr int kRing = 3;
+// Rows of a warp where there are few: 1021 tokens of 24 and 6 heads, d = 64,
+// take 6.9 us with 3 rows, 7.7 with 2 and 8.1 with 4.
+constexpr int kMinRows = 3;
 
 __device__ __forceinline__ void copy_ahead(uint32_t dst, const void *src, bool live)
 {
@@ -365,10 +372,9 @@ __global__ void __launch_bounds__(kThreads, kBwdBlocksPerSm) norm_rope_bwd_kerne
     const Place at = place_of<D>(lane % G::kLanes, a.rot);
     const int w = static_cast<int>(blockIdx.x) < a.blocks[0] ? 0 : 1;
     const int block = w == 0 ? blockIdx.x : blockIdx.x - a.blocks[0];
-    const int chunks = a.chunks[w];
-    const int token_blocks = static_cast<int>(a.items[w] / chunks);
-    const int stride = a.blocks[w] * kWarps;
-    const int step_blk = stride / chunks, step_chunk = stride - step_blk * chunks;
+    // This warp's rows: the first rows_over warps have one more than the others.
+    const int self = block * kWarps + warp, over = a.rows_over[w];
+    const long long row0 = self * a.rows_each[w] + min(self, over);
     const bool norm = a.w[w] != nullptr, in_row = G::in_row(lane);
     F8 wa, wb, acc_a, acc_b;
 #pragma unroll
@@ -378,29 +384,27 @@ __global__ void __launch_bounds__(kThreads, kBwdBlocksPerSm) norm_rope_bwd_kerne
         widen<kF16>(load16(a.w[w], at.a), wa);
         widen<kF16>(load16(a.w[w], at.b), wb);
     }
-    // Two walks over the warp's (item, head) rows: `ahead` copies, `now` computes.
+    // Two walks over the rows: `ahead` copies, `now` computes.
     struct Walk {
-        int blk, chunk, left;  // rows left of the item
+        int blk, head, left, rest;  // rows left in this block of tokens, and behind it
         Item x;
     };
     auto enter = [&](Walk &k) {
-        if (k.blk < token_blocks) {
-            k.x = item_at<D>(a, w, k.blk, k.chunk, lane);
-            k.left = k.x.h1 - k.x.h0;
-        }
+        k.left = min(a.H[w] - k.head, k.rest);
+        k.rest -= k.left;
+        if (k.left > 0)
+            k.x = item_at<D>(a, k.blk, lane);
     };
-    auto next_item = [&](Walk &k) {
-        k.blk += step_blk;
-        k.chunk += step_chunk;
-        if (k.chunk >= chunks) {
-            k.chunk -= chunks;
-            ++k.blk;
-        }
+    auto next_block = [&](Walk &k) {
+        ++k.blk;
+        k.head = 0;
         enter(k);
     };
     Walk ahead, now;
-    ahead.blk = (block * kWarps + warp) / chunks;
-    ahead.chunk = block * kWarps + warp - ahead.blk * chunks;
+    const unsigned H = static_cast<unsigned>(a.H[w]);
+    ahead.blk = static_cast<int>(row0 >> 32 == 0 ? static_cast<unsigned>(row0) / H : row0 / H);
+    ahead.head = static_cast<int>(row0 - static_cast<long long>(ahead.blk) * H);
+    ahead.rest = static_cast<int>(a.rows_each[w]) + (self < over ? 1 : 0);
     enter(ahead);
     now = ahead;
     // Where the copies read: stepped from head to head.  A lane without a row
@@ -408,13 +412,13 @@ __global__ void __launch_bounds__(kThreads, kBwdBlocksPerSm) norm_rope_bwd_kerne
     const uint16_t *g_at, *x_at;
     long long g_step, x_step;
     auto point = [&]() {
-        if (ahead.blk >= token_blocks)
+        if (ahead.left == 0)
             return;
         const bool live = ahead.x.live;
-        g_at = elem_ptr(a.g[w], live ? row_at(a.g_st[w], ahead.x) + ahead.x.h0 * a.g_st[w][1] + at.a : 0);
+        g_at = elem_ptr(a.g[w], live ? row_at(a.g_st[w], ahead.x) + ahead.head * a.g_st[w][1] + at.a : 0);
         g_step = live ? a.g_st[w][1] : 0;
         if (norm) {
-            x_at = elem_ptr(a.x[w], live ? row_at(a.x_st[w], ahead.x) + ahead.x.h0 * a.x_st[w][1] + at.a : 0);
+            x_at = elem_ptr(a.x[w], live ? row_at(a.x_st[w], ahead.x) + ahead.head * a.x_st[w][1] + at.a : 0);
             x_step = live ? a.x_st[w][1] : 0;
         }
     };
@@ -425,7 +429,7 @@ __global__ void __launch_bounds__(kThreads, kBwdBlocksPerSm) norm_rope_bwd_kerne
     uint32_t put = ring0;
     int get = 0;
     auto copy_row = [&]() {
-        if (ahead.blk < token_blocks) {
+        if (ahead.left > 0) {
             const bool live = ahead.x.live;
             copy_ahead(put, g_at, live);
             copy_ahead(put + 512, g_at + b_off, live);
@@ -437,7 +441,7 @@ __global__ void __launch_bounds__(kThreads, kBwdBlocksPerSm) norm_rope_bwd_kerne
             }
             put = put == ring0 + (kRing - 1) * kSlot ? ring0 : put + kSlot;
             if (--ahead.left == 0) {
-                next_item(ahead);
+                next_block(ahead);
                 point();
             }
         }
@@ -446,10 +450,10 @@ __global__ void __launch_bounds__(kThreads, kBwdBlocksPerSm) norm_rope_bwd_kerne
 #pragma unroll 1
     for (int i = 0; i < kRing - 1; ++i)
         copy_row();
-    while (now.blk < token_blocks) {
+    while (now.left > 0) {
         const bool live = now.x.live;
         uint16_t *y_at = static_cast<uint16_t *>(a.y[w]) + row_at(a.y_st[w], now.x) +
-                         now.x.h0 * a.y_st[w][1] + at.a;
+                         now.head * a.y_st[w][1] + at.a;
         Turn t;
         if (live && at.turned)
             load_turn<kInter>(a.table, now.x.pos, a.rot, at, -1.f, t);
@@ -494,7 +498,7 @@ __global__ void __launch_bounds__(kThreads, kBwdBlocksPerSm) norm_rope_bwd_kerne
             get = get + 1 == kRing ? 0 : get + 1;
             copy_row();
         }
-        next_item(now);
+        next_block(now);
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
     if (!norm)  // no weights: nothing to sum
@@ -700,21 +704,25 @@ template <int D, bool kF16, bool kInter>
 cudaError_t norm_rope(NormRopeArgs a, int num_sms, cudaStream_t stream)
 {
     const long long blocks = (a.tokens + Geo<D>::kTokens - 1) / Geo<D>::kTokens;
-    a.heads_per_chunk = heads_per_item(blocks, a.H[0] + a.H[1], num_sms);
-    for (int t = 0; t < 2; ++t) {
-        a.chunks[t] = (a.H[t] + a.heads_per_chunk - 1) / a.heads_per_chunk;
-        a.items[t] = blocks * a.chunks[t];
-    }
     if (a.g[0] == nullptr && a.g[1] == nullptr) {
+        a.heads_per_chunk = heads_per_item(blocks, a.H[0] + a.H[1], num_sms);
+        for (int t = 0; t < 2; ++t) {
+            a.chunks[t] = (a.H[t] + a.heads_per_chunk - 1) / a.heads_per_chunk;
+            a.items[t] = blocks * a.chunks[t];
+        }
         const long long grid = (a.items[0] + a.items[1] + kWarps - 1) / kWarps;
         if (grid > 0x7fffffffLL)
             return cudaErrorInvalidConfiguration;
         norm_rope_kernel<D, kF16, kInter><<<static_cast<unsigned>(grid), kThreads, 0, stream>>>(a);
         return cudaGetLastError();
     }
-    // One block a kWarps items while they all fit on the SMs, else the SMs'
-    // blocks in the ratio of the rows, each tensor at least one.
-    const long long need[2] = {(a.items[0] + kWarps - 1) / kWarps, (a.items[1] + kWarps - 1) / kWarps};
+    // kMinRows rows a warp while all blocks fit on the SMs, else the SMs' blocks
+    // in the ratio of the rows, each tensor at least one.
+    long long need[2];
+    for (int t = 0; t < 2; ++t) {
+        a.items[t] = blocks * a.H[t];
+        need[t] = (a.items[t] + kWarps * kMinRows - 1) / (kWarps * kMinRows);
+    }
     const int all = norm_rope_bwd_blocks(num_sms);
     if (need[0] + need[1] <= all) {
         a.blocks[0] = static_cast<int>(need[0]);
@@ -724,6 +732,11 @@ cudaError_t norm_rope(NormRopeArgs a, int num_sms, cudaStream_t stream)
                             (static_cast<long long>(a.H[0]) + a.H[1]);
         a.blocks[0] = static_cast<int>(a.H[0] == 0 ? 0 : a.H[1] == 0 ? all : q < 1 ? 1 : q > all - 1 ? all - 1 : q);
         a.blocks[1] = all - a.blocks[0];
+    }
+    for (int t = 0; t < 2; ++t) {
+        const int warps = std::max(a.blocks[t] * kWarps, 1);
+        a.rows_each[t] = a.items[t] / warps;
+        a.rows_over[t] = static_cast<int>(a.items[t] - a.rows_each[t] * warps);
     }
     const int grid = a.blocks[0] + a.blocks[1];
     norm_rope_bwd_kernel<D, kF16, kInter><<<grid, kThreads, 0, stream>>>(a);
