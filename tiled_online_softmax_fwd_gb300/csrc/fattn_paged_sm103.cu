@@ -53,6 +53,12 @@
 // partial O and log-sum-exp to its slot in the workspace (at most two a CTA),
 // and combine_paged_kernel merges them in slot order.  Ranges depend only on
 // the lengths and the SM count, so equal calls give equal bits.
+//
+// Code size.  Every role is code of its own, 138 KB in all at d = 64, and what
+// the warps of a batch with units of several kinds run at a time does not fit
+// the instruction caches: a CTA of quad units beside one of pairs took up to
+// 1.5 times as long as beside its like.  So what does not stand in an inner
+// loop is not unrolled, and divisions of 64 bits are calls.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <float.h>
@@ -186,10 +192,6 @@ __device__ __forceinline__ Seq in_range(const PagedArgs &a, Raw r, bool &bad)
     bad = s.q0 != r.c0 || s.n != static_cast<long long>(r.c1) - r.c0 || s.L != r.L;
     return s;
 }
-__device__ __forceinline__ Seq load_seq(const PagedArgs &a, int b, bool &bad)
-{
-    return in_range(a, load_raw(a, b), bad);
-}
 
 __device__ __forceinline__ int tiles_of(const PagedArgs &a, const Seq &s)
 {
@@ -204,11 +206,12 @@ __device__ __forceinline__ int keys_seen(const PagedArgs &a, const Seq &s, int e
 
 // a / b of non-negative values, in 32 bits where they fit (64-bit division is a
 // routine of some hundred instructions).
+__device__ __noinline__ long long long_quotient(long long a, long long b) { return a / b; }
 __device__ __forceinline__ long long quotient(long long a, long long b)
 {
     if (((a | b) >> 32) == 0)
         return static_cast<unsigned>(a) / static_cast<unsigned>(b);
-    return a / b;
+    return long_quotient(a, b);
 }
 
 // The kind of a (sequence, head)'s unit p.
@@ -267,6 +270,7 @@ __device__ void find_start(const PagedArgs &a, const Costs &cost, Bars &b)
     long long sum = 0;
     bool any_bad = false;
     Raw raw = {0, 0, 0};  // of the run's last sequence
+#pragma unroll 1
     for (int i = b0; i < b1; ++i) {
         bool bad;
         raw = load_raw(a, i);
@@ -307,6 +311,7 @@ __device__ void find_start(const PagedArgs &a, const Costs &cost, Bars &b)
     const long long lo = c * each + c * rest / shares, hi = (c + 1) * each + (c + 1) * rest / shares;
     if (c < shares && lo < hi && before <= lo && lo < before + sum) {
         long long x = lo - before;
+#pragma unroll 1
         for (int i = b0; i < b1; ++i) {
             bool bad;
             if (b1 - b0 > 1)
@@ -324,6 +329,7 @@ __device__ void find_start(const PagedArgs &a, const Costs &cost, Bars &b)
             st.h = static_cast<int>(quotient(x, head));
             x -= st.h * head;
             int p = 0, end = units;  // largest p with cost_before(p) <= x
+#pragma unroll 1
             while (end - p > 1) {
                 const int mid = (p + end) / 2;
                 if (cost_before(a, cost, s, tiles, mid) <= x)
@@ -478,10 +484,27 @@ __device__ __forceinline__ void record_failure(const PagedArgs &a, Bars &b, uint
     *reinterpret_cast<volatile int *>(&b.abort) = 1;
 }
 
-// Waits by a whole warp; the outcome is uniform.
+// Waits by a whole warp; the outcome is uniform.  Few instructions, as there are
+// some sixty of them (see Code size): 45 each, and the producer's copies unrolled
+// throughout, made the kernel 150 KB, and the ragged d = 64 batch took 74 us
+// instead of 62.
+__device__ __forceinline__ uint32_t timer_lo()
+{
+    uint32_t t;
+    asm volatile("mov.u32 %0, %%globaltimer_lo;" : "=r"(t));
+    return t;
+}
 __device__ __forceinline__ bool warp_wait(uint64_t &bar, uint32_t parity, const volatile int *abort)
 {
-    const bool ok = mbar_wait(smem_addr(&bar), parity, kWaitLimitNs, abort);
+    const uint32_t at = smem_addr(&bar);
+    bool ok = mbar_try_wait(at, parity);
+    if (!ok) {
+        const uint32_t t0 = timer_lo();
+#pragma unroll 1
+        do {
+            ok = mbar_try_wait(at, parity);
+        } while (!ok && *abort == 0 && timer_lo() - t0 < static_cast<uint32_t>(kWaitLimitNs));
+    }
     return __all_sync(0xffffffffu, ok);
 }
 
@@ -538,8 +561,7 @@ __device__ void run_load(const PagedArgs &a, Bars &b, uint32_t smem_base, const 
     const int per_tile = shift < 7 ? kBN >> shift : 1;  // pages a key tile touches
     const int box_rows = shift < 7 ? 1 << shift : kBN;
     const uint32_t q_row_bytes = C::kChunks * a.G * 128u;  // of a token
-    uint32_t q_phase[2] = {0, 0}, pos = 0;
-    int last_q[2] = {-1, -1};
+    uint32_t q_bits = 0, q_used = 0, pos = 0;  // of the Q buffers: phase, was ever filled
     bool ok = true;
     uint32_t pieces = 0;
     // The first table entries of the last piece: the next head's are the same.
@@ -565,32 +587,29 @@ __device__ void run_load(const PagedArgs &a, Bars &b, uint32_t smem_base, const 
             held_ahead = entries(first_page + 32);
         }
         int held = first_page, cur = held_cur, ahead = held_ahead;
-#pragma unroll
+#pragma unroll 1
         for (int t = 0; t < 2; ++t) {
-            if (!ok || (u.alt ? u.j0 == u.j1 || u.q_buf != t : u.n[t] == 0))
+            if (!ok || (u.alt ? u.j0 == u.j1 || u.q_buf != t : (t == 0 ? u.n[0] : u.n[1]) == 0))
                 continue;
-            ok = warp_wait(b.q_empty[t], q_phase[t] ^ 1, abort);
+            ok = warp_wait(b.q_empty[t], ((q_bits >> t) & 1u) ^ 1u, abort);
             if (!ok)
                 continue;
-            const int token = uniform(q0 + u.tile[t] * a.tile_tokens);
+            const int token = uniform(q0 + (t == 0 ? u.tile[0] : u.tile[1]) * a.tile_tokens);
             if (leader) {
                 const uint32_t full = smem_addr(&b.q_full[t]);
                 const uint32_t dst = smem_base + t * C::kTileBytes;
                 mbar_arrive_expect_tx(full, q_row_bytes * (u.quad ? 4 * a.q_quad_tokens : a.q_box_tokens));
+                const CUtensorMap *map = u.quad ? mq_quad : mq;
+                const uint32_t end = dst + (u.quad ? 4 * kQuadRows * 128 : 1);
+#pragma unroll 1
+                for (uint32_t at = dst; at < end; at += kQuadRows * 128) {
 #pragma unroll
-                for (int c = 0; c < C::kChunks; ++c) {
-                    if (!u.quad) {
-                        tma_load_4d(dst + c * kChunkBytes, mq, full, 64 * c, 0, head, token);
-                        continue;
-                    }
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        tma_load_4d(dst + c * kChunkBytes + k * kQuadRows * 128, mq_quad, full, 64 * c, 0,
-                                    head, token);
+                    for (int c = 0; c < C::kChunks; ++c)
+                        tma_load_4d(at + c * kChunkBytes, map, full, 64 * c, 0, head, token);
                 }
             }
-            last_q[t] = q_phase[t];
-            q_phase[t] ^= 1;
+            q_used |= 1u << t;
+            q_bits ^= 1u << t;
         }
         for (int j = u.j0; ok && j < u.j1; ++j) {
             const int p0 = (j * kBN) >> shift;
@@ -612,7 +631,7 @@ __device__ void run_load(const PagedArgs &a, Bars &b, uint32_t smem_base, const 
 #pragma unroll
             for (int i = 0; i < 8; ++i)
                 page[i] = __shfl_sync(0xffffffffu, entry, min(p0 - held + i, 31));
-#pragma unroll
+#pragma unroll 1
             for (int which = 0; which < 2; ++which, ++pos) {
                 const uint32_t stage = pos % C::kStages;
                 ok = ok && warp_wait(b.kv_empty[stage], ((pos / C::kStages) & 1) ^ 1, abort);
@@ -620,6 +639,7 @@ __device__ void run_load(const PagedArgs &a, Bars &b, uint32_t smem_base, const 
                     break;
                 const uint32_t full = smem_addr(&b.kv_full[stage]);
                 const uint32_t dst = smem_base + (2 + stage) * C::kTileBytes;
+                const CUtensorMap *map = which == 0 ? mk : mv;
                 if (leader) {
                     mbar_arrive_expect_tx(full, count * box_rows * 128u * C::kChunks);
 #pragma unroll
@@ -628,8 +648,8 @@ __device__ void run_load(const PagedArgs &a, Bars &b, uint32_t smem_base, const 
                             break;
 #pragma unroll
                         for (int c = 0; c < C::kChunks; ++c)
-                            tma_load_4d(dst + c * kChunkBytes + i * box_rows * 128, which == 0 ? mk : mv, full,
-                                        64 * c, slot, head, page[i]);
+                            tma_load_4d(dst + c * kChunkBytes + i * box_rows * 128, map, full, 64 * c, slot,
+                                        head, page[i]);
                     }
                 }
             }
@@ -648,8 +668,8 @@ __device__ void run_load(const PagedArgs &a, Bars &b, uint32_t smem_base, const 
             mbar_wait(smem_addr(&b.kv_full[q % C::kStages]), (q / C::kStages) & 1, kWaitLimitNs / 8,
                       nullptr);
         for (int t = 0; t < 2; ++t)
-            if (last_q[t] >= 0)
-                mbar_wait(smem_addr(&b.q_full[t]), last_q[t], kWaitLimitNs / 8, nullptr);
+            if ((q_used >> t) & 1u)
+                mbar_wait(smem_addr(&b.q_full[t]), ((q_bits >> t) & 1u) ^ 1u, kWaitLimitNs / 8, nullptr);
     }
 }
 
