@@ -54,7 +54,7 @@
 // and combine_paged_kernel merges them in slot order.  Ranges depend only on
 // the lengths and the SM count, so equal calls give equal bits.
 //
-// Code size.  Every role is code of its own, 138 KB in all at d = 64, and what
+// Code size.  Every role is code of its own, 133 KB in all at d = 64, and what
 // the warps of a batch with units of several kinds run at a time does not fit
 // the instruction caches: a CTA of quad units beside one of pairs took up to
 // 1.5 times as long as beside its like.  So what does not stand in an inner
@@ -487,7 +487,7 @@ __device__ __forceinline__ void record_failure(const PagedArgs &a, Bars &b, uint
 // Waits by a whole warp; the outcome is uniform.  Few instructions, as there are
 // some sixty of them (see Code size): 45 each, and the producer's copies unrolled
 // throughout, made the kernel 150 KB, and the ragged d = 64 batch took 74 us
-// instead of 62.
+// instead of 61.
 __device__ __forceinline__ uint32_t timer_lo()
 {
     uint32_t t;
@@ -1111,22 +1111,19 @@ __device__ __forceinline__ float softmax_quarter(float sl2, uint32_t t_s, int w,
 template <int D> __device__ __forceinline__ void rescale_o(uint32_t t_o, float alpha)
 {
     const uint64_t alpha2 = f2_pack(alpha, alpha);
-    uint32_t o[D / 32][32];
-#pragma unroll
-    for (int c = 0; c < D / 32; ++c)
-        tmem_ld32(t_o + c * 32, o[c]);
-    tmem_wait_ld();
-#pragma unroll
-    for (int c = 0; c < D / 32; ++c) {
+#pragma unroll 1
+    for (int c = 0; c < D; c += 32) {
+        uint32_t o[32];
+        tmem_ld32(t_o + c, o);
+        tmem_wait_ld();
 #pragma unroll
         for (int i = 0; i < 32; i += 2) {
             float x, y;
-            f2_unpack(f2_mul(f2_pack(__uint_as_float(o[c][i]), __uint_as_float(o[c][i + 1])), alpha2),
-                      x, y);
-            o[c][i] = __float_as_uint(x);
-            o[c][i + 1] = __float_as_uint(y);
+            f2_unpack(f2_mul(f2_pack(__uint_as_float(o[i]), __uint_as_float(o[i + 1])), alpha2), x, y);
+            o[i] = __float_as_uint(x);
+            o[i + 1] = __float_as_uint(y);
         }
-        tmem_st32(t_o + c * 32, o[c]);
+        tmem_st32(t_o + c, o);
     }
 }
 
@@ -1142,6 +1139,7 @@ __device__ __forceinline__ void stage_flush(const uint8_t *stage, int lane, bool
 {
     __syncwarp();
     const int g = half ? lane % 4 : lane % 8, step = half ? 8 : 4;
+#pragma unroll 2
     for (int r0 = 0; r0 < 32; r0 += step) {
         const int row = r0 + (half ? lane / 4 : lane / 8);
         const uint4 x = reinterpret_cast<const uint4 *>(stage + row * 128)[g ^ (row & 7)];
