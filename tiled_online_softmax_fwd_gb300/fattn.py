@@ -573,11 +573,17 @@ def _call(entry, dev, stream, *args):
         _check(st, entry)
 
 
+@functools.lru_cache(maxsize=None)
+def _device(dev):
+    # Given an index, torch makes a device of it in every call: 1.3 us.
+    return torch.device("cuda", dev)
+
+
 def _empty(shape, dtype, dev, stream):
     """A new tensor of the call's stream: memory that is freed while the call
     still runs there is then reused only behind it."""
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=dev)
+        return torch.empty(shape, dtype=dtype, device=_device(dev))
     if not isinstance(stream, torch.cuda.Stream):
         handle = _stream_handle(stream, dev)
         stream = (torch.cuda.ExternalStream(handle, device=dev) if handle
