@@ -54,7 +54,7 @@
 // and combine_paged_kernel merges them in slot order.  Ranges depend only on
 // the lengths and the SM count, so equal calls give equal bits.
 //
-// Code size.  Every role is code of its own, 133 KB in all at d = 64, and what
+// Code size.  Every role is code of its own, 127 KB in all at d = 64, and what
 // the warps of a batch with units of several kinds run at a time does not fit
 // the instruction caches: a CTA of quad units beside one of pairs took up to
 // 1.5 times as long as beside its like.  So what does not stand in an inner
@@ -94,7 +94,9 @@ constexpr uint32_t kStageBytes = 4096 + 128;
 // quad unit took 4800 cycles and 1300 a key tile, another single tile 5800 and
 // 1600, a pair of tiles 8300 and 2100; at d = 128 (bf16) 5800 and 2700, 9800 and
 // 2700, 9800 and 3600.  With one cost for all, the slowest CTA of such a batch
-// took 1.8 times the mean.
+// took 1.8 times the mean; with these 1.1 to 1.3 times.  The waits and copies
+// have become shorter since (4200 and 1300, 4400 and 1600, 6100 and 2100 at d =
+// 64), but costs fitted to that were no better over 24 such batches.
 enum UnitKind { kQuad, kSingle, kPair };
 struct Costs {
     int unit[3], key[3];
@@ -115,8 +117,9 @@ template <int D> __device__ __forceinline__ constexpr Costs costs_of()
                      : Costs{{2190, 3730, 3740}, {8, 8, 11}};
 }
 // A CTA's share of the work is at least a quad unit of this many keys: below,
-// the merge costs more than the shorter ranges save.
-constexpr int kMinShareKeys = 2 * kBN;
+// the merge costs more than the shorter ranges save.  With 256 four decodes of
+// 150 to 1100 keys took 16.7 us, with 128 15.2.
+constexpr int kMinShareKeys = kBN;
 
 template <int D, bool kF16> struct Cfg {
     static constexpr int kChunks = (D + 63) / 64;
@@ -484,17 +487,17 @@ __device__ __forceinline__ void record_failure(const PagedArgs &a, Bars &b, uint
     *reinterpret_cast<volatile int *>(&b.abort) = 1;
 }
 
-// Waits by a whole warp; the outcome is uniform.  Few instructions, as there are
-// some sixty of them (see Code size): 45 each, and the producer's copies unrolled
-// throughout, made the kernel 150 KB, and the ragged d = 64 batch took 74 us
-// instead of 61.
 __device__ __forceinline__ uint32_t timer_lo()
 {
     uint32_t t;
     asm volatile("mov.u32 %0, %%globaltimer_lo;" : "=r"(t));
     return t;
 }
-__device__ __forceinline__ bool warp_wait(uint64_t &bar, uint32_t parity, const volatile int *abort)
+// Waits for a phase: false when the time is up or another role has given up.
+// Few instructions, as there are some sixty of them (see Code size): 45 each, and
+// the producer's copies unrolled throughout, made the kernel 150 KB, and the
+// ragged d = 64 batch took 74 us instead of 62.
+__device__ __forceinline__ bool lane_wait(uint64_t &bar, uint32_t parity, const volatile int *abort)
 {
     const uint32_t at = smem_addr(&bar);
     bool ok = mbar_try_wait(at, parity);
@@ -505,7 +508,12 @@ __device__ __forceinline__ bool warp_wait(uint64_t &bar, uint32_t parity, const 
             ok = mbar_try_wait(at, parity);
         } while (!ok && *abort == 0 && timer_lo() - t0 < static_cast<uint32_t>(kWaitLimitNs));
     }
-    return __all_sync(0xffffffffu, ok);
+    return ok;
+}
+// The same by a whole warp; the outcome is uniform.
+__device__ __forceinline__ bool warp_wait(uint64_t &bar, uint32_t parity, const volatile int *abort)
+{
+    return __all_sync(0xffffffffu, lane_wait(bar, parity, abort));
 }
 
 // The producer's end of the pieces: waits for a free place, writes, signals.
@@ -778,72 +786,73 @@ __device__ __forceinline__ void issue_pv(uint32_t tmem_d, uint32_t tmem_p, uint3
                  kk > 0 || accumulate ? 1u : 0u);
 }
 
+// Run by one lane: no votes after the waits and no branches around each product
+// (127 KB of code instead of 133, 1.2 % over 24 ragged batches).
 template <int D, bool kF16>
 __device__ void run_mma(const PagedArgs &a, Bars &b, uint32_t smem_base, uint32_t tmem)
 {
     using C = Cfg<D, kF16>;
     const volatile int *abort = &b.abort;
-    const bool leader = elect_one();
+    const int lane = threadIdx.x & 31;
+    bool ok = true;
+    auto uniform = [&](int x) { return __shfl_sync(1u << lane, x, lane); };  // as its namesake
+    auto receive = [&](uint32_t k) {
+        ok = ok && lane_wait(b.piece_full[k % kPieces], (k / kPieces) & 1, abort);
+        return ok && b.pieces[k % kPieces].h >= 0;
+    };
+    auto give_back = [&](uint32_t k) { mbar_arrive(smem_addr(&b.piece_empty[k % kPieces])); };
     // Phases, a bit each (an array indexed by a variable would live in memory):
     // Q buffers, P halves and O by warpgroup, V by stage.
     uint32_t q_bits = 0, p_bits = 0, ph_bits = 0, oe_bits = 0, vr_bits = 0;
     uint32_t pos = 0;
-    bool ok = true;
     auto bit = [](uint32_t bits, int i) { return (bits >> i) & 1u; };
     auto stage_of = [&](uint32_t at) { return at % C::kStages; };
     auto kv_smem = [&](uint32_t at) { return smem_base + (2 + stage_of(at)) * C::kTileBytes; };
     auto k_wait = [&](uint32_t at) {
-        return warp_wait(b.kv_full[stage_of(at)], (at / C::kStages) & 1, abort);
+        return lane_wait(b.kv_full[stage_of(at)], (at / C::kStages) & 1, abort);
     };
     auto v_wait = [&](uint32_t at, bool whole) {
         if (kF16 && whole)
             return k_wait(at);
         const uint32_t st = stage_of(at);
-        const bool r = warp_wait(b.v_ready[st], bit(vr_bits, st), abort);
+        const bool r = lane_wait(b.v_ready[st], bit(vr_bits, st), abort);
         vr_bits ^= 1u << st;
         return r;
     };
     auto q_wait = [&](int buf) {
-        const bool r = warp_wait(b.q_full[buf], bit(q_bits, buf), abort);
+        const bool r = lane_wait(b.q_full[buf], bit(q_bits, buf), abort);
         q_bits ^= 1u << buf;
         return r;
     };
-    auto commit = [&](uint64_t &bar) {
-        if (leader)
-            mma_commit(smem_addr(&bar));
-    };
+    auto commit = [&](uint64_t &bar) { mma_commit(smem_addr(&bar)); };
     // P V of one key tile into warpgroup t's accumulator; where a warp writes
     // a whole row of P, the keys in two halves: the first as soon as it is written.
     auto pv = [&](int t, uint32_t at_v, bool first, bool halves) {
         const uint32_t col_s = tmem + t * 128, col_o = tmem + C::kColO0 + t * D;
         const uint32_t v = kv_smem(at_v);
         if (first) {  // overwrites O: the last unit's has to be read
-            if (!warp_wait(b.o_empty[t], bit(oe_bits, t) ^ 1, abort))
+            if (!lane_wait(b.o_empty[t], bit(oe_bits, t) ^ 1, abort))
                 return false;
             oe_bits ^= 1u << t;
         }
         if (halves) {
-            if (!warp_wait(b.p_half[t], bit(ph_bits, t), abort))
+            if (!lane_wait(b.p_half[t], bit(ph_bits, t), abort))
                 return false;
             ph_bits ^= 1u << t;
             tc_fence_after();
-            if (leader)
-                issue_pv<D, 0, kBN / 32>(col_o, col_s, v, !first);
+            issue_pv<D, 0, kBN / 32>(col_o, col_s, v, !first);
         }
-        if (!warp_wait(b.p_full[t], bit(p_bits, t), abort))
+        if (!lane_wait(b.p_full[t], bit(p_bits, t), abort))
             return false;
         p_bits ^= 1u << t;
         tc_fence_after();
-        if (leader) {
-            if (!halves)
-                issue_pv<D, 0, kBN / 32>(col_o, col_s, v, !first);
-            issue_pv<D, kBN / 32, kBN / 16>(col_o, col_s, v, true);
-        }
+        if (!halves)
+            issue_pv<D, 0, kBN / 32>(col_o, col_s, v, !first);
+        issue_pv<D, kBN / 32, kBN / 16>(col_o, col_s, v, true);
         return true;
     };
     auto s_product = [&](int t, int q_tile, uint32_t at_k) {
-        if (leader)
-            issue_s<D, kF16>(tmem + t * 128, smem_base + q_tile * C::kTileBytes, kv_smem(at_k));
+        issue_s<D, kF16>(tmem + t * 128, smem_base + q_tile * C::kTileBytes, kv_smem(at_k));
         commit(b.s_full[t]);
     };
 
@@ -866,10 +875,10 @@ __device__ void run_mma(const PagedArgs &a, Bars &b, uint32_t smem_base, uint32_
     };
     uint32_t turn = 0;  // key tiles of single-tile units so far: tile g is warpgroup g % 2's
     uint32_t k = 0;
-    while (receive(b, k, ok)) {
+    while (receive(k)) {
         Unit u = read(k);
         if (u.n == 0) {
-            give_back(b, k++);
+            give_back(k++);
             continue;
         }
         if (u.alt) {
@@ -889,7 +898,7 @@ __device__ void run_mma(const PagedArgs &a, Bars &b, uint32_t smem_base, uint32_
                     // place to publish it in.
                     if (ks + 1 - k >= kPieces - 1)
                         return;
-                    open = receive(b, ks + 1, ok);
+                    open = receive(ks + 1);
                     if (!open)
                         return;
                     us = read(++ks);
@@ -932,7 +941,7 @@ __device__ void run_mma(const PagedArgs &a, Bars &b, uint32_t smem_base, uint32_
                 }
                 if (!ok)
                     break;
-                give_back(b, k++);
+                give_back(k++);
                 if (ks < k)
                     next_s();
                 if (!ok || ks < k || (ks == k && !us.alt))
@@ -941,7 +950,7 @@ __device__ void run_mma(const PagedArgs &a, Bars &b, uint32_t smem_base, uint32_
             }
             continue;
         }
-        give_back(b, k++);
+        give_back(k++);
         const int n = u.n;
         const uint32_t base = uniform(pos);  // K_(j0+i) at base + 2i, V_(j0+i) at base + 2i + 1
         pos = base + 2 * n;
@@ -986,7 +995,7 @@ __device__ void run_mma(const PagedArgs &a, Bars &b, uint32_t smem_base, uint32_
                 commit(b.kv_empty[stage_of(at_k)]);
         }
     }
-    if (!ok && leader)
+    if (!ok)
         record_failure(a, b, kRoleMma);
     commit(b.drain);
     mbar_wait(smem_addr(&b.drain), 0, kWaitLimitNs, nullptr);
@@ -1620,8 +1629,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         run_softmax<D, kF16>(a, b, tmem, warp / 4);
     else if (warp == kWarpLoad)
         run_load<D, kF16>(a, b, smem_base, &mq, &mq_quad, &mk, &mv);
-    else if (warp == kWarpMma)
-        run_mma<D, kF16>(a, b, smem_base, tmem);
+    else if (warp == kWarpMma) {
+        if (elect_one())
+            run_mma<D, kF16>(a, b, smem_base, tmem);
+        __syncwarp();
+    }
     else
         run_convert<D, kF16>(a, b, smem, warp - kWarpConv);
     // Here, not at the start: merge CTAs waiting on the SMs that finish first cost
