@@ -482,7 +482,7 @@ fattn_status_t fattn_kv_append(const void *k, const void *v, void *k_cache, void
  *   o   = sum_j softmax_j( scale * q . k_j ) v_j        over keys j < L, with
  *   lse = log( sum_j exp( scale * q . k_j ) )           causal: j <= L - n + i
  *
- *   q, o      : 16-bit [T][Hq][d], element strides (token, head)
+ *   q, o      : 16-bit [T][Hq][d], element strides (token, head), T < 2^31 - 256
  *   lse       : fp32 [T][Hq], contiguous
  *   d         : 64, 96 or 128;  Hq a multiple of Hk, Hq / Hk <= 128
  *   max_q     : at least the new tokens of every sequence (it sizes the

@@ -218,6 +218,11 @@ def test_paged_attention_refusals(lib, kw, expect):
     assert paged(lib, **kw) == expect
 
 
+def test_paged_attention_token_indexes_stay_in_32_bits(lib):
+    assert paged(lib, T=(1 << 31) - 1) == UNSUPPORTED
+    assert paged(lib, T=(1 << 31) - 256) == UNSUPPORTED
+
+
 def test_workspace_sizes_of_bad_arguments_are_zero(lib):
     for args in ((0, 1, 64, 1), (4, 3, 64, 1), (4, 2, 80, 1), (4, 2, 64, 0), (-1, 1, 64, 1)):
         assert lib.attn_fwd_paged_workspace_size(*args) == 0

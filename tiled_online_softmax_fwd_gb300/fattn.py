@@ -489,6 +489,7 @@ def row_sum(x, out=None, stream=None):
 # devices is kept by those values (a plan); their memory is never looked at.
 _HALF = {torch.bfloat16: 0, torch.float16: 1}
 _Tensor, _raw_stream = torch.Tensor, torch._C._cuda_getCurrentRawStream
+_current_device = torch._C._cuda_getDevice
 _plans = {}
 _MAX_PLANS = 4096
 
@@ -564,7 +565,7 @@ def _call(entry, dev, stream, *args):
     """Call an entry point whose last argument is the stream, with device `dev` current."""
     f = getattr(_lib or load(), entry)
     handle = _raw_stream(dev) if stream is None else _stream_handle(stream, dev)
-    if torch.cuda.current_device() == dev:
+    if _current_device() == dev:
         st = f(*args, handle)
     else:
         with torch.cuda.device(dev):
