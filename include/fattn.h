@@ -494,7 +494,8 @@ fattn_status_t fattn_kv_append(const void *k, const void *v, void *k_cache, void
  *               ignored on entry, undefined on exit; calls that share one must
  *               not overlap on the device
  *
- * A row that sees no key gets o = 0 and lse = -inf.  Rows of o and lse from
+ * A row that sees no key gets o = 0 and lse = -inf, one with a NaN or +inf
+ * among its scores NaN in both (a score of -inf counts for nothing).  Rows of o and lse from
  * cu_q[B] on are left as they were.  Cache slots and table entries behind a
  * sequence's last key may hold anything, NaN included.  A list value out of
  * range (cu_q out of order or past T, more than max_q new tokens, kv_len

@@ -1317,12 +1317,14 @@ __device__ __forceinline__ bool write_quad(const PagedArgs &a, Bars &b, const Pi
 #pragma unroll
     for (int k = 0; k < 4; ++k)
         sum += ml[k].y * ex2(ml[k].x - mm);
-    const float f = sum > 0.f ? ex2(m - mm) / sum : 0.f;
+    // Only a sum of zero means no key: a NaN or infinite score makes it NaN,
+    // which goes on into o and lse (and the merge).
+    const float f = sum == 0.f ? 0.f : ex2(m - mm) / sum;
     w0 *= f;
     w1 *= f;
     const long long first = static_cast<long long>(u.s.q0) + u.tile[0] * a.tile_tokens;
     if (warp == 0 && lane < rows) {
-        const float lse2 = sum > 0.f ? mm + log2f(sum) : -INFINITY;
+        const float lse2 = sum == 0.f ? -INFINITY : mm + log2f(sum);
         const int tok = row_token(a, lane);
         if (whole)
             a.lse[(first + tok) * a.Hk * a.G + u.h * a.G + lane - tok * a.G] = lse2 * kLn2;
@@ -1547,8 +1549,9 @@ __device__ void run_softmax(const PagedArgs &a, Bars &b, uint32_t tmem, int t)
                 if (r < u.rows[t])
                     a.ws_l[static_cast<long long>(u.slot) * a.slot_rows + t * kBM + r] = -INFINITY;
             } else {
-                const float inv = l > 0.f ? 1.f / l : 0.f;
-                const float lse2 = l > 0.f ? m + log2f(l) : -INFINITY;
+                // l = 0: no key; NaN (a NaN or infinite score) goes on.
+                const float inv = l == 0.f ? 0.f : 1.f / l;
+                const float lse2 = l == 0.f ? -INFINITY : m + log2f(l);
                 write_rows<D, kF16>(a, u, t, warp * 32, t_o(t), t_o(t ^ 1), two, w0 * inv, w1 * inv,
                                     lse2, nt > 0, stages(t) + warp * kStageBytes);
             }
@@ -1771,7 +1774,7 @@ __global__ void __launch_bounds__(128) combine_paged_kernel(const PagedArgs a, i
         const int row = row0 + i, r = row % kBM, tok = row_token(a, r);
         const long long token = static_cast<long long>(unit.x) + row / kBM * a.tile_tokens + tok;
         const int head = mine_h * a.G + r - tok * a.G;
-        const float inv = se[i] > 0.f ? 1.f / se[i] : 0.f;
+        const float inv = se[i] == 0.f ? 0.f : 1.f / se[i];  // NaN goes on
         uint16_t *dst = static_cast<uint16_t *>(a.o) + token * a.o_st[0] + head * a.o_st[1] + lane * kCols;
         if constexpr (kCols % 2 == 0) {
 #pragma unroll
@@ -1783,7 +1786,7 @@ __global__ void __launch_bounds__(128) combine_paged_kernel(const PagedArgs a, i
                 dst[j] = static_cast<uint16_t>(pack2<kF16>(acc[i][j] * inv, 0.f) & 0xffffu);
         }
         if (lane == 0)
-            a.lse[token * a.Hk * a.G + head] = se[i] > 0.f ? (mx[i] + log2f(se[i])) * kLn2 : -INFINITY;
+            a.lse[token * a.Hk * a.G + head] = se[i] == 0.f ? -INFINITY : (mx[i] + log2f(se[i])) * kLn2;
     }
 }
 
