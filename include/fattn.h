@@ -459,9 +459,10 @@ fattn_status_t fattn_qk_norm_rope_bwd(const void *dq_out, const void *dk_out, co
  *                    (rot_dim 0: keys are copied)
  * Elements not turned are copied bit for bit.  A token with no valid place
  * (position < 0 or beyond max_pages * page_size or max_pos, a page outside
- * [0, num_pages), cu_q out of order or past T) is skipped and records
- * FATTN_ERR_INDEX (role 8) in the device status word.  Two tokens must not
- * share a place.  T, B or Hk 0 enqueues nothing.  One kernel; takes no
+ * [0, num_pages), a sequence that ends past T) is skipped and records
+ * FATTN_ERR_INDEX (role 8) in the device status word.  So does a cu_q that
+ * does not begin at 0, decreases or goes past T; the tokens that it leaves
+ * without a sequence are skipped.  Two tokens must not share a place.  T, B or Hk 0 enqueues nothing.  One kernel; takes no
  * memory.
  */
 fattn_status_t fattn_kv_append(const void *k, const void *v, void *k_cache, void *v_cache,
@@ -498,7 +499,7 @@ fattn_status_t fattn_kv_append(const void *k, const void *v, void *k_cache, void
  * among its scores NaN in both (a score of -inf counts for nothing).  Rows of o and lse from
  * cu_q[B] on are left as they were.  Cache slots and table entries behind a
  * sequence's last key may hold anything, NaN included.  A list value out of
- * range (cu_q out of order or past T, more than max_q new tokens, kv_len
+ * range (cu_q not from 0, out of order or past T, more than max_q new tokens, kv_len
  * outside 0 .. max_pages * page_size) is brought into range, a page outside
  * [0, num_pages) reads as zeros, and FATTN_ERR_INDEX (role 1) is recorded in
  * the device status word.  |v| >= 65520 in bf16 records FATTN_ERR_RANGE, as

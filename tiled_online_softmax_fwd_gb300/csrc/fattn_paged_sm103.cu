@@ -278,7 +278,7 @@ __device__ void find_start(const PagedArgs &a, const Costs &cost, Bars &b)
         bool bad;
         raw = load_raw(a, i);
         const Seq s = in_range(a, raw, bad);
-        any_bad = any_bad || bad;
+        any_bad = any_bad || bad || (i == 0 && raw.c0 != 0);
         const int tiles = tiles_of(a, s);
         sum += a.Hk * cost_before(a, cost, s, tiles, (tiles + 1) / 2);
     }

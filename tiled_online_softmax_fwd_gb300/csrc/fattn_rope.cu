@@ -571,10 +571,23 @@ __global__ void __launch_bounds__(kReduceCols *kReduceRows)
 }
 
 // ------------------------------------------------------------------ append
+// Whether cu_q is not a list of starts: from 0, none before the one ahead of
+// it, the last within the tokens.  Each thread's share of it.
+__device__ __forceinline__ bool list_is_bad(const int *cu, int B, long long T)
+{
+    bool bad = false;
+    for (int i = threadIdx.x; i <= B; i += kThreads) {
+        const int at = cu[i];
+        bad = bad || (i == 0 ? at != 0 : at < cu[i - 1]) || at > T;
+    }
+    return bad;
+}
+
 // The largest b in [0, B] with cu[b] <= t (-1: none), found by the lanes of a
 // group together: each step cuts the range into kLanes parts, so 256
 // sequences take two dependent loads where halving takes eight.  The number
-// of steps depends on B alone, so the groups of a warp stay together.
+// of steps depends on B alone, so the groups of a warp stay together.  In a
+// list out of order it ends at some entry, or none: list_is_bad reports that.
 template <int kLanes>
 __device__ __forceinline__ int find_sequence(const int *cu, int B, long long t, int v, int base)
 {
@@ -603,6 +616,13 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) kv_append_kernel(const
     using G = Geo<D>;
     constexpr int kBatch = 4;
     const int lane = threadIdx.x & 31, l = lane % G::kLanes, base = lane - l;
+    // The last block looks the list over, beside the others: a search finds no
+    // sequence for some tokens of a list out of order, as for padding.
+    if (blockIdx.x == gridDim.x - 1) {
+        if (list_is_bad(a.cu_q, a.B, a.T))
+            record_index(a.status, kRoleAppend);
+        return;
+    }
     const long long it = static_cast<long long>(blockIdx.x) * kWarps + threadIdx.x / 32;
     if (it >= a.items)
         return;
@@ -763,7 +783,7 @@ cudaError_t kv_append(KvAppendArgs a, int num_sms, cudaStream_t stream)
     a.heads_per_chunk = heads_per_item(2 * blocks, a.H, num_sms);
     a.chunks = (a.H + a.heads_per_chunk - 1) / a.heads_per_chunk;
     a.items = blocks * 2 * a.chunks;
-    const long long grid = (a.items + kWarps - 1) / kWarps;
+    const long long grid = (a.items + kWarps - 1) / kWarps + 1;
     if (grid > 0x7fffffffLL)
         return cudaErrorInvalidConfiguration;
     kv_append_kernel<D, kF16, kInter><<<static_cast<unsigned>(grid), kThreads, 0, stream>>>(a);
