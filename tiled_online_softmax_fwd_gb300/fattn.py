@@ -580,17 +580,18 @@ def _device(dev):
     return torch.device("cuda", dev)
 
 
-def _empty(shape, dtype, dev, stream):
-    """A new tensor of the call's stream: memory that is freed while the call
-    still runs there is then reused only behind it."""
+def _empty(shape, dtype, dev, stream, zero=False):
+    """A new tensor (of zeros, if asked for) of the call's stream: memory that
+    is freed while the call still runs there is then reused only behind it."""
+    make = torch.zeros if zero else torch.empty
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=_device(dev))
+        return make(shape, dtype=dtype, device=_device(dev))
     if not isinstance(stream, torch.cuda.Stream):
         handle = _stream_handle(stream, dev)
         stream = (torch.cuda.ExternalStream(handle, device=dev) if handle
                   else torch.cuda.default_stream(dev))
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=dev)
+        return make(shape, dtype=dtype, device=dev)
 
 
 def rope_table(positions: int, rot_dim: int, theta: float = 10000.0, device="cuda"):
@@ -703,8 +704,9 @@ def qk_norm_rope_bwd(dq_out, dk_out, q, k, wq=None, wk=None, rope=None, position
             raise ValueError("%s must have its tensor's shape" % name)
     dq = _like("dq", dq, q, dtype, dev, stream)
     dk = _like("dk", dk, k, dtype, dev, stream)
-    dwq = None if wq is None else _empty(d, torch.float32, dev, stream)
-    dwk = None if wk is None else _empty(d, torch.float32, dev, stream)
+    # Of a tensor without heads the library takes no notice: its sum is empty.
+    dwq = None if wq is None else _empty(d, torch.float32, dev, stream, zero=sizes[1] == 0)
+    dwk = None if wk is None else _empty(d, torch.float32, dev, stream, zero=sizes[2] == 0)
     if workspace is None and (wq is not None or wk is not None):
         workspace = _empty(qk_norm_rope_bwd_workspace_size(d, dev), torch.uint8, dev, stream)
     _call("fattn_qk_norm_rope_bwd", dev, stream, _ptr(dq_out), _ptr(dk_out), _ptr(q), _ptr(k),
