@@ -11,6 +11,7 @@ from __future__ import annotations
 import ctypes
 import functools
 import math
+import operator
 import os
 import threading
 
@@ -735,13 +736,15 @@ def _device_index(device) -> int:
 
 def qk_norm_rope_bwd_workspace_size(d: int, device=None) -> int:
     """Scratch bytes qk_norm_rope_bwd needs with weights."""
-    return _workspace_bytes("fattn_qk_norm_rope_bwd_workspace_size", _device_index(device), d)
+    return _workspace_bytes("fattn_qk_norm_rope_bwd_workspace_size", _device_index(device),
+                            operator.index(d))
 
 
 def paged_workspace_size(Hq: int, Hk: int, d: int, max_q: int, device=None) -> int:
     """Scratch bytes attn_fwd_paged needs for these heads and at most max_q
     new tokens a sequence."""
-    return _workspace_bytes("attn_fwd_paged_workspace_size", _device_index(device), Hq, Hk, d, max_q)
+    return _workspace_bytes("attn_fwd_paged_workspace_size", _device_index(device),
+                            *map(operator.index, (Hq, Hk, d, max_q)))
 
 
 def _paged_checks(page_table, cu_q, kv_len, k_cache, v_cache, dtype, dev, d):
@@ -839,6 +842,11 @@ def attn_fwd_paged(q, k_cache, v_cache, page_table, cu_q, kv_len, max_q: int,
     tokens' keys already appended; ``max_q`` is at least the new tokens of
     every sequence.  Returns (out [T, Hq, d], lse fp32 [T, Hq]); rows from
     cu_q[B] on are not written."""
+    # Plain numbers: a plan kept by a tensor would not follow its value.
+    if type(max_q) is not int:
+        max_q = operator.index(max_q)
+    if scale is not None and type(scale) is not float:
+        scale = float(scale)
     try:
         key = ("paged", _of(q), _of(k_cache), _of(v_cache), _of(page_table), _of(cu_q), _of(kv_len),
                max_q, bool(causal), scale)
