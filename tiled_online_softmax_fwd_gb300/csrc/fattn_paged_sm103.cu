@@ -125,6 +125,7 @@ template <int D, bool kF16> struct Cfg {
     static constexpr int kChunks = (D + 63) / 64;
     static constexpr uint32_t kTileBytes = kChunks * kChunkBytes;
     static constexpr int kStages = kChunks == 2 ? 4 : 8;
+    static_assert(kStages % 2 == 0, "V is on the odd stages");
     static constexpr uint32_t kStageOffset = (2 + kStages) * kTileBytes;  // epilogue staging
     static constexpr uint32_t kBarsOffset = kStageOffset + 8 * kStageBytes;
     static constexpr uint32_t kColO0 = 256;  // O of warpgroup t at kColO0 + t D
@@ -733,13 +734,21 @@ __device__ void run_convert(const PagedArgs &a, Bars &b, uint8_t *tiles, int cw)
         for (int j = j0; ok && j < j1; ++j, pos += 2) {
             const uint32_t at = pos + 1, stage = at % C::kStages;
             const int valid = L - j * kBN;
-            // Every copy is waited for: a waiter that ran two rounds of the
-            // ring ahead would take an older phase for its own.
+            // Every copy is waited for, and in fp16, whose whole tiles are used
+            // as they land, said to have been: the stage is not filled again
+            // before.  A phase is told by its parity, so a waiter two rounds
+            // of the ring from the copies, on either side, would take another
+            // for its own.
             ok = warp_wait(b.kv_full[stage], (at / C::kStages) & 1, abort);
             if (!ok)
                 break;
-            if (kF16 && valid >= kBN)
-                continue;  // whole fp16 tiles are used as they land
+            if (kF16) {
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(smem_addr(&b.kv_empty[stage]));
+                if (valid >= kBN)
+                    continue;
+            }
             uint4 *tile = reinterpret_cast<uint4 *>(tiles + (2 + stage) * C::kTileBytes);
             if (valid < kBN)
                 fix_v_tile<D, kF16, true>(tile, tid, valid);
@@ -1596,7 +1605,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         for (int s = 0; s < C::kStages; ++s) {
             mbar_init(smem_addr(&b.kv_full[s]), 1);
-            mbar_init(smem_addr(&b.kv_empty[s]), 1);
+            // V stages (odd) in fp16: by both warps that look at V, too.
+            mbar_init(smem_addr(&b.kv_empty[s]), kF16 && s % 2 == 1 ? 3 : 1);
             mbar_init(smem_addr(&b.v_ready[s]), 2);
         }
         for (int k = 0; k < kPieces; ++k) {
