@@ -365,10 +365,26 @@ __device__ void find_start(const PagedArgs &a, const Costs &cost, Bars &b)
 // loop whose trip count comes from memory around it, a coordinate computed
 // from values loaded outside the loop reached the copy without one of its
 // terms (the rows of a later unit were then some other tokens'), although
-// every lane held the right sum.  Shuffled values are read afresh.
+// every lane held the right sum.  Why is not known; shuffled values are read
+// afresh.  So every value of a copy or product that follows from the lists goes
+// through one inside the loop that uses it: tokens, heads, slots, pages and
+// ring positions here, tiles and ring positions in run_mma.
 __device__ __forceinline__ int uniform(int x)
 {
     return __shfl_sync(0xffffffffu, x, 0);
+}
+// The same where one lane runs alone: from `lane`, its own number as elect.sync
+// gave it, which no compiler can tell from another lane's.
+__device__ __forceinline__ int uniform_of(int x, uint32_t lane)
+{
+    return __shfl_sync(1u << lane, x, static_cast<int>(lane));
+}
+// The lane that elect_one picks.
+__device__ __forceinline__ uint32_t elected_lane()
+{
+    uint32_t lane;
+    asm volatile("{\n\t.reg .pred P1;\n\telect.sync %0|P1, 0xffffffff;\n\t}" : "=r"(lane));
+    return lane;
 }
 
 // The pieces of this CTA in order.  The next sequence's list entries are
@@ -635,7 +651,7 @@ __device__ void run_load(const PagedArgs &a, Bars &b, uint32_t smem_base, const 
             if (stray && lane >= p0 - held && lane < p0 - held + count)
                 atomicCAS(a.status, 0u,
                           6u /* FATTN_ERR_INDEX */ | (kRoleLoad << 8) | ((blockIdx.x & 0xffffu) << 16));
-            const int slot = shift < 7 ? 0 : (j * kBN) & ((1 << shift) - 1);
+            const int slot = uniform(shift < 7 ? 0 : (j * kBN) & ((1 << shift) - 1));
             int page[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i)
@@ -798,13 +814,12 @@ __device__ __forceinline__ void issue_pv(uint32_t tmem_d, uint32_t tmem_p, uint3
 // Run by one lane: no votes after the waits and no branches around each product
 // (127 KB of code instead of 133, 1.2 % over 24 ragged batches).
 template <int D, bool kF16>
-__device__ void run_mma(const PagedArgs &a, Bars &b, uint32_t smem_base, uint32_t tmem)
+__device__ void run_mma(const PagedArgs &a, Bars &b, uint32_t smem_base, uint32_t tmem, uint32_t lane)
 {
     using C = Cfg<D, kF16>;
     const volatile int *abort = &b.abort;
-    const int lane = threadIdx.x & 31;
     bool ok = true;
-    auto uniform = [&](int x) { return __shfl_sync(1u << lane, x, lane); };  // as its namesake
+    auto uniform = [&](int x) { return uniform_of(x, lane); };
     auto receive = [&](uint32_t k) {
         ok = ok && lane_wait(b.piece_full[k % kPieces], (k / kPieces) & 1, abort);
         return ok && b.pieces[k % kPieces].h >= 0;
@@ -1643,8 +1658,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     else if (warp == kWarpLoad)
         run_load<D, kF16>(a, b, smem_base, &mq, &mq_quad, &mk, &mv);
     else if (warp == kWarpMma) {
+        const uint32_t leader = elected_lane();
         if (elect_one())
-            run_mma<D, kF16>(a, b, smem_base, tmem);
+            run_mma<D, kF16>(a, b, smem_base, tmem, leader);
         __syncwarp();
     }
     else
