@@ -489,8 +489,10 @@ def row_sum(x, out=None, stream=None):
 # that a call checks and derives from its tensors' shapes, strides, types and
 # devices is kept by those values (a plan); their memory is never looked at.
 _HALF = {torch.bfloat16: 0, torch.float16: 1}
-_Tensor, _raw_stream = torch.Tensor, torch._C._cuda_getCurrentRawStream
-_current_device = torch._C._cuda_getDevice
+_Tensor = torch.Tensor
+# A torch without CUDA has none of these; its tensors do not pass the checks.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", None)
 _plans = {}
 _MAX_PLANS = 4096
 
