@@ -84,7 +84,8 @@ typedef enum fattn_status {
  * 0.0156 and P's rounding moves O across a rounding midpoint.  Both operands
  * of a tensor-core product share one type, so V is rounded to fp16 (on
  * chip, or by a pre-pass: see fattn_set_v_conversion; the bits are the
- * same).  That is exact for |v| < 65520; a V element of larger
+ * same).  That is exact for 2^-17 <= |v| < 65520; a smaller element is
+ * rounded to a multiple of 2^-24, and a V element of larger
  * magnitude becomes infinite in the product.  Any output row that comes out
  * non-finite -- from such a V element, or from non-finite inputs -- makes
  * the kernel record FATTN_ERR_RANGE in the device status word (those rows
@@ -457,12 +458,14 @@ fattn_status_t fattn_qk_norm_rope_bwd(const void *dq_out, const void *dk_out, co
  *                    slot); the two may be windows of one buffer
  *   rope, rot_dim, max_pos, interleaved, dtype, d: as fattn_qk_norm_rope
  *                    (rot_dim 0: keys are copied)
- * Elements not turned are copied bit for bit.  A token with no valid place
- * (position < 0 or beyond max_pages * page_size or max_pos, a page outside
- * [0, num_pages), a sequence that ends past T) is skipped and records
- * FATTN_ERR_INDEX (role 8) in the device status word.  So does a cu_q that
- * does not begin at 0, decreases or goes past T; the tokens that it leaves
- * without a sequence are skipped.  Two tokens must not share a place.  T, B or Hk 0 enqueues nothing.  One kernel; takes no
+ * Elements not turned are copied bit for bit; turned ones are formed in fp32
+ * and rounded once (in fp16 one that the turn takes past 65504 becomes
+ * infinite).  A token with no valid place (position < 0 or beyond max_pages *
+ * page_size or max_pos, a page outside [0, num_pages), a sequence that ends
+ * past T) is skipped and records FATTN_ERR_INDEX (role 8) in the device status
+ * word.  So does a cu_q that does not begin at 0, decreases or goes past T;
+ * the tokens that it leaves without a sequence are skipped.  Two tokens must
+ * not share a place.  T, B or Hk 0 enqueues nothing.  One kernel; takes no
  * memory.
  */
 fattn_status_t fattn_kv_append(const void *k, const void *v, void *k_cache, void *v_cache,
@@ -489,22 +492,29 @@ fattn_status_t fattn_kv_append(const void *k, const void *v, void *k_cache, void
  *   max_q     : at least the new tokens of every sequence (it sizes the
  *               workspace; of a sequence with more, at most max_q rows are
  *               written, and they are not meaningful)
- *   dtype     : 0 = bf16 (P and V rounded to fp16, as attn_fwd), 1 = fp16
+ *   dtype     : 0 = bf16 (P and V rounded to fp16, as attn_fwd), 1 = fp16 (P
+ *               rounded to fp16)
  *   workspace : device, 16-byte aligned, attn_fwd_paged_workspace_size(...)
  *               bytes on the current device (0 on invalid arguments); contents
  *               ignored on entry, undefined on exit; calls that share one must
  *               not overlap on the device
  *
  * A row that sees no key gets o = 0 and lse = -inf, one with a NaN or +inf
- * among its scores NaN in both (a score of -inf counts for nothing).  Rows of o and lse from
- * cu_q[B] on are left as they were.  Cache slots and table entries behind a
- * sequence's last key may hold anything, NaN included.  A list value out of
- * range (cu_q not from 0, out of order or past T, more than max_q new tokens, kv_len
- * outside 0 .. max_pages * page_size) is brought into range, a page outside
- * [0, num_pages) reads as zeros, and FATTN_ERR_INDEX (role 1) is recorded in
- * the device status word.  |v| >= 65520 in bf16 records FATTN_ERR_RANGE, as
- * in attn_fwd.  Two kernels are enqueued; the lists are read when they run.
- * Equal calls give equal bits.  Errors as for attn_fwd_strided.
+ * among its scores NaN in both (a score of -inf counts for nothing).  Rows of
+ * o and lse from cu_q[B] on are left as they were.  Cache slots and table
+ * entries behind a sequence's last key may hold anything, NaN included.  Keys
+ * that the mask hides from a row may be NaN or infinite; their values may not:
+ * a product with P = 0 is taken, so a value that is not finite (in bf16, also
+ * |v| >= 65520) makes its column NaN in rows of its sequence that do not see
+ * it yet, as in the dense calls.  In bf16 an output row that is not finite
+ * records FATTN_ERR_RANGE, as in attn_fwd; fp16 does not look for one.
+ *
+ * A list value out of range (cu_q not from 0, out of order or past T, more
+ * than max_q new tokens, kv_len outside 0 .. max_pages * page_size) is brought
+ * into range, a page outside [0, num_pages) reads as zeros, and
+ * FATTN_ERR_INDEX (role 1) is recorded in the device status word.  Two kernels
+ * are enqueued; the lists are read when they run.  Equal calls give equal
+ * bits.  Errors as for attn_fwd_strided.
  */
 size_t attn_fwd_paged_workspace_size(int Hq, int Hk, int d, int max_q);
 fattn_status_t attn_fwd_paged(const void *q, const void *k_cache, const void *v_cache,

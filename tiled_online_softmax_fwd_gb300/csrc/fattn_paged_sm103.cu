@@ -19,8 +19,8 @@
 // Bound.  With few new tokens the cache's bytes (HBM): 16 sequences of 16K to
 // 32K keys, one token each, 32 query and 8 key heads, d = 128, bf16, take 247 us
 // at 6.6 TB/s.  With many, the tensor cores and exponentials: two chunks of 2K
-// tokens against 16K keys run at 1360 to 1430 TFLOP/s (1490 in fp16, without the
-// conversion of V).  Short sequences are bound by a unit's start and end (see
+// tokens against 16K keys run at 1330 to 1480 TFLOP/s under the power cap (fp16,
+// without the conversion of V, 1420 to 1470).  Short sequences are bound by a unit's start and end (see
 // Costs).  One persistent CTA a SM serves all:
 //   warps 0-7    two softmax warpgroups (thread = row)
 //   warp 8       walks the CTA's work, publishes each piece of it to the other
@@ -96,7 +96,12 @@ constexpr uint32_t kStageBytes = 4096 + 128;
 // 2700, 9800 and 3600.  With one cost for all, the slowest CTA of such a batch
 // took 1.8 times the mean; with these 1.1 to 1.3 times.  The waits and copies
 // have become shorter since (4200 and 1300, 4400 and 1600, 6100 and 2100 at d =
-// 64), but costs fitted to that were no better over 24 such batches.
+// 64), but costs fitted to that were no better over 24 such batches.  At d = 96
+// equal whole units of 1 to 16 key tiles, keys from L2, take in these measures
+// 2490, 3570 and 3860 and 8, 7.8 and 10.4 a key (a quad unit's tile: 0.96 us);
+// the numbers here are within 15 % of that.  One set serves both types: fp16,
+// without the conversion of V, takes 4 % less a tile of a quad unit and 8 to
+// 15 % less of a pair, which moves the ratios by less than the fit is good for.
 enum UnitKind { kQuad, kSingle, kPair };
 struct Costs {
     int unit[3], key[3];
