@@ -373,7 +373,8 @@ __device__ void find_start(const PagedArgs &a, const Costs &cost, Bars &b)
 // every lane held the right sum.  Why is not known; shuffled values are read
 // afresh.  So every value of a copy or product that follows from the lists goes
 // through one inside the loop that uses it: tokens, heads, slots, pages and
-// ring positions here, tiles and ring positions in run_mma.
+// ring positions here, tiles and ring positions in run_mma.  The shuffles and the
+// votes of the waits also bring the warp's lanes together before each copy.
 __device__ __forceinline__ int uniform(int x)
 {
     return __shfl_sync(0xffffffffu, x, 0);
