@@ -526,6 +526,151 @@ fattn_status_t attn_fwd_paged(const void *q, const void *k_cache, const void *v_
                               float scale, int causal, int dtype, void *workspace,
                               size_t workspace_bytes, struct CUstream_st *stream);
 
+/*
+ * attn_fwd_tree -- attention of trees of drafted tokens over the paged cache:
+ * attn_fwd_paged, with a mask among a sequence's new tokens in place of the
+ * causal one.  New token i of sequence b (n new tokens, L = kv_len[b] keys)
+ * sees every key j < L - n, and of the new tokens' those with a bit in its mask:
+ *
+ *   key L - n + t is seen  <=>  bit t % 32 of mask[row][t / 32] is set,  t < n
+ *
+ * with row = cu_q[b] + i; itself, too, only with its own bit.  Any mask will
+ * do: one row a token, so a token may see some that come after it.
+ *
+ *   mask       : device, [T][mask_words] words mask_stride words apart (4-byte
+ *                aligned), 32 * mask_words at least max_q; bits from n on are
+ *                not looked at
+ *
+ * All else is as for attn_fwd_paged, its workspace size included: a row that
+ * sees no key gets o = 0 and lse = -inf, and a hidden key may be NaN or infinite
+ * but its value may not.
+ *
+ * fattn_tree_mask -- the masks and positions of trees given by each token's
+ * parent: a token sees itself and every token on the way to its root.
+ *   parents    : int32 [T]: for token i of its sequence a number below i in the
+ *                same sequence, or -1: it follows the keys before the new tokens
+ *   mask       : [T][mask_words], contiguous
+ *   positions  : int32 [T]: kv_len[b] - n + the tokens between it and its root,
+ *                the root included (0 for a root), for fattn_qk_norm_rope with
+ *                one sequence of T tokens
+ * A parent outside -1 .. i - 1 is taken for -1, a list value out of range is
+ * brought into it, tokens of a sequence from 32 * mask_words on are skipped;
+ * each records FATTN_ERR_INDEX (role 9) in the device status word.  Rows from
+ * cu_q[B] on are left as they were.  mask_words at most 2^24, T < 2^31 - 256.
+ * One kernel; takes no memory.
+ */
+fattn_status_t attn_fwd_tree(const void *q, const void *k_cache, const void *v_cache,
+                             const int *page_table, const int *cu_q, const int *kv_len,
+                             const unsigned *mask, void *o, float *lse, int T, int B, int Hq, int Hk,
+                             int d, int num_pages, int page_size, int max_pages,
+                             long long page_table_stride, int max_q, int mask_words,
+                             long long mask_stride, const long long *q_strides,
+                             const long long *k_cache_strides, const long long *v_cache_strides,
+                             const long long *o_strides, float scale, int dtype, void *workspace,
+                             size_t workspace_bytes, struct CUstream_st *stream);
+fattn_status_t fattn_tree_mask(const int *parents, const int *cu_q, const int *kv_len, unsigned *mask,
+                               int *positions, int T, int B, int mask_words,
+                               struct CUstream_st *stream);
+
+/*
+ * fattn_kv_keep -- after a step with drafted tokens, keeps of each sequence's n
+ * new tokens only those listed, in that order: for j = 0 .. m - 1, m =
+ * kept_len[b], the keys and values of position L - n + kept[b][j] move to
+ * position L - n + j, and kv_len_out[b] = L - n + m.  The slots behind keep what
+ * they held; the table's entries stay with the sequence.
+ *   kept, kept_len : int32 [B] rows of max_kept numbers (kept_stride apart), and
+ *                    [B]: the numbers are ascending, 0 .. n - 1; those from m on
+ *                    are not looked at
+ *   kv_len_out     : int32 [B], kv_len itself or apart from every list
+ * Rows are moved bit for bit (either 16-bit type).  A sequence whose lists are
+ * not so (kept out of order or range, m above n or max_kept, n < 0 or above L, a
+ * length beyond the table, a page outside [0, num_pages) where something moves)
+ * is left as it was, with kv_len_out = kv_len, and records FATTN_ERR_INDEX (role
+ * 10) in the device status word.  Two sequences must not share a page that holds
+ * new tokens.  d in {64, 96, 128, 256}.  One kernel; takes no memory.
+ *
+ * fattn_kv_fork -- forks, grows and frees sequences between steps: sequence b
+ * goes on as a copy of what sequence p = parents[b] was, with room for n_b =
+ * cu_q[b+1] - cu_q[b] new tokens:
+ *
+ *   kv_len_out[b] = kv_len[p] + n_b,   page_table_out[b] = page_table[p], ...
+ *
+ *   parents     : int32 [B], or NULL: parents[b] = b.  -1: an empty sequence
+ *                 (kv_len 0); its own pages, if no other goes on with them, are
+ *                 free.  A sequence may have any number of children.
+ *   cu_q        : int32 [B+1] as in fattn_kv_append, or NULL: no new tokens
+ *   page_refs   : int32 [num_pages]: how many table entries name each page (and
+ *                 anything else the caller counts); 0: the page is free
+ *   page_table_out, kv_len_out, page_refs_out: the state afterwards; each may be
+ *                 its input (a table with the same strides), else is apart from
+ *                 all inputs.  Every entry of them is written.
+ *
+ * The pages below kv_len[p] / page_size (rounded down) are shared by all of p's
+ * children.  The rest of p's entries -- a page that is partly filled, spare pages
+ * behind it -- go to one: p itself where parents[p] = p, else the first child.
+ * Every other child gets a page of its own for the partly filled one, with its
+ * filled slots copied in both caches.  Then each sequence gets pages for what it
+ * lacks up to ceil(kv_len_out / page_size): the lowest free pages (those whose
+ * count is 0 when all entries have changed hands), in the order of sequences and
+ * columns.  Other entries of page_table_out are -1, which in a table stands for
+ * no page.
+ *
+ * Out of range (a parent is taken for b itself, kv_len brought to 0 .. max_pages
+ * * page_size, n_b to what the table has room for and at least 0, an entry
+ * outside [-1, num_pages) for -1, a partly filled page that is not there for an
+ * unfilled one) or out of free pages (the entries become -1): FATTN_ERR_INDEX
+ * (role 11) is recorded.  The lists are read when the kernels run, so a captured
+ * graph follows them.  Equal calls give equal bits.  workspace: device, 16-byte
+ * aligned, fattn_kv_fork_workspace_size(...) bytes; contents ignored on entry,
+ * undefined on exit; calls that share one must not overlap on the device.  Two
+ * kernels (one without parents).
+ */
+fattn_status_t fattn_kv_keep(void *k_cache, void *v_cache, const int *page_table, const int *cu_q,
+                             const int *kv_len, const int *kept, const int *kept_len, int *kv_len_out,
+                             int B, int Hk, int d, int num_pages, int page_size, int max_pages,
+                             long long page_table_stride, int max_kept, long long kept_stride,
+                             const long long *k_cache_strides, const long long *v_cache_strides,
+                             struct CUstream_st *stream);
+size_t fattn_kv_fork_workspace_size(int B, int max_pages, int num_pages);
+fattn_status_t fattn_kv_fork(void *k_cache, void *v_cache, const int *page_table, const int *kv_len,
+                             const int *page_refs, const int *parents, const int *cu_q,
+                             int *page_table_out, int *kv_len_out, int *page_refs_out, int B, int Hk,
+                             int d, int num_pages, int page_size, int max_pages,
+                             long long page_table_stride, long long page_table_out_stride,
+                             const long long *k_cache_strides, const long long *v_cache_strides,
+                             void *workspace, size_t workspace_bytes, struct CUstream_st *stream);
+
+/*
+ * attn_fwd_cross -- attention of batched queries to keys of another length, an
+ * encoder's states, padded to Nk and grouped by heads: for query i of head h of
+ * sequence b, with key head h / (Hq / Hk) and L = kv_len[b] keys
+ *
+ *   o   = sum_{j < L} softmax_j( scale * q . k_j ) v_j
+ *   lse = log( sum_{j < L} exp( scale * q . k_j ) )
+ *
+ *   q, o      : 16-bit [B][Hq][Nq][d], k, v: [B][Hk][Nk][d], element strides
+ *               (batch, head, row), last dimension contiguous; Nq and Nk are
+ *               independent, from a single row on
+ *   kv_len    : int32 [B] on the device, or NULL: Nk for all.  A length outside
+ *               0 .. Nk is brought into it and records FATTN_ERR_INDEX (role 1)
+ *   lse       : fp32 [B][Hq][Nq], contiguous
+ *   d         : 64, 96 or 128;  Hq a multiple of Hk, Hq / Hk <= 128;  B*Nq and
+ *               Nk below 2^31 - 256
+ *   dtype     : 0 = bf16 (P and V rounded to fp16), 1 = fp16 (P rounded to fp16)
+ *   workspace : as in attn_fwd_paged, attn_fwd_cross_workspace_size(...) bytes
+ *
+ * Rows of k and v behind a sequence's last key may hold anything, NaN included.
+ * A sequence without keys gives o = 0 and lse = -inf.  Two kernels are enqueued;
+ * equal calls give equal bits.  Range reports and errors as for attn_fwd_paged.
+ */
+size_t attn_fwd_cross_workspace_size(int Hq, int Hk, int Nq, int d);
+fattn_status_t attn_fwd_cross(const void *q, const void *k, const void *v, const int *kv_len, void *o,
+                              float *lse, int B, int Hq, int Hk, int Nq, int Nk, int d,
+                              const long long *q_strides, const long long *k_strides,
+                              const long long *v_strides, const long long *o_strides, float scale,
+                              int dtype, void *workspace, size_t workspace_bytes,
+                              struct CUstream_st *stream);
+
 /* Human-readable name of a status code (static storage, never NULL). */
 const char *fattn_status_string(fattn_status_t status);
 
@@ -541,7 +686,8 @@ int fattn_last_cuda_error(void);
  * otherwise the first code recorded: bits 0..7 = FATTN_ERR_TIMEOUT,
  * FATTN_ERR_RANGE or FATTN_ERR_INDEX, bits 8..15 = the role that reported it
  * (1 load, 2 mma, 3 softmax, 4 epilogue, 5 self-test, 6 V conversion,
- * 7 norm and rotation, 8 cache append), bits 16..31 = the CTA
+ * 7 norm and rotation, 8 cache append, 9 tree masks, 10 kept tokens,
+ * 11 forked sequences, 12 cross attention's gradients), bits 16..31 = the CTA
  * index.  Returns the status in bits 0..7 (FATTN_ERR_TIMEOUT,
  * FATTN_ERR_RANGE or FATTN_ERR_INDEX) if *status is nonzero, FATTN_OK if it
  * is zero, or FATTN_ERR_INVALID_ARG / FATTN_ERR_CUDA.

@@ -1089,6 +1089,180 @@ fattn_status_t make_row_map(PFN_cuTensorMapEncodeTiled_v12000 encode, CUtensorMa
     return FATTN_OK;
 }
 
+// Attention of new tokens over a paged cache: causal or full, or (tree) with the
+// masks among the new tokens that are given.
+fattn_status_t paged_call(bool tree, const void *q, const void *k_cache, const void *v_cache,
+                          const int *page_table, const int *cu_q, const int *kv_len,
+                          const unsigned *mask, long long mask_stride, int mask_words, void *o,
+                          float *lse, int T, int B, int Hq, int Hk, int d, int num_pages,
+                          int page_size, int max_pages, long long page_table_stride, int max_q,
+                          const long long *q_strides, const long long *k_cache_strides,
+                          const long long *v_cache_strides, const long long *o_strides, float scale,
+                          int causal, int dtype, void *workspace, size_t workspace_bytes,
+                          cudaStream_t stream)
+{
+    if (T < 0 || (dtype != 0 && dtype != 1) || (causal != 0 && causal != 1))
+        return FATTN_ERR_INVALID_ARG;
+    if (T > 0x7fffffff - 256)  // token indexes are 32-bit, tiles included
+        return FATTN_ERR_UNSUPPORTED;
+    if (!(scale > 0.f) || !isfinite(scale))
+        return FATTN_ERR_INVALID_ARG;
+    if (tree && (mask_words < 1 || static_cast<long long>(mask_words) * 32 < max_q))
+        return FATTN_ERR_INVALID_ARG;
+    const Paging g{page_table, cu_q, kv_len, B, num_pages, page_size, max_pages, page_table_stride};
+    fattn_status_t s = check_heads(Hq, Hk, d, max_q);
+    if (s != FATTN_OK || (s = check_paging(g)) != FATTN_OK)
+        return s;
+    if (T == 0 || B == 0 || Hq == 0)
+        return FATTN_OK;
+    if ((s = check_lists(g)) != FATTN_OK)
+        return s;
+    if (!q_strides || !k_cache_strides || !v_cache_strides || !o_strides || num_pages == 0 || !lse ||
+        reinterpret_cast<uintptr_t>(lse) % 4 != 0)
+        return FATTN_ERR_INVALID_ARG;
+    if (tree && (!mask || reinterpret_cast<uintptr_t>(mask) % 4 != 0 ||
+                 (T > 1 && (mask_stride < mask_words || mask_stride > (1LL << 38)))))
+        return FATTN_ERR_INVALID_ARG;
+    const Rows rows[4] = {rows_of(q, q_strides, 2, T, Hq, 1, d),
+                          rows_of(k_cache, k_cache_strides, 3, num_pages, Hk, page_size, d),
+                          rows_of(v_cache, v_cache_strides, 3, num_pages, Hk, page_size, d),
+                          rows_of(o, o_strides, 2, T, Hq, 1, d)};
+    for (const Rows &r : rows)
+        if ((s = check_rows(r)) != FATTN_OK)
+            return s;
+    // The tensor map steps from one key head's query heads to the next's.
+    if (Hq > 1 && rows[0].st[1] > (1LL << 38) / (Hq / Hk))
+        return FATTN_ERR_UNSUPPORTED;
+    const Rows &out = rows[3];
+    const size_t lse_bytes = static_cast<size_t>(T) * Hq * 4;
+    const size_t lists[4] = {table_bytes(g), (static_cast<size_t>(B) + 1) * 4, static_cast<size_t>(B) * 4,
+                             tree ? static_cast<size_t>(mask_stride * (T - 1) + mask_words) * 4 : 0};
+    const void *list[4] = {page_table, cu_q, kv_len, mask};
+    if (!distinct(out) || !apart(out, lse, lse_bytes))
+        return FATTN_ERR_INVALID_ARG;
+    for (int i = 0; i < 4; ++i)
+        if ((i < 3 && (!apart(out, rows[i]) || !apart(rows[i], lse, lse_bytes))) ||
+            !apart(out, list[i], lists[i]) || (lists[i] > 0 && overlap(lse, lse_bytes, list[i], lists[i])))
+            return FATTN_ERR_INVALID_ARG;
+    int dev = 0;
+    DeviceInfo info;
+    const void *bufs[] = {q, k_cache, v_cache, o, lse, max_pages ? page_table : nullptr, cu_q, kv_len,
+                          workspace, tree ? mask : nullptr};
+    if ((s = check_buffers(bufs, &dev, &info)) != FATTN_OK)
+        return s;
+    const PagedWs ws = paged_ws(Hq, Hk, d, max_q, info.num_sms);
+    if (!workspace || !aligned16(workspace) || workspace_bytes < ws.bytes ||
+        overlap(workspace, ws.bytes, lse, lse_bytes))
+        return FATTN_ERR_INVALID_ARG;
+    for (int i = 0; i < 4; ++i)
+        if (!apart(rows[i], workspace, ws.bytes) ||
+            (lists[i] > 0 && overlap(workspace, ws.bytes, list[i], lists[i])))
+            return FATTN_ERR_INVALID_ARG;
+    PFN_cuTensorMapEncodeTiled_v12000 encode;
+    if ((s = get_encoder(&encode)) != FATTN_OK)
+        return s;
+    fattn::PagedArgs a = {};
+    if ((s = status_word(&a.status)) != FATTN_OK)
+        return s;
+    const int G = Hq / Hk;
+    const int box_tokens = std::min(max_q, ws.tile_tokens), quad_tokens = std::min(max_q, 32 / G);
+    const unsigned box_slots = static_cast<unsigned>(page_size < 128 ? page_size : 128);
+    fattn::PagedMaps maps;
+    const long long q_ext[3] = {G, Hk, T}, q_st[3] = {rows[0].st[1], rows[0].st[1] * G, rows[0].st[0]};
+    if ((s = make_row_map(encode, &maps.q, q, d, q_ext, q_st,
+                          {static_cast<unsigned>(G), 1u, static_cast<unsigned>(box_tokens)},
+                          dtype == 1)) != FATTN_OK)
+        return s;
+    maps.q_quad = maps.q;
+    if (quad_tokens > 0 && quad_tokens != box_tokens &&
+        (s = make_row_map(encode, &maps.q_quad, q, d, q_ext, q_st,
+                          {static_cast<unsigned>(G), 1u, static_cast<unsigned>(quad_tokens)},
+                          dtype == 1)) != FATTN_OK)
+        return s;
+    CUtensorMap *cache[2] = {&maps.k, &maps.v};
+    for (int i = 0; i < 2; ++i) {
+        const Rows &r = rows[1 + i];
+        if ((s = make_row_map(encode, cache[i], r.p, d, {page_size, Hk, num_pages},
+                              {r.st[2], r.st[1], r.st[0]}, {box_slots, 1u, 1u}, dtype == 1)) != FATTN_OK)
+            return s;
+    }
+    uint8_t *base = static_cast<uint8_t *>(workspace);
+    a.o = o;
+    a.lse = lse;
+    a.starts = reinterpret_cast<int4 *>(base);
+    a.ws_l = reinterpret_cast<float *>(base + ws.l);
+    a.ws_o = reinterpret_cast<float *>(base + ws.o);
+    a.page_table = page_table;
+    a.cu_q = cu_q;
+    a.kv_len = kv_len;
+    a.o_st[0] = out.st[0];
+    a.o_st[1] = out.st[1];
+    a.table_stride = page_table_stride;
+    a.T = T;
+    a.B = B;
+    a.Hk = Hk;
+    a.G = G;
+    a.d = d;
+    a.f16 = dtype;
+    a.causal = causal;
+    a.max_q = max_q;
+    a.num_pages = num_pages;
+    a.page_shift = __builtin_ctz(static_cast<unsigned>(page_size));
+    a.max_keys = max_pages * page_size;
+    a.tile_tokens = ws.tile_tokens;
+    a.q_box_tokens = box_tokens;
+    a.q_quad_tokens = quad_tokens;
+    a.slot_rows = ws.slot_rows;
+    a.g_inverse = (65536u + G - 1) / G;
+    a.sl2 = scale * 1.4426950408889634f;
+    a.mask = mask;
+    a.mask_stride = mask_stride;
+    a.mask_words = mask_words;
+    const cudaError_t e = tree ? fattn::launch_tree(a, maps, info.num_sms, stream)
+                               : fattn::launch_paged(a, maps, info.num_sms, stream);
+    return e == cudaSuccess ? FATTN_OK : cuda_fail(e);
+}
+
+// Tensor map of batched queries as the cross attention reads them: (d, G, Hk,
+// Nq, B), box (64, G, 1, tokens, 1).
+fattn_status_t make_query_map(PFN_cuTensorMapEncodeTiled_v12000 encode, CUtensorMap *m, const Rows &q,
+                              int G, int tokens, bool f16)
+{
+    const long long Hk = q.ext[1] / G;
+    const long long ext[4] = {G, Hk, q.ext[2], q.ext[0]};
+    const long long st[4] = {q.st[1], q.st[1] * G, q.st[2], q.st[0]};
+    cuuint64_t dims[5] = {static_cast<cuuint64_t>(q.d)}, strides[4];
+    const cuuint32_t box[5] = {64, static_cast<cuuint32_t>(G), 1, static_cast<cuuint32_t>(tokens), 1};
+    const cuuint32_t elem_strides[5] = {1, 1, 1, 1, 1};
+    for (int i = 0; i < 4; ++i) {
+        dims[i + 1] = static_cast<cuuint64_t>(ext[i]);
+        strides[i] = static_cast<cuuint64_t>(ext[i] > 1 ? st[i] : q.d) * 2;
+    }
+    const CUresult r = encode(m, f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+                              5, const_cast<void *>(q.p), dims, strides, box, elem_strides,
+                              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) {
+        t_last_cuda_error = static_cast<int>(r);
+        return FATTN_ERR_CUDA;
+    }
+    return FATTN_OK;
+}
+
+// What the cross attention calls check alike.
+fattn_status_t check_cross(int B, int Hq, int Hk, int Nq, int Nk, int d, float scale, int dtype)
+{
+    if (B < 0 || Nq < 0 || Nk < 0 || (dtype != 0 && dtype != 1) || !(scale > 0.f) || !isfinite(scale))
+        return FATTN_ERR_INVALID_ARG;
+    const fattn_status_t s = check_heads(Hq, Hk, d, 1);
+    if (s != FATTN_OK)
+        return s;
+    // Rows of queries and keys are counted in 32 bits, tiles included.
+    if (static_cast<long long>(B) * Nq > 0x7fffffffLL - 256 || Nk > 0x7fffffff - 256)
+        return FATTN_ERR_UNSUPPORTED;
+    return FATTN_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -1632,57 +1806,342 @@ fattn_status_t attn_fwd_paged(const void *q, const void *k_cache, const void *v_
                               float scale, int causal, int dtype, void *workspace,
                               size_t workspace_bytes, struct CUstream_st *stream)
 {
-    if (T < 0 || (dtype != 0 && dtype != 1) || (causal != 0 && causal != 1))
+    return paged_call(false, q, k_cache, v_cache, page_table, cu_q, kv_len, nullptr, 0, 0, o, lse, T, B,
+                      Hq, Hk, d, num_pages, page_size, max_pages, page_table_stride, max_q, q_strides,
+                      k_cache_strides, v_cache_strides, o_strides, scale, causal, dtype, workspace,
+                      workspace_bytes, stream);
+}
+
+fattn_status_t attn_fwd_tree(const void *q, const void *k_cache, const void *v_cache,
+                             const int *page_table, const int *cu_q, const int *kv_len,
+                             const unsigned *mask, void *o, float *lse, int T, int B, int Hq, int Hk,
+                             int d, int num_pages, int page_size, int max_pages,
+                             long long page_table_stride, int max_q, int mask_words,
+                             long long mask_stride, const long long *q_strides,
+                             const long long *k_cache_strides, const long long *v_cache_strides,
+                             const long long *o_strides, float scale, int dtype, void *workspace,
+                             size_t workspace_bytes, struct CUstream_st *stream)
+{
+    return paged_call(true, q, k_cache, v_cache, page_table, cu_q, kv_len, mask, mask_stride, mask_words,
+                      o, lse, T, B, Hq, Hk, d, num_pages, page_size, max_pages, page_table_stride, max_q,
+                      q_strides, k_cache_strides, v_cache_strides, o_strides, scale, 0, dtype, workspace,
+                      workspace_bytes, stream);
+}
+
+fattn_status_t fattn_tree_mask(const int *parents, const int *cu_q, const int *kv_len, unsigned *mask,
+                               int *positions, int T, int B, int mask_words,
+                               struct CUstream_st *stream)
+{
+    if (T < 0 || B < 0 || mask_words < 1)
         return FATTN_ERR_INVALID_ARG;
-    if (T > 0x7fffffff - 256)  // token indexes are 32-bit, tiles included
+    // Tokens of a sequence are counted in 32 bits.
+    if (T > 0x7fffffff - 256 || mask_words > (1 << 24))
         return FATTN_ERR_UNSUPPORTED;
-    if (!(scale > 0.f) || !isfinite(scale))
-        return FATTN_ERR_INVALID_ARG;
-    const Paging g{page_table, cu_q, kv_len, B, num_pages, page_size, max_pages, page_table_stride};
-    fattn_status_t s = check_heads(Hq, Hk, d, max_q);
-    if (s != FATTN_OK || (s = check_paging(g)) != FATTN_OK)
-        return s;
-    if (T == 0 || B == 0 || Hq == 0)
+    if (T == 0 || B == 0)
         return FATTN_OK;
-    if ((s = check_lists(g)) != FATTN_OK)
-        return s;
-    if (!q_strides || !k_cache_strides || !v_cache_strides || !o_strides || num_pages == 0 || !lse ||
-        reinterpret_cast<uintptr_t>(lse) % 4 != 0)
-        return FATTN_ERR_INVALID_ARG;
-    const Rows rows[4] = {rows_of(q, q_strides, 2, T, Hq, 1, d),
-                          rows_of(k_cache, k_cache_strides, 3, num_pages, Hk, page_size, d),
-                          rows_of(v_cache, v_cache_strides, 3, num_pages, Hk, page_size, d),
-                          rows_of(o, o_strides, 2, T, Hq, 1, d)};
-    for (const Rows &r : rows)
-        if ((s = check_rows(r)) != FATTN_OK)
-            return s;
-    // The tensor map steps from one key head's query heads to the next's.
-    if (Hq > 1 && rows[0].st[1] > (1LL << 38) / (Hq / Hk))
-        return FATTN_ERR_UNSUPPORTED;
-    const Rows &out = rows[3];
-    const size_t lse_bytes = static_cast<size_t>(T) * Hq * 4;
-    const size_t lists[3] = {table_bytes(g), (static_cast<size_t>(B) + 1) * 4, static_cast<size_t>(B) * 4};
-    const void *list[3] = {page_table, cu_q, kv_len};
-    if (!distinct(out) || !apart(out, lse, lse_bytes))
-        return FATTN_ERR_INVALID_ARG;
-    for (int i = 0; i < 3; ++i)
-        if (!apart(out, rows[i]) || !apart(rows[i], lse, lse_bytes) || !apart(out, list[i], lists[i]) ||
-            (lists[i] > 0 && overlap(lse, lse_bytes, list[i], lists[i])))
+    const void *bufs[5] = {parents, cu_q, kv_len, mask, positions};
+    const size_t bytes[5] = {static_cast<size_t>(T) * 4, (static_cast<size_t>(B) + 1) * 4,
+                             static_cast<size_t>(B) * 4, static_cast<size_t>(T) * mask_words * 4,
+                             static_cast<size_t>(T) * 4};
+    for (int i = 0; i < 5; ++i) {
+        if (!bufs[i] || reinterpret_cast<uintptr_t>(bufs[i]) % 4 != 0)
             return FATTN_ERR_INVALID_ARG;
+        for (int j = 0; j < i; ++j)  // an output (the last two) against all others
+            if (i >= 3 && overlap(bufs[i], bytes[i], bufs[j], bytes[j]))
+                return FATTN_ERR_INVALID_ARG;
+    }
     int dev = 0;
     DeviceInfo info;
-    const void *bufs[] = {q, k_cache, v_cache, o, lse, max_pages ? page_table : nullptr, cu_q, kv_len,
-                          workspace};
+    fattn_status_t s = check_buffers(bufs, &dev, &info);
+    fattn::TreeMaskArgs a{parents, cu_q, kv_len, mask, positions, nullptr, T, B, mask_words};
+    if (s != FATTN_OK || (s = status_word(&a.status)) != FATTN_OK)
+        return s;
+    const cudaError_t e = fattn::launch_tree_mask(a, stream);
+    return e == cudaSuccess ? FATTN_OK : cuda_fail(e);
+}
+
+fattn_status_t fattn_kv_keep(void *k_cache, void *v_cache, const int *page_table, const int *cu_q,
+                             const int *kv_len, const int *kept, const int *kept_len, int *kv_len_out,
+                             int B, int Hk, int d, int num_pages, int page_size, int max_pages,
+                             long long page_table_stride, int max_kept, long long kept_stride,
+                             const long long *k_cache_strides, const long long *v_cache_strides,
+                             struct CUstream_st *stream)
+{
+    if (Hk < 0 || max_kept < 0)
+        return FATTN_ERR_INVALID_ARG;
+    if (!head_dim_ok(d))
+        return FATTN_ERR_UNSUPPORTED;
+    const Paging g{page_table, cu_q, kv_len, B, num_pages, page_size, max_pages, page_table_stride};
+    fattn_status_t s = check_paging(g);
+    if (s != FATTN_OK || B == 0)
+        return s;
+    // Blocks are counted in 32 bits, up to eight a sequence.
+    if (B > 0x7fffffff / 8)
+        return FATTN_ERR_UNSUPPORTED;
+    if ((s = check_lists(g)) != FATTN_OK)
+        return s;
+    if ((!kept && max_kept > 0) || !kept_len || !kv_len_out || (B > 1 && max_kept > 0 &&
+        (kept_stride < max_kept || kept_stride > (1LL << 38))))
+        return FATTN_ERR_INVALID_ARG;
+    const size_t b4 = static_cast<size_t>(B) * 4;
+    const size_t kept_bytes =
+        max_kept > 0 ? static_cast<size_t>(kept_stride * (B - 1) + max_kept) * 4 : 0;
+    const void *in[5] = {kept, kept_len, page_table, cu_q, kv_len};
+    const size_t in_bytes[5] = {kept_bytes, b4, table_bytes(g), b4 + 4, b4};
+    if (reinterpret_cast<uintptr_t>(kept) % 4 != 0 || reinterpret_cast<uintptr_t>(kept_len) % 4 != 0 ||
+        reinterpret_cast<uintptr_t>(kv_len_out) % 4 != 0)
+        return FATTN_ERR_INVALID_ARG;
+    for (int i = 0; i < 5; ++i)
+        if (!(i == 4 && kv_len_out == kv_len) && in_bytes[i] > 0 && overlap(kv_len_out, b4, in[i], in_bytes[i]))
+            return FATTN_ERR_INVALID_ARG;
+    const bool rows = Hk > 0 && num_pages > 0;
+    Rows out[2] = {};
+    if (rows) {
+        if (!k_cache_strides || !v_cache_strides)
+            return FATTN_ERR_INVALID_ARG;
+        out[0] = rows_of(k_cache, k_cache_strides, 3, num_pages, Hk, page_size, d);
+        out[1] = rows_of(v_cache, v_cache_strides, 3, num_pages, Hk, page_size, d);
+        for (const Rows &r : out) {
+            if ((s = check_rows(r)) != FATTN_OK)
+                return s;
+            if (!distinct(r) || !apart(r, kv_len_out, b4))
+                return FATTN_ERR_INVALID_ARG;
+            for (int i = 0; i < 5; ++i)
+                if (!apart(r, in[i], in_bytes[i]))
+                    return FATTN_ERR_INVALID_ARG;
+        }
+        if (!apart(out[0], out[1]))
+            return FATTN_ERR_INVALID_ARG;
+    }
+    int dev = 0;
+    DeviceInfo info;
+    const void *bufs[] = {rows ? k_cache : nullptr, rows ? v_cache : nullptr,
+                          max_pages ? page_table : nullptr, cu_q, kv_len, max_kept ? kept : nullptr,
+                          kept_len, kv_len_out};
     if ((s = check_buffers(bufs, &dev, &info)) != FATTN_OK)
         return s;
-    const PagedWs ws = paged_ws(Hq, Hk, d, max_q, info.num_sms);
-    if (!workspace || !aligned16(workspace) || workspace_bytes < ws.bytes ||
-        overlap(workspace, ws.bytes, lse, lse_bytes))
+    fattn::KvKeepArgs a = {};
+    if ((s = status_word(&a.status)) != FATTN_OK)
+        return s;
+    a.k_cache = k_cache;
+    a.v_cache = v_cache;
+    a.page_table = page_table;
+    a.cu_q = cu_q;
+    a.kv_len = kv_len;
+    a.kept = kept;
+    a.kept_len = kept_len;
+    a.kv_len_out = kv_len_out;
+    copy_strides(a.kc_st, out[0]);
+    copy_strides(a.vc_st, out[1]);
+    a.table_stride = page_table_stride;
+    a.kept_stride = kept_stride;
+    a.B = B;
+    a.H = rows ? Hk : 0;
+    a.d = d;
+    a.num_pages = num_pages;
+    a.page_shift = __builtin_ctz(static_cast<unsigned>(page_size));
+    a.max_pages = max_pages;
+    a.max_kept = max_kept;
+    const cudaError_t e = fattn::launch_kv_keep(a, stream);
+    return e == cudaSuccess ? FATTN_OK : cuda_fail(e);
+}
+
+// Workspace of a fork: per-sequence lists, counts, the free list and copies of
+// a table and lengths that are overwritten in place.
+struct ForkWs {
+    size_t copies, lacks, counts, lens, list, stage, bytes;
+};
+static ForkWs fork_ws(int B, int max_pages, int num_pages)
+{
+    ForkWs w;
+    w.copies = align_up(static_cast<size_t>(B) * 4, kWsAlign);  // first before it
+    w.lacks = align_up(w.copies + static_cast<size_t>(B) * 16, kWsAlign);
+    w.lens = align_up(w.lacks + static_cast<size_t>(B) * 4, kWsAlign);
+    w.counts = align_up(w.lens + static_cast<size_t>(B) * 4, kWsAlign);
+    w.list = align_up(w.counts + fattn::kForkRanks * 4, kWsAlign);
+    w.stage = align_up(w.list + static_cast<size_t>(num_pages) * 4, kWsAlign);
+    w.bytes = w.stage + static_cast<size_t>(B) * max_pages * 4;
+    return w;
+}
+
+size_t fattn_kv_fork_workspace_size(int B, int max_pages, int num_pages)
+{
+    return B < 1 || max_pages < 0 || num_pages < 0 ? 0 : fork_ws(B, max_pages, num_pages).bytes;
+}
+
+fattn_status_t fattn_kv_fork(void *k_cache, void *v_cache, const int *page_table, const int *kv_len,
+                             const int *page_refs, const int *parents, const int *cu_q,
+                             int *page_table_out, int *kv_len_out, int *page_refs_out, int B, int Hk,
+                             int d, int num_pages, int page_size, int max_pages,
+                             long long page_table_stride, long long page_table_out_stride,
+                             const long long *k_cache_strides, const long long *v_cache_strides,
+                             void *workspace, size_t workspace_bytes, struct CUstream_st *stream)
+{
+    if (Hk < 0)
         return FATTN_ERR_INVALID_ARG;
-    for (int i = 0; i < 4; ++i)
-        if (!apart(rows[i], workspace, ws.bytes) ||
-            (i < 3 && lists[i] > 0 && overlap(workspace, ws.bytes, list[i], lists[i])))
+    if (!head_dim_ok(d))
+        return FATTN_ERR_UNSUPPORTED;
+    // cu_q may be absent: kv_len stands for it in the checks of the lists.
+    const Paging g{page_table, cu_q ? cu_q : kv_len, kv_len, B, num_pages, page_size, max_pages,
+                   page_table_stride};
+    fattn_status_t s = check_paging(g);
+    if (s != FATTN_OK || B == 0)
+        return s;
+    if (B > 0x7fffffff / 16)  // counted in 32 bits, rounded up to warps
+        return FATTN_ERR_UNSUPPORTED;
+    if ((s = check_lists(g)) != FATTN_OK)
+        return s;
+    const Paging go{page_table_out, kv_len, kv_len, B, num_pages, page_size, max_pages,
+                    page_table_out_stride};
+    if ((s = check_lists(go)) != FATTN_OK)
+        return s;
+    if (!kv_len_out || (num_pages > 0 && (!page_refs || !page_refs_out)))
+        return FATTN_ERR_INVALID_ARG;
+    const size_t b4 = static_cast<size_t>(B) * 4, p4 = static_cast<size_t>(num_pages) * 4;
+    const ForkWs ws = fork_ws(B, max_pages, num_pages);
+    if (!workspace || !aligned16(workspace) || workspace_bytes < ws.bytes)
+        return FATTN_ERR_INVALID_ARG;
+    const void *in[5] = {page_table, kv_len, page_refs, parents, cu_q};
+    const size_t in_bytes[5] = {table_bytes(g), b4, p4, parents ? b4 : 0, cu_q ? b4 + 4 : 0};
+    void *out[4] = {page_table_out, kv_len_out, page_refs_out, workspace};
+    const size_t out_bytes[4] = {table_bytes(go), b4, p4, ws.bytes};
+    for (int i = 0; i < 5; ++i)
+        if (reinterpret_cast<uintptr_t>(in[i]) % 4 != 0)
             return FATTN_ERR_INVALID_ARG;
+    for (int i = 0; i < 4; ++i) {
+        if (out_bytes[i] == 0)
+            continue;
+        if (reinterpret_cast<uintptr_t>(out[i]) % 4 != 0)
+            return FATTN_ERR_INVALID_ARG;
+        for (int j = 0; j < 5; ++j) {
+            // An output may be its own input, a table with the same rows.
+            const bool place = i == j && out[i] == in[j] &&
+                               (i != 0 || B == 1 || page_table_stride == page_table_out_stride);
+            if (!place && in_bytes[j] > 0 && overlap(out[i], out_bytes[i], in[j], in_bytes[j]))
+                return FATTN_ERR_INVALID_ARG;
+        }
+        for (int j = 0; j < i; ++j)
+            if (out_bytes[j] > 0 && overlap(out[i], out_bytes[i], out[j], out_bytes[j]))
+                return FATTN_ERR_INVALID_ARG;
+    }
+    const bool rows = Hk > 0 && num_pages > 0;
+    Rows cache[2] = {};
+    if (rows) {
+        if (!k_cache_strides || !v_cache_strides)
+            return FATTN_ERR_INVALID_ARG;
+        cache[0] = rows_of(k_cache, k_cache_strides, 3, num_pages, Hk, page_size, d);
+        cache[1] = rows_of(v_cache, v_cache_strides, 3, num_pages, Hk, page_size, d);
+        for (const Rows &r : cache) {
+            if ((s = check_rows(r)) != FATTN_OK)
+                return s;
+            if (!distinct(r))
+                return FATTN_ERR_INVALID_ARG;
+            for (int i = 0; i < 5; ++i)
+                if (!apart(r, in[i], in_bytes[i]) || (i < 4 && !apart(r, out[i], out_bytes[i])))
+                    return FATTN_ERR_INVALID_ARG;
+        }
+        if (!apart(cache[0], cache[1]))
+            return FATTN_ERR_INVALID_ARG;
+        // A page's pieces, and the blocks that copy them, are counted in 32 bits.
+        const long long pieces = static_cast<long long>(Hk) * page_size * (d / 8);
+        if (pieces > 0x7fffffffLL - 4096 || 2 * B * (pieces / 1024 + 1) > 0x7fffffffLL)
+            return FATTN_ERR_UNSUPPORTED;
+    }
+    int dev = 0;
+    DeviceInfo info;
+    const void *bufs[] = {rows ? k_cache : nullptr, rows ? v_cache : nullptr,
+                          max_pages ? page_table : nullptr, kv_len, num_pages ? page_refs : nullptr,
+                          parents, cu_q, max_pages ? page_table_out : nullptr, kv_len_out,
+                          num_pages ? page_refs_out : nullptr, workspace};
+    if ((s = check_buffers(bufs, &dev, &info)) != FATTN_OK)
+        return s;
+    fattn::KvForkArgs a = {};
+    if ((s = status_word(&a.status)) != FATTN_OK)
+        return s;
+    uint8_t *base = static_cast<uint8_t *>(workspace);
+    a.k_cache = k_cache;
+    a.v_cache = v_cache;
+    a.page_table = page_table;
+    a.kv_len = kv_len;
+    a.refs = page_refs;
+    a.parents = parents;
+    a.cu_q = cu_q;
+    a.table_out = page_table_out;
+    a.len_out = kv_len_out;
+    a.refs_out = page_refs_out;
+    a.first = reinterpret_cast<int *>(base);
+    a.copies = reinterpret_cast<int4 *>(base + ws.copies);
+    a.lacks = reinterpret_cast<int *>(base + ws.lacks);
+    a.stage_len = reinterpret_cast<int *>(base + ws.lens);
+    a.counts = reinterpret_cast<int *>(base + ws.counts);
+    a.free_list = reinterpret_cast<int *>(base + ws.list);
+    a.stage = reinterpret_cast<int *>(base + ws.stage);
+    copy_strides(a.kc_st, cache[0]);
+    copy_strides(a.vc_st, cache[1]);
+    a.table_stride = page_table_stride;
+    a.table_out_stride = page_table_out_stride;
+    a.staged = page_table_out == page_table || kv_len_out == kv_len;
+    a.B = B;
+    a.H = rows ? Hk : 0;
+    a.d = d;
+    a.num_pages = num_pages;
+    a.page_shift = __builtin_ctz(static_cast<unsigned>(page_size));
+    a.max_pages = max_pages;
+    const cudaError_t e = fattn::launch_kv_fork(a, stream);
+    return e == cudaSuccess ? FATTN_OK : cuda_fail(e);
+}
+
+size_t attn_fwd_cross_workspace_size(int Hq, int Hk, int Nq, int d)
+{
+    return Nq < 1 ? 0 : attn_fwd_paged_workspace_size(Hq, Hk, d, Nq);
+}
+
+fattn_status_t attn_fwd_cross(const void *q, const void *k, const void *v, const int *kv_len, void *o,
+                              float *lse, int B, int Hq, int Hk, int Nq, int Nk, int d,
+                              const long long *q_strides, const long long *k_strides,
+                              const long long *v_strides, const long long *o_strides, float scale,
+                              int dtype, void *workspace, size_t workspace_bytes,
+                              struct CUstream_st *stream)
+{
+    fattn_status_t s = check_cross(B, Hq, Hk, Nq, Nk, d, scale, dtype);
+    if (s != FATTN_OK || B == 0 || Hq == 0 || Nq == 0)
+        return s;
+    if (!q_strides || !o_strides || !lse || reinterpret_cast<uintptr_t>(lse) % 4 != 0 ||
+        reinterpret_cast<uintptr_t>(kv_len) % 4 != 0 || (Nk > 0 && (!k_strides || !v_strides)))
+        return FATTN_ERR_INVALID_ARG;
+    const Rows out = rows_of(o, o_strides, 3, B, Hq, Nq, d), rq = rows_of(q, q_strides, 3, B, Hq, Nq, d);
+    const long long none[3] = {d, d, d};
+    const Rows kv[2] = {rows_of(k, Nk > 0 ? k_strides : none, 3, B, Hk, Nk, d),
+                        rows_of(v, Nk > 0 ? v_strides : none, 3, B, Hk, Nk, d)};
+    const size_t lse_bytes = static_cast<size_t>(B) * Hq * Nq * 4, len_bytes = static_cast<size_t>(B) * 4;
+    if ((s = check_rows(out)) != FATTN_OK || (s = check_rows(rq)) != FATTN_OK)
+        return s;
+    // The tensor map steps from one key head's query heads to the next's.
+    if (Hq > 1 && rq.st[1] > (1LL << 38) / (Hq / Hk))
+        return FATTN_ERR_UNSUPPORTED;
+    if (!distinct(out) || !apart(out, rq) || !apart(out, lse, lse_bytes) || !apart(rq, lse, lse_bytes) ||
+        (kv_len && (!apart(out, kv_len, len_bytes) || overlap(lse, lse_bytes, kv_len, len_bytes))))
+        return FATTN_ERR_INVALID_ARG;
+    for (const Rows &r : kv) {
+        if (Nk == 0)
+            continue;
+        if ((s = check_rows(r)) != FATTN_OK)
+            return s;
+        if (!apart(out, r) || !apart(r, lse, lse_bytes))
+            return FATTN_ERR_INVALID_ARG;
+    }
+    int dev = 0;
+    DeviceInfo info;
+    const void *bufs[] = {q, Nk > 0 ? k : nullptr, Nk > 0 ? v : nullptr, o, lse, kv_len, workspace};
+    if ((s = check_buffers(bufs, &dev, &info)) != FATTN_OK)
+        return s;
+    const PagedWs ws = paged_ws(Hq, Hk, d, Nq, info.num_sms);
+    if (!workspace || !aligned16(workspace) || workspace_bytes < ws.bytes ||
+        overlap(workspace, ws.bytes, lse, lse_bytes) || !apart(out, workspace, ws.bytes) ||
+        !apart(rq, workspace, ws.bytes) ||
+        (kv_len && overlap(workspace, ws.bytes, kv_len, len_bytes)) ||
+        (Nk > 0 && (!apart(kv[0], workspace, ws.bytes) || !apart(kv[1], workspace, ws.bytes))))
+        return FATTN_ERR_INVALID_ARG;
     PFN_cuTensorMapEncodeTiled_v12000 encode;
     if ((s = get_encoder(&encode)) != FATTN_OK)
         return s;
@@ -1690,25 +2149,20 @@ fattn_status_t attn_fwd_paged(const void *q, const void *k_cache, const void *v_
     if ((s = status_word(&a.status)) != FATTN_OK)
         return s;
     const int G = Hq / Hk;
-    const int box_tokens = std::min(max_q, ws.tile_tokens), quad_tokens = std::min(max_q, 32 / G);
-    const unsigned box_slots = static_cast<unsigned>(page_size < 128 ? page_size : 128);
+    const int box_tokens = std::min(Nq, ws.tile_tokens), quad_tokens = std::min(Nq, 32 / G);
     fattn::PagedMaps maps;
-    const long long q_ext[3] = {G, Hk, T}, q_st[3] = {rows[0].st[1], rows[0].st[1] * G, rows[0].st[0]};
-    if ((s = make_row_map(encode, &maps.q, q, d, q_ext, q_st,
-                          {static_cast<unsigned>(G), 1u, static_cast<unsigned>(box_tokens)},
-                          dtype == 1)) != FATTN_OK)
+    if ((s = make_query_map(encode, &maps.q, rq, G, box_tokens, dtype == 1)) != FATTN_OK)
         return s;
     maps.q_quad = maps.q;
     if (quad_tokens > 0 && quad_tokens != box_tokens &&
-        (s = make_row_map(encode, &maps.q_quad, q, d, q_ext, q_st,
-                          {static_cast<unsigned>(G), 1u, static_cast<unsigned>(quad_tokens)},
-                          dtype == 1)) != FATTN_OK)
+        (s = make_query_map(encode, &maps.q_quad, rq, G, quad_tokens, dtype == 1)) != FATTN_OK)
         return s;
-    CUtensorMap *cache[2] = {&maps.k, &maps.v};
+    // Without keys nothing is copied; the maps then stand for q's rows.
+    CUtensorMap *map[2] = {&maps.k, &maps.v};
     for (int i = 0; i < 2; ++i) {
-        const Rows &r = rows[1 + i];
-        if ((s = make_row_map(encode, cache[i], r.p, d, {page_size, Hk, num_pages},
-                              {r.st[2], r.st[1], r.st[0]}, {box_slots, 1u, 1u}, dtype == 1)) != FATTN_OK)
+        const Rows &r = Nk > 0 ? kv[i] : rq;
+        if ((s = make_row_map(encode, map[i], r.p, d, {r.ext[2], r.ext[1], r.ext[0]},
+                              {r.st[2], r.st[1], r.st[0]}, {128u, 1u, 1u}, dtype == 1)) != FATTN_OK)
             return s;
     }
     uint8_t *base = static_cast<uint8_t *>(workspace);
@@ -1717,30 +2171,28 @@ fattn_status_t attn_fwd_paged(const void *q, const void *k_cache, const void *v_
     a.starts = reinterpret_cast<int4 *>(base);
     a.ws_l = reinterpret_cast<float *>(base + ws.l);
     a.ws_o = reinterpret_cast<float *>(base + ws.o);
-    a.page_table = page_table;
-    a.cu_q = cu_q;
     a.kv_len = kv_len;
-    a.o_st[0] = out.st[0];
+    a.o_st[0] = out.st[2];
     a.o_st[1] = out.st[1];
-    a.table_stride = page_table_stride;
-    a.T = T;
+    a.o_batch = out.st[0];
+    a.T = B * Nq;
     a.B = B;
     a.Hk = Hk;
     a.G = G;
     a.d = d;
     a.f16 = dtype;
-    a.causal = causal;
-    a.max_q = max_q;
-    a.num_pages = num_pages;
-    a.page_shift = __builtin_ctz(static_cast<unsigned>(page_size));
-    a.max_keys = max_pages * page_size;
+    a.max_q = Nq;
+    a.Nq = Nq;
+    a.num_pages = B;
+    a.page_shift = 7;  // a tile is copied whole
+    a.max_keys = Nk;
     a.tile_tokens = ws.tile_tokens;
     a.q_box_tokens = box_tokens;
     a.q_quad_tokens = quad_tokens;
     a.slot_rows = ws.slot_rows;
     a.g_inverse = (65536u + G - 1) / G;
     a.sl2 = scale * 1.4426950408889634f;
-    const cudaError_t e = fattn::launch_paged(a, maps, info.num_sms, stream);
+    const cudaError_t e = fattn::launch_cross(a, maps, info.num_sms, stream);
     return e == cudaSuccess ? FATTN_OK : cuda_fail(e);
 }
 

@@ -69,7 +69,11 @@ enum DeviceRole : uint32_t {
     kRoleSelfTest = 5,
     kRoleConvert = 6,
     kRoleRotate = 7,  // norm and rotation: a position outside the table
-    kRoleAppend = 8   // cache append: a page, position or length out of range
+    kRoleAppend = 8,  // cache append: a page, position or length out of range
+    kRoleTree = 9,    // tree masks: a parent or start out of range
+    kRoleKeep = 10,   // kept tokens: an index, page or length out of range
+    kRoleFork = 11,   // forked sequences: an entry out of range, no free page
+    kRoleCross = 12   // cross attention's gradients: a length out of range
 };
 
 // tcgen05 / TMA kernel: one persistent CTA per SM.
@@ -177,6 +181,14 @@ struct PagedArgs {
     int q_quad_tokens;   // tokens of a copy of at most 32 rows (0: G > 32)
     uint32_t g_inverse;  // ceil(2^16 / G)
     float sl2;           // scale * log2(e)
+    // Trees: [T] rows of mask_words words, mask_stride words apart.
+    const unsigned *mask;
+    long long mask_stride;
+    int mask_words;
+    // Cross attention: queries a sequence (T = B Nq, max_q = Nq) and o's batch
+    // stride; kv_len may be null, max_keys is Nk.
+    int Nq;
+    long long o_batch;
 };
 // q: (d, G, Hk, T), box (64, G, 1, q_box_tokens); q_quad: the same tensor, box
 // (64, G, 1, q_quad_tokens) (q's where that is 0); k, v: (d, slot, Hk, page),
@@ -185,5 +197,52 @@ struct PagedMaps {
     CUtensorMap q, q_quad, k, v;
 };
 cudaError_t launch_paged(const PagedArgs &a, const PagedMaps &maps, int num_sms, cudaStream_t stream);
+// The same with masks among the new tokens.
+cudaError_t launch_tree(const PagedArgs &a, const PagedMaps &maps, int num_sms, cudaStream_t stream);
+// Batched queries over contiguous keys: the maps of q are (d, G, Hk, Nq, B),
+// those of k and v (d, Nk, Hk, B), box (64, 128, 1, 1).
+cudaError_t launch_cross(const PagedArgs &a, const PagedMaps &maps, int num_sms, cudaStream_t stream);
+
+// Masks [T][words] and positions [T] of trees given by parents [T].
+struct TreeMaskArgs {
+    const int *parents, *cu_q, *kv_len;
+    unsigned *mask;
+    int *positions;
+    uint32_t *status;
+    int T, B, words;
+};
+cudaError_t launch_tree_mask(const TreeMaskArgs &a, cudaStream_t stream);
+
+// The listed ones of each sequence's new tokens, moved together, already
+// validated.  Strides as in KvAppendArgs.
+struct KvKeepArgs {
+    void *k_cache, *v_cache;
+    const int *page_table, *cu_q, *kv_len, *kept, *kept_len;
+    int *kv_len_out;  // may be kv_len
+    uint32_t *status;
+    long long kc_st[3], vc_st[3], table_stride, kept_stride;
+    int B, H, d, num_pages, page_shift, max_pages, max_kept;
+    int heads_per_chunk, chunks;  // filled in by the launch
+};
+cudaError_t launch_kv_keep(const KvKeepArgs &a, cudaStream_t stream);
+
+// Sequences that go on as copies of others, already validated.
+constexpr int kForkRanks = 8;  // blocks of the cluster
+struct KvForkArgs {
+    void *k_cache, *v_cache;
+    const int *page_table, *kv_len, *refs;
+    const int *parents, *cu_q;  // each may be null
+    int *table_out, *len_out, *refs_out;
+    uint32_t *status;
+    // Workspace, [B] each but counts [kForkRanks], free_list [num_pages] and,
+    // where an output is its input (staged), stage [B][max_pages].
+    int *first, *lacks, *counts, *free_list, *stage, *stage_len;
+    int4 *copies;  // source page (or -1), copy, filled slots, column
+    long long kc_st[3], vc_st[3], table_stride, table_out_stride;
+    int staged;
+    int B, H, d, num_pages, page_shift, max_pages;
+    int chunks;  // filled in by the launch
+};
+cudaError_t launch_kv_fork(const KvForkArgs &a, cudaStream_t stream);
 
 }  // namespace fattn
