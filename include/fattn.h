@@ -671,6 +671,44 @@ fattn_status_t attn_fwd_cross(const void *q, const void *k, const void *v, const
                               int dtype, void *workspace, size_t workspace_bytes,
                               struct CUstream_st *stream);
 
+/*
+ * attn_bwd_cross -- gradients of attn_fwd_cross, from its inputs, the o and lse
+ * it wrote and the upstream gradient dout (the scores are computed again): with
+ * P = exp(scale * Q K^T - lse), zero behind a sequence's last key, and D_i = dout_i
+ * . o_i, summed over the query heads of a key head,
+ *
+ *   dv = P^T dout,   dS = P * (dout V^T - D),   dq = scale dS K,   dk = scale dS^T Q
+ *
+ *   q, o, dout, dq : 16-bit [B][Hq][Nq][d], k, v, dk, dv: [B][Hk][Nk][d], each
+ *                    with element strides (batch, head, row) of its own
+ *   lse            : fp32 [B][Hq][Nq], contiguous
+ *   kv_len, scale, d, dtype: as given to attn_fwd_cross (a length out of range
+ *                    records FATTN_ERR_INDEX, role 12)
+ *   workspace      : device, 16-byte aligned, attn_bwd_cross_workspace_size(...)
+ *                    bytes on the current device (0 on invalid arguments);
+ *                    contents ignored on entry, undefined on exit; calls that
+ *                    share one must not overlap on the device
+ *
+ * Every row of dq, dk and dv is written: rows of dk and dv behind a sequence's
+ * last key, dq of a sequence without keys, and dk and dv without queries are
+ * zeros.  What lies behind a sequence's last key in k and v may be anything, NaN
+ * included.  P and dS are rounded to the inputs' type, dS in fp16 after a scaling
+ * by a power of two that follows from the largest |dout|; sums are fp32.  An
+ * output shares no element with an input or another output.  Sums are taken in an
+ * order that depends on the shapes and lengths alone: equal calls give equal bits.
+ * Up to four kernels are enqueued; the lengths are read when they run.  Errors as
+ * for attn_fwd_strided.
+ */
+size_t attn_bwd_cross_workspace_size(int B, int Hq, int Hk, int Nq, int Nk, int d);
+fattn_status_t attn_bwd_cross(const void *q, const void *k, const void *v, const void *o, const float *lse,
+                              const void *dout, const int *kv_len, void *dq, void *dk, void *dv, int B,
+                              int Hq, int Hk, int Nq, int Nk, int d, const long long *q_strides,
+                              const long long *k_strides, const long long *v_strides,
+                              const long long *o_strides, const long long *dout_strides,
+                              const long long *dq_strides, const long long *dk_strides,
+                              const long long *dv_strides, float scale, int dtype, void *workspace,
+                              size_t workspace_bytes, struct CUstream_st *stream);
+
 /* Human-readable name of a status code (static storage, never NULL). */
 const char *fattn_status_string(fattn_status_t status);
 

@@ -151,3 +151,58 @@ def cross(q, k, v, kv_len, scale):
             terms[b, h] = (q[b, h].double().abs() @ kk.abs().T * scale).amax(-1)
             vmax[b, h] = vv.abs().max()
     return o, lse, size, terms, vmax
+
+
+def cross_bwd(q, k, v, do, kv_len, scale, dtype=None, o_err=None):
+    """(dq, dk, dv) in fp64, and with a type the bounds of a computation that
+    rounds as the library says (first order, doubled nowhere):
+
+    h is half a step of the type, U = 2^-24.  A score adds d terms, and lse is
+    fp32: P is off by e = (d + 6) U sum|q k| scale + 3 U |lse| + 2^-22 relative,
+    then rounded by h (fp16: and 2^-25, below its normal numbers).  dP is off by
+    (d + 2) U sum|do v|; D by the rounding of o (o_err, else h |o|) and (d + 2) U
+    sum|do o|.  dS = P (dP - D) carries these, e, and its own rounding (fp16:
+    scaled to where the largest |do| is at least 1, so 2^-25 of that is its
+    floor).  Sums of n terms add (n + 64) U of the terms' sizes, the store h of
+    the result (fp16: and 2^-25)."""
+    B, Hq, Nq, d = q.shape
+    Hk, Nk = k.shape[1], k.shape[2]
+    G = Hq // Hk
+    out = [torch.zeros(x.shape, dtype=torch.float64) for x in (q, k, v)]
+    tol = [torch.zeros_like(x) for x in out]
+    U = 2.0 ** -24
+    h = torch.finfo(dtype).eps / 2 if dtype is not None else 0.0
+    tiny = 2.0 ** -25 if dtype == torch.float16 else 0.0
+    floor = tiny * float(do.double().abs().max()) if do.numel() else 0.0
+    for b in range(B):
+        n = Nk if kv_len is None else kv_len[b]
+        if n == 0:
+            continue
+        for hq in range(Hq):
+            qq, g = q[b, hq].double(), do[b, hq].double()
+            kk, vv = k[b, hq // G, :n].double(), v[b, hq // G, :n].double()
+            x = qq @ kk.T * scale
+            y = torch.logsumexp(x, -1, keepdim=True)
+            p = torch.exp(x - y)
+            o = p @ vv
+            dp = g @ vv.T
+            D = (g * o).sum(-1, keepdim=True)
+            ds = p * (dp - D)
+            out[0][b, hq] = ds @ kk * scale
+            out[1][b, hq // G, :n] += ds.T @ qq * scale
+            out[2][b, hq // G, :n] += p.T @ g
+            if dtype is None:
+                continue
+            e = (d + 6) * U * (qq.abs() @ kk.abs().T * scale) + 3 * U * y.abs() + 2.0 ** -22
+            p_err = p * (e + h) + tiny
+            oe = h * o.abs() if o_err is None else o_err[b, hq]
+            d_err = (g.abs() * oe).sum(-1, keepdim=True) + (d + 2) * U * (g * o).abs().sum(-1, keepdim=True)
+            dp_err = (d + 2) * U * (g.abs() @ vv.abs().T)
+            s_err = ds.abs() * (e + h + 4 * U) + p * (d_err + dp_err) * (1 + h) + floor
+            tol[0][b, hq] = scale * (s_err @ kk.abs() + (n + 64) * U * (ds.abs() @ kk.abs()))
+            m = G * Nq + 64
+            tol[1][b, hq // G, :n] += scale * (s_err.T @ qq.abs() + m * U * (ds.abs().T @ qq.abs()))
+            tol[2][b, hq // G, :n] += p_err.T @ g.abs() + m * U * (p.T @ g.abs())
+    if dtype is None:
+        return out
+    return out, [t * (1 + h) + h * x.abs() + tiny for t, x in zip(tol, out)]

@@ -2196,6 +2196,143 @@ fattn_status_t attn_fwd_cross(const void *q, const void *k, const void *v, const
     return e == cudaSuccess ? FATTN_OK : cuda_fail(e);
 }
 
+// Workspace of the gradients of cross attention (256-byte aligned each).
+struct CrossBwdWs {
+    size_t amax, starts, kv, q, bytes;
+};
+static CrossBwdWs cross_bwd_ws(long long rows, int d, int num_sms)
+{
+    const fattn::CrossBwdSizes n = fattn::cross_bwd_sizes(d, num_sms);
+    CrossBwdWs w;
+    w.amax = align_up(static_cast<size_t>(rows) * 4, kWsAlign);
+    w.starts = align_up(w.amax + n.amax * 4, kWsAlign);
+    w.kv = align_up(w.starts + n.starts * sizeof(int4), kWsAlign);
+    w.q = align_up(w.kv + n.kv * 4, kWsAlign);
+    w.bytes = w.q + n.q * 4;
+    return w;
+}
+
+size_t attn_bwd_cross_workspace_size(int B, int Hq, int Hk, int Nq, int Nk, int d)
+{
+    int dev = 0;
+    DeviceInfo info;
+    if (check_cross(B, Hq, Hk, Nq, Nk, d, 1.f, 0) != FATTN_OK || current_device(&dev, &info) != FATTN_OK)
+        return 0;
+    return cross_bwd_ws(static_cast<long long>(B) * Hq * Nq, d, info.num_sms).bytes;
+}
+
+fattn_status_t attn_bwd_cross(const void *q, const void *k, const void *v, const void *o, const float *lse,
+                              const void *dout, const int *kv_len, void *dq, void *dk, void *dv, int B,
+                              int Hq, int Hk, int Nq, int Nk, int d, const long long *q_strides,
+                              const long long *k_strides, const long long *v_strides,
+                              const long long *o_strides, const long long *dout_strides,
+                              const long long *dq_strides, const long long *dk_strides,
+                              const long long *dv_strides, float scale, int dtype, void *workspace,
+                              size_t workspace_bytes, struct CUstream_st *stream)
+{
+    fattn_status_t s = check_cross(B, Hq, Hk, Nq, Nk, d, scale, dtype);
+    if (s != FATTN_OK)
+        return s;
+    const bool queries = B > 0 && Hq > 0 && Nq > 0, keys = B > 0 && Hk > 0 && Nk > 0;
+    if (!queries && !keys)
+        return FATTN_OK;
+    // Units of work are counted in 32 bits.
+    const long long tiles_q = (Nq + 127) / 128, tiles_k = (Nk + 127) / 128;
+    if (Hq * tiles_q > 0x7fffffffLL || Hk * tiles_k > 0x7fffffffLL)
+        return FATTN_ERR_UNSUPPORTED;
+    // Rows 0 .. 3: q, o, dout and dq; 4 .. 7: k, v, dk and dv.
+    const void *ptr[8] = {q, o, dout, dq, k, v, dk, dv};
+    const long long *st[8] = {q_strides, o_strides, dout_strides, dq_strides,
+                              k_strides, v_strides, dk_strides, dv_strides};
+    Rows rows[8];
+    bool used[8];
+    const long long none[3] = {d, d, d};
+    for (int i = 0; i < 8; ++i) {
+        used[i] = i < 4 ? queries : keys;
+        if (used[i] && !st[i])
+            return FATTN_ERR_INVALID_ARG;
+        rows[i] = rows_of(ptr[i], used[i] ? st[i] : none, 3, B, i < 4 ? Hq : Hk, i < 4 ? Nq : Nk, d);
+        if (used[i] && (s = check_rows(rows[i])) != FATTN_OK)
+            return s;
+    }
+    const size_t lse_bytes = queries ? static_cast<size_t>(B) * Hq * Nq * 4 : 0;
+    const size_t len_bytes = kv_len ? static_cast<size_t>(B) * 4 : 0;
+    if ((queries && (!lse || reinterpret_cast<uintptr_t>(lse) % 4 != 0)) ||
+        reinterpret_cast<uintptr_t>(kv_len) % 4 != 0)
+        return FATTN_ERR_INVALID_ARG;
+    for (int i = 0; i < 8; ++i) {
+        if (!used[i] || (i != 3 && i != 6 && i != 7))
+            continue;  // outputs against everything
+        if (!distinct(rows[i]) || !apart(rows[i], lse, lse_bytes) || !apart(rows[i], kv_len, len_bytes))
+            return FATTN_ERR_INVALID_ARG;
+        for (int j = 0; j < 8; ++j)
+            if (j != i && used[j] && !apart(rows[i], rows[j]))
+                return FATTN_ERR_INVALID_ARG;
+    }
+    int dev = 0;
+    DeviceInfo info;
+    const void *bufs[11] = {lse_bytes ? lse : nullptr, kv_len, workspace};
+    for (int i = 0; i < 8; ++i)
+        bufs[3 + i] = used[i] ? ptr[i] : nullptr;
+    if ((s = check_buffers(bufs, &dev, &info)) != FATTN_OK)
+        return s;
+    const CrossBwdWs ws = cross_bwd_ws(static_cast<long long>(B) * Hq * Nq, d, info.num_sms);
+    if (!workspace || !aligned16(workspace) || workspace_bytes < ws.bytes ||
+        (lse_bytes && overlap(workspace, ws.bytes, lse, lse_bytes)) ||
+        (len_bytes && overlap(workspace, ws.bytes, kv_len, len_bytes)))
+        return FATTN_ERR_INVALID_ARG;
+    for (int i = 0; i < 8; ++i)
+        if (used[i] && !apart(rows[i], workspace, ws.bytes))
+            return FATTN_ERR_INVALID_ARG;
+    PFN_cuTensorMapEncodeTiled_v12000 encode;
+    if ((s = get_encoder(&encode)) != FATTN_OK)
+        return s;
+    fattn::CrossBwdArgs a = {};
+    if ((s = status_word(&a.status)) != FATTN_OK)
+        return s;
+    fattn::CrossBwdMaps maps;
+    CUtensorMap *map[4] = {&maps.q, &maps.dout, &maps.k, &maps.v};
+    const int of[4] = {0, 2, 4, 5};
+    for (int i = 0; i < 4; ++i) {
+        // Without queries, or without keys, nothing is copied: any valid map does.
+        const Rows &r = rows[used[of[i]] ? of[i] : queries ? 0 : 4];
+        if ((s = make_row_map(encode, map[i], r.p, d, {r.ext[2], r.ext[1], r.ext[0]},
+                              {r.st[2], r.st[1], r.st[0]}, {128u, 1u, 1u}, dtype == 1)) != FATTN_OK)
+            return s;
+    }
+    uint8_t *base = static_cast<uint8_t *>(workspace);
+    a.o = o;
+    a.dout = dout;
+    a.lse = lse;
+    a.kv_len = kv_len;
+    a.dq = dq;
+    a.dk = dk;
+    a.dv = dv;
+    a.dvec = reinterpret_cast<float *>(base);
+    a.amax = reinterpret_cast<float *>(base + ws.amax);
+    a.starts = reinterpret_cast<int4 *>(base + ws.starts);
+    a.ws_kv = reinterpret_cast<float *>(base + ws.kv);
+    a.ws_q = reinterpret_cast<float *>(base + ws.q);
+    copy_strides(a.o_st, rows[1]);
+    copy_strides(a.do_st, rows[2]);
+    copy_strides(a.dq_st, rows[3]);
+    copy_strides(a.dk_st, rows[6]);
+    copy_strides(a.dv_st, rows[7]);
+    a.B = B;
+    a.Hk = Hk;
+    a.G = Hq / Hk;
+    a.Nq = Nq;
+    a.Nk = Nk;
+    a.Tq = static_cast<int>(tiles_q);
+    a.d = d;
+    a.f16 = dtype;
+    a.grid = info.num_sms;
+    a.scale = scale;
+    a.sl2 = scale * 1.4426950408889634f;
+    const cudaError_t e = fattn::launch_cross_bwd(a, maps, stream);
+    return e == cudaSuccess ? FATTN_OK : cuda_fail(e);
+}
+
 const char *fattn_status_string(fattn_status_t status)
 {
     switch (status) {

@@ -1,0 +1,1165 @@
+// fattn_cross_bwd_sm103.cu -- gradients of cross attention on GB300 (sm_103a):
+// batched queries against keys of another length, ragged, with shared heads.
+//
+// From the saved q, k, v, o and lse, with P = exp(scale Q K^T - lse) (zero
+// behind a sequence's last key) and D_i = dO_i . o_i, for the G query heads h of
+// a key head:
+//   dV = sum_h P^T dO,     dP = dO V^T,   dS = P o (dP - D),
+//   dQ = scale dS K,       dK = scale sum_h dS^T Q.
+// Four kernels:
+//   prep     D, the largest |dO| (fp16), and zeros for key tiles without keys
+//   dkdv     a unit is a tile of 128 keys of one (sequence, key head).  K, V
+//            stay; the tiles of Q and dO of its G query heads stream by: S^T =
+//            K Q^T and dP^T = V dO^T, keys on TMEM lanes, P^T over S^T, then dV
+//            += P^T dO and dK += dS^T Q from TMEM
+//   dq       a unit is a tile of 128 queries of one head.  Q, dO stay; K and V
+//            stream by: S, dP, then dQ += dS K
+//   merge    sums of units that were split
+// S and dP are formed in both, so that neither needs atomics: 7 products where
+// 5 would do, and equal calls give equal bits.
+//
+// Schedule.  Lengths live on the device.  Every CTA (one an SM) sums the units'
+// costs, a step (tile pair) each and some for a unit's start and end, and takes
+// an equal share of the total, which may begin or end inside a unit: that
+// unit's sums go to the workspace in fp32, at most two a CTA, and the merge
+// kernel adds them in order.  So few key tiles under many queries (a short text)
+// fill the GPU as well as the reverse.
+//
+// Bound.  Tensor cores at d = 128, and the exponentials and conversions of the
+// elementwise warps at d = 64 (two warpgroups, a row of 64 columns a thread).
+//
+// Types.  P and dS enter the second products in the inputs' type.  dS in fp16
+// is scaled by a power of two that brings the largest |dO| to 1 .. 2, so that
+// small gradients keep their digits; the sums are scaled back in fp32.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <stdint.h>
+
+#include <type_traits>
+
+#include "fattn_internal.h"
+#include "ptx_sm103.cuh"
+
+namespace fattn {
+namespace {
+
+using namespace ptx;
+
+constexpr int kTile = 128;
+constexpr int kThreads = 320;  // warps 0-7 elementwise, 8 producer, 9 MMA
+constexpr int kElemWarps = 8;  // two warpgroups, a half of the 128 columns each
+constexpr int kWarpLoad = 8;
+constexpr int kWarpMma = 9;
+constexpr uint32_t kTmemCols = 512;
+constexpr uint64_t kWaitLimitNs = 2000000000ull;
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr uint32_t kChunkBytes = kTile * 64 * 2;
+constexpr uint32_t kColS = 0, kColDP = 128, kColAcc0 = 256;
+
+// A unit's start and end, in steps (see Schedule); a split leaves at least kSnap
+// steps on each side, and a share is at least kLeast.
+constexpr int kUnitCost = 3, kSnap = 2, kLeast = 8;
+
+template <int D, bool kDkDv> struct BCfg {
+    static constexpr int kChunks = (D + 63) / 64;
+    static constexpr uint32_t kTileBytes = kChunks * kChunkBytes;  // one [128][D] tile
+    // Two resident tiles, then dkdv: two stages of (Q, dO); dq: three of K and
+    // two of V (V is free as soon as dP has read it, K only after dQ).
+    static constexpr int kKStages = 3, kVStages = 2;
+    static constexpr uint32_t kKRing = 2 * kTileBytes;
+    static constexpr uint32_t kVRing = kKRing + kKStages * kTileBytes;
+    static constexpr uint32_t kTilesBytes = kDkDv ? 6 * kTileBytes : kVRing + kVStages * kTileBytes;
+    static constexpr uint32_t kColAcc1 = kColAcc0 + D;
+};
+// dq: the S buffer of a unit's i-th key tile.
+template <int D> __device__ __forceinline__ uint32_t dq_s_col(int i)
+{
+    return (i & 1) ? kColAcc0 + D : kColS;  // the second behind the accumulator
+}
+
+// Where a CTA starts: a sequence, the cost already behind in it, and its share.
+struct Start {
+    int b;
+    long long y, left;
+};
+
+struct alignas(16) BBars {
+    uint64_t res_full, res_empty;      // the resident pair
+    uint64_t st_full[3], st_empty[3];  // dkdv: Q stages; dq: K stages
+    uint64_t v_full[2], v_empty[2];    // dkdv: dO stages; dq: V stages
+    uint64_t s_full, p_full, o_full, o_empty;
+    uint64_t p1_full, dp_full;  // dkdv: P^T written; dP^T computed
+    uint64_t dp_free;           // dq: dP is in registers
+    // dq: dS of the CTA's n-th tile written, on dq_full[n % 2] (a warp may be a
+    // tile ahead of another, not two).
+    uint64_t dq_full[2];
+    uint64_t grp[2];  // dkdv: a warpgroup's lse and D of the tile are stored
+    uint64_t drain;
+    uint32_t tmem_base;
+    int abort;
+    float ds_scale;  // of dS
+    Start start;
+    long long warp_sum[kThreads / 32];
+    float warp_max[kThreads / 32];
+};
+// dkdv, behind the barriers: -lse log2(e) and -D (scaled) of the current query
+// tile, two deep.
+struct BXch {
+    float lse2[2][kTile], dd[2][kTile];
+};
+
+__device__ __forceinline__ int clamp_len(const CrossBwdArgs &a, int b)
+{
+    const int L = a.kv_len != nullptr ? a.kv_len[b] : a.Nk;
+    return min(max(L, 0), a.Nk);
+}
+
+// A piece of work: steps [t0, t1) of a unit.
+struct Piece {
+    int b, h, tile;
+    int L;       // keys of the sequence
+    int t0, t1;  // dkdv: (query head of the group, query tile); dq: key tiles
+    int slot;    // workspace slot of a partial result, or -1: the whole unit
+};
+
+// Units of sequence b and the steps of each.
+template <bool kDkDv>
+__device__ __forceinline__ void units_of(const CrossBwdArgs &a, int L, int &units, int &steps)
+{
+    const int F = (L + kTile - 1) / kTile;
+    units = kDkDv ? a.Hk * F : a.Hk * a.G * a.Tq;
+    steps = kDkDv ? a.G * a.Tq : F;
+}
+// Step that a cost of y inside a unit falls on.
+__device__ __forceinline__ int step_at(long long y, int steps)
+{
+    if (y >= steps + kUnitCost)
+        return steps;
+    const int t = y < kUnitCost ? 0 : static_cast<int>(y - kUnitCost);
+    return t < kSnap ? 0 : steps - t < kSnap ? steps : t;
+}
+
+struct Walk {
+    Start at;
+    int L, units, steps, u;
+};
+template <bool kDkDv> __device__ __forceinline__ void enter(const CrossBwdArgs &a, Walk &w)
+{
+    w.L = clamp_len(a, w.at.b);
+    units_of<kDkDv>(a, w.L, w.units, w.steps);
+}
+template <bool kDkDv> __device__ __forceinline__ Walk first_walk(const CrossBwdArgs &a, const BBars &b)
+{
+    Walk w;
+    w.at = b.start;
+    w.u = w.units = 0;
+    if (w.at.left > 0) {
+        enter<kDkDv>(a, w);
+        const int cost = w.steps + kUnitCost;
+        w.u = static_cast<int>(w.at.y / cost);
+        w.at.y -= static_cast<long long>(w.u) * cost;
+    }
+    return w;
+}
+template <bool kDkDv> __device__ __forceinline__ bool next_piece(const CrossBwdArgs &a, Walk &w, Piece &p)
+{
+    while (w.at.left > 0) {
+        if (w.u >= w.units) {
+            w.u = 0;
+            if (++w.at.b >= a.B)
+                return false;
+            enter<kDkDv>(a, w);
+            continue;
+        }
+        const int cost = w.steps + kUnitCost;
+        const long long y0 = w.at.y, y1 = min(y0 + w.at.left, static_cast<long long>(cost));
+        const int u = w.u++;
+        w.at.left -= y1 - y0;
+        w.at.y = 0;
+        p.t0 = step_at(y0, w.steps);
+        p.t1 = step_at(y1, w.steps);
+        // Nothing falls to this CTA (a unit without steps is its first CTA's).
+        if (w.steps == 0 ? y0 > 0 : p.t0 == p.t1)
+            continue;
+        const int per = kDkDv ? w.units / a.Hk : a.Tq;
+        p.b = w.at.b;
+        p.h = u / per;
+        p.tile = u - p.h * per;
+        p.L = w.L;
+        const int cta = static_cast<int>(blockIdx.x);
+        p.slot = p.t0 > 0 ? 2 * cta : p.t1 < w.steps ? 2 * cta + 1 : -1;
+        return true;
+    }
+    return false;
+}
+
+// The whole block finds this CTA's start.
+template <bool kDkDv> __device__ void find_start(const CrossBwdArgs &a, BBars &b)
+{
+    const int tid = threadIdx.x, lane = tid & 31;
+    long long sum = 0;
+    for (int i = tid; i < a.B; i += kThreads) {
+        int units, steps;
+        units_of<kDkDv>(a, clamp_len(a, i), units, steps);
+        sum += static_cast<long long>(units) * (steps + kUnitCost);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o /= 2)
+        sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if (lane == 0)
+        b.warp_sum[tid / 32] = sum;
+    __syncthreads();
+    if (tid >= 32)
+        return;
+    long long total = 0;
+#pragma unroll
+    for (int w = 0; w < kThreads / 32; ++w)
+        total += b.warp_sum[w];
+    const int c = blockIdx.x;
+    const int shares = static_cast<int>(min(static_cast<long long>(gridDim.x), max(total / kLeast, 1LL)));
+    const long long each = total / shares, rest = total - each * shares;
+    const long long lo = c * each + c * rest / shares, hi = (c + 1) * each + (c + 1) * rest / shares;
+    int4 *starts = a.starts + (kDkDv ? 0 : a.grid);
+    if (c >= shares || lo >= hi) {
+        if (lane == 0) {
+            b.start = Start{0, 0, 0};
+            starts[c] = make_int4(-1, 0, 0, 0);
+        }
+        return;
+    }
+    // 32 sequences at a time until the one that holds this CTA's first cost.
+    long long before = 0;
+    for (int b0 = 0; b0 < a.B; b0 += 32) {
+        const int i = b0 + lane;
+        int L = 0, units = 0, steps = 0;
+        if (i < a.B) {
+            L = clamp_len(a, i);
+            units_of<kDkDv>(a, L, units, steps);
+        }
+        const long long mine = static_cast<long long>(units) * (steps + kUnitCost);
+        long long incl = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o *= 2) {
+            const long long x = __shfl_up_sync(0xffffffffu, incl, o);
+            incl += lane >= o ? x : 0;
+        }
+        const long long first = before + incl - mine;
+        if (first <= lo && lo < first + mine) {
+            b.start = Start{i, lo - first, hi - lo};
+            const int cost = steps + kUnitCost, u = static_cast<int>((lo - first) / cost);
+            const int t = step_at(lo - first - static_cast<long long>(u) * cost, steps);
+            const int per = kDkDv ? units / a.Hk : a.Tq;
+            starts[c] = make_int4(i, u / per, u % per, t < steps ? t : 0);
+        }
+        before += __shfl_sync(0xffffffffu, incl, 31);
+    }
+}
+
+__device__ __forceinline__ void fail(const CrossBwdArgs &a, BBars &b, uint32_t role)
+{
+    const uint32_t code = 4u /* FATTN_ERR_TIMEOUT */ | (role << 8) | ((blockIdx.x & 0xffffu) << 16);
+    atomicCAS(a.status, 0u, code);
+    *reinterpret_cast<volatile int *>(&b.abort) = 1;
+}
+__device__ __forceinline__ bool warp_wait(uint64_t &bar, uint32_t parity, const volatile int *abort)
+{
+    const bool ok = mbar_wait(smem_addr(&bar), parity, kWaitLimitNs, abort);
+    return __all_sync(0xffffffffu, ok);
+}
+// The same value on every lane of a converged warp, read afresh: copy
+// coordinates that follow from the lists go through it inside the loop that uses
+// them (see paged_sm103.cuh).
+__device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xffffffffu, x, 0); }
+
+template <bool kF16> __device__ __forceinline__ uint32_t pack2(float lo, float hi)
+{
+    if constexpr (kF16) {
+        const __half2 v = __floats2half2_rn(lo, hi);
+        return *reinterpret_cast<const uint32_t *>(&v);
+    } else {
+        const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+        return *reinterpret_cast<const uint32_t *>(&v);
+    }
+}
+
+// ------------------------------------------------------------------ products
+// [128 x D] x [128 x D]^T, both K-major, into 128 fp32 columns.
+template <int D, bool kF16>
+__device__ __forceinline__ void mma_nt(uint32_t tmem_d, uint32_t a_smem, uint32_t b_smem)
+{
+    constexpr uint32_t idesc = idesc_f32acc(kTile, kTile, false, kF16);
+    constexpr uint32_t hi = smem_desc_hi(1024);
+    const uint32_t a_lo = smem_desc_lo(a_smem, 16), b_lo = smem_desc_lo(b_smem, 16);
+#pragma unroll
+    for (int kk = 0; kk < D / 16; ++kk) {
+        const uint32_t off = ((kk >> 2) * kChunkBytes + (kk & 3) * 32) >> 4;
+        mma_ss_w(tmem_d, a_lo + off, hi, b_lo + off, hi, idesc, kk > 0 ? 1u : 0u);
+    }
+}
+// A from TMEM: 16 packed columns at the head of each 32-column chunk of a score
+// region, K = 16 step kk at column 32 (kk / 2) + 8 (kk % 2).  B MN-major.
+template <int D, bool kF16>
+__device__ __forceinline__ void mma_tn(uint32_t tmem_d, uint32_t tmem_a, uint32_t b_smem, bool accumulate)
+{
+    constexpr uint32_t idesc = idesc_f32acc(kTile, D, true, kF16);
+    constexpr uint32_t hi = smem_desc_hi(1024);
+    const uint32_t b_lo = smem_desc_lo(b_smem, D > 64 ? kChunkBytes : 1024);
+#pragma unroll
+    for (int kk = 0; kk < kTile / 16; ++kk)
+        mma_ts_w(tmem_d, tmem_a + 32 * (kk >> 1) + 8 * (kk & 1), b_lo + ((kk * 16 * 128) >> 4), hi, idesc,
+                 kk > 0 || accumulate ? 1u : 0u);
+}
+
+// ------------------------------------------------------------------ producer
+template <int D, bool kDkDv>
+__device__ void bwd_load(const CrossBwdArgs &a, BBars &b, uint32_t smem, const CUtensorMap *mq,
+                         const CUtensorMap *mk, const CUtensorMap *mv, const CUtensorMap *mdo)
+{
+    using C = BCfg<D, kDkDv>;
+    const volatile int *abort = &b.abort;
+    const bool leader = elect_one();
+    // A tile whose barrier is waited for and armed here.
+    auto copy = [&](uint64_t &full_bar, uint32_t dst, const CUtensorMap *map, int row, int head, int batch) {
+        if (leader) {
+            const uint32_t full = smem_addr(&full_bar);
+            mbar_arrive_expect_tx(full, C::kTileBytes);
+#pragma unroll
+            for (int c = 0; c < C::kChunks; ++c)
+                tma_load_4d(dst + c * kChunkBytes, map, full, 64 * c, row, head, batch);
+        }
+    };
+    uint32_t res_phase = 0, res_issued = 0, kpos = 0, vpos = 0;
+    bool ok = true;
+    Walk w = first_walk<kDkDv>(a, b);
+    Piece p;
+    while (ok && next_piece<kDkDv>(a, w, p)) {
+        if (p.t0 == p.t1)
+            continue;
+        if (!warp_wait(b.res_empty, res_phase ^ 1, abort)) {
+            ok = false;
+            break;
+        }
+        res_phase ^= 1;
+        ++res_issued;
+        const int head = uniform(p.h), batch = uniform(p.b), own = uniform(p.tile * kTile);
+        if (leader) {
+            const uint32_t full = smem_addr(&b.res_full);
+            mbar_arrive_expect_tx(full, 2 * C::kTileBytes);
+#pragma unroll
+            for (int c = 0; c < C::kChunks; ++c) {
+                tma_load_4d(smem + c * kChunkBytes, kDkDv ? mk : mq, full, 64 * c, own, head, batch);
+                tma_load_4d(smem + C::kTileBytes + c * kChunkBytes, kDkDv ? mv : mdo, full, 64 * c, own, head,
+                            batch);
+            }
+        }
+        if constexpr (kDkDv) {
+            // dO first: its slot is released (after dV) before Q's (after dK).
+            int g = p.t0 / a.Tq, i = p.t0 - g * a.Tq;
+            for (int t = p.t0; ok && t < p.t1; ++t) {
+                const uint32_t stage = kpos & 1, phase = (kpos >> 1) & 1;
+                const uint32_t dst = smem + (2 + 2 * stage) * C::kTileBytes;
+                const int row = uniform(i * kTile), qh = uniform(p.h * a.G + g);
+                ok = warp_wait(b.v_empty[stage], phase ^ 1, abort);
+                if (!ok)
+                    break;
+                copy(b.v_full[stage], dst + C::kTileBytes, mdo, row, qh, batch);
+                ++vpos;
+                ok = warp_wait(b.st_empty[stage], phase ^ 1, abort);
+                if (!ok)
+                    break;
+                copy(b.st_full[stage], dst, mq, row, qh, batch);
+                ++kpos;
+                if (++i == a.Tq) {
+                    i = 0;
+                    ++g;
+                }
+            }
+        } else {
+            const int kh = uniform(p.h / a.G);
+            for (int t = p.t0; ok && t < p.t1; ++t) {
+                const uint32_t ks = kpos % C::kKStages, vs = vpos % C::kVStages;
+                const int row = uniform(t * kTile);
+                ok = warp_wait(b.st_empty[ks], ((kpos / C::kKStages) & 1) ^ 1, abort);
+                if (!ok)
+                    break;
+                copy(b.st_full[ks], smem + C::kKRing + ks * C::kTileBytes, mk, row, kh, batch);
+                ++kpos;
+                ok = warp_wait(b.v_empty[vs], ((vpos / C::kVStages) & 1) ^ 1, abort);
+                if (!ok)
+                    break;
+                copy(b.v_full[vs], smem + C::kVRing + vs * C::kTileBytes, mv, row, kh, batch);
+                ++vpos;
+            }
+        }
+    }
+    if (!ok) {
+        if (leader)
+            fail(a, b, kRoleLoad);
+        // Copies already issued land before the CTA exits.
+        const uint32_t ring = kDkDv ? 2 : C::kKStages;
+        for (uint32_t q = kpos > ring ? kpos - ring : 0; q < kpos; ++q)
+            mbar_wait(smem_addr(&b.st_full[q % ring]), (q / ring) & 1, kWaitLimitNs / 8, nullptr);
+        for (uint32_t q = vpos > 2 ? vpos - 2 : 0; q < vpos; ++q)
+            mbar_wait(smem_addr(&b.v_full[q & 1]), (q >> 1) & 1, kWaitLimitNs / 8, nullptr);
+        if (res_issued > 0)
+            mbar_wait(smem_addr(&b.res_full), res_phase ^ 1, kWaitLimitNs / 8, nullptr);
+    }
+}
+
+// ------------------------------------------------------------------ MMA issue
+template <int D, bool kF16, bool kDkDv>
+__device__ void bwd_mma(const CrossBwdArgs &a, BBars &b, uint32_t smem, uint32_t tmem)
+{
+    using C = BCfg<D, kDkDv>;
+    const volatile int *abort = &b.abort;
+    const bool leader = elect_one();
+    uint32_t res_phase = 0, s_phase = 0, oe_phase = 0, dp_phase = 0, pos = 0;
+    uint32_t n_tile = 0;  // dq: tiles of this CTA so far (dq_full[n % 2])
+    bool ok = true;
+    auto commit = [&](uint64_t &bar) {
+        if (leader)
+            mma_commit(smem_addr(&bar));
+    };
+    const uint32_t a0 = smem, a1 = smem + C::kTileBytes;  // resident pair
+    Walk w = first_walk<kDkDv>(a, b);
+    Piece p;
+    while (ok && next_piece<kDkDv>(a, w, p)) {
+        const int n = uniform(p.t1 - p.t0);
+        if (n == 0)
+            continue;
+        pos = uniform(pos);
+        ok = warp_wait(b.res_full, res_phase, abort);
+        res_phase ^= 1;
+        ok = ok && warp_wait(b.o_empty, oe_phase ^ 1, abort);
+        oe_phase ^= 1;
+        if (!ok)
+            break;
+        if constexpr (!kDkDv) {
+            // S(t+1) goes into the other S buffer before dS(t) is ready, dP(t+1)
+            // follows as soon as dP(t) is in registers (dp_free), dQ += dS(t) K(t)
+            // once dS(t) is written.
+            auto k_tile = [&](int t) { return smem + C::kKRing + ((pos + t) % C::kKStages) * C::kTileBytes; };
+            auto v_tile = [&](int t) { return smem + C::kVRing + ((pos + t) % C::kVStages) * C::kTileBytes; };
+            auto wait_k = [&](int t) {
+                return warp_wait(b.st_full[(pos + t) % C::kKStages], ((pos + t) / C::kKStages) & 1, abort);
+            };
+            auto wait_v = [&](int t) {
+                return warp_wait(b.v_full[(pos + t) % C::kVStages], ((pos + t) / C::kVStages) & 1, abort);
+            };
+            ok = wait_k(0) && wait_v(0);
+            if (!ok)
+                break;
+            tc_fence_after();
+            if (leader) {
+                mma_nt<D, kF16>(tmem + dq_s_col<D>(0), a0, k_tile(0));  // S = Q K^T
+                mma_nt<D, kF16>(tmem + kColDP, a1, v_tile(0));          // dP = dO V^T
+            }
+            commit(b.s_full);
+            commit(b.v_empty[pos % C::kVStages]);
+            if (n == 1)
+                commit(b.res_empty);
+            for (int t = 0; ok && t < n; ++t) {
+                if (t + 1 < n) {
+                    ok = wait_k(t + 1);
+                    if (!ok)
+                        break;
+                    tc_fence_after();
+                    if (leader)
+                        mma_nt<D, kF16>(tmem + dq_s_col<D>(t + 1), a0, k_tile(t + 1));
+                    ok = warp_wait(b.dp_free, dp_phase, abort);
+                    dp_phase ^= 1;
+                    ok = ok && wait_v(t + 1);
+                    if (!ok)
+                        break;
+                    tc_fence_after();
+                    if (leader)
+                        mma_nt<D, kF16>(tmem + kColDP, a1, v_tile(t + 1));
+                    commit(b.s_full);
+                    commit(b.v_empty[(pos + t + 1) % C::kVStages]);
+                    if (t + 2 == n)
+                        commit(b.res_empty);  // the resident pair is no longer read
+                }
+                ok = warp_wait(b.dq_full[n_tile & 1], (n_tile >> 1) & 1, abort);
+                ++n_tile;
+                if (!ok)
+                    break;
+                tc_fence_after();
+                if (leader)  // dQ += dS K
+                    mma_tn<D, kF16>(tmem + kColAcc0, tmem + dq_s_col<D>(t), k_tile(t), t > 0);
+                commit(b.st_empty[(pos + t) % C::kKStages]);
+                if (t + 1 == n)
+                    commit(b.o_full);
+            }
+        } else {
+            // P^T(t) is written over S^T(t), dS^T(t) over dP^T(t): S^T(t+1)
+            // follows dV(t), dP^T(t+1) follows dK(t).
+            auto stage = [&](int t) { return smem + (2 + 2 * ((pos + t) & 1)) * C::kTileBytes; };
+            auto wait_q = [&](int t) {
+                return warp_wait(b.st_full[(pos + t) & 1], ((pos + t) >> 1) & 1, abort);
+            };
+            auto wait_do = [&](int t) {
+                return warp_wait(b.v_full[(pos + t) & 1], ((pos + t) >> 1) & 1, abort);
+            };
+            ok = wait_q(0);
+            if (!ok)
+                break;
+            tc_fence_after();
+            if (leader)
+                mma_nt<D, kF16>(tmem + kColS, a0, stage(0));  // S^T = K Q^T
+            commit(b.s_full);
+            ok = wait_do(0);
+            if (!ok)
+                break;
+            tc_fence_after();
+            if (leader)
+                mma_nt<D, kF16>(tmem + kColDP, a1, stage(0) + C::kTileBytes);  // dP^T = V dO^T
+            commit(b.dp_full);
+            if (n == 1)
+                commit(b.res_empty);
+            for (int t = 0; ok && t < n; ++t) {
+                const bool next = t + 1 < n;
+                ok = warp_wait(b.p1_full, dp_phase, abort);
+                dp_phase ^= 1;
+                if (!ok)
+                    break;
+                tc_fence_after();
+                if (leader)  // dV += P^T dO
+                    mma_tn<D, kF16>(tmem + kColAcc0, tmem + kColS, stage(t) + C::kTileBytes, t > 0);
+                commit(b.v_empty[(pos + t) & 1]);
+                if (next) {
+                    ok = wait_q(t + 1);
+                    if (!ok)
+                        break;
+                    tc_fence_after();
+                    if (leader)
+                        mma_nt<D, kF16>(tmem + kColS, a0, stage(t + 1));
+                    commit(b.s_full);
+                }
+                ok = warp_wait(b.p_full, s_phase, abort);
+                s_phase ^= 1;
+                if (!ok)
+                    break;
+                tc_fence_after();
+                if (leader)  // dK += dS^T Q
+                    mma_tn<D, kF16>(tmem + C::kColAcc1, tmem + kColDP, stage(t), t > 0);
+                commit(b.st_empty[(pos + t) & 1]);
+                if (next) {
+                    ok = wait_do(t + 1);
+                    if (!ok)
+                        break;
+                    tc_fence_after();
+                    if (leader)
+                        mma_nt<D, kF16>(tmem + kColDP, a1, stage(t + 1) + C::kTileBytes);
+                    commit(b.dp_full);
+                    if (t + 2 == n)
+                        commit(b.res_empty);
+                } else {
+                    commit(b.o_full);
+                }
+            }
+        }
+        pos += n;
+    }
+    if (!ok && leader)
+        fail(a, b, kRoleMma);
+    commit(b.drain);
+    mbar_wait(smem_addr(&b.drain), 0, kWaitLimitNs, nullptr);
+}
+
+// -lse log2(e), with which P = 2^(s scale log2(e) + it); of a row that saw no
+// key (lse = -inf) -inf, so that its P is 0.
+__device__ __forceinline__ float neg_lse2(float lse)
+{
+    return lse == -INFINITY ? lse : -lse * kLog2e;
+}
+
+// ------------------------------------------------------------------ elementwise
+// Thread r of either warpgroup owns TMEM lane r, row 128 tile + r of the
+// resident tile; warpgroup h works on columns 64 h .. 64 h + 63 of it.
+template <int D, bool kF16, bool kDkDv>
+__device__ void bwd_elem(const CrossBwdArgs &a, BBars &b, BXch &xch, uint8_t *tiles, uint32_t tmem)
+{
+    using C = BCfg<D, kDkDv>;
+    const volatile int *abort = &b.abort;
+    const int warp = (threadIdx.x / 32) & 3, lane = threadIdx.x & 31;
+    const int half = threadIdx.x / 128;
+    const int r = warp * 32 + lane;
+    tmem += static_cast<uint32_t>(warp * 32) << 16;
+    constexpr int kHalfChunks = kTile / 64;  // 32-column chunks of a half
+    uint32_t s_phase = 0, of_phase = 0, dp_phase = 0, grp_phase = 0;
+    uint32_t n_tile = 0;
+    int xbuf = 0;
+    bool ok = true;
+    const float ds_scale = b.ds_scale;
+    const uint64_t sl2x2 = f2_pack(a.sl2, a.sl2), dss = f2_pack(ds_scale, ds_scale);
+    auto wait = [&](uint64_t &bar, uint32_t &phase) {
+        const bool good = mbar_wait(smem_addr(&bar), phase, kWaitLimitNs, abort);
+        phase ^= 1;
+        return good;
+    };
+    auto arrive = [&](uint64_t &bar) {
+        __syncwarp();
+        if (lane == 0)
+            mbar_arrive(smem_addr(&bar));
+    };
+    Walk w = first_walk<kDkDv>(a, b);
+    Piece p;
+    while (ok && next_piece<kDkDv>(a, w, p)) {
+        const int row = p.tile * kTile + r;
+        float row_nl2 = 0.f, row_nd = 0.f;
+        if (!kDkDv && row < a.Nq) {
+            const long long at = (static_cast<long long>(p.b) * a.Hk * a.G + p.h) * a.Nq + row;
+            row_nl2 = neg_lse2(a.lse[at]);
+            row_nd = -a.dvec[at] * ds_scale;
+        }
+        // dkdv: lse (threads 0-63 of a warpgroup) and D (64-127) of its 64
+        // queries of a tile, fetched a tile ahead.
+        const int xq = half * 64 + (r & 63);
+        int fg = 0, fi = 0;  // of the tile fetched next
+        const float *xsrc = nullptr;
+        auto fetch = [&]() {
+            const int q = fi * kTile + xq;
+            const float x = q < a.Nq ? xsrc[static_cast<long long>(fg) * a.Nq + q] : 0.f;
+            if (++fi == a.Tq) {
+                fi = 0;
+                ++fg;
+            }
+            return x;
+        };
+        float xnext = 0.f;
+        if (kDkDv && p.t0 < p.t1) {
+            fg = p.t0 / a.Tq;
+            fi = p.t0 - fg * a.Tq;
+            xsrc = (r < 64 ? a.lse : a.dvec) +
+                   (static_cast<long long>(p.b) * a.Hk + p.h) * a.G * a.Nq;
+            xnext = fetch();
+        }
+        for (int t = p.t0; ok && t < p.t1; ++t) {
+            if constexpr (kDkDv) {
+                if (r < 64)
+                    xch.lse2[xbuf][xq] = neg_lse2(xnext);
+                else
+                    xch.dd[xbuf][xq] = -xnext * ds_scale;
+                if (t + 1 < p.t1)
+                    xnext = fetch();
+                arrive(b.grp[half]);
+                ok = wait(b.grp[half], grp_phase) && wait(b.s_full, s_phase);
+                if (!ok)
+                    break;
+                tc_fence_after();
+                // P^T of this half's chunks, kept in registers and written over
+                // the first 16 columns of each S^T chunk.  Queries behind Nq are
+                // zero rows of Q and dO and add nothing; keys behind the last
+                // one are lanes of their own, not stored.
+                float pr[kHalfChunks][32];
+#pragma unroll
+                for (int hc = 0; hc < kHalfChunks; ++hc) {
+                    const int ch = half * kHalfChunks + hc;
+                    uint32_t sr[32], pk[16];
+                    __syncwarp();
+                    tmem_ld32(tmem + kColS + ch * 32, sr);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        const uint64_t nl2 = *reinterpret_cast<const uint64_t *>(&xch.lse2[xbuf][ch * 32 + 2 * i]);
+                        float x0, x1;
+                        f2_unpack(f2_fma(f2_pack(__uint_as_float(sr[2 * i]), __uint_as_float(sr[2 * i + 1])),
+                                         sl2x2, nl2),
+                                  x0, x1);
+                        pr[hc][2 * i] = ex2(x0);
+                        pr[hc][2 * i + 1] = ex2(x1);
+                        pk[i] = pack2<kF16>(pr[hc][2 * i], pr[hc][2 * i + 1]);
+                    }
+                    tmem_st16(tmem + kColS + ch * 32, pk);
+                }
+                tmem_wait_st();
+                tc_fence_before();
+                arrive(b.p1_full);
+                // dS^T = P^T (dP^T - D) over the first 16 columns of each chunk.
+                ok = wait(b.dp_full, dp_phase);
+                if (!ok)
+                    break;
+                tc_fence_after();
+#pragma unroll
+                for (int hc = 0; hc < kHalfChunks; ++hc) {
+                    const int ch = half * kHalfChunks + hc;
+                    uint32_t dr[32], dk[16];
+                    __syncwarp();
+                    tmem_ld32(tmem + kColDP + ch * 32, dr);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        const uint64_t nd = *reinterpret_cast<const uint64_t *>(&xch.dd[xbuf][ch * 32 + 2 * i]);
+                        float d0, d1;
+                        f2_unpack(f2_mul(f2_pack(pr[hc][2 * i], pr[hc][2 * i + 1]),
+                                         f2_fma(f2_pack(__uint_as_float(dr[2 * i]), __uint_as_float(dr[2 * i + 1])),
+                                                dss, nd)),
+                                  d0, d1);
+                        dk[i] = pack2<kF16>(d0, d1);
+                    }
+                    tmem_st16(tmem + kColDP + ch * 32, dk);
+                }
+                tmem_wait_st();
+                tc_fence_before();
+                arrive(b.p_full);
+                xbuf ^= 1;
+            } else {
+                ok = wait(b.s_full, s_phase);
+                if (!ok)
+                    break;
+                tc_fence_after();
+                const int valid = p.L - t * kTile;  // keys of this tile
+                const uint32_t col_s = dq_s_col<D>(t - p.t0);
+                if (valid < kTile) {
+                    // What lies behind the last key may be anything: dS is zero
+                    // there, and so must K be (S has read it).
+                    uint4 *k_tile = reinterpret_cast<uint4 *>(tiles + C::kKRing +
+                                                              (n_tile % C::kKStages) * C::kTileBytes);
+                    for (int at = threadIdx.x; at < C::kChunks * kTile * 8; at += 256)
+                        if ((at / 8) % kTile >= valid)
+                            k_tile[at] = make_uint4(0, 0, 0, 0);
+                    fence_proxy_async_smem();
+                }
+                // This half of the dP row into registers first, so that dP of
+                // the next tile is computed meanwhile.
+                uint32_t dr[kHalfChunks][32];
+                __syncwarp();
+#pragma unroll
+                for (int hc = 0; hc < kHalfChunks; ++hc)
+                    tmem_ld32(tmem + kColDP + (half * kHalfChunks + hc) * 32, dr[hc]);
+                tmem_wait_ld();
+                if (t + 1 < p.t1) {
+                    tc_fence_before();
+                    arrive(b.dp_free);
+                }
+                auto grads = [&](int ch, const uint32_t *sr, const uint32_t *dp, uint32_t *dk, auto tag) {
+                    constexpr bool kMasked = decltype(tag)::value;
+                    const uint64_t nl2 = f2_pack(row_nl2, row_nl2), nd = f2_pack(row_nd, row_nd);
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        const int c = ch * 32 + 2 * i;
+                        float x0, x1, d0, d1;
+                        f2_unpack(f2_fma(f2_pack(__uint_as_float(sr[2 * i]), __uint_as_float(sr[2 * i + 1])),
+                                         sl2x2, nl2),
+                                  x0, x1);
+                        f2_unpack(f2_mul(f2_pack(ex2(x0), ex2(x1)),
+                                         f2_fma(f2_pack(__uint_as_float(dp[2 * i]), __uint_as_float(dp[2 * i + 1])),
+                                                dss, nd)),
+                                  d0, d1);
+                        if constexpr (kMasked) {
+                            d0 = c < valid ? d0 : 0.f;
+                            d1 = c + 1 < valid ? d1 : 0.f;
+                        }
+                        dk[i] = pack2<kF16>(d0, d1);
+                    }
+                };
+#pragma unroll
+                for (int hc = 0; hc < kHalfChunks; ++hc) {
+                    const int ch = half * kHalfChunks + hc;
+                    uint32_t sr[32], dk[16];
+                    __syncwarp();
+                    tmem_ld32(tmem + col_s + ch * 32, sr);
+                    tmem_wait_ld();
+                    if (valid < kTile)
+                        grads(ch, sr, dr[hc], dk, std::true_type{});
+                    else
+                        grads(ch, sr, dr[hc], dk, std::false_type{});
+                    tmem_st16(tmem + col_s + ch * 32, dk);
+                }
+                tmem_wait_st();
+                tc_fence_before();
+                arrive(b.dq_full[n_tile & 1]);
+                ++n_tile;
+            }
+        }
+        if (!ok)
+            break;
+        const bool some = p.t0 < p.t1;
+        if (some) {
+            ok = wait(b.o_full, of_phase);
+            if (!ok)
+                break;
+            tc_fence_after();
+        }
+        // dkdv: warpgroup 0 writes dV, warpgroup 1 dK; dq: each half of dQ's
+        // 32-column chunks.
+        const bool is_dv = kDkDv && half == 0;
+        const uint32_t col = kDkDv && !is_dv ? C::kColAcc1 : kColAcc0;
+        const float f = is_dv ? 1.f : a.scale / ds_scale;
+        const int rows = kDkDv ? a.Nk : a.Nq;
+        constexpr int kChunks32 = D / 32;
+        const int c0 = kDkDv ? 0 : half * ((kChunks32 + 1) / 2);
+        const int c1 = kDkDv ? kChunks32 : half == 0 ? (kChunks32 + 1) / 2 : kChunks32;
+        const bool whole = p.slot < 0;
+        const bool live = row < rows;
+        const bool zero = !some || (kDkDv && row >= p.L);
+        const long long *st = kDkDv ? (is_dv ? a.dv_st : a.dk_st) : a.dq_st;
+        uint16_t *out = static_cast<uint16_t *>(kDkDv ? (is_dv ? a.dv : a.dk) : a.dq);
+        uint16_t *dst = out + p.b * st[0] + p.h * st[1] + row * st[2];
+        float *part = (kDkDv ? a.ws_kv : a.ws_q) +
+                      ((static_cast<long long>(p.slot) * (kDkDv ? 2 : 1) + (kDkDv ? half : 0)) * kTile + r) * D;
+#pragma unroll 1
+        for (int c = c0; c < c1; ++c) {
+            uint32_t o[32];
+            if (some) {
+                __syncwarp();
+                tmem_ld32(tmem + col + c * 32, o);
+                tmem_wait_ld();
+            }
+            if (!live)
+                continue;
+            if (whole) {
+                uint4 *d4 = reinterpret_cast<uint4 *>(dst + c * 32);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    uint32_t x[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        x[j] = zero ? 0u
+                                    : pack2<kF16>(__uint_as_float(o[8 * i + 2 * j]) * f,
+                                                  __uint_as_float(o[8 * i + 2 * j + 1]) * f);
+                    d4[i] = make_uint4(x[0], x[1], x[2], x[3]);
+                }
+            } else {
+                uint4 *d4 = reinterpret_cast<uint4 *>(part + c * 32);
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    d4[i] = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+            }
+        }
+        if (some) {
+            tc_fence_before();
+            arrive(b.o_empty);
+        }
+    }
+    if (!ok)
+        fail(a, b, kRoleSoftmax);
+}
+
+// The power of two that scales dS: 1 in bf16; in fp16 from the blocks' largest
+// |dO|.  The whole block.
+template <bool kF16> __device__ void find_scale(const CrossBwdArgs &a, BBars &b)
+{
+    float m = 0.f;
+    if (kF16) {
+        for (int i = threadIdx.x; i < a.prep_blocks; i += kThreads)
+            m = fmaxf(m, a.amax[i]);
+#pragma unroll
+        for (int o = 16; o > 0; o /= 2)
+            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        if ((threadIdx.x & 31) == 0)
+            b.warp_max[threadIdx.x / 32] = m;
+        __syncthreads();
+    }
+    if (threadIdx.x == 0) {
+        b.ds_scale = 1.f;
+        if (kF16) {
+            for (int w = 0; w < kThreads / 32; ++w)
+                m = fmaxf(m, b.warp_max[w]);
+            // fp16 values are 2^-24 .. 2^16: the scale is 2^24 .. 2^-16.
+            if (m > 0.f && m < 65536.f)
+                b.ds_scale = exp2f(-floorf(log2f(m)));
+        }
+    }
+}
+
+template <int D, bool kF16, bool kDkDv>
+__global__ void __launch_bounds__(kThreads, 1)
+    cross_bwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
+                     const __grid_constant__ CUtensorMap mv, const __grid_constant__ CUtensorMap mdo,
+                     const CrossBwdArgs a)
+{
+    using C = BCfg<D, kDkDv>;
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    const uint32_t raw = smem_addr(smem_raw);
+    const uint32_t smem = (raw + 1023u) & ~1023u;
+    uint8_t *tiles = smem_raw + (smem - raw);
+    BBars &b = *reinterpret_cast<BBars *>(tiles + C::kTilesBytes);
+    const int warp = threadIdx.x / 32;
+    if (threadIdx.x == 0) {
+        mbar_init(smem_addr(&b.res_full), 1);
+        mbar_init(smem_addr(&b.res_empty), 1);
+        for (int s = 0; s < 3; ++s) {
+            mbar_init(smem_addr(&b.st_full[s]), 1);
+            mbar_init(smem_addr(&b.st_empty[s]), 1);
+        }
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(smem_addr(&b.v_full[s]), 1);
+            mbar_init(smem_addr(&b.v_empty[s]), 1);
+            mbar_init(smem_addr(&b.dq_full[s]), kElemWarps);
+            mbar_init(smem_addr(&b.grp[s]), kElemWarps / 2);
+        }
+        mbar_init(smem_addr(&b.s_full), 1);
+        mbar_init(smem_addr(&b.p_full), kElemWarps);
+        mbar_init(smem_addr(&b.o_full), 1);
+        mbar_init(smem_addr(&b.o_empty), kElemWarps);
+        mbar_init(smem_addr(&b.p1_full), kElemWarps);
+        mbar_init(smem_addr(&b.dp_full), 1);
+        mbar_init(smem_addr(&b.dp_free), kElemWarps);
+        mbar_init(smem_addr(&b.drain), 1);
+        b.abort = 0;
+        fence_barrier_init();
+    }
+    if (warp == kWarpMma) {
+        tmem_alloc(smem_addr(&b.tmem_base), kTmemCols);
+        tmem_relinquish();
+    }
+    if (warp == kWarpLoad && (threadIdx.x & 31) == 0) {
+        prefetch_tensormap(&mq);
+        prefetch_tensormap(&mk);
+        prefetch_tensormap(&mv);
+        prefetch_tensormap(&mdo);
+    }
+    grid_dependency_wait();
+    find_scale<kF16>(a, b);
+    find_start<kDkDv>(a, b);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = b.tmem_base;
+    if (warp < kElemWarps)
+        bwd_elem<D, kF16, kDkDv>(a, b, *reinterpret_cast<BXch *>(&b + 1), tiles, tmem);
+    else if (warp == kWarpLoad)
+        bwd_load<D, kDkDv>(a, b, smem, &mq, &mk, &mv, &mdo);
+    else
+        bwd_mma<D, kF16, kDkDv>(a, b, smem, tmem);
+    grid_launch_dependents();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == kWarpMma) {
+        __syncwarp();
+        tmem_dealloc(tmem, kTmemCols);
+    }
+}
+
+// ------------------------------------------------------------------ prep
+constexpr int kPrepThreads = 256;
+constexpr int kPrepBlocks = 1216;  // at most: 8 a SM
+constexpr int kPrepRows = 4;       // of a group of lanes in flight
+
+template <bool kF16> __device__ __forceinline__ float2 unpack2(uint32_t w)
+{
+    if constexpr (kF16)
+        return __half22float2(*reinterpret_cast<const __half2 *>(&w));
+    else
+        return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&w));
+}
+
+// D of all rows, a group of lanes a row (16 bytes a lane), and the block's
+// largest |dO|.  Then zeros for the key tiles that no unit covers.
+template <int D, bool kF16> __global__ void __launch_bounds__(kPrepThreads) cross_prep_kernel(const CrossBwdArgs a)
+{
+    constexpr int kLanes = D / 8, kGroup = D == 64 ? 8 : 16;
+    grid_dependency_wait();
+    const int lane = threadIdx.x & 31, part = lane % kGroup;
+    const int groups = kPrepThreads / kGroup;
+    const long long stride = static_cast<long long>(gridDim.x) * groups;
+    const int Hq = a.Hk * a.G;
+    const long long rows = static_cast<long long>(a.B) * Hq * a.Nq;
+    float amax = 0.f;
+    for (long long row0 = static_cast<long long>(blockIdx.x) * groups + threadIdx.x / kGroup;
+         row0 - threadIdx.x / kGroup < rows; row0 += stride * kPrepRows) {
+        uint4 x[kPrepRows], y[kPrepRows];
+#pragma unroll
+        for (int i = 0; i < kPrepRows; ++i) {
+            const long long row = row0 + i * stride;
+            x[i] = y[i] = make_uint4(0, 0, 0, 0);
+            if (row < rows && part < kLanes) {
+                const long long bh = row / a.Nq;
+                const int n = static_cast<int>(row - bh * a.Nq);
+                const int bb = static_cast<int>(bh / Hq), h = static_cast<int>(bh - static_cast<long long>(bb) * Hq);
+                x[i] = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(a.o) + bb * a.o_st[0] +
+                                                        h * a.o_st[1] + n * a.o_st[2] + part * 8);
+                y[i] = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(a.dout) + bb * a.do_st[0] +
+                                                        h * a.do_st[1] + n * a.do_st[2] + part * 8);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < kPrepRows; ++i) {
+            const long long row = row0 + i * stride;
+            const uint32_t xv[4] = {x[i].x, x[i].y, x[i].z, x[i].w}, yv[4] = {y[i].x, y[i].y, y[i].z, y[i].w};
+            float acc = 0.f;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float2 u = unpack2<kF16>(xv[j]), v = unpack2<kF16>(yv[j]);
+                acc = fmaf(u.x, v.x, acc);
+                acc = fmaf(u.y, v.y, acc);
+                if (kF16)
+                    amax = fmaxf(amax, fmaxf(fabsf(v.x), fabsf(v.y)));
+            }
+#pragma unroll
+            for (int o = kGroup / 2; o > 0; o /= 2)
+                acc += __shfl_xor_sync(0xffffffffu, acc, o);
+            if (row < rows && part == 0)
+                a.dvec[row] = acc;
+        }
+    }
+    if (kF16) {
+        __shared__ float warp_max[kPrepThreads / 32];
+#pragma unroll
+        for (int o = 16; o > 0; o /= 2)
+            amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+        if (lane == 0)
+            warp_max[threadIdx.x / 32] = amax;
+        __syncthreads();
+        if (threadIdx.x == 0) {
+            for (int w = 1; w < kPrepThreads / 32; ++w)
+                amax = fmaxf(amax, warp_max[w]);
+            a.amax[blockIdx.x] = amax;
+        }
+    }
+    // Key tiles behind a sequence's last key: no unit's, zeros in dk and dv.
+    if (a.kv_len == nullptr)
+        return;
+    const int Tk = (a.Nk + kTile - 1) / kTile;
+    const long long tiles = static_cast<long long>(a.B) * a.Hk * Tk;
+    for (long long i = blockIdx.x; i < tiles; i += gridDim.x) {
+        const long long bh = i / Tk;
+        const int tile = static_cast<int>(i - bh * Tk), b = static_cast<int>(bh / a.Hk);
+        const int h = static_cast<int>(bh - static_cast<long long>(b) * a.Hk);
+        const int L = clamp_len(a, b);
+        if (tile == 0 && h == 0 && threadIdx.x == 0 && a.kv_len[b] != L)
+            atomicCAS(a.status, 0u, 6u /* FATTN_ERR_INDEX */ | (kRoleCross << 8));
+        if (tile * kTile < L || part >= kLanes)
+            continue;
+        const int end = min(a.Nk, (tile + 1) * kTile);
+        for (int n = tile * kTile + threadIdx.x / kGroup; n < end; n += groups) {
+            *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.dk) + b * a.dk_st[0] + h * a.dk_st[1] +
+                                       n * a.dk_st[2] + part * 8) = make_uint4(0, 0, 0, 0);
+            *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.dv) + b * a.dv_st[0] + h * a.dv_st[1] +
+                                       n * a.dv_st[2] + part * 8) = make_uint4(0, 0, 0, 0);
+        }
+    }
+}
+
+// ------------------------------------------------------------------ merge
+// Block (x, y) adds up the unit that CTA x + 1 starts inside, if that is the
+// first boundary in it: the partial of CTA x (its last slot) and those of CTAs
+// x + 1, x + 2, ... that start inside it.  y: dK, dV or dQ, and 32 rows of it.
+constexpr int kMergeThreads = 256, kMergeRows = 32;
+template <int D, bool kF16> __global__ void __launch_bounds__(kMergeThreads) cross_merge_kernel(const CrossBwdArgs a)
+{
+    grid_dependency_wait();
+    const int which = blockIdx.y / (kTile / kMergeRows);  // 0: dV, 1: dK, 2: dQ
+    const int r0 = blockIdx.y % (kTile / kMergeRows) * kMergeRows;
+    const int4 *starts = a.starts + (which == 2 ? a.grid : 0);
+    const int c = blockIdx.x + 1;
+    const int4 me = starts[c], last = starts[c - 1];
+    auto inside = [&](const int4 &s) { return s.x == me.x && s.y == me.y && s.z == me.z && s.w > 0; };
+    if (me.x < 0 || me.w == 0 || inside(last))
+        return;
+    int count = 1;
+    while (c + count < a.grid && inside(starts[c + count]))
+        ++count;
+    const float *ws = which == 2 ? a.ws_q : a.ws_kv;
+    const int parts = which == 2 ? 1 : 2, part = which == 1 ? 1 : 0;
+    const long long *st = which == 2 ? a.dq_st : which == 1 ? a.dk_st : a.dv_st;
+    uint16_t *out = static_cast<uint16_t *>(which == 2 ? a.dq : which == 1 ? a.dk : a.dv);
+    const int rows = which == 2 ? a.Nq : a.Nk, L = which == 2 ? a.Nq : clamp_len(a, me.x);
+    float f = 1.f;
+    if (which != 0) {
+        float m = 0.f;
+        if (kF16) {
+            for (int i = threadIdx.x & 31; i < a.prep_blocks; i += 32)
+                m = fmaxf(m, a.amax[i]);
+#pragma unroll
+            for (int o = 16; o > 0; o /= 2)
+                m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        }
+        f = a.scale / (m > 0.f && m < 65536.f ? exp2f(-floorf(log2f(m))) : 1.f);
+    }
+    constexpr int kVecs = D / 4;
+    for (int at = threadIdx.x; at < kMergeRows * kVecs; at += kMergeThreads) {
+        const int r = r0 + at / kVecs, v = at % kVecs, row = me.z * kTile + r;
+        if (row >= rows)
+            continue;
+        auto slot = [&](int k) {
+            const long long s = k == 0 ? 2LL * (c - 1) + 1 : 2LL * (c + k - 1);
+            return reinterpret_cast<const float4 *>(ws + ((s * parts + part) * kTile + r) * D)[v];
+        };
+        float4 x = slot(0);
+#pragma unroll 4
+        for (int k = 1; k <= count; ++k) {
+            const float4 y = slot(k);
+            x = make_float4(x.x + y.x, x.y + y.y, x.z + y.z, x.w + y.w);
+        }
+        const uint2 packed = row < L ? make_uint2(pack2<kF16>(x.x * f, x.y * f), pack2<kF16>(x.z * f, x.w * f))
+                                     : make_uint2(0, 0);
+        *reinterpret_cast<uint2 *>(out + me.x * st[0] + me.y * st[1] + row * st[2] + v * 4) = packed;
+    }
+}
+
+template <class... Params, class... Args>
+cudaError_t start(void (*kernel)(Params...), dim3 grid, int threads, size_t smem, cudaStream_t stream,
+                  const Args &...args)
+{
+    cudaLaunchAttribute pdl[1];
+    pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    pdl[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cfg.attrs = pdl;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+template <int D, bool kF16, bool kDkDv>
+cudaError_t launch_pass(const CrossBwdArgs &a, const CrossBwdMaps &m, cudaStream_t stream)
+{
+    const size_t smem = BCfg<D, kDkDv>::kTilesBytes + sizeof(BBars) + (kDkDv ? sizeof(BXch) : 0) + 1024;
+    const cudaError_t e = cudaFuncSetAttribute(
+        cross_bwd_kernel<D, kF16, kDkDv>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    return e != cudaSuccess ? e
+                            : start(cross_bwd_kernel<D, kF16, kDkDv>, dim3(a.grid), kThreads, smem, stream, m.q,
+                                    m.k, m.v, m.dout, a);
+}
+
+template <int D, bool kF16>
+cudaError_t launch(const CrossBwdArgs &args, const CrossBwdMaps &m, cudaStream_t stream)
+{
+    CrossBwdArgs a = args;
+    constexpr int kRows = kPrepThreads / (D == 64 ? 8 : 16) * kPrepRows;  // of a block
+    const long long rows = static_cast<long long>(a.B) * a.Hk * a.G * a.Nq;
+    const long long blocks = (rows + kRows - 1) / kRows;
+    // The zeros of short sequences want hands, too.
+    a.prep_blocks = static_cast<int>(a.kv_len != nullptr || blocks > kPrepBlocks ? kPrepBlocks
+                                     : blocks > 0                               ? blocks
+                                                                                : 1);
+    cudaError_t e = start(cross_prep_kernel<D, kF16>, dim3(a.prep_blocks), kPrepThreads, 0, stream, a);
+    if (e == cudaSuccess)
+        e = launch_pass<D, kF16, true>(a, m, stream);
+    if (e == cudaSuccess)
+        e = launch_pass<D, kF16, false>(a, m, stream);
+    if (e == cudaSuccess && a.grid > 1)
+        e = start(cross_merge_kernel<D, kF16>, dim3(a.grid - 1, 3 * (kTile / kMergeRows)), kMergeThreads, 0, stream,
+                  a);
+    return e;
+}
+
+template <int D> cudaError_t launch_typed(const CrossBwdArgs &a, const CrossBwdMaps &m, cudaStream_t stream)
+{
+    return a.f16 ? launch<D, true>(a, m, stream) : launch<D, false>(a, m, stream);
+}
+
+}  // namespace
+
+CrossBwdSizes cross_bwd_sizes(int d, int num_sms)
+{
+    return CrossBwdSizes{kPrepBlocks, 2 * num_sms, 2LL * num_sms * 2 * kTile * d, 2LL * num_sms * kTile * d};
+}
+
+cudaError_t launch_cross_bwd(const CrossBwdArgs &a, const CrossBwdMaps &m, cudaStream_t stream)
+{
+    switch (a.d) {
+    case 64: return launch_typed<64>(a, m, stream);
+    case 96: return launch_typed<96>(a, m, stream);
+    case 128: return launch_typed<128>(a, m, stream);
+    }
+    return cudaErrorInvalidValue;
+}
+
+}  // namespace fattn

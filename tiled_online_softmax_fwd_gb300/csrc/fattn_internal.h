@@ -245,4 +245,32 @@ struct KvForkArgs {
 };
 cudaError_t launch_kv_fork(const KvForkArgs &a, cudaStream_t stream);
 
+// Gradients of cross attention, already validated.  Strides (batch, head, row)
+// in elements.
+struct CrossBwdArgs {
+    const void *o, *dout;
+    const float *lse;
+    const int *kv_len;  // may be null
+    void *dq, *dk, *dv;
+    // Workspace: D [B Hq Nq], the prep blocks' largest |dO|, where the CTAs of
+    // the two passes start [2][grid], partial sums of two units a CTA.
+    float *dvec, *amax, *ws_kv, *ws_q;
+    int4 *starts;
+    uint32_t *status;
+    long long o_st[3], do_st[3], dq_st[3], dk_st[3], dv_st[3];
+    int B, Hk, G, Nq, Nk, Tq, d, f16, grid;
+    float scale, sl2;
+    int prep_blocks;  // filled in by the launch
+};
+// Maps (d, rows, heads, B) of q, k, v and dO, box (64, 128, 1, 1).
+struct CrossBwdMaps {
+    CUtensorMap q, k, v, dout;
+};
+// Sizes of a call's workspace: elements of amax, starts, ws_kv and ws_q.
+struct CrossBwdSizes {
+    long long amax, starts, kv, q;
+};
+CrossBwdSizes cross_bwd_sizes(int d, int num_sms);
+cudaError_t launch_cross_bwd(const CrossBwdArgs &a, const CrossBwdMaps &m, cudaStream_t stream);
+
 }  // namespace fattn

@@ -24,7 +24,8 @@ FATTN_OK = 0
 STATUS_NAMES = {0: "FATTN_OK", 1: "FATTN_ERR_INVALID_ARG", 2: "FATTN_ERR_UNSUPPORTED",
                 3: "FATTN_ERR_CUDA", 4: "FATTN_ERR_TIMEOUT", 5: "FATTN_ERR_RANGE",
                 6: "FATTN_ERR_INDEX"}
-EXPORTED = ["attn_bwd", "attn_bwd_workspace_size", "attn_fwd", "attn_fwd_cross",
+EXPORTED = ["attn_bwd", "attn_bwd_workspace_size", "attn_bwd_cross",
+            "attn_bwd_cross_workspace_size", "attn_fwd", "attn_fwd_cross",
             "attn_fwd_cross_workspace_size", "attn_fwd_fp16", "attn_fwd_host",
             "attn_fwd_kv", "attn_fwd_kv_workspace_size", "attn_fwd_paged", "attn_fwd_tree",
             "attn_fwd_paged_workspace_size", "attn_fwd_simt", "attn_fwd_strided",
@@ -143,6 +144,11 @@ def load():
         lib.attn_fwd_cross_workspace_size.argtypes = [ip] * 4
         lib.attn_fwd_cross.restype = ctypes.c_int
         lib.attn_fwd_cross.argtypes = [vp] * 6 + [ip] * 6 + [i64p] * 4 + [
+            fp, ip, vp, ctypes.c_size_t, vp]
+        lib.attn_bwd_cross_workspace_size.restype = ctypes.c_size_t
+        lib.attn_bwd_cross_workspace_size.argtypes = [ip] * 6
+        lib.attn_bwd_cross.restype = ctypes.c_int
+        lib.attn_bwd_cross.argtypes = [vp] * 10 + [ip] * 6 + [i64p] * 8 + [
             fp, ip, vp, ctypes.c_size_t, vp]
         lib.fattn_version.restype = ctypes.c_char_p
         lib.fattn_version.argtypes = []
@@ -1178,6 +1184,44 @@ def attn_fwd_cross(q, k, v, kv_len=None, scale: float | None = None, workspace=N
     _call("attn_fwd_cross", dev, stream, q.data_ptr(), k.data_ptr(), v.data_ptr(), _ptr(kv_len),
           out.data_ptr(), lse.data_ptr(), *args, o_st, *flags, workspace.data_ptr(), workspace.nbytes)
     return out, lse
+
+
+def cross_bwd_workspace_size(B: int, Hq: int, Hk: int, Nq: int, Nk: int, d: int, device=None) -> int:
+    """Scratch bytes attn_bwd_cross needs for this shape."""
+    return _workspace_bytes("attn_bwd_cross_workspace_size", _device_index(device),
+                            *map(operator.index, (B, Hq, Hk, Nq, Nk, d)))
+
+
+def attn_bwd_cross(q, k, v, o, lse, do, kv_len=None, scale: float | None = None, dq=None, dk=None,
+                   dv=None, workspace=None, stream=None):
+    """Gradients of attn_fwd_cross (libfattn attn_bwd_cross) for the upstream
+    gradient ``do``, from its inputs and the o and lse it returned: tensors of
+    q's and k's shapes, any strides with a contiguous last dimension (lse
+    contiguous).  Rows of dk and dv behind a sequence's last key are zeros.
+    Returns (dq, dk, dv) in the inputs' type, each of which may be given."""
+    if scale is not None and type(scale) is not float:
+        scale = float(scale)
+    try:
+        key = ("cross", _of(q), _of(k), _of(v), _of(kv_len), scale)
+    except AttributeError:  # not tensors: the checks say which
+        key = None
+    dev, dtype, shape, lse_shape, _, dense, args, flags = _plans.get(key) or _cross_plan(
+        key, q, k, v, kv_len, scale)
+    for name, t in (("o", o), ("do", do)):
+        _check_half(name, t, 4, dtype, dev)
+        if tuple(t.shape) != shape:
+            raise ValueError("%s must have q's shape" % name)
+    _check_plain("lse", lse, torch.float32, lse_shape, dev)
+    dq, dk, dv = (_like(name, out, t, dtype, dev, stream)
+                  for name, out, t in (("dq", dq, q), ("dk", dk, k), ("dv", dv, v)))
+    if workspace is None:
+        workspace = _empty(max(_workspace_bytes("attn_bwd_cross_workspace_size", dev, *args[:6]), 16),
+                           torch.uint8, dev, stream)
+    _call("attn_bwd_cross", dev, stream, q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(),
+          lse.data_ptr(), do.data_ptr(), _ptr(kv_len), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(),
+          *args, _outer(o), _outer(do), _outer(dq), _outer(dk), _outer(dv), *flags,
+          workspace.data_ptr(), workspace.nbytes)
+    return dq, dk, dv
 
 
 def version() -> str:
