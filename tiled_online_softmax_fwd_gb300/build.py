@@ -2,7 +2,8 @@
 
 Every translation unit is compiled for sm_103a only, in parallel, then linked
 into one shared library with the CUDA runtime linked statically and only the
-C-ABI symbols exported.
+C-ABI symbols exported.  Beside it goes the compiled part of the Python binding
+(csrc/binding.cpp), for the interpreter and torch that run the build.
 
     python -m tiled_online_softmax_fwd_gb300.build [--verbose] [--force]
 """
@@ -14,6 +15,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -21,6 +23,7 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(BUILD, "libfattn.so")
+BINDING = os.path.join(BUILD, "fattn_binding.so")
 
 SOURCES = ["fattn_api.cu", "fattn_fwd_sm103.cu", "fattn_bwd_sm103.cu", "fattn_fwd_simt.cu",
            "fattn_rowops.cu", "fattn_rope.cu", "fattn_paged_sm103.cu", "fattn_tree_sm103.cu",
@@ -66,21 +69,67 @@ def _compile(src: str, verbose: bool, force: bool) -> str:
     return obj
 
 
+def _run(cmd, what):
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        raise RuntimeError("%s failed:\n%s%s" % (what, res.stdout, res.stderr))
+
+
+def _compile_binding(force: bool):
+    """binding.cpp for this interpreter and its torch; None if that has no CUDA."""
+    import torch
+    if torch.version.cuda is None:
+        return None
+    obj = os.path.join(BUILD, "binding.o")
+    src = os.path.join(CSRC, "binding.cpp")
+    stamp = obj + ".torch"
+    built_for = "%s %s" % (torch.__version__, sys.version)
+    if not force and not _inputs_newer(obj, [src, os.path.join(INCLUDE, "fattn.h")]) \
+            and os.path.exists(stamp) and open(stamp).read() == built_for:
+        return obj
+    root = os.path.dirname(torch.__file__)
+    cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc()))), "include")
+    _run(["g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden",
+          "-D_GLIBCXX_USE_CXX11_ABI=%d" % int(torch._C._GLIBCXX_USE_CXX11_ABI),
+          "-I", INCLUDE, "-isystem", os.path.join(root, "include"),
+          "-isystem", os.path.join(root, "include", "torch", "csrc", "api", "include"),
+          "-isystem", sysconfig.get_paths()["include"], "-isystem", cuda, "-c", src, "-o", obj + ".tmp"],
+         "g++ on binding.cpp")
+    os.replace(obj + ".tmp", obj)
+    with open(stamp, "w") as f:
+        f.write(built_for)
+    return obj
+
+
+def _link_binding(obj: str, force: bool):
+    import torch
+    if not force and not _inputs_newer(BINDING, [obj, LIB]):
+        return
+    lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    _run(["g++", "-shared", "-o", BINDING + ".tmp", obj, "-L", BUILD, "-l:libfattn.so", "-L", lib, "-lc10",
+          "-lc10_cuda", "-ltorch_cpu", "-ltorch_python", "-Wl,-rpath,$ORIGIN", "-Wl,-rpath," + lib],
+         "linking the binding")
+    os.replace(BINDING + ".tmp", BINDING)
+
+
 def build(verbose: bool = False, force: bool = False) -> str:
-    """Compile and link libfattn.so; returns its path.  Rebuilds only what changed."""
+    """Compile and link libfattn.so and the binding; returns the library's path.
+    Rebuilds only what changed."""
     os.makedirs(BUILD, exist_ok=True)
-    with cf.ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
+    with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        binding = ex.submit(_compile_binding, force)
         objs = list(ex.map(lambda s: _compile(s, verbose, force), SOURCES))
+        binding = binding.result()
     if force or _inputs_newer(LIB, objs):
         vmap = os.path.join(BUILD, "exports.map")
         with open(vmap, "w") as f:
             f.write(EXPORTS)
         cmd = [nvcc(), *GENCODE, "-shared", "-cudart", "static", "-o", LIB + ".tmp", *objs,
                "-Xlinker", "--version-script=" + vmap]
-        res = subprocess.run(cmd, capture_output=True, text=True)
-        if res.returncode != 0:
-            raise RuntimeError("link failed:\n%s%s" % (res.stdout, res.stderr))
+        _run(cmd, "link")
         os.replace(LIB + ".tmp", LIB)
+    if binding is not None:
+        _link_binding(binding, force)
     return LIB
 
 

@@ -1,7 +1,8 @@
 """ctypes binding of libfattn's C ABI (include/fattn.h).
 
 Argument marshalling only: every step of the computation runs in the CUDA
-library.  PyTorch supplies device memory and streams.  The checks mirror the
+library.  The calls of a drafting or searching step and of cross attention go
+through a compiled module in the same manner (csrc/binding.cpp).  PyTorch supplies device memory and streams.  The checks mirror the
 wrapper of "Triton programming template" (device, shape, dtype, contiguity)
 so that misuse raises in Python before the C layer sees it; the C layer
 checks again and is the authority.
@@ -10,6 +11,8 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import importlib.machinery
+import importlib.util
 import math
 import operator
 import os
@@ -19,6 +22,7 @@ import torch
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _LIB_PATH = os.path.join(_HERE, "_build", "libfattn.so")
+_BINDING_PATH = os.path.join(_HERE, "_build", "fattn_binding.so")
 
 FATTN_OK = 0
 STATUS_NAMES = {0: "FATTN_OK", 1: "FATTN_ERR_INVALID_ARG", 2: "FATTN_ERR_UNSUPPORTED",
@@ -882,42 +886,48 @@ def attn_fwd_paged(q, k_cache, v_cache, page_table, cu_q, kv_len, max_q: int,
         key = None
     dev, dtype, shape, lse_shape, need, dense, args, flags = _plans.get(key) or _paged_plan(
         key, q, k_cache, v_cache, page_table, cu_q, kv_len, max_q, causal, scale)
-    out, o_st, lse, workspace = _outputs(q, out, lse, workspace, dev, dtype, shape, lse_shape, need,
-                                         dense, stream)
+    o_st = dense
+    if out is None:
+        out = _empty(shape, dtype, dev, stream)
+    else:
+        _check_half("out", out, 3, dtype, dev)
+        if out.shape != q.shape:
+            raise ValueError("out must have q's shape")
+        o_st = _outer(out)
+    if lse is None:
+        lse = _empty(lse_shape, torch.float32, dev, stream)
+    else:
+        _check_plain("lse", lse, torch.float32, lse_shape, dev)
+    if workspace is None:
+        workspace = _empty(need, torch.uint8, dev, stream)
     _call("attn_fwd_paged", dev, stream, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
           page_table.data_ptr(), cu_q.data_ptr(), kv_len.data_ptr(), out.data_ptr(), lse.data_ptr(),
           *args, o_st, *flags, workspace.data_ptr(), workspace.nbytes)
     return out, lse
 
 
-def _ints(name, t, shape, dev):
-    """An int32 list on CUDA device `dev` whose last dimension is contiguous."""
-    if not isinstance(t, _Tensor) or t.dtype != torch.int32 or tuple(t.shape) != tuple(shape) \
-            or t.get_device() != dev or (shape[-1] > 1 and t.stride(-1) != 1):
-        raise ValueError("%s must be an int32 %s tensor on CUDA device %d with a contiguous last "
-                         "dimension" % (name, list(shape), dev))
+_binding = None
 
 
-def _list_device(name, t):
-    """Device of the list that sets it for a call."""
-    if not isinstance(t, _Tensor):
-        raise TypeError("%s must be a torch.Tensor" % name)
-    if not t.is_cuda or t.dtype != torch.int32 or not t.is_contiguous():
-        raise ValueError("%s must be a contiguous int32 CUDA tensor, got %s on %s" % (name, t.dtype, t.device))
-    return t.get_device()
-
-
-def _tree_mask_plan(key, parents, cu_q, kv_len, max_q):
-    dev = _list_device("parents", parents)
-    if max_q < 1:
-        raise ValueError("max_q must be at least 1, got %d" % max_q)
-    if parents.dim() != 1 or not isinstance(kv_len, _Tensor) or kv_len.dim() != 1:
-        raise ValueError("parents [T] and kv_len [B] must have one dimension")
-    T, B = parents.shape[0], kv_len.shape[0]
-    _ints("kv_len", kv_len, (B,), dev)
-    _ints("cu_q", cu_q, (B + 1,), dev)
-    words = (max_q + 31) // 32
-    return _keep(key, (dev, (T, words), (1, T), (T, B, words)))
+def _native():
+    """The compiled binding of the calls below (csrc/binding.cpp): they check
+    their tensors, make their outputs and call the library without Python in
+    between.  Raises if it has not been built: there is no fallback."""
+    global _binding
+    if _binding is None:
+        load()
+        with _lock:
+            if _binding is None:
+                if not os.path.exists(_BINDING_PATH):
+                    raise RuntimeError("the binding is not built (%s); run "
+                                       "`python -m tiled_online_softmax_fwd_gb300.build`" % _BINDING_PATH)
+                loader = importlib.machinery.ExtensionFileLoader("fattn_binding", _BINDING_PATH)
+                spec = importlib.util.spec_from_loader("fattn_binding", loader)
+                module = importlib.util.module_from_spec(spec)
+                loader.exec_module(module)
+                module.init(_check)
+                _binding = module
+    return _binding
 
 
 def tree_mask(parents, cu_q, kv_len, max_q: int, mask=None, positions=None, stream=None):
@@ -928,36 +938,7 @@ def tree_mask(parents, cu_q, kv_len, max_q: int, mask=None, positions=None, stre
     kv_append.  Returns (mask int32 [T, ceil(max_q / 32)], positions int32
     [1, T]): attn_fwd_tree's mask, in which a token sees itself and those it
     continues, and each token's position for qk_norm_rope, by its depth."""
-    if type(max_q) is not int:
-        max_q = operator.index(max_q)
-    try:
-        key = ("tree_mask", _of(parents), _of(cu_q), _of(kv_len), max_q)
-    except AttributeError:  # not tensors: the checks say which
-        key = None
-    dev, shape, pos_shape, args = _plans.get(key) or _tree_mask_plan(key, parents, cu_q, kv_len, max_q)
-    if mask is None:
-        mask = _empty(shape, torch.int32, dev, stream)
-    else:
-        _check_plain("mask", mask, torch.int32, shape, dev)
-    if positions is None:
-        positions = _empty(pos_shape, torch.int32, dev, stream)
-    else:
-        _check_plain("positions", positions, torch.int32, pos_shape, dev)
-    _call("fattn_tree_mask", dev, stream, parents.data_ptr(), cu_q.data_ptr(), kv_len.data_ptr(),
-          mask.data_ptr(), positions.data_ptr(), *args)
-    return mask, positions
-
-
-def _tree_plan(key, q, k_cache, v_cache, page_table, cu_q, kv_len, mask, max_q, scale):
-    dev, dtype, shape, lse_shape, need, dense, args, flags = _paged_plan(
-        None, q, k_cache, v_cache, page_table, cu_q, kv_len, max_q, False, scale)
-    words = mask.shape[1] if isinstance(mask, _Tensor) and mask.dim() == 2 else (max_q + 31) // 32
-    _ints("mask", mask, (shape[0], words), dev)
-    if 32 * words < max_q:
-        raise ValueError("mask has %d words, max_q %d needs %d" % (words, max_q, (max_q + 31) // 32))
-    row = mask.stride(0) if shape[0] > 1 else words
-    return _keep(key, (dev, dtype, shape, lse_shape, need, dense, args[:10] + (words, row) + args[10:],
-                       (flags[0], flags[2])))
+    return (_binding or _native()).tree_mask(parents, cu_q, kv_len, max_q, mask, positions, stream)
 
 
 def attn_fwd_tree(q, k_cache, v_cache, page_table, cu_q, kv_len, mask, max_q: int,
@@ -967,77 +948,11 @@ def attn_fwd_tree(q, k_cache, v_cache, page_table, cu_q, kv_len, mask, max_q: in
     tokens in place of the causal one.  Every token sees all keys before the
     new tokens, and of those the ones with a bit in its row of ``mask`` (int32
     [T, words], 32 words at least max_q: bit j % 32 of word j / 32 is its own
-    sequence's token j), itself only if its own bit is set.  Returns (out
-    [T, Hq, d], lse fp32 [T, Hq]); rows from cu_q[B] on are not written."""
-    if type(max_q) is not int:
-        max_q = operator.index(max_q)
-    if scale is not None and type(scale) is not float:
-        scale = float(scale)
-    try:
-        key = ("tree", _of(q), _of(k_cache), _of(v_cache), _of(page_table), _of(cu_q), _of(kv_len),
-               _of(mask), max_q, scale)
-    except AttributeError:  # not tensors: the checks say which
-        key = None
-    dev, dtype, shape, lse_shape, need, dense, args, flags = _plans.get(key) or _tree_plan(
-        key, q, k_cache, v_cache, page_table, cu_q, kv_len, mask, max_q, scale)
-    out, o_st, lse, workspace = _outputs(q, out, lse, workspace, dev, dtype, shape, lse_shape, need,
-                                         dense, stream)
-    _call("attn_fwd_tree", dev, stream, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
-          page_table.data_ptr(), cu_q.data_ptr(), kv_len.data_ptr(), mask.data_ptr(), out.data_ptr(),
-          lse.data_ptr(), *args, o_st, *flags, workspace.data_ptr(), workspace.nbytes)
-    return out, lse
-
-
-def _outputs(q, out, lse, workspace, dev, dtype, shape, lse_shape, need, dense, stream):
-    """(out, its strides, lse, workspace) of an attention call: as given, or new."""
-    o_st = dense
-    if out is None:
-        out = _empty(shape, dtype, dev, stream)
-    else:
-        _check_half("out", out, len(shape), dtype, dev)
-        if out.shape != q.shape:
-            raise ValueError("out must have q's shape")
-        o_st = _outer(out)
-    if lse is None:
-        lse = _empty(lse_shape, torch.float32, dev, stream)
-    else:
-        _check_plain("lse", lse, torch.float32, lse_shape, dev)
-    if workspace is None:
-        workspace = _empty(need, torch.uint8, dev, stream)
-    return out, o_st, lse, workspace
-
-
-def _cache_checks(k_cache, v_cache, dev):
-    """(pages, heads, page size, d) of the two pools."""
-    dtype, at = _first_half("k_cache", k_cache, 4)
-    if at != dev:
-        raise ValueError("k_cache is on CUDA device %d, the lists on %d" % (at, dev))
-    _check_half("v_cache", v_cache, 4, dtype, dev)
-    pages, Hk, page, d = k_cache.shape
-    if v_cache.shape != k_cache.shape:
-        raise ValueError("k_cache and v_cache must have one shape, got %s %s"
-                         % (tuple(k_cache.shape), tuple(v_cache.shape)))
-    if d not in (64, 96, 128, 256):
-        raise ValueError("head dimension must be 64, 96, 128 or 256, got %d" % d)
-    if page < 16 or page & (page - 1):
-        raise ValueError("page size must be a power of two, 16 or more, got %d" % page)
-    return pages, Hk, page, d
-
-
-def _keep_plan(key, k_cache, v_cache, page_table, cu_q, kv_len, kept, kept_len):
-    dev = _list_device("kv_len", kv_len)
-    pages, Hk, page, d = _cache_checks(k_cache, v_cache, dev)
-    if kv_len.dim() != 1 or not isinstance(page_table, _Tensor) or page_table.dim() != 2 \
-            or not isinstance(kept, _Tensor) or kept.dim() != 2:
-        raise ValueError("kv_len [B], page_table [B, pages] and kept [B, tokens] do not match")
-    B, max_pages, m = kv_len.shape[0], page_table.shape[1], kept.shape[1]
-    _ints("page_table", page_table, (B, max_pages), dev)
-    _ints("kept", kept, (B, m), dev)
-    _ints("kept_len", kept_len, (B,), dev)
-    _ints("cu_q", cu_q, (B + 1,), dev)
-    return _keep(key, (dev, (B,), (B, Hk, d, pages, page, max_pages,
-                                   page_table.stride(0) if B > 1 else max_pages, m,
-                                   kept.stride(0) if B > 1 else m, _outer(k_cache), _outer(v_cache))))
+    sequence's token j), itself only if its own bit is set.  The workspace is
+    attn_fwd_paged's.  Returns (out [T, Hq, d], lse fp32 [T, Hq]); rows from
+    cu_q[B] on are not written."""
+    return (_binding or _native()).attn_fwd_tree(q, k_cache, v_cache, page_table, cu_q, kv_len, mask,
+                                                 max_q, scale, workspace, out, lse, stream)
 
 
 def kv_keep(k_cache, v_cache, page_table, cu_q, kv_len, kept, kept_len, kv_len_out=None, stream=None):
@@ -1048,44 +963,13 @@ def kv_keep(k_cache, v_cache, page_table, cu_q, kv_len, kept, kept_len, kv_len_o
     ``kept_len[b]`` (int32 [B]) of row b; the lists and caches are as in
     kv_append.  Returns kv_len_out int32 [B] (kv_len itself for in place): the
     sequences' keys afterwards."""
-    try:
-        key = ("keep", _of(k_cache), _of(v_cache), _of(page_table), _of(cu_q), _of(kv_len), _of(kept),
-               _of(kept_len))
-    except AttributeError:  # not tensors: the checks say which
-        key = None
-    dev, shape, args = _plans.get(key) or _keep_plan(key, k_cache, v_cache, page_table, cu_q, kv_len, kept,
-                                                     kept_len)
-    if kv_len_out is None:
-        kv_len_out = _empty(shape, torch.int32, dev, stream)
-    else:
-        _check_plain("kv_len_out", kv_len_out, torch.int32, shape, dev)
-    _call("fattn_kv_keep", dev, stream, k_cache.data_ptr(), v_cache.data_ptr(), page_table.data_ptr(),
-          cu_q.data_ptr(), kv_len.data_ptr(), kept.data_ptr(), kept_len.data_ptr(),
-          kv_len_out.data_ptr(), *args)
-    return kv_len_out
+    return (_binding or _native()).kv_keep(k_cache, v_cache, page_table, cu_q, kv_len, kept, kept_len,
+                                           kv_len_out, stream)
 
 
 def kv_fork_workspace_size(B: int, max_pages: int, num_pages: int) -> int:
     """Scratch bytes kv_fork needs."""
-    return int(load().fattn_kv_fork_workspace_size(B, max_pages, num_pages))
-
-
-def _fork_plan(key, k_cache, v_cache, page_table, kv_len, page_refs, parents, cu_q):
-    dev = _list_device("kv_len", kv_len)
-    pages, Hk, page, d = _cache_checks(k_cache, v_cache, dev)
-    if kv_len.dim() != 1 or not isinstance(page_table, _Tensor) or page_table.dim() != 2:
-        raise ValueError("kv_len [B] and page_table [B, pages] do not match")
-    B, max_pages = kv_len.shape[0], page_table.shape[1]
-    _ints("page_table", page_table, (B, max_pages), dev)
-    _check_plain("page_refs", page_refs, torch.int32, (pages,), dev)
-    if parents is not None:
-        _ints("parents", parents, (B,), dev)
-    if cu_q is not None:
-        _ints("cu_q", cu_q, (B + 1,), dev)
-    need = max(kv_fork_workspace_size(B, max_pages, pages), 16)
-    row = page_table.stride(0) if B > 1 else max_pages
-    return _keep(key, (dev, (B, max_pages), (B,), (pages,), need, (B, Hk, d, pages, page, max_pages, row),
-                       (_outer(k_cache), _outer(v_cache))))
+    return int(load().fattn_kv_fork_workspace_size(*map(operator.index, (B, max_pages, num_pages))))
 
 
 def kv_fork(k_cache, v_cache, page_table, kv_len, page_refs, parents=None, cu_q=None,
@@ -1104,62 +988,14 @@ def kv_fork(k_cache, v_cache, page_table, kv_len, page_refs, parents=None, cu_q=
     may be given, its input itself for in place; the caches are changed in
     place.  kv_len_out counts the new tokens, as kv_append and the attention
     take it."""
-    try:
-        key = ("fork", _of(k_cache), _of(v_cache), _of(page_table), _of(kv_len), _of(page_refs),
-               _of(parents), _of(cu_q))
-    except AttributeError:  # not tensors: the checks say which
-        key = None
-    dev, table_shape, shape, refs_shape, need, sizes, strides = _plans.get(key) or _fork_plan(
-        key, k_cache, v_cache, page_table, kv_len, page_refs, parents, cu_q)
-    row = table_shape[1]
-    if page_table_out is None:
-        page_table_out = _empty(table_shape, torch.int32, dev, stream)
-    else:
-        _ints("page_table_out", page_table_out, table_shape, dev)
-        row = page_table_out.stride(0) if table_shape[0] > 1 else row
-    if kv_len_out is None:
-        kv_len_out = _empty(shape, torch.int32, dev, stream)
-    else:
-        _check_plain("kv_len_out", kv_len_out, torch.int32, shape, dev)
-    if page_refs_out is None:
-        page_refs_out = _empty(refs_shape, torch.int32, dev, stream)
-    else:
-        _check_plain("page_refs_out", page_refs_out, torch.int32, refs_shape, dev)
-    if workspace is None:
-        workspace = _empty(need, torch.uint8, dev, stream)
-    _call("fattn_kv_fork", dev, stream, k_cache.data_ptr(), v_cache.data_ptr(), page_table.data_ptr(),
-          kv_len.data_ptr(), page_refs.data_ptr(), _ptr(parents), _ptr(cu_q), page_table_out.data_ptr(),
-          kv_len_out.data_ptr(), page_refs_out.data_ptr(), *sizes, row, *strides, workspace.data_ptr(),
-          workspace.nbytes)
-    return page_table_out, kv_len_out, page_refs_out
+    return (_binding or _native()).kv_fork(k_cache, v_cache, page_table, kv_len, page_refs, parents, cu_q,
+                                           page_table_out, kv_len_out, page_refs_out, workspace, stream)
 
 
 def cross_workspace_size(Hq: int, Hk: int, Nq: int, d: int, device=None) -> int:
     """Scratch bytes attn_fwd_cross needs for these heads and Nq queries."""
     return _workspace_bytes("attn_fwd_cross_workspace_size", _device_index(device),
                             *map(operator.index, (Hq, Hk, Nq, d)))
-
-
-def _cross_plan(key, q, k, v, kv_len, scale):
-    dtype, dev = _first_half("q", q, 4)
-    _check_half("k", k, 4, dtype, dev)
-    _check_half("v", v, 4, dtype, dev)
-    B, Hq, Nq, d = q.shape
-    Hk, Nk = k.shape[1], k.shape[2]
-    if d not in (64, 96, 128):
-        raise ValueError("head dimension must be 64, 96 or 128, got %d" % d)
-    if tuple(k.shape) != (B, Hk, Nk, d) or v.shape != k.shape:
-        raise ValueError("k and v must both be [%d, Hk, Nk, %d], got %s %s"
-                         % (B, d, tuple(k.shape), tuple(v.shape)))
-    if Hk == 0 or Hq % Hk or Hq > 128 * Hk:
-        raise ValueError("Hq must be 1 to 128 times Hk, got %d and %d" % (Hq, Hk))
-    if kv_len is not None:
-        _check_plain("kv_len", kv_len, torch.int32, (B,), dev)
-    need = _workspace_bytes("attn_fwd_cross_workspace_size", dev, Hq, Hk, Nq, d)
-    dense = (ctypes.c_longlong * 3)(Hq * Nq * d, Nq * d, d)
-    return _keep(key, (dev, dtype, (B, Hq, Nq, d), (B, Hq, Nq), max(need, 16), dense,
-                       (B, Hq, Hk, Nq, Nk, d, _outer(q), _outer(k), _outer(v)),
-                       (default_scale(d) if scale is None else scale, _HALF[dtype])))
 
 
 def attn_fwd_cross(q, k, v, kv_len=None, scale: float | None = None, workspace=None, out=None,
@@ -1171,19 +1007,7 @@ def attn_fwd_cross(q, k, v, kv_len=None, scale: float | None = None, workspace=N
     each sequence, what is behind them may hold anything (None: Nk).  A sequence
     without keys gives o = 0 and lse = -inf.  Returns (out [B, Hq, Nq, d], lse
     fp32 [B, Hq, Nq])."""
-    if scale is not None and type(scale) is not float:
-        scale = float(scale)
-    try:
-        key = ("cross", _of(q), _of(k), _of(v), _of(kv_len), scale)
-    except AttributeError:  # not tensors: the checks say which
-        key = None
-    dev, dtype, shape, lse_shape, need, dense, args, flags = _plans.get(key) or _cross_plan(
-        key, q, k, v, kv_len, scale)
-    out, o_st, lse, workspace = _outputs(q, out, lse, workspace, dev, dtype, shape, lse_shape, need,
-                                         dense, stream)
-    _call("attn_fwd_cross", dev, stream, q.data_ptr(), k.data_ptr(), v.data_ptr(), _ptr(kv_len),
-          out.data_ptr(), lse.data_ptr(), *args, o_st, *flags, workspace.data_ptr(), workspace.nbytes)
-    return out, lse
+    return (_binding or _native()).attn_fwd_cross(q, k, v, kv_len, scale, workspace, out, lse, stream)
 
 
 def cross_bwd_workspace_size(B: int, Hq: int, Hk: int, Nq: int, Nk: int, d: int, device=None) -> int:
@@ -1199,29 +1023,8 @@ def attn_bwd_cross(q, k, v, o, lse, do, kv_len=None, scale: float | None = None,
     q's and k's shapes, any strides with a contiguous last dimension (lse
     contiguous).  Rows of dk and dv behind a sequence's last key are zeros.
     Returns (dq, dk, dv) in the inputs' type, each of which may be given."""
-    if scale is not None and type(scale) is not float:
-        scale = float(scale)
-    try:
-        key = ("cross", _of(q), _of(k), _of(v), _of(kv_len), scale)
-    except AttributeError:  # not tensors: the checks say which
-        key = None
-    dev, dtype, shape, lse_shape, _, dense, args, flags = _plans.get(key) or _cross_plan(
-        key, q, k, v, kv_len, scale)
-    for name, t in (("o", o), ("do", do)):
-        _check_half(name, t, 4, dtype, dev)
-        if tuple(t.shape) != shape:
-            raise ValueError("%s must have q's shape" % name)
-    _check_plain("lse", lse, torch.float32, lse_shape, dev)
-    dq, dk, dv = (_like(name, out, t, dtype, dev, stream)
-                  for name, out, t in (("dq", dq, q), ("dk", dk, k), ("dv", dv, v)))
-    if workspace is None:
-        workspace = _empty(max(_workspace_bytes("attn_bwd_cross_workspace_size", dev, *args[:6]), 16),
-                           torch.uint8, dev, stream)
-    _call("attn_bwd_cross", dev, stream, q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(),
-          lse.data_ptr(), do.data_ptr(), _ptr(kv_len), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(),
-          *args, _outer(o), _outer(do), _outer(dq), _outer(dk), _outer(dv), *flags,
-          workspace.data_ptr(), workspace.nbytes)
-    return dq, dk, dv
+    return (_binding or _native()).attn_bwd_cross(q, k, v, o, lse, do, kv_len, scale, dq, dk, dv, workspace,
+                                                  stream)
 
 
 def version() -> str:
