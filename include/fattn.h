@@ -610,15 +610,15 @@ fattn_status_t fattn_tree_mask(const int *parents, const int *cu_q, const int *k
  * behind it -- go to one: p itself where parents[p] = p, else the first child.
  * Every other child gets a page of its own for the partly filled one, with its
  * filled slots copied in both caches.  Then each sequence gets pages for what it
- * lacks up to ceil(kv_len_out / page_size): the lowest free pages (those whose
+ * lacks from kv_len[p] / page_size up to ceil(kv_len_out / page_size): the lowest free pages (those whose
  * count is 0 when all entries have changed hands), in the order of sequences and
  * columns.  Other entries of page_table_out are -1, which in a table stands for
  * no page.
  *
  * Out of range (a parent is taken for b itself, kv_len brought to 0 .. max_pages
  * * page_size, n_b to what the table has room for and at least 0, an entry
- * outside [-1, num_pages) for -1, a partly filled page that is not there for an
- * unfilled one) or out of free pages (the entries become -1): FATTN_ERR_INDEX
+ * outside [-1, num_pages) for -1; no page where the parent has keys) or out of
+ * free pages (the entries become -1): FATTN_ERR_INDEX
  * (role 11) is recorded.  The lists are read when the kernels run, so a captured
  * graph follows them.  Equal calls give equal bits.  workspace: device, 16-byte
  * aligned, fattn_kv_fork_workspace_size(...) bytes; contents ignored on entry,

@@ -1949,16 +1949,14 @@ fattn_status_t fattn_kv_keep(void *k_cache, void *v_cache, const int *page_table
 // Workspace of a fork: per-sequence lists, counts, the free list and copies of
 // a table and lengths that are overwritten in place.
 struct ForkWs {
-    size_t copies, lacks, counts, lens, list, stage, bytes;
+    size_t copies, counts, list, stage, bytes;
 };
 static ForkWs fork_ws(int B, int max_pages, int num_pages)
 {
     ForkWs w;
-    w.copies = align_up(static_cast<size_t>(B) * 4, kWsAlign);  // first before it
-    w.lacks = align_up(w.copies + static_cast<size_t>(B) * 16, kWsAlign);
-    w.lens = align_up(w.lacks + static_cast<size_t>(B) * 4, kWsAlign);
-    w.counts = align_up(w.lens + static_cast<size_t>(B) * 4, kWsAlign);
-    w.list = align_up(w.counts + fattn::kForkRanks * 4, kWsAlign);
+    w.copies = align_up(static_cast<size_t>(B) * 5 * fattn::kForkRanks * 4, kWsAlign);  // seqs before it
+    w.counts = align_up(w.copies + static_cast<size_t>(B) * 16, kWsAlign);
+    w.list = align_up(w.counts + (fattn::kForkRanks + 1) * 4, kWsAlign);
     w.stage = align_up(w.list + static_cast<size_t>(num_pages) * 4, kWsAlign);
     w.bytes = w.stage + static_cast<size_t>(B) * max_pages * 4;
     return w;
@@ -2069,10 +2067,8 @@ fattn_status_t fattn_kv_fork(void *k_cache, void *v_cache, const int *page_table
     a.table_out = page_table_out;
     a.len_out = kv_len_out;
     a.refs_out = page_refs_out;
-    a.first = reinterpret_cast<int *>(base);
+    a.seqs = reinterpret_cast<int *>(base);
     a.copies = reinterpret_cast<int4 *>(base + ws.copies);
-    a.lacks = reinterpret_cast<int *>(base + ws.lacks);
-    a.stage_len = reinterpret_cast<int *>(base + ws.lens);
     a.counts = reinterpret_cast<int *>(base + ws.counts);
     a.free_list = reinterpret_cast<int *>(base + ws.list);
     a.stage = reinterpret_cast<int *>(base + ws.stage);
@@ -2080,7 +2076,7 @@ fattn_status_t fattn_kv_fork(void *k_cache, void *v_cache, const int *page_table
     copy_strides(a.vc_st, cache[1]);
     a.table_stride = page_table_stride;
     a.table_out_stride = page_table_out_stride;
-    a.staged = page_table_out == page_table || kv_len_out == kv_len;
+    a.staged = page_table_out == page_table;
     a.B = B;
     a.H = rows ? Hk : 0;
     a.d = d;

@@ -234,14 +234,14 @@ struct KvForkArgs {
     const int *parents, *cu_q;  // each may be null
     int *table_out, *len_out, *refs_out;
     uint32_t *status;
-    // Workspace, [B] each but counts [kForkRanks], free_list [num_pages] and,
-    // where an output is its input (staged), stage [B][max_pages].
-    int *first, *lacks, *counts, *free_list, *stage, *stage_len;
-    int4 *copies;  // source page (or -1), copy, filled slots, column
+    // Workspace: [kForkRanks][5][B], [kForkRanks + 1], [num_pages] and,
+    // where an output is its input (staged), [B][max_pages].
+    int *seqs, *counts, *free_list, *stage;
+    int4 *copies;  // [B]: source page (or -1), copy (or -1), filled slots, unused
     long long kc_st[3], vc_st[3], table_stride, table_out_stride;
     int staged;
     int B, H, d, num_pages, page_shift, max_pages;
-    int chunks;  // filled in by the launch
+    int chunks, in_shared;  // filled in by the launch
 };
 cudaError_t launch_kv_fork(const KvForkArgs &a, cudaStream_t stream);
 

@@ -33,7 +33,7 @@ using namespace ptx;
 
 // ------------------------------------------------------------------ keep
 constexpr int kKeepThreads = 256;
-constexpr int kKeepBatch = 4;  // 16-byte pieces of a thread in flight
+constexpr int kKeepBatch = 8;  // 16-byte pieces of a thread in flight
 
 // A block: one sequence, some heads, one of the two caches; a cluster: a
 // sequence, so that its length is written (in place, too) behind every reading.
@@ -111,65 +111,23 @@ __global__ void __launch_bounds__(kKeepThreads) kv_keep_kernel(const KvKeepArgs 
 }
 
 // ------------------------------------------------------------------ fork
-constexpr int kForkThreads = 512;
+constexpr int kForkThreads = 1024;
 constexpr int kForkWarps = kForkThreads / 32;
+constexpr int kForkSmall = 4096;
+constexpr int kForkRecount = 32 * kForkThreads;
+constexpr int kForkBatch = 8;  // 32-column runs of rows that a warp has in flight
 
-// What becomes of a sequence.
-struct Next {
-    int parent;  // -1: none
-    bool keeps;  // goes on with the parent's own pages
-    int whole;   // pages that it shares (or keeps) whole
-    int part;    // filled slots of the page behind them
-    int total, want;  // keys and pages afterwards
-    bool bad;
+// The sequences' lists, in range, and what follows from them.  Every block has
+// all of them, in shared memory where they fit, else in its own part of the
+// workspace.
+struct Seqs {
+    int *parent;  // -1: none
+    int *base;    // the parent's keys
+    int *total;   // keys afterwards
+    int *heir;    // of a parent: the child that keeps its pages, -1: itself
+    int *given;   // where its new pages begin among all that are given out
 };
-__device__ __forceinline__ int parent_of(const KvForkArgs &a, int b, bool &bad)
-{
-    const int p = a.parents != nullptr ? a.parents[b] : b;
-    bad = p < -1 || p >= a.B;
-    return bad ? b : p;
-}
-__device__ __forceinline__ Next next_of(const KvForkArgs &a, const int *old_len, int b)
-{
-    Next x;
-    x.parent = parent_of(a, b, x.bad);
-    x.keeps = x.parent >= 0 && __ldcg(&a.first[x.parent]) == b;
-    const long long max_keys = static_cast<long long>(a.max_pages) << a.page_shift;
-    long long base = 0;
-    if (x.parent >= 0) {
-        const int L = __ldcg(&old_len[x.parent]);
-        base = min(max(static_cast<long long>(L), 0LL), max_keys);
-        x.bad = x.bad || base != L;
-    }
-    long long total = base;
-    if (a.cu_q != nullptr) {
-        const long long n = static_cast<long long>(a.cu_q[b + 1]) - a.cu_q[b];
-        total = min(base + max(n, 0LL), max_keys);
-        x.bad = x.bad || n < 0 || total != base + n;
-    }
-    x.whole = static_cast<int>(base >> a.page_shift);
-    x.part = static_cast<int>(base & ((1 << a.page_shift) - 1));
-    x.total = static_cast<int>(total);
-    x.want = static_cast<int>((total + (1 << a.page_shift) - 1) >> a.page_shift);
-    return x;
-}
 
-// Sum over the block; every thread gets it.
-__device__ __forceinline__ int block_sum(int x, int *scratch)
-{
-#pragma unroll
-    for (int o = 16; o > 0; o /= 2)
-        x += __shfl_xor_sync(0xffffffffu, x, o);
-    __syncthreads();
-    if (threadIdx.x % 32 == 0)
-        scratch[threadIdx.x / 32] = x;
-    __syncthreads();
-    int sum = 0;
-#pragma unroll
-    for (int w = 0; w < kForkWarps; ++w)
-        sum += scratch[w];
-    return sum;
-}
 // Exclusive prefix over the block's threads, and the total.
 __device__ __forceinline__ int block_prefix(int x, int *scratch, int &total)
 {
@@ -184,27 +142,29 @@ __device__ __forceinline__ int block_prefix(int x, int *scratch, int &total)
     if (lane == 31)
         scratch[warp] = incl;
     __syncthreads();
-    int before = incl - x;
-    total = 0;
+    int w = scratch[lane];
 #pragma unroll
-    for (int w = 0; w < kForkWarps; ++w) {
-        before += w < warp ? scratch[w] : 0;
-        total += scratch[w];
+    for (int o = 1; o < 32; o *= 2) {
+        const int y = __shfl_up_sync(0xffffffffu, w, o);
+        w += lane >= o ? y : 0;
     }
-    return before;
+    total = __shfl_sync(0xffffffffu, w, 31);
+    const int before = __shfl_sync(0xffffffffu, w, max(warp - 1, 0));
+    return incl - x + (warp > 0 ? before : 0);
 }
+static_assert(kForkWarps == 32, "a warp scans the warps' sums");
 
-// The lists.  What one step writes the next reads past the first-level cache.
-// Blocks of the one cluster meet between the steps; rows and pages
-// are dealt to the cluster's warps and blocks.
+// The lists, by one cluster of blocks that meet between the steps (or one block,
+// where they are short).  What another block has written is read past the
+// first-level cache.
 __global__ void __launch_bounds__(kForkThreads) kv_fork_kernel(const KvForkArgs a)
 {
+    extern __shared__ int shared[];
     __shared__ int scratch[kForkWarps];
     cg::cluster_group cluster = cg::this_cluster();
     const int rank = blockIdx.x, ranks = gridDim.x;
     const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
     const int all = rank * kForkThreads + tid, threads = ranks * kForkThreads;
-    const int my_warp = rank * kForkWarps + warp, warps = ranks * kForkWarps;
     grid_launch_dependents();
     grid_dependency_wait();
     auto meet = [&]() {
@@ -213,100 +173,143 @@ __global__ void __launch_bounds__(kForkThreads) kv_fork_kernel(const KvForkArgs 
         else
             __syncthreads();
     };
+    int *mem = a.in_shared ? shared : a.seqs + static_cast<long long>(rank) * 5 * a.B;
+    const Seqs s{mem, mem + a.B, mem + 2LL * a.B, mem + 3LL * a.B, mem + 4LL * a.B};
+    const int page = 1 << a.page_shift;
+    const long long max_keys = static_cast<long long>(a.max_pages) << a.page_shift;
+    auto heir_of = [&](int p) { return *static_cast<volatile int *>(&s.heir[p]); };
+    auto keeps = [&](int b, int p) { return p >= 0 && (p == b || heir_of(p) == b); };
+    auto in_pool = [&](int e) { return e >= 0 && e < a.num_pages; };
     bool bad = false;
-    // 1. Copies of what is overwritten in place; counts; no child yet.
-    const int *old_table = a.page_table, *old_len = a.kv_len;
+    // 1. The lists, checked; each parent's heir; copies of what is overwritten in
+    // place, and the counts.
+    for (int b = tid; b < a.B; b += kForkThreads) {
+        const int p = a.parents != nullptr ? a.parents[b] : b;
+        const bool stray = p < -1 || p >= a.B;
+        s.parent[b] = stray ? b : p;
+        const int L = a.kv_len[b];
+        const long long n = a.cu_q != nullptr ? static_cast<long long>(a.cu_q[b + 1]) - a.cu_q[b] : 0;
+        s.total[b] = static_cast<int>(min(max(n, 0LL), max_keys));  // of the new tokens, so far
+        s.given[b] = static_cast<int>(min(max(static_cast<long long>(L), 0LL), max_keys));  // own keys
+        s.heir[b] = 0x7fffffff;
+        bad = bad || stray || s.given[b] != L || s.total[b] != n;
+    }
+    const int *old_table = a.page_table;
     long long old_stride = a.table_stride;
     if (a.staged) {
-        for (int b = my_warp; b < a.B; b += warps)
-            for (int c = lane; c < a.max_pages; c += 32)
-                a.stage[static_cast<long long>(b) * a.max_pages + c] = a.page_table[b * a.table_stride + c];
-        for (int b = all; b < a.B; b += threads)
-            a.stage_len[b] = a.kv_len[b];
+        const long long cells = static_cast<long long>(a.B) * a.max_pages;
+        for (long long i = all; i < cells; i += threads) {
+            const long long b = i / a.max_pages;
+            a.stage[i] = a.page_table[b * a.table_stride + (i - b * a.max_pages)];
+        }
         old_table = a.stage;
-        old_len = a.stage_len;
         old_stride = a.max_pages;
     }
     if (a.refs_out != a.refs)
         for (int i = all; i < a.num_pages; i += threads)
             a.refs_out[i] = a.refs[i];
-    for (int b = all; b < a.B; b += threads)
-        a.first[b] = 0x7fffffff;
-    meet();
-    // 2. Each parent's page owner: itself (as -1, below all), or the first child.
-    for (int b = all; b < a.B; b += threads) {
-        bool stray;
-        const int p = parent_of(a, b, stray);
+    __syncthreads();
+    for (int b = tid; b < a.B; b += kForkThreads) {
+        const int p = s.parent[b];
         if (p >= 0)
-            atomicMin(&a.first[p], p == b ? -1 : b);
+            atomicMin(&s.heir[p], p == b ? -1 : b);
+        const int base = p >= 0 ? s.given[p] : 0;
+        const long long total = static_cast<long long>(base) + s.total[b];
+        s.base[b] = base;
+        s.total[b] = static_cast<int>(min(total, max_keys));
+        bad = bad || total > max_keys;
     }
     meet();
-    for (int b = all; b < a.B; b += threads)
-        if (__ldcg(&a.first[b]) == -1)
-            a.first[b] = b;
-    meet();
-    // 3. The new rows as far as they follow from the old ones, the counts, and
-    // how many pages each lacks.
-    for (int b = my_warp; b < a.B; b += warps) {
-        const Next x = next_of(a, old_len, b);
-        bad = bad || x.bad;
-        const int *mine = old_table + b * old_stride;
-        const int *theirs = x.parent >= 0 ? old_table + x.parent * old_stride : mine;
-        const bool same = x.parent == b;
-        int lacks = 0;
-        for (int c0 = 0; c0 < a.max_pages; c0 += 32) {
-            const int c = c0 + lane;
-            int e = -1, was = -1;
-            if (c < a.max_pages) {
-                was = __ldcg(&mine[c]);
-                if (x.parent >= 0 && (x.keeps || c < x.whole))
-                    e = __ldcg(&theirs[c]);
-                bad = bad || was < -1 || was >= a.num_pages;
-                was = was >= a.num_pages ? -1 : was;
-                e = e >= a.num_pages ? -1 : max(e, -1);
-                a.table_out[b * a.table_out_stride + c] = e;
-                if (!same) {
-                    if (was >= 0)
-                        atomicSub(&a.refs_out[was], 1);
-                    if (e >= 0)
-                        atomicAdd(&a.refs_out[e], 1);
-                }
+    // 2. The new rows as far as they follow from the old ones, and the counts: the
+    // block's own rows, a warp some runs of 32 columns at a time.
+    const int row0 = static_cast<int>(static_cast<long long>(a.B) * rank / ranks);
+    const int row1 = static_cast<int>(static_cast<long long>(a.B) * (rank + 1) / ranks);
+    const int runs = (a.max_pages + 31) / 32;
+    const long long items = static_cast<long long>(row1 - row0) * runs;
+    for (long long i0 = static_cast<long long>(warp) * kForkBatch; i0 < items; i0 += kForkWarps * kForkBatch) {
+        int mine[kForkBatch], theirs[kForkBatch], row[kForkBatch], col[kForkBatch];
+        int at = static_cast<int>(i0 / runs), run = static_cast<int>(i0 - static_cast<long long>(at) * runs);
+#pragma unroll
+        for (int k = 0; k < kForkBatch; ++k) {
+            mine[k] = theirs[k] = -1;
+            const int b = row[k] = row0 + at, c = col[k] = run * 32 + lane;
+            if (++run == runs) {
+                run = 0;
+                ++at;
             }
-            lacks += __popc(__ballot_sync(0xffffffffu, c < x.want && e < 0));
+            if (i0 + k < items && c < a.max_pages) {
+                const int p = s.parent[b];
+                mine[k] = __ldcg(&old_table[b * old_stride + c]);
+                if (p >= 0)
+                    theirs[k] = p == b ? mine[k] : __ldcg(&old_table[p * old_stride + c]);
+            }
         }
-        if (lane == 0) {
-            a.lacks[b] = lacks;
-            a.len_out[b] = x.total;
-            // The page to copy, if any; its place is filled in below.
-            int src = -1;
-            if (x.parent >= 0 && !x.keeps && x.part > 0) {
-                src = __ldcg(&theirs[x.whole]);
-                if (src < 0 || src >= a.num_pages) {
-                    src = -1;
-                    bad = true;
-                }
+#pragma unroll
+        for (int k = 0; k < kForkBatch; ++k) {
+            const int b = row[k], c = col[k];
+            if (i0 + k >= items || c >= a.max_pages)
+                continue;
+            const int p = s.parent[b], base = s.base[b], whole = base >> a.page_shift;
+            const bool kept = keeps(b, p);
+            const int e = in_pool(theirs[k]) && (kept || c < whole) ? theirs[k] : -1;
+            a.table_out[b * a.table_out_stride + c] = e;
+            if (p != b) {
+                if (in_pool(mine[k]))
+                    atomicSub(&a.refs_out[mine[k]], 1);
+                if (e >= 0)
+                    atomicAdd(&a.refs_out[e], 1);
             }
-            a.copies[b] = make_int4(src, -1, x.part, x.whole);
+            // An entry of no page, or none where the parent has keys.
+            bad = bad || (mine[k] != -1 && !in_pool(mine[k])) ||
+                  (p >= 0 && static_cast<long long>(c) * page < base && !in_pool(theirs[k]));
         }
     }
+    // How many pages each sequence lacks behind its whole ones, and where those
+    // begin among all that are given out: every block for all sequences.
+    int need = 0;
+    for (int b0 = 0; b0 < a.B; b0 += kForkThreads) {
+        const int b = b0 + tid;
+        int lacks = 0, sum;
+        if (b < a.B) {
+            const int p = s.parent[b], whole = s.base[b] >> a.page_shift;
+            const int want = static_cast<int>((static_cast<long long>(s.total[b]) + page - 1) >> a.page_shift);
+            lacks = want - whole;
+            if (keeps(b, p))
+                for (int c = whole; c < want; ++c)
+                    lacks -= in_pool(__ldcg(&old_table[p * old_stride + c]));
+        }
+        const int k = block_prefix(lacks, scratch, sum);
+        if (b < a.B)
+            s.given[b] = need + k;
+        need += sum;
+    }
     meet();
-    // 4. Free pages among each block's range of them, and the lacks before its rows.
-    const int page0 = static_cast<int>(static_cast<long long>(a.num_pages) * rank / ranks);
-    const int page1 = static_cast<int>(static_cast<long long>(a.num_pages) * (rank + 1) / ranks);
-    int mine = 0, need = 0;
-    for (int i = page0 + tid; i < page1; i += kForkThreads)
-        mine += __ldcg(&a.refs_out[i]) == 0;
-    for (int b = tid; b < a.B; b += kForkThreads)
-        need += __ldcg(&a.lacks[b]);
-    mine = block_sum(mine, scratch);
-    need = block_sum(need, scratch);
-    if (tid == 0)
-        a.counts[rank] = mine;
-    meet();
+    // 3. The free pages in each block's part of them.
+    int have = 0;
     if (need > 0) {
+        const int page0 = static_cast<int>(static_cast<long long>(a.num_pages) * rank / ranks);
+        const int page1 = static_cast<int>(static_cast<long long>(a.num_pages) * (rank + 1) / ranks);
+        auto free_pages = [&](int from, int to) {
+            int n = 0, sum;
+#pragma unroll 4
+            for (int i = from + tid; i < to; i += kForkThreads)
+                n += __ldcg(&a.refs_out[i]) == 0;
+            block_prefix(n, scratch, sum);
+            return sum;
+        };
+        // Those of the blocks before: counted again while that is less than
+        // another meeting.
         int at = 0;
-        for (int r = 0; r < rank; ++r)
-            at += __ldcg(&a.counts[r]);
+        if (rank > 0 && a.num_pages <= kForkRecount) {
+            at = free_pages(0, page0);
+        } else if (ranks > 1 && a.num_pages > kForkRecount) {
+            const int n = free_pages(page0, page1);
+            if (tid == 0)
+                a.counts[rank] = n;
+            meet();
+            for (int r = 0; r < rank; ++r)
+                at += __ldcg(&a.counts[r]);
+        }
         for (int i0 = page0; i0 < page1 && at < need; i0 += kForkThreads) {
             const int i = i0 + tid;
             const bool is = i < page1 && __ldcg(&a.refs_out[i]) == 0;
@@ -316,50 +319,43 @@ __global__ void __launch_bounds__(kForkThreads) kv_fork_kernel(const KvForkArgs 
                 a.free_list[k] = i;
             at += found;
         }
-        // Where each row's pages begin in the list: every block all of them, in
-        // its own copy.
-        int before = 0;
-        for (int b0 = 0; b0 < a.B; b0 += kForkThreads) {
-            const int b = b0 + tid;
-            int sum;
-            const int k = block_prefix(b < a.B ? __ldcg(&a.lacks[b]) : 0, scratch, sum);
-            if (b < a.B && b % ranks == rank)
-                a.first[b] = before + k;
-            before += sum;
+        // Known to the last block: all that are needed, or all there are.
+        if (tid == 0 && rank == ranks - 1)
+            a.counts[kForkRanks] = min(at, need);
+        meet();
+        have = __ldcg(&a.counts[kForkRanks]);
+    }
+    // 4. The lacking entries, in order, and what is to be copied.
+    for (int b = row0 + warp; b < row1; b += kForkWarps) {
+        const int p = s.parent[b], base = s.base[b], whole = base >> a.page_shift, part = base & (page - 1);
+        const int want = static_cast<int>((static_cast<long long>(s.total[b]) + page - 1) >> a.page_shift);
+        const bool kept = keeps(b, p);
+        int *row = a.table_out + b * a.table_out_stride;
+        const int *old = old_table + max(p, 0) * old_stride;
+        int k = s.given[b];
+        if (lane == 0) {
+            a.len_out[b] = s.total[b];
+            // A partly filled page of a parent's that another child keeps.
+            const int src = p >= 0 && !kept && part > 0 ? __ldcg(&old[whole]) : -1;
+            a.copies[b] = make_int4(src, in_pool(src) && k < have ? __ldcg(&a.free_list[k]) : -1, part, 0);
+        }
+        for (int c0 = whole; c0 < want; c0 += 32) {
+            const int c = c0 + lane;
+            const bool lack = c < want && !(kept && in_pool(__ldcg(&old[c])));
+            const unsigned who = __ballot_sync(0xffffffffu, lack);
+            if (lack) {
+                const int at = k + __popc(who & ((1u << lane) - 1u));
+                if (at < have) {
+                    const int x = __ldcg(&a.free_list[at]);
+                    row[c] = x;
+                    a.refs_out[x] = 1;
+                } else {
+                    bad = true;
+                }
+            }
+            k += __popc(who);
         }
     }
-    int have = 0;
-    for (int r = 0; r < ranks; ++r)
-        have += __ldcg(&a.counts[r]);
-    meet();
-    // 5. The lacking entries, in order.
-    if (need > 0)
-        for (int b = my_warp; b < a.B; b += warps) {
-            if (__ldcg(&a.lacks[b]) == 0)
-                continue;
-            int at = __ldcg(&a.first[b]);
-            const int4 copy = __ldcg(&a.copies[b]);
-            const int want = (__ldcg(&a.len_out[b]) + (1 << a.page_shift) - 1) >> a.page_shift;
-            int *row = a.table_out + b * a.table_out_stride;
-            for (int c0 = 0; c0 < want; c0 += 32) {
-                const int c = c0 + lane;
-                const bool lack = c < want && __ldcg(&row[c]) < 0;
-                const unsigned who = __ballot_sync(0xffffffffu, lack);
-                if (lack) {
-                    const int k = at + __popc(who & ((1u << lane) - 1u));
-                    if (k < have) {
-                        const int page = __ldcg(&a.free_list[k]);
-                        row[c] = page;
-                        a.refs_out[page] = 1;
-                        if (c == copy.w && copy.x >= 0)
-                            a.copies[b].y = page;
-                    } else {
-                        bad = true;
-                    }
-                }
-                at += __popc(who);
-            }
-        }
     if (bad)
         atomicCAS(a.status, 0u, 6u /* FATTN_ERR_INDEX */ | (kRoleFork << 8));
 }
@@ -399,7 +395,7 @@ __global__ void __launch_bounds__(kCopyThreads) kv_fork_copy_kernel(const KvFork
 }
 
 template <class Args>
-cudaError_t start(void (*kernel)(Args), const Args &a, long long blocks, int threads, int cluster,
+cudaError_t start(void (*kernel)(Args), const Args &a, long long blocks, int threads, int cluster, size_t smem,
                   cudaStream_t stream)
 {
     if (blocks > 0x7fffffffLL)
@@ -413,6 +409,7 @@ cudaError_t start(void (*kernel)(Args), const Args &a, long long blocks, int thr
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(blocks));
     cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cfg.attrs = attrs;
     cfg.numAttrs = cluster > 1 ? 2 : 1;
@@ -428,9 +425,9 @@ cudaError_t launch_kv_keep(const KvKeepArgs &args, cudaStream_t stream)
     // eight): more while each has a batch of its threads' pieces to move at the
     // most tokens kept.
     const long long pieces = static_cast<long long>(a.max_kept) * a.H * (a.d / 8);
-    a.chunks = pieces <= kKeepThreads * kKeepBatch ? 1 : pieces <= 2 * kKeepThreads * kKeepBatch ? 2 : 4;
+    a.chunks = pieces <= kKeepThreads * kKeepBatch ? 1 : pieces <= 4 * kKeepThreads * kKeepBatch ? 2 : 4;
     a.heads_per_chunk = (a.H + a.chunks - 1) / a.chunks;
-    return start(kv_keep_kernel, a, 2LL * a.B * a.chunks, kKeepThreads, 2 * a.chunks, stream);
+    return start(kv_keep_kernel, a, 2LL * a.B * a.chunks, kKeepThreads, 2 * a.chunks, 0, stream);
 }
 
 cudaError_t launch_kv_fork(const KvForkArgs &args, cudaStream_t stream)
@@ -439,13 +436,16 @@ cudaError_t launch_kv_fork(const KvForkArgs &args, cudaStream_t stream)
     // One block up to some thousand entries: its barriers are shorter than a
     // cluster's, which has more hands for long lists.
     const long long entries = static_cast<long long>(a.B) * a.max_pages + a.num_pages;
-    const int ranks = entries <= 4096 ? 1 : kForkRanks;
-    cudaError_t e = start(kv_fork_kernel, a, ranks, kForkThreads, ranks, stream);
+    const int ranks = entries <= kForkSmall ? 1 : kForkRanks;
+    // The sequences' lists fit shared memory without asking for more of it.
+    const size_t lists = static_cast<size_t>(a.B) * 5 * sizeof(int);
+    a.in_shared = lists <= 40960;
+    cudaError_t e = start(kv_fork_kernel, a, ranks, kForkThreads, ranks, a.in_shared ? lists : 0, stream);
     if (e != cudaSuccess || a.parents == nullptr || a.H == 0)
         return e;
     const long long pieces = static_cast<long long>(a.H) * ((1 << a.page_shift) - 1) * (a.d / 8);
     a.chunks = static_cast<int>((pieces + kCopyThreads * kCopyBatch - 1) / (kCopyThreads * kCopyBatch));
-    return start(kv_fork_copy_kernel, a, 2LL * a.B * a.chunks, kCopyThreads, 1, stream);
+    return start(kv_fork_copy_kernel, a, 2LL * a.B * a.chunks, kCopyThreads, 1, 0, stream);
 }
 
 }  // namespace fattn

@@ -9,13 +9,15 @@ namespace {
 // A block a sequence, a thread a token: it walks to the tree's root, and sets
 // the bit of every token on the way.  Parents come before their children, so
 // the words of a row are finished from the last to the first and each is
-// written once.  Bound by latency: a step of the walk waits for the one before
-// (first-level cache), as many as the tree is deep; trees of up to 200 tokens in
-// 24 sequences, up to some 60 deep, take 4 us with the launch.
-constexpr int kMaskThreads = 128;
+// written once.  Bound by latency: a step of the walk waits for the one before,
+// as many as the tree is deep.  So the parents are brought into shared memory
+// first (trees that do not fit it are walked in the caches): @TIME@.
+constexpr int kMaskThreads = 256;
+constexpr int kMaskShared = 4096;
 
 __global__ void __launch_bounds__(kMaskThreads) tree_mask_kernel(const TreeMaskArgs a)
 {
+    __shared__ int near[kMaskShared];
     grid_launch_dependents();
     grid_dependency_wait();
     const int b = blockIdx.x;
@@ -25,6 +27,12 @@ __global__ void __launch_bounds__(kMaskThreads) tree_mask_kernel(const TreeMaskA
     const int n = static_cast<int>(min(static_cast<long long>(all), 32LL * a.words));
     bool bad = q0 != c0 || n != static_cast<long long>(c1) - c0 || (b == 0 && c0 != 0);
     const int *parents = a.parents + q0;
+    if (n <= kMaskShared) {
+        for (int i = threadIdx.x; i < n; i += kMaskThreads)
+            near[i] = parents[i];
+        __syncthreads();
+        parents = near;
+    }
     for (int i = threadIdx.x; i < n; i += kMaskThreads) {
         unsigned *row = a.mask + (static_cast<long long>(q0) + i) * a.words;
         int w = a.words - 1, depth = 0;
