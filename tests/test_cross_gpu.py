@@ -74,6 +74,41 @@ def test_long_keys_split_over_the_gpu(B, Hq, Hk, Nq, Nk, d):
 
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("d", [64, 96, 128])
+@pytest.mark.parametrize("G,Nq", [(1, 1), (2, 1), (1, 2), (3, 1), (1, 3), (4, 1), (2, 2), (1, 4), (5, 1)])
+def test_few_rows(G, Nq, d, dtype):
+    """One to five rows to a key head, keys around the pieces that warps, blocks
+    and clusters of them take; few heads and many."""
+    for B, Hk, Nk, lens in ((1, 1, 700, None), (2, 3, 65, [65, 64]), (1, 2, 3100, None), (3, 1, 17, [17, 0, 16]),
+                            (40, 8, 130, [i * 3 % 131 for i in range(40)]), (1, 1, 1, None)):
+        q, k, v = make(B, G * Hk, Hk, Nq, Nk, d, dtype, seed=Nk + G, lens=lens)
+        got = run(q, k, v, lens)
+        again = run(q, k, v, lens)
+        assert fattn.device_status() == 0
+        verify(got, q, k, v, lens, "%d keys" % Nk)
+        assert torch.equal(got[0], again[0]) and torch.equal(got[1], again[1])
+
+
+@pytest.mark.parametrize("Nq", [1, 40])
+def test_scores_that_are_not_finite(Nq):
+    """A NaN or +inf score makes its row NaN in both outputs, -inf counts for
+    nothing; other rows stay as they are."""
+    q, k, v = make(1, 1, 1, Nq, 200, 64, torch.float16, seed=9)
+    for bad, where in ((float("nan"), "nan"), (float("inf"), "nan"), (-float("inf"), "gone")):
+        k2 = k.clone()
+        k2[0, 0, 150] = 0
+        k2[0, 0, 150, 0] = bad
+        q2 = q.abs()
+        o, lse = run(q2, k2, v, None)
+        if where == "nan":
+            assert bool(torch.isnan(o).all()) and bool(torch.isnan(lse).all())
+        else:
+            keep = torch.arange(200) != 150
+            verify((o, lse), q2, k2[:, :, keep], v[:, :, keep], None)
+    assert fattn.device_status() == 0
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
 @pytest.mark.parametrize("fill", [float("nan"), float("inf"), -float("inf"), 3e4])
 def test_padding_may_hold_anything(fill, dtype):
     lens = [1, 100, 128, 200, 0, 255]
@@ -86,8 +121,7 @@ def test_padding_may_hold_anything(fill, dtype):
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
 def test_views_of_packed_projections(dtype):
     """q [B, Nq, Hq, d], keys and values [B, Nk, 2, Hk, d], the output a window
-    of a wider buffer whose rest stays as it was; a batch that repeats one
-    encoder (stride 0 is refused, so expanded keys are copied)."""
+    of a wider buffer whose rest stays as it was."""
     g = torch.Generator().manual_seed(5)
     B, Hq, Hk, Nq, Nk, d = 3, 6, 2, 70, 150, 128
     lens = [150, 33, 128]

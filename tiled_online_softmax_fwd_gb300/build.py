@@ -27,7 +27,8 @@ BINDING = os.path.join(BUILD, "fattn_binding.so")
 
 SOURCES = ["fattn_api.cu", "fattn_fwd_sm103.cu", "fattn_bwd_sm103.cu", "fattn_fwd_simt.cu",
            "fattn_rowops.cu", "fattn_rope.cu", "fattn_paged_sm103.cu", "fattn_tree_sm103.cu",
-           "fattn_cross_sm103.cu", "fattn_cross_bwd_sm103.cu", "fattn_pages.cu"]
+           "fattn_cross_sm103.cu", "fattn_cross_bwd_sm103.cu", "fattn_cross_few.cu",
+           "fattn_pages.cu"]
 GENCODE = ["-gencode", "arch=compute_103a,code=sm_103a"]
 EXPORTS = "{ global: attn_fwd*; attn_bwd*; fattn_*; local: *; };\n"
 

@@ -2138,13 +2138,39 @@ fattn_status_t attn_fwd_cross(const void *q, const void *k, const void *v, const
         (kv_len && overlap(workspace, ws.bytes, kv_len, len_bytes)) ||
         (Nk > 0 && (!apart(kv[0], workspace, ws.bytes) || !apart(kv[1], workspace, ws.bytes))))
         return FATTN_ERR_INVALID_ARG;
-    PFN_cuTensorMapEncodeTiled_v12000 encode;
-    if ((s = get_encoder(&encode)) != FATTN_OK)
-        return s;
     fattn::PagedArgs a = {};
     if ((s = status_word(&a.status)) != FATTN_OK)
         return s;
     const int G = Hq / Hk;
+    a.o = o;
+    a.lse = lse;
+    a.kv_len = kv_len;
+    a.o_st[0] = out.st[2];
+    a.o_st[1] = out.st[1];
+    a.o_batch = out.st[0];
+    a.B = B;
+    a.Hk = Hk;
+    a.G = G;
+    a.d = d;
+    a.f16 = dtype;
+    a.Nq = Nq;
+    a.max_keys = Nk;
+    a.sl2 = scale * 1.4426950408889634f;
+    const long long few_rows = static_cast<long long>(Nq) * G;
+    const int few = few_rows > fattn::kCrossFewRows
+                        ? 0
+                        : fattn::cross_few_splits(B, Hk, static_cast<int>(few_rows), Nk, d, info.num_sms);
+    if (few > 0) {
+        fattn::CrossFew x = {q, k, v, {}, {}, {}, static_cast<int>(few_rows), few};
+        copy_strides(x.q_st, rq);
+        copy_strides(x.k_st, kv[0]);
+        copy_strides(x.v_st, kv[1]);
+        const cudaError_t e = fattn::launch_cross_few(a, x, stream);
+        return e == cudaSuccess ? FATTN_OK : cuda_fail(e);
+    }
+    PFN_cuTensorMapEncodeTiled_v12000 encode;
+    if ((s = get_encoder(&encode)) != FATTN_OK)
+        return s;
     const int box_tokens = std::min(Nq, ws.tile_tokens), quad_tokens = std::min(Nq, 32 / G);
     fattn::PagedMaps maps;
     if ((s = make_query_map(encode, &maps.q, rq, G, box_tokens, dtype == 1)) != FATTN_OK)
@@ -2162,32 +2188,18 @@ fattn_status_t attn_fwd_cross(const void *q, const void *k, const void *v, const
             return s;
     }
     uint8_t *base = static_cast<uint8_t *>(workspace);
-    a.o = o;
-    a.lse = lse;
     a.starts = reinterpret_cast<int4 *>(base);
     a.ws_l = reinterpret_cast<float *>(base + ws.l);
     a.ws_o = reinterpret_cast<float *>(base + ws.o);
-    a.kv_len = kv_len;
-    a.o_st[0] = out.st[2];
-    a.o_st[1] = out.st[1];
-    a.o_batch = out.st[0];
     a.T = B * Nq;
-    a.B = B;
-    a.Hk = Hk;
-    a.G = G;
-    a.d = d;
-    a.f16 = dtype;
     a.max_q = Nq;
-    a.Nq = Nq;
     a.num_pages = B;
     a.page_shift = 7;  // a tile is copied whole
-    a.max_keys = Nk;
     a.tile_tokens = ws.tile_tokens;
     a.q_box_tokens = box_tokens;
     a.q_quad_tokens = quad_tokens;
     a.slot_rows = ws.slot_rows;
     a.g_inverse = (65536u + G - 1) / G;
-    a.sl2 = scale * 1.4426950408889634f;
     const cudaError_t e = fattn::launch_cross(a, maps, info.num_sms, stream);
     return e == cudaSuccess ? FATTN_OK : cuda_fail(e);
 }

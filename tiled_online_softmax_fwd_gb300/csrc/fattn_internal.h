@@ -203,6 +203,19 @@ cudaError_t launch_tree(const PagedArgs &a, const PagedMaps &maps, int num_sms, 
 // those of k and v (d, Nk, Hk, B), box (64, 128, 1, 1).
 cudaError_t launch_cross(const PagedArgs &a, const PagedMaps &maps, int num_sms, cudaStream_t stream);
 
+// The same for at most kCrossFewRows rows a key head, on the CUDA cores.  Of the
+// arguments o, lse, kv_len, status, strides, sizes and sl2 are used.
+constexpr int kCrossFewRows = 4;
+struct CrossFew {
+    const void *q, *k, *v;
+    long long q_st[3], k_st[3], v_st[3];  // batch, head, row
+    int rows;                             // Nq G
+    int splits;                           // blocks (of a cluster) that share a key head's keys
+};
+// Those blocks, or 0: the other kernel is to be taken.
+int cross_few_splits(int B, int Hk, int rows, int Nk, int d, int num_sms);
+cudaError_t launch_cross_few(const PagedArgs &a, const CrossFew &x, cudaStream_t stream);
+
 // Masks [T][words] and positions [T] of trees given by parents [T].
 struct TreeMaskArgs {
     const int *parents, *cu_q, *kv_len;
