@@ -63,19 +63,23 @@ constexpr int kUnitCost = 3, kSnap = 2, kLeast = 8;
 template <int D, bool kDkDv> struct BCfg {
     static constexpr int kChunks = (D + 63) / 64;
     static constexpr uint32_t kTileBytes = kChunks * kChunkBytes;  // one [128][D] tile
-    // Two resident tiles, then dkdv: two stages of (Q, dO); dq: three of K and
-    // two of V (V is free as soon as dP has read it, K only after dQ).
-    static constexpr int kKStages = 3, kVStages = 2;
-    static constexpr uint32_t kKRing = 2 * kTileBytes;
-    static constexpr uint32_t kVRing = kKRing + kKStages * kTileBytes;
-    static constexpr uint32_t kTilesBytes = kDkDv ? 6 * kTileBytes : kVRing + kVStages * kTileBytes;
-    static constexpr uint32_t kColAcc1 = kColAcc0 + D;
+    // Slots of the resident tiles, which take turns (K_j, V_j, K_j', ... or Q_i,
+    // dO_i, ...): at d = 64 the next unit's are there before this one ends.  Then
+    // the streamed tiles, dkdv: Q and dO; dq: K (held until dQ) and V (free as soon
+    // as dP has read it).
+    static constexpr int kRes = D == 64 ? 4 : 2;
+    static constexpr int kStages = kDkDv ? (D == 64 ? 4 : 2) : D == 64 ? 4 : 3;
+    static constexpr int kStages2 = kDkDv ? kStages : D == 64 ? 3 : 2;
+    static constexpr uint32_t kRing = kRes * kTileBytes;
+    static constexpr uint32_t kRing2 = kRing + kStages * kTileBytes;
+    static constexpr uint32_t kTilesBytes = kRing2 + kStages2 * kTileBytes;
+    // TMEM: S (dq: another S at the end), dP, and the accumulators, two sets where
+    // they fit.
+    static constexpr int kAccs = D == 64 ? 2 : 1;
+    static constexpr uint32_t kAccCols = kDkDv ? 2 * D : D;
+    static constexpr uint32_t kColS1 = kColAcc0 + kAccs * kAccCols;
+    static_assert(kDkDv ? kColS1 <= kTmemCols : kColS1 + kTile <= kTmemCols, "TMEM columns");
 };
-// dq: the S buffer of a unit's i-th key tile.
-template <int D> __device__ __forceinline__ uint32_t dq_s_col(int i)
-{
-    return (i & 1) ? kColAcc0 + D : kColS;  // the second behind the accumulator
-}
 
 // Where a CTA starts: a sequence, the cost already behind in it, and its share.
 struct Start {
@@ -83,11 +87,21 @@ struct Start {
     long long y, left;
 };
 
+// A piece of work: steps [t0, t1) of a unit.
+struct Piece {
+    int b, h, tile;  // h < 0: no more work
+    int L;           // keys of the sequence
+    int t0, t1;      // dkdv: (query head of the group, query tile); dq: key tiles
+    int slot;        // workspace slot of a partial result, or -1: the whole unit
+};
+constexpr int kPieces = 4;  // published ahead
+
 struct alignas(16) BBars {
-    uint64_t res_full, res_empty;      // the resident pair
-    uint64_t st_full[3], st_empty[3];  // dkdv: Q stages; dq: K stages
-    uint64_t v_full[2], v_empty[2];    // dkdv: dO stages; dq: V stages
-    uint64_t s_full, p_full, o_full, o_empty;
+    uint64_t res_full[4], res_empty[4];
+    uint64_t st_full[4], st_empty[4];  // dkdv: Q stages; dq: K stages
+    uint64_t v_full[4], v_empty[4];    // dkdv: dO stages; dq: V stages
+    uint64_t s_full, p_full, o_full[2], o_empty[2];
+    uint64_t piece_full[kPieces], piece_empty[kPieces];
     uint64_t p1_full, dp_full;  // dkdv: P^T written; dP^T computed
     uint64_t dp_free;           // dq: dP is in registers
     // dq: dS of the CTA's n-th tile written, on dq_full[n % 2] (a warp may be a
@@ -99,6 +113,7 @@ struct alignas(16) BBars {
     int abort;
     float ds_scale;  // of dS
     Start start;
+    Piece pieces[kPieces];
     long long warp_sum[kThreads / 32];
     float warp_max[kThreads / 32];
 };
@@ -114,21 +129,14 @@ __device__ __forceinline__ int clamp_len(const CrossBwdArgs &a, int b)
     return min(max(L, 0), a.Nk);
 }
 
-// A piece of work: steps [t0, t1) of a unit.
-struct Piece {
-    int b, h, tile;
-    int L;       // keys of the sequence
-    int t0, t1;  // dkdv: (query head of the group, query tile); dq: key tiles
-    int slot;    // workspace slot of a partial result, or -1: the whole unit
-};
-
-// Units of sequence b and the steps of each.
+// Units of a sequence with L keys, and the steps of each.  Units without steps
+// are none: the prep kernel writes their zeros.
 template <bool kDkDv>
 __device__ __forceinline__ void units_of(const CrossBwdArgs &a, int L, int &units, int &steps)
 {
     const int F = (L + kTile - 1) / kTile;
-    units = kDkDv ? a.Hk * F : a.Hk * a.G * a.Tq;
     steps = kDkDv ? a.G * a.Tq : F;
+    units = steps == 0 ? 0 : kDkDv ? a.Hk * F : a.Hk * a.G * a.Tq;
 }
 // Step that a cost of y inside a unit falls on.
 __device__ __forceinline__ int step_at(long long y, int steps)
@@ -178,8 +186,7 @@ template <bool kDkDv> __device__ __forceinline__ bool next_piece(const CrossBwdA
         w.at.y = 0;
         p.t0 = step_at(y0, w.steps);
         p.t1 = step_at(y1, w.steps);
-        // Nothing falls to this CTA (a unit without steps is its first CTA's).
-        if (w.steps == 0 ? y0 > 0 : p.t0 == p.t1)
+        if (p.t0 == p.t1)  // nothing of it falls to this CTA
             continue;
         const int per = kDkDv ? w.units / a.Hk : a.Tq;
         p.b = w.at.b;
@@ -271,6 +278,20 @@ __device__ __forceinline__ bool warp_wait(uint64_t &bar, uint32_t parity, const 
 // them (see paged_sm103.cuh).
 __device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xffffffffu, x, 0); }
 
+// The pieces, published by the producer.  The k-th, read in place; false when
+// there is none (ok) or a wait failed (!ok).  Held until given back.
+__device__ __forceinline__ bool receive(BBars &b, uint32_t k, bool &ok)
+{
+    ok = ok && warp_wait(b.piece_full[k % kPieces], (k / kPieces) & 1, &b.abort);
+    return ok && b.pieces[k % kPieces].h >= 0;
+}
+__device__ __forceinline__ void give_back(BBars &b, uint32_t k)
+{
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0)
+        mbar_arrive(smem_addr(&b.piece_empty[k % kPieces]));
+}
+
 template <bool kF16> __device__ __forceinline__ uint32_t pack2(float lo, float hi)
 {
     if constexpr (kF16) {
@@ -318,77 +339,60 @@ __device__ void bwd_load(const CrossBwdArgs &a, BBars &b, uint32_t smem, const C
     using C = BCfg<D, kDkDv>;
     const volatile int *abort = &b.abort;
     const bool leader = elect_one();
-    // A tile whose barrier is waited for and armed here.
-    auto copy = [&](uint64_t &full_bar, uint32_t dst, const CUtensorMap *map, int row, int head, int batch) {
+    uint32_t rpos = 0, kpos = 0, vpos = 0;  // resident, streamed and other streamed tiles
+    // A tile, when its slot is free.
+    auto load = [&](uint64_t *full, uint64_t *empty, uint32_t &pos, int slots, uint32_t base,
+                    const CUtensorMap *map, int row, int head, int batch) {
+        const uint32_t slot = pos % slots;
+        if (!warp_wait(empty[slot], ((pos / slots) & 1) ^ 1, abort))
+            return false;
         if (leader) {
-            const uint32_t full = smem_addr(&full_bar);
-            mbar_arrive_expect_tx(full, C::kTileBytes);
+            const uint32_t bar = smem_addr(&full[slot]), dst = smem + base + slot * C::kTileBytes;
+            mbar_arrive_expect_tx(bar, C::kTileBytes);
 #pragma unroll
             for (int c = 0; c < C::kChunks; ++c)
-                tma_load_4d(dst + c * kChunkBytes, map, full, 64 * c, row, head, batch);
+                tma_load_4d(dst + c * kChunkBytes, map, bar, 64 * c, row, head, batch);
         }
+        ++pos;
+        return true;
     };
-    uint32_t res_phase = 0, res_issued = 0, kpos = 0, vpos = 0;
     bool ok = true;
+    uint32_t k = 0;
     Walk w = first_walk<kDkDv>(a, b);
     Piece p;
-    while (ok && next_piece<kDkDv>(a, w, p)) {
-        if (p.t0 == p.t1)
-            continue;
-        if (!warp_wait(b.res_empty, res_phase ^ 1, abort)) {
-            ok = false;
+    bool more = true;
+    while (ok && more) {
+        more = next_piece<kDkDv>(a, w, p);
+        ok = warp_wait(b.piece_empty[k % kPieces], ((k / kPieces) & 1) ^ 1, abort);
+        if (!ok)
             break;
+        if (!more)
+            p.h = -1;
+        if ((threadIdx.x & 31) == 0) {
+            b.pieces[k % kPieces] = p;
+            mbar_arrive(smem_addr(&b.piece_full[k % kPieces]));
         }
-        res_phase ^= 1;
-        ++res_issued;
+        ++k;
+        if (!more)
+            break;
         const int head = uniform(p.h), batch = uniform(p.b), own = uniform(p.tile * kTile);
-        if (leader) {
-            const uint32_t full = smem_addr(&b.res_full);
-            mbar_arrive_expect_tx(full, 2 * C::kTileBytes);
-#pragma unroll
-            for (int c = 0; c < C::kChunks; ++c) {
-                tma_load_4d(smem + c * kChunkBytes, kDkDv ? mk : mq, full, 64 * c, own, head, batch);
-                tma_load_4d(smem + C::kTileBytes + c * kChunkBytes, kDkDv ? mv : mdo, full, 64 * c, own, head,
-                            batch);
-            }
-        }
-        if constexpr (kDkDv) {
-            // dO first: its slot is released (after dV) before Q's (after dK).
-            int g = p.t0 / a.Tq, i = p.t0 - g * a.Tq;
-            for (int t = p.t0; ok && t < p.t1; ++t) {
-                const uint32_t stage = kpos & 1, phase = (kpos >> 1) & 1;
-                const uint32_t dst = smem + (2 + 2 * stage) * C::kTileBytes;
+        ok = load(b.res_full, b.res_empty, rpos, C::kRes, 0, kDkDv ? mk : mq, own, head, batch) &&
+             load(b.res_full, b.res_empty, rpos, C::kRes, 0, kDkDv ? mv : mdo, own, head, batch);
+        int g = kDkDv ? p.t0 / a.Tq : 0, i = kDkDv ? p.t0 - g * a.Tq : 0;
+        for (int t = p.t0; ok && t < p.t1; ++t) {
+            if constexpr (kDkDv) {
+                // dO first: its slot is released (after dV) before Q's (after dK).
                 const int row = uniform(i * kTile), qh = uniform(p.h * a.G + g);
-                ok = warp_wait(b.v_empty[stage], phase ^ 1, abort);
-                if (!ok)
-                    break;
-                copy(b.v_full[stage], dst + C::kTileBytes, mdo, row, qh, batch);
-                ++vpos;
-                ok = warp_wait(b.st_empty[stage], phase ^ 1, abort);
-                if (!ok)
-                    break;
-                copy(b.st_full[stage], dst, mq, row, qh, batch);
-                ++kpos;
+                ok = load(b.v_full, b.v_empty, vpos, C::kStages2, C::kRing2, mdo, row, qh, batch) &&
+                     load(b.st_full, b.st_empty, kpos, C::kStages, C::kRing, mq, row, qh, batch);
                 if (++i == a.Tq) {
                     i = 0;
                     ++g;
                 }
-            }
-        } else {
-            const int kh = uniform(p.h / a.G);
-            for (int t = p.t0; ok && t < p.t1; ++t) {
-                const uint32_t ks = kpos % C::kKStages, vs = vpos % C::kVStages;
-                const int row = uniform(t * kTile);
-                ok = warp_wait(b.st_empty[ks], ((kpos / C::kKStages) & 1) ^ 1, abort);
-                if (!ok)
-                    break;
-                copy(b.st_full[ks], smem + C::kKRing + ks * C::kTileBytes, mk, row, kh, batch);
-                ++kpos;
-                ok = warp_wait(b.v_empty[vs], ((vpos / C::kVStages) & 1) ^ 1, abort);
-                if (!ok)
-                    break;
-                copy(b.v_full[vs], smem + C::kVRing + vs * C::kTileBytes, mv, row, kh, batch);
-                ++vpos;
+            } else {
+                const int row = uniform(t * kTile), kh = uniform(p.h / a.G);
+                ok = load(b.st_full, b.st_empty, kpos, C::kStages, C::kRing, mk, row, kh, batch) &&
+                     load(b.v_full, b.v_empty, vpos, C::kStages2, C::kRing2, mv, row, kh, batch);
             }
         }
     }
@@ -396,169 +400,159 @@ __device__ void bwd_load(const CrossBwdArgs &a, BBars &b, uint32_t smem, const C
         if (leader)
             fail(a, b, kRoleLoad);
         // Copies already issued land before the CTA exits.
-        const uint32_t ring = kDkDv ? 2 : C::kKStages;
-        for (uint32_t q = kpos > ring ? kpos - ring : 0; q < kpos; ++q)
-            mbar_wait(smem_addr(&b.st_full[q % ring]), (q / ring) & 1, kWaitLimitNs / 8, nullptr);
-        for (uint32_t q = vpos > 2 ? vpos - 2 : 0; q < vpos; ++q)
-            mbar_wait(smem_addr(&b.v_full[q & 1]), (q >> 1) & 1, kWaitLimitNs / 8, nullptr);
-        if (res_issued > 0)
-            mbar_wait(smem_addr(&b.res_full), res_phase ^ 1, kWaitLimitNs / 8, nullptr);
+        auto land = [&](uint64_t *full, uint32_t pos, uint32_t slots) {
+            for (uint32_t q = pos > slots ? pos - slots : 0; q < pos; ++q)
+                mbar_wait(smem_addr(&full[q % slots]), (q / slots) & 1, kWaitLimitNs / 8, nullptr);
+        };
+        land(b.st_full, kpos, C::kStages);
+        land(b.v_full, vpos, C::kStages2);
+        land(b.res_full, rpos, C::kRes);
     }
 }
 
 // ------------------------------------------------------------------ MMA issue
+// The CTA's tiles as one stream, across the pieces' ends: the first products of
+// a tile go out while the elementwise pass is at the one before, be it the last
+// of another unit.
 template <int D, bool kF16, bool kDkDv>
 __device__ void bwd_mma(const CrossBwdArgs &a, BBars &b, uint32_t smem, uint32_t tmem)
 {
     using C = BCfg<D, kDkDv>;
     const volatile int *abort = &b.abort;
     const bool leader = elect_one();
-    uint32_t res_phase = 0, s_phase = 0, oe_phase = 0, dp_phase = 0, pos = 0;
-    uint32_t n_tile = 0;  // dq: tiles of this CTA so far (dq_full[n % 2])
     bool ok = true;
     auto commit = [&](uint64_t &bar) {
         if (leader)
             mma_commit(smem_addr(&bar));
     };
-    const uint32_t a0 = smem, a1 = smem + C::kTileBytes;  // resident pair
-    Walk w = first_walk<kDkDv>(a, b);
-    Piece p;
-    while (ok && next_piece<kDkDv>(a, w, p)) {
-        const int n = uniform(p.t1 - p.t0);
-        if (n == 0)
-            continue;
-        pos = uniform(pos);
-        ok = warp_wait(b.res_full, res_phase, abort);
-        res_phase ^= 1;
-        ok = ok && warp_wait(b.o_empty, oe_phase ^ 1, abort);
-        oe_phase ^= 1;
-        if (!ok)
-            break;
-        if constexpr (!kDkDv) {
-            // S(t+1) goes into the other S buffer before dS(t) is ready, dP(t+1)
-            // follows as soon as dP(t) is in registers (dp_free), dQ += dS(t) K(t)
-            // once dS(t) is written.
-            auto k_tile = [&](int t) { return smem + C::kKRing + ((pos + t) % C::kKStages) * C::kTileBytes; };
-            auto v_tile = [&](int t) { return smem + C::kVRing + ((pos + t) % C::kVStages) * C::kTileBytes; };
-            auto wait_k = [&](int t) {
-                return warp_wait(b.st_full[(pos + t) % C::kKStages], ((pos + t) / C::kKStages) & 1, abort);
-            };
-            auto wait_v = [&](int t) {
-                return warp_wait(b.v_full[(pos + t) % C::kVStages], ((pos + t) / C::kVStages) & 1, abort);
-            };
-            ok = wait_k(0) && wait_v(0);
-            if (!ok)
-                break;
-            tc_fence_after();
-            if (leader) {
-                mma_nt<D, kF16>(tmem + dq_s_col<D>(0), a0, k_tile(0));  // S = Q K^T
-                mma_nt<D, kF16>(tmem + kColDP, a1, v_tile(0));          // dP = dO V^T
-            }
-            commit(b.s_full);
-            commit(b.v_empty[pos % C::kVStages]);
-            if (n == 1)
-                commit(b.res_empty);
-            for (int t = 0; ok && t < n; ++t) {
-                if (t + 1 < n) {
-                    ok = wait_k(t + 1);
-                    if (!ok)
-                        break;
-                    tc_fence_after();
-                    if (leader)
-                        mma_nt<D, kF16>(tmem + dq_s_col<D>(t + 1), a0, k_tile(t + 1));
-                    ok = warp_wait(b.dp_free, dp_phase, abort);
-                    dp_phase ^= 1;
-                    ok = ok && wait_v(t + 1);
-                    if (!ok)
-                        break;
-                    tc_fence_after();
-                    if (leader)
-                        mma_nt<D, kF16>(tmem + kColDP, a1, v_tile(t + 1));
-                    commit(b.s_full);
-                    commit(b.v_empty[(pos + t + 1) % C::kVStages]);
-                    if (t + 2 == n)
-                        commit(b.res_empty);  // the resident pair is no longer read
-                }
-                ok = warp_wait(b.dq_full[n_tile & 1], (n_tile >> 1) & 1, abort);
-                ++n_tile;
-                if (!ok)
-                    break;
-                tc_fence_after();
-                if (leader)  // dQ += dS K
-                    mma_tn<D, kF16>(tmem + kColAcc0, tmem + dq_s_col<D>(t), k_tile(t), t > 0);
-                commit(b.st_empty[(pos + t) % C::kKStages]);
-                if (t + 1 == n)
-                    commit(b.o_full);
-            }
-        } else {
-            // P^T(t) is written over S^T(t), dS^T(t) over dP^T(t): S^T(t+1)
-            // follows dV(t), dP^T(t+1) follows dK(t).
-            auto stage = [&](int t) { return smem + (2 + 2 * ((pos + t) & 1)) * C::kTileBytes; };
-            auto wait_q = [&](int t) {
-                return warp_wait(b.st_full[(pos + t) & 1], ((pos + t) >> 1) & 1, abort);
-            };
-            auto wait_do = [&](int t) {
-                return warp_wait(b.v_full[(pos + t) & 1], ((pos + t) >> 1) & 1, abort);
-            };
-            ok = wait_q(0);
-            if (!ok)
-                break;
-            tc_fence_after();
-            if (leader)
-                mma_nt<D, kF16>(tmem + kColS, a0, stage(0));  // S^T = K Q^T
-            commit(b.s_full);
-            ok = wait_do(0);
-            if (!ok)
-                break;
-            tc_fence_after();
-            if (leader)
-                mma_nt<D, kF16>(tmem + kColDP, a1, stage(0) + C::kTileBytes);  // dP^T = V dO^T
-            commit(b.dp_full);
-            if (n == 1)
-                commit(b.res_empty);
-            for (int t = 0; ok && t < n; ++t) {
-                const bool next = t + 1 < n;
-                ok = warp_wait(b.p1_full, dp_phase, abort);
-                dp_phase ^= 1;
-                if (!ok)
-                    break;
-                tc_fence_after();
-                if (leader)  // dV += P^T dO
-                    mma_tn<D, kF16>(tmem + kColAcc0, tmem + kColS, stage(t) + C::kTileBytes, t > 0);
-                commit(b.v_empty[(pos + t) & 1]);
-                if (next) {
-                    ok = wait_q(t + 1);
-                    if (!ok)
-                        break;
-                    tc_fence_after();
-                    if (leader)
-                        mma_nt<D, kF16>(tmem + kColS, a0, stage(t + 1));
-                    commit(b.s_full);
-                }
-                ok = warp_wait(b.p_full, s_phase, abort);
-                s_phase ^= 1;
-                if (!ok)
-                    break;
-                tc_fence_after();
-                if (leader)  // dK += dS^T Q
-                    mma_tn<D, kF16>(tmem + C::kColAcc1, tmem + kColDP, stage(t), t > 0);
-                commit(b.st_empty[(pos + t) & 1]);
-                if (next) {
-                    ok = wait_do(t + 1);
-                    if (!ok)
-                        break;
-                    tc_fence_after();
-                    if (leader)
-                        mma_nt<D, kF16>(tmem + kColDP, a1, stage(t + 1) + C::kTileBytes);
-                    commit(b.dp_full);
-                    if (t + 2 == n)
-                        commit(b.res_empty);
-                } else {
-                    commit(b.o_full);
-                }
-            }
+    // A place in the stream: tile `t` of `n` of a piece, the `pos`-th of all; n = 0:
+    // there is none.
+    struct At {
+        uint32_t piece, pos;
+        int t, n;
+    };
+    auto settle = [&](At &at) {
+        at.t = at.n = 0;
+        if (receive(b, at.piece, ok)) {
+            const Piece &p = b.pieces[at.piece % kPieces];
+            at.n = uniform(p.t1 - p.t0);
         }
-        pos += n;
+    };
+    auto step = [&](At at) {
+        at.pos = uniform(at.pos + 1);
+        if (++at.t == at.n) {
+            at.piece = uniform(at.piece + 1);
+            settle(at);
+        }
+        return at;
+    };
+    auto slot_wait = [&](uint64_t *full, uint32_t pos, int slots) {
+        return warp_wait(full[pos % slots], (pos / slots) & 1, abort);
+    };
+    auto tile = [&](uint32_t base, uint32_t pos, int slots) { return smem + base + pos % slots * C::kTileBytes; };
+    // The resident tiles of a piece: 2 piece and 2 piece + 1 of theirs.
+    auto first_wait = [&](const At &at, int which) {
+        return at.t > 0 || slot_wait(b.res_full, 2 * at.piece + which, C::kRes);
+    };
+    auto resident = [&](const At &at, int which) { return tile(0, 2 * at.piece + which, C::kRes); };
+    auto st_tile = [&](const At &at) { return tile(C::kRing, at.pos, C::kStages); };
+    auto v_tile = [&](const At &at) { return tile(C::kRing2, at.pos, C::kStages2); };
+    auto acc_col = [&](const At &at) { return tmem + kColAcc0 + at.piece % C::kAccs * C::kAccCols; };
+    // S (S^T) of a tile, and dP (dP^T).
+    auto scores = [&](const At &at) {
+        ok = first_wait(at, 0) && slot_wait(b.st_full, at.pos, C::kStages);
+        if (!ok)
+            return;
+        tc_fence_after();
+        if (leader)
+            mma_nt<D, kF16>(tmem + (!kDkDv && (at.pos & 1) ? C::kColS1 : kColS), resident(at, 0), st_tile(at));
+        if (at.t + 1 == at.n)
+            commit(b.res_empty[2 * at.piece % C::kRes]);
+    };
+    auto grads = [&](const At &at) {
+        ok = first_wait(at, 1) && slot_wait(b.v_full, at.pos, C::kStages2);
+        if (!ok)
+            return;
+        tc_fence_after();
+        if (leader)
+            mma_nt<D, kF16>(tmem + kColDP, resident(at, 1), v_tile(at));
+        if (at.t + 1 == at.n)
+            commit(b.res_empty[(2 * at.piece + 1) % C::kRes]);
+    };
+    auto acc_wait = [&](const At &at) {  // a piece's first sum: the accumulator has been read
+        return at.t > 0 || warp_wait(b.o_empty[at.piece % C::kAccs], (at.piece / C::kAccs & 1) ^ 1, abort);
+    };
+    At at = {0, 0, 0, 0};
+    settle(at);
+    if (ok && at.n > 0) {
+        scores(at);
+        if (kDkDv && ok)
+            commit(b.s_full);
+        if (ok)
+            grads(at);
+        if (ok) {
+            commit(kDkDv ? b.dp_full : b.s_full);
+            if (!kDkDv)
+                commit(b.v_empty[at.pos % C::kStages2]);
+        }
+    }
+    while (ok && at.n > 0) {
+        At next = at;
+        if constexpr (!kDkDv) {
+            // S of the next tile before dS of this one is ready, dP once this
+            // one's is in registers.
+            next = step(at);
+            if (ok && next.n > 0) {
+                scores(next);
+                ok = ok && warp_wait(b.dp_free, at.pos & 1, abort);
+                if (ok)
+                    grads(next);
+                if (ok) {
+                    commit(b.s_full);
+                    commit(b.v_empty[next.pos % C::kStages2]);
+                }
+            }
+            ok = ok && warp_wait(b.dq_full[at.pos & 1], (at.pos >> 1) & 1, abort) && acc_wait(at);
+            if (!ok)
+                break;
+            tc_fence_after();
+            if (leader)  // dQ += dS K
+                mma_tn<D, kF16>(acc_col(at), tmem + (at.pos & 1 ? C::kColS1 : kColS), st_tile(at), at.t > 0);
+            commit(b.st_empty[at.pos % C::kStages]);
+        } else {
+            // P^T is written over S^T, dS^T over dP^T: the next S^T follows dV, the
+            // next dP^T dK.
+            ok = warp_wait(b.p1_full, at.pos & 1, abort) && acc_wait(at);
+            if (!ok)
+                break;
+            tc_fence_after();
+            if (leader)  // dV += P^T dO
+                mma_tn<D, kF16>(acc_col(at), tmem + kColS, v_tile(at), at.t > 0);
+            commit(b.v_empty[at.pos % C::kStages2]);
+            next = step(at);
+            if (ok && next.n > 0) {
+                scores(next);
+                if (ok)
+                    commit(b.s_full);
+            }
+            ok = ok && warp_wait(b.p_full, at.pos & 1, abort);
+            if (!ok)
+                break;
+            tc_fence_after();
+            if (leader)  // dK += dS^T Q
+                mma_tn<D, kF16>(acc_col(at) + D, tmem + kColDP, st_tile(at), at.t > 0);
+            commit(b.st_empty[at.pos % C::kStages]);
+        }
+        if (at.t + 1 == at.n)
+            commit(b.o_full[at.piece % C::kAccs]);
+        if (kDkDv && next.n > 0) {
+            grads(next);
+            if (ok)
+                commit(b.dp_full);
+        }
+        if (at.t + 1 == at.n)
+            give_back(b, at.piece);
+        at = next;
     }
     if (!ok && leader)
         fail(a, b, kRoleMma);
@@ -586,64 +580,58 @@ __device__ void bwd_elem(const CrossBwdArgs &a, BBars &b, BXch &xch, uint8_t *ti
     const int r = warp * 32 + lane;
     tmem += static_cast<uint32_t>(warp * 32) << 16;
     constexpr int kHalfChunks = kTile / 64;  // 32-column chunks of a half
-    uint32_t s_phase = 0, of_phase = 0, dp_phase = 0, grp_phase = 0;
-    uint32_t n_tile = 0;
-    int xbuf = 0;
+    uint32_t pos = 0;  // tiles so far
     bool ok = true;
     const float ds_scale = b.ds_scale;
     const uint64_t sl2x2 = f2_pack(a.sl2, a.sl2), dss = f2_pack(ds_scale, ds_scale);
-    auto wait = [&](uint64_t &bar, uint32_t &phase) {
-        const bool good = mbar_wait(smem_addr(&bar), phase, kWaitLimitNs, abort);
-        phase ^= 1;
-        return good;
+    auto wait = [&](uint64_t &bar, uint32_t phase) {
+        return mbar_wait(smem_addr(&bar), phase & 1, kWaitLimitNs, abort);
     };
     auto arrive = [&](uint64_t &bar) {
         __syncwarp();
         if (lane == 0)
             mbar_arrive(smem_addr(&bar));
     };
-    Walk w = first_walk<kDkDv>(a, b);
-    Piece p;
-    while (ok && next_piece<kDkDv>(a, w, p)) {
-        const int row = p.tile * kTile + r;
+    // dkdv: lse (threads 0-63 of a warpgroup) and D (64-127) of its 64 queries of
+    // a tile, fetched a tile ahead, the next piece's first one too.
+    const int xq = half * 64 + (r & 63);
+    auto fetch = [&](const Piece &p, int t) {
+        const int g = t / a.Tq, q = (t - g * a.Tq) * kTile + xq;
+        const float *src = (r < 64 ? a.lse : a.dvec) +
+                           ((static_cast<long long>(p.b) * a.Hk + p.h) * a.G + g) * a.Nq;
+        return q < a.Nq ? src[q] : 0.f;
+    };
+    float xnext = 0.f;
+    for (uint32_t k = 0; receive(b, k, ok); ++k) {
+        const Piece &p = b.pieces[k % kPieces];
+        const int t0 = p.t0, t1 = p.t1;
         float row_nl2 = 0.f, row_nd = 0.f;
-        if (!kDkDv && row < a.Nq) {
-            const long long at = (static_cast<long long>(p.b) * a.Hk * a.G + p.h) * a.Nq + row;
-            row_nl2 = neg_lse2(a.lse[at]);
-            row_nd = -a.dvec[at] * ds_scale;
-        }
-        // dkdv: lse (threads 0-63 of a warpgroup) and D (64-127) of its 64
-        // queries of a tile, fetched a tile ahead.
-        const int xq = half * 64 + (r & 63);
-        int fg = 0, fi = 0;  // of the tile fetched next
-        const float *xsrc = nullptr;
-        auto fetch = [&]() {
-            const int q = fi * kTile + xq;
-            const float x = q < a.Nq ? xsrc[static_cast<long long>(fg) * a.Nq + q] : 0.f;
-            if (++fi == a.Tq) {
-                fi = 0;
-                ++fg;
+        if (kDkDv) {
+            if (k == 0)
+                xnext = fetch(p, t0);
+        } else {
+            const int row = p.tile * kTile + r;
+            if (row < a.Nq) {
+                const long long at = (static_cast<long long>(p.b) * a.Hk * a.G + p.h) * a.Nq + row;
+                row_nl2 = neg_lse2(a.lse[at]);
+                row_nd = -a.dvec[at] * ds_scale;
             }
-            return x;
-        };
-        float xnext = 0.f;
-        if (kDkDv && p.t0 < p.t1) {
-            fg = p.t0 / a.Tq;
-            fi = p.t0 - fg * a.Tq;
-            xsrc = (r < 64 ? a.lse : a.dvec) +
-                   (static_cast<long long>(p.b) * a.Hk + p.h) * a.G * a.Nq;
-            xnext = fetch();
         }
-        for (int t = p.t0; ok && t < p.t1; ++t) {
+        for (int t = t0; ok && t < t1; ++t, ++pos) {
             if constexpr (kDkDv) {
+                const int xbuf = pos & 1;
                 if (r < 64)
                     xch.lse2[xbuf][xq] = neg_lse2(xnext);
                 else
                     xch.dd[xbuf][xq] = -xnext * ds_scale;
-                if (t + 1 < p.t1)
-                    xnext = fetch();
+                if (t + 1 < t1) {
+                    xnext = fetch(p, t + 1);
+                } else if (receive(b, k + 1, ok)) {
+                    const Piece &n = b.pieces[(k + 1) % kPieces];
+                    xnext = fetch(n, n.t0);
+                }
                 arrive(b.grp[half]);
-                ok = wait(b.grp[half], grp_phase) && wait(b.s_full, s_phase);
+                ok = ok && wait(b.grp[half], pos) && wait(b.s_full, pos);
                 if (!ok)
                     break;
                 tc_fence_after();
@@ -676,7 +664,7 @@ __device__ void bwd_elem(const CrossBwdArgs &a, BBars &b, BXch &xch, uint8_t *ti
                 tc_fence_before();
                 arrive(b.p1_full);
                 // dS^T = P^T (dP^T - D) over the first 16 columns of each chunk.
-                ok = wait(b.dp_full, dp_phase);
+                ok = wait(b.dp_full, pos);
                 if (!ok)
                     break;
                 tc_fence_after();
@@ -702,19 +690,17 @@ __device__ void bwd_elem(const CrossBwdArgs &a, BBars &b, BXch &xch, uint8_t *ti
                 tmem_wait_st();
                 tc_fence_before();
                 arrive(b.p_full);
-                xbuf ^= 1;
             } else {
-                ok = wait(b.s_full, s_phase);
+                ok = wait(b.s_full, pos);
                 if (!ok)
                     break;
                 tc_fence_after();
                 const int valid = p.L - t * kTile;  // keys of this tile
-                const uint32_t col_s = dq_s_col<D>(t - p.t0);
+                const uint32_t col_s = pos & 1 ? C::kColS1 : kColS;
                 if (valid < kTile) {
                     // What lies behind the last key may be anything: dS is zero
                     // there, and so must K be (S has read it).
-                    uint4 *k_tile = reinterpret_cast<uint4 *>(tiles + C::kKRing +
-                                                              (n_tile % C::kKStages) * C::kTileBytes);
+                    uint4 *k_tile = reinterpret_cast<uint4 *>(tiles + C::kRing + pos % C::kStages * C::kTileBytes);
                     for (int at = threadIdx.x; at < C::kChunks * kTile * 8; at += 256)
                         if ((at / 8) % kTile >= valid)
                             k_tile[at] = make_uint4(0, 0, 0, 0);
@@ -728,10 +714,8 @@ __device__ void bwd_elem(const CrossBwdArgs &a, BBars &b, BXch &xch, uint8_t *ti
                 for (int hc = 0; hc < kHalfChunks; ++hc)
                     tmem_ld32(tmem + kColDP + (half * kHalfChunks + hc) * 32, dr[hc]);
                 tmem_wait_ld();
-                if (t + 1 < p.t1) {
-                    tc_fence_before();
-                    arrive(b.dp_free);
-                }
+                tc_fence_before();
+                arrive(b.dp_free);
                 auto grads = [&](int ch, const uint32_t *sr, const uint32_t *dp, uint32_t *dk, auto tag) {
                     constexpr bool kMasked = decltype(tag)::value;
                     const uint64_t nl2 = f2_pack(row_nl2, row_nl2), nd = f2_pack(row_nd, row_nd);
@@ -768,31 +752,29 @@ __device__ void bwd_elem(const CrossBwdArgs &a, BBars &b, BXch &xch, uint8_t *ti
                 }
                 tmem_wait_st();
                 tc_fence_before();
-                arrive(b.dq_full[n_tile & 1]);
-                ++n_tile;
+                arrive(b.dq_full[pos & 1]);
             }
         }
         if (!ok)
             break;
-        const bool some = p.t0 < p.t1;
-        if (some) {
-            ok = wait(b.o_full, of_phase);
-            if (!ok)
-                break;
-            tc_fence_after();
-        }
+        const uint32_t set = k % C::kAccs;
+        ok = wait(b.o_full[set], k / C::kAccs);
+        if (!ok)
+            break;
+        tc_fence_after();
         // dkdv: warpgroup 0 writes dV, warpgroup 1 dK; dq: each half of dQ's
         // 32-column chunks.
         const bool is_dv = kDkDv && half == 0;
-        const uint32_t col = kDkDv && !is_dv ? C::kColAcc1 : kColAcc0;
+        const uint32_t col = kColAcc0 + set * C::kAccCols + (kDkDv && !is_dv ? D : 0);
         const float f = is_dv ? 1.f : a.scale / ds_scale;
         const int rows = kDkDv ? a.Nk : a.Nq;
         constexpr int kChunks32 = D / 32;
         const int c0 = kDkDv ? 0 : half * ((kChunks32 + 1) / 2);
         const int c1 = kDkDv ? kChunks32 : half == 0 ? (kChunks32 + 1) / 2 : kChunks32;
         const bool whole = p.slot < 0;
+        const int row = p.tile * kTile + r;
         const bool live = row < rows;
-        const bool zero = !some || (kDkDv && row >= p.L);
+        const bool zero = kDkDv && row >= p.L;
         const long long *st = kDkDv ? (is_dv ? a.dv_st : a.dk_st) : a.dq_st;
         uint16_t *out = static_cast<uint16_t *>(kDkDv ? (is_dv ? a.dv : a.dk) : a.dq);
         uint16_t *dst = out + p.b * st[0] + p.h * st[1] + row * st[2];
@@ -801,11 +783,9 @@ __device__ void bwd_elem(const CrossBwdArgs &a, BBars &b, BXch &xch, uint8_t *ti
 #pragma unroll 1
         for (int c = c0; c < c1; ++c) {
             uint32_t o[32];
-            if (some) {
-                __syncwarp();
-                tmem_ld32(tmem + col + c * 32, o);
-                tmem_wait_ld();
-            }
+            __syncwarp();
+            tmem_ld32(tmem + col + c * 32, o);
+            tmem_wait_ld();
             if (!live)
                 continue;
             if (whole) {
@@ -827,10 +807,9 @@ __device__ void bwd_elem(const CrossBwdArgs &a, BBars &b, BXch &xch, uint8_t *ti
                     d4[i] = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
             }
         }
-        if (some) {
-            tc_fence_before();
-            arrive(b.o_empty);
-        }
+        give_back(b, k);
+        tc_fence_before();
+        arrive(b.o_empty[set]);
     }
     if (!ok)
         fail(a, b, kRoleSoftmax);
@@ -877,22 +856,26 @@ __global__ void __launch_bounds__(kThreads, 1)
     BBars &b = *reinterpret_cast<BBars *>(tiles + C::kTilesBytes);
     const int warp = threadIdx.x / 32;
     if (threadIdx.x == 0) {
-        mbar_init(smem_addr(&b.res_full), 1);
-        mbar_init(smem_addr(&b.res_empty), 1);
-        for (int s = 0; s < 3; ++s) {
-            mbar_init(smem_addr(&b.st_full[s]), 1);
-            mbar_init(smem_addr(&b.st_empty[s]), 1);
+        for (int i = 0; i < 4; ++i) {
+            mbar_init(smem_addr(&b.res_full[i]), 1);
+            mbar_init(smem_addr(&b.res_empty[i]), 1);
+            mbar_init(smem_addr(&b.st_full[i]), 1);
+            mbar_init(smem_addr(&b.st_empty[i]), 1);
+            mbar_init(smem_addr(&b.v_full[i]), 1);
+            mbar_init(smem_addr(&b.v_empty[i]), 1);
         }
-        for (int s = 0; s < 2; ++s) {
-            mbar_init(smem_addr(&b.v_full[s]), 1);
-            mbar_init(smem_addr(&b.v_empty[s]), 1);
-            mbar_init(smem_addr(&b.dq_full[s]), kElemWarps);
-            mbar_init(smem_addr(&b.grp[s]), kElemWarps / 2);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(smem_addr(&b.o_full[i]), 1);
+            mbar_init(smem_addr(&b.o_empty[i]), kElemWarps);
+            mbar_init(smem_addr(&b.dq_full[i]), kElemWarps);
+            mbar_init(smem_addr(&b.grp[i]), kElemWarps / 2);
+        }
+        for (int i = 0; i < kPieces; ++i) {
+            mbar_init(smem_addr(&b.piece_full[i]), 1);
+            mbar_init(smem_addr(&b.piece_empty[i]), kElemWarps + 1);
         }
         mbar_init(smem_addr(&b.s_full), 1);
         mbar_init(smem_addr(&b.p_full), kElemWarps);
-        mbar_init(smem_addr(&b.o_full), 1);
-        mbar_init(smem_addr(&b.o_empty), kElemWarps);
         mbar_init(smem_addr(&b.p1_full), kElemWarps);
         mbar_init(smem_addr(&b.dp_full), 1);
         mbar_init(smem_addr(&b.dp_free), kElemWarps);
@@ -946,8 +929,21 @@ template <bool kF16> __device__ __forceinline__ float2 unpack2(uint32_t w)
         return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&w));
 }
 
-// D of all rows, a group of lanes a row (16 bytes a lane), and the block's
-// largest |dO|.  Then zeros for the key tiles that no unit covers.
+// Zeros into 128 rows (as far as there are any) of a tensor's tile.
+template <int kGroup, int kLanes>
+__device__ __forceinline__ void zero_tile(void *t, const long long *st, int b, int h, int tile, int rows)
+{
+    const int part = threadIdx.x % kGroup, end = min(rows, (tile + 1) * kTile);
+    for (int n = tile * kTile + threadIdx.x / kGroup; n < end; n += kPrepThreads / kGroup)
+        if (part < kLanes)
+            *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(t) + b * st[0] + h * st[1] + n * st[2] + part * 8) =
+                make_uint4(0, 0, 0, 0);
+}
+
+// D of all rows, a group of lanes a row (16 bytes a lane), in the order in which
+// they lie in memory, and the block's largest |dO|.  Then zeros for what no unit
+// covers: key tiles behind a sequence's last key (all, without queries) and the
+// queries of a sequence without keys.
 template <int D, bool kF16> __global__ void __launch_bounds__(kPrepThreads) cross_prep_kernel(const CrossBwdArgs a)
 {
     constexpr int kLanes = D / 8, kGroup = D == 64 ? 8 : 16;
@@ -957,27 +953,33 @@ template <int D, bool kF16> __global__ void __launch_bounds__(kPrepThreads) cros
     const long long stride = static_cast<long long>(gridDim.x) * groups;
     const int Hq = a.Hk * a.G;
     const long long rows = static_cast<long long>(a.B) * Hq * a.Nq;
+    const bool heads_inside = a.do_st[1] < a.do_st[2];
     float amax = 0.f;
     for (long long row0 = static_cast<long long>(blockIdx.x) * groups + threadIdx.x / kGroup;
          row0 - threadIdx.x / kGroup < rows; row0 += stride * kPrepRows) {
         uint4 x[kPrepRows], y[kPrepRows];
+        long long to[kPrepRows];
 #pragma unroll
         for (int i = 0; i < kPrepRows; ++i) {
             const long long row = row0 + i * stride;
             x[i] = y[i] = make_uint4(0, 0, 0, 0);
-            if (row < rows && part < kLanes) {
-                const long long bh = row / a.Nq;
-                const int n = static_cast<int>(row - bh * a.Nq);
-                const int bb = static_cast<int>(bh / Hq), h = static_cast<int>(bh - static_cast<long long>(bb) * Hq);
-                x[i] = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(a.o) + bb * a.o_st[0] +
-                                                        h * a.o_st[1] + n * a.o_st[2] + part * 8);
-                y[i] = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(a.dout) + bb * a.do_st[0] +
-                                                        h * a.do_st[1] + n * a.do_st[2] + part * 8);
+            to[i] = -1;
+            if (row < rows) {
+                const int inner = heads_inside ? Hq : a.Nq, outer = heads_inside ? a.Nq : Hq;
+                const long long q1 = row / inner, q2 = q1 / outer;
+                const int i0 = static_cast<int>(row - q1 * inner), i1 = static_cast<int>(q1 - q2 * outer);
+                const int h = heads_inside ? i0 : i1, n = heads_inside ? i1 : i0;
+                to[i] = (q2 * Hq + h) * a.Nq + n;
+                if (part < kLanes) {
+                    x[i] = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(a.o) + q2 * a.o_st[0] +
+                                                            h * a.o_st[1] + n * a.o_st[2] + part * 8);
+                    y[i] = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(a.dout) + q2 * a.do_st[0] +
+                                                            h * a.do_st[1] + n * a.do_st[2] + part * 8);
+                }
             }
         }
 #pragma unroll
         for (int i = 0; i < kPrepRows; ++i) {
-            const long long row = row0 + i * stride;
             const uint32_t xv[4] = {x[i].x, x[i].y, x[i].z, x[i].w}, yv[4] = {y[i].x, y[i].y, y[i].z, y[i].w};
             float acc = 0.f;
 #pragma unroll
@@ -991,8 +993,8 @@ template <int D, bool kF16> __global__ void __launch_bounds__(kPrepThreads) cros
 #pragma unroll
             for (int o = kGroup / 2; o > 0; o /= 2)
                 acc += __shfl_xor_sync(0xffffffffu, acc, o);
-            if (row < rows && part == 0)
-                a.dvec[row] = acc;
+            if (to[i] >= 0 && part == 0)
+                a.dvec[to[i]] = acc;
         }
     }
     if (kF16) {
@@ -1009,26 +1011,24 @@ template <int D, bool kF16> __global__ void __launch_bounds__(kPrepThreads) cros
             a.amax[blockIdx.x] = amax;
         }
     }
-    // Key tiles behind a sequence's last key: no unit's, zeros in dk and dv.
-    if (a.kv_len == nullptr)
+    if (a.kv_len == nullptr && a.Nk > 0 && rows > 0)
         return;
     const int Tk = (a.Nk + kTile - 1) / kTile;
-    const long long tiles = static_cast<long long>(a.B) * a.Hk * Tk;
-    for (long long i = blockIdx.x; i < tiles; i += gridDim.x) {
-        const long long bh = i / Tk;
-        const int tile = static_cast<int>(i - bh * Tk), b = static_cast<int>(bh / a.Hk);
-        const int h = static_cast<int>(bh - static_cast<long long>(b) * a.Hk);
-        const int L = clamp_len(a, b);
-        if (tile == 0 && h == 0 && threadIdx.x == 0 && a.kv_len[b] != L)
+    const long long k_tiles = static_cast<long long>(a.Hk) * Tk, tiles = k_tiles + static_cast<long long>(Hq) * a.Tq;
+    for (long long i = blockIdx.x; i < tiles * a.B; i += gridDim.x) {
+        const int b = static_cast<int>(i / tiles), L = clamp_len(a, b);
+        const long long at = i - b * tiles;
+        if (at == 0 && threadIdx.x == 0 && a.kv_len != nullptr && a.kv_len[b] != L)
             atomicCAS(a.status, 0u, 6u /* FATTN_ERR_INDEX */ | (kRoleCross << 8));
-        if (tile * kTile < L || part >= kLanes)
-            continue;
-        const int end = min(a.Nk, (tile + 1) * kTile);
-        for (int n = tile * kTile + threadIdx.x / kGroup; n < end; n += groups) {
-            *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.dk) + b * a.dk_st[0] + h * a.dk_st[1] +
-                                       n * a.dk_st[2] + part * 8) = make_uint4(0, 0, 0, 0);
-            *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.dv) + b * a.dv_st[0] + h * a.dv_st[1] +
-                                       n * a.dv_st[2] + part * 8) = make_uint4(0, 0, 0, 0);
+        if (at < k_tiles) {
+            const int h = static_cast<int>(at / Tk), tile = static_cast<int>(at - static_cast<long long>(h) * Tk);
+            if (tile * kTile >= L || rows == 0) {
+                zero_tile<kGroup, kLanes>(a.dk, a.dk_st, b, h, tile, a.Nk);
+                zero_tile<kGroup, kLanes>(a.dv, a.dv_st, b, h, tile, a.Nk);
+            }
+        } else if (L == 0) {
+            const int h = static_cast<int>((at - k_tiles) / a.Tq);
+            zero_tile<kGroup, kLanes>(a.dq, a.dq_st, b, h, static_cast<int>(at - k_tiles) - h * a.Tq, a.Nq);
         }
     }
 }
@@ -1126,7 +1126,7 @@ cudaError_t launch(const CrossBwdArgs &args, const CrossBwdMaps &m, cudaStream_t
     const long long rows = static_cast<long long>(a.B) * a.Hk * a.G * a.Nq;
     const long long blocks = (rows + kRows - 1) / kRows;
     // The zeros of short sequences want hands, too.
-    a.prep_blocks = static_cast<int>(a.kv_len != nullptr || blocks > kPrepBlocks ? kPrepBlocks
+    a.prep_blocks = static_cast<int>(a.kv_len != nullptr || a.Nk == 0 || rows == 0 || blocks > kPrepBlocks ? kPrepBlocks
                                      : blocks > 0                               ? blocks
                                                                                 : 1);
     cudaError_t e = start(cross_prep_kernel<D, kF16>, dim3(a.prep_blocks), kPrepThreads, 0, stream, a);
