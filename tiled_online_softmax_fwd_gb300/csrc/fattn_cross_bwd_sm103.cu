@@ -46,10 +46,14 @@ namespace {
 using namespace ptx;
 
 constexpr int kTile = 128;
-constexpr int kThreads = 320;  // warps 0-7 elementwise, 8 producer, 9 MMA
-constexpr int kElemWarps = 8;  // two warpgroups, a half of the 128 columns each
-constexpr int kWarpLoad = 8;
-constexpr int kWarpMma = 9;
+// Warps 0-15 elementwise: four warpgroups, 32 of a tile's 128 columns each (four
+// warps a scheduler hide one another's waits for TMEM and barriers: with two
+// warpgroups a tile took 2500 to 2900 cycles, where its exponentials are 1024
+// and its products at d = 128 1536); 16 the producer, 17 MMA.
+constexpr int kElemWarps = 16;
+constexpr int kWarpLoad = 16;
+constexpr int kWarpMma = 17;
+constexpr int kThreads = 18 * 32;
 constexpr uint32_t kTmemCols = 512;
 constexpr uint64_t kWaitLimitNs = 2000000000ull;
 constexpr float kLog2e = 1.4426950408889634f;
@@ -107,7 +111,6 @@ struct alignas(16) BBars {
     // dq: dS of the CTA's n-th tile written, on dq_full[n % 2] (a warp may be a
     // tile ahead of another, not two).
     uint64_t dq_full[2];
-    uint64_t grp[2];  // dkdv: a warpgroup's lse and D of the tile are stored
     uint64_t drain;
     uint32_t tmem_base;
     int abort;
@@ -117,10 +120,10 @@ struct alignas(16) BBars {
     long long warp_sum[kThreads / 32];
     float warp_max[kThreads / 32];
 };
-// dkdv, behind the barriers: -lse log2(e) and -D (scaled) of the current query
-// tile, two deep.
+// dkdv, behind the barriers: each warp's -lse log2(e) and -D (scaled) of the 32
+// queries of its columns, two tiles deep.
 struct BXch {
-    float lse2[2][kTile], dd[2][kTile];
+    float lse2[kElemWarps][2][32], dd[kElemWarps][2][32];
 };
 
 __device__ __forceinline__ int clamp_len(const CrossBwdArgs &a, int b)
@@ -278,6 +281,18 @@ __device__ __forceinline__ bool warp_wait(uint64_t &bar, uint32_t parity, const 
 // them (see paged_sm103.cuh).
 __device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xffffffffu, x, 0); }
 
+// The same where one lane runs alone, by its number as elect.sync gave it.
+__device__ __forceinline__ uint32_t uniform_of(uint32_t x, uint32_t lane)
+{
+    return __shfl_sync(1u << lane, x, static_cast<int>(lane));
+}
+__device__ __forceinline__ uint32_t elected_lane()
+{
+    uint32_t lane;
+    asm volatile("{\n\t.reg .pred P1;\n\telect.sync %0|P1, 0xffffffff;\n\t}" : "=r"(lane));
+    return lane;
+}
+
 // The pieces, published by the producer.  The k-th, read in place; false when
 // there is none (ok) or a wait failed (!ok).  Held until given back.
 __device__ __forceinline__ bool receive(BBars &b, uint32_t k, bool &ok)
@@ -413,148 +428,147 @@ __device__ void bwd_load(const CrossBwdArgs &a, BBars &b, uint32_t smem, const C
 // ------------------------------------------------------------------ MMA issue
 // The CTA's tiles as one stream, across the pieces' ends: the first products of
 // a tile go out while the elementwise pass is at the one before, be it the last
-// of another unit.
+// of another unit.  Run by one lane, and what is between two products is short:
+// the tensor cores wait for it (with votes, shuffles and remainders for each
+// place in a ring, a fifth of the time).
+template <int kSlots> struct Ring {  // a place in a ring and its phase
+    uint32_t slot = 0, phase = 0;
+    __device__ __forceinline__ void step()
+    {
+        if (++slot == kSlots) {
+            slot = 0;
+            phase ^= 1;
+        }
+    }
+};
 template <int D, bool kF16, bool kDkDv>
-__device__ void bwd_mma(const CrossBwdArgs &a, BBars &b, uint32_t smem, uint32_t tmem)
+__device__ void bwd_mma(const CrossBwdArgs &a, BBars &b, uint32_t smem, uint32_t tmem, uint32_t lane)
 {
     using C = BCfg<D, kDkDv>;
     const volatile int *abort = &b.abort;
-    const bool leader = elect_one();
+    auto wait = [&](uint64_t &bar, uint32_t parity) {
+        return mbar_wait(smem_addr(&bar), parity & 1, kWaitLimitNs, abort);
+    };
+    auto commit = [&](uint64_t &bar) { mma_commit(smem_addr(&bar)); };
     bool ok = true;
-    auto commit = [&](uint64_t &bar) {
-        if (leader)
-            mma_commit(smem_addr(&bar));
+    uint32_t piece = 0, pos = 0;
+    // Tiles of the piece, 0: there is none.
+    auto tiles_of = [&](uint32_t k) {
+        ok = ok && wait(b.piece_full[k % kPieces], k / kPieces);
+        if (!ok || b.pieces[k % kPieces].h < 0)
+            return 0;
+        return static_cast<int>(uniform_of(b.pieces[k % kPieces].t1 - b.pieces[k % kPieces].t0, lane));
     };
-    // A place in the stream: tile `t` of `n` of a piece, the `pos`-th of all; n = 0:
-    // there is none.
-    struct At {
-        uint32_t piece, pos;
-        int t, n;
+    Ring<C::kRes> res0, res1;  // of the piece that S and dP are at
+    res1.step();
+    Ring<C::kStages> st_s, st_k;    // of S, and of dK or dQ
+    Ring<C::kStages2> v_d, v_v;     // of dP, and of dV
+    auto step2 = [](Ring<C::kRes> &x) {
+        x.step();
+        x.step();
     };
-    auto settle = [&](At &at) {
-        at.t = at.n = 0;
-        if (receive(b, at.piece, ok)) {
-            const Piece &p = b.pieces[at.piece % kPieces];
-            at.n = uniform(p.t1 - p.t0);
-        }
+    auto at = [&](uint32_t base, uint32_t slot) {
+        return uniform_of(smem + base + slot * C::kTileBytes, lane);
     };
-    auto step = [&](At at) {
-        at.pos = uniform(at.pos + 1);
-        if (++at.t == at.n) {
-            at.piece = uniform(at.piece + 1);
-            settle(at);
-        }
-        return at;
-    };
-    auto slot_wait = [&](uint64_t *full, uint32_t pos, int slots) {
-        return warp_wait(full[pos % slots], (pos / slots) & 1, abort);
-    };
-    auto tile = [&](uint32_t base, uint32_t pos, int slots) { return smem + base + pos % slots * C::kTileBytes; };
-    // The resident tiles of a piece: 2 piece and 2 piece + 1 of theirs.
-    auto first_wait = [&](const At &at, int which) {
-        return at.t > 0 || slot_wait(b.res_full, 2 * at.piece + which, C::kRes);
-    };
-    auto resident = [&](const At &at, int which) { return tile(0, 2 * at.piece + which, C::kRes); };
-    auto st_tile = [&](const At &at) { return tile(C::kRing, at.pos, C::kStages); };
-    auto v_tile = [&](const At &at) { return tile(C::kRing2, at.pos, C::kStages2); };
-    auto acc_col = [&](const At &at) { return tmem + kColAcc0 + at.piece % C::kAccs * C::kAccCols; };
-    // S (S^T) of a tile, and dP (dP^T).
-    auto scores = [&](const At &at) {
-        ok = first_wait(at, 0) && slot_wait(b.st_full, at.pos, C::kStages);
+    // S (S^T) of the next tile, the `t`-th of `n`, and dP (dP^T).
+    auto scores = [&](uint32_t n_th, int t, int n) {
+        ok = ok && (t > 0 || wait(b.res_full[res0.slot], res0.phase)) && wait(b.st_full[st_s.slot], st_s.phase);
         if (!ok)
             return;
         tc_fence_after();
-        if (leader)
-            mma_nt<D, kF16>(tmem + (!kDkDv && (at.pos & 1) ? C::kColS1 : kColS), resident(at, 0), st_tile(at));
-        if (at.t + 1 == at.n)
-            commit(b.res_empty[2 * at.piece % C::kRes]);
-    };
-    auto grads = [&](const At &at) {
-        ok = first_wait(at, 1) && slot_wait(b.v_full, at.pos, C::kStages2);
-        if (!ok)
-            return;
-        tc_fence_after();
-        if (leader)
-            mma_nt<D, kF16>(tmem + kColDP, resident(at, 1), v_tile(at));
-        if (at.t + 1 == at.n)
-            commit(b.res_empty[(2 * at.piece + 1) % C::kRes]);
-    };
-    auto acc_wait = [&](const At &at) {  // a piece's first sum: the accumulator has been read
-        return at.t > 0 || warp_wait(b.o_empty[at.piece % C::kAccs], (at.piece / C::kAccs & 1) ^ 1, abort);
-    };
-    At at = {0, 0, 0, 0};
-    settle(at);
-    if (ok && at.n > 0) {
-        scores(at);
-        if (kDkDv && ok)
+        mma_nt<D, kF16>(tmem + (!kDkDv && (n_th & 1) ? C::kColS1 : kColS), at(0, res0.slot),
+                        at(C::kRing, st_s.slot));
+        if (kDkDv)
             commit(b.s_full);
-        if (ok)
-            grads(at);
-        if (ok) {
-            commit(kDkDv ? b.dp_full : b.s_full);
-            if (!kDkDv)
-                commit(b.v_empty[at.pos % C::kStages2]);
+        if (t + 1 == n) {
+            commit(b.res_empty[res0.slot]);
+            step2(res0);
         }
+        st_s.step();
+    };
+    auto grads = [&](int t, int n) {
+        ok = ok && (t > 0 || wait(b.res_full[res1.slot], res1.phase)) && wait(b.v_full[v_d.slot], v_d.phase);
+        if (!ok)
+            return;
+        tc_fence_after();
+        mma_nt<D, kF16>(tmem + kColDP, at(0, res1.slot), at(C::kRing2, v_d.slot));
+        commit(kDkDv ? b.dp_full : b.s_full);
+        if (!kDkDv)
+            commit(b.v_empty[v_d.slot]);
+        if (t + 1 == n) {
+            commit(b.res_empty[res1.slot]);
+            step2(res1);
+        }
+        v_d.step();
+    };
+    int n = tiles_of(0);
+    if (n > 0) {
+        scores(0, 0, n);
+        grads(0, n);
     }
-    while (ok && at.n > 0) {
-        At next = at;
-        if constexpr (!kDkDv) {
-            // S of the next tile before dS of this one is ready, dP once this
-            // one's is in registers.
-            next = step(at);
-            if (ok && next.n > 0) {
-                scores(next);
-                ok = ok && warp_wait(b.dp_free, at.pos & 1, abort);
-                if (ok)
-                    grads(next);
-                if (ok) {
-                    commit(b.s_full);
-                    commit(b.v_empty[next.pos % C::kStages2]);
+    while (ok && n > 0) {
+        const uint32_t set = piece % C::kAccs, acc = uniform_of(tmem + kColAcc0 + set * C::kAccCols, lane);
+        int next = 0;
+        for (int t = 0; ok && t < n; ++t, ++pos) {
+            // The tile after this one: of this piece or the first of the next.
+            const bool last = t + 1 == n;
+            const int t_next = last ? 0 : t + 1;
+            if constexpr (!kDkDv) {
+                // S of the next tile before dS of this one is ready, dP once this
+                // one's is in registers.
+                if (last)
+                    next = tiles_of(piece + 1);
+                const int n_next = last ? next : n;
+                if (n_next > 0) {
+                    scores(pos + 1, t_next, n_next);
+                    ok = ok && wait(b.dp_free, pos);
+                    grads(t_next, n_next);
                 }
+                ok = ok && wait(b.dq_full[pos & 1], pos >> 1) &&
+                     (t > 0 || wait(b.o_empty[set], (piece / C::kAccs) ^ 1));
+                if (!ok)
+                    break;
+                tc_fence_after();
+                mma_tn<D, kF16>(acc, tmem + (pos & 1 ? C::kColS1 : kColS), at(C::kRing, st_k.slot), t > 0);  // dQ += dS K
+                commit(b.st_empty[st_k.slot]);
+                st_k.step();
+                if (last)
+                    commit(b.o_full[set]);
+            } else {
+                // P^T is written over S^T, dS^T over dP^T: the next S^T follows dV, the
+                // next dP^T dK.
+                ok = wait(b.p1_full, pos) && (t > 0 || wait(b.o_empty[set], (piece / C::kAccs) ^ 1));
+                if (!ok)
+                    break;
+                tc_fence_after();
+                mma_tn<D, kF16>(acc, tmem + kColS, at(C::kRing2, v_v.slot), t > 0);  // dV += P^T dO
+                commit(b.v_empty[v_v.slot]);
+                v_v.step();
+                if (last)
+                    next = tiles_of(piece + 1);
+                const int n_next = last ? next : n;
+                if (n_next > 0)
+                    scores(0, t_next, n_next);
+                ok = ok && wait(b.p_full, pos);
+                if (!ok)
+                    break;
+                tc_fence_after();
+                mma_tn<D, kF16>(acc + D, tmem + kColDP, at(C::kRing, st_k.slot), t > 0);  // dK += dS^T Q
+                commit(b.st_empty[st_k.slot]);
+                st_k.step();
+                if (last)
+                    commit(b.o_full[set]);
+                if (n_next > 0)
+                    grads(t_next, n_next);
             }
-            ok = ok && warp_wait(b.dq_full[at.pos & 1], (at.pos >> 1) & 1, abort) && acc_wait(at);
-            if (!ok)
-                break;
-            tc_fence_after();
-            if (leader)  // dQ += dS K
-                mma_tn<D, kF16>(acc_col(at), tmem + (at.pos & 1 ? C::kColS1 : kColS), st_tile(at), at.t > 0);
-            commit(b.st_empty[at.pos % C::kStages]);
-        } else {
-            // P^T is written over S^T, dS^T over dP^T: the next S^T follows dV, the
-            // next dP^T dK.
-            ok = warp_wait(b.p1_full, at.pos & 1, abort) && acc_wait(at);
-            if (!ok)
-                break;
-            tc_fence_after();
-            if (leader)  // dV += P^T dO
-                mma_tn<D, kF16>(acc_col(at), tmem + kColS, v_tile(at), at.t > 0);
-            commit(b.v_empty[at.pos % C::kStages2]);
-            next = step(at);
-            if (ok && next.n > 0) {
-                scores(next);
-                if (ok)
-                    commit(b.s_full);
-            }
-            ok = ok && warp_wait(b.p_full, at.pos & 1, abort);
-            if (!ok)
-                break;
-            tc_fence_after();
-            if (leader)  // dK += dS^T Q
-                mma_tn<D, kF16>(acc_col(at) + D, tmem + kColDP, st_tile(at), at.t > 0);
-            commit(b.st_empty[at.pos % C::kStages]);
         }
-        if (at.t + 1 == at.n)
-            commit(b.o_full[at.piece % C::kAccs]);
-        if (kDkDv && next.n > 0) {
-            grads(next);
-            if (ok)
-                commit(b.dp_full);
-        }
-        if (at.t + 1 == at.n)
-            give_back(b, at.piece);
-        at = next;
+        if (!ok)
+            break;
+        mbar_arrive(smem_addr(&b.piece_empty[piece % kPieces]));
+        ++piece;
+        n = next;
     }
-    if (!ok && leader)
+    if (!ok)
         fail(a, b, kRoleMma);
     commit(b.drain);
     mbar_wait(smem_addr(&b.drain), 0, kWaitLimitNs, nullptr);
@@ -568,18 +582,18 @@ __device__ __forceinline__ float neg_lse2(float lse)
 }
 
 // ------------------------------------------------------------------ elementwise
-// Thread r of either warpgroup owns TMEM lane r, row 128 tile + r of the
-// resident tile; warpgroup h works on columns 64 h .. 64 h + 63 of it.
+// Thread r of a warpgroup owns TMEM lane r, row 128 tile + r of the resident tile;
+// warpgroup g works on columns 32 g .. 32 g + 31 of it.
 template <int D, bool kF16, bool kDkDv>
 __device__ void bwd_elem(const CrossBwdArgs &a, BBars &b, BXch &xch, uint8_t *tiles, uint32_t tmem)
 {
     using C = BCfg<D, kDkDv>;
     const volatile int *abort = &b.abort;
     const int warp = (threadIdx.x / 32) & 3, lane = threadIdx.x & 31;
-    const int half = threadIdx.x / 128;
+    const int quarter = threadIdx.x / 128;
     const int r = warp * 32 + lane;
     tmem += static_cast<uint32_t>(warp * 32) << 16;
-    constexpr int kHalfChunks = kTile / 64;  // 32-column chunks of a half
+    const uint32_t col = quarter * 32;
     uint32_t pos = 0;  // tiles so far
     bool ok = true;
     const float ds_scale = b.ds_scale;
@@ -592,23 +606,22 @@ __device__ void bwd_elem(const CrossBwdArgs &a, BBars &b, BXch &xch, uint8_t *ti
         if (lane == 0)
             mbar_arrive(smem_addr(&bar));
     };
-    // dkdv: lse (threads 0-63 of a warpgroup) and D (64-127) of its 64 queries of
-    // a tile, fetched a tile ahead, the next piece's first one too.
-    const int xq = half * 64 + (r & 63);
+    // dkdv: lse and D of the query of this lane's column, fetched a tile ahead, the
+    // next piece's first one too.
+    float next_lse = 0.f, next_d = 0.f;
     auto fetch = [&](const Piece &p, int t) {
-        const int g = t / a.Tq, q = (t - g * a.Tq) * kTile + xq;
-        const float *src = (r < 64 ? a.lse : a.dvec) +
-                           ((static_cast<long long>(p.b) * a.Hk + p.h) * a.G + g) * a.Nq;
-        return q < a.Nq ? src[q] : 0.f;
+        const int g = t / a.Tq, q = (t - g * a.Tq) * kTile + col + lane;
+        const long long at = ((static_cast<long long>(p.b) * a.Hk + p.h) * a.G + g) * a.Nq + q;
+        next_lse = q < a.Nq ? a.lse[at] : 0.f;
+        next_d = q < a.Nq ? a.dvec[at] : 0.f;
     };
-    float xnext = 0.f;
     for (uint32_t k = 0; receive(b, k, ok); ++k) {
         const Piece &p = b.pieces[k % kPieces];
         const int t0 = p.t0, t1 = p.t1;
         float row_nl2 = 0.f, row_nd = 0.f;
         if (kDkDv) {
             if (k == 0)
-                xnext = fetch(p, t0);
+                fetch(p, t0);
         } else {
             const int row = p.tile * kTile + r;
             if (row < a.Nq) {
@@ -619,73 +632,73 @@ __device__ void bwd_elem(const CrossBwdArgs &a, BBars &b, BXch &xch, uint8_t *ti
         }
         for (int t = t0; ok && t < t1; ++t, ++pos) {
             if constexpr (kDkDv) {
-                const int xbuf = pos & 1;
-                if (r < 64)
-                    xch.lse2[xbuf][xq] = neg_lse2(xnext);
-                else
-                    xch.dd[xbuf][xq] = -xnext * ds_scale;
-                if (t + 1 < t1) {
-                    xnext = fetch(p, t + 1);
-                } else if (receive(b, k + 1, ok)) {
-                    const Piece &n = b.pieces[(k + 1) % kPieces];
-                    xnext = fetch(n, n.t0);
-                }
-                arrive(b.grp[half]);
-                ok = ok && wait(b.grp[half], pos) && wait(b.s_full, pos);
+                float *lse2 = xch.lse2[threadIdx.x / 32][pos & 1], *dd = xch.dd[threadIdx.x / 32][pos & 1];
+                lse2[lane] = neg_lse2(next_lse);
+                dd[lane] = -next_d * ds_scale;
+                if (t + 1 < t1)
+                    fetch(p, t + 1);
+                else if (receive(b, k + 1, ok))
+                    fetch(b.pieces[(k + 1) % kPieces], b.pieces[(k + 1) % kPieces].t0);
+                __syncwarp();
+                ok = ok && wait(b.s_full, pos);
                 if (!ok)
                     break;
                 tc_fence_after();
-                // P^T of this half's chunks, kept in registers and written over
-                // the first 16 columns of each S^T chunk.  Queries behind Nq are
-                // zero rows of Q and dO and add nothing; keys behind the last
-                // one are lanes of their own, not stored.
-                float pr[kHalfChunks][32];
-#pragma unroll
-                for (int hc = 0; hc < kHalfChunks; ++hc) {
-                    const int ch = half * kHalfChunks + hc;
+                // P^T, kept in registers and written over the first 16 columns of
+                // the S^T chunk.  Queries behind Nq are zero rows of Q and dO and
+                // add nothing; keys behind the last one are lanes of their own, not
+                // stored.
+                float pr[32];
+                {
                     uint32_t sr[32], pk[16];
                     __syncwarp();
-                    tmem_ld32(tmem + kColS + ch * 32, sr);
+                    tmem_ld32(tmem + kColS + col, sr);
                     tmem_wait_ld();
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        const uint64_t nl2 = *reinterpret_cast<const uint64_t *>(&xch.lse2[xbuf][ch * 32 + 2 * i]);
-                        float x0, x1;
-                        f2_unpack(f2_fma(f2_pack(__uint_as_float(sr[2 * i]), __uint_as_float(sr[2 * i + 1])),
-                                         sl2x2, nl2),
-                                  x0, x1);
-                        pr[hc][2 * i] = ex2(x0);
-                        pr[hc][2 * i + 1] = ex2(x1);
-                        pk[i] = pack2<kF16>(pr[hc][2 * i], pr[hc][2 * i + 1]);
+                    for (int i = 0; i < 16; i += 2) {
+                        const ulonglong2 nl2 = *reinterpret_cast<const ulonglong2 *>(&lse2[2 * i]);
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) {
+                            float x0, x1;
+                            f2_unpack(f2_fma(f2_pack(__uint_as_float(sr[2 * (i + j)]),
+                                                     __uint_as_float(sr[2 * (i + j) + 1])),
+                                             sl2x2, j == 0 ? nl2.x : nl2.y),
+                                      x0, x1);
+                            pr[2 * (i + j)] = ex2(x0);
+                            pr[2 * (i + j) + 1] = ex2(x1);
+                            pk[i + j] = pack2<kF16>(pr[2 * (i + j)], pr[2 * (i + j) + 1]);
+                        }
                     }
-                    tmem_st16(tmem + kColS + ch * 32, pk);
+                    tmem_st16(tmem + kColS + col, pk);
                 }
                 tmem_wait_st();
                 tc_fence_before();
                 arrive(b.p1_full);
-                // dS^T = P^T (dP^T - D) over the first 16 columns of each chunk.
+                // dS^T = P^T (dP^T - D) over the first 16 columns of the chunk.
                 ok = wait(b.dp_full, pos);
                 if (!ok)
                     break;
                 tc_fence_after();
-#pragma unroll
-                for (int hc = 0; hc < kHalfChunks; ++hc) {
-                    const int ch = half * kHalfChunks + hc;
+                {
                     uint32_t dr[32], dk[16];
                     __syncwarp();
-                    tmem_ld32(tmem + kColDP + ch * 32, dr);
+                    tmem_ld32(tmem + kColDP + col, dr);
                     tmem_wait_ld();
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        const uint64_t nd = *reinterpret_cast<const uint64_t *>(&xch.dd[xbuf][ch * 32 + 2 * i]);
-                        float d0, d1;
-                        f2_unpack(f2_mul(f2_pack(pr[hc][2 * i], pr[hc][2 * i + 1]),
-                                         f2_fma(f2_pack(__uint_as_float(dr[2 * i]), __uint_as_float(dr[2 * i + 1])),
-                                                dss, nd)),
-                                  d0, d1);
-                        dk[i] = pack2<kF16>(d0, d1);
+                    for (int i = 0; i < 16; i += 2) {
+                        const ulonglong2 nd = *reinterpret_cast<const ulonglong2 *>(&dd[2 * i]);
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) {
+                            const int c = 2 * (i + j);
+                            float d0, d1;
+                            f2_unpack(f2_mul(f2_pack(pr[c], pr[c + 1]),
+                                             f2_fma(f2_pack(__uint_as_float(dr[c]), __uint_as_float(dr[c + 1])), dss,
+                                                    j == 0 ? nd.x : nd.y)),
+                                      d0, d1);
+                            dk[i + j] = pack2<kF16>(d0, d1);
+                        }
                     }
-                    tmem_st16(tmem + kColDP + ch * 32, dk);
+                    tmem_st16(tmem + kColDP + col, dk);
                 }
                 tmem_wait_st();
                 tc_fence_before();
@@ -696,60 +709,42 @@ __device__ void bwd_elem(const CrossBwdArgs &a, BBars &b, BXch &xch, uint8_t *ti
                     break;
                 tc_fence_after();
                 const int valid = p.L - t * kTile;  // keys of this tile
-                const uint32_t col_s = pos & 1 ? C::kColS1 : kColS;
+                const uint32_t col_s = (pos & 1 ? C::kColS1 : kColS) + col;
                 if (valid < kTile) {
                     // What lies behind the last key may be anything: dS is zero
                     // there, and so must K be (S has read it).
                     uint4 *k_tile = reinterpret_cast<uint4 *>(tiles + C::kRing + pos % C::kStages * C::kTileBytes);
-                    for (int at = threadIdx.x; at < C::kChunks * kTile * 8; at += 256)
+                    for (int at = threadIdx.x; at < C::kChunks * kTile * 8; at += kElemWarps * 32)
                         if ((at / 8) % kTile >= valid)
                             k_tile[at] = make_uint4(0, 0, 0, 0);
                     fence_proxy_async_smem();
                 }
-                // This half of the dP row into registers first, so that dP of
-                // the next tile is computed meanwhile.
-                uint32_t dr[kHalfChunks][32];
+                // dP into registers, so that the next tile's is computed meanwhile.
+                uint32_t dr[32], sr[32], dk[16];
                 __syncwarp();
-#pragma unroll
-                for (int hc = 0; hc < kHalfChunks; ++hc)
-                    tmem_ld32(tmem + kColDP + (half * kHalfChunks + hc) * 32, dr[hc]);
+                tmem_ld32(tmem + kColDP + col, dr);
+                tmem_ld32(tmem + col_s, sr);
                 tmem_wait_ld();
                 tc_fence_before();
                 arrive(b.dp_free);
-                auto grads = [&](int ch, const uint32_t *sr, const uint32_t *dp, uint32_t *dk, auto tag) {
-                    constexpr bool kMasked = decltype(tag)::value;
-                    const uint64_t nl2 = f2_pack(row_nl2, row_nl2), nd = f2_pack(row_nd, row_nd);
+                const uint64_t nl2 = f2_pack(row_nl2, row_nl2), nd = f2_pack(row_nd, row_nd);
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        const int c = ch * 32 + 2 * i;
-                        float x0, x1, d0, d1;
-                        f2_unpack(f2_fma(f2_pack(__uint_as_float(sr[2 * i]), __uint_as_float(sr[2 * i + 1])),
-                                         sl2x2, nl2),
-                                  x0, x1);
-                        f2_unpack(f2_mul(f2_pack(ex2(x0), ex2(x1)),
-                                         f2_fma(f2_pack(__uint_as_float(dp[2 * i]), __uint_as_float(dp[2 * i + 1])),
-                                                dss, nd)),
-                                  d0, d1);
-                        if constexpr (kMasked) {
-                            d0 = c < valid ? d0 : 0.f;
-                            d1 = c + 1 < valid ? d1 : 0.f;
-                        }
-                        dk[i] = pack2<kF16>(d0, d1);
+                for (int i = 0; i < 16; ++i) {
+                    float x0, x1, d0, d1;
+                    f2_unpack(f2_fma(f2_pack(__uint_as_float(sr[2 * i]), __uint_as_float(sr[2 * i + 1])), sl2x2, nl2),
+                              x0, x1);
+                    f2_unpack(f2_mul(f2_pack(ex2(x0), ex2(x1)),
+                                     f2_fma(f2_pack(__uint_as_float(dr[2 * i]), __uint_as_float(dr[2 * i + 1])), dss,
+                                            nd)),
+                              d0, d1);
+                    if (valid < kTile) {  // uniform
+                        d0 = static_cast<int>(col) + 2 * i < valid ? d0 : 0.f;
+                        d1 = static_cast<int>(col) + 2 * i + 1 < valid ? d1 : 0.f;
                     }
-                };
-#pragma unroll
-                for (int hc = 0; hc < kHalfChunks; ++hc) {
-                    const int ch = half * kHalfChunks + hc;
-                    uint32_t sr[32], dk[16];
-                    __syncwarp();
-                    tmem_ld32(tmem + col_s + ch * 32, sr);
-                    tmem_wait_ld();
-                    if (valid < kTile)
-                        grads(ch, sr, dr[hc], dk, std::true_type{});
-                    else
-                        grads(ch, sr, dr[hc], dk, std::false_type{});
-                    tmem_st16(tmem + col_s + ch * 32, dk);
+                    dk[i] = pack2<kF16>(d0, d1);
                 }
+                // dS over the first half of its own chunk of S.
+                tmem_st16(tmem + col_s, dk);
                 tmem_wait_st();
                 tc_fence_before();
                 arrive(b.dq_full[pos & 1]);
@@ -762,29 +757,25 @@ __device__ void bwd_elem(const CrossBwdArgs &a, BBars &b, BXch &xch, uint8_t *ti
         if (!ok)
             break;
         tc_fence_after();
-        // dkdv: warpgroup 0 writes dV, warpgroup 1 dK; dq: each half of dQ's
-        // 32-column chunks.
-        const bool is_dv = kDkDv && half == 0;
-        const uint32_t col = kColAcc0 + set * C::kAccCols + (kDkDv && !is_dv ? D : 0);
+        // dkdv: dV by warpgroups 0 and 1, dK by 2 and 3, alternate 32-column
+        // chunks; dq: a chunk a warpgroup.
+        const bool is_dv = kDkDv && quarter < 2;
+        const uint32_t acc = tmem + kColAcc0 + set * C::kAccCols + (kDkDv && !is_dv ? D : 0);
         const float f = is_dv ? 1.f : a.scale / ds_scale;
-        const int rows = kDkDv ? a.Nk : a.Nq;
-        constexpr int kChunks32 = D / 32;
-        const int c0 = kDkDv ? 0 : half * ((kChunks32 + 1) / 2);
-        const int c1 = kDkDv ? kChunks32 : half == 0 ? (kChunks32 + 1) / 2 : kChunks32;
         const bool whole = p.slot < 0;
         const int row = p.tile * kTile + r;
-        const bool live = row < rows;
+        const bool live = row < (kDkDv ? a.Nk : a.Nq);
         const bool zero = kDkDv && row >= p.L;
         const long long *st = kDkDv ? (is_dv ? a.dv_st : a.dk_st) : a.dq_st;
         uint16_t *out = static_cast<uint16_t *>(kDkDv ? (is_dv ? a.dv : a.dk) : a.dq);
         uint16_t *dst = out + p.b * st[0] + p.h * st[1] + row * st[2];
         float *part = (kDkDv ? a.ws_kv : a.ws_q) +
-                      ((static_cast<long long>(p.slot) * (kDkDv ? 2 : 1) + (kDkDv ? half : 0)) * kTile + r) * D;
+                      ((static_cast<long long>(p.slot) * (kDkDv ? 2 : 1) + (kDkDv && !is_dv ? 1 : 0)) * kTile + r) * D;
 #pragma unroll 1
-        for (int c = c0; c < c1; ++c) {
+        for (int c = kDkDv ? quarter & 1 : quarter; c < D / 32; c += kDkDv ? 2 : 4) {
             uint32_t o[32];
             __syncwarp();
-            tmem_ld32(tmem + col + c * 32, o);
+            tmem_ld32(acc + c * 32, o);
             tmem_wait_ld();
             if (!live)
                 continue;
@@ -868,7 +859,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(smem_addr(&b.o_full[i]), 1);
             mbar_init(smem_addr(&b.o_empty[i]), kElemWarps);
             mbar_init(smem_addr(&b.dq_full[i]), kElemWarps);
-            mbar_init(smem_addr(&b.grp[i]), kElemWarps / 2);
         }
         for (int i = 0; i < kPieces; ++i) {
             mbar_init(smem_addr(&b.piece_full[i]), 1);
@@ -904,8 +894,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         bwd_elem<D, kF16, kDkDv>(a, b, *reinterpret_cast<BXch *>(&b + 1), tiles, tmem);
     else if (warp == kWarpLoad)
         bwd_load<D, kDkDv>(a, b, smem, &mq, &mk, &mv, &mdo);
-    else
-        bwd_mma<D, kF16, kDkDv>(a, b, smem, tmem);
+    else if (warp == kWarpMma) {
+        const uint32_t lane = elected_lane();
+        if (elect_one())
+            bwd_mma<D, kF16, kDkDv>(a, b, smem, tmem, lane);
+        __syncwarp();
+    }
     grid_launch_dependents();
     tc_fence_before();
     __syncthreads();
