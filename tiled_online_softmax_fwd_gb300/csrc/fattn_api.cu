@@ -2309,6 +2309,7 @@ fattn_status_t attn_bwd_cross(const void *q, const void *k, const void *v, const
             return s;
     }
     uint8_t *base = static_cast<uint8_t *>(workspace);
+    a.q = q;
     a.o = o;
     a.dout = dout;
     a.lse = lse;
@@ -2321,6 +2322,7 @@ fattn_status_t attn_bwd_cross(const void *q, const void *k, const void *v, const
     a.starts = reinterpret_cast<int4 *>(base + ws.starts);
     a.ws_kv = reinterpret_cast<float *>(base + ws.kv);
     a.ws_q = reinterpret_cast<float *>(base + ws.q);
+    copy_strides(a.q_st, rows[0]);
     copy_strides(a.o_st, rows[1]);
     copy_strides(a.do_st, rows[2]);
     copy_strides(a.dq_st, rows[3]);

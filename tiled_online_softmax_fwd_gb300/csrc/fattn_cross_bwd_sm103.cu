@@ -12,8 +12,8 @@
 //            stay; the tiles of Q and dO of its G query heads stream by: S^T =
 //            K Q^T and dP^T = V dO^T, keys on TMEM lanes, P^T over S^T, then dV
 //            += P^T dO and dK += dS^T Q from TMEM
-//   dq       a unit is a tile of 128 queries of one head.  Q, dO stay; K and V
-//            stream by: S, dP, then dQ += dS K
+//   dq       a unit is a tile of 128 queries of one head.  Q and dO stay, in TMEM; K
+//            and V stream by: S, dP, dS over dP, then dQ += dS K
 //   merge    sums of units that were split
 // S and dP are formed in both, so that neither needs atomics: 7 products where
 // 5 would do, and equal calls give equal bits.
@@ -58,7 +58,7 @@ constexpr uint32_t kTmemCols = 512;
 constexpr uint64_t kWaitLimitNs = 2000000000ull;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr uint32_t kChunkBytes = kTile * 64 * 2;
-constexpr uint32_t kColS = 0, kColDP = 128, kColAcc0 = 256;
+constexpr uint32_t kColS = 0, kColDP = 128;
 
 // A unit's start and end, in steps (see Schedule); a split leaves at least kSnap
 // steps on each side, and a share is at least kLeast.
@@ -67,22 +67,28 @@ constexpr int kUnitCost = 3, kSnap = 2, kLeast = 8;
 template <int D, bool kDkDv> struct BCfg {
     static constexpr int kChunks = (D + 63) / 64;
     static constexpr uint32_t kTileBytes = kChunks * kChunkBytes;  // one [128][D] tile
-    // Slots of the resident tiles, which take turns (K_j, V_j, K_j', ... or Q_i,
-    // dO_i, ...): at d = 64 the next unit's are there before this one ends.  Then
-    // the streamed tiles, dkdv: Q and dO; dq: K (held until dQ) and V (free as soon
-    // as dP has read it).
-    static constexpr int kRes = D == 64 ? 4 : 2;
-    static constexpr int kStages = kDkDv ? (D == 64 ? 4 : 2) : D == 64 ? 4 : 3;
-    static constexpr int kStages2 = kDkDv ? kStages : D == 64 ? 3 : 2;
+    // dkdv: slots of the resident tiles, which take turns (K_j, V_j, K_j', ...): at
+    // d = 64 the next unit's are there before this one ends.  (dq: Q and dO are in
+    // TMEM.)  Then the streamed tiles, dkdv: Q and dO; dq: K (held until dQ) and V.
+    static constexpr int kRes = !kDkDv ? 0 : D == 64 ? 4 : 2;
+    static constexpr int kStages = !kDkDv || D == 64 ? 4 : 2;
+    static constexpr int kStages2 = kDkDv ? kStages : 3;
     static constexpr uint32_t kRing = kRes * kTileBytes;
     static constexpr uint32_t kRing2 = kRing + kStages * kTileBytes;
     static constexpr uint32_t kTilesBytes = kRing2 + kStages2 * kTileBytes;
-    // TMEM: S (dq: another S at the end), dP, and the accumulators, two sets where
-    // they fit.
-    static constexpr int kAccs = D == 64 ? 2 : 1;
+    // TMEM: S, dP; dkdv: at d = 64 another S, so that the next one is there when
+    // the elementwise pass is done with this; dV and dK; dq: dQ, two where they
+    // fit, Q and dO.
+    static constexpr int kSs = kDkDv && D == 64 ? 2 : 1;
+    static constexpr uint32_t kColAcc = kSs == 2 ? 384 : 256;
+    static constexpr int kAccs = !kDkDv && D == 64 ? 2 : 1;
     static constexpr uint32_t kAccCols = kDkDv ? 2 * D : D;
-    static constexpr uint32_t kColS1 = kColAcc0 + kAccs * kAccCols;
-    static_assert(kDkDv ? kColS1 <= kTmemCols : kColS1 + kTile <= kTmemCols, "TMEM columns");
+    static constexpr uint32_t kColQ = kColAcc + kAccs * kAccCols, kColDO = kColQ + D / 2;
+    static_assert((kDkDv ? kColQ : kColDO + D / 2) <= kTmemCols, "TMEM columns");
+    static __device__ __forceinline__ uint32_t s_col(uint32_t pos)
+    {
+        return kSs == 2 && (pos & 1) ? 256 : kColS;
+    }
 };
 
 // Where a CTA starts: a sequence, the cost already behind in it, and its share.
@@ -101,16 +107,12 @@ struct Piece {
 constexpr int kPieces = 4;  // published ahead
 
 struct alignas(16) BBars {
-    uint64_t res_full[4], res_empty[4];
+    uint64_t res_full[4], res_empty[4];  // dq: full[0], Q and dO written
     uint64_t st_full[4], st_empty[4];  // dkdv: Q stages; dq: K stages
     uint64_t v_full[4], v_empty[4];    // dkdv: dO stages; dq: V stages
-    uint64_t s_full, p_full, o_full[2], o_empty[2];
+    uint64_t s_full[2], p_full, o_full[2], o_empty[2];  // s_full: of tile n on n % 2
     uint64_t piece_full[kPieces], piece_empty[kPieces];
-    uint64_t p1_full, dp_full;  // dkdv: P^T written; dP^T computed
-    uint64_t dp_free;           // dq: dP is in registers
-    // dq: dS of the CTA's n-th tile written, on dq_full[n % 2] (a warp may be a
-    // tile ahead of another, not two).
-    uint64_t dq_full[2];
+    uint64_t p1_full, dp_full;  // P^T written (dq: S is in registers); dP computed
     uint64_t drain;
     uint32_t tmem_base;
     int abort;
@@ -332,6 +334,18 @@ __device__ __forceinline__ void mma_nt(uint32_t tmem_d, uint32_t a_smem, uint32_
         mma_ss_w(tmem_d, a_lo + off, hi, b_lo + off, hi, idesc, kk > 0 ? 1u : 0u);
     }
 }
+// The same with A in TMEM, D / 2 packed columns.
+template <int D, bool kF16>
+__device__ __forceinline__ void mma_nt_ts(uint32_t tmem_d, uint32_t tmem_a, uint32_t b_smem)
+{
+    constexpr uint32_t idesc = idesc_f32acc(kTile, kTile, false, kF16);
+    constexpr uint32_t hi = smem_desc_hi(1024);
+    const uint32_t b_lo = smem_desc_lo(b_smem, 16);
+#pragma unroll
+    for (int kk = 0; kk < D / 16; ++kk)
+        mma_ts_w(tmem_d, tmem_a + kk * 8, b_lo + (((kk >> 2) * kChunkBytes + (kk & 3) * 32) >> 4), hi, idesc,
+                 kk > 0 ? 1u : 0u);
+}
 // A from TMEM: 16 packed columns at the head of each 32-column chunk of a score
 // region, K = 16 step kk at column 32 (kk / 2) + 8 (kk % 2).  B MN-major.
 template <int D, bool kF16>
@@ -391,8 +405,9 @@ __device__ void bwd_load(const CrossBwdArgs &a, BBars &b, uint32_t smem, const C
         if (!more)
             break;
         const int head = uniform(p.h), batch = uniform(p.b), own = uniform(p.tile * kTile);
-        ok = load(b.res_full, b.res_empty, rpos, C::kRes, 0, kDkDv ? mk : mq, own, head, batch) &&
-             load(b.res_full, b.res_empty, rpos, C::kRes, 0, kDkDv ? mv : mdo, own, head, batch);
+        if constexpr (kDkDv)
+            ok = load(b.res_full, b.res_empty, rpos, C::kRes, 0, mk, own, head, batch) &&
+                 load(b.res_full, b.res_empty, rpos, C::kRes, 0, mv, own, head, batch);
         int g = kDkDv ? p.t0 / a.Tq : 0, i = kDkDv ? p.t0 - g * a.Tq : 0;
         for (int t = p.t0; ok && t < p.t1; ++t) {
             if constexpr (kDkDv) {
@@ -421,7 +436,8 @@ __device__ void bwd_load(const CrossBwdArgs &a, BBars &b, uint32_t smem, const C
         };
         land(b.st_full, kpos, C::kStages);
         land(b.v_full, vpos, C::kStages2);
-        land(b.res_full, rpos, C::kRes);
+        if constexpr (kDkDv)
+            land(b.res_full, rpos, C::kRes);
     }
 }
 
@@ -459,43 +475,49 @@ __device__ void bwd_mma(const CrossBwdArgs &a, BBars &b, uint32_t smem, uint32_t
             return 0;
         return static_cast<int>(uniform_of(b.pieces[k % kPieces].t1 - b.pieces[k % kPieces].t0, lane));
     };
-    Ring<C::kRes> res0, res1;  // of the piece that S and dP are at
+    Ring<(kDkDv ? C::kRes : 2)> res0, res1;  // dkdv: of the piece that S and dP are at
     res1.step();
-    Ring<C::kStages> st_s, st_k;    // of S, and of dK or dQ
-    Ring<C::kStages2> v_d, v_v;     // of dP, and of dV
-    auto step2 = [](Ring<C::kRes> &x) {
+    Ring<C::kStages> st_s, st_k;  // of S, and of dK or dQ
+    Ring<C::kStages2> v_d, v_v;   // of dP, and of dV
+    auto step2 = [](auto &x) {
         x.step();
         x.step();
     };
     auto at = [&](uint32_t base, uint32_t slot) {
         return uniform_of(smem + base + slot * C::kTileBytes, lane);
     };
-    // S (S^T) of the next tile, the `t`-th of `n`, and dP (dP^T).
-    auto scores = [&](uint32_t n_th, int t, int n) {
-        ok = ok && (t > 0 || wait(b.res_full[res0.slot], res0.phase)) && wait(b.st_full[st_s.slot], st_s.phase);
+    // S (S^T) of a tile, the `t`-th of the `n` of piece `k`, `pos`-th of all; dP (dP^T).
+    auto scores = [&](uint32_t k, uint32_t pos, int t, int n) {
+        ok = ok && (t > 0 || (kDkDv ? wait(b.res_full[res0.slot], res0.phase) : wait(b.res_full[0], k))) &&
+             wait(b.st_full[st_s.slot], st_s.phase);
         if (!ok)
             return;
         tc_fence_after();
-        mma_nt<D, kF16>(tmem + (!kDkDv && (n_th & 1) ? C::kColS1 : kColS), at(0, res0.slot),
-                        at(C::kRing, st_s.slot));
-        if (kDkDv)
-            commit(b.s_full);
-        if (t + 1 == n) {
+        if constexpr (kDkDv)
+            mma_nt<D, kF16>(tmem + C::s_col(pos), at(0, res0.slot), at(C::kRing, st_s.slot));
+        else
+            mma_nt_ts<D, kF16>(tmem + kColS, tmem + C::kColQ, at(C::kRing, st_s.slot));
+        commit(b.s_full[pos & 1]);
+        if (kDkDv && t + 1 == n) {
             commit(b.res_empty[res0.slot]);
             step2(res0);
         }
         st_s.step();
     };
     auto grads = [&](int t, int n) {
-        ok = ok && (t > 0 || wait(b.res_full[res1.slot], res1.phase)) && wait(b.v_full[v_d.slot], v_d.phase);
+        ok = ok && (t > 0 || !kDkDv || wait(b.res_full[res1.slot], res1.phase)) &&
+             wait(b.v_full[v_d.slot], v_d.phase);
         if (!ok)
             return;
         tc_fence_after();
-        mma_nt<D, kF16>(tmem + kColDP, at(0, res1.slot), at(C::kRing2, v_d.slot));
-        commit(kDkDv ? b.dp_full : b.s_full);
+        if constexpr (kDkDv)
+            mma_nt<D, kF16>(tmem + kColDP, at(0, res1.slot), at(C::kRing2, v_d.slot));
+        else
+            mma_nt_ts<D, kF16>(tmem + kColDP, tmem + C::kColDO, at(C::kRing2, v_d.slot));
+        commit(b.dp_full);
         if (!kDkDv)
             commit(b.v_empty[v_d.slot]);
-        if (t + 1 == n) {
+        if (kDkDv && t + 1 == n) {
             commit(b.res_empty[res1.slot]);
             step2(res1);
         }
@@ -503,52 +525,60 @@ __device__ void bwd_mma(const CrossBwdArgs &a, BBars &b, uint32_t smem, uint32_t
     };
     int n = tiles_of(0);
     if (n > 0) {
-        scores(0, 0, n);
+        scores(0, 0, 0, n);
         grads(0, n);
     }
     while (ok && n > 0) {
-        const uint32_t set = piece % C::kAccs, acc = uniform_of(tmem + kColAcc0 + set * C::kAccCols, lane);
+        const uint32_t set = piece % C::kAccs, acc = uniform_of(tmem + C::kColAcc + set * C::kAccCols, lane);
         int next = 0;
         for (int t = 0; ok && t < n; ++t, ++pos) {
             // The tile after this one: of this piece or the first of the next.
             const bool last = t + 1 == n;
             const int t_next = last ? 0 : t + 1;
+            auto acc_wait = [&]() { return t > 0 || wait(b.o_empty[set], (piece / C::kAccs) ^ 1); };
             if constexpr (!kDkDv) {
-                // S of the next tile before dS of this one is ready, dP once this
-                // one's is in registers.
-                if (last)
-                    next = tiles_of(piece + 1);
-                const int n_next = last ? next : n;
-                if (n_next > 0) {
-                    scores(pos + 1, t_next, n_next);
-                    ok = ok && wait(b.dp_free, pos);
-                    grads(t_next, n_next);
-                }
-                ok = ok && wait(b.dq_full[pos & 1], pos >> 1) &&
-                     (t > 0 || wait(b.o_empty[set], (piece / C::kAccs) ^ 1));
+                // dS is written over dP.  S of the next tile once this one's is in
+                // registers, dP of it after dQ; another piece's Q and dO are written
+                // after this one's last dS.
+                ok = ok && wait(b.p1_full, pos);
+                if (!last)
+                    scores(piece, pos + 1, t_next, n);
+                ok = ok && wait(b.p_full, pos) && acc_wait();
                 if (!ok)
                     break;
                 tc_fence_after();
-                mma_tn<D, kF16>(acc, tmem + (pos & 1 ? C::kColS1 : kColS), at(C::kRing, st_k.slot), t > 0);  // dQ += dS K
+                mma_tn<D, kF16>(acc, tmem + kColDP, at(C::kRing, st_k.slot), t > 0);  // dQ += dS K
                 commit(b.st_empty[st_k.slot]);
                 st_k.step();
-                if (last)
+                if (last) {
                     commit(b.o_full[set]);
+                    next = tiles_of(piece + 1);
+                    if (next > 0)
+                        scores(piece + 1, pos + 1, 0, next);
+                }
+                if (!last || next > 0)
+                    grads(t_next, last ? next : n);
             } else {
-                // P^T is written over S^T, dS^T over dP^T: the next S^T follows dV, the
-                // next dP^T dK.
-                ok = wait(b.p1_full, pos) && (t > 0 || wait(b.o_empty[set], (piece / C::kAccs) ^ 1));
+                // P^T is written over S^T, dS^T over dP^T: the next S^T follows dV
+                // (with another S it is ahead), the next dP^T dK.
+                int n_next = n;
+                auto next_scores = [&]() {
+                    if (last)
+                        n_next = next = tiles_of(piece + 1);
+                    if (n_next > 0)
+                        scores(last ? piece + 1 : piece, pos + 1, t_next, n_next);
+                };
+                if constexpr (C::kSs == 2)
+                    next_scores();
+                ok = ok && wait(b.p1_full, pos) && acc_wait();
                 if (!ok)
                     break;
                 tc_fence_after();
-                mma_tn<D, kF16>(acc, tmem + kColS, at(C::kRing2, v_v.slot), t > 0);  // dV += P^T dO
+                mma_tn<D, kF16>(acc, tmem + C::s_col(pos), at(C::kRing2, v_v.slot), t > 0);  // dV += P^T dO
                 commit(b.v_empty[v_v.slot]);
                 v_v.step();
-                if (last)
-                    next = tiles_of(piece + 1);
-                const int n_next = last ? next : n;
-                if (n_next > 0)
-                    scores(0, t_next, n_next);
+                if constexpr (C::kSs == 1)
+                    next_scores();
                 ok = ok && wait(b.p_full, pos);
                 if (!ok)
                     break;
@@ -579,6 +609,30 @@ __device__ void bwd_mma(const CrossBwdArgs &a, BBars &b, uint32_t smem, uint32_t
 __device__ __forceinline__ float neg_lse2(float lse)
 {
     return lse == -INFINITY ? lse : -lse * kLog2e;
+}
+
+// Four lanes' 16-byte pieces change places: v[j] of lane i of four becomes v[i]
+// of lane j.  Rows held a lane each are then stored 64 bytes at a time, eight rows
+// an instruction (16 bytes at a time, half a sector each, the end of a unit took
+// 9400 cycles at d = 128).
+__device__ __forceinline__ void transpose4(uint4 (&v)[4], int lane)
+{
+    auto trade = [&](uint4 &a, uint4 &b, int by) {
+        const bool up = lane & by;
+        uint4 x = up ? a : b;
+        x.x = __shfl_xor_sync(0xffffffffu, x.x, by);
+        x.y = __shfl_xor_sync(0xffffffffu, x.y, by);
+        x.z = __shfl_xor_sync(0xffffffffu, x.z, by);
+        x.w = __shfl_xor_sync(0xffffffffu, x.w, by);
+        if (up)
+            a = x;
+        else
+            b = x;
+    };
+    trade(v[0], v[1], 1);
+    trade(v[2], v[3], 1);
+    trade(v[0], v[2], 2);
+    trade(v[1], v[3], 2);
 }
 
 // ------------------------------------------------------------------ elementwise
@@ -615,6 +669,44 @@ __device__ void bwd_elem(const CrossBwdArgs &a, BBars &b, BXch &xch, uint8_t *ti
         next_lse = q < a.Nq ? a.lse[at] : 0.f;
         next_d = q < a.Nq ? a.dvec[at] : 0.f;
     };
+    // dq: a piece's rows of Q and dO into TMEM, 32 elements of a row a job, a lane
+    // a row.
+    auto make_resident = [&](const Piece &p) {
+        const int row = p.tile * kTile + r;
+        constexpr int kJobs = D / 32;  // of each tensor
+        uint32_t x[2][16];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int job = quarter + 4 * i;
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+                x[i][j] = 0;
+            if (job < 2 * kJobs && row < a.Nq) {
+                const bool is_q = job < kJobs;
+                const long long *st = is_q ? a.q_st : a.do_st;
+                const uint16_t *src = static_cast<const uint16_t *>(is_q ? a.q : a.dout) + p.b * st[0] + p.h * st[1] +
+                                      row * st[2] + (is_q ? job : job - kJobs) * 32;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const uint4 v = reinterpret_cast<const uint4 *>(src)[j];
+                    x[i][4 * j] = v.x;
+                    x[i][4 * j + 1] = v.y;
+                    x[i][4 * j + 2] = v.z;
+                    x[i][4 * j + 3] = v.w;
+                }
+            }
+        }
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int job = quarter + 4 * i;
+            if (job < 2 * kJobs)  // kColDO follows kColQ
+                tmem_st16(tmem + C::kColQ + job * 16, x[i]);
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        arrive(b.res_full[0]);
+    };
     for (uint32_t k = 0; receive(b, k, ok); ++k) {
         const Piece &p = b.pieces[k % kPieces];
         const int t0 = p.t0, t1 = p.t1;
@@ -623,6 +715,8 @@ __device__ void bwd_elem(const CrossBwdArgs &a, BBars &b, BXch &xch, uint8_t *ti
             if (k == 0)
                 fetch(p, t0);
         } else {
+            if (k == 0)
+                make_resident(p);
             const int row = p.tile * kTile + r;
             if (row < a.Nq) {
                 const long long at = (static_cast<long long>(p.b) * a.Hk * a.G + p.h) * a.Nq + row;
@@ -640,7 +734,7 @@ __device__ void bwd_elem(const CrossBwdArgs &a, BBars &b, BXch &xch, uint8_t *ti
                 else if (receive(b, k + 1, ok))
                     fetch(b.pieces[(k + 1) % kPieces], b.pieces[(k + 1) % kPieces].t0);
                 __syncwarp();
-                ok = ok && wait(b.s_full, pos);
+                ok = ok && wait(b.s_full[pos & 1], pos >> 1);
                 if (!ok)
                     break;
                 tc_fence_after();
@@ -652,7 +746,7 @@ __device__ void bwd_elem(const CrossBwdArgs &a, BBars &b, BXch &xch, uint8_t *ti
                 {
                     uint32_t sr[32], pk[16];
                     __syncwarp();
-                    tmem_ld32(tmem + kColS + col, sr);
+                    tmem_ld32(tmem + C::s_col(pos) + col, sr);
                     tmem_wait_ld();
 #pragma unroll
                     for (int i = 0; i < 16; i += 2) {
@@ -669,7 +763,7 @@ __device__ void bwd_elem(const CrossBwdArgs &a, BBars &b, BXch &xch, uint8_t *ti
                             pk[i + j] = pack2<kF16>(pr[2 * (i + j)], pr[2 * (i + j) + 1]);
                         }
                     }
-                    tmem_st16(tmem + kColS + col, pk);
+                    tmem_st16(tmem + C::s_col(pos) + col, pk);
                 }
                 tmem_wait_st();
                 tc_fence_before();
@@ -704,12 +798,30 @@ __device__ void bwd_elem(const CrossBwdArgs &a, BBars &b, BXch &xch, uint8_t *ti
                 tc_fence_before();
                 arrive(b.p_full);
             } else {
-                ok = wait(b.s_full, pos);
+                ok = wait(b.s_full[pos & 1], pos >> 1);
                 if (!ok)
                     break;
                 tc_fence_after();
                 const int valid = p.L - t * kTile;  // keys of this tile
-                const uint32_t col_s = (pos & 1 ? C::kColS1 : kColS) + col;
+                // P in registers, so that the next S is computed meanwhile.
+                float pr[32];
+                {
+                    uint32_t sr[32];
+                    __syncwarp();
+                    tmem_ld32(tmem + kColS + col, sr);
+                    tmem_wait_ld();
+                    tc_fence_before();
+                    arrive(b.p1_full);
+                    const uint64_t nl2 = f2_pack(row_nl2, row_nl2);
+#pragma unroll
+                    for (int i = 0; i < 32; i += 2) {
+                        float x0, x1;
+                        f2_unpack(f2_fma(f2_pack(__uint_as_float(sr[i]), __uint_as_float(sr[i + 1])), sl2x2, nl2), x0,
+                                  x1);
+                        pr[i] = ex2(x0);
+                        pr[i + 1] = ex2(x1);
+                    }
+                }
                 if (valid < kTile) {
                     // What lies behind the last key may be anything: dS is zero
                     // there, and so must K be (S has read it).
@@ -719,35 +831,38 @@ __device__ void bwd_elem(const CrossBwdArgs &a, BBars &b, BXch &xch, uint8_t *ti
                             k_tile[at] = make_uint4(0, 0, 0, 0);
                     fence_proxy_async_smem();
                 }
-                // dP into registers, so that the next tile's is computed meanwhile.
-                uint32_t dr[32], sr[32], dk[16];
-                __syncwarp();
-                tmem_ld32(tmem + kColDP + col, dr);
-                tmem_ld32(tmem + col_s, sr);
-                tmem_wait_ld();
-                tc_fence_before();
-                arrive(b.dp_free);
-                const uint64_t nl2 = f2_pack(row_nl2, row_nl2), nd = f2_pack(row_nd, row_nd);
+                ok = wait(b.dp_full, pos);
+                if (!ok)
+                    break;
+                tc_fence_after();
+                {
+                    uint32_t dr[32], dk[16];
+                    __syncwarp();
+                    tmem_ld32(tmem + kColDP + col, dr);
+                    tmem_wait_ld();
+                    const uint64_t nd = f2_pack(row_nd, row_nd);
 #pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    float x0, x1, d0, d1;
-                    f2_unpack(f2_fma(f2_pack(__uint_as_float(sr[2 * i]), __uint_as_float(sr[2 * i + 1])), sl2x2, nl2),
-                              x0, x1);
-                    f2_unpack(f2_mul(f2_pack(ex2(x0), ex2(x1)),
-                                     f2_fma(f2_pack(__uint_as_float(dr[2 * i]), __uint_as_float(dr[2 * i + 1])), dss,
-                                            nd)),
-                              d0, d1);
-                    if (valid < kTile) {  // uniform
-                        d0 = static_cast<int>(col) + 2 * i < valid ? d0 : 0.f;
-                        d1 = static_cast<int>(col) + 2 * i + 1 < valid ? d1 : 0.f;
+                    for (int i = 0; i < 16; ++i) {
+                        float d0, d1;
+                        f2_unpack(f2_mul(f2_pack(pr[2 * i], pr[2 * i + 1]),
+                                         f2_fma(f2_pack(__uint_as_float(dr[2 * i]), __uint_as_float(dr[2 * i + 1])),
+                                                dss, nd)),
+                                  d0, d1);
+                        if (valid < kTile) {  // uniform
+                            d0 = static_cast<int>(col) + 2 * i < valid ? d0 : 0.f;
+                            d1 = static_cast<int>(col) + 2 * i + 1 < valid ? d1 : 0.f;
+                        }
+                        dk[i] = pack2<kF16>(d0, d1);
                     }
-                    dk[i] = pack2<kF16>(d0, d1);
+                    // dS over the first half of its own chunk of dP.
+                    tmem_st16(tmem + kColDP + col, dk);
                 }
-                // dS over the first half of its own chunk of S.
-                tmem_st16(tmem + col_s, dk);
                 tmem_wait_st();
                 tc_fence_before();
-                arrive(b.dq_full[pos & 1]);
+                arrive(b.p_full);
+                // S and dP of this piece are done: the next one's rows.
+                if (t + 1 == t1 && receive(b, k + 1, ok))
+                    make_resident(b.pieces[(k + 1) % kPieces]);
             }
         }
         if (!ok)
@@ -760,27 +875,26 @@ __device__ void bwd_elem(const CrossBwdArgs &a, BBars &b, BXch &xch, uint8_t *ti
         // dkdv: dV by warpgroups 0 and 1, dK by 2 and 3, alternate 32-column
         // chunks; dq: a chunk a warpgroup.
         const bool is_dv = kDkDv && quarter < 2;
-        const uint32_t acc = tmem + kColAcc0 + set * C::kAccCols + (kDkDv && !is_dv ? D : 0);
+        const uint32_t acc = tmem + C::kColAcc + set * C::kAccCols + (kDkDv && !is_dv ? D : 0);
         const float f = is_dv ? 1.f : a.scale / ds_scale;
         const bool whole = p.slot < 0;
-        const int row = p.tile * kTile + r;
-        const bool live = row < (kDkDv ? a.Nk : a.Nq);
-        const bool zero = kDkDv && row >= p.L;
+        const bool zero = kDkDv && p.tile * kTile + r >= p.L;
         const long long *st = kDkDv ? (is_dv ? a.dv_st : a.dk_st) : a.dq_st;
-        uint16_t *out = static_cast<uint16_t *>(kDkDv ? (is_dv ? a.dv : a.dk) : a.dq);
-        uint16_t *dst = out + p.b * st[0] + p.h * st[1] + row * st[2];
+        // This lane's piece of the first of its four rows, and the rows there are.
+        const int r4 = r & ~3, rows = (kDkDv ? a.Nk : a.Nq) - p.tile * kTile - r4;
+        uint16_t *dst = static_cast<uint16_t *>(kDkDv ? (is_dv ? a.dv : a.dk) : a.dq) + p.b * st[0] + p.h * st[1] +
+                        (static_cast<long long>(p.tile) * kTile + r4) * st[2] + (lane & 3) * 8;
         float *part = (kDkDv ? a.ws_kv : a.ws_q) +
-                      ((static_cast<long long>(p.slot) * (kDkDv ? 2 : 1) + (kDkDv && !is_dv ? 1 : 0)) * kTile + r) * D;
+                      ((static_cast<long long>(p.slot) * (kDkDv ? 2 : 1) + (kDkDv && !is_dv ? 1 : 0)) * kTile + r4) * D +
+                      (lane & 3) * 4;
 #pragma unroll 1
         for (int c = kDkDv ? quarter & 1 : quarter; c < D / 32; c += kDkDv ? 2 : 4) {
             uint32_t o[32];
             __syncwarp();
             tmem_ld32(acc + c * 32, o);
             tmem_wait_ld();
-            if (!live)
-                continue;
+            uint4 v[4];
             if (whole) {
-                uint4 *d4 = reinterpret_cast<uint4 *>(dst + c * 32);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     uint32_t x[4];
@@ -789,13 +903,26 @@ __device__ void bwd_elem(const CrossBwdArgs &a, BBars &b, BXch &xch, uint8_t *ti
                         x[j] = zero ? 0u
                                     : pack2<kF16>(__uint_as_float(o[8 * i + 2 * j]) * f,
                                                   __uint_as_float(o[8 * i + 2 * j + 1]) * f);
-                    d4[i] = make_uint4(x[0], x[1], x[2], x[3]);
+                    v[i] = make_uint4(x[0], x[1], x[2], x[3]);
                 }
-            } else {
-                uint4 *d4 = reinterpret_cast<uint4 *>(part + c * 32);
+                transpose4(v, lane);
 #pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    d4[i] = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+                for (int j = 0; j < 4; ++j)
+                    if (j < rows)
+                        *reinterpret_cast<uint4 *>(dst + c * 32 + j * st[2]) = v[j];
+            } else {
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        v[i] = make_uint4(o[16 * half + 4 * i], o[16 * half + 4 * i + 1], o[16 * half + 4 * i + 2],
+                                          o[16 * half + 4 * i + 3]);
+                    transpose4(v, lane);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        if (j < rows)
+                            *reinterpret_cast<uint4 *>(part + c * 32 + half * 16 + j * D) = v[j];
+                }
             }
         }
         give_back(b, k);
@@ -848,7 +975,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int warp = threadIdx.x / 32;
     if (threadIdx.x == 0) {
         for (int i = 0; i < 4; ++i) {
-            mbar_init(smem_addr(&b.res_full[i]), 1);
+            mbar_init(smem_addr(&b.res_full[i]), kDkDv ? 1 : kElemWarps);
             mbar_init(smem_addr(&b.res_empty[i]), 1);
             mbar_init(smem_addr(&b.st_full[i]), 1);
             mbar_init(smem_addr(&b.st_empty[i]), 1);
@@ -856,19 +983,17 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(smem_addr(&b.v_empty[i]), 1);
         }
         for (int i = 0; i < 2; ++i) {
+            mbar_init(smem_addr(&b.s_full[i]), 1);
             mbar_init(smem_addr(&b.o_full[i]), 1);
             mbar_init(smem_addr(&b.o_empty[i]), kElemWarps);
-            mbar_init(smem_addr(&b.dq_full[i]), kElemWarps);
         }
         for (int i = 0; i < kPieces; ++i) {
             mbar_init(smem_addr(&b.piece_full[i]), 1);
             mbar_init(smem_addr(&b.piece_empty[i]), kElemWarps + 1);
         }
-        mbar_init(smem_addr(&b.s_full), 1);
         mbar_init(smem_addr(&b.p_full), kElemWarps);
         mbar_init(smem_addr(&b.p1_full), kElemWarps);
         mbar_init(smem_addr(&b.dp_full), 1);
-        mbar_init(smem_addr(&b.dp_free), kElemWarps);
         mbar_init(smem_addr(&b.drain), 1);
         b.abort = 0;
         fence_barrier_init();

@@ -261,7 +261,7 @@ cudaError_t launch_kv_fork(const KvForkArgs &a, cudaStream_t stream);
 // Gradients of cross attention, already validated.  Strides (batch, head, row)
 // in elements.
 struct CrossBwdArgs {
-    const void *o, *dout;
+    const void *q, *o, *dout;
     const float *lse;
     const int *kv_len;  // may be null
     void *dq, *dk, *dv;
@@ -270,7 +270,7 @@ struct CrossBwdArgs {
     float *dvec, *amax, *ws_kv, *ws_q;
     int4 *starts;
     uint32_t *status;
-    long long o_st[3], do_st[3], dq_st[3], dk_st[3], dv_st[3];
+    long long q_st[3], o_st[3], do_st[3], dq_st[3], dk_st[3], dv_st[3];
     int B, Hk, G, Nq, Nk, Tq, d, f16, grid;
     float scale, sl2;
     int prep_blocks;  // filled in by the launch
