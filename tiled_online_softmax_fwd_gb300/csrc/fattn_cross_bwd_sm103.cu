@@ -67,27 +67,29 @@ constexpr int kUnitCost = 3, kSnap = 2, kLeast = 8;
 template <int D, bool kDkDv> struct BCfg {
     static constexpr int kChunks = (D + 63) / 64;
     static constexpr uint32_t kTileBytes = kChunks * kChunkBytes;  // one [128][D] tile
-    // dkdv: slots of the resident tiles, which take turns (K_j, V_j, K_j', ...): at
-    // d = 64 the next unit's are there before this one ends.  (dq: Q and dO are in
-    // TMEM.)  Then the streamed tiles, dkdv: Q and dO; dq: K (held until dQ) and V.
-    static constexpr int kRes = !kDkDv ? 0 : D == 64 ? 4 : 2;
-    static constexpr int kStages = !kDkDv || D == 64 ? 4 : 2;
-    static constexpr int kStages2 = kDkDv ? kStages : 3;
+    // Slots of the resident tiles, which take turns (K_j, V_j, K_j', ... or Q_i, dO_i,
+    // ...); dq copies them to TMEM, so a slot is free at once.  Then the streamed
+    // tiles, dkdv: Q and dO; dq: K (held until dQ) and V.
+    static constexpr int kRes = D == 64 ? 4 : 2;
+    static constexpr int kStages = D == 64 ? 4 : kDkDv ? 2 : 3;
+    static constexpr int kStages2 = kDkDv ? kStages : D == 64 ? 3 : 2;
     static constexpr uint32_t kRing = kRes * kTileBytes;
     static constexpr uint32_t kRing2 = kRing + kStages * kTileBytes;
     static constexpr uint32_t kTilesBytes = kRing2 + kStages2 * kTileBytes;
-    // TMEM: S, dP; dkdv: at d = 64 another S, so that the next one is there when
-    // the elementwise pass is done with this; dV and dK; dq: dQ, two where they
-    // fit, Q and dO.
-    static constexpr int kSs = kDkDv && D == 64 ? 2 : 1;
-    static constexpr uint32_t kColAcc = kSs == 2 ? 384 : 256;
-    static constexpr int kAccs = !kDkDv && D == 64 ? 2 : 1;
+    // TMEM: S, dP; at d = 64 a second S (dkdv) or dP (dq), so that the next one is
+    // there when the elementwise pass is done with this; the sums; dq: Q and dO.
+    static constexpr int kTwo = D == 64;
+    static constexpr uint32_t kColAcc = kTwo ? 384 : 256;
     static constexpr uint32_t kAccCols = kDkDv ? 2 * D : D;
-    static constexpr uint32_t kColQ = kColAcc + kAccs * kAccCols, kColDO = kColQ + D / 2;
+    static constexpr uint32_t kColQ = kColAcc + kAccCols, kColDO = kColQ + D / 2;
     static_assert((kDkDv ? kColQ : kColDO + D / 2) <= kTmemCols, "TMEM columns");
     static __device__ __forceinline__ uint32_t s_col(uint32_t pos)
     {
-        return kSs == 2 && (pos & 1) ? 256 : kColS;
+        return kDkDv && kTwo && (pos & 1) ? 256 : kColS;
+    }
+    static __device__ __forceinline__ uint32_t dp_col(uint32_t pos)
+    {
+        return !kDkDv && kTwo && (pos & 1) ? 256 : kColDP;
     }
 };
 
@@ -107,12 +109,13 @@ struct Piece {
 constexpr int kPieces = 4;  // published ahead
 
 struct alignas(16) BBars {
-    uint64_t res_full[4], res_empty[4];  // dq: full[0], Q and dO written
+    uint64_t res_full[4], res_empty[4], q_full;  // q_full: dq, Q and dO are in TMEM
     uint64_t st_full[4], st_empty[4];  // dkdv: Q stages; dq: K stages
     uint64_t v_full[4], v_empty[4];    // dkdv: dO stages; dq: V stages
-    uint64_t s_full[2], p_full, o_full[2], o_empty[2];  // s_full: of tile n on n % 2
+    uint64_t s_full[2], dp_full[2];  // of tile n on n % 2
+    uint64_t p_full, o_full, o_empty;
     uint64_t piece_full[kPieces], piece_empty[kPieces];
-    uint64_t p1_full, dp_full;  // P^T written (dq: S is in registers); dP computed
+    uint64_t p1_full;  // P^T written (dq: S is in registers)
     uint64_t drain;
     uint32_t tmem_base;
     int abort;
@@ -152,6 +155,13 @@ __device__ __forceinline__ int step_at(long long y, int steps)
     return t < kSnap ? 0 : steps - t < kSnap ? steps : t;
 }
 
+// a / b of non-negative values, in 32 bits where they fit.
+__device__ __noinline__ long long long_quotient(long long a, long long b) { return a / b; }
+__device__ __forceinline__ long long quotient(long long a, int b)
+{
+    return (a >> 32) == 0 ? static_cast<unsigned>(a) / static_cast<unsigned>(b) : long_quotient(a, b);
+}
+
 struct Walk {
     Start at;
     int L, units, steps, u;
@@ -169,7 +179,7 @@ template <bool kDkDv> __device__ __forceinline__ Walk first_walk(const CrossBwdA
     if (w.at.left > 0) {
         enter<kDkDv>(a, w);
         const int cost = w.steps + kUnitCost;
-        w.u = static_cast<int>(w.at.y / cost);
+        w.u = static_cast<int>(quotient(w.at.y, cost));
         w.at.y -= static_cast<long long>(w.u) * cost;
     }
     return w;
@@ -229,7 +239,8 @@ template <bool kDkDv> __device__ void find_start(const CrossBwdArgs &a, BBars &b
         total += b.warp_sum[w];
     const int c = blockIdx.x;
     const int shares = static_cast<int>(min(static_cast<long long>(gridDim.x), max(total / kLeast, 1LL)));
-    const long long each = total / shares, rest = total - each * shares;
+    const long long each = quotient(total, shares);
+    const int rest = static_cast<int>(total - each * shares);
     const long long lo = c * each + c * rest / shares, hi = (c + 1) * each + (c + 1) * rest / shares;
     int4 *starts = a.starts + (kDkDv ? 0 : a.grid);
     if (c >= shares || lo >= hi) {
@@ -258,7 +269,7 @@ template <bool kDkDv> __device__ void find_start(const CrossBwdArgs &a, BBars &b
         const long long first = before + incl - mine;
         if (first <= lo && lo < first + mine) {
             b.start = Start{i, lo - first, hi - lo};
-            const int cost = steps + kUnitCost, u = static_cast<int>((lo - first) / cost);
+            const int cost = steps + kUnitCost, u = static_cast<int>(quotient(lo - first, cost));
             const int t = step_at(lo - first - static_cast<long long>(u) * cost, steps);
             const int per = kDkDv ? units / a.Hk : a.Tq;
             starts[c] = make_int4(i, u / per, u % per, t < steps ? t : 0);
@@ -405,9 +416,8 @@ __device__ void bwd_load(const CrossBwdArgs &a, BBars &b, uint32_t smem, const C
         if (!more)
             break;
         const int head = uniform(p.h), batch = uniform(p.b), own = uniform(p.tile * kTile);
-        if constexpr (kDkDv)
-            ok = load(b.res_full, b.res_empty, rpos, C::kRes, 0, mk, own, head, batch) &&
-                 load(b.res_full, b.res_empty, rpos, C::kRes, 0, mv, own, head, batch);
+        ok = load(b.res_full, b.res_empty, rpos, C::kRes, 0, kDkDv ? mk : mq, own, head, batch) &&
+             load(b.res_full, b.res_empty, rpos, C::kRes, 0, kDkDv ? mv : mdo, own, head, batch);
         int g = kDkDv ? p.t0 / a.Tq : 0, i = kDkDv ? p.t0 - g * a.Tq : 0;
         for (int t = p.t0; ok && t < p.t1; ++t) {
             if constexpr (kDkDv) {
@@ -436,8 +446,7 @@ __device__ void bwd_load(const CrossBwdArgs &a, BBars &b, uint32_t smem, const C
         };
         land(b.st_full, kpos, C::kStages);
         land(b.v_full, vpos, C::kStages2);
-        if constexpr (kDkDv)
-            land(b.res_full, rpos, C::kRes);
+        land(b.res_full, rpos, C::kRes);
     }
 }
 
@@ -475,7 +484,7 @@ __device__ void bwd_mma(const CrossBwdArgs &a, BBars &b, uint32_t smem, uint32_t
             return 0;
         return static_cast<int>(uniform_of(b.pieces[k % kPieces].t1 - b.pieces[k % kPieces].t0, lane));
     };
-    Ring<(kDkDv ? C::kRes : 2)> res0, res1;  // dkdv: of the piece that S and dP are at
+    Ring<C::kRes> res0, res1;  // dkdv: of the piece that S and dP are at
     res1.step();
     Ring<C::kStages> st_s, st_k;  // of S, and of dK or dQ
     Ring<C::kStages2> v_d, v_v;   // of dP, and of dV
@@ -488,7 +497,7 @@ __device__ void bwd_mma(const CrossBwdArgs &a, BBars &b, uint32_t smem, uint32_t
     };
     // S (S^T) of a tile, the `t`-th of the `n` of piece `k`, `pos`-th of all; dP (dP^T).
     auto scores = [&](uint32_t k, uint32_t pos, int t, int n) {
-        ok = ok && (t > 0 || (kDkDv ? wait(b.res_full[res0.slot], res0.phase) : wait(b.res_full[0], k))) &&
+        ok = ok && (t > 0 || (kDkDv ? wait(b.res_full[res0.slot], res0.phase) : wait(b.q_full, k))) &&
              wait(b.st_full[st_s.slot], st_s.phase);
         if (!ok)
             return;
@@ -504,7 +513,7 @@ __device__ void bwd_mma(const CrossBwdArgs &a, BBars &b, uint32_t smem, uint32_t
         }
         st_s.step();
     };
-    auto grads = [&](int t, int n) {
+    auto grads = [&](uint32_t pos, int t, int n) {
         ok = ok && (t > 0 || !kDkDv || wait(b.res_full[res1.slot], res1.phase)) &&
              wait(b.v_full[v_d.slot], v_d.phase);
         if (!ok)
@@ -513,8 +522,8 @@ __device__ void bwd_mma(const CrossBwdArgs &a, BBars &b, uint32_t smem, uint32_t
         if constexpr (kDkDv)
             mma_nt<D, kF16>(tmem + kColDP, at(0, res1.slot), at(C::kRing2, v_d.slot));
         else
-            mma_nt_ts<D, kF16>(tmem + kColDP, tmem + C::kColDO, at(C::kRing2, v_d.slot));
-        commit(b.dp_full);
+            mma_nt_ts<D, kF16>(tmem + C::dp_col(pos), tmem + C::kColDO, at(C::kRing2, v_d.slot));
+        commit(b.dp_full[pos & 1]);
         if (!kDkDv)
             commit(b.v_empty[v_d.slot]);
         if (kDkDv && t + 1 == n) {
@@ -526,38 +535,41 @@ __device__ void bwd_mma(const CrossBwdArgs &a, BBars &b, uint32_t smem, uint32_t
     int n = tiles_of(0);
     if (n > 0) {
         scores(0, 0, 0, n);
-        grads(0, n);
+        grads(0, 0, n);
     }
+    const uint32_t acc = tmem + C::kColAcc;
     while (ok && n > 0) {
-        const uint32_t set = piece % C::kAccs, acc = uniform_of(tmem + C::kColAcc + set * C::kAccCols, lane);
         int next = 0;
         for (int t = 0; ok && t < n; ++t, ++pos) {
             // The tile after this one: of this piece or the first of the next.
             const bool last = t + 1 == n;
             const int t_next = last ? 0 : t + 1;
-            auto acc_wait = [&]() { return t > 0 || wait(b.o_empty[set], (piece / C::kAccs) ^ 1); };
+            auto acc_wait = [&]() { return t > 0 || wait(b.o_empty, piece ^ 1); };
             if constexpr (!kDkDv) {
                 // dS is written over dP.  S of the next tile once this one's is in
-                // registers, dP of it after dQ; another piece's Q and dO are written
-                // after this one's last dS.
+                // registers, dP of it after dQ (with another dP at once); another
+                // piece's Q and dO are written after this one's last dS.
                 ok = ok && wait(b.p1_full, pos);
-                if (!last)
+                if (!last) {
                     scores(piece, pos + 1, t_next, n);
+                    if (C::kTwo)
+                        grads(pos + 1, t_next, n);
+                }
                 ok = ok && wait(b.p_full, pos) && acc_wait();
                 if (!ok)
                     break;
                 tc_fence_after();
-                mma_tn<D, kF16>(acc, tmem + kColDP, at(C::kRing, st_k.slot), t > 0);  // dQ += dS K
+                mma_tn<D, kF16>(acc, tmem + C::dp_col(pos), at(C::kRing, st_k.slot), t > 0);  // dQ += dS K
                 commit(b.st_empty[st_k.slot]);
                 st_k.step();
                 if (last) {
-                    commit(b.o_full[set]);
+                    commit(b.o_full);
                     next = tiles_of(piece + 1);
                     if (next > 0)
                         scores(piece + 1, pos + 1, 0, next);
                 }
-                if (!last || next > 0)
-                    grads(t_next, last ? next : n);
+                if (last ? next > 0 : !C::kTwo)
+                    grads(pos + 1, t_next, last ? next : n);
             } else {
                 // P^T is written over S^T, dS^T over dP^T: the next S^T follows dV
                 // (with another S it is ahead), the next dP^T dK.
@@ -568,7 +580,7 @@ __device__ void bwd_mma(const CrossBwdArgs &a, BBars &b, uint32_t smem, uint32_t
                     if (n_next > 0)
                         scores(last ? piece + 1 : piece, pos + 1, t_next, n_next);
                 };
-                if constexpr (C::kSs == 2)
+                if constexpr (C::kTwo)
                     next_scores();
                 ok = ok && wait(b.p1_full, pos) && acc_wait();
                 if (!ok)
@@ -577,7 +589,7 @@ __device__ void bwd_mma(const CrossBwdArgs &a, BBars &b, uint32_t smem, uint32_t
                 mma_tn<D, kF16>(acc, tmem + C::s_col(pos), at(C::kRing2, v_v.slot), t > 0);  // dV += P^T dO
                 commit(b.v_empty[v_v.slot]);
                 v_v.step();
-                if constexpr (C::kSs == 1)
+                if constexpr (!C::kTwo)
                     next_scores();
                 ok = ok && wait(b.p_full, pos);
                 if (!ok)
@@ -587,9 +599,9 @@ __device__ void bwd_mma(const CrossBwdArgs &a, BBars &b, uint32_t smem, uint32_t
                 commit(b.st_empty[st_k.slot]);
                 st_k.step();
                 if (last)
-                    commit(b.o_full[set]);
+                    commit(b.o_full);
                 if (n_next > 0)
-                    grads(t_next, n_next);
+                    grads(pos + 1, t_next, n_next);
             }
         }
         if (!ok)
@@ -669,60 +681,57 @@ __device__ void bwd_elem(const CrossBwdArgs &a, BBars &b, BXch &xch, uint8_t *ti
         next_lse = q < a.Nq ? a.lse[at] : 0.f;
         next_d = q < a.Nq ? a.dvec[at] : 0.f;
     };
-    // dq: a piece's rows of Q and dO into TMEM, 32 elements of a row a job, a lane
-    // a row.
-    auto make_resident = [&](const Piece &p) {
+    // dq: the k-th piece's Q and dO into TMEM, 32 elements of a row a job, a lane a
+    // row; and the row's lse and D.
+    float row_nl2 = 0.f, row_nd = 0.f;
+    auto make_resident = [&](uint32_t k, const Piece &p) {
         const int row = p.tile * kTile + r;
-        constexpr int kJobs = D / 32;  // of each tensor
-        uint32_t x[2][16];
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int job = quarter + 4 * i;
-#pragma unroll
-            for (int j = 0; j < 16; ++j)
-                x[i][j] = 0;
-            if (job < 2 * kJobs && row < a.Nq) {
-                const bool is_q = job < kJobs;
-                const long long *st = is_q ? a.q_st : a.do_st;
-                const uint16_t *src = static_cast<const uint16_t *>(is_q ? a.q : a.dout) + p.b * st[0] + p.h * st[1] +
-                                      row * st[2] + (is_q ? job : job - kJobs) * 32;
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const uint4 v = reinterpret_cast<const uint4 *>(src)[j];
-                    x[i][4 * j] = v.x;
-                    x[i][4 * j + 1] = v.y;
-                    x[i][4 * j + 2] = v.z;
-                    x[i][4 * j + 3] = v.w;
-                }
-            }
+        row_nl2 = row_nd = 0.f;
+        if (row < a.Nq) {
+            const long long at = (static_cast<long long>(p.b) * a.Hk * a.G + p.h) * a.Nq + row;
+            row_nl2 = a.lse[at];
+            row_nd = a.dvec[at];
         }
-        __syncwarp();
+        constexpr int kJobs = D / 32;  // of each tensor
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            const int job = quarter + 4 * i;
-            if (job < 2 * kJobs)  // kColDO follows kColQ
-                tmem_st16(tmem + C::kColQ + job * 16, x[i]);
+            const uint32_t slot = (2 * k + i) % C::kRes;
+            ok = ok && wait(b.res_full[slot], (2 * k + i) / C::kRes);
+#pragma unroll
+            for (int j = 0; j < (kJobs + 3) / 4; ++j) {
+                // dO's jobs begin where Q's end (kColDO follows kColQ).
+                const int job = (quarter + 4 * j + (i == 0 ? 0 : 4 - kJobs % 4)) % 4 + 4 * j;
+                if (!ok || job >= kJobs)
+                    continue;
+                const uint8_t *tile = tiles + slot * C::kTileBytes + (job / 2) * kChunkBytes + r * 128;
+                uint32_t x[16];
+#pragma unroll
+                for (int g = 0; g < 4; ++g) {  // 16-byte piece g of the row is at g ^ (r % 8)
+                    const uint4 v = reinterpret_cast<const uint4 *>(tile)[((job % 2) * 4 + g) ^ (r & 7)];
+                    x[4 * g] = v.x;
+                    x[4 * g + 1] = v.y;
+                    x[4 * g + 2] = v.z;
+                    x[4 * g + 3] = v.w;
+                }
+                __syncwarp();
+                tmem_st16(tmem + (i == 0 ? C::kColQ : C::kColDO) + job * 16, x);
+            }
+            arrive(b.res_empty[slot]);
         }
         tmem_wait_st();
         tc_fence_before();
-        arrive(b.res_full[0]);
+        arrive(b.q_full);
+        row_nl2 = neg_lse2(row_nl2);
+        row_nd *= -ds_scale;
     };
     for (uint32_t k = 0; receive(b, k, ok); ++k) {
         const Piece &p = b.pieces[k % kPieces];
         const int t0 = p.t0, t1 = p.t1;
-        float row_nl2 = 0.f, row_nd = 0.f;
-        if (kDkDv) {
-            if (k == 0)
+        if (k == 0) {
+            if (kDkDv)
                 fetch(p, t0);
-        } else {
-            if (k == 0)
-                make_resident(p);
-            const int row = p.tile * kTile + r;
-            if (row < a.Nq) {
-                const long long at = (static_cast<long long>(p.b) * a.Hk * a.G + p.h) * a.Nq + row;
-                row_nl2 = neg_lse2(a.lse[at]);
-                row_nd = -a.dvec[at] * ds_scale;
-            }
+            else
+                make_resident(k, p);
         }
         for (int t = t0; ok && t < t1; ++t, ++pos) {
             if constexpr (kDkDv) {
@@ -769,7 +778,7 @@ __device__ void bwd_elem(const CrossBwdArgs &a, BBars &b, BXch &xch, uint8_t *ti
                 tc_fence_before();
                 arrive(b.p1_full);
                 // dS^T = P^T (dP^T - D) over the first 16 columns of the chunk.
-                ok = wait(b.dp_full, pos);
+                ok = wait(b.dp_full[pos & 1], pos >> 1);
                 if (!ok)
                     break;
                 tc_fence_after();
@@ -831,14 +840,14 @@ __device__ void bwd_elem(const CrossBwdArgs &a, BBars &b, BXch &xch, uint8_t *ti
                             k_tile[at] = make_uint4(0, 0, 0, 0);
                     fence_proxy_async_smem();
                 }
-                ok = wait(b.dp_full, pos);
+                ok = wait(b.dp_full[pos & 1], pos >> 1);
                 if (!ok)
                     break;
                 tc_fence_after();
                 {
                     uint32_t dr[32], dk[16];
                     __syncwarp();
-                    tmem_ld32(tmem + kColDP + col, dr);
+                    tmem_ld32(tmem + C::dp_col(pos) + col, dr);
                     tmem_wait_ld();
                     const uint64_t nd = f2_pack(row_nd, row_nd);
 #pragma unroll
@@ -855,27 +864,26 @@ __device__ void bwd_elem(const CrossBwdArgs &a, BBars &b, BXch &xch, uint8_t *ti
                         dk[i] = pack2<kF16>(d0, d1);
                     }
                     // dS over the first half of its own chunk of dP.
-                    tmem_st16(tmem + kColDP + col, dk);
+                    tmem_st16(tmem + C::dp_col(pos) + col, dk);
                 }
                 tmem_wait_st();
                 tc_fence_before();
                 arrive(b.p_full);
                 // S and dP of this piece are done: the next one's rows.
                 if (t + 1 == t1 && receive(b, k + 1, ok))
-                    make_resident(b.pieces[(k + 1) % kPieces]);
+                    make_resident(k + 1, b.pieces[(k + 1) % kPieces]);
             }
         }
         if (!ok)
             break;
-        const uint32_t set = k % C::kAccs;
-        ok = wait(b.o_full[set], k / C::kAccs);
+        ok = ok && wait(b.o_full, k);
         if (!ok)
             break;
         tc_fence_after();
         // dkdv: dV by warpgroups 0 and 1, dK by 2 and 3, alternate 32-column
         // chunks; dq: a chunk a warpgroup.
         const bool is_dv = kDkDv && quarter < 2;
-        const uint32_t acc = tmem + C::kColAcc + set * C::kAccCols + (kDkDv && !is_dv ? D : 0);
+        const uint32_t acc = tmem + C::kColAcc + (kDkDv && !is_dv ? D : 0);
         const float f = is_dv ? 1.f : a.scale / ds_scale;
         const bool whole = p.slot < 0;
         const bool zero = kDkDv && p.tile * kTile + r >= p.L;
@@ -927,7 +935,7 @@ __device__ void bwd_elem(const CrossBwdArgs &a, BBars &b, BXch &xch, uint8_t *ti
         }
         give_back(b, k);
         tc_fence_before();
-        arrive(b.o_empty[set]);
+        arrive(b.o_empty);
     }
     if (!ok)
         fail(a, b, kRoleSoftmax);
@@ -975,8 +983,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int warp = threadIdx.x / 32;
     if (threadIdx.x == 0) {
         for (int i = 0; i < 4; ++i) {
-            mbar_init(smem_addr(&b.res_full[i]), kDkDv ? 1 : kElemWarps);
-            mbar_init(smem_addr(&b.res_empty[i]), 1);
+            mbar_init(smem_addr(&b.res_full[i]), 1);
+            mbar_init(smem_addr(&b.res_empty[i]), kDkDv ? 1 : kElemWarps);
             mbar_init(smem_addr(&b.st_full[i]), 1);
             mbar_init(smem_addr(&b.st_empty[i]), 1);
             mbar_init(smem_addr(&b.v_full[i]), 1);
@@ -984,16 +992,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(smem_addr(&b.s_full[i]), 1);
-            mbar_init(smem_addr(&b.o_full[i]), 1);
-            mbar_init(smem_addr(&b.o_empty[i]), kElemWarps);
+            mbar_init(smem_addr(&b.dp_full[i]), 1);
         }
+        mbar_init(smem_addr(&b.o_full), 1);
+        mbar_init(smem_addr(&b.o_empty), kElemWarps);
+        mbar_init(smem_addr(&b.q_full), kElemWarps);
         for (int i = 0; i < kPieces; ++i) {
             mbar_init(smem_addr(&b.piece_full[i]), 1);
             mbar_init(smem_addr(&b.piece_empty[i]), kElemWarps + 1);
         }
         mbar_init(smem_addr(&b.p_full), kElemWarps);
         mbar_init(smem_addr(&b.p1_full), kElemWarps);
-        mbar_init(smem_addr(&b.dp_full), 1);
         mbar_init(smem_addr(&b.drain), 1);
         b.abort = 0;
         fence_barrier_init();
@@ -1008,9 +1017,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         prefetch_tensormap(&mv);
         prefetch_tensormap(&mdo);
     }
-    grid_dependency_wait();
-    find_scale<kF16>(a, b);
+    // The kernel ahead has begun, so what it waited for is there: the lengths, and
+    // for dq, behind dkdv, all that it reads; dq only ends behind dkdv.
     find_start<kDkDv>(a, b);
+    if (kDkDv) {
+        grid_dependency_wait();
+        grid_launch_dependents();
+    }
+    find_scale<kF16>(a, b);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -1025,7 +1039,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             bwd_mma<D, kF16, kDkDv>(a, b, smem, tmem, lane);
         __syncwarp();
     }
-    grid_launch_dependents();
+    if (!kDkDv) {
+        grid_launch_dependents();
+        grid_dependency_wait();
+    }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -1067,6 +1084,7 @@ template <int D, bool kF16> __global__ void __launch_bounds__(kPrepThreads) cros
 {
     constexpr int kLanes = D / 8, kGroup = D == 64 ? 8 : 16;
     grid_dependency_wait();
+    grid_launch_dependents();
     const int lane = threadIdx.x & 31, part = lane % kGroup;
     const int groups = kPrepThreads / kGroup;
     const long long stride = static_cast<long long>(gridDim.x) * groups;
