@@ -193,3 +193,21 @@ def test_a_captured_call_follows_its_lengths():
         torch.cuda.synchronize()
         verify(out, q, k, v, do, n, str(n))
     assert fattn.device_status() == 0
+
+
+@pytest.mark.parametrize("d,Nq,Nk", [(64, 2048, 2048), (64, 2048, 200), (96, 900, 900), (128, 1024, 1024)])
+def test_many_calls_in_a_row(d, Nq, Nk):
+    """No wait of the pipelines ever runs out, whatever the warps' order: some
+    thousand calls of many tiles, the last one's bits the first one's."""
+    g = torch.Generator().manual_seed(13)
+    q, do = (torch.randn(4, 8, Nq, d, generator=g).bfloat16().cuda() for _ in range(2))
+    k, v = (torch.randn(4, 8, Nk, d, generator=g).bfloat16().cuda() for _ in range(2))
+    o, lse = fattn.attn_fwd_cross(q, k, v)
+    first = fattn.attn_bwd_cross(q, k, v, o, lse, do)
+    outs = [torch.empty_like(t) for t in first]
+    ws = torch.empty(fattn.cross_bwd_workspace_size(4, 8, 8, Nq, Nk, d), dtype=torch.uint8, device="cuda")
+    for _ in range(2000):
+        fattn.attn_bwd_cross(q, k, v, o, lse, do, dq=outs[0], dk=outs[1], dv=outs[2], workspace=ws)
+    torch.cuda.synchronize()
+    assert fattn.device_status() == 0
+    assert all(torch.equal(x, y) for x, y in zip(first, outs))

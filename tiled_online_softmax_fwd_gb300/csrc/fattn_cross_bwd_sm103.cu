@@ -112,17 +112,19 @@ struct alignas(16) BBars {
     uint64_t res_full[4], res_empty[4], q_full;  // q_full: dq, Q and dO are in TMEM
     uint64_t st_full[4], st_empty[4];  // dkdv: Q stages; dq: K stages
     uint64_t v_full[4], v_empty[4];    // dkdv: dO stages; dq: V stages
-    uint64_t s_full[2], dp_full[2];  // of tile n on n % 2
-    uint64_t p_full, o_full, o_empty;
+    // Of tile n on n % 2: S and dP computed, P^T (dq: S is in registers) and dS
+    // written.  With two S or two dP the elementwise pass can be done with the tile
+    // after the one that the MMA lane is about to wait for: on one barrier that
+    // would be two phases, which a parity does not tell from none.
+    uint64_t s_full[2], dp_full[2], p1_full[2], p_full[2];
+    uint64_t o_full, o_empty;
     uint64_t piece_full[kPieces], piece_empty[kPieces];
-    uint64_t p1_full;  // P^T written (dq: S is in registers)
     uint64_t drain;
     uint32_t tmem_base;
     int abort;
     float ds_scale;  // of dS
     Start start;
     Piece pieces[kPieces];
-    long long warp_sum[kThreads / 32];
     float warp_max[kThreads / 32];
 };
 // dkdv, behind the barriers: each warp's -lse log2(e) and -D (scaled) of the 32
@@ -215,30 +217,28 @@ template <bool kDkDv> __device__ __forceinline__ bool next_piece(const CrossBwdA
     return false;
 }
 
-// The whole block finds this CTA's start.
+// Finds this CTA's start: warp 0 alone, 32 sequences at a time.
 template <bool kDkDv> __device__ void find_start(const CrossBwdArgs &a, BBars &b)
 {
-    const int tid = threadIdx.x, lane = tid & 31;
-    long long sum = 0;
-    for (int i = tid; i < a.B; i += kThreads) {
-        int units, steps;
-        units_of<kDkDv>(a, clamp_len(a, i), units, steps);
-        sum += static_cast<long long>(units) * (steps + kUnitCost);
-    }
+    if (threadIdx.x >= 32)
+        return;
+    const int lane = threadIdx.x;
+    // Cost of sequence i, whose lengths the second walk finds in the cache.
+    auto cost_of = [&](int i, int &units, int &steps) {
+        units = steps = 0;
+        if (i < a.B)
+            units_of<kDkDv>(a, clamp_len(a, i), units, steps);
+        return static_cast<long long>(units) * (steps + kUnitCost);
+    };
+    int units, steps;
+    long long total = 0;
+    for (int i = lane; i < a.B; i += 32)
+        total += cost_of(i, units, steps);
 #pragma unroll
     for (int o = 16; o > 0; o /= 2)
-        sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    if (lane == 0)
-        b.warp_sum[tid / 32] = sum;
-    __syncthreads();
-    if (tid >= 32)
-        return;
-    long long total = 0;
-#pragma unroll
-    for (int w = 0; w < kThreads / 32; ++w)
-        total += b.warp_sum[w];
+        total += __shfl_xor_sync(0xffffffffu, total, o);
     const int c = blockIdx.x;
-    const int shares = static_cast<int>(min(static_cast<long long>(gridDim.x), max(total / kLeast, 1LL)));
+    const int shares = static_cast<int>(min(static_cast<long long>(gridDim.x), max(quotient(total, kLeast), 1LL)));
     const long long each = quotient(total, shares);
     const int rest = static_cast<int>(total - each * shares);
     const long long lo = c * each + c * rest / shares, hi = (c + 1) * each + (c + 1) * rest / shares;
@@ -250,16 +250,10 @@ template <bool kDkDv> __device__ void find_start(const CrossBwdArgs &a, BBars &b
         }
         return;
     }
-    // 32 sequences at a time until the one that holds this CTA's first cost.
+    // The sequence that holds this CTA's first cost.
     long long before = 0;
-    for (int b0 = 0; b0 < a.B; b0 += 32) {
-        const int i = b0 + lane;
-        int L = 0, units = 0, steps = 0;
-        if (i < a.B) {
-            L = clamp_len(a, i);
-            units_of<kDkDv>(a, L, units, steps);
-        }
-        const long long mine = static_cast<long long>(units) * (steps + kUnitCost);
+    for (int b0 = 0; b0 < a.B && before <= lo; b0 += 32) {
+        const long long mine = cost_of(b0 + lane, units, steps);
         long long incl = mine;
 #pragma unroll
         for (int o = 1; o < 32; o *= 2) {
@@ -268,11 +262,11 @@ template <bool kDkDv> __device__ void find_start(const CrossBwdArgs &a, BBars &b
         }
         const long long first = before + incl - mine;
         if (first <= lo && lo < first + mine) {
-            b.start = Start{i, lo - first, hi - lo};
+            b.start = Start{b0 + lane, lo - first, hi - lo};
             const int cost = steps + kUnitCost, u = static_cast<int>(quotient(lo - first, cost));
             const int t = step_at(lo - first - static_cast<long long>(u) * cost, steps);
-            const int per = kDkDv ? units / a.Hk : a.Tq;
-            starts[c] = make_int4(i, u / per, u % per, t < steps ? t : 0);
+            const int per = kDkDv ? units / a.Hk : a.Tq, h = u / per;
+            starts[c] = make_int4(b0 + lane, h, u - h * per, t < steps ? t : 0);
         }
         before += __shfl_sync(0xffffffffu, incl, 31);
     }
@@ -549,13 +543,13 @@ __device__ void bwd_mma(const CrossBwdArgs &a, BBars &b, uint32_t smem, uint32_t
                 // dS is written over dP.  S of the next tile once this one's is in
                 // registers, dP of it after dQ (with another dP at once); another
                 // piece's Q and dO are written after this one's last dS.
-                ok = ok && wait(b.p1_full, pos);
+                ok = ok && wait(b.p1_full[pos & 1], pos >> 1);
                 if (!last) {
                     scores(piece, pos + 1, t_next, n);
                     if (C::kTwo)
                         grads(pos + 1, t_next, n);
                 }
-                ok = ok && wait(b.p_full, pos) && acc_wait();
+                ok = ok && wait(b.p_full[pos & 1], pos >> 1) && acc_wait();
                 if (!ok)
                     break;
                 tc_fence_after();
@@ -572,7 +566,8 @@ __device__ void bwd_mma(const CrossBwdArgs &a, BBars &b, uint32_t smem, uint32_t
                     grads(pos + 1, t_next, last ? next : n);
             } else {
                 // P^T is written over S^T, dS^T over dP^T: the next S^T follows dV
-                // (with another S it is ahead), the next dP^T dK.
+                // (with another S it is ahead), the next dP^T dK.  Behind a piece's last
+                // tile dK goes first where the next piece's K is still to be loaded.
                 int n_next = n;
                 auto next_scores = [&]() {
                     if (last)
@@ -582,24 +577,27 @@ __device__ void bwd_mma(const CrossBwdArgs &a, BBars &b, uint32_t smem, uint32_t
                 };
                 if constexpr (C::kTwo)
                     next_scores();
-                ok = ok && wait(b.p1_full, pos) && acc_wait();
+                ok = ok && wait(b.p1_full[pos & 1], pos >> 1) && acc_wait();
                 if (!ok)
                     break;
                 tc_fence_after();
                 mma_tn<D, kF16>(acc, tmem + C::s_col(pos), at(C::kRing2, v_v.slot), t > 0);  // dV += P^T dO
                 commit(b.v_empty[v_v.slot]);
                 v_v.step();
-                if constexpr (!C::kTwo)
+                if (!C::kTwo && !last)
                     next_scores();
-                ok = ok && wait(b.p_full, pos);
+                ok = ok && wait(b.p_full[pos & 1], pos >> 1);
                 if (!ok)
                     break;
                 tc_fence_after();
                 mma_tn<D, kF16>(acc + D, tmem + kColDP, at(C::kRing, st_k.slot), t > 0);  // dK += dS^T Q
                 commit(b.st_empty[st_k.slot]);
                 st_k.step();
-                if (last)
+                if (last) {
                     commit(b.o_full);
+                    if (!C::kTwo)
+                        next_scores();
+                }
                 if (n_next > 0)
                     grads(pos + 1, t_next, n_next);
             }
@@ -682,16 +680,15 @@ __device__ void bwd_elem(const CrossBwdArgs &a, BBars &b, BXch &xch, uint8_t *ti
         next_d = q < a.Nq ? a.dvec[at] : 0.f;
     };
     // dq: the k-th piece's Q and dO into TMEM, 32 elements of a row a job, a lane a
-    // row; and the row's lse and D.
+    // row; and the row's lse and D, fetched before.
     float row_nl2 = 0.f, row_nd = 0.f;
-    auto make_resident = [&](uint32_t k, const Piece &p) {
+    auto fetch_row = [&](const Piece &p) {
         const int row = p.tile * kTile + r;
-        row_nl2 = row_nd = 0.f;
-        if (row < a.Nq) {
-            const long long at = (static_cast<long long>(p.b) * a.Hk * a.G + p.h) * a.Nq + row;
-            row_nl2 = a.lse[at];
-            row_nd = a.dvec[at];
-        }
+        const long long at = (static_cast<long long>(p.b) * a.Hk * a.G + p.h) * a.Nq + row;
+        next_lse = row < a.Nq ? a.lse[at] : 0.f;
+        next_d = row < a.Nq ? a.dvec[at] : 0.f;
+    };
+    auto make_resident = [&](uint32_t k) {
         constexpr int kJobs = D / 32;  // of each tensor
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
@@ -721,17 +718,19 @@ __device__ void bwd_elem(const CrossBwdArgs &a, BBars &b, BXch &xch, uint8_t *ti
         tmem_wait_st();
         tc_fence_before();
         arrive(b.q_full);
-        row_nl2 = neg_lse2(row_nl2);
-        row_nd *= -ds_scale;
+        row_nl2 = neg_lse2(next_lse);
+        row_nd = -next_d * ds_scale;
     };
     for (uint32_t k = 0; receive(b, k, ok); ++k) {
         const Piece &p = b.pieces[k % kPieces];
         const int t0 = p.t0, t1 = p.t1;
         if (k == 0) {
-            if (kDkDv)
+            if (kDkDv) {
                 fetch(p, t0);
-            else
-                make_resident(k, p);
+            } else {
+                fetch_row(p);
+                make_resident(k);
+            }
         }
         for (int t = t0; ok && t < t1; ++t, ++pos) {
             if constexpr (kDkDv) {
@@ -776,7 +775,7 @@ __device__ void bwd_elem(const CrossBwdArgs &a, BBars &b, BXch &xch, uint8_t *ti
                 }
                 tmem_wait_st();
                 tc_fence_before();
-                arrive(b.p1_full);
+                arrive(b.p1_full[pos & 1]);
                 // dS^T = P^T (dP^T - D) over the first 16 columns of the chunk.
                 ok = wait(b.dp_full[pos & 1], pos >> 1);
                 if (!ok)
@@ -805,13 +804,15 @@ __device__ void bwd_elem(const CrossBwdArgs &a, BBars &b, BXch &xch, uint8_t *ti
                 }
                 tmem_wait_st();
                 tc_fence_before();
-                arrive(b.p_full);
+                arrive(b.p_full[pos & 1]);
             } else {
                 ok = wait(b.s_full[pos & 1], pos >> 1);
                 if (!ok)
                     break;
                 tc_fence_after();
                 const int valid = p.L - t * kTile;  // keys of this tile
+                if (t + 1 == t1 && receive(b, k + 1, ok))
+                    fetch_row(b.pieces[(k + 1) % kPieces]);
                 // P in registers, so that the next S is computed meanwhile.
                 float pr[32];
                 {
@@ -820,7 +821,7 @@ __device__ void bwd_elem(const CrossBwdArgs &a, BBars &b, BXch &xch, uint8_t *ti
                     tmem_ld32(tmem + kColS + col, sr);
                     tmem_wait_ld();
                     tc_fence_before();
-                    arrive(b.p1_full);
+                    arrive(b.p1_full[pos & 1]);
                     const uint64_t nl2 = f2_pack(row_nl2, row_nl2);
 #pragma unroll
                     for (int i = 0; i < 32; i += 2) {
@@ -868,10 +869,10 @@ __device__ void bwd_elem(const CrossBwdArgs &a, BBars &b, BXch &xch, uint8_t *ti
                 }
                 tmem_wait_st();
                 tc_fence_before();
-                arrive(b.p_full);
+                arrive(b.p_full[pos & 1]);
                 // S and dP of this piece are done: the next one's rows.
                 if (t + 1 == t1 && receive(b, k + 1, ok))
-                    make_resident(k + 1, b.pieces[(k + 1) % kPieces]);
+                    make_resident(k + 1);
             }
         }
         if (!ok)
@@ -993,6 +994,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i = 0; i < 2; ++i) {
             mbar_init(smem_addr(&b.s_full[i]), 1);
             mbar_init(smem_addr(&b.dp_full[i]), 1);
+            mbar_init(smem_addr(&b.p1_full[i]), kElemWarps);
+            mbar_init(smem_addr(&b.p_full[i]), kElemWarps);
         }
         mbar_init(smem_addr(&b.o_full), 1);
         mbar_init(smem_addr(&b.o_empty), kElemWarps);
@@ -1001,8 +1004,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(smem_addr(&b.piece_full[i]), 1);
             mbar_init(smem_addr(&b.piece_empty[i]), kElemWarps + 1);
         }
-        mbar_init(smem_addr(&b.p_full), kElemWarps);
-        mbar_init(smem_addr(&b.p1_full), kElemWarps);
         mbar_init(smem_addr(&b.drain), 1);
         b.abort = 0;
         fence_barrier_init();
@@ -1103,7 +1104,7 @@ template <int D, bool kF16> __global__ void __launch_bounds__(kPrepThreads) cros
             to[i] = -1;
             if (row < rows) {
                 const int inner = heads_inside ? Hq : a.Nq, outer = heads_inside ? a.Nq : Hq;
-                const long long q1 = row / inner, q2 = q1 / outer;
+                const long long q1 = quotient(row, inner), q2 = quotient(q1, outer);
                 const int i0 = static_cast<int>(row - q1 * inner), i1 = static_cast<int>(q1 - q2 * outer);
                 const int h = heads_inside ? i0 : i1, n = heads_inside ? i1 : i0;
                 to[i] = (q2 * Hq + h) * a.Nq + n;
