@@ -1055,8 +1055,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // ------------------------------------------------------------------ prep
 constexpr int kPrepThreads = 256;
-constexpr int kPrepBlocks = 1216;  // at most: 8 a SM
-constexpr int kPrepRows = 4;       // of a group of lanes in flight
+constexpr int kPrepBlocks = 760;  // at most: 5 a SM
+constexpr int kPrepRows = 2;       // of a group of lanes in flight
 
 template <bool kF16> __device__ __forceinline__ float2 unpack2(uint32_t w)
 {
@@ -1081,7 +1081,7 @@ __device__ __forceinline__ void zero_tile(void *t, const long long *st, int b, i
 // they lie in memory, and the block's largest |dO|.  Then zeros for what no unit
 // covers: key tiles behind a sequence's last key (all, without queries) and the
 // queries of a sequence without keys.
-template <int D, bool kF16> __global__ void __launch_bounds__(kPrepThreads) cross_prep_kernel(const CrossBwdArgs a)
+template <int D, bool kF16> __global__ void __launch_bounds__(kPrepThreads, 5) cross_prep_kernel(const CrossBwdArgs a)
 {
     constexpr int kLanes = D / 8, kGroup = D == 64 ? 8 : 16;
     grid_dependency_wait();
