@@ -1,6 +1,6 @@
-// binding.cpp -- torch tensors for the calls of a decoding step and of cross
-// attention: attn_fwd_tree, fattn_tree_mask, fattn_kv_keep, fattn_kv_fork,
-// attn_fwd_cross, attn_bwd_cross.
+// binding.cpp -- torch tensors for the calls of a drafting or searching step and
+// of cross attention: attn_fwd_tree, fattn_tree_mask, fattn_kv_append,
+// fattn_kv_keep, fattn_kv_fork, attn_fwd_cross, attn_bwd_cross.
 //
 // Such a call is a few microseconds of GPU work, made once a layer or a step.
 // Checking its tensors, making its outputs and passing some thirty arguments took
@@ -227,6 +227,11 @@ Cache cache_of(PyObject *ko, PyObject *vo, std::optional<Kind> &kind)
 {
     const Tensor &k = half("k_cache", ko, 4, kind), &v = half("v_cache", vo, 4, kind);
     expect("v_cache", v, k.sizes());
+    const int64_t page = k.size(2), d = k.size(3);
+    if (page < 16 || (page & (page - 1)) != 0)
+        bad_value("page size must be a power of two, 16 or more, got " + std::to_string(page));
+    if (d != 64 && d != 96 && d != 128 && d != 256)
+        bad_value("head dimension must be 64, 96, 128 or 256, got " + std::to_string(d));
     return Cache{k, v, small("the pool", k.size(0)), small("Hk", k.size(1)), small("the page size", k.size(2)),
                  small("d", k.size(3))};
 }
@@ -287,6 +292,49 @@ PyObject *tree_mask(PyObject *const *a)
                                words, place.stream);
     });
     return Py_BuildValue("NN", THPVariable_Wrap(mask), THPVariable_Wrap(pos));
+}
+
+// k, v, k_cache, v_cache, page_table, cu_q, kv_len, rope, interleaved, stream
+PyObject *kv_append(PyObject *const *a)
+{
+    std::optional<Kind> kind;
+    const Tensor &k = half("k", a[0], 3, kind), &v = half("v", a[1], 3, kind);
+    expect("v", v, k.sizes());
+    const Cache c = cache_of(a[2], a[3], kind);
+    int dev = kind->dev;
+    const Tensor &table = list("page_table", a[4], 2, dev), &cu = list("cu_q", a[5], 1, dev),
+                 &kv_len = list("kv_len", a[6], 1, dev);
+    const int T = small("T", k.size(0)), B = small("B", table.size(0));
+    expect("k", k, {T, c.heads, c.d});
+    expect("cu_q", cu, {B + 1});
+    expect("kv_len", kv_len, {B});
+    const float *rope = nullptr;
+    int rot = 0, max_pos = 0;
+    if (a[7] != Py_None) {
+        const Tensor &t = tensor("rope", a[7]);
+        if (t.scalar_type() != at::kFloat || t.dim() != 2 || !t.is_contiguous() || !t.is_cuda() ||
+            t.get_device() != dev)
+            bad_value("rope must be a contiguous fp32 [positions, rot_dim] tensor on CUDA device " +
+                      std::to_string(dev));
+        if (t.size(1) % 16 != 0 || t.size(1) < 1 || t.size(1) > c.d)
+            bad_value("rope must have 16, 32, ... up to " + std::to_string(c.d) + " columns, got " +
+                      std::to_string(t.size(1)));
+        rope = ptr<const float>(t);
+        rot = small("rope", t.size(1));
+        max_pos = small("rope", t.size(0));
+    }
+    const int interleaved = PyObject_IsTrue(a[8]);
+    if (interleaved < 0)
+        throw Raised{};
+    Place place(a[9], dev);
+    const Strides ks(k), vs(v), kcs(c.k), vcs(c.v);
+    call("fattn_kv_append", [&] {
+        return fattn_kv_append(k.data_ptr(), v.data_ptr(), c.k.data_ptr(), c.v.data_ptr(), ints(table), ints(cu),
+                               ints(kv_len), rope, T, B, c.heads, c.d, c.pages, c.page,
+                               static_cast<int>(table.size(1)), row_stride(table), rot, max_pos, ks.at, vs.at,
+                               kcs.at, vcs.at, interleaved, kind->f16(), place.stream);
+    });
+    return Py_BuildValue("OO", a[2], a[3]);
 }
 
 // k_cache, v_cache, page_table, cu_q, kv_len, kept, kept_len, kv_len_out, stream
@@ -464,6 +512,7 @@ PyObject *init(PyObject *, PyObject *check)
     }
 PyMethodDef methods[] = {ENTRY(attn_fwd_tree, 13),
                          ENTRY(tree_mask, 7),
+                         ENTRY(kv_append, 10),
                          ENTRY(kv_keep, 9),
                          ENTRY(kv_fork, 12),
                          ENTRY(attn_fwd_cross, 9),

@@ -115,7 +115,7 @@ constexpr int kForkThreads = 1024;
 constexpr int kForkWarps = kForkThreads / 32;
 constexpr int kForkSmall = 4096;
 constexpr int kForkRecount = 32 * kForkThreads;
-constexpr int kForkBatch = 8;  // 32-column runs of rows that a warp has in flight
+constexpr int kForkBatch = 2;  // 32-column runs of rows that a warp has in flight
 
 // The sequences' lists, in range, and what follows from them.  Every block has
 // all of them, in shared memory where they fit, else in its own part of the
@@ -129,7 +129,7 @@ struct Seqs {
 };
 
 // Exclusive prefix over the block's threads, and the total.
-__device__ __forceinline__ int block_prefix(int x, int *scratch, int &total)
+__device__ __noinline__ int block_prefix(int x, int *scratch, int &total)
 {
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
     int incl = x;

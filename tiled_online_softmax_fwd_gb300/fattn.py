@@ -1,11 +1,12 @@
 """ctypes binding of libfattn's C ABI (include/fattn.h).
 
 Argument marshalling only: every step of the computation runs in the CUDA
-library.  The calls of a drafting or searching step and of cross attention go
-through a compiled module in the same manner (csrc/binding.cpp).  PyTorch supplies device memory and streams.  The checks mirror the
+library.  PyTorch supplies device memory and streams.  The checks mirror the
 wrapper of "Triton programming template" (device, shape, dtype, contiguity)
 so that misuse raises in Python before the C layer sees it; the C layer
-checks again and is the authority.
+checks again and is the authority.  The calls of a drafting or searching step
+and of cross attention go through a compiled module in the same manner
+(csrc/binding.cpp).
 """
 from __future__ import annotations
 
@@ -804,24 +805,6 @@ def _paged_checks(page_table, cu_q, kv_len, k_cache, v_cache, dtype, dev, d):
     return B, max_pages, page_table.stride(0) if B > 1 else max_pages, pages, Hk, page
 
 
-def _append_plan(key, k, v, k_cache, v_cache, page_table, cu_q, kv_len, rope, interleaved):
-    dtype, dev = _first_half("k", k, 3)
-    _check_half("v", v, 3, dtype, dev)
-    T, Hk, d = k.shape
-    if v.shape != k.shape:
-        raise ValueError("k and v must have one shape, got %s %s" % (tuple(k.shape), tuple(v.shape)))
-    if d not in (64, 96, 128, 256):
-        raise ValueError("head dimension must be 64, 96, 128 or 256, got %d" % d)
-    B, max_pages, row, pages, heads, page = _paged_checks(page_table, cu_q, kv_len, k_cache, v_cache,
-                                                          dtype, dev, d)
-    if heads != Hk:
-        raise ValueError("the caches have %d heads, k and v %d" % (heads, Hk))
-    rot, max_pos = _check_rope(rope, d, dev)
-    return _keep(key, (dev, (T, B, Hk, d, pages, page, max_pages, row, rot, max_pos, _outer(k),
-                             _outer(v), _outer(k_cache), _outer(v_cache), 1 if interleaved else 0,
-                             _HALF[dtype])))
-
-
 def kv_append(k, v, k_cache, v_cache, page_table, cu_q, kv_len, rope=None,
               interleaved: bool = False, stream=None):
     """Append the new tokens' keys and values k, v [T, Hk, d] to the paged
@@ -832,17 +815,8 @@ def kv_append(k, v, k_cache, v_cache, page_table, cu_q, kv_len, rope=None,
     strides; ``page_table`` int32 [B, pages], ``cu_q`` int32 [B + 1],
     ``kv_len`` int32 [B] (keys of each sequence, the new ones included).
     Returns (k_cache, v_cache)."""
-    try:
-        key = ("append", _of(k), _of(v), _of(k_cache), _of(v_cache), _of(page_table), _of(cu_q),
-               _of(kv_len), _of(rope), bool(interleaved))
-    except AttributeError:  # not tensors: the checks say which
-        key = None
-    dev, args = _plans.get(key) or _append_plan(key, k, v, k_cache, v_cache, page_table, cu_q, kv_len,
-                                                rope, interleaved)
-    _call("fattn_kv_append", dev, stream, k.data_ptr(), v.data_ptr(), k_cache.data_ptr(),
-          v_cache.data_ptr(), page_table.data_ptr(), cu_q.data_ptr(), kv_len.data_ptr(), _ptr(rope),
-          *args)
-    return k_cache, v_cache
+    return (_binding or _native(k)).kv_append(k, v, k_cache, v_cache, page_table, cu_q, kv_len, rope,
+                                              interleaved, stream)
 
 
 def _paged_plan(key, q, k_cache, v_cache, page_table, cu_q, kv_len, max_q, causal, scale):
@@ -909,12 +883,17 @@ def attn_fwd_paged(q, k_cache, v_cache, page_table, cu_q, kv_len, max_q: int,
 _binding = None
 
 
-def _native():
-    """The compiled binding of the calls below (csrc/binding.cpp): they check
-    their tensors, make their outputs and call the library without Python in
-    between.  Raises if it has not been built: there is no fallback."""
+def _native(first=None):
+    """The compiled binding (csrc/binding.cpp) of the calls that check their
+    tensors, make their outputs and call the library without Python in between.
+    Raises if it has not been built: there is no fallback (with a torch without
+    CUDA there is none to build, and no tensor, `first` of a call, to take)."""
     global _binding
     if _binding is None:
+        if isinstance(first, _Tensor) and not first.is_cuda:
+            raise ValueError("a CUDA tensor is needed, got one on %s" % first.device)
+        if first is not None and not isinstance(first, _Tensor):
+            raise TypeError("a torch.Tensor is needed, got %s" % type(first).__name__)
         load()
         with _lock:
             if _binding is None:
@@ -938,7 +917,7 @@ def tree_mask(parents, cu_q, kv_len, max_q: int, mask=None, positions=None, stre
     kv_append.  Returns (mask int32 [T, ceil(max_q / 32)], positions int32
     [1, T]): attn_fwd_tree's mask, in which a token sees itself and those it
     continues, and each token's position for qk_norm_rope, by its depth."""
-    return (_binding or _native()).tree_mask(parents, cu_q, kv_len, max_q, mask, positions, stream)
+    return (_binding or _native(parents)).tree_mask(parents, cu_q, kv_len, max_q, mask, positions, stream)
 
 
 def attn_fwd_tree(q, k_cache, v_cache, page_table, cu_q, kv_len, mask, max_q: int,
@@ -951,7 +930,7 @@ def attn_fwd_tree(q, k_cache, v_cache, page_table, cu_q, kv_len, mask, max_q: in
     sequence's token j), itself only if its own bit is set.  The workspace is
     attn_fwd_paged's.  Returns (out [T, Hq, d], lse fp32 [T, Hq]); rows from
     cu_q[B] on are not written."""
-    return (_binding or _native()).attn_fwd_tree(q, k_cache, v_cache, page_table, cu_q, kv_len, mask,
+    return (_binding or _native(q)).attn_fwd_tree(q, k_cache, v_cache, page_table, cu_q, kv_len, mask,
                                                  max_q, scale, workspace, out, lse, stream)
 
 
@@ -963,7 +942,7 @@ def kv_keep(k_cache, v_cache, page_table, cu_q, kv_len, kept, kept_len, kv_len_o
     ``kept_len[b]`` (int32 [B]) of row b; the lists and caches are as in
     kv_append.  Returns kv_len_out int32 [B] (kv_len itself for in place): the
     sequences' keys afterwards."""
-    return (_binding or _native()).kv_keep(k_cache, v_cache, page_table, cu_q, kv_len, kept, kept_len,
+    return (_binding or _native(k_cache)).kv_keep(k_cache, v_cache, page_table, cu_q, kv_len, kept, kept_len,
                                            kv_len_out, stream)
 
 
@@ -1007,7 +986,7 @@ def attn_fwd_cross(q, k, v, kv_len=None, scale: float | None = None, workspace=N
     each sequence, what is behind them may hold anything (None: Nk).  A sequence
     without keys gives o = 0 and lse = -inf.  Returns (out [B, Hq, Nq, d], lse
     fp32 [B, Hq, Nq])."""
-    return (_binding or _native()).attn_fwd_cross(q, k, v, kv_len, scale, workspace, out, lse, stream)
+    return (_binding or _native(q)).attn_fwd_cross(q, k, v, kv_len, scale, workspace, out, lse, stream)
 
 
 def cross_bwd_workspace_size(B: int, Hq: int, Hk: int, Nq: int, Nk: int, d: int, device=None) -> int:
@@ -1023,7 +1002,7 @@ def attn_bwd_cross(q, k, v, o, lse, do, kv_len=None, scale: float | None = None,
     q's and k's shapes, any strides with a contiguous last dimension (lse
     contiguous).  Rows of dk and dv behind a sequence's last key are zeros.
     Returns (dq, dk, dv) in the inputs' type, each of which may be given."""
-    return (_binding or _native()).attn_bwd_cross(q, k, v, o, lse, do, kv_len, scale, dq, dk, dv, workspace,
+    return (_binding or _native(q)).attn_bwd_cross(q, k, v, o, lse, do, kv_len, scale, dq, dk, dv, workspace,
                                                   stream)
 
 
