@@ -176,6 +176,21 @@ def test_tree_mask_is_the_paths(q_lens, extra):
     assert pos.shape == (1, p.T) and pos[0].tolist() == want
 
 
+def test_a_tree_beyond_the_shared_memory():
+    """5000 tokens: a chain of 130 to every 40th, the others leaves of those."""
+    n, g = 5000, torch.Generator().manual_seed(3)
+    parents = [i - 40 if i % 40 == 0 else i // 40 * 40 for i in range(n)]
+    parents[0] = -1
+    mask, pos = fattn.tree_mask(torch.tensor(parents, dtype=torch.int32).cuda(),
+                                torch.tensor([0, n], dtype=torch.int32).cuda(),
+                                torch.tensor([n + 9], dtype=torch.int32).cuda(), n)
+    assert fattn.device_status() == 0
+    rows = ref.paths(parents)
+    some = torch.randperm(n, generator=g)[:300].tolist() + [0, 1, n - 1]
+    assert torch.equal(mask[some].cpu(), ref.pack([rows[i] for i in some], 157))
+    assert pos[0].tolist() == [9 + len(r) - 1 for r in rows]
+
+
 def test_tree_mask_of_a_chain_is_causal():
     n = 150
     parents = torch.arange(-1, n - 1, dtype=torch.int32)
