@@ -33,7 +33,7 @@ using namespace ptx;
 
 // ------------------------------------------------------------------ keep
 constexpr int kKeepThreads = 256;
-constexpr int kKeepBatch = 8;  // 16-byte pieces of a thread in flight
+constexpr int kKeepBatch = 4;  // 16-byte pieces of a thread in flight
 
 // A block: one sequence, some heads, one of the two caches; a cluster: a
 // sequence, so that its length is written (in place, too) behind every reading.
@@ -88,25 +88,29 @@ __global__ void __launch_bounds__(kKeepThreads) kv_keep_kernel(const KvKeepArgs 
         return reinterpret_cast<uint4 *>(cache + table[pos >> a.page_shift] * st[0] + (h0 + h) * st[1] +
                                          (pos & slots) * st[2] + c * 8);
     };
-    const long long total = static_cast<long long>(m - first) * each;
-    for (long long base = 0; base < total; base += kKeepThreads * kKeepBatch) {
-        uint4 x[kKeepBatch], *to[kKeepBatch];
+    // Some tokens at a time, as many as the threads' pieces hold, or parts of one.
+    constexpr int kWave = kKeepThreads * kKeepBatch;
+    const int group = max(kWave / max(each, 1), 1);
+    for (int j0 = first; each > 0 && j0 < m; j0 += min(group, m - j0)) {
+        const int pieces = min(group, m - j0) * each;
+        for (int base = 0; base < pieces; base += kWave) {
+            uint4 x[kKeepBatch], *to[kKeepBatch];
 #pragma unroll
-        for (int i = 0; i < kKeepBatch; ++i) {
-            const long long item = base + i * kKeepThreads + tid;
-            to[i] = nullptr;
-            if (item < total) {
-                const int t = static_cast<int>(item / each), rest = static_cast<int>(item - static_cast<long long>(t) * each);
-                const int h = rest / vecs, c = rest - h * vecs, j = first + t;
-                x[i] = *at(prefix + kept[j], h, c);
-                to[i] = at(prefix + j, h, c);
+            for (int i = 0; i < kKeepBatch; ++i) {
+                const int item = base + i * kKeepThreads + tid;
+                to[i] = nullptr;
+                if (item < pieces) {
+                    const int t = item / each, rest = item - t * each, h = rest / vecs, c = rest - h * vecs;
+                    x[i] = *at(prefix + kept[j0 + t], h, c);
+                    to[i] = at(prefix + j0 + t, h, c);
+                }
             }
-        }
-        __syncthreads();
+            __syncthreads();
 #pragma unroll
-        for (int i = 0; i < kKeepBatch; ++i)
-            if (to[i] != nullptr)
-                *to[i] = x[i];
+            for (int i = 0; i < kKeepBatch; ++i)
+                if (to[i] != nullptr)
+                    *to[i] = x[i];
+        }
     }
 }
 
