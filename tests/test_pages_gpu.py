@@ -324,3 +324,23 @@ def test_a_drafting_loop_gives_the_plain_loops_outputs():
                       kv_len_out=lens)
         assert lens.tolist() == lens_now
     assert fattn.device_status() == 0
+
+
+@pytest.mark.parametrize("B,spare", [(2049, 100), (2500, 36000), (70, 40000)])
+def test_fork_of_many_sequences_and_pages(B, spare):
+    """More sequences than the lists in shared memory hold, more pages than each
+    block counts for itself; free pages before, between and behind those in use."""
+    g = torch.Generator().manual_seed(B)
+    lens = torch.randint(0, 70, (B,), generator=g).tolist()
+    parents = torch.randint(-1, B, (B,), generator=g).tolist()
+    new = torch.randint(0, 40, (B,), generator=g).tolist()
+    p, table, refs = state(lens, 1, 64, 16, seed=9, spare=spare + 3 * B, cols=8)
+    check_fork(p, table, lens, refs, parents, new)
+
+
+def test_growth_of_a_long_cache():
+    """One sequence of 40000 pages, room for 30000 more: one table row, most of
+    the pool."""
+    cols = 70001
+    p, table, refs = state([40000 * 16 - 5], 1, 64, 16, seed=10, spare=30100, cols=cols)
+    check_fork(p, table, [40000 * 16 - 5], refs, None, [30000 * 16])

@@ -266,3 +266,28 @@ def test_masks_made_in_a_captured_graph_follow_the_parents():
         torch.cuda.synchronize()
         assert fattn.device_status() == 0
         check(out, lse, reference(p, q, rows), torch.bfloat16, 200)
+
+
+def test_two_trees_at_once_on_two_streams():
+    """Workspaces of their own: calls that overlap do not meet."""
+    sets, streams = [], [torch.cuda.Stream(), torch.cuda.Stream()]
+    for seed, shape in ((20, ([26] * 6, [700 + 90 * i for i in range(6)], 2, 128, 16)),
+                        (21, ([60, 200], [3000, 900], 4, 64, 32))):
+        p, trees, rows = make(*shape, torch.bfloat16, seed=seed)
+        q = queries(p.T, 8, shape[3], torch.bfloat16, seed)
+        args = [t.cuda() for t in (q, p.k_cache, p.v_cache)]
+        parents = torch.tensor([x for t in trees for x in t], dtype=torch.int32).cuda()
+        sets.append((p, q, rows, args, p.lists(), parents))
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(10):
+        for (p, q, rows, args, lists, parents), s in zip(sets, streams):
+            mask, _ = fattn.tree_mask(parents, lists[1], lists[2], p.max_q, stream=s)
+            got.append(fattn.attn_fwd_tree(*args, *lists, mask, p.max_q, stream=s))
+    torch.cuda.synchronize()
+    assert fattn.device_status() == 0
+    for i, (o, lse) in enumerate(got):
+        p, q, rows = sets[i % 2][:3]
+        if i < 2:
+            check(o, lse, reference(p, q, rows), torch.bfloat16, 3000)
+        assert torch.equal(o, got[i % 2][0]) and torch.equal(lse, got[i % 2][1])
