@@ -61,8 +61,14 @@ constexpr uint32_t kChunkBytes = kTile * 64 * 2;
 constexpr uint32_t kColS = 0, kColDP = 128;
 
 // A unit's start and end, in steps (see Schedule); a split leaves at least kSnap
-// steps on each side, and a share is at least kLeast.
-constexpr int kUnitCost = 3, kSnap = 2, kLeast = 8;
+// steps on each side, and a share is at least kLeast.  At d = 128 a unit's end and
+// the next one's start take some 2.5 steps, at d = 64 3 to 4, of which the first
+// pieces' copies hide part: 2 there is up to 10 % better on small calls (3 and 12
+// heads, 333 queries, 501 keys: 24.9 us, with 3 27.8) and 3 at d = 128 1.5 % on
+// large ones; kLeast 8 takes 20.6 us for 8 x 4 heads, 100 queries and keys, 6 15.7,
+// 5 18.6.
+template <int D> __device__ __forceinline__ constexpr int unit_cost() { return D == 64 ? 2 : 3; }
+constexpr int kSnap = 2, kLeast = 6;
 
 template <int D, bool kDkDv> struct BCfg {
     static constexpr int kChunks = (D + 63) / 64;
@@ -149,7 +155,7 @@ __device__ __forceinline__ void units_of(const CrossBwdArgs &a, int L, int &unit
     units = steps == 0 ? 0 : kDkDv ? a.Hk * F : a.Hk * a.G * a.Tq;
 }
 // Step that a cost of y inside a unit falls on.
-__device__ __forceinline__ int step_at(long long y, int steps)
+template <int kUnitCost> __device__ __forceinline__ int step_at(long long y, int steps)
 {
     if (y >= steps + kUnitCost)
         return steps;
@@ -173,7 +179,7 @@ template <bool kDkDv> __device__ __forceinline__ void enter(const CrossBwdArgs &
     w.L = clamp_len(a, w.at.b);
     units_of<kDkDv>(a, w.L, w.units, w.steps);
 }
-template <bool kDkDv> __device__ __forceinline__ Walk first_walk(const CrossBwdArgs &a, const BBars &b)
+template <bool kDkDv, int kUnitCost> __device__ __forceinline__ Walk first_walk(const CrossBwdArgs &a, const BBars &b)
 {
     Walk w;
     w.at = b.start;
@@ -186,7 +192,7 @@ template <bool kDkDv> __device__ __forceinline__ Walk first_walk(const CrossBwdA
     }
     return w;
 }
-template <bool kDkDv> __device__ __forceinline__ bool next_piece(const CrossBwdArgs &a, Walk &w, Piece &p)
+template <bool kDkDv, int kUnitCost> __device__ __forceinline__ bool next_piece(const CrossBwdArgs &a, Walk &w, Piece &p)
 {
     while (w.at.left > 0) {
         if (w.u >= w.units) {
@@ -201,8 +207,8 @@ template <bool kDkDv> __device__ __forceinline__ bool next_piece(const CrossBwdA
         const int u = w.u++;
         w.at.left -= y1 - y0;
         w.at.y = 0;
-        p.t0 = step_at(y0, w.steps);
-        p.t1 = step_at(y1, w.steps);
+        p.t0 = step_at<kUnitCost>(y0, w.steps);
+        p.t1 = step_at<kUnitCost>(y1, w.steps);
         if (p.t0 == p.t1)  // nothing of it falls to this CTA
             continue;
         const int per = kDkDv ? w.units / a.Hk : a.Tq;
@@ -218,7 +224,7 @@ template <bool kDkDv> __device__ __forceinline__ bool next_piece(const CrossBwdA
 }
 
 // Finds this CTA's start: warp 0 alone, 32 sequences at a time.
-template <bool kDkDv> __device__ void find_start(const CrossBwdArgs &a, BBars &b)
+template <bool kDkDv, int kUnitCost> __device__ void find_start(const CrossBwdArgs &a, BBars &b)
 {
     if (threadIdx.x >= 32)
         return;
@@ -264,7 +270,7 @@ template <bool kDkDv> __device__ void find_start(const CrossBwdArgs &a, BBars &b
         if (first <= lo && lo < first + mine) {
             b.start = Start{b0 + lane, lo - first, hi - lo};
             const int cost = steps + kUnitCost, u = static_cast<int>(quotient(lo - first, cost));
-            const int t = step_at(lo - first - static_cast<long long>(u) * cost, steps);
+            const int t = step_at<kUnitCost>(lo - first - static_cast<long long>(u) * cost, steps);
             const int per = kDkDv ? units / a.Hk : a.Tq, h = u / per;
             starts[c] = make_int4(b0 + lane, h, u - h * per, t < steps ? t : 0);
         }
@@ -392,11 +398,11 @@ __device__ void bwd_load(const CrossBwdArgs &a, BBars &b, uint32_t smem, const C
     };
     bool ok = true;
     uint32_t k = 0;
-    Walk w = first_walk<kDkDv>(a, b);
+    Walk w = first_walk<kDkDv, unit_cost<D>()>(a, b);
     Piece p;
     bool more = true;
     while (ok && more) {
-        more = next_piece<kDkDv>(a, w, p);
+        more = next_piece<kDkDv, unit_cost<D>()>(a, w, p);
         ok = warp_wait(b.piece_empty[k % kPieces], ((k / kPieces) & 1) ^ 1, abort);
         if (!ok)
             break;
@@ -1020,7 +1026,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     // The kernel ahead has begun, so what it waited for is there: the lengths, and
     // for dq, behind dkdv, all that it reads; dq only ends behind dkdv.
-    find_start<kDkDv>(a, b);
+    find_start<kDkDv, unit_cost<D>()>(a, b);
     if (kDkDv) {
         grid_dependency_wait();
         grid_launch_dependents();
