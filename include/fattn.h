@@ -660,8 +660,10 @@ fattn_status_t fattn_kv_fork(void *k_cache, void *v_cache, const int *page_table
  *   workspace : as in attn_fwd_paged, attn_fwd_cross_workspace_size(...) bytes
  *
  * Rows of k and v behind a sequence's last key may hold anything, NaN included.
- * A sequence without keys gives o = 0 and lse = -inf.  Two kernels are enqueued;
- * equal calls give equal bits.  Range reports and errors as for attn_fwd_paged.
+ * A sequence without keys gives o = 0 and lse = -inf.  Two kernels are enqueued, or
+ * one where a key head has at most four rows (Nq Hq / Hk) and few enough units: it
+ * works on the CUDA cores, with P and V as they are, not rounded to fp16.  Equal
+ * calls give equal bits.  Range reports and errors as for attn_fwd_paged.
  */
 size_t attn_fwd_cross_workspace_size(int Hq, int Hk, int Nq, int d);
 fattn_status_t attn_fwd_cross(const void *q, const void *k, const void *v, const int *kv_len, void *o,

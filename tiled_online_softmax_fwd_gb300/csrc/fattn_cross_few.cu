@@ -5,7 +5,7 @@
 // many for its value, against 4 d bytes: at R <= 4 the memory is the bound.  The
 // tensor-core kernel spends its time on copies, hand-overs and 128-row tiles
 // that are mostly empty (37.5 us for 32 sequences of 500 to 1500 keys, 16 heads,
-// d = 64, 128 MB, where this one takes 27.6: 4.6 TB/s).
+// d = 64, 128 MB, where this one takes 28: 4.6 TB/s).
 //
 // Copies (cp.async) run two batches of 16 or 8 keys ahead of a warp, some 64 KB
 // a SM on their way: with plain loads, a batch of each warp at a time, it took

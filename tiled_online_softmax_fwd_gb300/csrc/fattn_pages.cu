@@ -7,7 +7,9 @@
 // with kept ascending, so kept[j] >= j and a block that goes through j in order
 // never reads a slot it has written: it loads a batch of rows, meets, and
 // stores them.  Bound by latency at a step's few tokens (a chain of four loads:
-// lengths, kept, pages, rows), by bytes at many.
+// lengths, kept, pages, rows): 6 us with the append before it for 4 sequences of 26
+// tokens; 8.7 us for 192 of up to 129, up to 24 of them kept (8 key heads, d = 128;
+// the rows were written just before and come from L2).
 //
 // Fork.  Sequence b goes on as its parent's copy with room for new tokens:
 //   table'[b] = the parent's entries, L'[b] = L[parent] + n_b.
@@ -18,7 +20,10 @@
 // are given out in the order of sequences and columns, so equal calls give equal
 // tables whatever the order of the atomic counts.  One cluster of blocks does
 // the lists in steps between cluster barriers (a block alone where they are
-// short), a second kernel copies the pages' rows.
+// short), a second kernel copies the pages' rows.  Bound by latency: the lists are
+// a few KB, read in four dependent steps (entries, their counts, the counts' sums,
+// the free pages) with a meeting of the blocks between two: 9.3 us for 8 sequences
+// of up to 900 keys, 16.7 for 256 of up to 4000 and 700 new ones; pages of 16 and 32.
 #include <cooperative_groups.h>
 #include <stdint.h>
 
