@@ -195,6 +195,34 @@ def test_a_captured_call_follows_its_lengths():
     assert fattn.device_status() == 0
 
 
+@pytest.mark.parametrize("d,dtype", [(64, torch.float16), (128, torch.bfloat16)])
+def test_inputs_changed_in_place(d, dtype):
+    """Calls one behind the other on the same buffers, whose contents and lengths
+    change before each: none reads what the one before has left in a cache."""
+    g = torch.Generator().manual_seed(17)
+    B, H, Hk, Nq, Nk = 3, 4, 2, 300, 400
+    sets = []
+    for i in range(2):
+        q, do = ((torch.randn(B, H, Nq, d, generator=g) * (1 + 7 * i)).to(dtype).cuda() for _ in range(2))
+        k, v = (torch.randn(B, Hk, Nk, d, generator=g).to(dtype).cuda() for _ in range(2))
+        kv_len = torch.tensor([[400, 1, 129], [7, 400, 256]][i], dtype=torch.int32, device="cuda")
+        o, lse = fattn.attn_fwd_cross(q, k, v, kv_len)
+        ins = (q, k, v, o, lse, do, kv_len)
+        sets.append((ins, fattn.attn_bwd_cross(*ins)))
+    bufs = [torch.empty_like(t) for t in sets[0][0]]
+    outs = [torch.empty_like(t) for t in sets[0][1]]
+    ws = torch.empty(fattn.cross_bwd_workspace_size(B, H, Hk, Nq, Nk, d), dtype=torch.uint8, device="cuda")
+    wrong = torch.zeros((), dtype=torch.int64, device="cuda")
+    for n in range(200):
+        ins, want = sets[n % 2]
+        for to, t in zip(bufs, ins):
+            to.copy_(t)
+        fattn.attn_bwd_cross(*bufs, dq=outs[0], dk=outs[1], dv=outs[2], workspace=ws)
+        for x, y in zip(outs, want):
+            wrong += (x != y).sum()
+    assert int(wrong) == 0 and fattn.device_status() == 0
+
+
 @pytest.mark.parametrize("d,Nq,Nk", [(64, 2048, 2048), (64, 2048, 200), (96, 900, 900), (128, 1024, 1024)])
 def test_many_calls_in_a_row(d, Nq, Nk):
     """No wait of the pipelines ever runs out, whatever the warps' order: some

@@ -145,7 +145,7 @@ struct BXch {
 
 __device__ __forceinline__ int clamp_len(const CrossBwdArgs &a, int b)
 {
-    const int L = a.kv_len != nullptr ? a.kv_len[b] : a.Nk;
+    const int L = a.kv_len != nullptr ? __ldcg(a.kv_len + b) : a.Nk;
     return min(max(L, 0), a.Nk);
 }
 
@@ -686,8 +686,8 @@ __device__ void bwd_elem(const CrossBwdArgs &a, BBars &b, BXch &xch, uint8_t *ti
     auto fetch = [&](const Piece &p, int t) {
         const int g = t / a.Tq, q = (t - g * a.Tq) * kTile + col + lane;
         const long long at = ((static_cast<long long>(p.b) * a.Hk + p.h) * a.G + g) * a.Nq + q;
-        next_lse = q < a.Nq ? a.lse[at] : 0.f;
-        next_d = q < a.Nq ? a.dvec[at] : 0.f;
+        next_lse = q < a.Nq ? __ldcg(a.lse + at) : 0.f;
+        next_d = q < a.Nq ? __ldcg(a.dvec + at) : 0.f;
     };
     // dq: the k-th piece's Q and dO into TMEM, 32 elements of a row a job, a lane a
     // row; and the row's lse and D, fetched before.
@@ -695,8 +695,8 @@ __device__ void bwd_elem(const CrossBwdArgs &a, BBars &b, BXch &xch, uint8_t *ti
     auto fetch_row = [&](const Piece &p) {
         const int row = p.tile * kTile + r;
         const long long at = (static_cast<long long>(p.b) * a.Hk * a.G + p.h) * a.Nq + row;
-        next_lse = row < a.Nq ? a.lse[at] : 0.f;
-        next_d = row < a.Nq ? a.dvec[at] : 0.f;
+        next_lse = row < a.Nq ? __ldcg(a.lse + at) : 0.f;
+        next_d = row < a.Nq ? __ldcg(a.dvec + at) : 0.f;
     };
     auto make_resident = [&](uint32_t k) {
         constexpr int kJobs = D / 32;  // of each tensor
@@ -959,7 +959,7 @@ template <bool kF16> __device__ void find_scale(const CrossBwdArgs &a, BBars &b)
     float m = 0.f;
     if (kF16) {
         for (int i = threadIdx.x; i < a.prep_blocks; i += kThreads)
-            m = fmaxf(m, a.amax[i]);
+            m = fmaxf(m, __ldcg(a.amax + i));
 #pragma unroll
         for (int o = 16; o > 0; o /= 2)
             m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
@@ -1029,7 +1029,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         prefetch_tensormap(&mdo);
     }
     // The kernel ahead has begun, so what it waited for is there: the lengths, and
-    // for dq, behind dkdv, all that it reads; dq only ends behind dkdv.
+    // for dq, behind dkdv, all that it reads; dq only ends behind dkdv.  What is
+    // read without a wait of this kernel's own is read past the first-level cache.
     find_start<kDkDv, unit_cost<D>()>(a, b);
     if (kDkDv) {
         grid_dependency_wait();
