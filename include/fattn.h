@@ -610,10 +610,10 @@ fattn_status_t fattn_tree_mask(const int *parents, const int *cu_q, const int *k
  * behind it -- go to one: p itself where parents[p] = p, else the first child.
  * Every other child gets a page of its own for the partly filled one, with its
  * filled slots copied in both caches.  Then each sequence gets pages for what it
- * lacks from kv_len[p] / page_size up to ceil(kv_len_out / page_size): the lowest free pages (those whose
- * count is 0 when all entries have changed hands), in the order of sequences and
- * columns.  Other entries of page_table_out are -1, which in a table stands for
- * no page.
+ * lacks from kv_len[p] / page_size up to ceil(kv_len_out / page_size): the lowest
+ * free pages (those whose count is 0 when all entries have changed hands), in the
+ * order of sequences and columns.  Other entries of page_table_out are -1, which
+ * in a table stands for no page.
  *
  * Out of range (a parent is taken for b itself, kv_len brought to 0 .. max_pages
  * * page_size, n_b to what the table has room for and at least 0, an entry
