@@ -649,7 +649,9 @@ fattn_status_t fattn_kv_fork(void *k_cache, void *v_cache, const int *page_table
  *   lse = log( sum_{j < L} exp( scale * q . k_j ) )
  *
  *   q, o      : 16-bit [B][Hq][Nq][d], k, v: [B][Hk][Nk][d], element strides
- *               (batch, head, row), last dimension contiguous; Nq and Nk are
+ *               (batch, head, row), last dimension contiguous; strides of
+ *               dimensions longer than 1 are positive multiples of 8 (no
+ *               broadcast ones), pointers 16-byte aligned; Nq and Nk are
  *               independent, from a single row on
  *   kv_len    : int32 [B] on the device, or NULL: Nk for all.  A length outside
  *               0 .. Nk is brought into it and records FATTN_ERR_INDEX (role 1)

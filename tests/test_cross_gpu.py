@@ -180,3 +180,14 @@ def test_two_streams_and_a_graph():
         torch.cuda.synchronize()
         verify((out, lse), q, k, v, n)
     assert fattn.device_status() == 0
+
+
+def test_workspaces_that_do_not_fit():
+    q, k, v = (t.cuda() for t in make(2, 4, 2, 9, 40, 64, torch.float16))
+    need = fattn.cross_workspace_size(4, 2, 9, 64)
+    for ws in (torch.empty(need, dtype=torch.uint8), torch.empty(2 * need, dtype=torch.uint8, device="cuda")[::2],
+               torch.empty(need - 1, dtype=torch.uint8, device="cuda")):
+        with pytest.raises((ValueError, RuntimeError)):
+            fattn.attn_fwd_cross(q, k, v, workspace=ws)
+    with pytest.raises(TypeError):
+        fattn.attn_fwd_cross(q, k, v, workspace=need)

@@ -198,7 +198,10 @@ Tensor workspace_of(PyObject *o, size_t need, int dev)
 {
     if (o == Py_None)
         return make({static_cast<int64_t>(need < 16 ? 16 : need)}, at::kByte, dev);
-    return tensor("workspace", o);
+    const Tensor &t = tensor("workspace", o);
+    if (!t.is_cuda() || t.get_device() != dev || !t.is_contiguous())
+        bad_value("workspace must be a contiguous tensor on CUDA device " + std::to_string(dev));
+    return t;
 }
 
 template <class T> T *ptr(const Tensor &t) { return static_cast<T *>(t.data_ptr()); }

@@ -980,8 +980,9 @@ def cross_workspace_size(Hq: int, Hk: int, Nq: int, d: int, device=None) -> int:
 def attn_fwd_cross(q, k, v, kv_len=None, scale: float | None = None, workspace=None, out=None,
                    lse=None, stream=None):
     """Cross attention of q [B, Hq, Nq, d] to an encoder's keys and values k, v
-    [B, Hk, Nk, d] (libfattn attn_fwd_cross): bf16 or fp16 views with any
-    strides and a contiguous last dimension, d 64, 96 or 128, Hq a multiple of
+    [B, Hk, Nk, d] (libfattn attn_fwd_cross): bf16 or fp16 views with
+    strides of 8 elements or multiples (none of 0: a broadcast input is copied
+    first) and a contiguous last dimension, d 64, 96 or 128, Hq a multiple of
     Hk, Nq and Nk independent.  ``kv_len`` int32 [B] on the device: the keys of
     each sequence, what is behind them may hold anything (None: Nk).  A sequence
     without keys gives o = 0 and lse = -inf.  Returns (out [B, Hq, Nq, d], lse
