@@ -191,3 +191,17 @@ def test_workspaces_that_do_not_fit():
             fattn.attn_fwd_cross(q, k, v, workspace=ws)
     with pytest.raises(TypeError):
         fattn.attn_fwd_cross(q, k, v, workspace=need)
+
+
+@pytest.mark.parametrize("B", [5, 31, 32, 33])
+@pytest.mark.parametrize("bad", [None, -1, 301, -2 ** 31, 2 ** 31 - 1])
+def test_single_tokens_of_sequences_in_any_order_of_length(B, bad):
+    lens = [(37 * i * i + 11 * i) % 301 for i in range(B)]
+    lens[1] = lens[3] = 150  # equal ones
+    given = list(lens)
+    if bad is not None:
+        given[2], lens[2] = bad, min(max(bad, 0), 300)
+    q, k, v = make(B, 6, 6, 1, 300, 64, torch.float16, seed=B, lens=lens)
+    got = run(q, k, v, given)
+    assert fattn.device_status() & 0xffff == (0 if bad is None else 6 | 1 << 8)
+    verify(got, q, k, v, lens)

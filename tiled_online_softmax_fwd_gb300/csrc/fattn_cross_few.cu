@@ -5,11 +5,11 @@
 // many for its value, against 4 d bytes: at R <= 4 the memory is the bound.  The
 // tensor-core kernel spends its time on copies, hand-overs and 128-row tiles
 // that are mostly empty (37.5 us for 32 sequences of 500 to 1500 keys, 16 heads,
-// d = 64, 128 MB, where this one takes 28: 4.6 TB/s).
+// d = 64, 128 MB, where this one takes 24.8: 5.2 TB/s).
 //
 // Copies (cp.async) run two batches of 16 or 8 keys ahead of a warp, some 64 KB
-// a SM on their way: with plain loads, a batch of each warp at a time, it took
-// 34.4 us.
+// a SM on their way: with plain loads, a batch of each warp at a time, it took a
+// quarter longer.
 //
 // A warp takes keys in turns: a group of d / 8 lanes (rounded up to a power of
 // two) holds a key's 16-byte pieces and the same pieces of the R queries.  Each
@@ -21,6 +21,7 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <float.h>
+#include <limits.h>
 #include <stdint.h>
 
 #include "fattn_internal.h"
@@ -85,13 +86,31 @@ __global__ void __launch_bounds__(kThreads, 2) cross_few_kernel(const PagedArgs 
     __shared__ alignas(16) float whole[kPart];
     cg::cluster_group cluster = cg::this_cluster();
     const int splits = x.splits, rank = blockIdx.x % splits;
-    const int unit = blockIdx.x / splits, b = unit / a.Hk, h = unit - b * a.Hk;
+    const int unit = blockIdx.x / splits, place = unit / a.Hk, h = unit - place * a.Hk;
     const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
     const int piece = lane % kGroup, group = lane / kGroup;
     const bool real = piece < kLanes;
     grid_dependency_wait();
     grid_launch_dependents();
-    const int given = a.kv_len != nullptr ? a.kv_len[b] : a.max_keys;
+    // The longest sequences first, up to 32 of them, so that the last blocks to start
+    // are short (24.8 us for the batch above, in the given order 28; more sequences
+    // make more blocks, of which the last ones weigh less).
+    int b = place, given = a.max_keys;
+    if (a.kv_len != nullptr) {
+        if (a.B <= 32) {
+            const int mine = lane < a.B ? a.kv_len[lane] : INT_MIN;
+            int before = 0;
+#pragma unroll 8
+            for (int j = 0; j < 32; ++j) {
+                const int other = __shfl_sync(0xffffffffu, mine, j);
+                before += other > mine || (other == mine && j < lane);
+            }
+            b = __ffs(__ballot_sync(0xffffffffu, before == place)) - 1;
+            given = __shfl_sync(0xffffffffu, mine, b);
+        } else {
+            given = a.kv_len[b];
+        }
+    }
     const int L = min(max(given, 0), a.max_keys);
     if (given != L && h == 0 && rank == 0 && tid == 0)
         atomicCAS(a.status, 0u, 6u /* FATTN_ERR_INDEX */ | (kRoleLoad << 8));
