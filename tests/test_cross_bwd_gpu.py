@@ -239,3 +239,23 @@ def test_many_calls_in_a_row(d, Nq, Nk):
     torch.cuda.synchronize()
     assert fattn.device_status() == 0
     assert all(torch.equal(x, y) for x, y in zip(first, outs))
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("G,Nq,d", [(1, 3, 64), (4, 300, 128), (8, 2000, 64), (2, 77, 96)])
+def test_one_key_has_no_gradient_but_its_values(G, Nq, d, dtype):
+    """A softmax over one key is 1 whatever q and k are; units whole and split."""
+    q, k, v = (t.cuda() for t in make(3, 2 * G, 2, Nq, 40, d, dtype, seed=d, lens=[1, 40, 1]))
+    do = torch.randn(q.shape, generator=torch.Generator().manual_seed(2)).to(dtype).cuda()
+    kv_len = torch.tensor([1, 40, 1], dtype=torch.int32, device="cuda")
+    o, lse = fattn.attn_fwd_cross(q, k, v, kv_len)
+    dq, dk, dv = fattn.attn_bwd_cross(q, k, v, o, lse, do, kv_len)
+    for b in (0, 2):
+        assert not dq[b].any() and not dk[b].any() and not dv[b, :, 1:].any()
+        # P is 1 in the inputs' type (its exponent is off by some 1e-6), so dv is a sum
+        # of G Nq values in fp32, each addition off by at most 2^-23 of all their sizes,
+        # and rounded once.
+        x = do[b].double().reshape(2, G * Nq, d)
+        bound = torch.finfo(dtype).eps / 2 * x.sum(1).abs() + 1.01 * G * Nq * 2 ** -23 * x.abs().sum(1)
+        assert bool(((dv[b, :, 0].double() - x.sum(1)).abs() <= bound).all())
+    assert bool(dq[1].any()) and bool(dk[1].any()) and fattn.device_status() == 0

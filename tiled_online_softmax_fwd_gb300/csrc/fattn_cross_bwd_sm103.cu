@@ -655,6 +655,14 @@ __device__ __forceinline__ void transpose4(uint4 (&v)[4], int lane)
     trade(v[1], v[3], 2);
 }
 
+// What dQ's and dK's sums are multiplied by.  With one key P is 1 whatever q and k
+// are, and dS is zero: D, from o in 16 bits and in another order of sums, would leave
+// some 1e-6 |dO| |v| of it.
+__device__ __forceinline__ float grad_scale(const CrossBwdArgs &a, int keys, float ds_scale)
+{
+    return keys == 1 ? 0.f : a.scale / ds_scale;
+}
+
 // ------------------------------------------------------------------ elementwise
 // Thread r of a warpgroup owns TMEM lane r, row 128 tile + r of the resident tile;
 // warpgroup g works on columns 32 g .. 32 g + 31 of it.
@@ -895,7 +903,7 @@ __device__ void bwd_elem(const CrossBwdArgs &a, BBars &b, BXch &xch, uint8_t *ti
         // chunks; dq: a chunk a warpgroup.
         const bool is_dv = kDkDv && quarter < 2;
         const uint32_t acc = tmem + C::kColAcc + (kDkDv && !is_dv ? D : 0);
-        const float f = is_dv ? 1.f : a.scale / ds_scale;
+        const float f = is_dv ? 1.f : grad_scale(a, p.L, ds_scale);
         const bool whole = p.slot < 0;
         const bool zero = kDkDv && p.tile * kTile + r >= p.L;
         const long long *st = kDkDv ? (is_dv ? a.dv_st : a.dk_st) : a.dq_st;
@@ -1205,7 +1213,7 @@ template <int D, bool kF16> __global__ void __launch_bounds__(kMergeThreads) cro
     const int parts = which == 2 ? 1 : 2, part = which == 1 ? 1 : 0;
     const long long *st = which == 2 ? a.dq_st : which == 1 ? a.dk_st : a.dv_st;
     uint16_t *out = static_cast<uint16_t *>(which == 2 ? a.dq : which == 1 ? a.dk : a.dv);
-    const int rows = which == 2 ? a.Nq : a.Nk, L = which == 2 ? a.Nq : clamp_len(a, me.x);
+    const int keys = clamp_len(a, me.x), rows = which == 2 ? a.Nq : a.Nk, L = which == 2 ? a.Nq : keys;
     float f = 1.f;
     if (which != 0) {
         float m = 0.f;
@@ -1216,7 +1224,7 @@ template <int D, bool kF16> __global__ void __launch_bounds__(kMergeThreads) cro
             for (int o = 16; o > 0; o /= 2)
                 m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
         }
-        f = a.scale / (m > 0.f && m < 65536.f ? exp2f(-floorf(log2f(m))) : 1.f);
+        f = grad_scale(a, keys, m > 0.f && m < 65536.f ? exp2f(-floorf(log2f(m))) : 1.f);
     }
     constexpr int kVecs = D / 4;
     for (int at = threadIdx.x; at < kMergeRows * kVecs; at += kMergeThreads) {
