@@ -695,7 +695,8 @@ fattn_status_t attn_fwd_cross(const void *q, const void *k, const void *v, const
  *
  * Every row of dq, dk and dv is written: rows of dk and dv behind a sequence's
  * last key, dq of a sequence without keys, and dk and dv without queries are
- * zeros.  What lies behind a sequence's last key in k and v may be anything, NaN
+ * zeros; so are dq and dk of a sequence of one key (finite inputs), whose softmax
+ * is constant.  What lies behind a sequence's last key in k and v may be anything, NaN
  * included.  P and dS are rounded to the inputs' type, dS in fp16 after a scaling
  * by a power of two that follows from the largest |dout|; sums are fp32.  An
  * output shares no element with an input or another output.  Sums are taken in an
