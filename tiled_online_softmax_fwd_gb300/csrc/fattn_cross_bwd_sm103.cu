@@ -23,13 +23,16 @@
 // an equal share of the total, which may begin or end inside a unit: that
 // unit's sums go to the workspace in fp32, at most two a CTA, and the merge
 // kernel adds them in order.  So few key tiles under many queries (a short text)
-// fill the GPU as well as the reverse.
+// fill the GPU as well as the reverse.  Where units are short they are dealt out
+// whole, without a merge, and small calls run their passes side by side: dq starts on
+// the SMs that dkdv leaves.
 //
 // Bound.  At d = 128 the tensor cores and the shared memory that feeds them: a tile
 // of dkdv takes some 2520 cycles, its products 2048 and its reads and copies in
 // shared memory 2350; a tile of dq 2005, its products 1536 (Q and dO in TMEM save it
 // two reads of 32 KB).  4 sequences, 16 heads, 2048 queries, up to 4096 keys, bf16:
-// 486 us, 975 TFLOP/s of the formulas' five products, 1365 of the seven.  At d = 64 the chain TMEM, exponential, conversion, TMEM of the
+// 490 us, 970 TFLOP/s of the formulas' five products, 1355 of the seven.  At d = 64
+// the chain TMEM, exponential, conversion, TMEM of the
 // elementwise warps, shortened by a second S or dP; with few tiles a unit its start
 // and end: 2 sequences, 16 heads, 4096 queries, up to 154 keys 57 us, 1.2 TB/s.
 //
@@ -64,15 +67,19 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr uint32_t kChunkBytes = kTile * 64 * 2;
 constexpr uint32_t kColS = 0, kColDP = 128;
 
-// A unit's start and end, in steps (see Schedule); a split leaves at least kSnap
-// steps on each side, and a share is at least kLeast.  At d = 128 a unit's end and
-// the next one's start take some 2.5 steps, at d = 64 3 to 4, of which the first
-// pieces' copies hide part: 2 there is up to 10 % better on small calls (3 and 12
-// heads, 333 queries, 501 keys: 24.9 us, with 3 27.8) and 3 at d = 128 1.5 % on
-// large ones; kLeast 8 takes 20.6 us for 8 x 4 heads, 100 queries and keys, 6 15.7,
-// 5 18.6.
-template <int D> __device__ __forceinline__ constexpr int unit_cost() { return D == 64 ? 2 : 3; }
-constexpr int kSnap = 2, kLeast = 6;
+// A unit's start and end, in steps (see Schedule): some 4000 cycles, where a step
+// takes 1500 to 2800.  A split leaves at least kSnap steps on each side, and a share is
+// at least a unit of one step: 30 calls of 2 to 2000 queries and 1 to 4000 keys, d =
+// 64, 96 and 128, take 24.5, 20.1 and 22.6 us in the (geometric) mean, with kLeast 6
+// 25.7, 21.8 and 24.0, with 3 24.2, 20.2 and 22.7, but whole units up to 10 % more.
+constexpr int kUnitCost = 3, kSnap = 2, kLeast = kUnitCost + 1;
+// What the merge kernel takes, in steps (see whole_units).
+template <int D> constexpr int kMergeCost = D == 64 ? 6 : 3;
+// A step of dkdv to one of dq; and the steps a SM up to which the passes run side by
+// side, each on its part of the SMs: that saves the second start and end, in the calls
+// above 1 to 3 % in the mean, in some a sixth (36 to 30 us).  In longer calls it is
+// little, and the passes in turn need no guess of their steps' lengths.
+constexpr int kStepKv = 4, kStepQ = 3, kTogether = 32;
 
 template <int D, bool kDkDv> struct BCfg {
     static constexpr int kChunks = (D + 63) / 64;
@@ -159,12 +166,12 @@ __device__ __forceinline__ void units_of(const CrossBwdArgs &a, int L, int &unit
     units = steps == 0 ? 0 : kDkDv ? a.Hk * F : a.Hk * a.G * a.Tq;
 }
 // Step that a cost of y inside a unit falls on.
-template <int kUnitCost> __device__ __forceinline__ int step_at(long long y, int steps)
+__device__ __forceinline__ int step_at(long long y, int steps, int snap)
 {
     if (y >= steps + kUnitCost)
         return steps;
     const int t = y < kUnitCost ? 0 : static_cast<int>(y - kUnitCost);
-    return t < kSnap ? 0 : steps - t < kSnap ? steps : t;
+    return t < snap ? 0 : steps - t < snap ? steps : t;
 }
 
 // a / b of non-negative values, in 32 bits where they fit.
@@ -183,7 +190,7 @@ template <bool kDkDv> __device__ __forceinline__ void enter(const CrossBwdArgs &
     w.L = clamp_len(a, w.at.b);
     units_of<kDkDv>(a, w.L, w.units, w.steps);
 }
-template <bool kDkDv, int kUnitCost> __device__ __forceinline__ Walk first_walk(const CrossBwdArgs &a, const BBars &b)
+template <bool kDkDv> __device__ __forceinline__ Walk first_walk(const CrossBwdArgs &a, const BBars &b)
 {
     Walk w;
     w.at = b.start;
@@ -196,7 +203,7 @@ template <bool kDkDv, int kUnitCost> __device__ __forceinline__ Walk first_walk(
     }
     return w;
 }
-template <bool kDkDv, int kUnitCost> __device__ __forceinline__ bool next_piece(const CrossBwdArgs &a, Walk &w, Piece &p)
+template <bool kDkDv> __device__ __forceinline__ bool next_piece(const CrossBwdArgs &a, Walk &w, Piece &p)
 {
     while (w.at.left > 0) {
         if (w.u >= w.units) {
@@ -211,8 +218,8 @@ template <bool kDkDv, int kUnitCost> __device__ __forceinline__ bool next_piece(
         const int u = w.u++;
         w.at.left -= y1 - y0;
         w.at.y = 0;
-        p.t0 = step_at<kUnitCost>(y0, w.steps);
-        p.t1 = step_at<kUnitCost>(y1, w.steps);
+        p.t0 = step_at(y0, w.steps, a.snap);
+        p.t1 = step_at(y1, w.steps, a.snap);
         if (p.t0 == p.t1)  // nothing of it falls to this CTA
             continue;
         const int per = kDkDv ? w.units / a.Hk : a.Tq;
@@ -228,7 +235,7 @@ template <bool kDkDv, int kUnitCost> __device__ __forceinline__ bool next_piece(
 }
 
 // Finds this CTA's start: warp 0 alone, 32 sequences at a time.
-template <bool kDkDv, int kUnitCost> __device__ void find_start(const CrossBwdArgs &a, BBars &b)
+template <bool kDkDv> __device__ void find_start(const CrossBwdArgs &a, BBars &b)
 {
     if (threadIdx.x >= 32)
         return;
@@ -241,14 +248,26 @@ template <bool kDkDv, int kUnitCost> __device__ void find_start(const CrossBwdAr
         return static_cast<long long>(units) * (steps + kUnitCost);
     };
     int units, steps;
-    long long total = 0;
-    for (int i = lane; i < a.B; i += 32)
+    long long total = 0, other = 0;  // of this pass and of the other one
+    for (int i = lane; i < a.B; i += 32) {
         total += cost_of(i, units, steps);
+        units_of<!kDkDv>(a, clamp_len(a, i), units, steps);
+        other += static_cast<long long>(units) * (steps + kUnitCost);
+    }
 #pragma unroll
-    for (int o = 16; o > 0; o /= 2)
+    for (int o = 16; o > 0; o /= 2) {
         total += __shfl_xor_sync(0xffffffffu, total, o);
+        other += __shfl_xor_sync(0xffffffffu, other, o);
+    }
     const int c = blockIdx.x;
-    const int shares = static_cast<int>(min(static_cast<long long>(gridDim.x), max(quotient(total, kLeast), 1LL)));
+    // A small call's passes run side by side, each on its part of the SMs.
+    const long long mine = total * (kDkDv ? kStepKv : kStepQ), both = mine + other * (kDkDv ? kStepQ : kStepKv);
+    int most = gridDim.x;
+    if (both <= static_cast<long long>(kTogether) * kStepKv * most && total > 0 && other > 0) {
+        const int kv = static_cast<int>(quotient((kDkDv ? mine : both - mine) * most + both / 2, static_cast<int>(both)));
+        most = max(kDkDv ? kv : most - kv, 1);
+    }
+    const int shares = static_cast<int>(min(static_cast<long long>(most), max(quotient(total, kLeast), 1LL)));
     const long long each = quotient(total, shares);
     const int rest = static_cast<int>(total - each * shares);
     const long long lo = c * each + c * rest / shares, hi = (c + 1) * each + (c + 1) * rest / shares;
@@ -274,7 +293,7 @@ template <bool kDkDv, int kUnitCost> __device__ void find_start(const CrossBwdAr
         if (first <= lo && lo < first + mine) {
             b.start = Start{b0 + lane, lo - first, hi - lo};
             const int cost = steps + kUnitCost, u = static_cast<int>(quotient(lo - first, cost));
-            const int t = step_at<kUnitCost>(lo - first - static_cast<long long>(u) * cost, steps);
+            const int t = step_at(lo - first - static_cast<long long>(u) * cost, steps, a.snap);
             const int per = kDkDv ? units / a.Hk : a.Tq, h = u / per;
             starts[c] = make_int4(b0 + lane, h, u - h * per, t < steps ? t : 0);
         }
@@ -402,11 +421,11 @@ __device__ void bwd_load(const CrossBwdArgs &a, BBars &b, uint32_t smem, const C
     };
     bool ok = true;
     uint32_t k = 0;
-    Walk w = first_walk<kDkDv, unit_cost<D>()>(a, b);
+    Walk w = first_walk<kDkDv>(a, b);
     Piece p;
     bool more = true;
     while (ok && more) {
-        more = next_piece<kDkDv, unit_cost<D>()>(a, w, p);
+        more = next_piece<kDkDv>(a, w, p);
         ok = warp_wait(b.piece_empty[k % kPieces], ((k / kPieces) & 1) ^ 1, abort);
         if (!ok)
             break;
@@ -1039,7 +1058,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // The kernel ahead has begun, so what it waited for is there: the lengths, and
     // for dq, behind dkdv, all that it reads; dq only ends behind dkdv.  What is
     // read without a wait of this kernel's own is read past the first-level cache.
-    find_start<kDkDv, unit_cost<D>()>(a, b);
+    find_start<kDkDv>(a, b);
     if (kDkDv) {
         grid_dependency_wait();
         grid_launch_dependents();
@@ -1275,6 +1294,17 @@ cudaError_t launch_pass(const CrossBwdArgs &a, const CrossBwdMaps &m, cudaStream
                                     m.k, m.v, m.dout, a);
 }
 
+// Whether the units are dealt out whole, so that there is nothing to merge: where a
+// unit of each pass takes no longer than the least shares and the merge, whatever the
+// lengths (3 x 333 queries of 12 heads, 4 key heads, up to 501 keys, d = 64: 23.5 us,
+// split and merged 28; 4 x 500 queries and keys of 16 heads, d = 128: 39.6 and 46.7).
+template <int D> bool whole_units(const CrossBwdArgs &a)
+{
+    const long long keys = (a.Nk + kTile - 1) / kTile, queries = static_cast<long long>(a.G) * a.Tq;
+    auto longer = [](long long steps) { return steps > kLeast ? steps - kLeast : 0; };
+    return a.grid == 1 || longer(keys) + longer(queries) <= kMergeCost<D>;
+}
+
 template <int D, bool kF16>
 cudaError_t launch(const CrossBwdArgs &args, const CrossBwdMaps &m, cudaStream_t stream)
 {
@@ -1286,12 +1316,14 @@ cudaError_t launch(const CrossBwdArgs &args, const CrossBwdMaps &m, cudaStream_t
     a.prep_blocks = static_cast<int>(a.kv_len != nullptr || a.Nk == 0 || rows == 0 || blocks > kPrepBlocks ? kPrepBlocks
                                      : blocks > 0                               ? blocks
                                                                                 : 1);
+    const bool whole = whole_units<D>(a);
+    a.snap = whole ? 0x7fffffff : kSnap;
     cudaError_t e = start(cross_prep_kernel<D, kF16>, dim3(a.prep_blocks), kPrepThreads, 0, stream, a);
     if (e == cudaSuccess)
         e = launch_pass<D, kF16, true>(a, m, stream);
     if (e == cudaSuccess)
         e = launch_pass<D, kF16, false>(a, m, stream);
-    if (e == cudaSuccess && a.grid > 1)
+    if (e == cudaSuccess && !whole)
         e = start(cross_merge_kernel<D, kF16>, dim3(a.grid - 1, 3 * (kTile / kMergeRows)), kMergeThreads, 0, stream,
                   a);
     return e;

@@ -273,7 +273,7 @@ struct CrossBwdArgs {
     long long q_st[3], o_st[3], do_st[3], dq_st[3], dk_st[3], dv_st[3];
     int B, Hk, G, Nq, Nk, Tq, d, f16, grid;
     float scale, sl2;
-    int prep_blocks;  // filled in by the launch
+    int prep_blocks, snap;  // filled in by the launch
 };
 // Maps (d, rows, heads, B) of q, k, v and dO, box (64, 128, 1, 1).
 struct CrossBwdMaps {
