@@ -108,7 +108,7 @@ def _link_binding(obj: str, force: bool):
         return
     lib = os.path.join(os.path.dirname(torch.__file__), "lib")
     _run(["g++", "-shared", "-o", BINDING + ".tmp", obj, "-L", BUILD, "-l:libfattn.so", "-L", lib, "-lc10",
-          "-lc10_cuda", "-ltorch_cpu", "-ltorch_python", "-Wl,-rpath,$ORIGIN", "-Wl,-rpath," + lib],
+          "-lc10_cuda", "-ltorch_cpu", "-ltorch_cuda", "-ltorch_python", "-Wl,-rpath,$ORIGIN", "-Wl,-rpath," + lib],
          "linking the binding")
     os.replace(BINDING + ".tmp", BINDING)
 

@@ -11,7 +11,8 @@
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
-#include <ATen/ops/empty.h>
+#include <ATen/cuda/EmptyTensor.h>
+#include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -168,10 +169,11 @@ struct Place {
     }
 };
 
+// Past the dispatcher, which takes as long as the allocation.
 Tensor make(at::IntArrayRef shape, at::ScalarType type, int dev)
 {
-    return at::empty(shape, at::TensorOptions().dtype(type).device(
-                                at::Device(at::kCUDA, static_cast<c10::DeviceIndex>(dev))));
+    return Tensor(at::detail::empty_cuda(shape, type, at::Device(at::kCUDA, static_cast<c10::DeviceIndex>(dev)),
+                                         std::nullopt));
 }
 
 // An output: as given, checked, or new.
@@ -194,15 +196,27 @@ Tensor plain_out(const char *name, PyObject *o, at::IntArrayRef shape, at::Scala
                   " tensor on CUDA device " + std::to_string(dev));
     return t;
 }
-Tensor workspace_of(PyObject *o, size_t need, int dev)
-{
-    if (o == Py_None)
-        return make({static_cast<int64_t>(need < 16 ? 16 : need)}, at::kByte, dev);
-    const Tensor &t = tensor("workspace", o);
-    if (!t.is_cuda() || t.get_device() != dev || !t.is_contiguous())
-        bad_value("workspace must be a contiguous tensor on CUDA device " + std::to_string(dev));
-    return t;
-}
+// A call's workspace: as given, or memory of the current device and stream until
+// the call has been enqueued.
+struct Workspace {
+    c10::DataPtr own;
+    void *at;
+    size_t bytes;
+    Workspace(PyObject *o, size_t need, int dev)
+    {
+        if (o == Py_None) {
+            bytes = need < 16 ? 16 : need;
+            own = c10::cuda::CUDACachingAllocator::get()->allocate(bytes);
+            at = own.get();
+            return;
+        }
+        const Tensor &t = tensor("workspace", o);
+        if (!t.is_cuda() || t.get_device() != dev || !t.is_contiguous())
+            bad_value("workspace must be a contiguous tensor on CUDA device " + std::to_string(dev));
+        at = t.data_ptr();
+        bytes = t.nbytes();
+    }
+};
 
 template <class T> T *ptr(const Tensor &t) { return static_cast<T *>(t.data_ptr()); }
 const int *ints(const Tensor &t) { return ptr<const int>(t); }
@@ -262,14 +276,14 @@ PyObject *attn_fwd_tree(PyObject *const *a)
     Place place(a[12], dev);
     const Tensor out = half_out("out", a[10], q.sizes(), kind);
     const Tensor lse = plain_out("lse", a[11], {T, Hq}, at::kFloat, dev);
-    const Tensor ws = workspace_of(a[9], attn_fwd_paged_workspace_size(Hq, c.heads, d, max_q), dev);
+    const Workspace ws(a[9], attn_fwd_paged_workspace_size(Hq, c.heads, d, max_q), dev);
     const Strides qs(q), ks(c.k), vs(c.v), os(out);
     call("attn_fwd_tree", [&] {
         return ::attn_fwd_tree(q.data_ptr(), c.k.data_ptr(), c.v.data_ptr(), ints(table), ints(cu),
                                ints(kv_len), ptr<const unsigned>(mask), out.data_ptr(), ptr<float>(lse), T, B,
                                Hq, c.heads, d, c.pages, c.page, static_cast<int>(table.size(1)),
                                row_stride(table), max_q, static_cast<int>(mask.size(1)), row_stride(mask),
-                               qs.at, ks.at, vs.at, os.at, scale, kind->f16(), ws.data_ptr(), ws.nbytes(),
+                               qs.at, ks.at, vs.at, os.at, scale, kind->f16(), ws.at, ws.bytes,
                                place.stream);
     });
     return Py_BuildValue("NN", THPVariable_Wrap(out), THPVariable_Wrap(lse));
@@ -401,13 +415,13 @@ PyObject *kv_fork(PyObject *const *a)
     }
     const Tensor len_out = plain_out("kv_len_out", a[8], {B}, at::kInt, dev);
     const Tensor refs_out = plain_out("page_refs_out", a[9], {c.pages}, at::kInt, dev);
-    const Tensor ws = workspace_of(a[10], fattn_kv_fork_workspace_size(B, cols, c.pages), dev);
+    const Workspace ws(a[10], fattn_kv_fork_workspace_size(B, cols, c.pages), dev);
     const Strides ks(c.k), vs(c.v);
     call("fattn_kv_fork", [&] {
         return fattn_kv_fork(c.k.data_ptr(), c.v.data_ptr(), ints(table), ints(kv_len), ints(refs), parents, cu,
                              ptr<int>(table_out), ptr<int>(len_out), ptr<int>(refs_out), B, c.heads, c.d,
                              c.pages, c.page, cols, row_stride(table), row_stride(table_out), ks.at, vs.at,
-                             ws.data_ptr(), ws.nbytes(), place.stream);
+                             ws.at, ws.bytes, place.stream);
     });
     auto give = [](PyObject *o, const Tensor &t) { return o == Py_None ? THPVariable_Wrap(t) : Py_NewRef(o); };
     return Py_BuildValue("NNN", give(a[7], table_out), give(a[8], len_out), give(a[9], refs_out));
@@ -446,12 +460,12 @@ PyObject *attn_fwd_cross(PyObject *const *a)
     Place place(a[8], c.dev);
     const Tensor out = half_out("out", a[6], c.q.sizes(), c.kind);
     const Tensor lse = plain_out("lse", a[7], {c.B, c.Hq, c.Nq}, at::kFloat, c.dev);
-    const Tensor ws = workspace_of(a[5], attn_fwd_cross_workspace_size(c.Hq, c.Hk, c.Nq, c.d), c.dev);
+    const Workspace ws(a[5], attn_fwd_cross_workspace_size(c.Hq, c.Hk, c.Nq, c.d), c.dev);
     const Strides qs(c.q), ks(c.k), vs(c.v), os(out);
     call("attn_fwd_cross", [&] {
         return ::attn_fwd_cross(c.q.data_ptr(), c.k.data_ptr(), c.v.data_ptr(), c.kv_len, out.data_ptr(),
                                 ptr<float>(lse), c.B, c.Hq, c.Hk, c.Nq, c.Nk, c.d, qs.at, ks.at, vs.at, os.at,
-                                scale, c.kind->f16(), ws.data_ptr(), ws.nbytes(), place.stream);
+                                scale, c.kind->f16(), ws.at, ws.bytes, place.stream);
     });
     return Py_BuildValue("NN", THPVariable_Wrap(out), THPVariable_Wrap(lse));
 }
@@ -470,14 +484,13 @@ PyObject *attn_bwd_cross(PyObject *const *a)
     Place place(a[12], c.dev);
     const Tensor dq = half_out("dq", a[8], c.q.sizes(), c.kind);
     const Tensor dk = half_out("dk", a[9], c.k.sizes(), c.kind), dv = half_out("dv", a[10], c.v.sizes(), c.kind);
-    const Tensor ws =
-        workspace_of(a[11], attn_bwd_cross_workspace_size(c.B, c.Hq, c.Hk, c.Nq, c.Nk, c.d), c.dev);
+    const Workspace ws(a[11], attn_bwd_cross_workspace_size(c.B, c.Hq, c.Hk, c.Nq, c.Nk, c.d), c.dev);
     const Strides qs(c.q), ks(c.k), vs(c.v), os(o), gs(dout), dqs(dq), dks(dk), dvs(dv);
     call("attn_bwd_cross", [&] {
         return ::attn_bwd_cross(c.q.data_ptr(), c.k.data_ptr(), c.v.data_ptr(), o.data_ptr(),
                                 ptr<const float>(lse), dout.data_ptr(), c.kv_len, dq.data_ptr(), dk.data_ptr(),
                                 dv.data_ptr(), c.B, c.Hq, c.Hk, c.Nq, c.Nk, c.d, qs.at, ks.at, vs.at, os.at,
-                                gs.at, dqs.at, dks.at, dvs.at, scale, c.kind->f16(), ws.data_ptr(), ws.nbytes(),
+                                gs.at, dqs.at, dks.at, dvs.at, scale, c.kind->f16(), ws.at, ws.bytes,
                                 place.stream);
     });
     return Py_BuildValue("NNN", THPVariable_Wrap(dq), THPVariable_Wrap(dk), THPVariable_Wrap(dv));
