@@ -554,8 +554,8 @@ fattn_status_t attn_fwd_paged(const void *q, const void *k_cache, const void *v_
  *                the root included (0 for a root), for fattn_qk_norm_rope with
  *                one sequence of T tokens
  * A parent outside -1 .. i - 1 is taken for -1, a list value out of range is
- * brought into it, tokens of a sequence from 32 * mask_words on are skipped;
- * each records FATTN_ERR_INDEX (role 9) in the device status word.  Rows from
+ * brought into it (kv_len[b] below n: n), tokens of a sequence from 32 *
+ * mask_words on are skipped; each records FATTN_ERR_INDEX (role 9) in the device status word.  Rows from
  * cu_q[B] on are left as they were.  mask_words at most 2^24, T < 2^31 - 256.
  * One kernel; takes no memory.
  */

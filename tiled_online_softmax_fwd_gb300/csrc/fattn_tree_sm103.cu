@@ -27,7 +27,8 @@ __global__ void __launch_bounds__(kMaskThreads) tree_mask_kernel(const TreeMaskA
     const int q0 = min(max(c0, 0), a.T);
     const int all = min(max(c1, q0), a.T) - q0;
     const int n = static_cast<int>(min(static_cast<long long>(all), 32LL * a.words));
-    bool bad = q0 != c0 || n != static_cast<long long>(c1) - c0 || (b == 0 && c0 != 0);
+    bool bad = q0 != c0 || n != static_cast<long long>(c1) - c0 || (b == 0 && c0 != 0) || L < all;
+    const int prefix = L > all ? L - all : 0;  // keys before the new tokens
     const int *parents = a.parents + q0;
     auto parent_of = [&](int i) {
         const int p = parents[i];
@@ -73,7 +74,7 @@ __global__ void __launch_bounds__(kMaskThreads) tree_mask_kernel(const TreeMaskA
         }
         for (; w >= 0; --w, bits = 0)
             row[w] = bits;
-        a.positions[q0 + i] = L - all + tokens - 1;
+        a.positions[q0 + i] = prefix + tokens - 1;
     }
     if (bad)
         atomicCAS(a.status, 0u, 6u /* FATTN_ERR_INDEX */ | (kRoleTree << 8));
