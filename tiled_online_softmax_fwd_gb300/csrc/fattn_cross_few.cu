@@ -302,7 +302,8 @@ __global__ void __launch_bounds__(kThreads, 2) cross_few_kernel(const PagedArgs 
         if (c == 0)
             a.lse[(static_cast<long long>(b) * a.Hk * a.G + head) * a.Nq + tok] =
                 ll == 0.f ? -INFINITY : (mm + log2f(ll)) * kLn2;
-        if (!kF16 && !(fabsf((y[0] + y[1]) * inv) <= FLT_MAX))
+        // Each for itself: the sum of two that fit may not.
+        if (!kF16 && !(fabsf(y[0] * inv) <= FLT_MAX && fabsf(y[1] * inv) <= FLT_MAX))
             atomicCAS(a.status, 0u,
                       5u /* FATTN_ERR_RANGE */ | (kRoleEpilogue << 8) | ((blockIdx.x & 0xffffu) << 16));
     }
