@@ -497,6 +497,17 @@ PyObject *attn_bwd_cross(PyObject *const *a)
 }
 
 // ------------------------------------------------------------------ module
+// torch's own exception, as its allocations raise it in Python.
+void raise_out_of_memory(const char *what)
+{
+    PyObject *torch = PyImport_ImportModule("torch");
+    PyObject *type = torch != nullptr ? PyObject_GetAttrString(torch, "OutOfMemoryError") : nullptr;
+    if (type != nullptr)
+        PyErr_SetString(type, what);
+    Py_XDECREF(type);
+    Py_XDECREF(torch);
+}
+
 template <PyObject *(*kF)(PyObject *const *), int kArgs>
 PyObject *entry(PyObject *, PyObject *const *args, Py_ssize_t n)
 {
@@ -509,7 +520,9 @@ PyObject *entry(PyObject *, PyObject *const *args, Py_ssize_t n)
     } catch (const Raised &) {
         if (!PyErr_Occurred())
             PyErr_SetString(PyExc_RuntimeError, "the library's error was not raised");
-    } catch (const std::exception &e) {  // out of memory, a device that is not there
+    } catch (const c10::OutOfMemoryError &e) {
+        raise_out_of_memory(e.what_without_backtrace());
+    } catch (const std::exception &e) {  // a device that is not there
         PyErr_SetString(PyExc_RuntimeError, e.what());
     }
     return nullptr;
