@@ -281,8 +281,8 @@ PyObject *attn_fwd_tree(PyObject *const *a)
     call("attn_fwd_tree", [&] {
         return ::attn_fwd_tree(q.data_ptr(), c.k.data_ptr(), c.v.data_ptr(), ints(table), ints(cu),
                                ints(kv_len), ptr<const unsigned>(mask), out.data_ptr(), ptr<float>(lse), T, B,
-                               Hq, c.heads, d, c.pages, c.page, static_cast<int>(table.size(1)),
-                               row_stride(table), max_q, static_cast<int>(mask.size(1)), row_stride(mask),
+                               Hq, c.heads, d, c.pages, c.page, small("the table", table.size(1)),
+                               row_stride(table), max_q, small("the mask", mask.size(1)), row_stride(mask),
                                qs.at, ks.at, vs.at, os.at, scale, kind->f16(), ws.at, ws.bytes,
                                place.stream);
     });
@@ -348,7 +348,7 @@ PyObject *kv_append(PyObject *const *a)
     call("fattn_kv_append", [&] {
         return fattn_kv_append(k.data_ptr(), v.data_ptr(), c.k.data_ptr(), c.v.data_ptr(), ints(table), ints(cu),
                                ints(kv_len), rope, T, B, c.heads, c.d, c.pages, c.page,
-                               static_cast<int>(table.size(1)), row_stride(table), rot, max_pos, ks.at, vs.at,
+                               small("the table", table.size(1)), row_stride(table), rot, max_pos, ks.at, vs.at,
                                kcs.at, vcs.at, interleaved, kind->f16(), place.stream);
     });
     return Py_BuildValue("OO", a[2], a[3]);
@@ -375,8 +375,8 @@ PyObject *kv_keep(PyObject *const *a)
     call("fattn_kv_keep", [&] {
         return fattn_kv_keep(c.k.data_ptr(), c.v.data_ptr(), ints(table), ints(cu), ints(kv_len), ints(kept),
                              ints(kept_len), ptr<int>(out), B, c.heads, c.d, c.pages, c.page,
-                             static_cast<int>(table.size(1)), row_stride(table),
-                             static_cast<int>(kept.size(1)), row_stride(kept), ks.at, vs.at, place.stream);
+                             small("the table", table.size(1)), row_stride(table),
+                             small("kept", kept.size(1)), row_stride(kept), ks.at, vs.at, place.stream);
     });
     return a[7] == Py_None ? THPVariable_Wrap(out) : Py_NewRef(a[7]);
 }
