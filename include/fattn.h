@@ -622,8 +622,8 @@ fattn_status_t fattn_tree_mask(const int *parents, const int *cu_q, const int *k
  * (role 11) is recorded.  The lists are read when the kernels run, so a captured
  * graph follows them.  Equal calls give equal bits.  workspace: device, 16-byte
  * aligned, fattn_kv_fork_workspace_size(...) bytes; contents ignored on entry,
- * undefined on exit; calls that share one must not overlap on the device.  Two
- * kernels (one without parents).
+ * undefined on exit; calls that share one must not overlap on the device.  B *
+ * max_pages below 2^31.  Two kernels (one without parents).
  */
 fattn_status_t fattn_kv_keep(void *k_cache, void *v_cache, const int *page_table, const int *cu_q,
                              const int *kv_len, const int *kept, const int *kept_len, int *kv_len_out,

@@ -1985,7 +1985,9 @@ fattn_status_t fattn_kv_fork(void *k_cache, void *v_cache, const int *page_table
     fattn_status_t s = check_paging(g);
     if (s != FATTN_OK || B == 0)
         return s;
-    if (B > 0x7fffffff / 16)  // counted in 32 bits, rounded up to warps
+    // Sequences are counted in 32 bits, rounded up to warps, and so are the pages that
+    // they may lack, together.
+    if (B > 0x7fffffff / 16 || static_cast<long long>(B) * max_pages > 0x7fffffffLL)
         return FATTN_ERR_UNSUPPORTED;
     if ((s = check_lists(g)) != FATTN_OK)
         return s;
