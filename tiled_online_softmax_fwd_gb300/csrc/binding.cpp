@@ -222,12 +222,17 @@ template <class T> T *ptr(const Tensor &t) { return static_cast<T *>(t.data_ptr(
 const int *ints(const Tensor &t) { return ptr<const int>(t); }
 
 // Runs the C call without the interpreter's lock and has its status looked at.
+struct Unlocked {  // takes the lock again when an exception leaves, too
+    PyThreadState *state = PyEval_SaveThread();
+    ~Unlocked() { PyEval_RestoreThread(state); }
+};
 template <class F> void call(const char *entry, F f)
 {
     fattn_status_t s;
-    Py_BEGIN_ALLOW_THREADS;
-    s = f();
-    Py_END_ALLOW_THREADS;
+    {
+        const Unlocked unlocked;
+        s = f();
+    }
     if (s == FATTN_OK)
         return;
     PyObject *r = PyObject_CallFunction(g_check, "is", static_cast<int>(s), entry);
