@@ -7,7 +7,7 @@
 //   dV = sum_h P^T dO,     dP = dO V^T,   dS = P o (dP - D),
 //   dQ = scale dS K,       dK = scale sum_h dS^T Q.
 // Four kernels, each started under the tail of the one before:
-//   prep     D, the largest |dO| (fp16), and zeros for key tiles without keys
+//   prep     D, the norms of dO's rows (fp16), and zeros for key tiles without keys
 //   dkdv     a unit is a tile of 128 keys of one (sequence, key head).  K, V
 //            stay; the tiles of Q and dO of its G query heads stream by: S^T =
 //            K Q^T and dP^T = V dO^T, keys on TMEM lanes, P^T over S^T, then dV
@@ -37,12 +37,15 @@
 // and end: 2 sequences, 16 heads, 4096 queries, up to 154 keys 57 us, 1.2 TB/s.
 //
 // Types.  P and dS enter the second products in the inputs' type.  dS in fp16
-// is scaled by a power of two that brings the largest |dO| to 1 .. 2, so that
-// small gradients keep their digits; the sums are scaled back in fp32.
+// is scaled by a power of two that brings the norm of dO's row to 1 .. 2, so that
+// small gradients keep their digits whatever stands beside them; for dK, whose sums
+// go over the rows, the largest norm of the key head's.  The sums are scaled back
+// in fp32.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <stdint.h>
 
+#include <algorithm>
 #include <type_traits>
 
 #include "fattn_internal.h"
@@ -139,10 +142,8 @@ struct alignas(16) BBars {
     uint64_t drain;
     uint32_t tmem_base;
     int abort;
-    float ds_scale;  // of dS
     Start start;
     Piece pieces[kPieces];
-    float warp_max[kThreads / 32];
 };
 // dkdv, behind the barriers: each warp's -lse log2(e) and -D (scaled) of the 32
 // queries of its columns, two tiles deep.
@@ -682,6 +683,29 @@ __device__ __forceinline__ float grad_scale(const CrossBwdArgs &a, int keys, flo
     return keys == 1 ? 0.f : a.scale / ds_scale;
 }
 
+// The largest of some values, NaN aside, each lane some of them; and of the lanes'.
+__device__ __forceinline__ float lanes_max(const float *x, int n, int lane)
+{
+    float m = 0.f;
+#pragma unroll 2
+    for (int i = lane; i < n; i += 32)
+        m = fmaxf(m, __ldcg(x + i));
+    return m;
+}
+__device__ __forceinline__ float warp_max(float m)
+{
+#pragma unroll
+    for (int o = 16; o > 0; o /= 2)
+        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    return m;
+}
+// The power of two that brings a norm to 1 .. 2: 1 for none and for what is not finite.
+__device__ __forceinline__ float to_one(float x)
+{
+    const uint32_t e = __float_as_uint(x) >> 23;  // of fp16 values' norms 103 .. 147
+    return x > 0.f && e >= 1 && e <= 253 ? __uint_as_float((254u - e) << 23) : 1.f;
+}
+
 // ------------------------------------------------------------------ elementwise
 // Thread r of a warpgroup owns TMEM lane r, row 128 tile + r of the resident tile;
 // warpgroup g works on columns 32 g .. 32 g + 31 of it.
@@ -697,8 +721,10 @@ __device__ void bwd_elem(const CrossBwdArgs &a, BBars &b, BXch &xch, uint8_t *ti
     const uint32_t col = quarter * 32;
     uint32_t pos = 0;  // tiles so far
     bool ok = true;
-    const float ds_scale = b.ds_scale;
-    const uint64_t sl2x2 = f2_pack(a.sl2, a.sl2), dss = f2_pack(ds_scale, ds_scale);
+    // What dS is multiplied by: dkdv, of the piece; dq, of the row.
+    float ds_scale = 1.f;
+    uint64_t dss = f2_pack(1.f, 1.f);
+    const uint64_t sl2x2 = f2_pack(a.sl2, a.sl2);
     auto wait = [&](uint64_t &bar, uint32_t phase) {
         return mbar_wait(smem_addr(&bar), phase & 1, kWaitLimitNs, abort);
     };
@@ -710,6 +736,17 @@ __device__ void bwd_elem(const CrossBwdArgs &a, BBars &b, BXch &xch, uint8_t *ti
     // dkdv: lse and D of the query of this lane's column, fetched a tile ahead, the
     // next piece's first one too.
     float next_lse = 0.f, next_d = 0.f;
+    float next_norm = 0.f;  // dkdv: a lane's part of the next piece's; dq: the row's
+    auto fetch_norm = [&](const Piece &p) {
+        if constexpr (kF16 && kDkDv)
+            next_norm = lanes_max(a.do_max + (static_cast<long long>(p.b) * a.Hk + p.h) * a.do_parts, a.do_parts, lane);
+    };
+    auto set_scale = [&](float norm) {
+        if constexpr (kF16) {
+            ds_scale = to_one(norm);
+            dss = f2_pack(ds_scale, ds_scale);
+        }
+    };
     auto fetch = [&](const Piece &p, int t) {
         const int g = t / a.Tq, q = (t - g * a.Tq) * kTile + col + lane;
         const long long at = ((static_cast<long long>(p.b) * a.Hk + p.h) * a.G + g) * a.Nq + q;
@@ -724,6 +761,8 @@ __device__ void bwd_elem(const CrossBwdArgs &a, BBars &b, BXch &xch, uint8_t *ti
         const long long at = (static_cast<long long>(p.b) * a.Hk * a.G + p.h) * a.Nq + row;
         next_lse = row < a.Nq ? __ldcg(a.lse + at) : 0.f;
         next_d = row < a.Nq ? __ldcg(a.dvec + at) : 0.f;
+        if (kF16)
+            next_norm = row < a.Nq ? __ldcg(a.norms + at) : 0.f;
     };
     auto make_resident = [&](uint32_t k) {
         constexpr int kJobs = D / 32;  // of each tensor
@@ -755,6 +794,7 @@ __device__ void bwd_elem(const CrossBwdArgs &a, BBars &b, BXch &xch, uint8_t *ti
         tmem_wait_st();
         tc_fence_before();
         arrive(b.q_full);
+        set_scale(next_norm);
         row_nl2 = neg_lse2(next_lse);
         row_nd = -next_d * ds_scale;
     };
@@ -764,20 +804,27 @@ __device__ void bwd_elem(const CrossBwdArgs &a, BBars &b, BXch &xch, uint8_t *ti
         if (k == 0) {
             if (kDkDv) {
                 fetch(p, t0);
+                fetch_norm(p);
             } else {
                 fetch_row(p);
                 make_resident(k);
             }
         }
+        // dq: the next piece's rows have scales of their own before this one is stored.
+        const float row_scale = kDkDv ? 0.f : grad_scale(a, p.L, ds_scale);
         for (int t = t0; ok && t < t1; ++t, ++pos) {
             if constexpr (kDkDv) {
+                if (kF16 && t == t0)
+                    set_scale(warp_max(next_norm));
                 float *lse2 = xch.lse2[threadIdx.x / 32][pos & 1], *dd = xch.dd[threadIdx.x / 32][pos & 1];
                 lse2[lane] = neg_lse2(next_lse);
                 dd[lane] = -next_d * ds_scale;
                 if (t + 1 < t1)
                     fetch(p, t + 1);
-                else if (receive(b, k + 1, ok))
+                else if (receive(b, k + 1, ok)) {
                     fetch(b.pieces[(k + 1) % kPieces], b.pieces[(k + 1) % kPieces].t0);
+                    fetch_norm(b.pieces[(k + 1) % kPieces]);
+                }
                 __syncwarp();
                 ok = ok && wait(b.s_full[pos & 1], pos >> 1);
                 if (!ok)
@@ -922,7 +969,7 @@ __device__ void bwd_elem(const CrossBwdArgs &a, BBars &b, BXch &xch, uint8_t *ti
         // chunks; dq: a chunk a warpgroup.
         const bool is_dv = kDkDv && quarter < 2;
         const uint32_t acc = tmem + C::kColAcc + (kDkDv && !is_dv ? D : 0);
-        const float f = is_dv ? 1.f : grad_scale(a, p.L, ds_scale);
+        const float f = is_dv ? 1.f : kDkDv ? grad_scale(a, p.L, ds_scale) : row_scale;
         const bool whole = p.slot < 0;
         const bool zero = kDkDv && p.tile * kTile + r >= p.L;
         const long long *st = kDkDv ? (is_dv ? a.dv_st : a.dk_st) : a.dq_st;
@@ -977,33 +1024,6 @@ __device__ void bwd_elem(const CrossBwdArgs &a, BBars &b, BXch &xch, uint8_t *ti
     }
     if (!ok)
         fail(a, b, kRoleSoftmax);
-}
-
-// The power of two that scales dS: 1 in bf16; in fp16 from the blocks' largest
-// |dO|.  The whole block.
-template <bool kF16> __device__ void find_scale(const CrossBwdArgs &a, BBars &b)
-{
-    float m = 0.f;
-    if (kF16) {
-        for (int i = threadIdx.x; i < a.prep_blocks; i += kThreads)
-            m = fmaxf(m, __ldcg(a.amax + i));
-#pragma unroll
-        for (int o = 16; o > 0; o /= 2)
-            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-        if ((threadIdx.x & 31) == 0)
-            b.warp_max[threadIdx.x / 32] = m;
-        __syncthreads();
-    }
-    if (threadIdx.x == 0) {
-        b.ds_scale = 1.f;
-        if (kF16) {
-            for (int w = 0; w < kThreads / 32; ++w)
-                m = fmaxf(m, b.warp_max[w]);
-            // fp16 values are 2^-24 .. 2^16: the scale is 2^24 .. 2^-16.
-            if (m > 0.f && m < 65536.f)
-                b.ds_scale = exp2f(-floorf(log2f(m)));
-        }
-    }
 }
 
 template <int D, bool kF16, bool kDkDv>
@@ -1063,7 +1083,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         grid_dependency_wait();
         grid_launch_dependents();
     }
-    find_scale<kF16>(a, b);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -1116,75 +1135,103 @@ __device__ __forceinline__ void zero_tile(void *t, const long long *st, int b, i
 }
 
 // D of all rows, a group of lanes a row (16 bytes a lane), in the order in which
-// they lie in memory, and the block's largest |dO|.  Then zeros for what no unit
-// covers: key tiles behind a sequence's last key (all, without queries) and the
-// queries of a sequence without keys.
+// they lie in memory; in fp16 a run of a key head's rows at a time, with their norms
+// and the run's largest.  Then zeros for what no unit covers: key tiles behind a
+// sequence's last key (all, without queries) and the queries of a sequence without
+// keys.
 template <int D, bool kF16> __global__ void __launch_bounds__(kPrepThreads, 5) cross_prep_kernel(const CrossBwdArgs a)
 {
     constexpr int kLanes = D / 8, kGroup = D == 64 ? 8 : 16;
+    __shared__ float warp_max_of[kPrepThreads / 32];
     grid_dependency_wait();
     grid_launch_dependents();
     const int lane = threadIdx.x & 31, part = lane % kGroup;
     const int groups = kPrepThreads / kGroup;
-    const long long stride = static_cast<long long>(gridDim.x) * groups;
     const int Hq = a.Hk * a.G;
     const long long rows = static_cast<long long>(a.B) * Hq * a.Nq;
     const bool heads_inside = a.do_st[1] < a.do_st[2];
-    float amax = 0.f;
-    for (long long row0 = static_cast<long long>(blockIdx.x) * groups + threadIdx.x / kGroup;
-         row0 - threadIdx.x / kGroup < rows; row0 += stride * kPrepRows) {
-        uint4 x[kPrepRows], y[kPrepRows];
-        long long to[kPrepRows];
+    // bf16: one item a block, all rows in turns.
+    const long long head_rows = static_cast<long long>(a.G) * a.Nq, per = (head_rows + a.do_parts - 1) / a.do_parts;
+    const long long items = !kF16 ? gridDim.x : rows > 0 ? static_cast<long long>(a.B) * a.Hk * a.do_parts : 0;
+    for (long long item = blockIdx.x; item < items; item += gridDim.x) {
+        long long begin = item * groups, end = rows, stride = static_cast<long long>(gridDim.x) * groups, run = 0;
+        int batch = 0, key_head = 0;
+        if (kF16) {  // heads side by side
+            const long long q1 = quotient(item, a.Hk);
+            batch = static_cast<int>(quotient(q1, a.do_parts));
+            key_head = static_cast<int>(item - q1 * a.Hk);
+            const int c = static_cast<int>(q1 - static_cast<long long>(batch) * a.do_parts);
+            run = (static_cast<long long>(batch) * a.Hk + key_head) * a.do_parts + c;
+            begin = c * per;
+            end = min(begin + per, head_rows);
+            stride = groups;
+        }
+        float top = 0.f;
+        for (long long row0 = begin + threadIdx.x / kGroup; row0 - threadIdx.x / kGroup < end;
+             row0 += stride * kPrepRows) {
+            uint4 x[kPrepRows], y[kPrepRows];
+            long long to[kPrepRows];
 #pragma unroll
-        for (int i = 0; i < kPrepRows; ++i) {
-            const long long row = row0 + i * stride;
-            x[i] = y[i] = make_uint4(0, 0, 0, 0);
-            to[i] = -1;
-            if (row < rows) {
-                const int inner = heads_inside ? Hq : a.Nq, outer = heads_inside ? a.Nq : Hq;
-                const long long q1 = quotient(row, inner), q2 = quotient(q1, outer);
-                const int i0 = static_cast<int>(row - q1 * inner), i1 = static_cast<int>(q1 - q2 * outer);
-                const int h = heads_inside ? i0 : i1, n = heads_inside ? i1 : i0;
-                to[i] = (q2 * Hq + h) * a.Nq + n;
-                if (part < kLanes) {
-                    x[i] = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(a.o) + q2 * a.o_st[0] +
-                                                            h * a.o_st[1] + n * a.o_st[2] + part * 8);
-                    y[i] = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(a.dout) + q2 * a.do_st[0] +
-                                                            h * a.do_st[1] + n * a.do_st[2] + part * 8);
+            for (int i = 0; i < kPrepRows; ++i) {
+                const long long row = row0 + i * stride;
+                x[i] = y[i] = make_uint4(0, 0, 0, 0);
+                to[i] = -1;
+                if (row < end) {
+                    const int heads = kF16 ? a.G : Hq;
+                    const int inner = heads_inside ? heads : a.Nq, outer = heads_inside ? a.Nq : heads;
+                    const long long q1 = quotient(row, inner), q2 = kF16 ? batch : quotient(q1, outer);
+                    const int i0 = static_cast<int>(row - q1 * inner);
+                    const int i1 = static_cast<int>(kF16 ? q1 : q1 - q2 * outer);
+                    const int h = (heads_inside ? i0 : i1) + key_head * a.G, n = heads_inside ? i1 : i0;
+                    to[i] = (q2 * Hq + h) * a.Nq + n;
+                    if (part < kLanes) {
+                        x[i] = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(a.o) + q2 * a.o_st[0] +
+                                                                h * a.o_st[1] + n * a.o_st[2] + part * 8);
+                        y[i] = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(a.dout) +
+                                                                q2 * a.do_st[0] + h * a.do_st[1] + n * a.do_st[2] +
+                                                                part * 8);
+                    }
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < kPrepRows; ++i) {
+                const uint32_t xv[4] = {x[i].x, x[i].y, x[i].z, x[i].w}, yv[4] = {y[i].x, y[i].y, y[i].z, y[i].w};
+                float acc = 0.f, squares = 0.f;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float2 u = unpack2<kF16>(xv[j]), v = unpack2<kF16>(yv[j]);
+                    acc = fmaf(u.x, v.x, acc);
+                    acc = fmaf(u.y, v.y, acc);
+                    if (kF16)
+                        squares = fmaf(v.x, v.x, fmaf(v.y, v.y, squares));
+                }
+#pragma unroll
+                for (int o = kGroup / 2; o > 0; o /= 2) {
+                    acc += __shfl_xor_sync(0xffffffffu, acc, o);
+                    if (kF16)
+                        squares += __shfl_xor_sync(0xffffffffu, squares, o);
+                }
+                if (to[i] >= 0 && part == 0) {
+                    a.dvec[to[i]] = acc;
+                    if (kF16) {
+                        const float norm = sqrtf(squares);
+                        a.norms[to[i]] = norm;
+                        top = fmaxf(top, norm);
+                    }
                 }
             }
         }
-#pragma unroll
-        for (int i = 0; i < kPrepRows; ++i) {
-            const uint32_t xv[4] = {x[i].x, x[i].y, x[i].z, x[i].w}, yv[4] = {y[i].x, y[i].y, y[i].z, y[i].w};
-            float acc = 0.f;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const float2 u = unpack2<kF16>(xv[j]), v = unpack2<kF16>(yv[j]);
-                acc = fmaf(u.x, v.x, acc);
-                acc = fmaf(u.y, v.y, acc);
-                if (kF16)
-                    amax = fmaxf(amax, fmaxf(fabsf(v.x), fabsf(v.y)));
+        if (kF16) {
+            top = warp_max(top);
+            if (lane == 0)
+                warp_max_of[threadIdx.x / 32] = top;
+            __syncthreads();
+            if (threadIdx.x == 0) {
+                for (int w = 1; w < kPrepThreads / 32; ++w)
+                    top = fmaxf(top, warp_max_of[w]);
+                a.do_max[run] = top;
             }
-#pragma unroll
-            for (int o = kGroup / 2; o > 0; o /= 2)
-                acc += __shfl_xor_sync(0xffffffffu, acc, o);
-            if (to[i] >= 0 && part == 0)
-                a.dvec[to[i]] = acc;
-        }
-    }
-    if (kF16) {
-        __shared__ float warp_max[kPrepThreads / 32];
-#pragma unroll
-        for (int o = 16; o > 0; o /= 2)
-            amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-        if (lane == 0)
-            warp_max[threadIdx.x / 32] = amax;
-        __syncthreads();
-        if (threadIdx.x == 0) {
-            for (int w = 1; w < kPrepThreads / 32; ++w)
-                amax = fmaxf(amax, warp_max[w]);
-            a.amax[blockIdx.x] = amax;
+            __syncthreads();
         }
     }
     if (a.kv_len == nullptr && a.Nk > 0 && rows > 0)
@@ -1233,18 +1280,11 @@ template <int D, bool kF16> __global__ void __launch_bounds__(kMergeThreads) cro
     const long long *st = which == 2 ? a.dq_st : which == 1 ? a.dk_st : a.dv_st;
     uint16_t *out = static_cast<uint16_t *>(which == 2 ? a.dq : which == 1 ? a.dk : a.dv);
     const int keys = clamp_len(a, me.x), rows = which == 2 ? a.Nq : a.Nk, L = which == 2 ? a.Nq : keys;
-    float f = 1.f;
-    if (which != 0) {
-        float m = 0.f;
-        if (kF16) {
-            for (int i = threadIdx.x & 31; i < a.prep_blocks; i += 32)
-                m = fmaxf(m, a.amax[i]);
-#pragma unroll
-            for (int o = 16; o > 0; o /= 2)
-                m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-        }
-        f = grad_scale(a, keys, m > 0.f && m < 65536.f ? exp2f(-floorf(log2f(m))) : 1.f);
-    }
+    const float *norms = a.norms + (static_cast<long long>(me.x) * a.Hk * a.G + me.y) * a.Nq;
+    float scale = 1.f;
+    if (kF16 && which == 1)
+        scale = to_one(warp_max(lanes_max(a.do_max + (static_cast<long long>(me.x) * a.Hk + me.y) * a.do_parts,
+                                          a.do_parts, threadIdx.x & 31)));
     constexpr int kVecs = D / 4;
     for (int at = threadIdx.x; at < kMergeRows * kVecs; at += kMergeThreads) {
         const int r = r0 + at / kVecs, v = at % kVecs, row = me.z * kTile + r;
@@ -1260,6 +1300,9 @@ template <int D, bool kF16> __global__ void __launch_bounds__(kMergeThreads) cro
             const float4 y = slot(k);
             x = make_float4(x.x + y.x, x.y + y.y, x.z + y.z, x.w + y.w);
         }
+        if (kF16 && which == 2)
+            scale = to_one(norms[row]);
+        const float f = which == 0 ? 1.f : grad_scale(a, keys, scale);
         const uint2 packed = row < L ? make_uint2(pack2<kF16>(x.x * f, x.y * f), pack2<kF16>(x.z * f, x.w * f))
                                      : make_uint2(0, 0);
         *reinterpret_cast<uint2 *>(out + me.x * st[0] + me.y * st[1] + row * st[2] + v * 4) = packed;
@@ -1312,8 +1355,8 @@ cudaError_t launch(const CrossBwdArgs &args, const CrossBwdMaps &m, cudaStream_t
     constexpr int kRows = kPrepThreads / (D == 64 ? 8 : 16) * kPrepRows;  // of a block
     const long long rows = static_cast<long long>(a.B) * a.Hk * a.G * a.Nq;
     const long long blocks = (rows + kRows - 1) / kRows;
-    // The zeros of short sequences want hands, too.
-    a.prep_blocks = static_cast<int>(a.kv_len != nullptr || a.Nk == 0 || rows == 0 || blocks > kPrepBlocks ? kPrepBlocks
+    // The zeros of short sequences, and fp16's runs, want hands, too.
+    a.prep_blocks = static_cast<int>(kF16 || a.kv_len != nullptr || a.Nk == 0 || rows == 0 || blocks > kPrepBlocks ? kPrepBlocks
                                      : blocks > 0                               ? blocks
                                                                                 : 1);
     const bool whole = whole_units<D>(a);
@@ -1338,7 +1381,15 @@ template <int D> cudaError_t launch_typed(const CrossBwdArgs &a, const CrossBwdM
 
 CrossBwdSizes cross_bwd_sizes(int d, int num_sms)
 {
-    return CrossBwdSizes{kPrepBlocks, 2 * num_sms, 2LL * num_sms * 2 * kTile * d, 2LL * num_sms * kTile * d};
+    return CrossBwdSizes{2 * num_sms, 2LL * num_sms * 2 * kTile * d, 2LL * num_sms * kTile * d};
+}
+
+// Two runs a prep block together, of 64 rows at least; a warp of the passes reads one
+// key head's at most 256 of them where its piece starts.
+int cross_bwd_parts(long long heads, long long rows)
+{
+    const long long want = heads > 0 ? (2 * kPrepBlocks + heads - 1) / heads : 1;
+    return static_cast<int>(std::max(std::min({want, (rows + 63) / 64, 256LL}), 1LL));
 }
 
 cudaError_t launch_cross_bwd(const CrossBwdArgs &a, const CrossBwdMaps &m, cudaStream_t stream)

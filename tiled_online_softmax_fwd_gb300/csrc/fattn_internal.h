@@ -265,25 +265,29 @@ struct CrossBwdArgs {
     const float *lse;
     const int *kv_len;  // may be null
     void *dq, *dk, *dv;
-    // Workspace: D [B Hq Nq], the prep blocks' largest |dO|, where the CTAs of
-    // the two passes start [2][grid], partial sums of two units a CTA.
-    float *dvec, *amax, *ws_kv, *ws_q;
+    // Workspace: D [B Hq Nq]; in fp16 the norms of dO's rows [B Hq Nq] and the largest
+    // of each of do_parts runs of a key head's rows [B Hk][do_parts]; where the CTAs
+    // of the two passes start [2][grid], partial sums of two units a CTA.
+    float *dvec, *norms, *do_max, *ws_kv, *ws_q;
     int4 *starts;
     uint32_t *status;
     long long q_st[3], o_st[3], do_st[3], dq_st[3], dk_st[3], dv_st[3];
     int B, Hk, G, Nq, Nk, Tq, d, f16, grid;
     float scale, sl2;
+    int do_parts;
     int prep_blocks, snap;  // filled in by the launch
 };
 // Maps (d, rows, heads, B) of q, k, v and dO, box (64, 128, 1, 1).
 struct CrossBwdMaps {
     CUtensorMap q, k, v, dout;
 };
-// Sizes of a call's workspace: elements of amax, starts, ws_kv and ws_q.
+// Sizes of a call's workspace: elements of starts, ws_kv and ws_q; and the runs
+// into which `rows` rows of each of `heads` key heads are cut.
 struct CrossBwdSizes {
-    long long amax, starts, kv, q;
+    long long starts, kv, q;
 };
 CrossBwdSizes cross_bwd_sizes(int d, int num_sms);
+int cross_bwd_parts(long long heads, long long rows);
 cudaError_t launch_cross_bwd(const CrossBwdArgs &a, const CrossBwdMaps &m, cudaStream_t stream);
 
 }  // namespace fattn
