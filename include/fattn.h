@@ -699,7 +699,8 @@ fattn_status_t attn_fwd_cross(const void *q, const void *k, const void *v, const
  * is constant.  What lies behind a sequence's last key in k and v may be anything, NaN
  * included.  P and dS are rounded to the inputs' type, dS in fp16 after a scaling
  * by a power of two that follows from |dout| of the query (for dk, of all queries of
- * the key head's, in one sequence); sums are fp32.  An
+ * the key head's, in one sequence) and the largest |v| that it sees, with which no dS
+ * is beyond fp16; sums are fp32.  An
  * output shares no element with an input or another output.  Sums are taken in an
  * order that depends on the shapes and lengths alone: equal calls give equal bits.
  * Up to four kernels are enqueued; the lengths are read when they run.  Errors as

@@ -2208,18 +2208,20 @@ fattn_status_t attn_fwd_cross(const void *q, const void *k, const void *v, const
 
 // Workspace of the gradients of cross attention (256-byte aligned each).
 struct CrossBwdWs {
-    int do_parts;
-    size_t norms, do_max, starts, kv, q, bytes;
+    int do_parts, v_parts;
+    size_t norms, do_max, v_max, starts, kv, q, bytes;
 };
-static CrossBwdWs cross_bwd_ws(int B, int Hq, int Hk, int Nq, int d, int num_sms)
+static CrossBwdWs cross_bwd_ws(int B, int Hq, int Hk, int Nq, int Nk, int d, int num_sms)
 {
     const fattn::CrossBwdSizes n = fattn::cross_bwd_sizes(d, num_sms);
     const long long heads = static_cast<long long>(B) * Hk, head_rows = Hk > 0 ? static_cast<long long>(Hq / Hk) * Nq : 0;
     CrossBwdWs w;
     w.do_parts = fattn::cross_bwd_parts(heads, head_rows);
+    w.v_parts = fattn::cross_bwd_parts(heads, Nk);
     w.norms = align_up(static_cast<size_t>(heads) * head_rows * 4, kWsAlign);
     w.do_max = align_up(2 * w.norms, kWsAlign);
-    w.starts = align_up(w.do_max + static_cast<size_t>(heads) * w.do_parts * 4, kWsAlign);
+    w.v_max = align_up(w.do_max + static_cast<size_t>(heads) * w.do_parts * 4, kWsAlign);
+    w.starts = align_up(w.v_max + static_cast<size_t>(heads) * w.v_parts * 4, kWsAlign);
     w.kv = align_up(w.starts + n.starts * sizeof(int4), kWsAlign);
     w.q = align_up(w.kv + n.kv * 4, kWsAlign);
     w.bytes = w.q + n.q * 4;
@@ -2232,7 +2234,7 @@ size_t attn_bwd_cross_workspace_size(int B, int Hq, int Hk, int Nq, int Nk, int 
     DeviceInfo info;
     if (check_cross(B, Hq, Hk, Nq, Nk, d, 1.f, 0) != FATTN_OK || current_device(&dev, &info) != FATTN_OK)
         return 0;
-    return cross_bwd_ws(B, Hq, Hk, Nq, d, info.num_sms).bytes;
+    return cross_bwd_ws(B, Hq, Hk, Nq, Nk, d, info.num_sms).bytes;
 }
 
 fattn_status_t attn_bwd_cross(const void *q, const void *k, const void *v, const void *o, const float *lse,
@@ -2290,7 +2292,7 @@ fattn_status_t attn_bwd_cross(const void *q, const void *k, const void *v, const
         bufs[3 + i] = used[i] ? ptr[i] : nullptr;
     if ((s = check_buffers(bufs, &dev, &info)) != FATTN_OK)
         return s;
-    const CrossBwdWs ws = cross_bwd_ws(B, Hq, Hk, Nq, d, info.num_sms);
+    const CrossBwdWs ws = cross_bwd_ws(B, Hq, Hk, Nq, Nk, d, info.num_sms);
     if (!workspace || !aligned16(workspace) || workspace_bytes < ws.bytes ||
         (lse_bytes && overlap(workspace, ws.bytes, lse, lse_bytes)) ||
         (len_bytes && overlap(workspace, ws.bytes, kv_len, len_bytes)))
@@ -2316,6 +2318,7 @@ fattn_status_t attn_bwd_cross(const void *q, const void *k, const void *v, const
     }
     uint8_t *base = static_cast<uint8_t *>(workspace);
     a.q = q;
+    a.v = v;
     a.o = o;
     a.dout = dout;
     a.lse = lse;
@@ -2326,11 +2329,14 @@ fattn_status_t attn_bwd_cross(const void *q, const void *k, const void *v, const
     a.dvec = reinterpret_cast<float *>(base);
     a.norms = reinterpret_cast<float *>(base + ws.norms);
     a.do_max = reinterpret_cast<float *>(base + ws.do_max);
+    a.v_max = reinterpret_cast<float *>(base + ws.v_max);
     a.do_parts = ws.do_parts;
+    a.v_parts = ws.v_parts;
     a.starts = reinterpret_cast<int4 *>(base + ws.starts);
     a.ws_kv = reinterpret_cast<float *>(base + ws.kv);
     a.ws_q = reinterpret_cast<float *>(base + ws.q);
     copy_strides(a.q_st, rows[0]);
+    copy_strides(a.v_st, rows[5]);
     copy_strides(a.o_st, rows[1]);
     copy_strides(a.do_st, rows[2]);
     copy_strides(a.dq_st, rows[3]);

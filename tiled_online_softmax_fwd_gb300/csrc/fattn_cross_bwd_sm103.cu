@@ -7,7 +7,8 @@
 //   dV = sum_h P^T dO,     dP = dO V^T,   dS = P o (dP - D),
 //   dQ = scale dS K,       dK = scale sum_h dS^T Q.
 // Four kernels, each started under the tail of the one before:
-//   prep     D, the norms of dO's rows (fp16), and zeros for key tiles without keys
+//   prep     D, the norms of dO's rows and V's (fp16), and zeros for key tiles without
+//            keys
 //   dkdv     a unit is a tile of 128 keys of one (sequence, key head).  K, V
 //            stay; the tiles of Q and dO of its G query heads stream by: S^T =
 //            K Q^T and dP^T = V dO^T, keys on TMEM lanes, P^T over S^T, then dV
@@ -37,10 +38,12 @@
 // and end: 2 sequences, 16 heads, 4096 queries, up to 154 keys 57 us, 1.2 TB/s.
 //
 // Types.  P and dS enter the second products in the inputs' type.  dS in fp16
-// is scaled by a power of two that brings the norm of dO's row to 1 .. 2, so that
-// small gradients keep their digits whatever stands beside them; for dK, whose sums
-// go over the rows, the largest norm of the key head's.  The sums are scaled back
-// in fp32.
+// is scaled by a power of two that follows from the norm of dO's row (for dK, whose
+// sums go over the rows, the largest of the key head's) and the largest norm of a row
+// of V before the sequence's end: |dP| is at most their product N, and P (1 - P) at
+// most 1/4, so |dS| is at most N / 2.  N is brought to 2^15 .. 2^16, where no dS is
+// infinite and small ones keep their digits whatever stands beside them.  The sums
+// are scaled back in fp32.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <stdint.h>
@@ -699,11 +702,12 @@ __device__ __forceinline__ float warp_max(float m)
         m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
     return m;
 }
-// The power of two that brings a norm to 1 .. 2: 1 for none and for what is not finite.
-__device__ __forceinline__ float to_one(float x)
+// The power of two that brings the product of two norms to 2^15 .. 2^16: 1 where it
+// is zero or not finite.
+__device__ __forceinline__ float scale_of(float x)
 {
-    const uint32_t e = __float_as_uint(x) >> 23;  // of fp16 values' norms 103 .. 147
-    return x > 0.f && e >= 1 && e <= 253 ? __uint_as_float((254u - e) << 23) : 1.f;
+    const uint32_t e = __float_as_uint(x) >> 23;  // of fp16 rows' norms 79 .. 167
+    return x > 0.f && e >= 16 && e <= 253 ? __uint_as_float((269u - e) << 23) : 1.f;
 }
 
 // ------------------------------------------------------------------ elementwise
@@ -736,14 +740,19 @@ __device__ void bwd_elem(const CrossBwdArgs &a, BBars &b, BXch &xch, uint8_t *ti
     // dkdv: lse and D of the query of this lane's column, fetched a tile ahead, the
     // next piece's first one too.
     float next_lse = 0.f, next_d = 0.f;
-    float next_norm = 0.f;  // dkdv: a lane's part of the next piece's; dq: the row's
+    float next_norm = 0.f;  // of dO; dkdv: a lane's part of the next piece's; dq: the row's
+    float next_v = 0.f;     // of V, a lane's part
     auto fetch_norm = [&](const Piece &p) {
-        if constexpr (kF16 && kDkDv)
-            next_norm = lanes_max(a.do_max + (static_cast<long long>(p.b) * a.Hk + p.h) * a.do_parts, a.do_parts, lane);
-    };
-    auto set_scale = [&](float norm) {
         if constexpr (kF16) {
-            ds_scale = to_one(norm);
+            const long long head = static_cast<long long>(p.b) * a.Hk + (kDkDv ? p.h : p.h / a.G);
+            next_v = lanes_max(a.v_max + head * a.v_parts, a.v_parts, lane);
+            if (kDkDv)
+                next_norm = lanes_max(a.do_max + head * a.do_parts, a.do_parts, lane);
+        }
+    };
+    auto set_scale = [&]() {
+        if constexpr (kF16) {
+            ds_scale = scale_of((kDkDv ? warp_max(next_norm) : next_norm) * warp_max(next_v));
             dss = f2_pack(ds_scale, ds_scale);
         }
     };
@@ -763,6 +772,7 @@ __device__ void bwd_elem(const CrossBwdArgs &a, BBars &b, BXch &xch, uint8_t *ti
         next_d = row < a.Nq ? __ldcg(a.dvec + at) : 0.f;
         if (kF16)
             next_norm = row < a.Nq ? __ldcg(a.norms + at) : 0.f;
+        fetch_norm(p);
     };
     auto make_resident = [&](uint32_t k) {
         constexpr int kJobs = D / 32;  // of each tensor
@@ -794,7 +804,7 @@ __device__ void bwd_elem(const CrossBwdArgs &a, BBars &b, BXch &xch, uint8_t *ti
         tmem_wait_st();
         tc_fence_before();
         arrive(b.q_full);
-        set_scale(next_norm);
+        set_scale();
         row_nl2 = neg_lse2(next_lse);
         row_nd = -next_d * ds_scale;
     };
@@ -815,7 +825,7 @@ __device__ void bwd_elem(const CrossBwdArgs &a, BBars &b, BXch &xch, uint8_t *ti
         for (int t = t0; ok && t < t1; ++t, ++pos) {
             if constexpr (kDkDv) {
                 if (kF16 && t == t0)
-                    set_scale(warp_max(next_norm));
+                    set_scale();
                 float *lse2 = xch.lse2[threadIdx.x / 32][pos & 1], *dd = xch.dd[threadIdx.x / 32][pos & 1];
                 lse2[lane] = neg_lse2(next_lse);
                 dd[lane] = -next_d * ds_scale;
@@ -1136,7 +1146,7 @@ __device__ __forceinline__ void zero_tile(void *t, const long long *st, int b, i
 
 // D of all rows, a group of lanes a row (16 bytes a lane), in the order in which
 // they lie in memory; in fp16 a run of a key head's rows at a time, with their norms
-// and the run's largest.  Then zeros for what no unit covers: key tiles behind a
+// and the run's largest, and the same of V's rows.  Then zeros for what no unit covers: key tiles behind a
 // sequence's last key (all, without queries) and the queries of a sequence without
 // keys.
 template <int D, bool kF16> __global__ void __launch_bounds__(kPrepThreads, 5) cross_prep_kernel(const CrossBwdArgs a)
@@ -1150,6 +1160,18 @@ template <int D, bool kF16> __global__ void __launch_bounds__(kPrepThreads, 5) c
     const int Hq = a.Hk * a.G;
     const long long rows = static_cast<long long>(a.B) * Hq * a.Nq;
     const bool heads_inside = a.do_st[1] < a.do_st[2];
+    auto block_max = [&](float x, float *to) {
+        x = warp_max(x);
+        if (lane == 0)
+            warp_max_of[threadIdx.x / 32] = x;
+        __syncthreads();
+        if (threadIdx.x == 0) {
+            for (int w = 1; w < kPrepThreads / 32; ++w)
+                x = fmaxf(x, warp_max_of[w]);
+            *to = x;
+        }
+        __syncthreads();
+    };
     // bf16: one item a block, all rows in turns.
     const long long head_rows = static_cast<long long>(a.G) * a.Nq, per = (head_rows + a.do_parts - 1) / a.do_parts;
     const long long items = !kF16 ? gridDim.x : rows > 0 ? static_cast<long long>(a.B) * a.Hk * a.do_parts : 0;
@@ -1221,17 +1243,46 @@ template <int D, bool kF16> __global__ void __launch_bounds__(kPrepThreads, 5) c
                 }
             }
         }
-        if (kF16) {
-            top = warp_max(top);
-            if (lane == 0)
-                warp_max_of[threadIdx.x / 32] = top;
-            __syncthreads();
-            if (threadIdx.x == 0) {
-                for (int w = 1; w < kPrepThreads / 32; ++w)
-                    top = fmaxf(top, warp_max_of[w]);
-                a.do_max[run] = top;
+        if (kF16)
+            block_max(top, a.do_max + run);
+    }
+    if constexpr (kF16) {
+        // Rows of V before the sequence's end, runs as above, the first ones to the last
+        // blocks, which have had fewer of dO's.
+        const long long v_items = a.Nk > 0 ? static_cast<long long>(a.B) * a.Hk * a.v_parts : 0;
+        const int v_per = (a.Nk + a.v_parts - 1) / a.v_parts;
+        for (long long item = gridDim.x - 1 - blockIdx.x; item < v_items; item += gridDim.x) {
+            const long long q1 = quotient(item, a.Hk);
+            const int b = static_cast<int>(quotient(q1, a.v_parts)), h = static_cast<int>(item - q1 * a.Hk);
+            const int c = static_cast<int>(q1 - static_cast<long long>(b) * a.v_parts);
+            const long long begin = static_cast<long long>(c) * v_per;
+            const long long end = min(begin + v_per, static_cast<long long>(clamp_len(a, b)));
+            const uint16_t *v = static_cast<const uint16_t *>(a.v) + b * a.v_st[0] + h * a.v_st[1] + part * 8;
+            float top = 0.f;
+            for (long long row0 = begin + threadIdx.x / kGroup; row0 - threadIdx.x / kGroup < end; row0 += 4 * groups) {
+                uint4 x[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    x[i] = make_uint4(0, 0, 0, 0);
+                    if (row0 + i * groups < end && part < kLanes)
+                        x[i] = *reinterpret_cast<const uint4 *>(v + (row0 + i * groups) * a.v_st[2]);
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+                    float squares = 0.f;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const float2 f = unpack2<kF16>(w[j]);
+                        squares = fmaf(f.x, f.x, fmaf(f.y, f.y, squares));
+                    }
+#pragma unroll
+                    for (int o = kGroup / 2; o > 0; o /= 2)
+                        squares += __shfl_xor_sync(0xffffffffu, squares, o);
+                    top = fmaxf(top, sqrtf(squares));
+                }
             }
-            __syncthreads();
+            block_max(top, a.v_max + (static_cast<long long>(b) * a.Hk + h) * a.v_parts + c);
         }
     }
     if (a.kv_len == nullptr && a.Nk > 0 && rows > 0)
@@ -1281,10 +1332,14 @@ template <int D, bool kF16> __global__ void __launch_bounds__(kMergeThreads) cro
     uint16_t *out = static_cast<uint16_t *>(which == 2 ? a.dq : which == 1 ? a.dk : a.dv);
     const int keys = clamp_len(a, me.x), rows = which == 2 ? a.Nq : a.Nk, L = which == 2 ? a.Nq : keys;
     const float *norms = a.norms + (static_cast<long long>(me.x) * a.Hk * a.G + me.y) * a.Nq;
-    float scale = 1.f;
-    if (kF16 && which == 1)
-        scale = to_one(warp_max(lanes_max(a.do_max + (static_cast<long long>(me.x) * a.Hk + me.y) * a.do_parts,
-                                          a.do_parts, threadIdx.x & 31)));
+    float scale = 1.f, v_norm = 0.f;
+    if (kF16 && which != 0) {
+        const long long head = static_cast<long long>(me.x) * a.Hk + (which == 1 ? me.y : me.y / a.G);
+        v_norm = warp_max(lanes_max(a.v_max + head * a.v_parts, a.v_parts, threadIdx.x & 31));
+        if (which == 1)
+            scale = scale_of(
+                warp_max(lanes_max(a.do_max + head * a.do_parts, a.do_parts, threadIdx.x & 31)) * v_norm);
+    }
     constexpr int kVecs = D / 4;
     for (int at = threadIdx.x; at < kMergeRows * kVecs; at += kMergeThreads) {
         const int r = r0 + at / kVecs, v = at % kVecs, row = me.z * kTile + r;
@@ -1301,7 +1356,7 @@ template <int D, bool kF16> __global__ void __launch_bounds__(kMergeThreads) cro
             x = make_float4(x.x + y.x, x.y + y.y, x.z + y.z, x.w + y.w);
         }
         if (kF16 && which == 2)
-            scale = to_one(norms[row]);
+            scale = scale_of(norms[row] * v_norm);
         const float f = which == 0 ? 1.f : grad_scale(a, keys, scale);
         const uint2 packed = row < L ? make_uint2(pack2<kF16>(x.x * f, x.y * f), pack2<kF16>(x.z * f, x.w * f))
                                      : make_uint2(0, 0);
