@@ -37,11 +37,13 @@
 // elementwise warps, shortened by a second S or dP; with few tiles a unit its start
 // and end: 2 sequences, 16 heads, 4096 queries, up to 154 keys 57 us, 1.2 TB/s.
 //
-// Types.  P and dS enter the second products in the inputs' type.  dS in fp16
+// Types.  P and dS enter the second products in the inputs' type.  P in fp16 is
+// multiplied by 2^15, in its exponent and so at no cost: with 10^5 keys it is below fp16's
+// normal numbers, where dV would lose digits.  dS = P (dP - D) has that factor, and
 // is scaled by a power of two that follows from the norm of dO's row (for dK, whose
 // sums go over the rows, the largest of the key head's) and the largest norm of a row
 // of V before the sequence's end: |dP| is at most their product N, and P (1 - P) at
-// most 1/4, so |dS| is at most N / 2.  N is brought to 2^15 .. 2^16, where no dS is
+// most 1/4, so |dS| is at most N / 2.  N is brought to 1 .. 2, so that no dS is
 // infinite and small ones keep their digits whatever stands beside them.  The sums
 // are scaled back in fp32.
 #include <cuda_bf16.h>
@@ -647,11 +649,15 @@ __device__ void bwd_mma(const CrossBwdArgs &a, BBars &b, uint32_t smem, uint32_t
     mbar_wait(smem_addr(&b.drain), 0, kWaitLimitNs, nullptr);
 }
 
-// -lse log2(e), with which P = 2^(s scale log2(e) + it); of a row that saw no
-// key (lse = -inf) -inf, so that its P is 0.
-__device__ __forceinline__ float neg_lse2(float lse)
+// What fp16's P is multiplied by (see Types): P is at most 1, and 2^16 too large.
+template <bool kF16> constexpr float kPExponent = kF16 ? 15.f : 0.f;
+template <bool kF16> constexpr float kPInverse = kF16 ? 1.f / 32768.f : 1.f;
+
+// -lse log2(e), with which P = 2^(s scale log2(e) + it), and P's factor; of a row
+// that saw no key (lse = -inf) -inf, so that its P is 0.
+template <bool kF16> __device__ __forceinline__ float neg_lse2(float lse)
 {
-    return lse == -INFINITY ? lse : -lse * kLog2e;
+    return lse == -INFINITY ? lse : kF16 ? fmaf(-lse, kLog2e, kPExponent<kF16>) : -lse * kLog2e;
 }
 
 // Four lanes' 16-byte pieces change places: v[j] of lane i of four becomes v[i]
@@ -681,9 +687,9 @@ __device__ __forceinline__ void transpose4(uint4 (&v)[4], int lane)
 // What dQ's and dK's sums are multiplied by.  With one key P is 1 whatever q and k
 // are, and dS is zero: D, from o in 16 bits and in another order of sums, would leave
 // some 1e-6 |dO| |v| of it.
-__device__ __forceinline__ float grad_scale(const CrossBwdArgs &a, int keys, float ds_scale)
+template <bool kF16> __device__ __forceinline__ float grad_scale(const CrossBwdArgs &a, int keys, float ds_scale)
 {
-    return keys == 1 ? 0.f : a.scale / ds_scale;
+    return keys == 1 ? 0.f : a.scale / ds_scale * kPInverse<kF16>;
 }
 
 // The largest of some values, NaN aside, each lane some of them; and of the lanes'.
@@ -702,12 +708,12 @@ __device__ __forceinline__ float warp_max(float m)
         m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
     return m;
 }
-// The power of two that brings the product of two norms to 2^15 .. 2^16: 1 where it
-// is zero or not finite.
+// The power of two that brings the product of two norms to 1 .. 2: 1 where it is zero
+// or not finite.
 __device__ __forceinline__ float scale_of(float x)
 {
     const uint32_t e = __float_as_uint(x) >> 23;  // of fp16 rows' norms 79 .. 167
-    return x > 0.f && e >= 16 && e <= 253 ? __uint_as_float((269u - e) << 23) : 1.f;
+    return x > 0.f && e >= 1 && e <= 253 ? __uint_as_float((254u - e) << 23) : 1.f;
 }
 
 // ------------------------------------------------------------------ elementwise
@@ -805,7 +811,7 @@ __device__ void bwd_elem(const CrossBwdArgs &a, BBars &b, BXch &xch, uint8_t *ti
         tc_fence_before();
         arrive(b.q_full);
         set_scale();
-        row_nl2 = neg_lse2(next_lse);
+        row_nl2 = neg_lse2<kF16>(next_lse);
         row_nd = -next_d * ds_scale;
     };
     for (uint32_t k = 0; receive(b, k, ok); ++k) {
@@ -821,13 +827,13 @@ __device__ void bwd_elem(const CrossBwdArgs &a, BBars &b, BXch &xch, uint8_t *ti
             }
         }
         // dq: the next piece's rows have scales of their own before this one is stored.
-        const float row_scale = kDkDv ? 0.f : grad_scale(a, p.L, ds_scale);
+        const float row_scale = kDkDv ? 0.f : grad_scale<kF16>(a, p.L, ds_scale);
         for (int t = t0; ok && t < t1; ++t, ++pos) {
             if constexpr (kDkDv) {
                 if (kF16 && t == t0)
                     set_scale();
                 float *lse2 = xch.lse2[threadIdx.x / 32][pos & 1], *dd = xch.dd[threadIdx.x / 32][pos & 1];
-                lse2[lane] = neg_lse2(next_lse);
+                lse2[lane] = neg_lse2<kF16>(next_lse);
                 dd[lane] = -next_d * ds_scale;
                 if (t + 1 < t1)
                     fetch(p, t + 1);
@@ -979,7 +985,7 @@ __device__ void bwd_elem(const CrossBwdArgs &a, BBars &b, BXch &xch, uint8_t *ti
         // chunks; dq: a chunk a warpgroup.
         const bool is_dv = kDkDv && quarter < 2;
         const uint32_t acc = tmem + C::kColAcc + (kDkDv && !is_dv ? D : 0);
-        const float f = is_dv ? 1.f : kDkDv ? grad_scale(a, p.L, ds_scale) : row_scale;
+        const float f = is_dv ? kPInverse<kF16> : kDkDv ? grad_scale<kF16>(a, p.L, ds_scale) : row_scale;
         const bool whole = p.slot < 0;
         const bool zero = kDkDv && p.tile * kTile + r >= p.L;
         const long long *st = kDkDv ? (is_dv ? a.dv_st : a.dk_st) : a.dq_st;
@@ -1357,7 +1363,7 @@ template <int D, bool kF16> __global__ void __launch_bounds__(kMergeThreads) cro
         }
         if (kF16 && which == 2)
             scale = scale_of(norms[row] * v_norm);
-        const float f = which == 0 ? 1.f : grad_scale(a, keys, scale);
+        const float f = which == 0 ? kPInverse<kF16> : grad_scale<kF16>(a, keys, scale);
         const uint2 packed = row < L ? make_uint2(pack2<kF16>(x.x * f, x.y * f), pack2<kF16>(x.z * f, x.w * f))
                                      : make_uint2(0, 0);
         *reinterpret_cast<uint2 *>(out + me.x * st[0] + me.y * st[1] + row * st[2] + v * 4) = packed;
