@@ -697,7 +697,8 @@ fattn_status_t attn_fwd_cross(const void *q, const void *k, const void *v, const
  * last key, dq of a sequence without keys, and dk and dv without queries are
  * zeros; so are dq and dk of a sequence of one key (finite inputs), whose softmax
  * is constant.  What lies behind a sequence's last key in k and v may be anything, NaN
- * included.  P and dS are rounded to the inputs' type, in fp16 P after a scaling by
+ * included.  With at most 16 keys D is worked out as their sum of P (dout . v),
+ * without o's rounding.  P and dS are rounded to the inputs' type, in fp16 P after a scaling by
  * 2^15 (of many keys it is below fp16's normal numbers), dS by that and
  * by a power of two that follows from |dout| of the query (for dk, of all queries of
  * the key head's, in one sequence) and the largest |v| that it sees, with which no dS

@@ -2209,7 +2209,7 @@ fattn_status_t attn_fwd_cross(const void *q, const void *k, const void *v, const
 // Workspace of the gradients of cross attention (256-byte aligned each).
 struct CrossBwdWs {
     int do_parts, v_parts;
-    size_t norms, do_max, v_max, starts, kv, q, bytes;
+    size_t dfew, norms, do_max, v_max, starts, kv, q, bytes;
 };
 static CrossBwdWs cross_bwd_ws(int B, int Hq, int Hk, int Nq, int Nk, int d, int num_sms)
 {
@@ -2218,8 +2218,9 @@ static CrossBwdWs cross_bwd_ws(int B, int Hq, int Hk, int Nq, int Nk, int d, int
     CrossBwdWs w;
     w.do_parts = fattn::cross_bwd_parts(heads, head_rows);
     w.v_parts = fattn::cross_bwd_parts(heads, Nk);
-    w.norms = align_up(static_cast<size_t>(heads) * head_rows * 4, kWsAlign);
-    w.do_max = align_up(2 * w.norms, kWsAlign);
+    w.dfew = align_up(static_cast<size_t>(heads) * head_rows * 4, kWsAlign);  // D before it
+    w.norms = 2 * w.dfew;
+    w.do_max = 3 * w.dfew;
     w.v_max = align_up(w.do_max + static_cast<size_t>(heads) * w.do_parts * 4, kWsAlign);
     w.starts = align_up(w.v_max + static_cast<size_t>(heads) * w.v_parts * 4, kWsAlign);
     w.kv = align_up(w.starts + n.starts * sizeof(int4), kWsAlign);
@@ -2318,6 +2319,7 @@ fattn_status_t attn_bwd_cross(const void *q, const void *k, const void *v, const
     }
     uint8_t *base = static_cast<uint8_t *>(workspace);
     a.q = q;
+    a.k = k;
     a.v = v;
     a.o = o;
     a.dout = dout;
@@ -2327,6 +2329,7 @@ fattn_status_t attn_bwd_cross(const void *q, const void *k, const void *v, const
     a.dk = dk;
     a.dv = dv;
     a.dvec = reinterpret_cast<float *>(base);
+    a.dfew = reinterpret_cast<float *>(base + ws.dfew);
     a.norms = reinterpret_cast<float *>(base + ws.norms);
     a.do_max = reinterpret_cast<float *>(base + ws.do_max);
     a.v_max = reinterpret_cast<float *>(base + ws.v_max);
@@ -2336,6 +2339,7 @@ fattn_status_t attn_bwd_cross(const void *q, const void *k, const void *v, const
     a.ws_kv = reinterpret_cast<float *>(base + ws.kv);
     a.ws_q = reinterpret_cast<float *>(base + ws.q);
     copy_strides(a.q_st, rows[0]);
+    copy_strides(a.k_st, rows[4]);
     copy_strides(a.v_st, rows[5]);
     copy_strides(a.o_st, rows[1]);
     copy_strides(a.do_st, rows[2]);

@@ -89,6 +89,14 @@ template <int D> constexpr int kMergeCost = D == 64 ? 6 : 3;
 // little, and the passes in turn need no guess of their steps' lengths.
 constexpr int kStepKv = 4, kStepQ = 3, kTogether = 32;
 
+// With few keys the rounding of o is the larger part of the gradients' error: D = dO . o
+// is off by h |dO| |o|, h half a step of the type, where dS = P (dP - D) is a
+// difference that o's mean over many keys does not enter.  There D is summed up from
+// P and dP in 32 bits instead.  Error of bf16 dQ in the norm (d = 64, the roundings
+// alone): 2 keys 0.0023, from o 0.0041; 4 keys 0.0023 and 0.0029; 16 keys 0.0024 and
+// 0.0025; from 24 keys on the two are alike.
+constexpr int kFewKeys = 16;
+
 template <int D, bool kDkDv> struct BCfg {
     static constexpr int kChunks = (D + 63) / 64;
     static constexpr uint32_t kTileBytes = kChunks * kChunkBytes;  // one [128][D] tile
@@ -766,7 +774,7 @@ __device__ void bwd_elem(const CrossBwdArgs &a, BBars &b, BXch &xch, uint8_t *ti
         const int g = t / a.Tq, q = (t - g * a.Tq) * kTile + col + lane;
         const long long at = ((static_cast<long long>(p.b) * a.Hk + p.h) * a.G + g) * a.Nq + q;
         next_lse = q < a.Nq ? __ldcg(a.lse + at) : 0.f;
-        next_d = q < a.Nq ? __ldcg(a.dvec + at) : 0.f;
+        next_d = q < a.Nq ? __ldcg((p.L <= kFewKeys ? a.dfew : a.dvec) + at) : 0.f;
     };
     // dq: the k-th piece's Q and dO into TMEM, 32 elements of a row a job, a lane a
     // row; and the row's lse and D, fetched before.
@@ -775,7 +783,7 @@ __device__ void bwd_elem(const CrossBwdArgs &a, BBars &b, BXch &xch, uint8_t *ti
         const int row = p.tile * kTile + r;
         const long long at = (static_cast<long long>(p.b) * a.Hk * a.G + p.h) * a.Nq + row;
         next_lse = row < a.Nq ? __ldcg(a.lse + at) : 0.f;
-        next_d = row < a.Nq ? __ldcg(a.dvec + at) : 0.f;
+        next_d = row < a.Nq ? __ldcg((p.L <= kFewKeys ? a.dfew : a.dvec) + at) : 0.f;
         if (kF16)
             next_norm = row < a.Nq ? __ldcg(a.norms + at) : 0.f;
         fetch_norm(p);
@@ -1150,11 +1158,52 @@ __device__ __forceinline__ void zero_tile(void *t, const long long *st, int b, i
                 make_uint4(0, 0, 0, 0);
 }
 
+// D of a tile's rows of one head, a group of lanes a row; all rows have the same keys.
+template <int D, bool kF16, int kGroup, int kLanes>
+__device__ __forceinline__ void few_keys(const CrossBwdArgs &a, int b, int h, int tile, int L)
+{
+    const int part = threadIdx.x % kGroup, end = min(a.Nq, (tile + 1) * kTile);
+    const bool real = part < kLanes;
+    const uint16_t *k = static_cast<const uint16_t *>(a.k) + b * a.k_st[0] + h / a.G * a.k_st[1] + part * 8;
+    const uint16_t *v = static_cast<const uint16_t *>(a.v) + b * a.v_st[0] + h / a.G * a.v_st[1] + part * 8;
+    auto piece = [&](const void *p, const long long *st, int n) {
+        return real && n < end ? *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p) + b * st[0] +
+                                                                  h * st[1] + n * st[2] + part * 8)
+                               : make_uint4(0, 0, 0, 0);
+    };
+    auto dot = [&](const uint4 &x, const uint16_t *row) {
+        const uint4 y = real ? *reinterpret_cast<const uint4 *>(row) : make_uint4(0, 0, 0, 0);
+        const uint32_t xv[4] = {x.x, x.y, x.z, x.w}, yv[4] = {y.x, y.y, y.z, y.w};
+        float sum = 0.f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float2 u = unpack2<kF16>(xv[i]), w = unpack2<kF16>(yv[i]);
+            sum = fmaf(u.y, w.y, fmaf(u.x, w.x, sum));
+        }
+#pragma unroll
+        for (int o = kGroup / 2; o > 0; o /= 2)
+            sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        return sum;
+    };
+    for (int n0 = tile * kTile; n0 < end; n0 += kPrepThreads / kGroup) {
+        const int n = n0 + threadIdx.x / kGroup;
+        const long long at = (static_cast<long long>(b) * a.Hk * a.G + h) * a.Nq + n;
+        const uint4 q = piece(a.q, a.q_st, n), g = piece(a.dout, a.do_st, n);
+        float sum = 0.f;
+        const float nl2 = n < end ? neg_lse2<false>(a.lse[at]) : 0.f;
+#pragma unroll 1
+        for (int j = 0; j < L; ++j)
+            sum = fmaf(ex2(fmaf(dot(q, k + j * a.k_st[2]), a.sl2, nl2)), dot(g, v + j * a.v_st[2]), sum);
+        if (n < end && part == 0)
+            a.dfew[at] = sum;
+    }
+}
+
 // D of all rows, a group of lanes a row (16 bytes a lane), in the order in which
 // they lie in memory; in fp16 a run of a key head's rows at a time, with their norms
-// and the run's largest, and the same of V's rows.  Then zeros for what no unit covers: key tiles behind a
-// sequence's last key (all, without queries) and the queries of a sequence without
-// keys.
+// and the run's largest, and the same of V's rows.  Then D of the rows with few keys,
+// and zeros for what no unit covers: key tiles behind a sequence's last key (all,
+// without queries) and the queries of a sequence without keys.
 template <int D, bool kF16> __global__ void __launch_bounds__(kPrepThreads, 5) cross_prep_kernel(const CrossBwdArgs a)
 {
     constexpr int kLanes = D / 8, kGroup = D == 64 ? 8 : 16;
@@ -1166,6 +1215,7 @@ template <int D, bool kF16> __global__ void __launch_bounds__(kPrepThreads, 5) c
     const int Hq = a.Hk * a.G;
     const long long rows = static_cast<long long>(a.B) * Hq * a.Nq;
     const bool heads_inside = a.do_st[1] < a.do_st[2];
+    const bool some_few = a.kv_len != nullptr || a.Nk <= kFewKeys;  // as far as can be told
     auto block_max = [&](float x, float *to) {
         x = warp_max(x);
         if (lane == 0)
@@ -1291,7 +1341,7 @@ template <int D, bool kF16> __global__ void __launch_bounds__(kPrepThreads, 5) c
             block_max(top, a.v_max + (static_cast<long long>(b) * a.Hk + h) * a.v_parts + c);
         }
     }
-    if (a.kv_len == nullptr && a.Nk > 0 && rows > 0)
+    if (!some_few && rows > 0)
         return;
     const int Tk = (a.Nk + kTile - 1) / kTile;
     const long long k_tiles = static_cast<long long>(a.Hk) * Tk, tiles = k_tiles + static_cast<long long>(Hq) * a.Tq;
@@ -1306,9 +1356,13 @@ template <int D, bool kF16> __global__ void __launch_bounds__(kPrepThreads, 5) c
                 zero_tile<kGroup, kLanes>(a.dk, a.dk_st, b, h, tile, a.Nk);
                 zero_tile<kGroup, kLanes>(a.dv, a.dv_st, b, h, tile, a.Nk);
             }
-        } else if (L == 0) {
+        } else if (L <= kFewKeys) {
             const int h = static_cast<int>((at - k_tiles) / a.Tq);
-            zero_tile<kGroup, kLanes>(a.dq, a.dq_st, b, h, static_cast<int>(at - k_tiles) - h * a.Tq, a.Nq);
+            const int tile = static_cast<int>(at - k_tiles - static_cast<long long>(h) * a.Tq);
+            if (L == 0)
+                zero_tile<kGroup, kLanes>(a.dq, a.dq_st, b, h, tile, a.Nq);
+            else
+                few_keys<D, kF16, kGroup, kLanes>(a, b, h, tile, L);
         }
     }
 }

@@ -261,18 +261,18 @@ cudaError_t launch_kv_fork(const KvForkArgs &a, cudaStream_t stream);
 // Gradients of cross attention, already validated.  Strides (batch, head, row)
 // in elements.
 struct CrossBwdArgs {
-    const void *q, *v, *o, *dout;
+    const void *q, *k, *v, *o, *dout;
     const float *lse;
     const int *kv_len;  // may be null
     void *dq, *dk, *dv;
-    // Workspace: D [B Hq Nq]; in fp16 the norms of dO's rows [B Hq Nq] and the largest
+    // Workspace: D [B Hq Nq], and that of sequences with few keys; in fp16 the norms of dO's rows [B Hq Nq] and the largest
     // of each of do_parts runs of a key head's rows [B Hk][do_parts], and of its rows
     // of v [B Hk][v_parts]; where the CTAs of the two passes start [2][grid], partial
     // sums of two units a CTA.
-    float *dvec, *norms, *do_max, *v_max, *ws_kv, *ws_q;
+    float *dvec, *dfew, *norms, *do_max, *v_max, *ws_kv, *ws_q;
     int4 *starts;
     uint32_t *status;
-    long long q_st[3], v_st[3], o_st[3], do_st[3], dq_st[3], dk_st[3], dv_st[3];
+    long long q_st[3], k_st[3], v_st[3], o_st[3], do_st[3], dq_st[3], dk_st[3], dv_st[3];
     int B, Hk, G, Nq, Nk, Tq, d, f16, grid;
     float scale, sl2;
     int do_parts, v_parts;
