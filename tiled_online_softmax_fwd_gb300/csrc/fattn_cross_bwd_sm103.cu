@@ -703,9 +703,9 @@ template <bool kF16> __device__ __forceinline__ float grad_scale(const CrossBwdA
 // The largest of some values, NaN aside, each lane some of them; and of the lanes'.
 __device__ __forceinline__ float lanes_max(const float *x, int n, int lane)
 {
-    float m = 0.f;
+    float m = lane < n ? __ldcg(x + lane) : 0.f;  // of up to 32 not waited for here
 #pragma unroll 2
-    for (int i = lane; i < n; i += 32)
+    for (int i = lane + 32; i < n; i += 32)
         m = fmaxf(m, __ldcg(x + i));
     return m;
 }
@@ -739,9 +739,13 @@ __device__ void bwd_elem(const CrossBwdArgs &a, BBars &b, BXch &xch, uint8_t *ti
     const uint32_t col = quarter * 32;
     uint32_t pos = 0;  // tiles so far
     bool ok = true;
-    // What dS is multiplied by: dkdv, of the piece; dq, of the row.
-    float ds_scale = 1.f;
+    // What dS is multiplied by, twice: dkdv, of the piece; dq, of the row.
     uint64_t dss = f2_pack(1.f, 1.f);
+    auto ds_scale = [&]() {
+        float x, y;
+        f2_unpack(dss, x, y);
+        return x;
+    };
     const uint64_t sl2x2 = f2_pack(a.sl2, a.sl2);
     auto wait = [&](uint64_t &bar, uint32_t phase) {
         return mbar_wait(smem_addr(&bar), phase & 1, kWaitLimitNs, abort);
@@ -754,20 +758,26 @@ __device__ void bwd_elem(const CrossBwdArgs &a, BBars &b, BXch &xch, uint8_t *ti
     // dkdv: lse and D of the query of this lane's column, fetched a tile ahead, the
     // next piece's first one too.
     float next_lse = 0.f, next_d = 0.f;
-    float next_norm = 0.f;  // of dO; dkdv: a lane's part of the next piece's; dq: the row's
-    float next_v = 0.f;     // of V, a lane's part
-    auto fetch_norm = [&](const Piece &p) {
+    // fp16: norms of dO (dkdv: a lane's part of the piece's; dq: the row's) and of V (a
+    // lane's part).  Read and used outside the loop over tiles: inside of it, in what is
+    // done once at its end, their shuffles cost dq an eighth of its time.
+    float norm = 0.f, v_norm = 0.f;
+    auto fetch_norms = [&](const Piece &p) {
         if constexpr (kF16) {
             const long long head = static_cast<long long>(p.b) * a.Hk + (kDkDv ? p.h : p.h / a.G);
-            next_v = lanes_max(a.v_max + head * a.v_parts, a.v_parts, lane);
+            const int row = p.tile * kTile + r;
+            v_norm = lanes_max(a.v_max + head * a.v_parts, a.v_parts, lane);
             if (kDkDv)
-                next_norm = lanes_max(a.do_max + head * a.do_parts, a.do_parts, lane);
+                norm = lanes_max(a.do_max + head * a.do_parts, a.do_parts, lane);
+            else
+                norm = row < a.Nq ? __ldcg(a.norms + (static_cast<long long>(p.b) * a.Hk * a.G + p.h) * a.Nq + row)
+                                  : 0.f;
         }
     };
     auto set_scale = [&]() {
         if constexpr (kF16) {
-            ds_scale = scale_of((kDkDv ? warp_max(next_norm) : next_norm) * warp_max(next_v));
-            dss = f2_pack(ds_scale, ds_scale);
+            const float x = scale_of((kDkDv ? warp_max(norm) : norm) * warp_max(v_norm));
+            dss = f2_pack(x, x);
         }
     };
     auto fetch = [&](const Piece &p, int t) {
@@ -784,9 +794,6 @@ __device__ void bwd_elem(const CrossBwdArgs &a, BBars &b, BXch &xch, uint8_t *ti
         const long long at = (static_cast<long long>(p.b) * a.Hk * a.G + p.h) * a.Nq + row;
         next_lse = row < a.Nq ? __ldcg(a.lse + at) : 0.f;
         next_d = row < a.Nq ? __ldcg((p.L <= kFewKeys ? a.dfew : a.dvec) + at) : 0.f;
-        if (kF16)
-            next_norm = row < a.Nq ? __ldcg(a.norms + at) : 0.f;
-        fetch_norm(p);
     };
     auto make_resident = [&](uint32_t k) {
         constexpr int kJobs = D / 32;  // of each tensor
@@ -818,9 +825,6 @@ __device__ void bwd_elem(const CrossBwdArgs &a, BBars &b, BXch &xch, uint8_t *ti
         tmem_wait_st();
         tc_fence_before();
         arrive(b.q_full);
-        set_scale();
-        row_nl2 = neg_lse2<kF16>(next_lse);
-        row_nd = -next_d * ds_scale;
     };
     for (uint32_t k = 0; receive(b, k, ok); ++k) {
         const Piece &p = b.pieces[k % kPieces];
@@ -828,27 +832,27 @@ __device__ void bwd_elem(const CrossBwdArgs &a, BBars &b, BXch &xch, uint8_t *ti
         if (k == 0) {
             if (kDkDv) {
                 fetch(p, t0);
-                fetch_norm(p);
+                fetch_norms(p);
             } else {
                 fetch_row(p);
+                fetch_norms(p);
                 make_resident(k);
             }
         }
-        // dq: the next piece's rows have scales of their own before this one is stored.
-        const float row_scale = kDkDv ? 0.f : grad_scale<kF16>(a, p.L, ds_scale);
+        set_scale();
+        if (!kDkDv) {
+            row_nl2 = neg_lse2<kF16>(next_lse);
+            row_nd = -next_d * ds_scale();
+        }
         for (int t = t0; ok && t < t1; ++t, ++pos) {
             if constexpr (kDkDv) {
-                if (kF16 && t == t0)
-                    set_scale();
                 float *lse2 = xch.lse2[threadIdx.x / 32][pos & 1], *dd = xch.dd[threadIdx.x / 32][pos & 1];
                 lse2[lane] = neg_lse2<kF16>(next_lse);
-                dd[lane] = -next_d * ds_scale;
+                dd[lane] = -next_d * ds_scale();
                 if (t + 1 < t1)
                     fetch(p, t + 1);
-                else if (receive(b, k + 1, ok)) {
+                else if (receive(b, k + 1, ok))
                     fetch(b.pieces[(k + 1) % kPieces], b.pieces[(k + 1) % kPieces].t0);
-                    fetch_norm(b.pieces[(k + 1) % kPieces]);
-                }
                 __syncwarp();
                 ok = ok && wait(b.s_full[pos & 1], pos >> 1);
                 if (!ok)
@@ -985,6 +989,8 @@ __device__ void bwd_elem(const CrossBwdArgs &a, BBars &b, BXch &xch, uint8_t *ti
         }
         if (!ok)
             break;
+        if (kF16 && receive(b, k + 1, ok))
+            fetch_norms(b.pieces[(k + 1) % kPieces]);
         ok = ok && wait(b.o_full, k);
         if (!ok)
             break;
@@ -993,7 +999,7 @@ __device__ void bwd_elem(const CrossBwdArgs &a, BBars &b, BXch &xch, uint8_t *ti
         // chunks; dq: a chunk a warpgroup.
         const bool is_dv = kDkDv && quarter < 2;
         const uint32_t acc = tmem + C::kColAcc + (kDkDv && !is_dv ? D : 0);
-        const float f = is_dv ? kPInverse<kF16> : kDkDv ? grad_scale<kF16>(a, p.L, ds_scale) : row_scale;
+        const float f = is_dv ? kPInverse<kF16> : grad_scale<kF16>(a, p.L, ds_scale());
         const bool whole = p.slot < 0;
         const bool zero = kDkDv && p.tile * kTile + r >= p.L;
         const long long *st = kDkDv ? (is_dv ? a.dv_st : a.dk_st) : a.dq_st;
@@ -1499,11 +1505,12 @@ CrossBwdSizes cross_bwd_sizes(int d, int num_sms)
     return CrossBwdSizes{2 * num_sms, 2LL * num_sms * 2 * kTile * d, 2LL * num_sms * kTile * d};
 }
 
-// Two runs a prep block together, of 64 rows at least; a warp of the passes reads one
-// key head's at most 256 of them where its piece starts.
+// A run a prep block, or where the heads alone are some hundred four, so that no round
+// of the blocks is half empty; of 64 rows at least.  A warp of the passes reads one
+// key head's at most 256 where its piece starts.
 int cross_bwd_parts(long long heads, long long rows)
 {
-    const long long want = heads > 0 ? (2 * kPrepBlocks + heads - 1) / heads : 1;
+    const long long want = heads > 0 ? (heads > kPrepBlocks / 4 ? 4 : 1) * kPrepBlocks / heads : 1;
     return static_cast<int>(std::max(std::min({want, (rows + 63) / 64, 256LL}), 1LL));
 }
 
