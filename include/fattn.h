@@ -664,8 +664,13 @@ fattn_status_t fattn_kv_fork(void *k_cache, void *v_cache, const int *page_table
  * Rows of k and v behind a sequence's last key may hold anything, NaN included.
  * A sequence without keys gives o = 0 and lse = -inf.  Two kernels are enqueued, or
  * one where a key head has at most four rows (Nq Hq / Hk) and few enough units: it
- * works on the CUDA cores, with P and V as they are, not rounded to fp16.  Equal
- * calls give equal bits.  Range reports and errors as for attn_fwd_paged.
+ * works on the CUDA cores, with P and V as they are, not rounded to fp16 (their sums,
+ * before the division by the softmax's, in fp32).  Which of the two it is follows from
+ * the sizes and the GPU's SMs, so bf16 values beyond 65504, which the first one reports
+ * as out of range, should not be counted on.  Equal calls give equal bits.  Range
+ * reports and errors as for attn_fwd_paged.  Without lengths and with Hq = Hk,
+ * attn_fwd_strided takes the same inputs and is the faster one of many queries at d =
+ * 64 or of short keys.
  */
 size_t attn_fwd_cross_workspace_size(int Hq, int Hk, int Nq, int d);
 fattn_status_t attn_fwd_cross(const void *q, const void *k, const void *v, const int *kv_len, void *o,

@@ -7,8 +7,8 @@
 //   dV = sum_h P^T dO,     dP = dO V^T,   dS = P o (dP - D),
 //   dQ = scale dS K,       dK = scale sum_h dS^T Q.
 // Four kernels, each started under the tail of the one before:
-//   prep     D, the norms of dO's rows and V's (fp16), and zeros for key tiles without
-//            keys
+//   prep     D (of few keys from P and dP), the norms of dO's rows and V's (fp16), and
+//            zeros for key tiles without keys
 //   dkdv     a unit is a tile of 128 keys of one (sequence, key head).  K, V
 //            stay; the tiles of Q and dO of its G query heads stream by: S^T =
 //            K Q^T and dP^T = V dO^T, keys on TMEM lanes, P^T over S^T, then dV
@@ -32,10 +32,12 @@
 // of dkdv takes some 2520 cycles, its products 2048 and its reads and copies in
 // shared memory 2350; a tile of dq 2005, its products 1536 (Q and dO in TMEM save it
 // two reads of 32 KB).  4 sequences, 16 heads, 2048 queries, up to 4096 keys, bf16:
-// 490 us, 970 TFLOP/s of the formulas' five products, 1355 of the seven.  At d = 64
+// 490 us alone in a graph, 970 TFLOP/s of the formulas' five products, 1355 of the
+// seven; at the power cap's clocks 522 us.  fp16, whose prep reads V, too, takes 4 %
+// longer (keys of one length, graphs at the cap: 697 and 666 us).  At d = 64
 // the chain TMEM, exponential, conversion, TMEM of the
 // elementwise warps, shortened by a second S or dP; with few tiles a unit its start
-// and end: 2 sequences, 16 heads, 4096 queries, up to 154 keys 57 us, 1.2 TB/s.
+// and end: 2 sequences, 16 heads, 4096 queries, up to 154 keys 59 us, 1.2 TB/s.
 //
 // Types.  P and dS enter the second products in the inputs' type.  P in fp16 is
 // multiplied by 2^15, in its exponent and so at no cost: with 10^5 keys it is below fp16's

@@ -93,8 +93,8 @@ __global__ void __launch_bounds__(kThreads, 2) cross_few_kernel(const PagedArgs 
     grid_dependency_wait();
     grid_launch_dependents();
     // The longest sequences first, up to 32 of them, so that the last blocks to start
-    // are short (24.8 us for the batch above, in the given order 28; more sequences
-    // make more blocks, of which the last ones weigh less).
+    // are short (24.8 us for the batch above, in the given order 28).  More than a warp's
+    // lanes are taken as given; that was not measured.
     int b = place, given = a.max_keys;
     if (a.kv_len != nullptr) {
         if (a.B <= 32) {

@@ -7,9 +7,10 @@
 // with kept ascending, so kept[j] >= j and a block that goes through j in order
 // never reads a slot it has written: it loads a batch of rows, meets, and
 // stores them.  Bound by latency at a step's few tokens (a chain of four loads:
-// lengths, kept, pages, rows): 6 us with the append before it for 4 sequences of 26
-// tokens; 8.7 us for 192 of up to 129, up to 24 of them kept (8 key heads, d = 128;
-// the rows were written just before and come from L2).
+// lengths, kept, pages, rows): 6 us on the GPU, in a graph, with the append before it
+// for 4 sequences of 26 tokens (plain calls 12, the host's); 8.7 us for 192 of up to
+// 129, up to 24 of them kept (8 key heads, d = 128; the rows were written just before
+// and come from L2).
 //
 // Fork.  Sequence b goes on as its parent's copy with room for new tokens:
 //   table'[b] = the parent's entries, L'[b] = L[parent] + n_b.
@@ -22,8 +23,12 @@
 // the lists in steps between cluster barriers (a block alone where they are
 // short), a second kernel copies the pages' rows.  Bound by latency: the lists are
 // a few KB, read in four dependent steps (entries, their counts, the counts' sums,
-// the free pages) with a meeting of the blocks between two: 9.3 us for 8 sequences
-// of up to 900 keys, 16.7 for 256 of up to 4000 and 700 new ones; pages of 16 and 32.
+// the free pages) with a meeting of the blocks between two: 9.3 us in a graph for 8
+// sequences of up to 900 keys, 16.7 for 256 of up to 4000 and 700 new ones; pages of 16
+// and 32.  A sequence that goes on with its own pages adds a walk by one thread along
+// the columns that it grows by, a read each: 64 sequences that grow by a page 8.3 us
+// (with 50000 pages in the pool, all looked at, 12.0), one by 1000 pages 62, 16 by 1000
+// each 81.
 #include <cooperative_groups.h>
 #include <stdint.h>
 

@@ -62,14 +62,16 @@
 // them and of the new ones those whose bits its mask has.  Only key tiles that
 // reach into the last n keys look at masks: 128 bits of a row's words, shifted
 // to the tile (a word for a quad unit's warp), in place of the limit.  16 sequences
-// of 64 new tokens against 12K to 32K keys, 32 and 8 heads, d = 128, bf16: 273 us,
-// 5.2 TB/s and 1300 TFLOP/s, 76 and 68 % of what a copy and a plain product reach.
+// of 64 new tokens against 12K to 32K keys, 32 and 8 heads, d = 128, bf16: 273 us alone
+// in a graph, 5.2 TB/s and 1300 TFLOP/s, 76 and 68 % of what a copy and a plain product
+// reach; among other calls, at the power cap's clocks, 296 us.
 //
 // Cross attention.  A sequence's keys are rows 0 .. L - 1 of its slice of k and
 // v, copied as pages of their own are: the tile's keys at coordinate 128 j.  Its
 // queries are a slice of q, so the maps of q have a fifth dimension.  8 sequences of
-// 2048 queries against up to 4096 keys, 32 and 8 heads, d = 128, bf16: 550 us, 1390
-// TFLOP/s (fp16, without the conversion of V, 512 us).
+// 2048 queries against up to 4096 keys, 32 and 8 heads, d = 128, bf16: 550 us alone in
+// a graph, 1390 TFLOP/s (fp16, without the conversion of V, 512 us); at the power cap's
+// clocks 597 us.
 //
 // Code size.  Every role is code of its own, 127 KB in all at d = 64, and what
 // the warps of a batch with units of several kinds run at a time does not fit

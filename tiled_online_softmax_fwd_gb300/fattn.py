@@ -985,8 +985,9 @@ def attn_fwd_cross(q, k, v, kv_len=None, scale: float | None = None, workspace=N
     first) and a contiguous last dimension, d 64, 96 or 128, Hq a multiple of
     Hk, Nq and Nk independent.  ``kv_len`` int32 [B] on the device: the keys of
     each sequence, what is behind them may hold anything (None: Nk).  A sequence
-    without keys gives o = 0 and lse = -inf.  Returns (out [B, Hq, Nq, d], lse
-    fp32 [B, Hq, Nq])."""
+    without keys gives o = 0 and lse = -inf.  Without lengths and with Hq = Hk,
+    attn_fwd_strided may be faster (many queries at d = 64, or short keys).  Returns
+    (out [B, Hq, Nq, d], lse fp32 [B, Hq, Nq])."""
     return (_binding or _native(q)).attn_fwd_cross(q, k, v, kv_len, scale, workspace, out, lse, stream)
 
 
@@ -1000,8 +1001,8 @@ def attn_bwd_cross(q, k, v, o, lse, do, kv_len=None, scale: float | None = None,
                    dv=None, workspace=None, stream=None):
     """Gradients of attn_fwd_cross (libfattn attn_bwd_cross) for the upstream
     gradient ``do``, from its inputs and the o and lse it returned: tensors of
-    q's and k's shapes, any strides with a contiguous last dimension (lse
-    contiguous).  Rows of dk and dv behind a sequence's last key are zeros.
+    q's and k's shapes, strides as for attn_fwd_cross (a broadcast ``do`` is
+    copied first; lse contiguous).  Rows of dk and dv behind a sequence's last key are zeros.
     Returns (dq, dk, dv) in the inputs' type, each of which may be given."""
     return (_binding or _native(q)).attn_bwd_cross(q, k, v, o, lse, do, kv_len, scale, dq, dk, dv, workspace,
                                                   stream)
