@@ -91,10 +91,9 @@ template <int D> constexpr int kMergeCost = D == 64 ? 6 : 3;
 // little, and the passes in turn need no guess of their steps' lengths.
 constexpr int kStepKv = 4, kStepQ = 3, kTogether = 32;
 
-// With few keys the rounding of o is the larger part of the gradients' error: D = dO . o
-// is off by h |dO| |o|, h half a step of the type, where dS = P (dP - D) is a
-// difference that o's mean over many keys does not enter.  There D is summed up from
-// P and dP in 32 bits instead.  Error of bf16 dQ in the norm (d = 64, the roundings
+// D = dO . o is off by h |dO| |o|, h half a step of the type.  Over many keys o is a
+// mean, and small; of a few it is as large as their values, and its rounding the larger
+// part of the gradients' error.  There D is summed up from P and dP in 32 bits.  Error of bf16 dQ in the norm (d = 64, the roundings
 // alone): 2 keys 0.0023, from o 0.0041; 4 keys 0.0023 and 0.0029; 16 keys 0.0024 and
 // 0.0025; from 24 keys on the two are alike.
 constexpr int kFewKeys = 16;
@@ -1166,44 +1165,81 @@ __device__ __forceinline__ void zero_tile(void *t, const long long *st, int b, i
                 make_uint4(0, 0, 0, 0);
 }
 
-// D of a tile's rows of one head, a group of lanes a row; all rows have the same keys.
-template <int D, bool kF16, int kGroup, int kLanes>
-__device__ __forceinline__ void few_keys(const CrossBwdArgs &a, int b, int h, int tile, int L)
+// Sums over d of 16 rows of x with 16 keys' rows of y, on the tensor cores: c[n] is rows
+// lane / 4 and 8 behind it, keys 8 n + 2 (lane % 4) and the next.  The elements of a row
+// may come in any order, the same for both, so a lane takes 16 bytes at a time.
+template <int D, bool kF16, class X, class Y>
+__device__ __forceinline__ void product16(const X &x, const Y &y, float (&c)[2][4])
 {
-    const int part = threadIdx.x % kGroup, end = min(a.Nq, (tile + 1) * kTile);
-    const bool real = part < kLanes;
-    const uint16_t *k = static_cast<const uint16_t *>(a.k) + b * a.k_st[0] + h / a.G * a.k_st[1] + part * 8;
-    const uint16_t *v = static_cast<const uint16_t *>(a.v) + b * a.v_st[0] + h / a.G * a.v_st[1] + part * 8;
-    auto piece = [&](const void *p, const long long *st, int n) {
-        return real && n < end ? *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p) + b * st[0] +
-                                                                  h * st[1] + n * st[2] + part * 8)
-                               : make_uint4(0, 0, 0, 0);
+#pragma unroll
+    for (int n = 0; n < 2; ++n)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            c[n][i] = 0.f;
+    auto mma = [](float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+        if constexpr (kF16)
+            asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+                "{%0, %1, %2, %3};"
+                : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+        else
+            asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+                "{%0, %1, %2, %3};"
+                : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
     };
-    auto dot = [&](const uint4 &x, const uint16_t *row) {
-        const uint4 y = real ? *reinterpret_cast<const uint4 *>(row) : make_uint4(0, 0, 0, 0);
-        const uint32_t xv[4] = {x.x, x.y, x.z, x.w}, yv[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll 1
+    for (int e = 0; e < D; e += 32) {
+        const uint4 x0 = x(0, e), x1 = x(8, e);
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+            const uint4 w = y(8 * n, e);
+            mma(c[n], x0.x, x1.x, x0.y, x1.y, w.x, w.y);
+            mma(c[n], x0.z, x1.z, x0.w, x1.w, w.z, w.w);
+        }
+    }
+}
+
+// D of a tile's rows of one head, which have the same few keys: a warp 16 rows.  Bound by
+// reading q and dO once more: 8 sequences, 16 heads, 4096 queries, 16 keys, d = 64, bf16
+// 169 us in all, 141 with D from o (with sums on the CUDA cores, a row a group of lanes,
+// 351).
+template <int D, bool kF16> __device__ __forceinline__ void few_keys(const CrossBwdArgs &a, int b, int h, int tile, int L)
+{
+    static_assert(kFewKeys == 16 && kPrepThreads / 32 * 16 == kTile, "a product is 16 keys, a block's warps a tile");
+    const int lane = threadIdx.x & 31, quad = lane / 4;
+    const int row = tile * kTile + threadIdx.x / 32 * 16 + quad, piece = lane % 4 * 8;
+    auto rows_of = [&](const void *p, const long long *st) {
+        const uint16_t *at = static_cast<const uint16_t *>(p) + b * st[0] + h * st[1] + row * st[2] + piece;
+        return [at, st, left = a.Nq - row](int r, int e) {
+            return r < left ? *reinterpret_cast<const uint4 *>(at + r * st[2] + e) : make_uint4(0, 0, 0, 0);
+        };
+    };
+    auto keys_of = [&](const void *p, const long long *st) {
+        const uint16_t *at = static_cast<const uint16_t *>(p) + b * st[0] + h / a.G * st[1] + quad * st[2] + piece;
+        return [at, st, left = L - quad](int j, int e) {
+            return j < left ? *reinterpret_cast<const uint4 *>(at + j * st[2] + e) : make_uint4(0, 0, 0, 0);
+        };
+    };
+    float s[2][4], dp[2][4];
+    product16<D, kF16>(rows_of(a.q, a.q_st), keys_of(a.k, a.k_st), s);
+    product16<D, kF16>(rows_of(a.dout, a.do_st), keys_of(a.v, a.v_st), dp);
+    const long long at = (static_cast<long long>(b) * a.Hk * a.G + h) * a.Nq + row;
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+        const bool live = row + 8 * half < a.Nq;
+        const float nl2 = live ? neg_lse2<false>(a.lse[at + 8 * half]) : 0.f;
         float sum = 0.f;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const float2 u = unpack2<kF16>(xv[i]), w = unpack2<kF16>(yv[i]);
-            sum = fmaf(u.y, w.y, fmaf(u.x, w.x, sum));
+            const int n = i / 2, c = 2 * half + i % 2;
+            if (8 * n + lane % 4 * 2 + i % 2 < L)
+                sum = fmaf(ex2(fmaf(s[n][c], a.sl2, nl2)), dp[n][c], sum);
         }
-#pragma unroll
-        for (int o = kGroup / 2; o > 0; o /= 2)
-            sum += __shfl_xor_sync(0xffffffffu, sum, o);
-        return sum;
-    };
-    for (int n0 = tile * kTile; n0 < end; n0 += kPrepThreads / kGroup) {
-        const int n = n0 + threadIdx.x / kGroup;
-        const long long at = (static_cast<long long>(b) * a.Hk * a.G + h) * a.Nq + n;
-        const uint4 q = piece(a.q, a.q_st, n), g = piece(a.dout, a.do_st, n);
-        float sum = 0.f;
-        const float nl2 = n < end ? neg_lse2<false>(a.lse[at]) : 0.f;
-#pragma unroll 1
-        for (int j = 0; j < L; ++j)
-            sum = fmaf(ex2(fmaf(dot(q, k + j * a.k_st[2]), a.sl2, nl2)), dot(g, v + j * a.v_st[2]), sum);
-        if (n < end && part == 0)
-            a.dfew[at] = sum;
+        sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+        sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+        if (live && lane % 4 == 0)
+            a.dfew[at + 8 * half] = sum;
     }
 }
 
@@ -1370,7 +1406,7 @@ template <int D, bool kF16> __global__ void __launch_bounds__(kPrepThreads, 5) c
             if (L == 0)
                 zero_tile<kGroup, kLanes>(a.dq, a.dq_st, b, h, tile, a.Nq);
             else
-                few_keys<D, kF16, kGroup, kLanes>(a, b, h, tile, L);
+                few_keys<D, kF16>(a, b, h, tile, L);
         }
     }
 }
