@@ -93,9 +93,9 @@ constexpr int kStepKv = 4, kStepQ = 3, kTogether = 32;
 
 // D = dO . o is off by h |dO| |o|, h half a step of the type.  Over many keys o is a
 // mean, and small; of a few it is as large as their values, and its rounding the larger
-// part of the gradients' error.  There D is summed up from P and dP in 32 bits.  Error of bf16 dQ in the norm (d = 64, the roundings
-// alone): 2 keys 0.0023, from o 0.0041; 4 keys 0.0023 and 0.0029; 16 keys 0.0024 and
-// 0.0025; from 24 keys on the two are alike.
+// part of the gradients' error.  There D is summed up from P and dP in 32 bits.  Error
+// of bf16 dQ in the norm (d = 64, the roundings alone): 2 keys 0.0023, from o 0.0041; 4
+// keys 0.0023 and 0.0029; 16 keys 0.0024 and 0.0025; from 24 keys on the two are alike.
 constexpr int kFewKeys = 16;
 
 template <int D, bool kDkDv> struct BCfg {
@@ -1204,7 +1204,8 @@ __device__ __forceinline__ void product16(const X &x, const Y &y, float (&c)[2][
 // reading q and dO once more: 8 sequences, 16 heads, 4096 queries, 16 keys, d = 64, bf16
 // 169 us in all, 141 with D from o (with sums on the CUDA cores, a row a group of lanes,
 // 351).
-template <int D, bool kF16> __device__ __forceinline__ void few_keys(const CrossBwdArgs &a, int b, int h, int tile, int L)
+template <int D, bool kF16>
+__device__ __forceinline__ void few_keys(const CrossBwdArgs &a, int b, int h, int tile, int L)
 {
     static_assert(kFewKeys == 16 && kPrepThreads / 32 * 16 == kTile, "a product is 16 keys, a block's warps a tile");
     const int lane = threadIdx.x & 31, quad = lane / 4;
@@ -1515,9 +1516,8 @@ cudaError_t launch(const CrossBwdArgs &args, const CrossBwdMaps &m, cudaStream_t
     const long long rows = static_cast<long long>(a.B) * a.Hk * a.G * a.Nq;
     const long long blocks = (rows + kRows - 1) / kRows;
     // The zeros of short sequences, and fp16's runs, want hands, too.
-    a.prep_blocks = static_cast<int>(kF16 || a.kv_len != nullptr || a.Nk == 0 || rows == 0 || blocks > kPrepBlocks ? kPrepBlocks
-                                     : blocks > 0                               ? blocks
-                                                                                : 1);
+    const bool most = kF16 || a.kv_len != nullptr || a.Nk == 0 || rows == 0 || blocks > kPrepBlocks;
+    a.prep_blocks = most ? kPrepBlocks : static_cast<int>(blocks);
     const bool whole = whole_units<D>(a);
     a.snap = whole ? 0x7fffffff : kSnap;
     cudaError_t e = start(cross_prep_kernel<D, kF16>, dim3(a.prep_blocks), kPrepThreads, 0, stream, a);
